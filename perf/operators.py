@@ -229,7 +229,7 @@ def _handle(state):
     plan = lib.fp8kv_attn_chunk_plan(lib.make_chunk_desc(
         batch=case["batch"], total_q=state["q"].shape[0], max_q=case["q_hi"], num_q_heads=case["heads"],
         num_kv_heads=case["kv_heads"], head_dim=case["dim"], page_size=case["page"],
-        max_kv_len=case["ctx_hi"] + case["q_hi"], max_blocks=state["table"].shape[1],
+        max_kv_len=max(kv for _, kv in _requests(case)), max_blocks=state["table"].shape[1],
         num_kv_blocks=state["k"].shape[0], window=case["window"], sinks=case["sinks"],
         dtype=lib.DTYPE_F16 if case["dtype"] == "f16" else lib.DTYPE_BF16, kv_format=fmt))
     workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
