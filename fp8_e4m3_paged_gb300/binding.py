@@ -95,6 +95,7 @@ class Args(ctypes.Structure):
 
 DTYPE_F16 = 0
 DTYPE_BF16 = 1
+DTYPE_F32 = 2  # cache read outputs only
 
 
 class CacheWriteArgs(ctypes.Structure):
@@ -139,6 +140,70 @@ class SelectArgs(ctypes.Structure):
     ]
 
 
+CHUNK_AUTO = 0
+CHUNK_STREAM = 1
+CHUNK_TILE = 2
+
+
+class ChunkDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "total_q", "max_q", "num_q_heads", "num_kv_heads", "head_dim", "page_size", "max_kv_len",
+        "max_blocks", "num_kv_blocks", "window", "sinks", "dtype", "kv_format", "num_sms", "num_splits", "kernel")]
+
+
+class ChunkPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "revision", "batch", "total_q", "max_q", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
+        "max_kv_len", "max_blocks", "num_kv_blocks", "window", "sinks", "dtype", "kv_format", "group", "kernel",
+        "num_splits", "row_tiles", "num_sms")] + [
+        ("partial_offset", ctypes.c_int64), ("ml_offset", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 8),
+    ]
+
+
+class ChunkArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_stride_block", ctypes.c_int64), ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("v_stride_block", ctypes.c_int64), ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+        ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("softmax_scale", ctypes.c_float), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("k_scale_dev", ctypes.c_void_p), ("v_scale_dev", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class CacheReadArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "total", "num_kv_heads", "head_dim", "page_size", "max_blocks", "num_kv_blocks", "dtype",
+        "kv_format")] + [
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("kc_stride_block", ctypes.c_int64), ("kc_stride_token", ctypes.c_int64),
+        ("kc_stride_head", ctypes.c_int64),
+        ("vc_stride_block", ctypes.c_int64), ("vc_stride_token", ctypes.c_int64),
+        ("vc_stride_head", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+        ("cu_len", ctypes.c_void_p), ("start", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+        ("ko_stride_token", ctypes.c_int64), ("ko_stride_head", ctypes.c_int64),
+        ("vo_stride_token", ctypes.c_int64), ("vo_stride_head", ctypes.c_int64),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("k_scale_dev", ctypes.c_void_p), ("v_scale_dev", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class CalibrateArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_kv_heads", "head_dim", "dtype", "kv_format")] + [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+        ("slot_mapping", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"{LIB_PATH} is missing: build it with `python -m fp8_e4m3_paged_gb300.build_lib` "
@@ -169,6 +234,14 @@ lib.fp8kv_attn_select_to_entries.restype = ctypes.c_int
 lib.fp8kv_attn_select_to_entries.argtypes = [ctypes.POINTER(SelectArgs), ctypes.c_void_p]
 lib.fp8kv_attn_cache_write.restype = ctypes.c_int
 lib.fp8kv_attn_cache_write.argtypes = [ctypes.POINTER(CacheWriteArgs), ctypes.c_void_p]
+lib.fp8kv_attn_chunk_plan.restype = ctypes.c_int
+lib.fp8kv_attn_chunk_plan.argtypes = [ctypes.POINTER(ChunkDesc), ctypes.POINTER(ChunkPlan)]
+lib.fp8kv_attn_chunk.restype = ctypes.c_int
+lib.fp8kv_attn_chunk.argtypes = [ctypes.POINTER(ChunkPlan), ctypes.POINTER(ChunkArgs), ctypes.c_void_p]
+lib.fp8kv_attn_cache_read.restype = ctypes.c_int
+lib.fp8kv_attn_cache_read.argtypes = [ctypes.POINTER(CacheReadArgs), ctypes.c_void_p]
+lib.fp8kv_attn_cache_calibrate.restype = ctypes.c_int
+lib.fp8kv_attn_cache_calibrate.argtypes = [ctypes.POINTER(CalibrateArgs), ctypes.c_void_p]
 
 
 class Fp8kvError(RuntimeError):
@@ -386,3 +459,189 @@ def fp8kv_attn_select_to_entries(args: SelectArgs, stream: int = 0) -> None:
     rc = lib.fp8kv_attn_select_to_entries(ctypes.byref(args), ctypes.c_void_p(stream))
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_select_to_entries")
+
+
+# ---------------------------------------------------------------- chunk attention, cache read, calibration
+
+def _torch_dtype(t, *allowed) -> int:
+    import torch
+
+    code = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(t.dtype, -1)
+    if code not in allowed:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _check(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _int32(t, n: int, name: str) -> None:
+    import torch
+
+    _check(t.dtype == torch.int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous(),
+           f"{name}: a contiguous int32 tensor of {n} elements")
+
+
+def _device_scale(t, name: str) -> None:
+    import torch
+
+    _check(t is None or (t.dtype == torch.float32 and t.numel() == 1), f"{name}: one float32 element")
+
+
+def _pages(t, name: str):
+    """Byte strides (block, token, head) of a cache view [blocks][page][Hkv][D], d contiguous."""
+    _check(t.dim() == 4 and t.element_size() == 1 and t.stride(3) == 1,
+           f"{name}: one-byte elements [blocks][page][Hkv][D] with d contiguous")
+    return t.stride()[:3]
+
+
+def _rows(t, name: str):
+    _check(t.dim() == 3 and t.stride(2) == 1, f"{name}: [rows][heads][D] with d contiguous")
+    return t.stride()[:2]
+
+
+def make_chunk_desc(*, batch: int, total_q: int, max_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                    page_size: int, max_kv_len: int, max_blocks: int, num_kv_blocks: int, window: int = 0,
+                    sinks: int = 0, dtype: int = DTYPE_F16, kv_format: int = KV_E4M3, num_sms: int = 0,
+                    num_splits: int = 0, kernel: int = CHUNK_AUTO) -> ChunkDesc:
+    return ChunkDesc(batch, total_q, max_q, num_q_heads, num_kv_heads, head_dim, page_size, max_kv_len, max_blocks,
+                     num_kv_blocks, window, sinks, dtype, kv_format, num_sms, num_splits, kernel)
+
+
+def fp8kv_attn_chunk_plan(desc: ChunkDesc) -> ChunkPlan:
+    plan = ChunkPlan()
+    rc = lib.fp8kv_attn_chunk_plan(ctypes.byref(desc), ctypes.byref(plan))
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_chunk_plan")
+    return plan
+
+
+def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float, block_table, cu_q, kv_len,
+                    k_scale: float = 1.0, v_scale: float = 1.0, k_scale_dev=None, v_scale_dev=None) -> ChunkArgs:
+    """Fill a ChunkArgs struct from torch CUDA tensors.
+
+    q / out: fp16 or bf16 [total_q][Hq][D] (any row and head strides, d
+    contiguous); k_cache / v_cache: uint8 [blocks][page][Hkv][D] views;
+    block_table: int32 [B][columns]; cu_q: int32 [B+1]; kv_len: int32 [B];
+    workspace: a uint8 tensor of at least plan.workspace_bytes bytes, its
+    first four bytes (the status word) zeroed once.  The plan's sizes must be
+    those of the tensors."""
+    import torch
+
+    _torch_dtype(q, DTYPE_F16, DTYPE_BF16)
+    _check(out.dtype == q.dtype and out.shape == q.shape, "out: same type and shape as q")
+    _check(block_table.dtype == torch.int32 and block_table.dim() == 2 and
+           (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [B][columns]")
+    _int32(cu_q, block_table.shape[0] + 1, "cu_q")
+    _int32(kv_len, block_table.shape[0], "kv_len")
+    _device_scale(k_scale_dev, "k_scale_dev")
+    _device_scale(v_scale_dev, "v_scale_dev")
+    a = ChunkArgs()
+    a.q, (a.q_stride_token, a.q_stride_head) = _ptr(q), _rows(q, "q")
+    a.out, (a.out_stride_token, a.out_stride_head) = _ptr(out), _rows(out, "out")
+    a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+    a.k_stride_block, a.k_stride_token, a.k_stride_head = _pages(k_cache, "k_cache")
+    a.v_stride_block, a.v_stride_token, a.v_stride_head = _pages(v_cache, "v_cache")
+    a.block_table = _ptr(block_table)
+    # a table of one request may carry any stride: its next row is never read
+    a.block_table_stride = max(block_table.stride(0), block_table.shape[1])
+    a.cu_q, a.kv_len = _ptr(cu_q), _ptr(kv_len)
+    a.softmax_scale, a.k_scale, a.v_scale = float(softmax_scale), float(k_scale), float(v_scale)
+    a.k_scale_dev, a.v_scale_dev = _ptr(k_scale_dev), _ptr(v_scale_dev)
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    return a
+
+
+def fp8kv_attn_chunk(plan: ChunkPlan, args: ChunkArgs, stream: int = 0) -> None:
+    rc = lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(args), ctypes.c_void_p(stream))
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_chunk")
+
+
+@dataclass
+class ChunkCall:
+    """A planned chunk attention over fixed device buffers (graph friendly)."""
+    plan: ChunkPlan
+    args: ChunkArgs
+
+    def run(self, stream: int) -> None:
+        fp8kv_attn_chunk(self.plan, self.args, stream)
+
+
+def make_cache_read_args(*, k_cache, v_cache, block_table, cu_len, k_out, v_out, start=None, k_scale: float = 1.0,
+                         v_scale: float = 1.0, k_scale_dev=None, v_scale_dev=None, status=None,
+                         kv_format: int = KV_E4M3) -> CacheReadArgs:
+    """Fill a CacheReadArgs struct from torch CUDA tensors.
+
+    k_cache / v_cache: uint8 [blocks][page][Hkv][D] views; block_table: int32
+    [B][columns]; cu_len: int32 [B+1]; start: optional int32 [B]; k_out /
+    v_out: fp16, bf16 or fp32 [total][Hkv][D] (d contiguous); status: optional
+    int32 tensor of one element."""
+    import torch
+
+    a = CacheReadArgs()
+    a.dtype = _torch_dtype(k_out, DTYPE_F16, DTYPE_BF16, DTYPE_F32)
+    _check(v_out.dtype == k_out.dtype and v_out.shape == k_out.shape, "v_out: same type and shape as k_out")
+    _check(k_cache.shape == v_cache.shape and k_out.shape[1:] == k_cache.shape[2:],
+           "k_out / v_out: [total][Hkv][D] with the caches' Hkv and D")
+    _check(block_table.dtype == torch.int32 and block_table.dim() == 2 and
+           (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [B][columns]")
+    _int32(cu_len, block_table.shape[0] + 1, "cu_len")
+    if start is not None:
+        _int32(start, block_table.shape[0], "start")
+    _device_scale(k_scale_dev, "k_scale_dev")
+    _device_scale(v_scale_dev, "v_scale_dev")
+    a.batch, a.max_blocks = block_table.shape
+    a.total, a.num_kv_heads, a.head_dim = k_out.shape
+    a.num_kv_blocks, a.page_size = k_cache.shape[:2]
+    a.kv_format = kv_format
+    a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+    a.kc_stride_block, a.kc_stride_token, a.kc_stride_head = _pages(k_cache, "k_cache")
+    a.vc_stride_block, a.vc_stride_token, a.vc_stride_head = _pages(v_cache, "v_cache")
+    a.block_table = _ptr(block_table)
+    a.block_table_stride = max(block_table.stride(0), block_table.shape[1])
+    a.cu_len, a.start = _ptr(cu_len), _ptr(start)
+    a.k_out, (a.ko_stride_token, a.ko_stride_head) = _ptr(k_out), _rows(k_out, "k_out")
+    a.v_out, (a.vo_stride_token, a.vo_stride_head) = _ptr(v_out), _rows(v_out, "v_out")
+    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+    a.k_scale_dev, a.v_scale_dev, a.status = _ptr(k_scale_dev), _ptr(v_scale_dev), _ptr(status)
+    return a
+
+
+def fp8kv_attn_cache_read(args: CacheReadArgs, stream: int = 0) -> None:
+    rc = lib.fp8kv_attn_cache_read(ctypes.byref(args), ctypes.c_void_p(stream))
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_cache_read")
+
+
+def make_calibrate_args(*, k, v, k_scale, v_scale, slot_mapping=None, kv_format: int = KV_E4M3) -> CalibrateArgs:
+    """Fill a CalibrateArgs struct from torch CUDA tensors.
+
+    k / v: fp16 or bf16 [N][Hkv][D] (d contiguous); k_scale / v_scale: float32
+    tensors of one element, raised in place; slot_mapping: optional int64 [N]
+    (tokens with a negative slot do not count)."""
+    import torch
+
+    a = CalibrateArgs()
+    a.dtype = _torch_dtype(k, DTYPE_F16, DTYPE_BF16)
+    _check(v.dtype == k.dtype and v.shape == k.shape, "v: same type and shape as k")
+    _check(k_scale is not None and v_scale is not None, "k_scale, v_scale: float32 tensors of one element")
+    _device_scale(k_scale, "k_scale")
+    _device_scale(v_scale, "v_scale")
+    if slot_mapping is not None:
+        _check(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == k.shape[0] and
+               slot_mapping.is_contiguous(), "slot_mapping: a contiguous int64 tensor of N elements")
+    a.num_tokens, a.num_kv_heads, a.head_dim = k.shape
+    a.kv_format = kv_format
+    a.k, (a.k_stride_token, a.k_stride_head) = _ptr(k), _rows(k, "k")
+    a.v, (a.v_stride_token, a.v_stride_head) = _ptr(v), _rows(v, "v")
+    a.slot_mapping, a.k_scale, a.v_scale = _ptr(slot_mapping), _ptr(k_scale), _ptr(v_scale)
+    return a
+
+
+def fp8kv_attn_cache_calibrate(args: CalibrateArgs, stream: int = 0) -> None:
+    rc = lib.fp8kv_attn_cache_calibrate(ctypes.byref(args), ctypes.c_void_p(stream))
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_cache_calibrate")

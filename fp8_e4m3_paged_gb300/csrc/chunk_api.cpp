@@ -1,0 +1,229 @@
+// C ABI entry points of the chunk attention, the cache read and the scale
+// calibration: planning (host only), argument validation, dispatch.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "chunk.h"
+#include "fp8kv_attn.h"
+
+using namespace fp8kv;
+
+namespace {
+
+int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
+bool strides_ok(const int64_t* s, int n, int64_t unit) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] < 0 || s[i] % unit) return false;
+  return true;
+}
+bool fp8_format(int32_t f) { return f == FP8KV_KV_E4M3 || f == FP8KV_KV_E5M2; }
+int done(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ECUDA; }
+
+}  // namespace
+
+extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan) {
+  if (!d || !plan) return FP8KV_EINVAL;
+  if (d->batch < 0 || d->total_q < 0 || d->max_q < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1)
+    return FP8KV_EINVAL;
+  if (d->num_q_heads % d->num_kv_heads) return FP8KV_EINVAL;
+  if (d->page_size < 1 || d->max_kv_len < 0 || d->max_blocks < 0 || d->num_kv_blocks < 1) return FP8KV_EINVAL;
+  if ((int64_t)d->max_blocks * d->page_size < d->max_kv_len) return FP8KV_EINVAL;
+  if (d->window < 0 || d->sinks < 0 || (d->window == 0 && d->sinks > 0)) return FP8KV_EINVAL;
+  if (d->dtype != FP8KV_DTYPE_F16 && d->dtype != FP8KV_DTYPE_BF16) return FP8KV_EINVAL;
+  if (d->num_sms < 0 || d->num_splits < 0 || d->num_splits > 65535) return FP8KV_EINVAL;
+  if (d->kernel < FP8KV_CHUNK_AUTO || d->kernel > FP8KV_CHUNK_TILE) return FP8KV_EINVAL;
+  if (d->kv_format == FP8KV_KV_BF16) return FP8KV_EUNSUPPORTED;
+  if (!fp8_format(d->kv_format)) return FP8KV_EINVAL;
+  if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return FP8KV_EUNSUPPORTED;
+  // 32-bit positions, packed rows and grid sizes
+  const int64_t group = d->num_q_heads / d->num_kv_heads;
+  if (d->total_q > (1 << 30) || d->max_q > (1 << 24) || d->max_kv_len > (1 << 30) || d->num_kv_heads > 65535 ||
+      d->max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32))
+    return FP8KV_EUNSUPPORTED;
+  if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > kChunkStreamRows) return FP8KV_EUNSUPPORTED;
+
+  int sms = d->num_sms;
+  if (sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ECUDA;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FP8KV_ECUDA;
+    if (sms < 1) return FP8KV_ECUDA;
+  }
+
+  fp8kv_chunk_plan_t P;
+  std::memset(&P, 0, sizeof(P));
+  P.revision = FP8KV_ATTN_REVISION;
+  P.batch = d->batch;
+  P.total_q = d->total_q;
+  // no request has more new tokens than there are rows
+  P.max_q = std::min(d->max_q, std::max(d->total_q, 1));
+  P.num_q_heads = d->num_q_heads;
+  P.num_kv_heads = d->num_kv_heads;
+  P.head_dim = d->head_dim;
+  P.page_size = d->page_size;
+  P.max_kv_len = d->max_kv_len;
+  P.max_blocks = d->max_blocks;
+  P.num_kv_blocks = d->num_kv_blocks;
+  // a window that reaches back over every context is none
+  P.window = d->window >= d->max_kv_len ? 0 : d->window;
+  P.sinks = P.window ? std::min(d->sinks, d->max_kv_len) : 0;
+  P.dtype = d->dtype;
+  P.kv_format = d->kv_format;
+  P.group = (int32_t)group;
+  P.num_sms = sms;
+
+  const int64_t rows = P.max_q * group;  // query vectors per (request, KV head)
+  P.kernel = d->kernel ? d->kernel : FP8KV_CHUNK_STREAM;
+  // positions that one CTA's rows see at most
+  int64_t seen = P.max_kv_len;
+  const int64_t chunks = ceil_div(rows, kChunkStreamRows);
+  if (P.window) seen = std::min<int64_t>(seen, (int64_t)P.window + P.sinks + P.max_q - 1);
+
+  int64_t S = 1, most = 1;
+  if (P.kernel == FP8KV_CHUNK_STREAM) {
+    if (chunks > 65535) return FP8KV_EUNSUPPORTED;
+    const int64_t units = (int64_t)P.batch * P.num_kv_heads * chunks;
+    const int64_t slots = (int64_t)sms * (P.head_dim == 64 ? 4 : P.head_dim == 128 ? 3 : 2);
+    most = std::max<int64_t>(1, ceil_div(seen, 4 * kChunkStreamBlock));
+    S = units ? slots / units : 1;
+  }
+  S = std::max<int64_t>(1, std::min(S, most));
+  if (d->num_splits) S = d->num_splits;
+  if (P.batch > 0 && P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;
+  P.num_splits = (int32_t)S;
+
+  const int64_t nvec = S > 1 ? S * P.total_q * P.num_q_heads : 0;
+  P.partial_offset = 256;
+  P.ml_offset = align_up(P.partial_offset + nvec * P.head_dim * 4, 256);
+  P.workspace_bytes = align_up(P.ml_offset + nvec * 8, 256);
+  *plan = P;
+  return FP8KV_OK;
+}
+
+namespace {
+
+int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, ChunkParams* p) {
+  if (!plan || !a) return FP8KV_EINVAL;
+  if (plan->revision != FP8KV_ATTN_REVISION) return FP8KV_EVERSION;
+  std::memset(p, 0, sizeof(*p));
+  if (plan->kernel != FP8KV_CHUNK_STREAM && plan->kernel != FP8KV_CHUNK_TILE) return FP8KV_EINVAL;
+  if (plan->num_splits < 1 || plan->group < 1 || plan->page_size < 1 || !fp8_format(plan->kv_format) ||
+      (plan->dtype != FP8KV_DTYPE_F16 && plan->dtype != FP8KV_DTYPE_BF16))
+    return FP8KV_EINVAL;
+  if (!a->workspace || !aligned(a->workspace, 256)) return FP8KV_EINVAL;
+  if ((int64_t)a->workspace_bytes < plan->workspace_bytes) return FP8KV_EWORKSPACE;
+  if (plan->batch == 0 || plan->total_q == 0) return FP8KV_OK;
+  const void* ptrs[] = {a->q, a->out, a->k_cache, a->v_cache};
+  for (const void* x : ptrs)
+    if (!x || !aligned(x, 16)) return FP8KV_EINVAL;
+  const int64_t es[] = {a->q_stride_token, a->q_stride_head, a->out_stride_token, a->out_stride_head};
+  const int64_t bs[] = {a->k_stride_block, a->k_stride_token, a->k_stride_head,
+                        a->v_stride_block, a->v_stride_token, a->v_stride_head};
+  if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
+  if (!a->cu_q || !a->kv_len || !aligned(a->cu_q, 4) || !aligned(a->kv_len, 4)) return FP8KV_EINVAL;
+  if (plan->max_kv_len > 0 && (!a->block_table || !aligned(a->block_table, 4))) return FP8KV_EINVAL;
+  if (a->block_table_stride < plan->max_blocks) return FP8KV_EINVAL;
+  if (!std::isfinite(a->softmax_scale)) return FP8KV_EINVAL;
+  if (!a->k_scale_dev && !std::isfinite(a->k_scale)) return FP8KV_EINVAL;
+  if (!a->v_scale_dev && !std::isfinite(a->v_scale)) return FP8KV_EINVAL;
+
+  p->B = plan->batch;
+  p->total_q = plan->total_q;
+  p->max_q = plan->max_q;
+  p->Hq = plan->num_q_heads;
+  p->Hkv = plan->num_kv_heads;
+  p->G = plan->group;
+  p->S = plan->num_splits;
+  p->page_size = plan->page_size;
+  p->page_div = plan->page_size >= 2 ? ~0ull / (uint64_t)plan->page_size + 1 : 0ull;
+  p->max_kv_len = plan->max_kv_len;
+  p->num_kv_blocks = plan->num_kv_blocks;
+  p->window = plan->window;
+  p->sinks = plan->sinks;
+  p->row_tiles = plan->row_tiles;
+  p->q = reinterpret_cast<const uint16_t*>(a->q);
+  p->q_st = a->q_stride_token;
+  p->q_sh = a->q_stride_head;
+  p->out = reinterpret_cast<uint16_t*>(a->out);
+  p->o_st = a->out_stride_token;
+  p->o_sh = a->out_stride_head;
+  p->k_cache = a->k_cache;
+  p->v_cache = a->v_cache;
+  p->ksb = bs[0];
+  p->kst = bs[1];
+  p->ksh = bs[2];
+  p->vsb = bs[3];
+  p->vst = bs[4];
+  p->vsh = bs[5];
+  p->block_table = a->block_table;
+  p->bt_stride = a->block_table_stride;
+  p->cu_q = a->cu_q;
+  p->kv_len = a->kv_len;
+  p->softmax_scale = a->softmax_scale;
+  p->k_scale = a->k_scale;
+  p->v_scale = a->v_scale;
+  p->k_scale_dev = a->k_scale_dev;
+  p->v_scale_dev = a->v_scale_dev;
+  char* ws = reinterpret_cast<char*>(a->workspace);
+  p->status = reinterpret_cast<unsigned int*>(ws);
+  p->partial = reinterpret_cast<float*>(ws + plan->partial_offset);
+  p->ml = reinterpret_cast<float2*>(ws + plan->ml_offset);
+  return FP8KV_OK;
+}
+
+}  // namespace
+
+extern "C" int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, fp8kv_stream_t stream) {
+  ChunkParams p;
+  const int rc = build_chunk(plan, a, &p);
+  if (rc != FP8KV_OK || plan->batch == 0 || plan->total_q == 0) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_chunk_stream(plan, p, st);
+  if (e == cudaSuccess && p.S > 1) e = launch_chunk_join(plan, p, st);
+  return done(e);
+}
+
+extern "C" int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_stream_t stream) {
+  if (!a) return FP8KV_EINVAL;
+  if (a->batch < 0 || a->total < 0 || a->num_kv_heads < 1 || a->page_size < 1 || a->max_blocks < 1 ||
+      a->num_kv_blocks < 1)
+    return FP8KV_EINVAL;
+  if (a->head_dim < 16 || a->head_dim > 1024 || a->head_dim % 16) return FP8KV_EINVAL;
+  if (a->dtype != FP8KV_DTYPE_F16 && a->dtype != FP8KV_DTYPE_BF16 && a->dtype != FP8KV_DTYPE_F32)
+    return FP8KV_EINVAL;
+  if (!fp8_format(a->kv_format)) return FP8KV_EINVAL;
+  if (a->batch == 0 || a->total == 0) return FP8KV_OK;
+  const void* ptrs[] = {a->k_cache, a->v_cache, a->k_out, a->v_out};
+  for (const void* x : ptrs)
+    if (!x || !aligned(x, 16)) return FP8KV_EINVAL;
+  const int64_t es[] = {a->ko_stride_token, a->ko_stride_head, a->vo_stride_token, a->vo_stride_head};
+  const int64_t bs[] = {a->kc_stride_block, a->kc_stride_token, a->kc_stride_head,
+                        a->vc_stride_block, a->vc_stride_token, a->vc_stride_head};
+  if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
+  if (!a->block_table || !a->cu_len || a->block_table_stride < a->max_blocks) return FP8KV_EINVAL;
+  if (!aligned(a->block_table, 4) || !aligned(a->cu_len, 4) || !aligned(a->start, 4)) return FP8KV_EINVAL;
+  if (!a->k_scale_dev && !std::isfinite(a->k_scale)) return FP8KV_EINVAL;
+  if (!a->v_scale_dev && !std::isfinite(a->v_scale)) return FP8KV_EINVAL;
+  return done(launch_cache_read(*a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t stream) {
+  if (!a) return FP8KV_EINVAL;
+  if (a->num_tokens < 0 || a->num_kv_heads < 1) return FP8KV_EINVAL;
+  if (a->head_dim < 16 || a->head_dim > 1024 || a->head_dim % 16) return FP8KV_EINVAL;
+  if (a->dtype != FP8KV_DTYPE_F16 && a->dtype != FP8KV_DTYPE_BF16) return FP8KV_EINVAL;
+  if (!fp8_format(a->kv_format)) return FP8KV_EINVAL;
+  if (a->num_tokens == 0) return FP8KV_OK;
+  if (!a->k || !a->v || !aligned(a->k, 16) || !aligned(a->v, 16)) return FP8KV_EINVAL;
+  const int64_t es[] = {a->k_stride_token, a->k_stride_head, a->v_stride_token, a->v_stride_head};
+  if (!strides_ok(es, 4, 8) || !aligned(a->slot_mapping, 8)) return FP8KV_EINVAL;
+  if (!a->k_scale || !a->v_scale || a->k_scale == a->v_scale || !aligned(a->k_scale, 4) || !aligned(a->v_scale, 4))
+    return FP8KV_EINVAL;
+  return done(launch_calibrate(*a, reinterpret_cast<cudaStream_t>(stream)));
+}

@@ -1,0 +1,504 @@
+// Chunk attention for few query vectors (at most 16 per CTA: the query heads
+// of one KV head times a few new tokens): bound by streaming the cache.
+//
+// One CTA of four warps per (request, KV head, partition, 16 query vectors); each warp walks
+// blocks of 16 virtual tokens (chunk_span) on its own, with no barrier and no
+// shared memory in the loop, and the four are joined at the end.  The FP8
+// bytes go from global memory straight into the registers of the MMA that
+// uses them:
+//   S[16 x 8 tokens] = Q . K^T, m16n8k16: a lane of the B operand needs four
+//     d of one token, so lane (n = lane/4, c = lane%4) loads the 16-byte pieces c, c + 4, ... of token n's row; each 32-bit word
+//     decodes to one MMA's B fragment, and the d that a word holds is simply
+//     the order in which Q's A fragments are laid out;
+//   O[16 x D] += P . V: a B fragment needs two tokens of one d in a register,
+//     so the lane loads the same 16-byte piece n of tokens 2c, 2c+1, 2c+8,
+//     2c+9 (a warp reads whole rows) and interleaves their bytes before the
+//     decode; P's fragment is what S's accumulators already hold.
+// So a warp needs about 150 instructions per 4 KB of K and V.  Legacy
+// mma.sync rather than tcgen05: with 4 to 16 useful rows the products are a
+// few percent of the tensor peak, and TMEM or shared-memory operands would
+// only add copies and barriers to a kernel whose time is the bytes' arrival.
+//
+// With at most 8 query vectors the upper 8 rows of P's fragment are free:
+// they carry P_lo = 2^11 (p - fp16(p)), which makes the probabilities good
+// to 22 bits at no cost.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "chunk_common.cuh"
+#include "internal.h"
+
+namespace fp8kv {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreadsS = 32 * kWarps;
+constexpr int kBlk = kChunkStreamBlock;
+constexpr int kR = kChunkStreamRows;
+constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;
+
+template <int D>
+struct StreamCfg {
+  static constexpr int kKP = D / 64;                 // 16-byte pieces of a K row per lane
+  static constexpr int kVP = D >= 128 ? D / 128 : 1; // pieces of a V row per lane
+  static constexpr int kVWords = D >= 128 ? 4 : 2;   // 32-bit words per piece
+  static constexpr int kNT = D / 8;                  // n-tiles of O
+  static constexpr int kQStride = D + 8;             // fp16 elements (padding: fragment loads without conflicts)
+  static constexpr bool kQRegs = D <= 128;           // Q's fragments stay in registers
+  static constexpr int kCtas = D == 64 ? 4 : D == 128 ? 3 : 2;  // resident per SM
+  static constexpr int kQBytes = kR * kQStride * 2;
+  static constexpr int kOBytes(int rows) { return kWarps * rows * D * 4; }
+  // Q, then the warps' numerators (their place also holds the non-finite marks)
+  static constexpr int smem(bool wide) { return kQBytes + kOBytes(wide ? 16 : 8) + 1024; }
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes that no other CTA soon reads: not kept in L1.
+__device__ __forceinline__ uint4 ld_stream16(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint4 ld_stream8(const uint8_t* p) {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4& w, int i) {
+  return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+}
+
+template <int D, int FMT, int DT, bool WIDE>
+__global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(const ChunkParams p) {
+  using C = StreamCfg<D>;
+  constexpr int ROWS = WIDE ? 16 : 8;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint16_t* sQ = reinterpret_cast<uint16_t*>(smem);
+  float* sO = reinterpret_cast<float*>(smem + C::kQBytes);                  // [warp][ROWS][D]
+  float* sM = reinterpret_cast<float*>(smem + C::kQBytes + C::kOBytes(ROWS));  // [warp][16]
+  float* sL = sM + kWarps * 16;
+  float* sBack = sL + kWarps * 16;                                          // [16] inverse row scales
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rq = lane >> 2, c = lane & 3;
+  const int b = blockIdx.x / p.S, s = blockIdx.x - b * p.S;
+  const int g = blockIdx.y;
+  const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
+  const ChunkRequest req = chunk_request(p, b);
+  if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
+  const int RC = min(kR, req.n * p.G - row_first);
+  if (RC <= 0) return;
+  const int64_t plane = (int64_t)p.total_q * p.Hq;
+  auto vec_of = [&](int r) {
+    const int rr = row_first + r;
+    return (int64_t)(req.row0 + rr / p.G) * p.Hq + g * p.G + rr % p.G;
+  };
+
+  const ChunkSpan span = chunk_span(p, req, row_first / p.G, (row_first + RC - 1) / p.G);
+  int per = (span.U + p.S - 1) / p.S;
+  per = (per + kBlk * kWarps - 1) / (kBlk * kWarps) * (kBlk * kWarps);
+  const int u0 = min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
+  if (u0 >= u1 && p.S > 1) {
+    if (tid < RC) p.ml[s * plane + vec_of(tid)] = make_float2(kNoMax, 0.f);
+    return;
+  }
+
+  // Places of a block's 16 tokens, one per lane (both halves of the warp hold them).
+  const uint8_t* kbase = p.k_cache + g * p.ksh;
+  const uint8_t* vbase = p.v_cache + g * p.vsh;
+  int64_t koff, voff;
+  uint32_t vnext;  // which of them hold data
+  auto find = [&](int t) {
+    const int v = t + (lane & 15);
+    bool ok = v < u1;
+    koff = voff = 0;
+    if (ok) {
+      int64_t blk;
+      int slot;
+      ok = chunk_place(p, b, span.position(v), blk, slot);
+      if (ok) {
+        koff = blk * p.ksb + (int64_t)slot * p.kst;
+        voff = blk * p.vsb + (int64_t)slot * p.vst;
+      } else {
+        set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
+      }
+    }
+    vnext = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
+  };
+  uint4 kr[2][C::kKP], vr[4][C::kVP];
+  auto load_k = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t off = __shfl_sync(0xffffffffu, koff, rq + 8 * h);
+      const bool ok = (vnext >> (rq + 8 * h)) & 1u;
+#pragma unroll
+      for (int i = 0; i < C::kKP; ++i)
+        kr[h][i] = ok ? ld_stream16(kbase + off + (c + 4 * i) * 16) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = 2 * c + (j & 1) + 8 * (j >> 1);
+      const int64_t off = __shfl_sync(0xffffffffu, voff, t);
+      const bool ok = (vnext >> t) & 1u;
+#pragma unroll
+      for (int i = 0; i < C::kVP; ++i) {
+        if (D >= 128)
+          vr[j][i] = ok ? ld_stream16(vbase + off + (rq + 8 * i) * 16) : make_uint4(0, 0, 0, 0);
+        else
+          vr[j][i] = ok ? ld_stream8(vbase + off + rq * 8) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  const int t_first = u0 + kBlk * warp;
+  find(t_first);
+  load_k();
+  load_v();
+
+  // Q -> shared memory as fp16 (bf16 rows scaled by a power of two); rows past
+  // RC are zero.  One warp per row.
+  float sign = 1.f;
+  const float ks = p.k_scale_dev ? *p.k_scale_dev : p.k_scale;
+  const double cd = (double)p.softmax_scale * (double)ks * 1.4426950408889634074;
+  if (cd < 0) sign = -1.f;  // logit factors are non-negative from here on
+  for (int r = warp; r < kR; r += kWarps) {
+    constexpr int V = D / 32;  // elements per lane
+    uint32_t w[V / 2] = {};
+    if (r < RC) {
+      const int rr = row_first + r;
+      const uint16_t* src = p.q + (int64_t)(req.row0 + rr / p.G) * p.q_st + (int64_t)(g * p.G + rr % p.G) * p.q_sh;
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + lane * V + 2 * j);
+    }
+    RowScale rs = {1.f, 1.f};
+    float f[V];
+    if (DT == FP8KV_DTYPE_BF16) {
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        // as integers: a NaN is larger than every number, and is not dropped
+        amax = __uint_as_float(max(__float_as_uint(amax), max(__float_as_uint(fabsf(f[2 * j])),
+                                                              __float_as_uint(fabsf(f[2 * j + 1])))));
+      }
+      rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = pack_half2(f[2 * j] * rs.to_f16, f[2 * j + 1] * rs.to_f16);
+    }
+    if (sign < 0.f)
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] ^= 0x80008000u;
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j)
+      *reinterpret_cast<uint32_t*>(sQ + r * C::kQStride + lane * V + 2 * j) = w[j];
+    if (lane == 0) sBack[r] = rs.back;
+  }
+  __syncthreads();
+  const float c0f = (float)(fabs(cd) * sBack[rq]), c1f = (float)(fabs(cd) * sBack[rq + 8]);
+
+  // What this lane's two rows see; rows past RC see everything (their values are dropped).
+  ChunkRow row0 = {INT_MAX, INT_MIN}, row1 = {INT_MAX, INT_MIN};
+  if (rq < RC) row0 = chunk_row(p, req, span, (row_first + rq) / p.G);
+  if (rq + 8 < RC) row1 = chunk_row(p, req, span, (row_first + rq + 8) / p.G);
+  const int hi_min = __reduce_min_sync(0xffffffffu, min(row0.hi, row1.hi));
+  const int lo_max = __reduce_max_sync(0xffffffffu, max(row0.lo, row1.lo));
+
+  // Q's A fragments: step (i, w) covers d = 16 (c + 4 i) + 4 w + {0..3} of lane c
+  auto q_frag = [&](int i, int w, uint32_t (&a)[4]) {
+    const int d = (c + 4 * i) * 16 + 4 * w;
+    const uint2 x = *reinterpret_cast<const uint2*>(sQ + rq * C::kQStride + d);
+    a[0] = x.x;
+    a[2] = x.y;
+    if (WIDE) {
+      const uint2 y = *reinterpret_cast<const uint2*>(sQ + (rq + 8) * C::kQStride + d);
+      a[1] = y.x;
+      a[3] = y.y;
+    } else {
+      a[1] = a[3] = 0u;
+    }
+  };
+  uint32_t qa[C::kQRegs ? D / 16 : 1][4];
+  if (C::kQRegs) {
+#pragma unroll
+    for (int i = 0; i < C::kKP; ++i)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) q_frag(i, w, qa[C::kQRegs ? i * 4 + w : 0]);
+  }
+
+  float o[C::kNT][4];
+  float m0, m1, l0, l1;
+  bool zap = false;  // second pass: non-finite V codes enter as 0
+  while (true) {
+#pragma unroll
+    for (int n = 0; n < C::kNT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    m0 = m1 = kNoMax;
+    l0 = l1 = 0.f;
+    uint32_t valid = vnext;
+    if (t_first < u1) find(t_first + kBlk * kWarps);
+    for (int t = t_first; t < u1; t += kBlk * kWarps) {
+      float sc[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < C::kKP; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t b0, b1;
+            fp8x4_to_f16<FMT>(word(kr[h][i], w), b0, b1);
+            if (C::kQRegs) {
+              mma16816(sc[h], qa[C::kQRegs ? i * 4 + w : 0], b0, b1);
+            } else {
+              uint32_t a[4];
+              q_frag(i, w, a);
+              mma16816(sc[h], a, b0, b1);
+            }
+          }
+      }
+      if (t + kBlk * kWarps < u1) load_k();  // of the next block
+      // base-2 logits; tokens that a row does not see by selection
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sc[h][0] *= c0f;
+        sc[h][1] *= c0f;
+        if (WIDE) {
+          sc[h][2] *= c1f;
+          sc[h][3] *= c1f;
+        }
+      }
+      if (valid != 0xFFFFu || t + kBlk > hi_min || !(t >= lo_max || t + kBlk <= span.sk)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int x = 8 * h + 2 * c + e, v = t + x;
+            const bool ok = (valid >> x) & 1u;
+            if (!(ok && v < row0.hi && (v >= row0.lo || v < span.sk))) sc[h][e] = -INFINITY;
+            if (WIDE && !(ok && v < row1.hi && (v >= row1.lo || v < span.sk))) sc[h][2 + e] = -INFINITY;
+          }
+      }
+      const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      const float x1 = WIDE ? fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) : -INFINITY;
+      if (__any_sync(0xffffffffu, (x0 > -INFINITY && !(x0 <= m0 + kChunkTau)) ||
+                                      (x1 > -INFINITY && !(x1 <= m1 + kChunkTau)))) {
+        // a row's running maximum moves (integers: rescaling is exact)
+        float y0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, 2));
+        float y1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, 2));
+        const float n0 = y0 > m0 + kChunkTau || m0 == kNoMax ? fmaxf(m0, ceilf(y0)) : m0;
+        const float n1 = y1 > m1 + kChunkTau || m1 == kNoMax ? fmaxf(m1, ceilf(y1)) : m1;
+        const float a0 = n0 == m0 ? 1.f : exp2_int(m0 - n0), a1 = n1 == m1 ? 1.f : exp2_int(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int n = 0; n < C::kNT; ++n) {
+          o[n][0] *= a0;
+          o[n][1] *= a0;
+          o[n][2] *= WIDE ? a1 : a0;
+          o[n][3] *= WIDE ? a1 : a0;
+        }
+      }
+      const float s0 = (m0 == kNoMax ? 0.f : m0) - kChunkPShift, s1 = (m1 == kNoMax ? 0.f : m1) - kChunkPShift;
+      uint32_t pa[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = fast_exp2(sc[h][0] - s0), p1 = fast_exp2(sc[h][1] - s0);
+        l0 += p0 + p1;
+        pa[2 * h] = pack_half2(p0, p1);
+        if (WIDE) {
+          const float p2 = fast_exp2(sc[h][2] - s1), p3 = fast_exp2(sc[h][3] - s1);
+          l1 += p2 + p3;
+          pa[2 * h + 1] = pack_half2(p2, p3);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&pa[2 * h]));
+          pa[2 * h + 1] = pack_half2((p0 - f.x) * kLoUp, (p1 - f.y) * kLoUp);
+        }
+      }
+      if (zap) {
+        constexpr bool e5 = FMT == FP8KV_KV_E5M2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < C::kVP; ++i)
+            vr[j][i] = make_uint4(zap_nonfinite(vr[j][i].x, e5), zap_nonfinite(vr[j][i].y, e5),
+                                  zap_nonfinite(vr[j][i].z, e5), zap_nonfinite(vr[j][i].w, e5));
+      }
+#pragma unroll
+      for (int i = 0; i < C::kVP; ++i)
+#pragma unroll
+        for (int w = 0; w < C::kVWords; ++w) {
+          uint32_t f[2][4];  // [token pair][d of the word]
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t wa = word(vr[2 * j][i], w), wb = word(vr[2 * j + 1][i], w);
+            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[j][0], f[j][1]);
+            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[j][2], f[j][3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma16816(o[(i * C::kVWords + w) * 4 + e], pa, f[0][e], f[1][e]);
+        }
+      valid = vnext;
+      if (t + kBlk * kWarps < u1) {
+        load_v();
+        find(t + 2 * kBlk * kWarps);
+      }
+    }
+    if (zap) break;
+    // Non-finite sums: maybe only from codes of tokens that some rows do not see (0 * NaN).
+    float bad = 0.f;
+#pragma unroll
+    for (int n = 0; n < C::kNT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad = fmaf(o[n][e], 0.f, bad);
+    if (!__syncthreads_or(bad != 0.f)) break;
+    zap = true;
+    find(t_first);
+    load_k();
+    load_v();
+  }
+
+  // ------------------------------------------------------------ join the warps
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  if (c == 0) {
+    sM[warp * 16 + rq] = m0;
+    sL[warp * 16 + rq] = l0;
+    if (WIDE) {
+      sM[warp * 16 + rq + 8] = m1;
+      sL[warp * 16 + rq + 8] = l1;
+    }
+  }
+  // n-tile (i, x) column n of O is d = 128 i + PB n + x, PB the bytes of a V piece
+  constexpr int PB = 4 * C::kVWords;
+#pragma unroll
+  for (int i = 0; i < C::kVP; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int x = 0; x < PB; x += 4) {
+        const int d = 128 * i + PB * (2 * c + e) + x;
+        float f[4], h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k] = o[i * PB + x + k][e];
+          h[k] = o[i * PB + x + k][2 + e];
+          if (!WIDE) f[k] = fmaf(h[k], kLoDown, f[k]);
+        }
+        *reinterpret_cast<float4*>(sO + (warp * ROWS + rq) * D + d) = make_float4(f[0], f[1], f[2], f[3]);
+        if (WIDE)
+          *reinterpret_cast<float4*>(sO + (warp * ROWS + rq + 8) * D + d) = make_float4(h[0], h[1], h[2], h[3]);
+      }
+  __syncthreads();
+  const float vs = p.v_scale_dev ? *p.v_scale_dev : p.v_scale;
+  constexpr int kIter = (ROWS * D / 4 + kThreadsS - 1) / kThreadsS;
+  float4 acc[kIter];
+  float Ls[kIter];
+#pragma unroll
+  for (int k = 0; k < kIter; ++k) {
+    const int x = tid + k * kThreadsS;
+    const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    Ls[k] = 0.f;
+    if (r >= RC) continue;
+    float M = kNoMax;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w * 16 + r]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = sM[w * 16 + r], lw = sL[w * 16 + r];
+      if (mw == kNoMax && lw == 0.f) continue;
+      const float a = mw == M ? 1.f : exp2_int(mw - M);
+      Ls[k] = fmaf(a, lw, Ls[k]);
+      const float4 y = *reinterpret_cast<const float4*>(sO + (w * ROWS + r) * D + d);
+      acc[k].x = fmaf(a, y.x, acc[k].x);
+      acc[k].y = fmaf(a, y.y, acc[k].y);
+      acc[k].z = fmaf(a, y.z, acc[k].z);
+      acc[k].w = fmaf(a, y.w, acc[k].w);
+    }
+    if (p.S > 1 && d == 0) p.ml[s * plane + vec_of(r)] = make_float2(M, Ls[k] * kChunkInvPShift);
+  }
+  uint32_t* kinds = reinterpret_cast<uint32_t*>(sO);
+  if (zap) {
+    __syncthreads();
+    mark_nonfinite_v<D, FMT>(p, kinds, b, g, u0, u1, span, RC,
+                             [&](int i) { return chunk_row(p, req, span, (row_first + i) / p.G); });
+  }
+#pragma unroll
+  for (int k = 0; k < kIter; ++k) {
+    const int x = tid + k * kThreadsS;
+    const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+    if (r >= RC) continue;
+    float y[4] = {acc[k].x, acc[k].y, acc[k].z, acc[k].w};
+    const bool dead = Ls[k] == 0.f;
+    const float f = p.S > 1 ? kChunkInvPShift : (dead ? 0.f : vs / Ls[k]);
+    const uint32_t kd = zap ? kinds[r * (D / 4) + d / 4] : 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      y[j] *= f;
+      const uint32_t kind = (kd >> (8 * j)) & 0xFFu;
+      if (kind) y[j] = nonfinite_value(kind) * (p.S > 1 ? 1.f : vs);
+    }
+    if (p.S > 1) {
+      *reinterpret_cast<float4*>(p.partial + (s * plane + vec_of(r)) * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+      const int rr = row_first + r;
+      uint16_t* dst = p.out + (int64_t)(req.row0 + rr / p.G) * p.o_st + (int64_t)(g * p.G + rr % p.G) * p.o_sh + d;
+      *reinterpret_cast<uint2*>(dst) =
+          dead ? make_uint2(0u, 0u) : make_uint2(pack_out<DT>(y[0], y[1]), pack_out<DT>(y[2], y[3]));
+    }
+  }
+}
+
+template <int D, int FMT, int DT, bool WIDE>
+cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  auto fn = chunk_stream<D, FMT, DT, WIDE>;
+  constexpr int smem = StreamCfg<D>::smem(WIDE);
+  static DeviceOnce once;
+  cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
+  const int chunks = (int)(((int64_t)p.max_q * p.G + kR - 1) / kR);
+  fn<<<dim3((unsigned)(p.B * p.S), p.Hkv, chunks), kThreadsS, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int FMT, int DT>
+cudaError_t pick_wide(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  return (int64_t)p.max_q * p.G > 8 ? run<D, FMT, DT, true>(plan, p, st) : run<D, FMT, DT, false>(plan, p, st);
+}
+
+template <int D>
+cudaError_t pick(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  constexpr int E4 = FP8KV_KV_E4M3, E5 = FP8KV_KV_E5M2, F16 = FP8KV_DTYPE_F16, BF16 = FP8KV_DTYPE_BF16;
+  if (plan->kv_format == E5)
+    return plan->dtype == BF16 ? pick_wide<D, E5, BF16>(plan, p, st) : pick_wide<D, E5, F16>(plan, p, st);
+  return plan->dtype == BF16 ? pick_wide<D, E4, BF16>(plan, p, st) : pick_wide<D, E4, F16>(plan, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_stream(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  switch (plan->head_dim) {
+    case 64: return pick<64>(plan, p, st);
+    case 128: return pick<128>(plan, p, st);
+    default: return pick<256>(plan, p, st);
+  }
+}
+
+}  // namespace fp8kv

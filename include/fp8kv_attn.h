@@ -369,6 +369,190 @@ typedef struct {
 
 int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Chunk attention: a ragged batch of new tokens over the paged FP8 cache.
+ *
+ * Request b brings the new tokens cu_q[b] .. cu_q[b+1]-1 of q; they are the
+ * last n_b = cu_q[b+1] - cu_q[b] of its kv_len[b] positions, and their K and V
+ * rows are in the cache already (fp8kv_attn_cache_write on the same stream).
+ * New token i stands at position p = kv_len[b] - n_b + i, and its query heads
+ * attend to the positions
+ *
+ *   j <= p                                   window = 0
+ *   j <= p and (p - j < window or j < sinks) window > 0
+ *
+ * with the logits, scales and cache addressing of fp8kv_attn_split.  So one
+ * call serves a piece of a long prompt, whole prompts, single new tokens, and
+ * any mixture of them; with a window, layers that keep the last `window`
+ * positions and the first `sinks`.  Positions outside of a request's windows
+ * are never read.  A token that sees nothing (kv_len[b] < n_b puts it before
+ * position 0) yields +0.0, rows of q from cu_q[B] on are left as they are.
+ *
+ * Numerical contract: FP32 logits, running maximum and sum; probabilities
+ * enter the PV product as fp16 (2^-11 of their own value; groups of at most 8
+ * query vectors: as two fp16 halves), accumulated in FP32, and a context is
+ * split where one FP32 sum would run over more than 32768 positions; one
+ * rounding to q's type at the end.  bf16 queries are scaled to fp16 per row by
+ * a power of two, which is exact for elements above 2^-28 of the row's
+ * largest.
+ *
+ * Device-side anomalies set FP8KV_STATUS_* bits in the workspace's first word
+ * as in fp8kv_attn_split: a position in an out-of-range block counts as not
+ * visible (BAD_BLOCK); a kv_len outside [0, max_kv_len], a cu_q that
+ * decreases or leaves [0, total_q], and more than max_q new tokens of a
+ * request are clamped (BAD_LEN; new tokens past max_q are not computed).
+ *
+ * Two calls that may overlap on the GPU need a workspace each.  The calls are
+ * graph-capturable: lengths may change between replays within the plan.
+ * ------------------------------------------------------------------------ */
+#define FP8KV_CHUNK_AUTO 0
+#define FP8KV_CHUNK_STREAM 1 /* at most 16 query vectors per (request, KV head): max_q * Hq/Hkv <= 16 */
+#define FP8KV_CHUNK_TILE 2   /* tcgen05 tiles of 128 query vectors */
+
+typedef struct {
+  int32_t batch;         /* B >= 0 requests (0: nothing to do) */
+  int32_t total_q;       /* rows of q and out, >= cu_q[B]; 0..2^30 */
+  int32_t max_q;         /* most new tokens of one request, 1..2^24 */
+  int32_t num_q_heads;   /* Hq >= 1 */
+  int32_t num_kv_heads;  /* Hkv >= 1, Hq % Hkv == 0 */
+  int32_t head_dim;      /* D: 64, 128 or 256 */
+  int32_t page_size;     /* tokens per physical block, >= 1 */
+  int32_t max_kv_len;    /* upper bound of kv_len, 0..2^30 */
+  int32_t max_blocks;    /* block-table columns used per request (>= ceil(max_kv_len/page_size)) */
+  int32_t num_kv_blocks; /* physical blocks in the pool, >= 1 */
+  int32_t window;        /* 0 = every earlier position, else the last `window` positions */
+  int32_t sinks;         /* first positions that stay visible beside the window (0 without one) */
+  int32_t dtype;         /* FP8KV_DTYPE_F16 or FP8KV_DTYPE_BF16 (q and out) */
+  int32_t kv_format;     /* FP8KV_KV_E4M3 or FP8KV_KV_E5M2 (bf16 caches: FP8KV_EUNSUPPORTED) */
+  int32_t num_sms;       /* SMs to plan for; 0 = ask the current device */
+  int32_t num_splits;    /* partitions of the context; 0 = planner's choice */
+  int32_t kernel;        /* FP8KV_CHUNK_* */
+} fp8kv_chunk_desc;
+
+/* Plain data; pass it back unmodified. */
+typedef struct {
+  int32_t revision; /* FP8KV_ATTN_REVISION */
+  int32_t batch, total_q, max_q, num_q_heads, num_kv_heads, head_dim, page_size;
+  int32_t max_kv_len, max_blocks, num_kv_blocks, window, sinks, dtype, kv_format;
+  int32_t group;           /* Hq / Hkv */
+  int32_t kernel;          /* FP8KV_CHUNK_STREAM or FP8KV_CHUNK_TILE */
+  int32_t num_splits;      /* S */
+  int32_t row_tiles;       /* tile kernel: bound of the row tiles of all requests */
+  int32_t num_sms;
+  int64_t partial_offset;  /* workspace: FP32 numerators [S][total_q][Hq][D] (S > 1) */
+  int64_t ml_offset;       /* workspace: FP32 (max, sum) pairs [S][total_q][Hq] (S > 1) */
+  int64_t workspace_bytes; /* minimum workspace size */
+  int32_t reserved[8];
+} fp8kv_chunk_plan_t;
+
+typedef struct {
+  const void* q;          /* (row, head, d) at element row*q_stride_token + head*q_stride_head + d; 16-byte aligned */
+  int64_t q_stride_token, q_stride_head;     /* elements, multiples of 8, >= 0 */
+  void* out;              /* same type and addressing with the out_* values; not overlapping q */
+  int64_t out_stride_token, out_stride_head; /* elements, multiples of 8, >= 0 */
+  const uint8_t* k_cache; /* as fp8kv_attn_args.k_cache */
+  const uint8_t* v_cache;
+  int64_t k_stride_block, k_stride_token, k_stride_head; /* bytes, multiples of 16 */
+  int64_t v_stride_block, v_stride_token, v_stride_head; /* bytes, multiples of 16 */
+  const int32_t* block_table;   /* [B][block_table_stride] physical block ids */
+  int64_t block_table_stride;   /* elements, >= max_blocks */
+  const int32_t* cu_q;          /* [B+1] first row of each request, then the row past the last */
+  const int32_t* kv_len;        /* [B] positions of each request, its new tokens among them */
+  float softmax_scale;          /* logit scale before the K scale */
+  float k_scale, v_scale;       /* host scales (used when the device pointers are NULL) */
+  const float* k_scale_dev;     /* optional device scalars */
+  const float* v_scale_dev;
+  void* workspace;              /* >= plan->workspace_bytes, 256-byte aligned; status word first */
+  size_t workspace_bytes;
+} fp8kv_chunk_args;
+
+/* Validate `d` and fill `plan` (host only). */
+int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan);
+/* Launch the attention on `stream` (one kernel, and a second that joins the
+ * partitions when the plan has more than one). */
+int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, fp8kv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Cache read: rows of the paged cache back as fp16, bf16 or FP32.
+ *
+ * For request b and its rows cu_len[b] .. cu_len[b+1]-1, the i-th of them at
+ * position t = start[b] + i, every KV head h and d:
+ *
+ *   k_out[cu_len[b] + i][h][d] = round(dec(k_cache[block][t % P][h][d]) * k_scale)
+ *
+ * with block = block_table[b][t / P], the product in FP32 and one rounding to
+ * nearest even (an fp16 overflow gives an infinity); NaN and infinite codes
+ * stay what they are.  The inverse of fp8kv_attn_cache_write up to its
+ * quantisation; it takes a prefix out of the pages (to move it, to requantise
+ * it, to run another kernel on it).  A row whose position is negative or past
+ * the block table, or whose block is out of range, becomes +0.0 and sets
+ * FP8KV_STATUS_BAD_BLOCK in *status; rows below cu_len[0] or from cu_len[B] on are
+ * left as they are.  A cu_len that decreases or leaves [0, total] sets
+ * FP8KV_STATUS_BAD_LEN (no row outside [0, total) is ever written).
+ * ------------------------------------------------------------------------ */
+#define FP8KV_DTYPE_F32 2 /* cache read outputs only */
+
+typedef struct {
+  int32_t batch;         /* B >= 0 */
+  int32_t total;         /* rows of k_out and v_out, >= cu_len[B] */
+  int32_t num_kv_heads;  /* Hkv >= 1 */
+  int32_t head_dim;      /* D: a multiple of 16, 16..1024 */
+  int32_t page_size;     /* >= 1 */
+  int32_t max_blocks;    /* block-table columns, >= 1 */
+  int32_t num_kv_blocks; /* >= 1 */
+  int32_t dtype;         /* FP8KV_DTYPE_F16, _BF16 or _F32 */
+  int32_t kv_format;     /* FP8KV_KV_E4M3 or FP8KV_KV_E5M2 */
+  const uint8_t* k_cache;  /* as fp8kv_attn_args.k_cache */
+  const uint8_t* v_cache;
+  int64_t kc_stride_block, kc_stride_token, kc_stride_head; /* bytes, multiples of 16 */
+  int64_t vc_stride_block, vc_stride_token, vc_stride_head;
+  const int32_t* block_table; /* [B][block_table_stride] */
+  int64_t block_table_stride; /* elements, >= max_blocks */
+  const int32_t* cu_len;      /* [B+1] */
+  const int32_t* start;       /* [B] first position of each request; NULL = 0 */
+  void* k_out;                /* (row, h, d) at element row*stride_token + h*stride_head + d; 16-byte aligned */
+  void* v_out;
+  int64_t ko_stride_token, ko_stride_head; /* elements, multiples of 8, >= 0 */
+  int64_t vo_stride_token, vo_stride_head;
+  float k_scale, v_scale;     /* finite (used when the device pointers are NULL) */
+  const float* k_scale_dev;
+  const float* v_scale_dev;
+  uint32_t* status;           /* optional device word, NULL = none */
+} fp8kv_cache_read_args;
+
+int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Scale calibration: the per-tensor scales of rows about to be written.
+ *
+ *   *k_scale = max(*k_scale, max |k| / fmax)       (fmax: 448 or 57344)
+ *
+ * over the finite elements of the tokens with slot_mapping[n] >= 0 (all tokens
+ * when it is NULL), the quotient rounded to nearest in FP32; v likewise.
+ * The scales are device floats that the cache write, the attention calls and
+ * the cache read take as k_scale_dev / v_scale_dev, so "calibrate, write,
+ * attend" is one stream of launches.  They only ever rise: start them at the
+ * smallest positive scale wanted, once per layer; rows already written keep the
+ * scale that they were written with, so calibrate before the first write
+ * that counts.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t num_tokens;     /* N >= 0 (0: nothing to do) */
+  int32_t num_kv_heads;   /* Hkv >= 1 */
+  int32_t head_dim;       /* D: a multiple of 16, 16..1024 */
+  int32_t dtype;          /* FP8KV_DTYPE_F16 or FP8KV_DTYPE_BF16 */
+  int32_t kv_format;      /* FP8KV_KV_E4M3 or FP8KV_KV_E5M2 */
+  const void* k;          /* as fp8kv_cache_write_args.k */
+  const void* v;
+  int64_t k_stride_token, k_stride_head;  /* elements, multiples of 8, >= 0 */
+  int64_t v_stride_token, v_stride_head;
+  const int64_t* slot_mapping;            /* [N], < 0 = token not counted; NULL = all count */
+  float* k_scale;         /* device floats, read and raised; not the same address */
+  float* v_scale;
+} fp8kv_calibrate_args;
+
+int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t stream);
+
 /* Size of the library-owned device scratch used by fp8kv_attn_forward_static
  * (16 MiB; one copy per GPU that loads the library, held until exit). */
 #define FP8KV_STATIC_SCRATCH_BYTES (16u << 20)

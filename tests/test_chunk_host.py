@@ -1,0 +1,224 @@
+"""Host-side tests of the chunk attention, cache read and calibration calls
+(no GPU needed): struct layouts, plans, refusals.  Calls are made only with
+arguments that the host-side validation rejects, or with nothing to do, so
+no kernel is launched.
+"""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 20  # aligned, never dereferenced on the host
+
+
+@pytest.fixture(scope="module")
+def B():
+    from fp8_e4m3_paged_gb300 import build_lib
+
+    build_lib.build()
+    from fp8_e4m3_paged_gb300 import binding
+
+    return binding
+
+
+def test_struct_layouts_match_the_header(B, tmp_path):
+    """Size and field offsets of every new struct, as a C compiler sees them."""
+    structs = {"fp8kv_chunk_desc": B.ChunkDesc, "fp8kv_chunk_plan_t": B.ChunkPlan, "fp8kv_chunk_args": B.ChunkArgs,
+               "fp8kv_cache_read_args": B.CacheReadArgs, "fp8kv_calibrate_args": B.CalibrateArgs}
+    lines = ['#include <stdio.h>', '#include "fp8kv_attn.h"', "int main(void) {"]
+    for name, cls in structs.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("\n".join(lines + ["return 0; }"]))
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    want = []
+    for cls in structs.values():
+        want.append(ctypes.sizeof(cls))
+        want += [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want
+
+
+def _desc(B, **kw):
+    base = dict(batch=3, total_q=100, max_q=64, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16,
+                max_kv_len=4000, max_blocks=250, num_kv_blocks=900, num_sms=152)
+    base.update(kw)
+    return B.make_chunk_desc(**base)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), -1), (dict(total_q=-1), -1), (dict(max_q=0), -1), (dict(num_q_heads=0), -1),
+    (dict(num_q_heads=7), -1), (dict(num_kv_heads=0), -1), (dict(page_size=0), -1), (dict(max_kv_len=-1), -1),
+    (dict(max_blocks=249), -1), (dict(num_kv_blocks=0), -1), (dict(window=-1), -1), (dict(sinks=-1, window=5), -1),
+    (dict(sinks=4), -1), (dict(dtype=2), -1), (dict(kv_format=3), -1), (dict(kv_format=-1), -1),
+    (dict(num_splits=-1), -1), (dict(num_splits=1 << 17), -1), (dict(kernel=3), -1), (dict(num_sms=-1), -1),
+    (dict(kv_format=2), -2), (dict(head_dim=96), -2), (dict(head_dim=0), -2), (dict(kernel=1), -2),
+    (dict(max_q=(1 << 24) + 1), -2), (dict(total_q=(1 << 30) + 1), -2),
+    (dict(max_kv_len=(1 << 30) + 1, max_blocks=(1 << 27)), -2),
+    (dict(num_q_heads=1 << 17, num_kv_heads=1 << 17), -2),
+])
+def test_chunk_plan_rejects(B, kw, code):
+    with pytest.raises(B.Fp8kvError) as e:
+        B.fp8kv_attn_chunk_plan(_desc(B, **kw))
+    assert e.value.code == code
+
+
+def test_chunk_plan_null(B):
+    d = _desc(B)
+    assert B.lib.fp8kv_attn_chunk_plan(None, ctypes.byref(B.ChunkPlan())) == B.EINVAL
+    assert B.lib.fp8kv_attn_chunk_plan(ctypes.byref(d), None) == B.EINVAL
+
+
+def test_chunk_plan_workspace_and_windows(B):
+    for S in (1, 2, 7):
+        p = B.fp8kv_attn_chunk_plan(_desc(B, num_splits=S))
+        n = S * 100 * 8 if S > 1 else 0
+        assert p.num_splits == S and p.revision == B.REVISION
+        assert p.partial_offset >= 4 and p.ml_offset >= p.partial_offset + n * 128 * 4
+        assert p.workspace_bytes >= max(256, p.ml_offset + n * 8) and p.workspace_bytes % 256 == 0
+    # a window that reaches back over every context is none
+    assert B.fp8kv_attn_chunk_plan(_desc(B, window=4000, sinks=4)).window == 0
+    p = B.fp8kv_attn_chunk_plan(_desc(B, window=3999, sinks=1 << 30))
+    assert p.window == 3999 and p.sinks == 4000
+    # no request has more new tokens than there are rows
+    assert B.fp8kv_attn_chunk_plan(_desc(B, total_q=5)).max_q == 5
+    assert B.fp8kv_attn_chunk_plan(_desc(B, batch=0, total_q=0)).workspace_bytes >= 4
+    assert B.fp8kv_attn_chunk_plan(_desc(B, max_q=4)).kernel == B.CHUNK_STREAM
+
+
+def _args(B, plan, **kw):
+    a = B.ChunkArgs()
+    a.q = a.out = a.k_cache = a.v_cache = a.block_table = a.cu_q = a.kv_len = FAKE
+    a.q_stride_token = a.out_stride_token = 1024
+    a.q_stride_head = a.out_stride_head = 128
+    a.k_stride_block = a.v_stride_block = 4096
+    a.k_stride_token = a.v_stride_token = 256
+    a.k_stride_head = a.v_stride_head = 128
+    a.block_table_stride = plan.max_blocks
+    a.softmax_scale = a.k_scale = a.v_scale = 1.0
+    a.workspace, a.workspace_bytes = FAKE, plan.workspace_bytes
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=0), dict(out=0), dict(k_cache=0), dict(v_cache=0), dict(block_table=0), dict(cu_q=0), dict(kv_len=0),
+    dict(workspace=0), dict(q=FAKE + 8), dict(out=FAKE + 2), dict(k_cache=FAKE + 1), dict(workspace=FAKE + 16),
+    dict(cu_q=FAKE + 2), dict(q_stride_token=1020), dict(q_stride_head=-8), dict(out_stride_head=4),
+    dict(k_stride_token=250), dict(v_stride_block=-16), dict(block_table_stride=249),
+    dict(softmax_scale=float("nan")), dict(k_scale=float("inf")), dict(v_scale=float("nan")),
+])
+def test_chunk_rejects_arguments(B, kw):
+    plan = B.fp8kv_attn_chunk_plan(_desc(B))
+    assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(_args(B, plan, **kw)), None) == B.EINVAL
+
+
+def test_chunk_plan_and_workspace_checks(B):
+    plan = B.fp8kv_attn_chunk_plan(_desc(B))
+    assert B.lib.fp8kv_attn_chunk(None, ctypes.byref(_args(B, plan)), None) == B.EINVAL
+    assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), None, None) == B.EINVAL
+    a = _args(B, plan, workspace_bytes=plan.workspace_bytes - 1)
+    assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(a), None) == B.EWORKSPACE
+    plan.revision += 1
+    assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(_args(B, plan)), None) == B.EVERSION
+    # nothing to do: no pointers needed but the workspace
+    for kw in (dict(batch=0), dict(total_q=0)):
+        plan = B.fp8kv_attn_chunk_plan(_desc(B, **kw))
+        a = _args(B, plan, q=0, out=0, k_cache=0, v_cache=0, cu_q=0, kv_len=0, block_table=0)
+        assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(a), None) == B.OK
+
+
+def _read(B, **kw):
+    a = B.CacheReadArgs()
+    a.batch, a.total, a.num_kv_heads, a.head_dim, a.page_size, a.max_blocks, a.num_kv_blocks = 2, 9, 2, 128, 16, 4, 9
+    a.k_cache = a.v_cache = a.block_table = a.cu_len = a.k_out = a.v_out = FAKE
+    a.kc_stride_block = a.vc_stride_block = 4096
+    a.kc_stride_token = a.vc_stride_token = 256
+    a.kc_stride_head = a.vc_stride_head = a.ko_stride_head = a.vo_stride_head = 128
+    a.ko_stride_token = a.vo_stride_token = 256
+    a.block_table_stride = 4
+    a.k_scale = a.v_scale = 1.0
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=-1), dict(total=-1), dict(num_kv_heads=0), dict(head_dim=24), dict(head_dim=0), dict(head_dim=1040),
+    dict(page_size=0), dict(max_blocks=0), dict(num_kv_blocks=0), dict(dtype=3), dict(kv_format=2), dict(k_cache=0),
+    dict(v_cache=FAKE + 8), dict(k_out=0), dict(v_out=FAKE + 2), dict(block_table=0), dict(cu_len=0),
+    dict(start=FAKE + 1), dict(kc_stride_token=8), dict(vc_stride_head=-16), dict(ko_stride_token=4),
+    dict(vo_stride_head=-8), dict(block_table_stride=3), dict(k_scale=float("nan")), dict(v_scale=float("inf")),
+])
+def test_cache_read_rejects(B, kw):
+    assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, **kw)), None) == B.EINVAL
+
+
+def test_cache_read_nothing_to_do(B):
+    assert B.lib.fp8kv_attn_cache_read(None, None) == B.EINVAL
+    for kw in (dict(batch=0), dict(total=0)):
+        assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, k_cache=0, k_out=0, **kw)), None) == B.OK
+
+
+def _cal(B, **kw):
+    a = B.CalibrateArgs()
+    a.num_tokens, a.num_kv_heads, a.head_dim = 5, 2, 128
+    a.k = a.v = a.k_scale = FAKE
+    a.v_scale = FAKE + 4
+    a.k_stride_token = a.v_stride_token = 256
+    a.k_stride_head = a.v_stride_head = 128
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(num_tokens=-1), dict(num_kv_heads=0), dict(head_dim=8), dict(head_dim=1040), dict(dtype=2),
+    dict(kv_format=2), dict(k=0), dict(v=FAKE + 8), dict(k_stride_token=4), dict(v_stride_head=-8),
+    dict(k_scale=0), dict(v_scale=0), dict(v_scale=FAKE), dict(k_scale=FAKE + 2), dict(slot_mapping=FAKE + 4),
+])
+def test_calibrate_rejects(B, kw):
+    assert B.lib.fp8kv_attn_cache_calibrate(ctypes.byref(_cal(B, **kw)), None) == B.EINVAL
+
+
+def test_calibrate_nothing_to_do(B):
+    assert B.lib.fp8kv_attn_cache_calibrate(None, None) == B.EINVAL
+    assert B.lib.fp8kv_attn_cache_calibrate(ctypes.byref(_cal(B, num_tokens=0, k=0, v=0, k_scale=0)), None) == B.OK
+
+
+def test_binding_refuses_tensors_that_do_not_fit(B):
+    """What the struct cannot carry is checked where it is filled."""
+    import torch
+
+    q = torch.zeros(4, 8, 64, dtype=torch.float16)
+    cache = torch.zeros(5, 16, 2, 64, dtype=torch.uint8)
+    good = dict(q=q, out=torch.zeros_like(q), k_cache=cache, v_cache=cache, workspace=torch.zeros(256, dtype=torch.uint8),
+                softmax_scale=1.0, block_table=torch.zeros(2, 3, dtype=torch.int32),
+                cu_q=torch.zeros(3, dtype=torch.int32), kv_len=torch.zeros(2, dtype=torch.int32))
+    B.make_chunk_args(**good)
+    for bad in (dict(q=q.float()), dict(out=q.bfloat16()), dict(out=q[:3]), dict(q=q.transpose(1, 2)),
+                dict(k_cache=cache.float()), dict(v_cache=cache[0]), dict(cu_q=torch.zeros(2, dtype=torch.int32)),
+                dict(kv_len=torch.zeros(2, dtype=torch.int64)), dict(block_table=torch.zeros(2, 3)),
+                dict(k_scale_dev=torch.zeros(2))):
+        with pytest.raises(ValueError):
+            B.make_chunk_args(**{**good, **bad})
+    k = torch.zeros(5, 2, 64, dtype=torch.float16)
+    one = torch.ones(1)
+    B.make_calibrate_args(k=k, v=k, k_scale=one, v_scale=one)
+    for bad in (dict(k=k.float()), dict(v=k[:2]), dict(k_scale=one.double()), dict(v_scale=None),
+                dict(slot_mapping=torch.zeros(5, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            B.make_calibrate_args(**{**dict(k=k, v=k, k_scale=one, v_scale=one), **bad})
+    table, cu = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    good = dict(k_cache=cache, v_cache=cache, block_table=table, cu_len=cu, k_out=k, v_out=k)
+    B.make_cache_read_args(**good)
+    for bad in (dict(k_out=k.double()), dict(v_out=k.bfloat16()), dict(k_out=k[:, :1]), dict(cu_len=cu[:2]),
+                dict(start=cu), dict(block_table=table.long())):
+        with pytest.raises(ValueError):
+            B.make_cache_read_args(**{**good, **bad})

@@ -1,0 +1,322 @@
+"""GPU parity of the chunk attention (fp8kv_attn_chunk) with its definition in 64 bits.
+
+Ragged batches, single tokens, windows with sinks, both cache formats, both
+query types, head dims 64/128/256, page sizes that end inside a tile,
+partitions, strides, dead rows, rows behind the last request, non-finite
+codes, bad blocks and lengths, graph replay, streams.  Every cache slot that no
+new token may see holds a NaN code.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from tests._chunk_ref import Case
+
+pytestmark = pytest.mark.gpu
+
+P_ERR = 2.0 ** -11  # probabilities as fp16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from fp8_e4m3_paged_gb300 import build_lib
+
+    build_lib.build()
+
+
+class Run:
+    """Device buffers and plan of a case."""
+
+    def __init__(self, c, kernel=0, num_splits=0, spread=False, device_scales=False, **over):
+        from fp8_e4m3_paged_gb300 import binding as B
+
+        self.B, self.c = B, c
+        dev = "cuda"
+        self.cu = torch.from_numpy(c.cu).to(dev)
+        self.kv_len = torch.from_numpy(c.kv_len).to(dev)
+        self.table = c.table.to(dev)
+        q, k, v = c.q.to(dev), c.k.to(dev), c.v.to(dev)
+        if spread:  # rows, heads and pages further apart than they need to be
+            qw = torch.zeros(c.total, c.Hq + 1, c.D + 8, dtype=q.dtype, device=dev)
+            qw[:, :c.Hq, :c.D] = q
+            q = qw[:, :c.Hq, :c.D]
+            ow = torch.full((c.total, c.Hq + 2, c.D + 16), 7.0, dtype=q.dtype, device=dev)
+            self.out_all, self.out = ow, ow[:, :c.Hq, :c.D]
+            both = torch.full((c.blocks, c.page, 2, c.Hkv, c.D), 0x7F, dtype=torch.uint8, device=dev)
+            both[:, :, 0], both[:, :, 1] = k, v
+            k, v = both[:, :, 0], both[:, :, 1]
+        else:
+            self.out = torch.full((c.total, c.Hq, c.D), 7.0, dtype=q.dtype, device=dev)
+        self.q, self.k, self.v = q, k, v
+        desc = dict(batch=len(c.requests), total_q=c.total, max_q=c.max_q, num_q_heads=c.Hq, num_kv_heads=c.Hkv,
+                    head_dim=c.D, page_size=c.page, max_kv_len=c.max_kv, max_blocks=c.cols, num_kv_blocks=c.blocks,
+                    window=c.window, sinks=c.sinks,
+                    dtype=B.DTYPE_F16 if c.dtype == torch.float16 else B.DTYPE_BF16,
+                    kv_format=B.KV_E4M3 if c.fmt == "e4m3" else B.KV_E5M2, kernel=kernel, num_splits=num_splits)
+        desc.update(over)
+        self.plan = B.fp8kv_attn_chunk_plan(B.make_chunk_desc(**desc))
+        self.ws = torch.full((self.plan.workspace_bytes,), 0xFF, dtype=torch.uint8, device=dev)
+        self.ws[:4] = 0
+        self.scales = [torch.tensor([x], dtype=torch.float32, device=dev) for x in (c.k_scale, c.v_scale)]
+        sc = dict(k_scale_dev=self.scales[0], v_scale_dev=self.scales[1]) if device_scales else \
+            dict(k_scale=c.k_scale, v_scale=c.v_scale)
+        self.args = B.make_chunk_args(q=q, k_cache=k, v_cache=v, out=self.out, workspace=self.ws,
+                                      softmax_scale=c.softmax_scale, block_table=self.table, cu_q=self.cu,
+                                      kv_len=self.kv_len, **sc)
+
+    def __call__(self, stream=None):
+        s = torch.cuda.current_stream() if stream is None else stream
+        self.B.fp8kv_attn_chunk(self.plan, self.args, s.cuda_stream)
+        s.synchronize()
+        return self.out.cpu().double()
+
+    def status(self):
+        return int(self.ws[:4].view(torch.int32).item())
+
+
+def check(got, c, ref=None, rows=None):
+    out, tol, cond = c.reference() if ref is None else ref
+    used = int(c.cu[-1]) if rows is None else rows
+    assert (got[int(c.cu[-1]):] == 7.0).all(), "rows behind the last request were written"
+    g, r = got[:used], out[:used]
+    bound = tol[:used] + P_ERR * cond[:used]
+    assert torch.equal(torch.isnan(g), torch.isnan(r)), "NaN in other places"
+    inf = torch.isinf(r)
+    assert torch.equal(torch.isinf(g), inf) and torch.equal(g[inf], r[inf]), "infinities in other places"
+    fine = torch.isfinite(r)
+    d = torch.where(fine, (g - torch.nan_to_num(r, posinf=0, neginf=0)).abs(), 0.0)
+    worst = (torch.where(fine, d / bound, 0.0)).max() if used else torch.tensor(0.0)
+    assert worst <= 1.0, f"{float(worst):.3f} of the bound"
+    return float(worst)
+
+
+def kernels(c):
+    """Every kernel that takes the case: (kernel, partitions)."""
+    small = c.max_q * c.group <= 16
+    return ([(1, 0), (1, 1), (1, 3)] if small else []) + [(2, 0), (2, 1), (2, 3), (0, 0)]
+
+
+CASES = {
+    "decode": Case([(1, 1), (1, 2), (1, 611), (1, 64), (1, 65), (1, 1023)], Hq=6, Hkv=1, D=256),
+    "decode_gqa8": Case([(1, 700), (1, 17), (1, 128)], Hq=16, Hkv=2, D=128, page=3),
+    "decode_group1": Case([(1, 300), (1, 33)], Hq=3, Hkv=3, D=64, page=5, fmt="e5m2", k_scale=0.001),
+    "decode_group12": Case([(1, 333), (1, 1)], Hq=24, Hkv=2, D=128, page=4, dtype=torch.bfloat16),
+    "drafts": Case([(3, 130), (8, 8), (5, 777)], Hq=4, Hkv=2, D=64, fmt="e5m2", k_scale=0.001, window=50, sinks=1),
+    "ragged": Case([(1, 130), (0, 40), (33, 33), (7, 500), (150, 401)], Hq=8, Hkv=2, D=128),
+    "ragged_bf16": Case([(70, 70), (1, 257), (129, 300)], Hq=8, Hkv=2, D=128, dtype=torch.bfloat16, page=64),
+    "wide": Case([(100, 431), (3, 3)], Hq=6, Hkv=1, D=256, page=1728),
+    "wide_e5m2": Case([(65, 200), (22, 150)], Hq=4, Hkv=2, D=256, fmt="e5m2", k_scale=0.001, dtype=torch.bfloat16),
+    "narrow": Case([(200, 200), (31, 700)], Hq=4, Hkv=4, D=64, page=7),
+    "odd_group": Case([(77, 300), (200, 290)], Hq=5, Hkv=1, D=128, page=1),
+    "window_decode": Case([(1, 900), (1, 130), (1, 5), (1, 134), (1, 1)], Hq=8, Hkv=2, D=128, window=129, sinks=4),
+    "window_long_sinks": Case([(1, 900), (2, 300)], Hq=4, Hkv=2, D=128, window=20, sinks=100),
+    "window_prompt": Case([(500, 500), (90, 700)], Hq=4, Hkv=2, D=128, window=100, sinks=3, dtype=torch.bfloat16),
+    "window_one": Case([(40, 300), (1, 300)], Hq=2, Hkv=1, D=128, window=1),
+    "window_wide": Case([(300, 800)], Hq=2, Hkv=1, D=256, window=257, sinks=1, page=16),
+    "window_past_all": Case([(30, 300)], Hq=2, Hkv=1, D=64, window=5000, sinks=9),
+    "dead_rows": Case([(9, 4), (3, 0), (20, 19), (1, 0)], Hq=4, Hkv=2, D=128),
+    "dead_rows_many": Case([(200, 50), (70, 0)], Hq=4, Hkv=2, D=128, window=16, sinks=2),
+    "empty_requests": Case([(0, 0), (0, 100), (2, 2), (0, 0)], Hq=4, Hkv=2, D=128, extra_rows=5),
+    "behind_the_last": Case([(40, 90), (3, 60)], Hq=8, Hkv=2, D=64, extra_rows=70),
+    "many_requests": Case([(1 + i % 4, 1 + (i * 37) % 210 + i % 4) for i in range(75)], Hq=2, Hkv=1, D=64),
+    "negative_scale": Case([(20, 200), (1, 90)], Hq=4, Hkv=2, D=128, softmax_scale=-0.11),
+    "large_logits": Case([(20, 200), (1, 90)], Hq=4, Hkv=2, D=128, q_scale=30.0),
+    "long": Case([(3, 5000), (1, 4097)], Hq=4, Hkv=2, D=128),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_parity(name):
+    c = CASES[name]
+    ref = c.reference()
+    for kernel, splits in kernels(c):
+        r = Run(c, kernel, splits)
+        got = r()
+        try:
+            check(got, c, ref)
+        except AssertionError as e:
+            raise AssertionError(f"kernel {r.plan.kernel}, {r.plan.num_splits} partitions: {e}") from None
+        assert r.status() == 0
+        again = r()
+        assert torch.equal(got, again), "two calls differ"
+
+
+@pytest.mark.parametrize("name", ["decode", "ragged", "drafts", "window_prompt", "wide"])
+def test_strides_and_device_scales(name):
+    c = CASES[name]
+    for kernel, splits in kernels(c):
+        r = Run(c, kernel, splits, spread=True, device_scales=True)
+        check(r(), c)
+        assert (r.out_all[:, c.Hq:] == 7.0).all() and (r.out_all[:, :, c.D:] == 7.0).all()
+
+
+def test_bf16_rows_of_very_different_size():
+    c = Case([(40, 200), (2, 33)], Hq=4, Hkv=2, D=128, dtype=torch.bfloat16, softmax_scale=1.0)
+    size = torch.tensor([1e-30, 1e-6, 1.0, 300.0])[torch.arange(c.total) % 4]
+    c.q = (c.q.float() * size[:, None, None] * 0.02).to(torch.bfloat16)
+    c.q[5] = 0
+    for kernel, splits in kernels(c):
+        check(Run(c, kernel, splits)(), c)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nonfinite_codes_reach_the_rows_that_see_them(fmt, D):
+    """A non-finite V code makes that column of exactly the rows that see the
+    token non-finite; a NaN K code the whole output of those rows."""
+    for requests, window in (([(4, 90), (3, 40)], 0), ([(4, 90), (3, 40)], 20), ([(120, 150)], 30)):
+        c = Case(requests, Hq=4, Hkv=2, D=D, fmt=fmt, k_scale=0.02 if fmt == "e4m3" else 0.001, window=window, seed=3)
+        nan = 0x7F
+        kv0 = c.requests[0][1]
+
+        def put(cache, t, g, d, code):
+            cache[c.table[0, t // c.page].long(), t % c.page, g, d] = code
+
+        put(c.v, kv0 - 3, 0, 5, nan)          # seen by the last rows only
+        put(c.v, kv0 - 2, 1, D - 1, nan)
+        put(c.k, kv0 - 1, 1, 7, nan)          # the last row of KV head 1
+        if fmt == "e5m2":
+            put(c.v, kv0 - 4, 0, 9, 0x7C)     # +inf
+            put(c.v, kv0 - 2, 0, 9, 0x7C)
+            put(c.v, kv0 - 4, 0, 10, 0xFC)    # -inf
+            put(c.v, kv0 - 4, 0, 11, 0x7C)    # both signs
+            put(c.v, kv0 - 1, 0, 11, 0xFC)
+        ref = c.reference()
+        assert torch.isnan(ref[0]).any() and not torch.isnan(ref[0]).all()
+        for kernel, splits in kernels(c):
+            check(Run(c, kernel, splits)(), c, ref)
+
+
+def test_bad_blocks_count_as_not_visible():
+    c = Case([(40, 200), (3, 70)], Hq=4, Hkv=2, D=128, page=16, seed=5)
+    victims = [int(c.table[0, 2]), int(c.table[1, 0])]
+    ref = c.reference(bad_blocks=victims)
+    c.table[0, 2] = c.blocks
+    c.table[1, 0] = -1
+    for kernel, splits in kernels(c):
+        r = Run(c, kernel, splits)
+        check(r(), c, ref)
+        assert r.status() == r.B.STATUS_BAD_BLOCK
+
+
+def test_lengths_are_clamped():
+    c = Case([(4, 90), (3, 60)], Hq=4, Hkv=2, D=128)
+    for kernel, splits in [(1, 0), (2, 0), (2, 2), (1, 2)]:
+        r = Run(c, kernel, splits)
+        r.kv_len[0] = 10 ** 9           # as max_kv_len
+        check(r(), c)
+        assert r.status() == r.B.STATUS_BAD_LEN
+        r = Run(c, kernel, splits)
+        r.kv_len[1] = -5                # as 0: nothing to see
+        got = r()
+        assert (got[4:7] == 0).all() and r.status() == r.B.STATUS_BAD_LEN
+        r = Run(c, kernel, splits)
+        r.cu[2] = 100                   # past total_q
+        check(r(), c)
+        assert r.status() == r.B.STATUS_BAD_LEN
+        r = Run(c, kernel, splits)
+        r.cu[1] = -3                    # request 0 is empty, request 1 begins at row 0
+        r()
+        assert r.status() == r.B.STATUS_BAD_LEN
+        r = Run(c, kernel, splits, max_q=3)  # request 0 has one more than the plan
+        r()
+        assert r.status() == r.B.STATUS_BAD_LEN
+
+
+def test_graph_replay_with_other_lengths():
+    big = Case([(6, 300), (2, 200), (4, 90)], Hq=8, Hkv=2, D=128, window=70, sinks=2)
+    others = [Case([(2, 300), (6, 90), (1, 1)], Hq=8, Hkv=2, D=128, window=70, sinks=2, extra_rows=3),
+              Case([(0, 0), (6, 200), (3, 50)], Hq=8, Hkv=2, D=128, window=70, sinks=2, extra_rows=3)]
+    for kernel, splits in [(0, 0), (2, 2), (2, 1)]:
+        r = Run(big, kernel, splits)
+        side = torch.cuda.Stream()
+        r(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            r.B.fp8kv_attn_chunk(r.plan, r.args, side.cuda_stream)
+        for c in [big] + others:
+            r.q.copy_(c.q)
+            n = min(r.k.shape[0], c.k.shape[0])
+            r.k[:n].copy_(c.k[:n])
+            r.v[:n].copy_(c.v[:n])
+            r.table[:, :c.cols].copy_(c.table)
+            r.cu.copy_(torch.from_numpy(c.cu))
+            r.kv_len.copy_(torch.from_numpy(c.kv_len))
+            r.out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            check(r.out.cpu().double(), c)
+            assert r.status() == 0
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    c, d = CASES["ragged"], CASES["window_prompt"]
+    rc, rd = c.reference(), d.reference()
+    a, b = Run(c, 2, 2), Run(d, 2, 2)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.B.fp8kv_attn_chunk(a.plan, a.args, s.cuda_stream)
+        b.B.fp8kv_attn_chunk(b.plan, b.args, t.cuda_stream)
+    torch.cuda.synchronize()
+    check(a.out.cpu().double(), c, rc)
+    check(b.out.cpu().double(), d, rd)
+
+
+def test_cache_offsets_past_32_bits():
+    """Blocks 700 MB apart: byte offsets pass 2^31 and 2^32."""
+    c = Case([(3, 100), (20, 64)], Hq=4, Hkv=2, D=128, page=16)
+    stride = 700 << 20
+    for kernel, splits in [(0, 0), (2, 1)]:
+        r = Run(c, kernel, splits)
+        blocks = c.blocks
+        pool = torch.empty(stride * (blocks - 1) + c.page * c.Hkv * c.D, dtype=torch.uint8, device="cuda")
+        view = pool.as_strided((blocks, c.page, c.Hkv, c.D), (stride, c.Hkv * c.D, c.D, 1))
+        view.copy_(r.k)
+        r.args.k_cache, r.args.k_stride_block = view.data_ptr(), stride
+        check(r(), c)
+        view.copy_(r.v)
+        r.args.k_cache, r.args.k_stride_block = r.k.data_ptr(), r.k.stride(0)
+        r.args.v_cache, r.args.v_stride_block = view.data_ptr(), stride
+        check(r(), c)
+        del pool, view
+
+
+def test_matches_the_decode_path():
+    """One new token, no window: the decode call's result."""
+    from fp8_e4m3_paged_gb300.device_problem import DeviceProblem
+    from synth import make_dense
+
+    p = make_dense(name="d128", B=4, q=1, Hq=16, Hkv=4, D=128, page_size=16, lens=[700, 2000, 130, 1025], seed=8)
+    dp = DeviceProblem(p)
+    old = dp.run().clone()
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    plan = B.fp8kv_attn_chunk_plan(B.make_chunk_desc(
+        batch=4, total_q=4, max_q=1, num_q_heads=16, num_kv_heads=4, head_dim=128, page_size=16,
+        max_kv_len=int(p.max_kv_len), max_blocks=int(p.block_table.shape[1]), num_kv_blocks=int(p.k_cache.shape[0])))
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(4, 16, 128, dtype=torch.float16, device="cuda")
+    args = B.make_chunk_args(q=dp.q.view(4, 16, 128), k_cache=dp.k_caches[0], v_cache=dp.v_caches[0], out=out,
+                             workspace=ws, softmax_scale=p.softmax_scale, k_scale=p.k_scale, v_scale=p.v_scale,
+                             block_table=dp.block_table, cu_q=torch.arange(5, dtype=torch.int32, device="cuda"),
+                             kv_len=dp.row_len.view(4).contiguous())
+    B.ChunkCall(plan, args).run(torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    a, b = out.double(), old.view(4, 16, 128).double()
+    # each is within half an fp16 ulp of its sum; the sums differ by less than that
+    assert float(((a - b).abs() / (b.abs() * 2.0 ** -10 + 2.0 ** -13 * b.abs().max())).max()) <= 1.0
+
+
+def test_workspace_and_device_of_tensors():
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    c = CASES["ragged"]
+    r = Run(c, 2, 3)
+    r.args.workspace_bytes = r.plan.workspace_bytes - 1
+    with pytest.raises(B.Fp8kvError) as e:
+        r()
+    assert e.value.code == B.EWORKSPACE
