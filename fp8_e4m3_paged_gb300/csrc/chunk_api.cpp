@@ -79,21 +79,30 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   P.num_sms = sms;
 
   const int64_t rows = P.max_q * group;  // query vectors per (request, KV head)
-  P.kernel = d->kernel ? d->kernel : FP8KV_CHUNK_STREAM;
-  // positions that one CTA's rows see at most
-  int64_t seen = P.max_kv_len;
-  const int64_t chunks = ceil_div(rows, kChunkStreamRows);
-  if (P.window) seen = std::min<int64_t>(seen, (int64_t)P.window + P.sinks + P.max_q - 1);
+  P.kernel = d->kernel ? d->kernel : rows <= kChunkStreamRows ? FP8KV_CHUNK_STREAM : FP8KV_CHUNK_TILE;
 
-  int64_t S = 1, most = 1;
+  // Partitions: about one CTA per slot of the GPU, none shorter than `unit`
+  // positions of what one CTA's rows see together.
+  int64_t units, slots, unit, span_q;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
-    if (chunks > 65535) return FP8KV_EUNSUPPORTED;
-    const int64_t units = (int64_t)P.batch * P.num_kv_heads * chunks;
-    const int64_t slots = (int64_t)sms * (P.head_dim == 64 ? 4 : P.head_dim == 128 ? 3 : 2);
-    most = std::max<int64_t>(1, ceil_div(seen, 4 * kChunkStreamBlock));
-    S = units ? slots / units : 1;
+    units = (int64_t)P.batch * P.num_kv_heads;
+    slots = (int64_t)sms * (P.head_dim == 64 ? 4 : P.head_dim == 128 ? 3 : 2);
+    unit = 4 * kChunkStreamBlock;
+    span_q = P.max_q;
+  } else {
+    const int64_t tile = chunk_tile_rows(P.head_dim);
+    P.row_tiles = (int32_t)(P.total_q * group / tile + std::min(P.batch, P.total_q));
+    units = (int64_t)P.row_tiles * P.num_kv_heads;
+    slots = sms;
+    unit = kChunkTileTokens;
+    span_q = std::min<int64_t>(P.max_q, ceil_div(tile, group) + 1);
   }
-  S = std::max<int64_t>(1, std::min(S, most));
+  const int64_t seen =
+      P.window ? std::min<int64_t>(P.max_kv_len, (int64_t)P.window + P.sinks + span_q - 1) : P.max_kv_len;
+  int64_t S = units ? slots / units : 1;
+  S = std::min(S, ceil_div(seen, unit));
+  if (P.kernel == FP8KV_CHUNK_TILE) S = std::max(S, ceil_div(seen, kChunkMaxPart));
+  S = std::max<int64_t>(1, S);
   if (d->num_splits) S = d->num_splits;
   if (P.batch > 0 && P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;
   P.num_splits = (int32_t)S;
@@ -184,7 +193,7 @@ extern "C" int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chun
   const int rc = build_chunk(plan, a, &p);
   if (rc != FP8KV_OK || plan->batch == 0 || plan->total_q == 0) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_chunk_stream(plan, p, st);
+  cudaError_t e = plan->kernel == FP8KV_CHUNK_STREAM ? launch_chunk_stream(plan, p, st) : launch_chunk_tile(plan, p, st);
   if (e == cudaSuccess && p.S > 1) e = launch_chunk_join(plan, p, st);
   return done(e);
 }

@@ -1,7 +1,7 @@
 // Chunk attention for few query vectors (at most 16 per CTA: the query heads
 // of one KV head times a few new tokens): bound by streaming the cache.
 //
-// One CTA of four warps per (request, KV head, partition, 16 query vectors); each warp walks
+// One CTA of four warps per (request, KV head, partition); each warp walks
 // blocks of 16 virtual tokens (chunk_span) on its own, with no barrier and no
 // shared memory in the loop, and the four are joined at the end.  The FP8
 // bytes go from global memory straight into the registers of the MMA that
@@ -93,18 +93,16 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
   const int rq = lane >> 2, c = lane & 3;
   const int b = blockIdx.x / p.S, s = blockIdx.x - b * p.S;
   const int g = blockIdx.y;
-  const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-  const int RC = min(kR, req.n * p.G - row_first);
+  const int RC = min(kR, req.n * p.G);  // packed rows: token * G + head of the group
   if (RC <= 0) return;
   const int64_t plane = (int64_t)p.total_q * p.Hq;
   auto vec_of = [&](int r) {
-    const int rr = row_first + r;
-    return (int64_t)(req.row0 + rr / p.G) * p.Hq + g * p.G + rr % p.G;
+    return (int64_t)(req.row0 + r / p.G) * p.Hq + g * p.G + r % p.G;
   };
 
-  const ChunkSpan span = chunk_span(p, req, row_first / p.G, (row_first + RC - 1) / p.G);
+  const ChunkSpan span = chunk_span(p, req, 0, (RC - 1) / p.G);
   int per = (span.U + p.S - 1) / p.S;
   per = (per + kBlk * kWarps - 1) / (kBlk * kWarps) * (kBlk * kWarps);
   const int u0 = min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
@@ -176,8 +174,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
     constexpr int V = D / 32;  // elements per lane
     uint32_t w[V / 2] = {};
     if (r < RC) {
-      const int rr = row_first + r;
-      const uint16_t* src = p.q + (int64_t)(req.row0 + rr / p.G) * p.q_st + (int64_t)(g * p.G + rr % p.G) * p.q_sh;
+      const uint16_t* src = p.q + (int64_t)(req.row0 + r / p.G) * p.q_st + (int64_t)(g * p.G + r % p.G) * p.q_sh;
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + lane * V + 2 * j);
     }
@@ -210,8 +207,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
 
   // What this lane's two rows see; rows past RC see everything (their values are dropped).
   ChunkRow row0 = {INT_MAX, INT_MIN}, row1 = {INT_MAX, INT_MIN};
-  if (rq < RC) row0 = chunk_row(p, req, span, (row_first + rq) / p.G);
-  if (rq + 8 < RC) row1 = chunk_row(p, req, span, (row_first + rq + 8) / p.G);
+  if (rq < RC) row0 = chunk_row(p, req, span, rq / p.G);
+  if (rq + 8 < RC) row1 = chunk_row(p, req, span, (rq + 8) / p.G);
   const int hi_min = __reduce_min_sync(0xffffffffu, min(row0.hi, row1.hi));
   const int lo_max = __reduce_max_sync(0xffffffffu, max(row0.lo, row1.lo));
 
@@ -438,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
   if (zap) {
     __syncthreads();
     mark_nonfinite_v<D, FMT>(p, kinds, b, g, u0, u1, span, RC,
-                             [&](int i) { return chunk_row(p, req, span, (row_first + i) / p.G); });
+                             [&](int i) { return chunk_row(p, req, span, i / p.G); });
   }
 #pragma unroll
   for (int k = 0; k < kIter; ++k) {
@@ -458,8 +455,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
     if (p.S > 1) {
       *reinterpret_cast<float4*>(p.partial + (s * plane + vec_of(r)) * D + d) = make_float4(y[0], y[1], y[2], y[3]);
     } else {
-      const int rr = row_first + r;
-      uint16_t* dst = p.out + (int64_t)(req.row0 + rr / p.G) * p.o_st + (int64_t)(g * p.G + rr % p.G) * p.o_sh + d;
+      uint16_t* dst = p.out + (int64_t)(req.row0 + r / p.G) * p.o_st + (int64_t)(g * p.G + r % p.G) * p.o_sh + d;
       *reinterpret_cast<uint2*>(dst) =
           dead ? make_uint2(0u, 0u) : make_uint2(pack_out<DT>(y[0], y[1]), pack_out<DT>(y[2], y[3]));
     }
@@ -473,8 +469,7 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  const int chunks = (int)(((int64_t)p.max_q * p.G + kR - 1) / kR);
-  fn<<<dim3((unsigned)(p.B * p.S), p.Hkv, chunks), kThreadsS, smem, st>>>(p);
+  fn<<<dim3((unsigned)(p.B * p.S), p.Hkv), kThreadsS, smem, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,629 @@
+// Chunk attention for many query vectors: tcgen05 tiles of 128 vectors by 128
+// positions.
+//
+// The query heads of one KV head and the new tokens of one request are packed
+// into rows (token * G + head), so a tile is full whatever the group size and
+// one decode of K and V serves all of them.  A CTA owns 256 rows (two row
+// tiles; 128 rows for D = 256) of one request and KV head, and one partition
+// of the positions that its rows see.  Warp roles:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1 (thread = row = TMEM lane);
+//                    D = 256: warps 0-3 only, and warps 4-7 decode K;
+//   warps 8-11       decode K and V (D = 256: V): FP8 rows from global memory
+//                    through registers, one tile ahead, into swizzled fp16 operand tiles;
+//   warp 12          TMEM, and every UMMA (one thread).
+// Per tile j and row tile q:  S_q = Q_q . K_j^T (M 128, N 128),
+// P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM).
+// Two row tiles alternate: while one's softmax runs, the tensor core works on
+// the other's S and O.  For D = 256 two S buffers of the one row tile do the
+// same: QK of tile j+1 is issued before PV of tile j.
+// TMEM: S at columns 0 and 128, O at 256 (256 columns).
+//
+// Every wait is bounded (see split_tc_kernel.cuh): a wait that gives up sets the
+// CTA's abort flag and FP8KV_STATUS_TIMEOUT, every role stops, and the issued
+// UMMAs are drained before TMEM is freed.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "chunk_common.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace fp8kv {
+namespace {
+
+using namespace tc;
+
+constexpr int kT = kChunkTileTokens;
+constexpr int kM = 128;                  // rows per tile
+constexpr int kTileThreads = 13 * 32;
+constexpr int kMmaWarp = 12;
+constexpr int kStagesMax = 4;
+constexpr uint32_t kPolls = 1u << 20;    // polls per wait
+
+template <int D>
+struct TileCfg {
+  static constexpr int kNQ = D == 256 ? 1 : 2;
+  static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 4;  // K stages, and V stages
+  static constexpr int kOpBytes = kT * D * 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kNQ * kM * D * 2;
+  static constexpr int kOffV = kOffK + kStages * kOpBytes;
+  static constexpr int kOffMeta = kOffV + kStages * kOpBytes;
+  static constexpr int kSmem = kOffMeta + 2048 + 1024;  // meta, alignment
+  static constexpr uint32_t kColO = 256;
+  static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
+  static constexpr int kRowsIt = 32 / kCh;    // rows a warp moves at a time
+  static constexpr int kIts = 32 / kRowsIt;   // times, for its 32 rows
+  static_assert(kNQ * D <= 256 && kSmem <= 232448, "TMEM and shared memory");
+};
+
+struct TileMeta {
+  uint64_t q_full, drain;
+  uint64_t k_full[kStagesMax], k_empty[kStagesMax], v_full[kStagesMax], v_empty[kStagesMax];
+  uint64_t s_full[2], p_ready[2], o_all[2];  // o_all: a row tile's last PV is done
+  uint64_t o_done;                           // D = 256: PV(j) is done, every tile but the last
+  uint32_t valid[8][4];  // per tile (j % 8): positions whose block is in range
+  uint32_t tmem, abort, vbad;
+  float back[2 * kM];    // inverse row scales
+};
+static_assert(sizeof(TileMeta) <= 2048, "meta block");
+
+// A bounded wait of a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls, abort_flag));
+}
+
+// Request and first packed row of this CTA: tiles count over the requests in
+// order, taken from the last (a request's last rows see the most positions,
+// so the longest work starts first).
+struct TileWork {
+  int b, row0;
+};
+__device__ __forceinline__ int tiles_of(const ChunkParams& p, int b, int rows, bool& bad) {
+  if (b >= p.B) return 0;
+  const ChunkRequest r = chunk_request(p, b);
+  bad |= r.bad;
+  return (r.n * p.G + rows - 1) / rows;
+}
+__device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int lane, TileWork& w) {
+  int total = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, tiles_of(p, b0 + lane, rows, bad));
+  if (bad && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 32)
+    set_status(p.status, FP8KV_STATUS_BAD_LEN);
+  int idx = total - 1 - (int)blockIdx.x;
+  if (idx < 0) return false;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int mine = tiles_of(p, b0 + lane, rows, bad);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > idx);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      w.b = b0 + l;
+      w.row0 = (idx - __shfl_sync(0xffffffffu, upto - mine, l)) * rows;
+      return true;
+    }
+    idx -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// What a decoder lane knows about one tile: the place of position 32 w + lane.
+struct Places {
+  int64_t k, v;
+  uint32_t ok;  // ballot over the warp
+};
+
+// One tile's 32 rows of a warp: FP8 pieces in registers.
+template <int D>
+__device__ __forceinline__ void fetch_rows(const uint8_t* base, int64_t off, uint32_t ok, int lane,
+                                           uint4 (&w)[TileCfg<D>::kIts]) {
+  using C = TileCfg<D>;
+#pragma unroll
+  for (int it = 0; it < C::kIts; ++it) {
+    const int r = it * C::kRowsIt + lane / C::kCh;
+    const int64_t o = __shfl_sync(0xffffffffu, off, r);
+    w[it] = ((ok >> r) & 1u) ? __ldg(reinterpret_cast<const uint4*>(base + o + (lane % C::kCh) * 16))
+                             : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// ... and as fp16 in the operand tile: 64-column blocks of kT rows of 128
+// bytes, 16-byte chunk c of row r at c ^ (r % 8).  Odd column blocks store
+// their two chunks in the other order, so that eight lanes hit eight banks.
+template <int D, int FMT>
+__device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[TileCfg<D>::kIts], int row_base, int lane) {
+  using C = TileCfg<D>;
+  const int c = lane % C::kCh, db = c / 4, h0 = (c % 4) * 2;
+  const bool swap = db & 1;
+  const int first = swap ? h0 + 1 : h0, second = swap ? h0 : h0 + 1;
+#pragma unroll
+  for (int it = 0; it < C::kIts; ++it) {
+    const int r = row_base + it * C::kRowsIt + lane / C::kCh;
+    uint8_t* row = op + db * (kT * 128) + r * 128;
+    uint4 a, b;
+    fp8x4_to_f16<FMT>(w[it].x, a.x, a.y);
+    fp8x4_to_f16<FMT>(w[it].y, a.z, a.w);
+    fp8x4_to_f16<FMT>(w[it].z, b.x, b.y);
+    fp8x4_to_f16<FMT>(w[it].w, b.z, b.w);
+    *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) * 16)) = swap ? b : a;
+    *reinterpret_cast<uint4*>(row + ((second ^ (r & 7)) * 16)) = swap ? a : b;
+  }
+}
+
+// Decoders: K, V or both streams of every tile.  Rows whose block is out of
+// range, or past the partition, are zero.
+template <int D, int FMT, bool DO_K, bool DO_V>
+__device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt, uint8_t* smem, int b, int g, int u0,
+                                             int u1, int n_tiles, const ChunkSpan& span, int w, int lane) {
+  using C = TileCfg<D>;
+  constexpr int NS = C::kStages;
+  volatile uint32_t* const abort_flag = &mt.abort;
+  const uint8_t* kbase = p.k_cache + g * p.ksh;
+  const uint8_t* vbase = p.v_cache + g * p.vsh;
+  auto find = [&](int j) {
+    Places f = {0, 0, 0u};
+    const int v = u0 + j * kT + 32 * w + lane;
+    bool ok = v < u1;
+    if (ok) {
+      int64_t blk;
+      int slot;
+      ok = chunk_place(p, b, span.position(v), blk, slot);
+      if (ok) {
+        f.k = blk * p.ksb + (int64_t)slot * p.kst;
+        f.v = blk * p.vsb + (int64_t)slot * p.vst;
+      } else if (DO_K) {
+        set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
+      }
+    }
+    f.ok = __ballot_sync(0xffffffffu, ok);
+    return f;
+  };
+  uint4 kr[DO_K ? C::kIts : 1], vr[DO_V ? C::kIts : 1];
+  bool bad = false;
+  Places f = find(0);
+  if constexpr (DO_K) fetch_rows<D>(kbase, f.k, f.ok, lane, kr);
+  if constexpr (DO_V) fetch_rows<D>(vbase, f.v, f.ok, lane, vr);
+  uint32_t ok_now = f.ok;
+  if (n_tiles > 1) f = find(1);
+  for (int j = 0; j < n_tiles; ++j) {
+    const int st = j % NS;
+    const uint32_t empty_parity = ((j / NS) - 1) & 1;
+    if constexpr (DO_K) {
+      if (j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) return false;
+      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w, lane);
+      // K(j+8) is decoded after QK(j+4) at the earliest, and that after softmax j+3
+      if (lane == 0) mt.valid[j & 7][w] = ok_now;
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.k_full[st]);
+      if (j + 1 < n_tiles) fetch_rows<D>(kbase, f.k, f.ok, lane, kr);
+    }
+    if constexpr (DO_V) {
+      constexpr bool e5 = FMT == FP8KV_KV_E5M2;
+      uint32_t any = 0u;
+#pragma unroll
+      for (int i = 0; i < C::kIts; ++i) any |= nonfinite_codes(vr[i], e5);
+      if (any != 0u) {
+        bad = true;
+#pragma unroll
+        for (int i = 0; i < C::kIts; ++i)
+          vr[i] = make_uint4(zap_nonfinite(vr[i].x, e5), zap_nonfinite(vr[i].y, e5), zap_nonfinite(vr[i].z, e5),
+                             zap_nonfinite(vr[i].w, e5));
+      }
+      if (j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) return false;
+      store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, vr, 32 * w, lane);
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.v_full[st]);
+      if (j + 1 < n_tiles) fetch_rows<D>(vbase, f.v, f.ok, lane, vr);
+    }
+    ok_now = f.ok;
+    if (j + 2 < n_tiles) f = find(j + 2);
+  }
+  if (bad) mt.vbad = 1u;
+  return true;
+}
+
+// Visibility of 32 virtual tokens v0 .. v0+31 for one row, as bits.
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t sees32(const ChunkRow& r, int sk, int v0) {
+  return below(r.hi - v0) & (~below(r.lo - v0) | below(sk - v0));
+}
+
+template <int D, int FMT, int DT>
+__global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const ChunkParams p) {
+  using C = TileCfg<D>;
+  constexpr int NQ = C::kNQ, ROWS = NQ * kM;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TileMeta& mt = *reinterpret_cast<TileMeta*>(smem + C::kOffMeta);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = blockIdx.y, s = blockIdx.z;
+
+  TileWork work;
+  if (!locate(p, ROWS, lane, work)) return;
+  const int b = work.b;
+  const ChunkRequest req = chunk_request(p, b);
+  const int RC = min(ROWS, req.n * p.G - work.row0);
+  if (RC <= 0 || work.row0 < 0) return;
+  const int64_t plane = (int64_t)p.total_q * p.Hq;
+  auto vec_of = [&](int r) {
+    const int rr = work.row0 + r;
+    return (int64_t)(req.row0 + rr / p.G) * p.Hq + g * p.G + rr % p.G;
+  };
+  const ChunkSpan span = chunk_span(p, req, work.row0 / p.G, (work.row0 + RC - 1) / p.G);
+  int per = (span.U + p.S - 1) / p.S;
+  per = (per + kT - 1) / kT * kT;
+  const int u0 = (int)min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
+  if (u0 >= u1) {  // nothing to see here: an empty partition, or rows before position 0
+    if (p.S > 1) {
+      for (int r = tid; r < RC; r += kTileThreads) p.ml[s * plane + vec_of(r)] = make_float2(kNoMax, 0.f);
+    } else {
+      for (int x = tid; x < RC * (D / 8); x += kTileThreads) {
+        const int rr = work.row0 + x / (D / 8);
+        *reinterpret_cast<uint4*>(p.out + (int64_t)(req.row0 + rr / p.G) * p.o_st +
+                                  (int64_t)(g * p.G + rr % p.G) * p.o_sh + (x % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  const int n_tiles = (u1 - u0 + kT - 1) / kT;
+  const int nq = NQ == 2 && RC > kM ? 2 : 1;  // row tiles in use
+
+  if (tid == 0) {
+    mbar_init(&mt.q_full, nq * kM);
+    mbar_init(&mt.drain, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&mt.k_full[i], 128);
+      mbar_init(&mt.k_empty[i], 1);
+      mbar_init(&mt.v_full[i], 128);
+      mbar_init(&mt.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&mt.s_full[i], 1);
+      mbar_init(&mt.p_ready[i], kM);
+      mbar_init(&mt.o_all[i], 1);
+    }
+    mbar_init(&mt.o_done, 1);
+    mt.abort = 0u;
+    mt.vbad = 0u;
+    mbar_init_fence();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&mt.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = mt.tmem;
+  volatile uint32_t* const abort_flag = &mt.abort;
+  const float ks = p.k_scale_dev ? *p.k_scale_dev : p.k_scale;
+  const double cd = (double)p.softmax_scale * (double)ks * 1.4426950408889634074;
+  bool ok = true;
+
+  if (warp < 4 * NQ) {
+    const int q = warp >> 2;
+    if (q < nq) {
+      // ====================================================== Q tile
+      // One warp per row: fp16 as it is, bf16 scaled by a power of two; the
+      // sign of the logit factor goes into Q.
+      constexpr int V = D / 32;
+      uint8_t* sQ = smem + C::kOffQ + q * (kM * D * 2);
+      const uint32_t flip = cd < 0 ? 0x80008000u : 0u;
+#pragma unroll 4
+      for (int k = 0; k < 32; ++k) {
+        const int r = 32 * (warp & 3) + k, rr = q * kM + r;
+        uint32_t w[V / 2] = {};
+        if (rr < RC) {
+          const int pr = work.row0 + rr;
+          const uint16_t* src = p.q + (int64_t)(req.row0 + pr / p.G) * p.q_st + (int64_t)(g * p.G + pr % p.G) * p.q_sh;
+          if constexpr (V == 2) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(src + lane * V));
+          } else if constexpr (V == 4) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + lane * V));
+            w[0] = x.x;
+            w[1] = x.y;
+          } else {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + lane * V));
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
+          }
+        }
+        if (DT == FP8KV_DTYPE_BF16) {
+          uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i)
+            top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+          const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i)
+            w[i] = pack_half2(__uint_as_float(w[i] << 16) * rs.to_f16, __uint_as_float(w[i] & 0xFFFF0000u) * rs.to_f16);
+          if (lane == 0) mt.back[rr] = rs.back;
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] ^= flip;
+        const int e = lane * V;  // first element of the lane
+        uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
+        if constexpr (V == 2)
+          *reinterpret_cast<uint32_t*>(dst) = w[0];
+        else if constexpr (V == 4)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.q_full);
+
+      // ====================================================== softmax
+      const int rr = q * kM + 32 * (warp & 3) + lane;  // this thread's row of the CTA
+      const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+      const float c = (float)(fabs(cd) * (DT == FP8KV_DTYPE_BF16 ? (double)mt.back[rr] : 1.0));
+      ChunkRow row = {INT_MAX, INT_MIN};  // rows past RC: everything, dropped at the end
+      if (rr < RC) row = chunk_row(p, req, span, (work.row0 + rr) / p.G);
+      const int hi_min = __reduce_min_sync(0xffffffffu, row.hi), lo_max = __reduce_max_sync(0xffffffffu, row.lo);
+      float m = kNoMax, l = 0.f;
+      const uint32_t tO = tmem + C::kColO + q * D + lane_off;
+      for (int j = 0; j < n_tiles; ++j) {
+        const int buf = NQ == 2 ? q : j & 1;
+        const uint32_t parity = (NQ == 2 ? j : j >> 1) & 1;
+        ok = warp_wait(&mt.s_full[buf], parity, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tS = tmem + buf * 128 + lane_off;
+        const int v0 = u0 + j * kT;
+        uint32_t vis[4];
+        bool full = v0 + kT <= hi_min && (v0 >= lo_max || v0 + kT <= span.sk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vis[i] = mt.valid[j & 7][i];
+          full &= vis[i] == 0xFFFFFFFFu;
+        }
+        if (!full)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vis[i] &= sees32(row, span.sk, v0 + 32 * i);
+        // row maximum over the visible logits
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[32];
+          tmem_ld32(tS + 32 * i, x);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            mx = fmaxf(mx, full || ((vis[i] >> k) & 1u) ? __uint_as_float(x[k]) : -INFINITY);
+        }
+        if (mx > -INFINITY) mx *= c;
+        if (__any_sync(0xffffffffu, mx > -INFINITY && !(mx <= m + kChunkTau))) {
+          const float n = mx > m + kChunkTau || m == kNoMax ? fmaxf(m, ceilf(mx)) : m;
+          const float a = n == m || m == kNoMax ? 1.f : exp2_int(m - n);
+          m = n;
+          l *= a;
+          if (j > 0 && __any_sync(0xffffffffu, a != 1.f)) {
+            // O holds the PVs of the tiles before this one.  Two row tiles: S(j)
+            // was issued behind PV(j-1), so s_full covers it; one: s_full
+            // covers PV(j-2), and this waits for PV(j-1).
+            bool go = true;
+            if (NQ == 1) go = warp_wait(&mt.o_done, (j - 1) & 1, abort_flag);
+            tc_fence_after();
+            if (go) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + c0, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                tmem_st16(tO + c0, o);
+              }
+            }
+          }
+        }
+        const float sh = kChunkPShift - (m == kNoMax ? 0.f : m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[32], y[16];
+          tmem_ld32(tS + 32 * i, x);
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float e0 = fmaf(__uint_as_float(x[k]), c, sh), e1 = fmaf(__uint_as_float(x[k + 1]), c, sh);
+            if (!full) {
+              e0 = ((vis[i] >> k) & 1u) ? e0 : -INFINITY;
+              e1 = ((vis[i] >> (k + 1)) & 1u) ? e1 : -INFINITY;
+            }
+            const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
+            l += p0 + p1;
+            y[k / 2] = pack_half2(p0, p1);
+          }
+          tmem_st16(tS + 16 * i, y);  // over S columns that were read
+        }
+        tc_fence_before();
+        mbar_arrive(&mt.p_ready[buf]);
+      }
+      // ====================================================== epilogue
+      if (ok) ok = warp_wait(&mt.o_all[q], 0, abort_flag);
+      tc_fence_after();
+      if (ok) {
+        const bool live = rr < RC;
+        const float vs = p.v_scale_dev ? *p.v_scale_dev : p.v_scale;
+        const int64_t vec = live ? vec_of(rr) : 0;
+        const bool dead = l == 0.f;
+        const float f = p.S > 1 ? kChunkInvPShift : (dead ? 0.f : vs / l);
+        const int pr = work.row0 + rr;
+        uint16_t* dst = p.out + (int64_t)(req.row0 + pr / p.G) * p.o_st + (int64_t)(g * p.G + pr % p.G) * p.o_sh;
+        if (p.S > 1 && live) p.ml[s * plane + vec] = make_float2(m, l * kChunkInvPShift);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c0, o);
+          if (!live) {
+          } else if (p.S > 1) {
+            float* part = p.partial + (s * plane + vec) * D + c0;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(part + k) =
+                  make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
+                              __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+          } else {
+            uint32_t y[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2)
+              y[k / 2] = dead ? 0u : pack_out<DT>(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(dst + c0 + 2 * k) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ======================================================== decoders
+    const int w = warp & 3;
+    if constexpr (NQ == 2)
+      ok = decode_tiles<D, FMT, true, true>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
+    else if (warp < 8)
+      ok = decode_tiles<D, FMT, true, false>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
+    else
+      ok = decode_tiles<D, FMT, false, true>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
+  } else if (lane == 0) {
+    // ======================================================== UMMA issue
+    constexpr int NS = C::kStages;
+    const uint32_t idesc_qk = idesc_f16_f32(kM, kT, false, false);
+    const uint32_t idesc_pv = idesc_f16_f32(kM, D, false, true);
+    const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kSw128);
+    const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
+    const uint64_t vdesc = smem_desc(smem_u32(smem + C::kOffV), kT * 128, 1024, kSw128);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait(bar, parity, kPolls, abort_flag);
+      tc_fence_after();
+      return ok;
+    };
+    auto qk = [&](int q, int buf, int j) {
+      const uint64_t qd = qdesc + (uint64_t)((q * (kM * D * 2)) >> 4);
+      const uint64_t kd = kdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);  // kM == kT
+        mma_ss(tmem + buf * 128, qd + step, kd + step, idesc_qk, kk > 0);
+      }
+      mma_commit(&mt.s_full[buf]);
+    };
+    auto pv = [&](int q, int buf, int j) {
+      const uint64_t vd = vdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kT / 16; ++kk)
+        mma_ts(tmem + C::kColO + q * D, tmem + buf * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+               (j > 0 || kk > 0) ? 1u : 0u);
+    };
+    static_assert(kM == kT, "Q and K tiles share their block stride");
+    if (wait(&mt.q_full, 0) && wait(&mt.k_full[0], 0)) {
+      if (NQ == 2) {
+        // S and P of a row tile share their columns: QK(j+1) follows PV(j) in
+        // issue order, in which the tensor core runs one CTA's UMMAs
+        for (int q = 0; q < nq; ++q) qk(q, q, 0);
+        mma_commit(&mt.k_empty[0]);
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          if (!wait(&mt.v_full[j % NS], (j / NS) & 1)) break;
+          for (int q = 0; q < nq; ++q) {
+            if (!wait(&mt.p_ready[q], j & 1)) break;
+            pv(q, q, j);
+            if (q == nq - 1) mma_commit(&mt.v_empty[j % NS]);
+            if (j + 1 == n_tiles) {
+              mma_commit(&mt.o_all[q]);
+            } else {
+              if (q == 0 && !wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
+              qk(q, q, j + 1);
+              if (q == nq - 1) mma_commit(&mt.k_empty[(j + 1) % NS]);
+            }
+          }
+        }
+      } else {
+        qk(0, 0, 0);
+        mma_commit(&mt.k_empty[0]);
+        for (int j = 0; j < n_tiles; ++j) {
+          if (j + 1 < n_tiles) {
+            // its buffer held P(j-1), whose PV was issued before
+            if (!wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
+            qk(0, (j + 1) & 1, j + 1);
+            mma_commit(&mt.k_empty[(j + 1) % NS]);
+          }
+          if (!wait(&mt.v_full[j % NS], (j / NS) & 1) || !wait(&mt.p_ready[j & 1], (j >> 1) & 1)) break;
+          pv(0, j & 1, j);
+          mma_commit(&mt.v_empty[j % NS]);
+          mma_commit(j + 1 == n_tiles ? &mt.o_all[0] : &mt.o_done);
+        }
+      }
+    }
+    // every UMMA issued must be done before TMEM is freed
+    mma_commit(&mt.drain);
+    mbar_wait_plain(&mt.drain, 0, kPolls);
+  }
+  if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (mt.vbad) {
+    // non-finite V codes (entered as 0): the elements of the rows that see them
+    uint32_t* kinds = reinterpret_cast<uint32_t*>(smem + C::kOffQ);
+    static_assert(ROWS * D <= C::kOffMeta, "room for the marks");
+    mark_nonfinite_v<D, FMT>(p, kinds, b, g, u0, u1, span, RC,
+                             [&](int i) { return chunk_row(p, req, span, (work.row0 + i) / p.G); });
+    const float vs = p.v_scale_dev ? *p.v_scale_dev : p.v_scale;
+    for (int x = tid; x < RC * D; x += kTileThreads) {
+      const int i = x / D, d = x % D;
+      const uint32_t kind = (kinds[i * (D / 4) + d / 4] >> (8 * (d % 4))) & 0xFFu;
+      if (!kind) continue;
+      const float v = nonfinite_value(kind);
+      if (p.S > 1) {
+        p.partial[(s * plane + vec_of(i)) * D + d] = v;
+      } else {
+        const int rr = work.row0 + i;
+        p.out[(int64_t)(req.row0 + rr / p.G) * p.o_st + (int64_t)(g * p.G + rr % p.G) * p.o_sh + d] =
+            (uint16_t)(pack_out<DT>(v * vs, 0.f) & 0xFFFFu);
+      }
+    }
+  }
+}
+
+template <int D, int FMT, int DT>
+cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  auto fn = chunk_tile<D, FMT, DT>;
+  constexpr int smem = TileCfg<D>::kSmem;
+  static DeviceOnce once;
+  cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
+  fn<<<dim3(p.row_tiles, p.Hkv, p.S), kTileThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t pick(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  constexpr int E4 = FP8KV_KV_E4M3, E5 = FP8KV_KV_E5M2, F16 = FP8KV_DTYPE_F16, BF16 = FP8KV_DTYPE_BF16;
+  if (plan->kv_format == E5)
+    return plan->dtype == BF16 ? run<D, E5, BF16>(plan, p, st) : run<D, E5, F16>(plan, p, st);
+  return plan->dtype == BF16 ? run<D, E4, BF16>(plan, p, st) : run<D, E4, F16>(plan, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tile(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  switch (plan->head_dim) {
+    case 64: return pick<64>(plan, p, st);
+    case 128: return pick<128>(plan, p, st);
+    default: return pick<256>(plan, p, st);
+  }
+}
+
+}  // namespace fp8kv
