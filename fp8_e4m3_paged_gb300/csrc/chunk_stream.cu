@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t word(const uint4& w, int i) {
 }
 
 template <int D, int FMT, int DT, bool WIDE>
-__global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(const ChunkParams p) {
+__global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(const __grid_constant__ ChunkParams p) {
   using C = StreamCfg<D>;
   constexpr int ROWS = WIDE ? 16 : 8;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -111,56 +111,54 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
     return;
   }
 
-  // Places of a block's 16 tokens, one per lane (both halves of the warp hold them).
+  // Places of a block's 16 tokens, one per lane (both halves of the warp hold
+  // them).  The block id is requested a block before it is needed; the loads
+  // are unconditional (tokens without a place read the pool's first row and
+  // are masked, V also zeroed): a load under a condition is waited for on the spot.
   const uint8_t* kbase = p.k_cache + g * p.ksh;
   const uint8_t* vbase = p.v_cache + g * p.vsh;
   int64_t koff, voff;
   uint32_t vnext;  // which of them hold data
-  auto find = [&](int t) {
+  int blk = -1, slot = 0;
+  bool in = false;
+  auto ask = [&](int t) {
     const int v = t + (lane & 15);
-    bool ok = v < u1;
-    koff = voff = 0;
-    if (ok) {
-      int64_t blk;
-      int slot;
-      ok = chunk_place(p, b, span.position(v), blk, slot);
-      if (ok) {
-        koff = blk * p.ksb + (int64_t)slot * p.kst;
-        voff = blk * p.vsb + (int64_t)slot * p.vst;
-      } else {
-        set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-      }
+    in = v < u1;
+    blk = -1;
+    if (in) {
+      const int pos = span.position(v), page = div_page(pos, p.page_size, p.page_div);
+      slot = pos - page * p.page_size;
+      blk = __ldg(p.block_table + (int64_t)b * p.bt_stride + page);
     }
+  };
+  auto find = [&]() {
+    const bool ok = blk >= 0 && blk < p.num_kv_blocks;
+    if (in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
+    koff = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
+    voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
     vnext = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
   };
   uint4 kr[2][C::kKP], vr[4][C::kVP];
   auto load_k = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t off = __shfl_sync(0xffffffffu, koff, rq + 8 * h);
-      const bool ok = (vnext >> (rq + 8 * h)) & 1u;
+      const uint8_t* src = kbase + __shfl_sync(0xffffffffu, koff, rq + 8 * h) + c * 16;
 #pragma unroll
-      for (int i = 0; i < C::kKP; ++i)
-        kr[h][i] = ok ? ld_stream16(kbase + off + (c + 4 * i) * 16) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < C::kKP; ++i) kr[h][i] = ld_stream16(src + 64 * i);
     }
   };
   auto load_v = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = 2 * c + (j & 1) + 8 * (j >> 1);
-      const int64_t off = __shfl_sync(0xffffffffu, voff, t);
-      const bool ok = (vnext >> t) & 1u;
+      const uint8_t* src = vbase + __shfl_sync(0xffffffffu, voff, 2 * c + (j & 1) + 8 * (j >> 1));
 #pragma unroll
-      for (int i = 0; i < C::kVP; ++i) {
-        if (D >= 128)
-          vr[j][i] = ok ? ld_stream16(vbase + off + (rq + 8 * i) * 16) : make_uint4(0, 0, 0, 0);
-        else
-          vr[j][i] = ok ? ld_stream8(vbase + off + rq * 8) : make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < C::kVP; ++i)
+        vr[j][i] = D >= 128 ? ld_stream16(src + (rq + 8 * i) * 16) : ld_stream8(src + rq * 8);
     }
   };
   const int t_first = u0 + kBlk * warp;
-  find(t_first);
+  ask(t_first);
+  find();
   load_k();
   load_v();
 
@@ -243,9 +241,11 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
     m0 = m1 = kNoMax;
     l0 = l1 = 0.f;
     uint32_t valid = vnext;
-    if (t_first < u1) find(t_first + kBlk * kWarps);
+    ask(t_first + kBlk * kWarps);
     for (int t = t_first; t < u1; t += kBlk * kWarps) {
       float sc[2][4];
+            find();  // of the next block
+      ask(t + 2 * kBlk * kWarps);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
@@ -326,6 +326,13 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
           pa[2 * h + 1] = pack_half2((p0 - f.x) * kLoUp, (p1 - f.y) * kLoUp);
         }
       }
+      if (valid != 0xFFFFu) {  // 0 * NaN of a token that is not there
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (!((valid >> (2 * c + (j & 1) + 8 * (j >> 1))) & 1u))
+#pragma unroll
+            for (int i = 0; i < C::kVP; ++i) vr[j][i] = make_uint4(0, 0, 0, 0);
+      }
       if (zap) {
         constexpr bool e5 = FMT == FP8KV_KV_E5M2;
 #pragma unroll
@@ -350,10 +357,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
           for (int e = 0; e < 4; ++e) mma16816(o[(i * C::kVWords + w) * 4 + e], pa, f[0][e], f[1][e]);
         }
       valid = vnext;
-      if (t + kBlk * kWarps < u1) {
-        load_v();
-        find(t + 2 * kBlk * kWarps);
-      }
+      if (t + kBlk * kWarps < u1) load_v();
     }
     if (zap) break;
     // Non-finite sums: maybe only from codes of tokens that some rows do not see (0 * NaN).
@@ -364,7 +368,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
       for (int e = 0; e < 4; ++e) bad = fmaf(o[n][e], 0.f, bad);
     if (!__syncthreads_or(bad != 0.f)) break;
     zap = true;
-    find(t_first);
+    ask(t_first);
+    find();
     load_k();
     load_v();
   }

@@ -8,8 +8,8 @@
 // of the positions that its rows see.  Warp roles:
 //   warps 0-3, 4-7   softmax of row tile 0 and 1 (thread = row = TMEM lane);
 //                    D = 256: warps 0-3 only, and warps 4-7 decode K;
-//   warps 8-11       decode K and V (D = 256: V): FP8 rows from global memory
-//                    through registers, one tile ahead, into swizzled fp16 operand tiles;
+//   warps 8-11       decode K and V (D = 256: V): FP8 rows, requested one tile
+//                    ahead, into swizzled fp16 operand tiles;
 //   warp 12          TMEM, and every UMMA (one thread).
 // Per tile j and row tile q:  S_q = Q_q . K_j^T (M 128, N 128),
 // P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM).
@@ -50,7 +50,8 @@ struct TileCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kNQ * kM * D * 2;
   static constexpr int kOffV = kOffK + kStages * kOpBytes;
-  static constexpr int kOffMeta = kOffV + kStages * kOpBytes;
+  static constexpr int kOffRaw = kOffV + kStages * kOpBytes;  // D <= 128: FP8 K, then V rows of a tile
+  static constexpr int kOffMeta = kOffRaw + (D == 256 ? 0 : 2 * kT * D);
   static constexpr int kSmem = kOffMeta + 2048 + 1024;  // meta, alignment
   static constexpr uint32_t kColO = 256;
   static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
@@ -115,23 +116,38 @@ __device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int lane,
   return false;
 }
 
-// What a decoder lane knows about one tile: the place of position 32 w + lane.
-struct Places {
-  int64_t k, v;
-  uint32_t ok;  // ballot over the warp
-};
-
-// One tile's 32 rows of a warp: FP8 pieces in registers.
+// A decoder lane's 16-byte pieces of one tile (piece lane % kCh of rows it *
+// kRowsIt + lane / kCh of the warp's 32).  All loads are unconditional (rows
+// without a place read the pool's first one): a load under a condition is
+// waited for on the spot, one after the other.
+//
+// D <= 128: K and V together would take 64 registers of pieces in flight, so
+// they wait in shared memory instead: cp.async into places that only this
+// lane writes and reads, so no barrier is needed.
 template <int D>
-__device__ __forceinline__ void fetch_rows(const uint8_t* base, int64_t off, uint32_t ok, int lane,
-                                           uint4 (&w)[TileCfg<D>::kIts]) {
+__device__ __forceinline__ void stage_rows(const uint8_t* base, int64_t off, int lane, uint8_t* raw) {
   using C = TileCfg<D>;
 #pragma unroll
   for (int it = 0; it < C::kIts; ++it) {
-    const int r = it * C::kRowsIt + lane / C::kCh;
-    const int64_t o = __shfl_sync(0xffffffffu, off, r);
-    w[it] = ((ok >> r) & 1u) ? __ldg(reinterpret_cast<const uint4*>(base + o + (lane % C::kCh) * 16))
-                             : make_uint4(0, 0, 0, 0);
+    const int64_t o = __shfl_sync(0xffffffffu, off, it * C::kRowsIt + lane / C::kCh);
+    cp_async16(raw + (it * 32 + lane) * 16, base + o + (lane % C::kCh) * 16);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int D>
+__device__ __forceinline__ void take_rows(const uint8_t* raw, int lane, uint4 (&w)[TileCfg<D>::kIts]) {
+  using C = TileCfg<D>;
+#pragma unroll
+  for (int it = 0; it < C::kIts; ++it) w[it] = *reinterpret_cast<const uint4*>(raw + (it * 32 + lane) * 16);
+}
+// D = 256 (no shared memory left, but one stream per warp): in registers.
+template <int D>
+__device__ __forceinline__ void fetch_rows(const uint8_t* base, int64_t off, int lane, uint4 (&w)[TileCfg<D>::kIts]) {
+  using C = TileCfg<D>;
+#pragma unroll
+  for (int it = 0; it < C::kIts; ++it) {
+    const int64_t o = __shfl_sync(0xffffffffu, off, it * C::kRowsIt + lane / C::kCh);
+    w[it] = __ldg(reinterpret_cast<const uint4*>(base + o + (lane % C::kCh) * 16));
   }
 }
 
@@ -158,76 +174,129 @@ __device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[TileCfg
   }
 }
 
-// Decoders: K, V or both streams of every tile.  Rows whose block is out of
-// range, or past the partition, are zero.
+// V pieces before they are stored: zero for rows whose block is out of range or that
+// lie past the partition (their weight is 0, and 0 * NaN would not be; K rows
+// need not, their logits are masked), and non-finite codes as zero (returns
+// true if there were any).
+template <int D, int FMT>
+__device__ __forceinline__ bool clean_v(uint4 (&w)[TileCfg<D>::kIts], uint32_t ok, int lane) {
+  using C = TileCfg<D>;
+  constexpr bool e5 = FMT == FP8KV_KV_E5M2;
+  if (ok != 0xFFFFFFFFu) {
+#pragma unroll
+    for (int i = 0; i < C::kIts; ++i)
+      if (!((ok >> (i * C::kRowsIt + lane / C::kCh)) & 1u)) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  uint32_t any = 0u;
+#pragma unroll
+  for (int i = 0; i < C::kIts; ++i) any |= nonfinite_codes(w[i], e5);
+  if (any == 0u) return false;
+#pragma unroll
+  for (int i = 0; i < C::kIts; ++i)
+    w[i] = make_uint4(zap_nonfinite(w[i].x, e5), zap_nonfinite(w[i].y, e5), zap_nonfinite(w[i].z, e5),
+                      zap_nonfinite(w[i].w, e5));
+  return true;
+}
+
+// Decoders: K, V or both streams of every tile.
 template <int D, int FMT, bool DO_K, bool DO_V>
 __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt, uint8_t* smem, int b, int g, int u0,
                                              int u1, int n_tiles, const ChunkSpan& span, int w, int lane) {
   using C = TileCfg<D>;
   constexpr int NS = C::kStages;
+  constexpr bool BOTH = DO_K && DO_V;  // through shared memory
   volatile uint32_t* const abort_flag = &mt.abort;
   const uint8_t* kbase = p.k_cache + g * p.ksh;
   const uint8_t* vbase = p.v_cache + g * p.vsh;
-  auto find = [&](int j) {
-    Places f = {0, 0, 0u};
+  // Position 32 w + lane of a tile: its block id is requested one tile before
+  // the place is needed, so that nothing waits for that load either.
+  int blk = -1, slot = 0;
+  bool in = false;
+  auto ask = [&](int j) {
     const int v = u0 + j * kT + 32 * w + lane;
-    bool ok = v < u1;
-    if (ok) {
-      int64_t blk;
-      int slot;
-      ok = chunk_place(p, b, span.position(v), blk, slot);
-      if (ok) {
-        f.k = blk * p.ksb + (int64_t)slot * p.kst;
-        f.v = blk * p.vsb + (int64_t)slot * p.vst;
-      } else if (DO_K) {
-        set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-      }
+    in = v < u1;
+    blk = -1;
+    if (in) {
+      const int pos = span.position(v), page = div_page(pos, p.page_size, p.page_div);
+      slot = pos - page * p.page_size;
+      blk = __ldg(p.block_table + (int64_t)b * p.bt_stride + page);
     }
-    f.ok = __ballot_sync(0xffffffffu, ok);
-    return f;
   };
-  uint4 kr[DO_K ? C::kIts : 1], vr[DO_V ? C::kIts : 1];
+  int64_t koff = 0, voff = 0;
+  uint32_t ok_next = 0u;
+  auto find = [&]() {
+    const bool ok = blk >= 0 && blk < p.num_kv_blocks;
+    if (DO_K && in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
+    if (DO_K) koff = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
+    if (DO_V) voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
+    ok_next = __ballot_sync(0xffffffffu, ok);
+  };
+  uint8_t* rawk = smem + C::kOffRaw + w * (32 * D);
+  uint8_t* rawv = rawk + kT * D;
+  uint4 x[C::kIts];
   bool bad = false;
-  Places f = find(0);
-  if constexpr (DO_K) fetch_rows<D>(kbase, f.k, f.ok, lane, kr);
-  if constexpr (DO_V) fetch_rows<D>(vbase, f.v, f.ok, lane, vr);
-  uint32_t ok_now = f.ok;
-  if (n_tiles > 1) f = find(1);
+  auto request_k = [&]() {
+    if constexpr (BOTH)
+      stage_rows<D>(kbase, koff, lane, rawk);
+    else
+      fetch_rows<D>(kbase, koff, lane, x);
+  };
+  auto request_v = [&]() {
+    if constexpr (BOTH)
+      stage_rows<D>(vbase, voff, lane, rawv);
+    else
+      fetch_rows<D>(vbase, voff, lane, x);
+  };
+  ask(0);
+  find();
+  if constexpr (DO_K) request_k();
+  if constexpr (DO_V) request_v();
+  uint32_t ok_now = ok_next;
+  if (n_tiles > 1) ask(1);
+  bool ok = true;
   for (int j = 0; j < n_tiles; ++j) {
     const int st = j % NS;
     const uint32_t empty_parity = ((j / NS) - 1) & 1;
+    if (j + 1 < n_tiles) find();
+    if (j + 2 < n_tiles) ask(j + 2);
+    // The last tile requests itself again, so that the count of groups in
+    // flight is the same for every tile.
     if constexpr (DO_K) {
-      if (j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) return false;
-      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w, lane);
+      if constexpr (BOTH) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V's may be under way
+        take_rows<D>(rawk, lane, x);
+      }
+      if (j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) {
+        ok = false;
+        break;
+      }
+      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, x, 32 * w, lane);
       // K(j+8) is decoded after QK(j+4) at the earliest, and that after softmax j+3
       if (lane == 0) mt.valid[j & 7][w] = ok_now;
       fence_proxy_async_smem();
       mbar_arrive(&mt.k_full[st]);
-      if (j + 1 < n_tiles) fetch_rows<D>(kbase, f.k, f.ok, lane, kr);
+      request_k();
     }
     if constexpr (DO_V) {
-      constexpr bool e5 = FMT == FP8KV_KV_E5M2;
-      uint32_t any = 0u;
-#pragma unroll
-      for (int i = 0; i < C::kIts; ++i) any |= nonfinite_codes(vr[i], e5);
-      if (any != 0u) {
-        bad = true;
-#pragma unroll
-        for (int i = 0; i < C::kIts; ++i)
-          vr[i] = make_uint4(zap_nonfinite(vr[i].x, e5), zap_nonfinite(vr[i].y, e5), zap_nonfinite(vr[i].z, e5),
-                             zap_nonfinite(vr[i].w, e5));
+      if constexpr (BOTH) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        take_rows<D>(rawv, lane, x);
       }
-      if (j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) return false;
-      store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, vr, 32 * w, lane);
+      bad |= clean_v<D, FMT>(x, ok_now, lane);
+      if (j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) {
+        ok = false;
+        break;
+      }
+      store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, x, 32 * w, lane);
       fence_proxy_async_smem();
       mbar_arrive(&mt.v_full[st]);
-      if (j + 1 < n_tiles) fetch_rows<D>(vbase, f.v, f.ok, lane, vr);
+      request_v();
     }
-    ok_now = f.ok;
-    if (j + 2 < n_tiles) f = find(j + 2);
+    ok_now = ok_next;
   }
+  if constexpr (BOTH) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (bad) mt.vbad = 1u;
-  return true;
+  return ok;
 }
 
 // Visibility of 32 virtual tokens v0 .. v0+31 for one row, as bits.
@@ -236,8 +305,74 @@ __device__ __forceinline__ uint32_t sees32(const ChunkRow& r, int sk, int v0) {
   return below(r.hi - v0) & (~below(r.lo - v0) | below(sk - v0));
 }
 
+// Two FP32 values in a register pair (packed arithmetic of sm_100).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Largest visible element of this thread's 128 columns of S (a NaN is passed
+// over: it makes the row's sum NaN).  FULL: every column is visible.
+template <bool FULL>
+__device__ __forceinline__ float row_max(uint32_t tS, const uint32_t (&vis)[4]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[64];
+    tmem_ld64(tS + 64 * h, x);
+#pragma unroll
+    for (int k = 0; k < 64; ++k) {
+      const float v = __uint_as_float(x[k]);
+      m[(k / 2) & 3] = fmaxf(m[(k / 2) & 3], FULL || ((vis[2 * h + k / 32] >> (k & 31)) & 1u) ? v : -INFINITY);
+    }
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// P = 2^(c S + sh) as fp16 over S (masked columns: 0); returns the sum.
+template <bool FULL>
+__device__ __forceinline__ float exp_tile(uint32_t tS, const uint32_t (&vis)[4], float c, float sh) {
+  const uint64_t c2 = pair(c, c), sh2 = pair(sh, sh);
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[32], y[16];
+    tmem_ld32(tS + 32 * i, x);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
+      if (!FULL) {
+        e.x = ((vis[i] >> k) & 1u) ? e.x : -INFINITY;
+        e.y = ((vis[i] >> (k + 1)) & 1u) ? e.y : -INFINITY;
+      }
+      const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+      sum[(k / 2) & 1] = add2(sum[(k / 2) & 1], pair(p0, p1));
+      y[k / 2] = pack_half2(p0, p1);
+    }
+    tmem_st16(tS + 16 * i, y);  // over S columns that were read
+  }
+  const float2 t = unpair(add2(sum[0], sum[1]));
+  return t.x + t.y;
+}
+
 template <int D, int FMT, int DT>
-__global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const ChunkParams p) {
+__global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_constant__ ChunkParams p) {
   using C = TileCfg<D>;
   constexpr int NQ = C::kNQ, ROWS = NQ * kM;
   extern __shared__ uint8_t smem_raw[];
@@ -391,16 +526,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const ChunkParams 
         if (!full)
 #pragma unroll
           for (int i = 0; i < 4; ++i) vis[i] &= sees32(row, span.sk, v0 + 32 * i);
-        // row maximum over the visible logits
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t x[32];
-          tmem_ld32(tS + 32 * i, x);
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            mx = fmaxf(mx, full || ((vis[i] >> k) & 1u) ? __uint_as_float(x[k]) : -INFINITY);
-        }
+        float mx = full ? row_max<true>(tS, vis) : row_max<false>(tS, vis);
         if (mx > -INFINITY) mx *= c;
         if (__any_sync(0xffffffffu, mx > -INFINITY && !(mx <= m + kChunkTau))) {
           const float n = mx > m + kChunkTau || m == kNoMax ? fmaxf(m, ceilf(mx)) : m;
@@ -427,23 +553,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const ChunkParams 
           }
         }
         const float sh = kChunkPShift - (m == kNoMax ? 0.f : m);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t x[32], y[16];
-          tmem_ld32(tS + 32 * i, x);
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float e0 = fmaf(__uint_as_float(x[k]), c, sh), e1 = fmaf(__uint_as_float(x[k + 1]), c, sh);
-            if (!full) {
-              e0 = ((vis[i] >> k) & 1u) ? e0 : -INFINITY;
-              e1 = ((vis[i] >> (k + 1)) & 1u) ? e1 : -INFINITY;
-            }
-            const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
-            l += p0 + p1;
-            y[k / 2] = pack_half2(p0, p1);
-          }
-          tmem_st16(tS + 16 * i, y);  // over S columns that were read
-        }
+        l += full ? exp_tile<true>(tS, vis, c, sh) : exp_tile<false>(tS, vis, c, sh);
         tc_fence_before();
         mbar_arrive(&mt.p_ready[buf]);
       }
