@@ -10,7 +10,7 @@
 //                    D = 256: warps 0-3 only, and warps 4-7 decode K;
 //   warps 8-11       decode K and V (D = 256: V): FP8 rows, requested one tile
 //                    ahead, into swizzled fp16 operand tiles;
-//   warp 12          TMEM, and every UMMA (one thread).
+//   warp 12          TMEM, and every UMMA.
 // Per tile j and row tile q:  S_q = Q_q . K_j^T (M 128, N 128),
 // P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM).
 // Two row tiles alternate: while one's softmax runs, the tensor core works on
@@ -47,16 +47,18 @@ struct TileCfg {
   static constexpr int kNQ = D == 256 ? 1 : 2;
   static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 4;  // K stages, and V stages
   static constexpr int kOpBytes = kT * D * 2;
+  static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
+  static constexpr int kRowsIt = 32 / kCh;    // rows a warp moves at a time
+  static constexpr int kParts = D == 256 ? 2 : 1;       // a tile's rows are staged in so many parts (shared memory)
+  static constexpr int kIts = 32 / kRowsIt / kParts;    // times, for its rows of a part
+  static constexpr int kRawBytes = 2 * kT * D / kParts; // staged FP8 rows of K and V
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kNQ * kM * D * 2;
   static constexpr int kOffV = kOffK + kStages * kOpBytes;
-  static constexpr int kOffRaw = kOffV + kStages * kOpBytes;  // D <= 128: FP8 K, then V rows of a tile
-  static constexpr int kOffMeta = kOffRaw + (D == 256 ? 0 : 2 * kT * D);
+  static constexpr int kOffRaw = kOffV + kStages * kOpBytes;  // FP8 K rows, then V rows
+  static constexpr int kOffMeta = kOffRaw + kRawBytes;
   static constexpr int kSmem = kOffMeta + 2048 + 1024;  // meta, alignment
   static constexpr uint32_t kColO = 256;
-  static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
-  static constexpr int kRowsIt = 32 / kCh;    // rows a warp moves at a time
-  static constexpr int kIts = 32 / kRowsIt;   // times, for its 32 rows
   static_assert(kNQ * D <= 256 && kSmem <= 232448, "TMEM and shared memory");
 };
 
@@ -74,6 +76,13 @@ static_assert(sizeof(TileMeta) <= 2048, "meta block");
 // A bounded wait of a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls, abort_flag));
+}
+
+// One lane of a converged warp (always the same).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
 
 // Request and first packed row of this CTA: tiles count over the requests in
@@ -116,20 +125,17 @@ __device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int lane,
   return false;
 }
 
-// A decoder lane's 16-byte pieces of one tile (piece lane % kCh of rows it *
-// kRowsIt + lane / kCh of the warp's 32).  All loads are unconditional (rows
-// without a place read the pool's first one): a load under a condition is
-// waited for on the spot, one after the other.
-//
-// D <= 128: K and V together would take 64 registers of pieces in flight, so
-// they wait in shared memory instead: cp.async into places that only this
-// lane writes and reads, so no barrier is needed.
+// A decoder lane's 16-byte pieces of one tile part (piece lane % kCh of rows
+// it * kRowsIt + lane / kCh of the warp's rows of the part).  They wait in shared memory,
+// in places that only this lane writes (cp.async) and reads, so no barrier is
+// needed; in registers, K and V in flight would take 64.  The copies are
+// unconditional: rows without a place read the pool's first one.
 template <int D>
-__device__ __forceinline__ void stage_rows(const uint8_t* base, int64_t off, int lane, uint8_t* raw) {
+__device__ __forceinline__ void stage_rows(const uint8_t* base, int64_t off, int part, int lane, uint8_t* raw) {
   using C = TileCfg<D>;
 #pragma unroll
   for (int it = 0; it < C::kIts; ++it) {
-    const int64_t o = __shfl_sync(0xffffffffu, off, it * C::kRowsIt + lane / C::kCh);
+    const int64_t o = __shfl_sync(0xffffffffu, off, (part * C::kIts + it) * C::kRowsIt + lane / C::kCh);
     cp_async16(raw + (it * 32 + lane) * 16, base + o + (lane % C::kCh) * 16);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -139,16 +145,6 @@ __device__ __forceinline__ void take_rows(const uint8_t* raw, int lane, uint4 (&
   using C = TileCfg<D>;
 #pragma unroll
   for (int it = 0; it < C::kIts; ++it) w[it] = *reinterpret_cast<const uint4*>(raw + (it * 32 + lane) * 16);
-}
-// D = 256 (no shared memory left, but one stream per warp): in registers.
-template <int D>
-__device__ __forceinline__ void fetch_rows(const uint8_t* base, int64_t off, int lane, uint4 (&w)[TileCfg<D>::kIts]) {
-  using C = TileCfg<D>;
-#pragma unroll
-  for (int it = 0; it < C::kIts; ++it) {
-    const int64_t o = __shfl_sync(0xffffffffu, off, it * C::kRowsIt + lane / C::kCh);
-    w[it] = __ldg(reinterpret_cast<const uint4*>(base + o + (lane % C::kCh) * 16));
-  }
 }
 
 // ... and as fp16 in the operand tile: 64-column blocks of kT rows of 128
@@ -177,7 +173,7 @@ __device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[TileCfg
 // V pieces before they are stored: zero for rows whose block is out of range or that
 // lie past the partition (their weight is 0, and 0 * NaN would not be; K rows
 // need not, their logits are masked), and non-finite codes as zero (returns
-// true if there were any).
+// true if there were any).  ok: the part's rows from bit 0 on.
 template <int D, int FMT>
 __device__ __forceinline__ bool clean_v(uint4 (&w)[TileCfg<D>::kIts], uint32_t ok, int lane) {
   using C = TileCfg<D>;
@@ -203,8 +199,7 @@ template <int D, int FMT, bool DO_K, bool DO_V>
 __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt, uint8_t* smem, int b, int g, int u0,
                                              int u1, int n_tiles, const ChunkSpan& span, int w, int lane) {
   using C = TileCfg<D>;
-  constexpr int NS = C::kStages;
-  constexpr bool BOTH = DO_K && DO_V;  // through shared memory
+  constexpr int NS = C::kStages, PARTS = C::kParts, PART_ROWS = 32 / PARTS;
   volatile uint32_t* const abort_flag = &mt.abort;
   const uint8_t* kbase = p.k_cache + g * p.ksh;
   const uint8_t* vbase = p.v_cache + g * p.vsh;
@@ -231,70 +226,71 @@ __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt,
     if (DO_V) voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
     ok_next = __ballot_sync(0xffffffffu, ok);
   };
-  uint8_t* rawk = smem + C::kOffRaw + w * (32 * D);
-  uint8_t* rawv = rawk + kT * D;
-  uint4 x[C::kIts];
-  bool bad = false;
-  auto request_k = [&]() {
-    if constexpr (BOTH)
-      stage_rows<D>(kbase, koff, lane, rawk);
-    else
-      fetch_rows<D>(kbase, koff, lane, x);
-  };
-  auto request_v = [&]() {
-    if constexpr (BOTH)
-      stage_rows<D>(vbase, voff, lane, rawv);
-    else
-      fetch_rows<D>(vbase, voff, lane, x);
-  };
+  uint8_t* rawk = smem + C::kOffRaw + w * (PART_ROWS * D);
+  uint8_t* rawv = rawk + C::kRawBytes / 2;
   ask(0);
   find();
-  if constexpr (DO_K) request_k();
-  if constexpr (DO_V) request_v();
+  if (DO_K) stage_rows<D>(kbase, koff, 0, lane, rawk);
+  if (DO_V) stage_rows<D>(vbase, voff, 0, lane, rawv);
   uint32_t ok_now = ok_next;
   if (n_tiles > 1) ask(1);
-  bool ok = true;
-  for (int j = 0; j < n_tiles; ++j) {
+  bool ok = true, bad = false;
+  for (int j = 0; j < n_tiles && ok; ++j) {
     const int st = j % NS;
     const uint32_t empty_parity = ((j / NS) - 1) & 1;
-    if (j + 1 < n_tiles) find();
-    if (j + 2 < n_tiles) ask(j + 2);
-    // The last tile requests itself again, so that the count of groups in
-    // flight is the same for every tile.
-    if constexpr (DO_K) {
-      if constexpr (BOTH) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V's may be under way
+    // A stage copy follows each part taken (the very last one again), so that the
+    // number of copies in flight is always the same.
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      const int next = (part + 1) % PARTS;
+      if (next == 0) {
+        if (j + 1 < n_tiles) find();
+        if (j + 2 < n_tiles) ask(j + 2);
+      }
+      uint4 x[C::kIts];
+      if constexpr (DO_K) {
+        if (DO_V)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");  // V's is still under way
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
         take_rows<D>(rawk, lane, x);
+        if (part == 0 && j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) {
+          ok = false;
+          break;
+        }
+        store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, x, 32 * w + part * PART_ROWS, lane);
+        if (next == 0) {
+          // K(j+8) is decoded after QK(j+4) at the earliest, and that after softmax j+3
+          if (lane == 0) mt.valid[j & 7][w] = ok_now;
+          fence_proxy_async_smem();
+          mbar_arrive(&mt.k_full[st]);
+        }
+        stage_rows<D>(kbase, koff, next, lane, rawk);
       }
-      if (j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) {
-        ok = false;
-        break;
-      }
-      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, x, 32 * w, lane);
-      // K(j+8) is decoded after QK(j+4) at the earliest, and that after softmax j+3
-      if (lane == 0) mt.valid[j & 7][w] = ok_now;
-      fence_proxy_async_smem();
-      mbar_arrive(&mt.k_full[st]);
-      request_k();
-    }
-    if constexpr (DO_V) {
-      if constexpr (BOTH) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if constexpr (DO_V) {
+        if (DO_K)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
         take_rows<D>(rawv, lane, x);
+        // the part's rows from bit 0 on, no row missing above them
+        constexpr uint32_t above = PARTS == 1 ? 0u : 0xFFFF0000u;
+        bad |= clean_v<D, FMT>(x, (ok_now >> (part * PART_ROWS)) | above, lane);
+        if (part == 0 && j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) {
+          ok = false;
+          break;
+        }
+        store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, x, 32 * w + part * PART_ROWS, lane);
+        if (next == 0) {
+          fence_proxy_async_smem();
+          mbar_arrive(&mt.v_full[st]);
+        }
+        stage_rows<D>(vbase, voff, next, lane, rawv);
       }
-      bad |= clean_v<D, FMT>(x, ok_now, lane);
-      if (j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) {
-        ok = false;
-        break;
-      }
-      store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, x, 32 * w, lane);
-      fence_proxy_async_smem();
-      mbar_arrive(&mt.v_full[st]);
-      request_v();
     }
     ok_now = ok_next;
   }
-  if constexpr (BOTH) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (bad) mt.vbad = 1u;
   return ok;
 }
@@ -333,13 +329,13 @@ template <bool FULL>
 __device__ __forceinline__ float row_max(uint32_t tS, const uint32_t (&vis)[4]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t x[64];
-    tmem_ld64(tS + 64 * h, x);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[32];
+    tmem_ld32(tS + 32 * i, x);
 #pragma unroll
-    for (int k = 0; k < 64; ++k) {
+    for (int k = 0; k < 32; ++k) {
       const float v = __uint_as_float(x[k]);
-      m[(k / 2) & 3] = fmaxf(m[(k / 2) & 3], FULL || ((vis[2 * h + k / 32] >> (k & 31)) & 1u) ? v : -INFINITY);
+      m[(k / 2) & 3] = fmaxf(m[(k / 2) & 3], FULL || ((vis[i] >> k) & 1u) ? v : -INFINITY);
     }
   }
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
@@ -449,51 +445,52 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       // ====================================================== Q tile
       // One warp per row: fp16 as it is, bf16 scaled by a power of two; the
       // sign of the logit factor goes into Q.
-      constexpr int V = D / 32;
+      constexpr int V = D / 32;  // elements per lane
+      constexpr int kRowsAtOnce = 8;
       uint8_t* sQ = smem + C::kOffQ + q * (kM * D * 2);
       const uint32_t flip = cd < 0 ? 0x80008000u : 0u;
-#pragma unroll 4
-      for (int k = 0; k < 32; ++k) {
-        const int r = 32 * (warp & 3) + k, rr = q * kM + r;
-        uint32_t w[V / 2] = {};
-        if (rr < RC) {
-          const int pr = work.row0 + rr;
-          const uint16_t* src = p.q + (int64_t)(req.row0 + pr / p.G) * p.q_st + (int64_t)(g * p.G + pr % p.G) * p.q_sh;
+      const int e = lane * V;  // first element of the lane
+#pragma unroll 1
+      for (int k0 = 0; k0 < 32; k0 += kRowsAtOnce) {
+        uint32_t w[kRowsAtOnce][V / 2];
+        // all loads first, rows past RC read the last one (their results are dropped)
+#pragma unroll
+        for (int k = 0; k < kRowsAtOnce; ++k) {
+          const int pr = work.row0 + min(q * kM + 32 * (warp & 3) + k0 + k, RC - 1);
+          const uint16_t* src =
+              p.q + (int64_t)(req.row0 + pr / p.G) * p.q_st + (int64_t)(g * p.G + pr % p.G) * p.q_sh + e;
           if constexpr (V == 2) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t*>(src + lane * V));
+            w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
           } else if constexpr (V == 4) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + lane * V));
-            w[0] = x.x;
-            w[1] = x.y;
+            *reinterpret_cast<uint2*>(w[k]) = __ldg(reinterpret_cast<const uint2*>(src));
           } else {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + lane * V));
-            w[0] = x.x;
-            w[1] = x.y;
-            w[2] = x.z;
-            w[3] = x.w;
+            *reinterpret_cast<uint4*>(w[k]) = __ldg(reinterpret_cast<const uint4*>(src));
           }
         }
-        if (DT == FP8KV_DTYPE_BF16) {
-          uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i)
-            top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
-          const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+        for (int k = 0; k < kRowsAtOnce; ++k) {
+          const int r = 32 * (warp & 3) + k0 + k;
+          if (DT == FP8KV_DTYPE_BF16) {
+            uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i)
-            w[i] = pack_half2(__uint_as_float(w[i] << 16) * rs.to_f16, __uint_as_float(w[i] & 0xFFFF0000u) * rs.to_f16);
-          if (lane == 0) mt.back[rr] = rs.back;
+            for (int i = 0; i < V / 2; ++i) top = max(top, max((w[k][i] << 16) & 0x7FFFFFFFu, w[k][i] & 0x7FFF0000u));
+            const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+              w[k][i] = pack_half2(__uint_as_float(w[k][i] << 16) * rs.to_f16,
+                                   __uint_as_float(w[k][i] & 0xFFFF0000u) * rs.to_f16);
+            if (lane == 0) mt.back[q * kM + r] = rs.back;
+          }
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) w[k][i] ^= flip;
+          uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
+          if constexpr (V == 2)
+            *reinterpret_cast<uint32_t*>(dst) = w[k][0];
+          else if constexpr (V == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(w[k][0], w[k][1]);
+          else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
         }
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) w[i] ^= flip;
-        const int e = lane * V;  // first element of the lane
-        uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
-        if constexpr (V == 2)
-          *reinterpret_cast<uint32_t*>(dst) = w[0];
-        else if constexpr (V == 4)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        else
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       __syncwarp();
       fence_proxy_async_smem();
@@ -603,77 +600,81 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       ok = decode_tiles<D, FMT, true, false>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
     else
       ok = decode_tiles<D, FMT, false, true>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
-  } else if (lane == 0) {
+  } else {
     // ======================================================== UMMA issue
+    // The whole warp walks the schedule and one elected lane issues: operands
+    // then stay in uniform registers (issued by a lone diverged lane, each UMMA cost
+    // its thread ~80 cycles, more than the 65 that the tensor core needs).
     constexpr int NS = C::kStages;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t idesc_qk = idesc_f16_f32(kM, kT, false, false);
     const uint32_t idesc_pv = idesc_f16_f32(kM, D, false, true);
     const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kSw128);
     const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
     const uint64_t vdesc = smem_desc(smem_u32(smem + C::kOffV), kT * 128, 1024, kSw128);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait(bar, parity, kPolls, abort_flag);
+      ok = ok && warp_wait(bar, parity, abort_flag);
       tc_fence_after();
       return ok;
     };
-    auto qk = [&](int q, int buf, int j) {
+    static_assert(kM == kT, "Q and K tiles share their block stride");
+    // S(buf) = Q_q . K_j^T, then the barriers that it completes
+    auto qk = [&](int q, int buf, int j, bool k_last) {
       const uint64_t qd = qdesc + (uint64_t)((q * (kM * D * 2)) >> 4);
       const uint64_t kd = kdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);  // kM == kT
-        mma_ss(tmem + buf * 128, qd + step, kd + step, idesc_qk, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);
+          mma_ss(tm + buf * 128, qd + step, kd + step, idesc_qk, kk > 0);
+        }
+        mma_commit(&mt.s_full[buf]);
+        if (k_last) mma_commit(&mt.k_empty[j % NS]);
       }
-      mma_commit(&mt.s_full[buf]);
     };
-    auto pv = [&](int q, int buf, int j) {
+    // O_q += P(buf) . V_j
+    auto pv = [&](int q, int buf, int j, bool v_last, uint64_t* done) {
       const uint64_t vd = vdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk)
-        mma_ts(tmem + C::kColO + q * D, tmem + buf * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
-               (j > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < kT / 16; ++kk)
+          mma_ts(tm + C::kColO + q * D, tm + buf * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                 (j > 0 || kk > 0) ? 1u : 0u);
+        if (v_last) mma_commit(&mt.v_empty[j % NS]);
+        if (done) mma_commit(done);
+      }
     };
-    static_assert(kM == kT, "Q and K tiles share their block stride");
     if (wait(&mt.q_full, 0) && wait(&mt.k_full[0], 0)) {
       if (NQ == 2) {
         // S and P of a row tile share their columns: QK(j+1) follows PV(j) in
         // issue order, in which the tensor core runs one CTA's UMMAs
-        for (int q = 0; q < nq; ++q) qk(q, q, 0);
-        mma_commit(&mt.k_empty[0]);
+        for (int q = 0; q < nq; ++q) qk(q, q, 0, q == nq - 1);
         for (int j = 0; j < n_tiles && ok; ++j) {
           if (!wait(&mt.v_full[j % NS], (j / NS) & 1)) break;
           for (int q = 0; q < nq; ++q) {
             if (!wait(&mt.p_ready[q], j & 1)) break;
-            pv(q, q, j);
-            if (q == nq - 1) mma_commit(&mt.v_empty[j % NS]);
-            if (j + 1 == n_tiles) {
-              mma_commit(&mt.o_all[q]);
-            } else {
-              if (q == 0 && !wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
-              qk(q, q, j + 1);
-              if (q == nq - 1) mma_commit(&mt.k_empty[(j + 1) % NS]);
-            }
+            pv(q, q, j, q == nq - 1, j + 1 == n_tiles ? &mt.o_all[q] : nullptr);
+            if (j + 1 == n_tiles) continue;
+            if (q == 0 && !wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
+            qk(q, q, j + 1, q == nq - 1);
           }
         }
       } else {
-        qk(0, 0, 0);
-        mma_commit(&mt.k_empty[0]);
+        qk(0, 0, 0, true);
         for (int j = 0; j < n_tiles; ++j) {
           if (j + 1 < n_tiles) {
             // its buffer held P(j-1), whose PV was issued before
             if (!wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
-            qk(0, (j + 1) & 1, j + 1);
-            mma_commit(&mt.k_empty[(j + 1) % NS]);
+            qk(0, (j + 1) & 1, j + 1, true);
           }
           if (!wait(&mt.v_full[j % NS], (j / NS) & 1) || !wait(&mt.p_ready[j & 1], (j >> 1) & 1)) break;
-          pv(0, j & 1, j);
-          mma_commit(&mt.v_empty[j % NS]);
-          mma_commit(j + 1 == n_tiles ? &mt.o_all[0] : &mt.o_done);
+          pv(0, j & 1, j, true, j + 1 == n_tiles ? &mt.o_all[0] : &mt.o_done);
         }
       }
     }
     // every UMMA issued must be done before TMEM is freed
-    mma_commit(&mt.drain);
+    if (elect_one()) mma_commit(&mt.drain);
+    __syncwarp();
     mbar_wait_plain(&mt.drain, 0, kPolls);
   }
   if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
