@@ -5,17 +5,20 @@
 // into rows (token * G + head), so a tile is full whatever the group size and
 // one decode of K and V serves all of them.  A CTA owns 256 rows (two row
 // tiles; 128 rows for D = 256) of one request and KV head, and one partition
-// of the positions that its rows see.  Warp roles:
-//   warps 0-3, 4-7   softmax of row tile 0 and 1 (thread = row = TMEM lane);
+// of the positions that its rows see.  Twelve warps, so that each thread may
+// have 168 registers (a row of S is 128 of them):
+//   warps 0-3, 4-7   row tiles 0 and 1 (thread = row = TMEM lane): softmax, and
+//                    the first warp of the four issues the row tile's UMMAs;
 //                    D = 256: warps 0-3 only, and warps 4-7 decode K;
 //   warps 8-11       decode K and V (D = 256: V): FP8 rows, requested one tile
-//                    ahead, into swizzled fp16 operand tiles;
-//   warp 12          TMEM, and every UMMA.
+//                    ahead into registers, to swizzled fp16 operand tiles.
 // Per tile j and row tile q:  S_q = Q_q . K_j^T (M 128, N 128),
-// P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM).
-// Two row tiles alternate: while one's softmax runs, the tensor core works on
-// the other's S and O.  For D = 256 two S buffers of the one row tile do the
-// same: QK of tile j+1 is issued before PV of tile j.
+// P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM),
+// P and PV by halves of 64 positions, so that the first half's PV runs under
+// the second half's exponentials.  Two row tiles alternate: while one's
+// softmax runs, the tensor core works on the other's S and O.  For D = 256
+// two S buffers of the one row tile do the same: QK of tile j+1 is issued between
+// the halves of PV(j).
 // TMEM: S at columns 0 and 128, O at 256 (256 columns).
 //
 // Every wait is bounded (see split_tc_kernel.cuh): a wait that gives up sets the
@@ -37,10 +40,10 @@ using namespace tc;
 
 constexpr int kT = kChunkTileTokens;
 constexpr int kM = 128;                  // rows per tile
-constexpr int kTileThreads = 13 * 32;
-constexpr int kMmaWarp = 12;
+constexpr int kTileThreads = 12 * 32;
 constexpr int kStagesMax = 4;
 constexpr uint32_t kPolls = 1u << 20;    // polls per wait
+constexpr int kMetaBytes = 4096;
 
 template <int D>
 struct TileCfg {
@@ -49,29 +52,26 @@ struct TileCfg {
   static constexpr int kOpBytes = kT * D * 2;
   static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
   static constexpr int kRowsIt = 32 / kCh;    // rows a warp moves at a time
-  static constexpr int kParts = D == 256 ? 2 : 1;       // a tile's rows are staged in so many parts (shared memory)
-  static constexpr int kIts = 32 / kRowsIt / kParts;    // times, for its rows of a part
-  static constexpr int kRawBytes = 2 * kT * D / kParts; // staged FP8 rows of K and V
+  static constexpr int kIts = 32 / kRowsIt;   // times, for its 32 rows
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kNQ * kM * D * 2;
   static constexpr int kOffV = kOffK + kStages * kOpBytes;
-  static constexpr int kOffRaw = kOffV + kStages * kOpBytes;  // FP8 K rows, then V rows
-  static constexpr int kOffMeta = kOffRaw + kRawBytes;
-  static constexpr int kSmem = kOffMeta + 2048 + 1024;  // meta, alignment
+  static constexpr int kOffMeta = kOffV + kStages * kOpBytes;
+  static constexpr int kSmem = kOffMeta + kMetaBytes + 1024;  // meta, alignment
   static constexpr uint32_t kColO = 256;
   static_assert(kNQ * D <= 256 && kSmem <= 232448, "TMEM and shared memory");
 };
 
 struct TileMeta {
-  uint64_t q_full, drain;
+  uint64_t q_full[2], drain[2];
   uint64_t k_full[kStagesMax], k_empty[kStagesMax], v_full[kStagesMax], v_empty[kStagesMax];
-  uint64_t s_full[2], p_ready[2], o_all[2];  // o_all: a row tile's last PV is done
-  uint64_t o_done;                           // D = 256: PV(j) is done, every tile but the last
-  uint32_t valid[8][4];  // per tile (j % 8): positions whose block is in range
+  uint64_t s_full[2], p_ready[2][2], o_all[2];  // P by halves; o_all: a row tile's last PV is done
+  uint64_t o_done;                              // D = 256: PV(j) is done, every tile but the last
+  alignas(16) uint32_t valid[8][4];             // per tile (j % 8): positions whose block is in range
+  int64_t place[2][4][32];                      // per decoder warp: byte offsets of its rows
   uint32_t tmem, abort, vbad;
-  float back[2 * kM];    // inverse row scales
 };
-static_assert(sizeof(TileMeta) <= 2048, "meta block");
+static_assert(sizeof(TileMeta) <= kMetaBytes, "meta block");
 
 // A bounded wait of a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
@@ -125,26 +125,19 @@ __device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int lane,
   return false;
 }
 
-// A decoder lane's 16-byte pieces of one tile part (piece lane % kCh of rows
-// it * kRowsIt + lane / kCh of the warp's rows of the part).  They wait in shared memory,
-// in places that only this lane writes (cp.async) and reads, so no barrier is
-// needed; in registers, K and V in flight would take 64.  The copies are
-// unconditional: rows without a place read the pool's first one.
+// A decoder lane's 16-byte pieces of one tile (piece lane % kCh of rows it *
+// kRowsIt + lane / kCh of the warp's 32).  The loads are unconditional (rows
+// without a place read the pool's first one): a load under a condition is
+// waited for on the spot, one after the other.  The rows' offsets come
+// through shared memory: one access each, where a shuffle would take two.
 template <int D>
-__device__ __forceinline__ void stage_rows(const uint8_t* base, int64_t off, int part, int lane, uint8_t* raw) {
+__device__ __forceinline__ void fetch_rows(const uint8_t* base, const int64_t* place, int lane,
+                                           uint4 (&w)[TileCfg<D>::kIts]) {
   using C = TileCfg<D>;
+  base += (lane % C::kCh) * 16;
+  place += lane / C::kCh;
 #pragma unroll
-  for (int it = 0; it < C::kIts; ++it) {
-    const int64_t o = __shfl_sync(0xffffffffu, off, (part * C::kIts + it) * C::kRowsIt + lane / C::kCh);
-    cp_async16(raw + (it * 32 + lane) * 16, base + o + (lane % C::kCh) * 16);
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int D>
-__device__ __forceinline__ void take_rows(const uint8_t* raw, int lane, uint4 (&w)[TileCfg<D>::kIts]) {
-  using C = TileCfg<D>;
-#pragma unroll
-  for (int it = 0; it < C::kIts; ++it) w[it] = *reinterpret_cast<const uint4*>(raw + (it * 32 + lane) * 16);
+  for (int it = 0; it < C::kIts; ++it) w[it] = __ldg(reinterpret_cast<const uint4*>(base + place[it * C::kRowsIt]));
 }
 
 // ... and as fp16 in the operand tile: 64-column blocks of kT rows of 128
@@ -173,7 +166,7 @@ __device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[TileCfg
 // V pieces before they are stored: zero for rows whose block is out of range or that
 // lie past the partition (their weight is 0, and 0 * NaN would not be; K rows
 // need not, their logits are masked), and non-finite codes as zero (returns
-// true if there were any).  ok: the part's rows from bit 0 on.
+// true if there were any).
 template <int D, int FMT>
 __device__ __forceinline__ bool clean_v(uint4 (&w)[TileCfg<D>::kIts], uint32_t ok, int lane) {
   using C = TileCfg<D>;
@@ -199,7 +192,7 @@ template <int D, int FMT, bool DO_K, bool DO_V>
 __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt, uint8_t* smem, int b, int g, int u0,
                                              int u1, int n_tiles, const ChunkSpan& span, int w, int lane) {
   using C = TileCfg<D>;
-  constexpr int NS = C::kStages, PARTS = C::kParts, PART_ROWS = 32 / PARTS;
+  constexpr int NS = C::kStages;
   volatile uint32_t* const abort_flag = &mt.abort;
   const uint8_t* kbase = p.k_cache + g * p.ksh;
   const uint8_t* vbase = p.v_cache + g * p.vsh;
@@ -226,71 +219,58 @@ __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt,
     if (DO_V) voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
     ok_next = __ballot_sync(0xffffffffu, ok);
   };
-  uint8_t* rawk = smem + C::kOffRaw + w * (PART_ROWS * D);
-  uint8_t* rawv = rawk + C::kRawBytes / 2;
+  int64_t* place = mt.place[DO_K ? 0 : 1][w];
+  uint4 kr[DO_K ? C::kIts : 1], vr[DO_V ? C::kIts : 1];
+  auto fetch_k = [&]() {
+    __syncwarp();
+    place[lane] = koff;
+    __syncwarp();
+    if constexpr (DO_K) fetch_rows<D>(kbase, place, lane, kr);
+  };
+  auto fetch_v = [&]() {
+    __syncwarp();
+    place[lane] = voff;
+    __syncwarp();
+    if constexpr (DO_V) fetch_rows<D>(vbase, place, lane, vr);
+  };
   ask(0);
   find();
-  if (DO_K) stage_rows<D>(kbase, koff, 0, lane, rawk);
-  if (DO_V) stage_rows<D>(vbase, voff, 0, lane, rawv);
+  if (DO_K) fetch_k();
+  if (DO_V) fetch_v();
   uint32_t ok_now = ok_next;
   if (n_tiles > 1) ask(1);
   bool ok = true, bad = false;
-  for (int j = 0; j < n_tiles && ok; ++j) {
+  for (int j = 0; j < n_tiles; ++j) {
     const int st = j % NS;
     const uint32_t empty_parity = ((j / NS) - 1) & 1;
-    // A stage copy follows each part taken (the very last one again), so that the
-    // number of copies in flight is always the same.
-#pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-      const int next = (part + 1) % PARTS;
-      if (next == 0) {
-        if (j + 1 < n_tiles) find();
-        if (j + 2 < n_tiles) ask(j + 2);
+    if (j + 1 < n_tiles) find();
+    if (j + 2 < n_tiles) ask(j + 2);
+    // (the last tile is requested again: the requests stay unconditional)
+    if constexpr (DO_K) {
+      if (j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) {
+        ok = false;
+        break;
       }
-      uint4 x[C::kIts];
-      if constexpr (DO_K) {
-        if (DO_V)
-          asm volatile("cp.async.wait_group 1;" ::: "memory");  // V's is still under way
-        else
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        take_rows<D>(rawk, lane, x);
-        if (part == 0 && j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) {
-          ok = false;
-          break;
-        }
-        store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, x, 32 * w + part * PART_ROWS, lane);
-        if (next == 0) {
-          // K(j+8) is decoded after QK(j+4) at the earliest, and that after softmax j+3
-          if (lane == 0) mt.valid[j & 7][w] = ok_now;
-          fence_proxy_async_smem();
-          mbar_arrive(&mt.k_full[st]);
-        }
-        stage_rows<D>(kbase, koff, next, lane, rawk);
+      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w, lane);
+      // K(j+8) is decoded after QK(j+4) at the earliest, and that after softmax j+3
+      if (lane == 0) mt.valid[j & 7][w] = ok_now;
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.k_full[st]);
+      fetch_k();
+    }
+    if constexpr (DO_V) {
+      bad |= clean_v<D, FMT>(vr, ok_now, lane);
+      if (j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) {
+        ok = false;
+        break;
       }
-      if constexpr (DO_V) {
-        if (DO_K)
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        take_rows<D>(rawv, lane, x);
-        // the part's rows from bit 0 on, no row missing above them
-        constexpr uint32_t above = PARTS == 1 ? 0u : 0xFFFF0000u;
-        bad |= clean_v<D, FMT>(x, (ok_now >> (part * PART_ROWS)) | above, lane);
-        if (part == 0 && j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) {
-          ok = false;
-          break;
-        }
-        store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, x, 32 * w + part * PART_ROWS, lane);
-        if (next == 0) {
-          fence_proxy_async_smem();
-          mbar_arrive(&mt.v_full[st]);
-        }
-        stage_rows<D>(vbase, voff, next, lane, rawv);
-      }
+      store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, vr, 32 * w, lane);
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.v_full[st]);
+      fetch_v();
     }
     ok_now = ok_next;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (bad) mt.vbad = 1u;
   return ok;
 }
@@ -323,48 +303,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Largest visible element of this thread's 128 columns of S (a NaN is passed
-// over: it makes the row's sum NaN).  FULL: every column is visible.
-template <bool FULL>
-__device__ __forceinline__ float row_max(uint32_t tS, const uint32_t (&vis)[4]) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// P = 2^(c S + sh) as fp16 for 64 of a row's logits; adds to the row's sums.
+__device__ __forceinline__ void exp_half(const uint32_t* x, uint64_t c2, uint64_t sh2, uint64_t (&sum)[2],
+                                         uint32_t (&y)[32]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t x[32];
-    tmem_ld32(tS + 32 * i, x);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float v = __uint_as_float(x[k]);
-      m[(k / 2) & 3] = fmaxf(m[(k / 2) & 3], FULL || ((vis[i] >> k) & 1u) ? v : -INFINITY);
-    }
+  for (int k = 0; k < 64; k += 2) {
+    const float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
+    const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+    sum[(k / 2) & 1] = add2(sum[(k / 2) & 1], pair(p0, p1));
+    y[k / 2] = pack_half2(p0, p1);
   }
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-
-// P = 2^(c S + sh) as fp16 over S (masked columns: 0); returns the sum.
-template <bool FULL>
-__device__ __forceinline__ float exp_tile(uint32_t tS, const uint32_t (&vis)[4], float c, float sh) {
-  const uint64_t c2 = pair(c, c), sh2 = pair(sh, sh);
-  uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t x[32], y[16];
-    tmem_ld32(tS + 32 * i, x);
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
-      if (!FULL) {
-        e.x = ((vis[i] >> k) & 1u) ? e.x : -INFINITY;
-        e.y = ((vis[i] >> (k + 1)) & 1u) ? e.y : -INFINITY;
-      }
-      const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
-      sum[(k / 2) & 1] = add2(sum[(k / 2) & 1], pair(p0, p1));
-      y[k / 2] = pack_half2(p0, p1);
-    }
-    tmem_st16(tS + 16 * i, y);  // over S columns that were read
-  }
-  const float2 t = unpair(add2(sum[0], sum[1]));
-  return t.x + t.y;
 }
 
 template <int D, int FMT, int DT>
@@ -408,17 +356,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   const int nq = NQ == 2 && RC > kM ? 2 : 1;  // row tiles in use
 
   if (tid == 0) {
-    mbar_init(&mt.q_full, nq * kM);
-    mbar_init(&mt.drain, 1);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&mt.k_full[i], 128);
-      mbar_init(&mt.k_empty[i], 1);
+      mbar_init(&mt.k_empty[i], nq);
       mbar_init(&mt.v_full[i], 128);
-      mbar_init(&mt.v_empty[i], 1);
+      mbar_init(&mt.v_empty[i], nq);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&mt.q_full[i], kM);
+      mbar_init(&mt.drain[i], 1);
       mbar_init(&mt.s_full[i], 1);
-      mbar_init(&mt.p_ready[i], kM);
+      mbar_init(&mt.p_ready[i][0], 4);  // one lane of each of the row tile's warps
+      mbar_init(&mt.p_ready[i][1], 4);
       mbar_init(&mt.o_all[i], 1);
     }
     mbar_init(&mt.o_done, 1);
@@ -426,14 +375,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
     mt.vbad = 0u;
     mbar_init_fence();
   }
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     tmem_alloc(&mt.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = mt.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, mt.tmem, 0);
   volatile uint32_t* const abort_flag = &mt.abort;
   const float ks = p.k_scale_dev ? *p.k_scale_dev : p.k_scale;
   const double cd = (double)p.softmax_scale * (double)ks * 1.4426950408889634074;
@@ -450,6 +399,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       uint8_t* sQ = smem + C::kOffQ + q * (kM * D * 2);
       const uint32_t flip = cd < 0 ? 0x80008000u : 0u;
       const int e = lane * V;  // first element of the lane
+      float back = 1.f;        // inverse scale of this thread's row
 #pragma unroll 1
       for (int k0 = 0; k0 < 32; k0 += kRowsAtOnce) {
         uint32_t w[kRowsAtOnce][V / 2];
@@ -479,7 +429,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
             for (int i = 0; i < V / 2; ++i)
               w[k][i] = pack_half2(__uint_as_float(w[k][i] << 16) * rs.to_f16,
                                    __uint_as_float(w[k][i] & 0xFFFF0000u) * rs.to_f16);
-            if (lane == 0) mt.back[q * kM + r] = rs.back;
+            if (lane == k0 + k) back = rs.back;
           }
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) w[k][i] ^= flip;
@@ -494,39 +444,106 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       }
       __syncwarp();
       fence_proxy_async_smem();
-      mbar_arrive(&mt.q_full);
+      mbar_arrive(&mt.q_full[q]);
+
+      // ====================================================== UMMA issue
+      // The row tile's first warp walks the schedule and one elected lane issues
+      // (operands of a converged warp stay in uniform registers).  S and P of
+      // a row tile share their columns: QK(j+1) follows PV(j) in issue order, in
+      // which the tensor core runs one thread's UMMAs.
+      const bool issuer = (warp & 3) == 0;
+      constexpr int NS = C::kStages;
+      static_assert(kM == kT, "Q and K tiles share their block stride");
+      const uint32_t idesc_qk = idesc_f16_f32(kM, kT, false, false);
+      const uint32_t idesc_pv = idesc_f16_f32(kM, D, false, true);
+      const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ + q * (kM * D * 2)), 16, 1024, kSw128);
+      const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
+      const uint64_t vdesc = smem_desc(smem_u32(smem + C::kOffV), kT * 128, 1024, kSw128);
+      auto buf_of = [&](int j) { return NQ == 2 ? q : j & 1; };
+      auto issue_qk = [&](int j) {
+        ok = ok && warp_wait(&mt.k_full[j % NS], (j / NS) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t kd = kdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);
+            mma_ss(tmem + buf_of(j) * 128, qdesc + step, kd + step, idesc_qk, kk > 0);
+          }
+          mma_commit(&mt.s_full[buf_of(j)]);
+          mma_commit(&mt.k_empty[j % NS]);
+        }
+      };
+      // PV of half h, once every warp has written its rows of P
+      auto issue_pv = [&](int j, int h) {
+        if (h == 0) ok = ok && warp_wait(&mt.v_full[j % NS], (j / NS) & 1, abort_flag);
+        ok = ok && warp_wait(&mt.p_ready[q][h], j & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t vd = vdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kT / 32; ++k) {
+            const int kk = h * (kT / 32) + k;
+            mma_ts(tmem + C::kColO + q * D, tmem + buf_of(j) * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                   idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (h == 1) {
+            mma_commit(&mt.v_empty[j % NS]);
+            if (j + 1 == n_tiles)
+              mma_commit(&mt.o_all[q]);
+            else if (NQ == 1)
+              mma_commit(&mt.o_done);
+          }
+        }
+      };
+      if (issuer) {
+        ok = warp_wait(&mt.q_full[q], 0, abort_flag);
+        issue_qk(0);
+      }
 
       // ====================================================== softmax
       const int rr = q * kM + 32 * (warp & 3) + lane;  // this thread's row of the CTA
       const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-      const float c = (float)(fabs(cd) * (DT == FP8KV_DTYPE_BF16 ? (double)mt.back[rr] : 1.0));
+      // (not 0, so that c * -inf stays -inf for masked logits)
+      const float c = fmaxf((float)(fabs(cd) * (double)back), 1e-30f);
       ChunkRow row = {INT_MAX, INT_MIN};  // rows past RC: everything, dropped at the end
       if (rr < RC) row = chunk_row(p, req, span, (work.row0 + rr) / p.G);
       const int hi_min = __reduce_min_sync(0xffffffffu, row.hi), lo_max = __reduce_max_sync(0xffffffffu, row.lo);
       float m = kNoMax, l = 0.f;
       const uint32_t tO = tmem + C::kColO + q * D + lane_off;
       for (int j = 0; j < n_tiles; ++j) {
-        const int buf = NQ == 2 ? q : j & 1;
-        const uint32_t parity = (NQ == 2 ? j : j >> 1) & 1;
-        ok = warp_wait(&mt.s_full[buf], parity, abort_flag);
+        const int buf = buf_of(j);
+        ok = ok && warp_wait(&mt.s_full[buf], (NQ == 2 ? j : j >> 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + buf * 128 + lane_off;
         const int v0 = u0 + j * kT;
-        uint32_t vis[4];
-        bool full = v0 + kT <= hi_min && (v0 >= lo_max || v0 + kT <= span.sk);
+        const uint4 there = *reinterpret_cast<const uint4*>(mt.valid[j & 7]);
+        uint32_t x[128];
+        tmem_ld128(tS, x);
+        if ((there.x & there.y & there.z & there.w) != 0xFFFFFFFFu || v0 + kT > hi_min ||
+            !(v0 >= lo_max || v0 + kT <= span.sk)) {
+          // logits that the row does not see become -inf (a NaN among them too)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vis[i] = mt.valid[j & 7][i];
-          full &= vis[i] == 0xFFFFFFFFu;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t vis =
+                (i == 0 ? there.x : i == 1 ? there.y : i == 2 ? there.z : there.w) & sees32(row, span.sk, v0 + 32 * i);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[32 * i + k] = ((vis >> k) & 1u) ? x[32 * i + k] : 0xFF800000u;
+          }
         }
-        if (!full)
+        // row maximum (a NaN is passed over: it makes the sum NaN)
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vis[i] &= sees32(row, span.sk, v0 + 32 * i);
-        float mx = full ? row_max<true>(tS, vis) : row_max<false>(tS, vis);
-        if (mx > -INFINITY) mx *= c;
-        if (__any_sync(0xffffffffu, mx > -INFINITY && !(mx <= m + kChunkTau))) {
-          const float n = mx > m + kChunkTau || m == kNoMax ? fmaxf(m, ceilf(mx)) : m;
+        for (int k = 0; k < 128; k += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[k + 2 * i])), __uint_as_float(x[k + 2 * i + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (__any_sync(0xffffffffu, top > m + kChunkTau || (m == kNoMax && top > -INFINITY))) {
+          const float n = top > m + kChunkTau || m == kNoMax ? fmaxf(m, ceilf(top)) : m;
           const float a = n == m || m == kNoMax ? 1.f : exp2_int(m - n);
           m = n;
           l *= a;
@@ -534,25 +551,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
             // O holds the PVs of the tiles before this one.  Two row tiles: S(j)
             // was issued behind PV(j-1), so s_full covers it; one: s_full
             // covers PV(j-2), and this waits for PV(j-1).
-            bool go = true;
-            if (NQ == 1) go = warp_wait(&mt.o_done, (j - 1) & 1, abort_flag);
+            if (NQ == 1) ok = warp_wait(&mt.o_done, (j - 1) & 1, abort_flag);
+            if (!ok) break;
             tc_fence_after();
-            if (go) {
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16(tO + c0, o);
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c0, o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                tmem_st16(tO + c0, o);
-              }
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tmem_st16(tO + c0, o);
             }
           }
         }
         const float sh = kChunkPShift - (m == kNoMax ? 0.f : m);
-        l += full ? exp_tile<true>(tS, vis, c, sh) : exp_tile<false>(tS, vis, c, sh);
-        tc_fence_before();
-        mbar_arrive(&mt.p_ready[buf]);
+        const uint64_t c2 = pair(c, c), sh2 = pair(sh, sh);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t y[32];
+          exp_half(x + 64 * h, c2, sh2, sum, y);
+          tmem_st32(tS + 32 * h, y);  // over S, all of which is in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&mt.p_ready[q][h]);
+          if (issuer) {
+            if (h == 1 && NQ == 1 && j + 1 < n_tiles) issue_qk(j + 1);  // its buffer held P(j-1)
+            issue_pv(j, h);
+            if (h == 1 && NQ == 2 && j + 1 < n_tiles) issue_qk(j + 1);
+          }
+        }
+        const float2 t = unpair(add2(sum[0], sum[1]));
+        l += t.x + t.y;
+      }
+      if (issuer) {
+        // every UMMA issued must be done before TMEM is freed
+        if (elect_one()) mma_commit(&mt.drain[q]);
+        __syncwarp();
+        mbar_wait_plain(&mt.drain[q], 0, kPolls);
+        __syncwarp();
       }
       // ====================================================== epilogue
       if (ok) ok = warp_wait(&mt.o_all[q], 0, abort_flag);
@@ -591,7 +628,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
         }
       }
     }
-  } else if (warp < kMmaWarp) {
+  } else {
     // ======================================================== decoders
     const int w = warp & 3;
     if constexpr (NQ == 2)
@@ -600,88 +637,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       ok = decode_tiles<D, FMT, true, false>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
     else
       ok = decode_tiles<D, FMT, false, true>(p, mt, smem, b, g, u0, u1, n_tiles, span, w, lane);
-  } else {
-    // ======================================================== UMMA issue
-    // The whole warp walks the schedule and one elected lane issues: operands
-    // then stay in uniform registers (issued by a lone diverged lane, each UMMA cost
-    // its thread ~80 cycles, more than the 65 that the tensor core needs).
-    constexpr int NS = C::kStages;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t idesc_qk = idesc_f16_f32(kM, kT, false, false);
-    const uint32_t idesc_pv = idesc_f16_f32(kM, D, false, true);
-    const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kSw128);
-    const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
-    const uint64_t vdesc = smem_desc(smem_u32(smem + C::kOffV), kT * 128, 1024, kSw128);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && warp_wait(bar, parity, abort_flag);
-      tc_fence_after();
-      return ok;
-    };
-    static_assert(kM == kT, "Q and K tiles share their block stride");
-    // S(buf) = Q_q . K_j^T, then the barriers that it completes
-    auto qk = [&](int q, int buf, int j, bool k_last) {
-      const uint64_t qd = qdesc + (uint64_t)((q * (kM * D * 2)) >> 4);
-      const uint64_t kd = kdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);
-          mma_ss(tm + buf * 128, qd + step, kd + step, idesc_qk, kk > 0);
-        }
-        mma_commit(&mt.s_full[buf]);
-        if (k_last) mma_commit(&mt.k_empty[j % NS]);
-      }
-    };
-    // O_q += P(buf) . V_j
-    auto pv = [&](int q, int buf, int j, bool v_last, uint64_t* done) {
-      const uint64_t vd = vdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)
-          mma_ts(tm + C::kColO + q * D, tm + buf * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
-                 (j > 0 || kk > 0) ? 1u : 0u);
-        if (v_last) mma_commit(&mt.v_empty[j % NS]);
-        if (done) mma_commit(done);
-      }
-    };
-    if (wait(&mt.q_full, 0) && wait(&mt.k_full[0], 0)) {
-      if (NQ == 2) {
-        // S and P of a row tile share their columns: QK(j+1) follows PV(j) in
-        // issue order, in which the tensor core runs one CTA's UMMAs
-        for (int q = 0; q < nq; ++q) qk(q, q, 0, q == nq - 1);
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          if (!wait(&mt.v_full[j % NS], (j / NS) & 1)) break;
-          for (int q = 0; q < nq; ++q) {
-            if (!wait(&mt.p_ready[q], j & 1)) break;
-            pv(q, q, j, q == nq - 1, j + 1 == n_tiles ? &mt.o_all[q] : nullptr);
-            if (j + 1 == n_tiles) continue;
-            if (q == 0 && !wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
-            qk(q, q, j + 1, q == nq - 1);
-          }
-        }
-      } else {
-        qk(0, 0, 0, true);
-        for (int j = 0; j < n_tiles; ++j) {
-          if (j + 1 < n_tiles) {
-            // its buffer held P(j-1), whose PV was issued before
-            if (!wait(&mt.k_full[(j + 1) % NS], ((j + 1) / NS) & 1)) break;
-            qk(0, (j + 1) & 1, j + 1, true);
-          }
-          if (!wait(&mt.v_full[j % NS], (j / NS) & 1) || !wait(&mt.p_ready[j & 1], (j >> 1) & 1)) break;
-          pv(0, j & 1, j, true, j + 1 == n_tiles ? &mt.o_all[0] : &mt.o_done);
-        }
-      }
-    }
-    // every UMMA issued must be done before TMEM is freed
-    if (elect_one()) mma_commit(&mt.drain);
-    __syncwarp();
-    mbar_wait_plain(&mt.drain, 0, kPolls);
   }
   if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
