@@ -9,7 +9,8 @@
 
 namespace fp8kv {
 
-constexpr int kChunkStreamRows = 16;      // query vectors per (request, KV head) of the stream kernel
+constexpr int kChunkStreamRows = 16;      // query vectors per CTA of the stream kernel
+constexpr int kChunkClusterMax = 8;       // partitions that the stream kernel joins in one launch (portable cluster size)
 constexpr int kChunkStreamBlock = 16;     // positions per warp step of the stream kernel
 constexpr int kChunkTileTokens = 128;     // positions per tile of the tile kernel
 // Longest partition of the tile kernel: the tensor core's FP32 accumulation
@@ -44,6 +45,11 @@ struct ChunkParams {
   float* partial;          // [S][total_q][Hq][D] (S > 1)
   float2* ml;              // [S][total_q][Hq]
 };
+
+// Whether the partitions form a cluster that joins them itself.
+inline bool chunk_clustered(const fp8kv_chunk_plan_t* plan) {
+  return plan->kernel == FP8KV_CHUNK_STREAM && plan->num_splits > 1 && plan->num_splits <= kChunkClusterMax;
+}
 
 cudaError_t launch_chunk_stream(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_chunk_tile(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);

@@ -46,7 +46,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   if (d->total_q > (1 << 30) || d->max_q > (1 << 24) || d->max_kv_len > (1 << 30) || d->num_kv_heads > 65535 ||
       d->max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32))
     return FP8KV_EUNSUPPORTED;
-  if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > kChunkStreamRows) return FP8KV_EUNSUPPORTED;
+  if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > 65535 * (int64_t)kChunkStreamRows) return FP8KV_EUNSUPPORTED;
 
   int sms = d->num_sms;
   if (sms == 0) {
@@ -85,8 +85,8 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   // positions of what one CTA's rows see together.
   int64_t units, slots, unit, span_q;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
-    units = (int64_t)P.batch * P.num_kv_heads;
-    slots = (int64_t)sms * (P.head_dim == 64 ? 4 : P.head_dim == 128 ? 3 : 2);
+    units = (int64_t)P.batch * P.num_kv_heads * ceil_div(rows, kChunkStreamRows);
+    slots = (int64_t)sms * (P.head_dim == 64 ? 5 : P.head_dim == 128 ? 3 : 2);
     unit = 4 * kChunkStreamBlock;
     span_q = P.max_q;
   } else {
@@ -102,12 +102,13 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   int64_t S = units ? slots / units : 1;
   S = std::min(S, ceil_div(seen, unit));
   if (P.kernel == FP8KV_CHUNK_TILE) S = std::max(S, ceil_div(seen, kChunkMaxPart));
+  if (P.kernel == FP8KV_CHUNK_STREAM && S > kChunkClusterMax && seen <= kChunkClusterMax * 8 * unit) S = kChunkClusterMax;
   S = std::max<int64_t>(1, S);
   if (d->num_splits) S = d->num_splits;
   if (P.batch > 0 && P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;
   P.num_splits = (int32_t)S;
 
-  const int64_t nvec = S > 1 ? S * P.total_q * P.num_q_heads : 0;
+  const int64_t nvec = S > 1 && !chunk_clustered(&P) ? S * P.total_q * P.num_q_heads : 0;
   P.partial_offset = 256;
   P.ml_offset = align_up(P.partial_offset + nvec * P.head_dim * 4, 256);
   P.workspace_bytes = align_up(P.ml_offset + nvec * 8, 256);
@@ -194,7 +195,7 @@ extern "C" int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chun
   if (rc != FP8KV_OK || plan->batch == 0 || plan->total_q == 0) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = plan->kernel == FP8KV_CHUNK_STREAM ? launch_chunk_stream(plan, p, st) : launch_chunk_tile(plan, p, st);
-  if (e == cudaSuccess && p.S > 1) e = launch_chunk_join(plan, p, st);
+  if (e == cudaSuccess && p.S > 1 && !chunk_clustered(plan)) e = launch_chunk_join(plan, p, st);
   return done(e);
 }
 

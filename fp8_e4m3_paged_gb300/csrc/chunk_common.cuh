@@ -58,6 +58,11 @@ __device__ __forceinline__ ChunkSpan chunk_span(const ChunkParams& p, const Chun
   return s;
 }
 
+// 2^(m - M), the weight of a partition that saw something in the joint sum:
+// never 0, so that an infinite numerator of a far smaller partition stays
+// infinite (0 * inf would not).
+__device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : exp2f(fmaxf(m - M, -120.f)); }
+
 // What one row sees on that axis: v < hi and (v >= lo or v < sk).
 struct ChunkRow {
   int hi, lo;

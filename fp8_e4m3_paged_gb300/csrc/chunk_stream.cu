@@ -1,11 +1,11 @@
 // Chunk attention for few query vectors (at most 16 per CTA: the query heads
 // of one KV head times a few new tokens): bound by streaming the cache.
 //
-// One CTA of four warps per (request, KV head, partition); each warp walks
-// blocks of 16 virtual tokens (chunk_span) on its own, with no barrier and no
-// shared memory in the loop, and the four are joined at the end.  The FP8
-// bytes go from global memory straight into the registers of the MMA that
-// uses them:
+// One CTA of four warps per (request, KV head, 16 query vectors, partition);
+// each warp walks blocks of 16 virtual tokens (chunk_span) on its own, and the four are joined at
+// the end.  A block's FP8 bytes are requested two blocks ahead by cp.async
+// into places of shared memory that only the requesting lane reads, so the
+// loop has no barrier; each lane asks for the bytes that its MMA fragments hold:
 //   S[16 x 8 tokens] = Q . K^T, m16n8k16: a lane of the B operand needs four
 //     d of one token, so lane (n = lane/4, c = lane%4) loads the 16-byte pieces c, c + 4, ... of token n's row; each 32-bit word
 //     decodes to one MMA's B fragment, and the d that a word holds is simply
@@ -19,6 +19,10 @@
 // few percent of the tensor peak, and TMEM or shared-memory operands would
 // only add copies and barriers to a kernel whose time is the bytes' arrival.
 //
+// Partitions of one request and KV head form a thread-block cluster when there
+// are at most 8: their sums are joined through distributed shared memory in
+// the same launch.  More go through the workspace and chunk_join.
+//
 // With at most 8 query vectors the upper 8 rows of P's fragment are free:
 // they carry P_lo = 2^11 (p - fp16(p)), which makes the probabilities good
 // to 22 bits at no cost.
@@ -29,6 +33,7 @@
 
 #include "chunk_common.cuh"
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace fp8kv {
 namespace {
@@ -39,19 +44,26 @@ constexpr int kBlk = kChunkStreamBlock;
 constexpr int kR = kChunkStreamRows;
 constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;
 
-template <int D>
+template <int D, bool WIDE>
 struct StreamCfg {
+  static constexpr int kRows = WIDE ? 16 : 8;
   static constexpr int kKP = D / 64;                 // 16-byte pieces of a K row per lane
   static constexpr int kVP = D >= 128 ? D / 128 : 1; // pieces of a V row per lane
   static constexpr int kVWords = D >= 128 ? 4 : 2;   // 32-bit words per piece
   static constexpr int kNT = D / 8;                  // n-tiles of O
   static constexpr int kQStride = D + 8;             // fp16 elements (padding: fragment loads without conflicts)
   static constexpr bool kQRegs = D <= 128;           // Q's fragments stay in registers
-  static constexpr int kCtas = D == 64 ? 4 : D == 128 ? 3 : 2;  // resident per SM
+  static constexpr int kCtas = D == 256 ? 2 : D == 128 ? 3 : 5;  // resident per SM
+  static constexpr int kStages = D == 64 ? 4 : 3;    // blocks of a warp in flight or in use
+  static constexpr int kKBytes = 2 * kKP * 512;      // a block's K pieces: [piece][lane] of 16 bytes
+  static constexpr int kVBytes = 4 * kVP * (D >= 128 ? 512 : 256);
+  static constexpr int kRing = kStages * (kKBytes + kVBytes);  // per warp; then its numerators [row][D]
   static constexpr int kQBytes = kR * kQStride * 2;
-  static constexpr int kOBytes(int rows) { return kWarps * rows * D * 4; }
-  // Q, then the warps' numerators (their place also holds the non-finite marks)
-  static constexpr int smem(bool wide) { return kQBytes + kOBytes(wide ? 16 : 8) + 1024; }
+  static constexpr int kOffQ = kWarps * kRing;
+  static constexpr int kOffRed = kOffQ + kQBytes;    // per warp and row: maximum, sum; inverse row scales; joined
+  static constexpr int kSmem = kOffRed + (2 * kWarps + 3) * 16 * 4;
+  static_assert(kRing >= kRows * D * 4, "a warp's numerators fit its ring");
+  static_assert(kWarps * kRing >= kRows * D * 5, "joined numerators and the non-finite marks");
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -61,64 +73,83 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 16 bytes that no other CTA soon reads: not kept in L1.
-__device__ __forceinline__ uint4 ld_stream16(const uint8_t* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+__device__ __forceinline__ void cp_async8(void* dst_smem, const void* src_gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst_smem)), "l"(src_gmem) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Thread-block cluster: barrier over all its CTAs, and loads from a peer's
+// shared memory (the address that `p` has in CTA `rank`).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ uint4 ld_stream8(const uint8_t* p) {
-  uint4 r = make_uint4(0, 0, 0, 0);
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a));
+  return x;
 }
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a));
+  return x;
+}
+
 __device__ __forceinline__ uint32_t word(const uint4& w, int i) {
   return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
 }
 
 template <int D, int FMT, int DT, bool WIDE>
-__global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(const __grid_constant__ ChunkParams p) {
-  using C = StreamCfg<D>;
-  constexpr int ROWS = WIDE ? 16 : 8;
+__global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
+    chunk_stream(const __grid_constant__ ChunkParams p, const int clustered) {
+  using C = StreamCfg<D, WIDE>;
+  constexpr int ROWS = C::kRows, ST = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint16_t* sQ = reinterpret_cast<uint16_t*>(smem);
-  float* sO = reinterpret_cast<float*>(smem + C::kQBytes);                  // [warp][ROWS][D]
-  float* sM = reinterpret_cast<float*>(smem + C::kQBytes + C::kOBytes(ROWS));  // [warp][16]
+  uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
+  float* sM = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp][16]
   float* sL = sM + kWarps * 16;
-  float* sBack = sL + kWarps * 16;                                          // [16] inverse row scales
+  float* sBack = sL + kWarps * 16;                          // [16] inverse row scales
+  float* sMj = sBack + 16;                                  // [16] of the CTA
+  float* sLj = sMj + 16;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
   const int b = blockIdx.x / p.S, s = blockIdx.x - b * p.S;
   const int g = blockIdx.y;
+  const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-  const int RC = min(kR, req.n * p.G);  // packed rows: token * G + head of the group
-  if (RC <= 0) return;
+  const int RC = min(kR, req.n * p.G - row_first);
+  if (RC <= 0) return;  // every CTA of the cluster
   const int64_t plane = (int64_t)p.total_q * p.Hq;
-  auto vec_of = [&](int r) {
-    return (int64_t)(req.row0 + r / p.G) * p.Hq + g * p.G + r % p.G;
-  };
+  auto token_of = [&](int r) { return (row_first + r) / p.G; };
+  auto head_of = [&](int r) { return g * p.G + (row_first + r) % p.G; };
+  auto vec_of = [&](int r) { return (int64_t)(req.row0 + token_of(r)) * p.Hq + head_of(r); };
 
-  const ChunkSpan span = chunk_span(p, req, 0, (RC - 1) / p.G);
+  const ChunkSpan span = chunk_span(p, req, token_of(0), token_of(RC - 1));
   int per = (span.U + p.S - 1) / p.S;
   per = (per + kBlk * kWarps - 1) / (kBlk * kWarps) * (kBlk * kWarps);
-  const int u0 = min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
-  if (u0 >= u1 && p.S > 1) {
+  const int u0 = (int)min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
+  if (u0 >= u1 && p.S > 1 && !clustered) {
     if (tid < RC) p.ml[s * plane + vec_of(tid)] = make_float2(kNoMax, 0.f);
     return;
   }
 
   // Places of a block's 16 tokens, one per lane (both halves of the warp hold
-  // them).  The block id is requested a block before it is needed; the loads
+  // them).  The block id is requested a block before it is needed; the copies
   // are unconditional (tokens without a place read the pool's first row and
-  // are masked, V also zeroed): a load under a condition is waited for on the spot.
-  const uint8_t* kbase = p.k_cache + g * p.ksh;
-  const uint8_t* vbase = p.v_cache + g * p.vsh;
-  int64_t koff, voff;
-  uint32_t vnext;  // which of them hold data
+  // are masked, V also zeroed).
+  const uint8_t* kbase = p.k_cache + g * p.ksh + c * 16;
+  const uint8_t* vbase = p.v_cache + g * p.vsh + rq * (D >= 128 ? 16 : 8);
+  uint8_t* ring = smem + warp * C::kRing;
   int blk = -1, slot = 0;
   bool in = false;
   auto ask = [&](int t) {
@@ -131,36 +162,47 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
       blk = __ldg(p.block_table + (int64_t)b * p.bt_stride + page);
     }
   };
-  auto find = [&]() {
+  // Copies of the block asked for into stage `st`; returns the tokens that are there.
+  auto request = [&](int st) {
     const bool ok = blk >= 0 && blk < p.num_kv_blocks;
     if (in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    koff = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
-    voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
-    vnext = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
-  };
-  uint4 kr[2][C::kKP], vr[4][C::kVP];
-  auto load_k = [&]() {
+    const int64_t koff = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
+    const int64_t voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
+    uint8_t* dst = ring + st * (C::kKBytes + C::kVBytes);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint8_t* src = kbase + __shfl_sync(0xffffffffu, koff, rq + 8 * h) + c * 16;
+      const uint8_t* src = kbase + __shfl_sync(0xffffffffu, koff, rq + 8 * h);
 #pragma unroll
-      for (int i = 0; i < C::kKP; ++i) kr[h][i] = ld_stream16(src + 64 * i);
+      for (int i = 0; i < C::kKP; ++i) tc::cp_async16(dst + ((h * C::kKP + i) * 32 + lane) * 16, src + 64 * i);
     }
-  };
-  auto load_v = [&]() {
+    dst += C::kKBytes;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint8_t* src = vbase + __shfl_sync(0xffffffffu, voff, 2 * c + (j & 1) + 8 * (j >> 1));
 #pragma unroll
-      for (int i = 0; i < C::kVP; ++i)
-        vr[j][i] = D >= 128 ? ld_stream16(src + (rq + 8 * i) * 16) : ld_stream8(src + rq * 8);
+      for (int i = 0; i < C::kVP; ++i) {
+        if (D >= 128)
+          tc::cp_async16(dst + ((j * C::kVP + i) * 32 + lane) * 16, src + 128 * i);
+        else
+          cp_async8(dst + (j * 32 + lane) * 8, src);
+      }
     }
+    return __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
   };
+  constexpr int kStep = kBlk * kWarps;  // a warp's blocks are this far apart
   const int t_first = u0 + kBlk * warp;
-  ask(t_first);
-  find();
-  load_k();
-  load_v();
+  uint32_t there[ST];  // tokens of the blocks in flight, the oldest first
+  auto fill = [&]() {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      ask(t_first + i * kStep);
+      there[i] = 0u;
+      if (t_first + i * kStep < u1) there[i] = request(i);
+      cp_commit();
+    }
+    ask(t_first + (ST - 1) * kStep);
+  };
+  fill();
 
   // Q -> shared memory as fp16 (bf16 rows scaled by a power of two); rows past
   // RC are zero.  One warp per row.
@@ -172,7 +214,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
     constexpr int V = D / 32;  // elements per lane
     uint32_t w[V / 2] = {};
     if (r < RC) {
-      const uint16_t* src = p.q + (int64_t)(req.row0 + r / p.G) * p.q_st + (int64_t)(g * p.G + r % p.G) * p.q_sh;
+      const uint16_t* src = p.q + (int64_t)(req.row0 + token_of(r)) * p.q_st + (int64_t)head_of(r) * p.q_sh;
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + lane * V + 2 * j);
     }
@@ -205,8 +247,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
 
   // What this lane's two rows see; rows past RC see everything (their values are dropped).
   ChunkRow row0 = {INT_MAX, INT_MIN}, row1 = {INT_MAX, INT_MIN};
-  if (rq < RC) row0 = chunk_row(p, req, span, rq / p.G);
-  if (rq + 8 < RC) row1 = chunk_row(p, req, span, (rq + 8) / p.G);
+  if (rq < RC) row0 = chunk_row(p, req, span, token_of(rq));
+  if (rq + 8 < RC) row1 = chunk_row(p, req, span, token_of(rq + 8));
   const int hi_min = __reduce_min_sync(0xffffffffu, min(row0.hi, row1.hi));
   const int lo_max = __reduce_max_sync(0xffffffffu, max(row0.lo, row1.lo));
 
@@ -240,12 +282,28 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
     for (int n = 0; n < C::kNT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     m0 = m1 = kNoMax;
     l0 = l1 = 0.f;
-    uint32_t valid = vnext;
-    ask(t_first + kBlk * kWarps);
-    for (int t = t_first; t < u1; t += kBlk * kWarps) {
+    int st = 0;
+    for (int t = t_first; t < u1; t += kStep) {
+      // the block ST - 1 ahead goes where the block before this one was
+      there[ST - 1] = 0u;
+      if (t + (ST - 1) * kStep < u1) {
+        there[ST - 1] = request(st == 0 ? ST - 1 : st - 1);
+        ask(t + ST * kStep);
+      }
+      cp_commit();
+      cp_wait<ST - 1>();
+      const uint8_t* kst = ring + st * (C::kKBytes + C::kVBytes) + lane * 16;
+      const uint8_t* vst = ring + st * (C::kKBytes + C::kVBytes) + C::kKBytes + lane * (D >= 128 ? 16 : 8);
+      st = st + 1 == ST ? 0 : st + 1;
+      const uint32_t valid = there[0];
+#pragma unroll
+      for (int i = 0; i + 1 < ST; ++i) there[i] = there[i + 1];
       float sc[2][4];
-            find();  // of the next block
-      ask(t + 2 * kBlk * kWarps);
+      uint4 kr[2][C::kKP];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < C::kKP; ++i) kr[h][i] = *reinterpret_cast<const uint4*>(kst + (h * C::kKP + i) * 512);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
@@ -264,7 +322,18 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
             }
           }
       }
-      if (t + kBlk * kWarps < u1) load_k();  // of the next block
+      uint4 vr[4][C::kVP];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < C::kVP; ++i) {
+          if (D >= 128) {
+            vr[j][i] = *reinterpret_cast<const uint4*>(vst + (j * C::kVP + i) * 512);
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(vst + j * 256);
+            vr[j][i] = make_uint4(y.x, y.y, 0u, 0u);
+          }
+        }
       // base-2 logits; tokens that a row does not see by selection
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -356,9 +425,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
 #pragma unroll
           for (int e = 0; e < 4; ++e) mma16816(o[(i * C::kVWords + w) * 4 + e], pa, f[0][e], f[1][e]);
         }
-      valid = vnext;
-      if (t + kBlk * kWarps < u1) load_v();
     }
+    cp_wait<0>();
     if (zap) break;
     // Non-finite sums: maybe only from codes of tokens that some rows do not see (0 * NaN).
     float bad = 0.f;
@@ -368,10 +436,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
       for (int e = 0; e < 4; ++e) bad = fmaf(o[n][e], 0.f, bad);
     if (!__syncthreads_or(bad != 0.f)) break;
     zap = true;
-    ask(t_first);
-    find();
-    load_k();
-    load_v();
+    fill();
   }
 
   // ------------------------------------------------------------ join the warps
@@ -389,6 +454,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
   }
   // n-tile (i, x) column n of O is d = 128 i + PB n + x, PB the bytes of a V piece
   constexpr int PB = 4 * C::kVWords;
+  float* sO = reinterpret_cast<float*>(ring);  // this warp's numerators [ROWS][D]
 #pragma unroll
   for (int i = 0; i < C::kVP; ++i)
 #pragma unroll
@@ -403,66 +469,119 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
           h[k] = o[i * PB + x + k][2 + e];
           if (!WIDE) f[k] = fmaf(h[k], kLoDown, f[k]);
         }
-        *reinterpret_cast<float4*>(sO + (warp * ROWS + rq) * D + d) = make_float4(f[0], f[1], f[2], f[3]);
-        if (WIDE)
-          *reinterpret_cast<float4*>(sO + (warp * ROWS + rq + 8) * D + d) = make_float4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<float4*>(sO + rq * D + d) = make_float4(f[0], f[1], f[2], f[3]);
+        if (WIDE) *reinterpret_cast<float4*>(sO + (rq + 8) * D + d) = make_float4(h[0], h[1], h[2], h[3]);
       }
   __syncthreads();
   const float vs = p.v_scale_dev ? *p.v_scale_dev : p.v_scale;
-  constexpr int kIter = (ROWS * D / 4 + kThreadsS - 1) / kThreadsS;
+  constexpr int kItems = ROWS * D / 4;  // float4 of the joined numerators
+  constexpr int kIter = (kItems + kThreadsS - 1) / kThreadsS;
   float4 acc[kIter];
-  float Ls[kIter];
+  float Ms[kIter], Ls[kIter];
 #pragma unroll
   for (int k = 0; k < kIter; ++k) {
     const int x = tid + k * kThreadsS;
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;
     acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     Ls[k] = 0.f;
-    if (r >= RC) continue;
-    float M = kNoMax;
+    Ms[k] = kNoMax;
+    if (x >= kItems) continue;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w * 16 + r]);
+    for (int w = 0; w < kWarps; ++w) Ms[k] = fmaxf(Ms[k], sM[w * 16 + r]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float mw = sM[w * 16 + r], lw = sL[w * 16 + r];
-      if (mw == kNoMax && lw == 0.f) continue;
-      const float a = mw == M ? 1.f : exp2_int(mw - M);
+      const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem + w * C::kRing) + r * D + d);
+      if (mw == kNoMax && lw == 0.f) continue;  // saw nothing
+      const float a = mw == Ms[k] ? 1.f : exp2_int(mw - Ms[k]);
       Ls[k] = fmaf(a, lw, Ls[k]);
-      const float4 y = *reinterpret_cast<const float4*>(sO + (w * ROWS + r) * D + d);
       acc[k].x = fmaf(a, y.x, acc[k].x);
       acc[k].y = fmaf(a, y.y, acc[k].y);
       acc[k].z = fmaf(a, y.z, acc[k].z);
       acc[k].w = fmaf(a, y.w, acc[k].w);
     }
-    if (p.S > 1 && d == 0) p.ml[s * plane + vec_of(r)] = make_float2(M, Ls[k] * kChunkInvPShift);
   }
-  uint32_t* kinds = reinterpret_cast<uint32_t*>(sO);
+  float* sF = reinterpret_cast<float*>(smem);                               // the CTA's numerators [ROWS][D]
+  uint32_t* kinds = reinterpret_cast<uint32_t*>(smem + ROWS * D * 4);       // non-finite marks
+  if (zap || clustered) __syncthreads();
   if (zap) {
-    __syncthreads();
     mark_nonfinite_v<D, FMT>(p, kinds, b, g, u0, u1, span, RC,
-                             [&](int i) { return chunk_row(p, req, span, i / p.G); });
+                             [&](int i) { return chunk_row(p, req, span, token_of(i)); });
+#pragma unroll
+    for (int k = 0; k < kIter; ++k) {
+      const int x = tid + k * kThreadsS;
+      const int r = x / (D / 4);
+      if (r >= RC) continue;
+      const uint32_t kd = kinds[x];
+      float y[4] = {acc[k].x, acc[k].y, acc[k].z, acc[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((kd >> (8 * j)) & 0xFFu) y[j] = nonfinite_value((kd >> (8 * j)) & 0xFFu);
+      acc[k] = make_float4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  auto write_out = [&](int r, int d, const float4& y, float L) {
+    const float f = vs / L;
+    *reinterpret_cast<uint2*>(p.out + (int64_t)(req.row0 + token_of(r)) * p.o_st + (int64_t)head_of(r) * p.o_sh + d) =
+        L == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_out<DT>(y.x * f, y.y * f), pack_out<DT>(y.z * f, y.w * f));
+  };
+  if (clustered) {
+    // ---------------------------------------------------------- join the cluster
+#pragma unroll
+    for (int k = 0; k < kIter; ++k) {
+      const int x = tid + k * kThreadsS;
+      if (x >= kItems) continue;
+      *reinterpret_cast<float4*>(sF + 4 * x) = acc[k];
+      if (x % (D / 4) == 0) {
+        sMj[x / (D / 4)] = Ms[k];
+        sLj[x / (D / 4)] = Ls[k];
+      }
+    }
+    cluster_sync();
+    for (int x = s * kThreadsS + tid; x < kItems; x += p.S * kThreadsS) {
+      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+      if (r >= RC) continue;
+      float mw[kChunkClusterMax], lw[kChunkClusterMax];
+      float4 y[kChunkClusterMax];
+      float M = kNoMax, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kChunkClusterMax; ++w) {
+        const int q = min(w, p.S - 1);
+        mw[w] = peer_f32(peer_addr(sMj + r, q));
+        lw[w] = peer_f32(peer_addr(sLj + r, q));
+        y[w] = peer_f32x4(peer_addr(sF + 4 * x, q));
+      }
+#pragma unroll
+      for (int w = 0; w < kChunkClusterMax; ++w)
+        if (w < p.S) M = fmaxf(M, mw[w]);
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kChunkClusterMax; ++w) {
+        if (w >= p.S || (mw[w] == kNoMax && lw[w] == 0.f)) continue;
+        const float a = part_weight(mw[w], M);
+        L = fmaf(a, lw[w], L);
+        z.x = fmaf(a, y[w].x, z.x);
+        z.y = fmaf(a, y[w].y, z.y);
+        z.z = fmaf(a, y[w].z, z.z);
+        z.w = fmaf(a, y[w].w, z.w);
+      }
+      write_out(r, d, z, L);
+    }
+    cluster_sync();  // peers may still be reading this CTA's sums
+    return;
   }
 #pragma unroll
   for (int k = 0; k < kIter; ++k) {
     const int x = tid + k * kThreadsS;
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;
     if (r >= RC) continue;
-    float y[4] = {acc[k].x, acc[k].y, acc[k].z, acc[k].w};
-    const bool dead = Ls[k] == 0.f;
-    const float f = p.S > 1 ? kChunkInvPShift : (dead ? 0.f : vs / Ls[k]);
-    const uint32_t kd = zap ? kinds[r * (D / 4) + d / 4] : 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] *= f;
-      const uint32_t kind = (kd >> (8 * j)) & 0xFFu;
-      if (kind) y[j] = nonfinite_value(kind) * (p.S > 1 ? 1.f : vs);
-    }
     if (p.S > 1) {
-      *reinterpret_cast<float4*>(p.partial + (s * plane + vec_of(r)) * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+      if (d == 0) p.ml[s * plane + vec_of(r)] = make_float2(Ms[k], Ls[k] * kChunkInvPShift);
+      *reinterpret_cast<float4*>(p.partial + (s * plane + vec_of(r)) * D + d) =
+          make_float4(acc[k].x * kChunkInvPShift, acc[k].y * kChunkInvPShift, acc[k].z * kChunkInvPShift,
+                      acc[k].w * kChunkInvPShift);
     } else {
-      uint16_t* dst = p.out + (int64_t)(req.row0 + r / p.G) * p.o_st + (int64_t)(g * p.G + r % p.G) * p.o_sh + d;
-      *reinterpret_cast<uint2*>(dst) =
-          dead ? make_uint2(0u, 0u) : make_uint2(pack_out<DT>(y[0], y[1]), pack_out<DT>(y[2], y[3]));
+      write_out(r, d, acc[k], Ls[k]);
     }
   }
 }
@@ -470,12 +589,24 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D>::kCtas) chunk_stream(c
 template <int D, int FMT, int DT, bool WIDE>
 cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
   auto fn = chunk_stream<D, FMT, DT, WIDE>;
-  constexpr int smem = StreamCfg<D>::smem(WIDE);
+  constexpr int smem = StreamCfg<D, WIDE>::kSmem;
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  fn<<<dim3((unsigned)(p.B * p.S), p.Hkv), kThreadsS, smem, st>>>(p);
-  return cudaGetLastError();
+  const int chunks = (int)(((int64_t)p.max_q * p.G + kR - 1) / kR);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.S), p.Hkv, chunks);
+  cfg.blockDim = dim3(kThreadsS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.S;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  const bool clustered = chunk_clustered(plan);
+  cfg.attrs = &attr;
+  cfg.numAttrs = clustered ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, p, (int)clustered);
 }
 
 template <int D, int FMT, int DT>

@@ -406,7 +406,7 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  * graph-capturable: lengths may change between replays within the plan.
  * ------------------------------------------------------------------------ */
 #define FP8KV_CHUNK_AUTO 0
-#define FP8KV_CHUNK_STREAM 1 /* at most 16 query vectors per (request, KV head): max_q * Hq/Hkv <= 16 */
+#define FP8KV_CHUNK_STREAM 1 /* streams the cache past 16 query vectors per CTA */
 #define FP8KV_CHUNK_TILE 2   /* tcgen05 tiles of 128 query vectors */
 
 typedef struct {

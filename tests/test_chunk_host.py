@@ -57,7 +57,8 @@ def _desc(B, **kw):
     (dict(max_blocks=249), -1), (dict(num_kv_blocks=0), -1), (dict(window=-1), -1), (dict(sinks=-1, window=5), -1),
     (dict(sinks=4), -1), (dict(dtype=2), -1), (dict(kv_format=3), -1), (dict(kv_format=-1), -1),
     (dict(num_splits=-1), -1), (dict(num_splits=1 << 17), -1), (dict(kernel=3), -1), (dict(num_sms=-1), -1),
-    (dict(kv_format=2), -2), (dict(head_dim=96), -2), (dict(head_dim=0), -2), (dict(kernel=1), -2),
+    (dict(kv_format=2), -2), (dict(head_dim=96), -2), (dict(head_dim=0), -2),
+    (dict(kernel=1, max_q=300000, total_q=1 << 20), -2),
     (dict(max_q=(1 << 24) + 1), -2), (dict(total_q=(1 << 30) + 1), -2),
     (dict(max_kv_len=(1 << 30) + 1, max_blocks=(1 << 27)), -2),
     (dict(num_q_heads=1 << 17, num_kv_heads=1 << 17), -2),

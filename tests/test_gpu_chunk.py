@@ -95,8 +95,7 @@ def check(got, c, ref=None, rows=None):
 
 def kernels(c):
     """Every kernel that takes the case: (kernel, partitions)."""
-    small = c.max_q * c.group <= 16
-    return ([(1, 0), (1, 1), (1, 3)] if small else []) + [(2, 0), (2, 1), (2, 3), (0, 0)]
+    return [(1, 0), (1, 1), (1, 3), (1, 11), (2, 0), (2, 1), (2, 3), (0, 0)]
 
 
 CASES = {
