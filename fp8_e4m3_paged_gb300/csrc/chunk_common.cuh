@@ -58,10 +58,18 @@ __device__ __forceinline__ ChunkSpan chunk_span(const ChunkParams& p, const Chun
   return s;
 }
 
-// 2^(m - M), the weight of a partition that saw something in the joint sum:
-// never 0, so that an infinite numerator of a far smaller partition stays
-// infinite (0 * inf would not).
-__device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : exp2f(fmaxf(m - M, -120.f)); }
+// 2^x for a whole x <= 0 (0 below the normal range; NaN, from infinite maxima, stays NaN).
+__device__ __forceinline__ float exp2_whole(float x) {
+  if (x != x) return x;
+  return x < -126.f ? 0.f : __int_as_float(((int)x + 127) << 23);
+}
+
+// 2^(m - M), the weight of a partition that saw something in the joint sum
+// (whole maxima): never 0, so that an infinite numerator of a far smaller
+// partition stays infinite (0 * inf would not).
+__device__ __forceinline__ float part_weight(float m, float M) {
+  return m == M ? 1.f : exp2_whole(fmaxf(m - M, -120.f));
+}
 
 // What one row sees on that axis: v < hi and (v >= lo or v < sk).
 struct ChunkRow {

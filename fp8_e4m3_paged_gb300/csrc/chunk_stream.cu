@@ -54,16 +54,22 @@ struct StreamCfg {
   static constexpr int kQStride = D + 8;             // fp16 elements (padding: fragment loads without conflicts)
   static constexpr bool kQRegs = D <= 128;           // Q's fragments stay in registers
   static constexpr int kCtas = D == 256 ? 2 : D == 128 ? 3 : 5;  // resident per SM
-  static constexpr int kStages = D == 64 ? 4 : 3;    // blocks of a warp in flight or in use
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // blocks of a warp in flight or in use
   static constexpr int kKBytes = 2 * kKP * 512;      // a block's K pieces: [piece][lane] of 16 bytes
   static constexpr int kVBytes = 4 * kVP * (D >= 128 ? 512 : 256);
   static constexpr int kRing = kStages * (kKBytes + kVBytes);  // per warp; then its numerators [row][D]
   static constexpr int kQBytes = kR * kQStride * 2;
   static constexpr int kOffQ = kWarps * kRing;
-  static constexpr int kOffRed = kOffQ + kQBytes;    // per warp and row: maximum, sum; inverse row scales; joined
-  static constexpr int kSmem = kOffRed + (2 * kWarps + 3) * 16 * 4;
+  static constexpr int kOffRed = kOffQ + kQBytes;    // per warp and row: maximum, sum; then inverse row scales
+  // Cluster: the joined numerators, as float4 items, are owned by its CTAs in
+  // equal runs; an owner receives every partition's items and (maximum, sum) pairs here.
+  static constexpr int kItems = kRows * D / 4;
+  static constexpr int kIter = (kItems + kThreadsS - 1) / kThreadsS;
+  static constexpr int kOffPairs = kOffRed + (2 * kWarps + 1) * 16 * 4;  // [partition][row]
+  static constexpr int kOffItems = kOffPairs + kChunkClusterMax * 16 * 8;  // [partition][item of the run]
+  static constexpr int kSmem = kOffItems + (kItems + kChunkClusterMax) * 16;
   static_assert(kRing >= kRows * D * 4, "a warp's numerators fit its ring");
-  static_assert(kWarps * kRing >= kRows * D * 5, "joined numerators and the non-finite marks");
+  static_assert(kRing * kWarps >= kRows * D, "non-finite marks");
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -82,25 +88,21 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Thread-block cluster: barrier over all its CTAs, and loads from a peer's
-// shared memory (the address that `p` has in CTA `rank`).
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// Thread-block cluster: barrier over all its CTAs in two halves, and stores
+// into a peer's shared memory (the place that `p` has in CTA `rank`).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float peer_f32(uint32_t a) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a));
-  return x;
+__device__ __forceinline__ void peer_store(uint32_t a, float2 x) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(x.x), "f"(x.y) : "memory");
 }
-__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a));
-  return x;
+__device__ __forceinline__ void peer_store(uint32_t a, float4 x) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& w, int i) {
@@ -111,14 +113,12 @@ template <int D, int FMT, int DT, bool WIDE>
 __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     chunk_stream(const __grid_constant__ ChunkParams p, const int clustered) {
   using C = StreamCfg<D, WIDE>;
-  constexpr int ROWS = C::kRows, ST = C::kStages;
+  constexpr int ST = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
   float* sM = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp][16]
   float* sL = sM + kWarps * 16;
   float* sBack = sL + kWarps * 16;                          // [16] inverse row scales
-  float* sMj = sBack + 16;                                  // [16] of the CTA
-  float* sLj = sMj + 16;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
   const int RC = min(kR, req.n * p.G - row_first);
   if (RC <= 0) return;  // every CTA of the cluster
+  if (clustered) cluster_arrive();  // peers may write here once all have come this far
   const int64_t plane = (int64_t)p.total_q * p.Hq;
   auto token_of = [&](int r) { return (row_first + r) / p.G; };
   auto head_of = [&](int r) { return g * p.G + (row_first + r) % p.G; };
@@ -150,24 +151,26 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
   const uint8_t* kbase = p.k_cache + g * p.ksh + c * 16;
   const uint8_t* vbase = p.v_cache + g * p.vsh + rq * (D >= 128 ? 16 : 8);
   uint8_t* ring = smem + warp * C::kRing;
-  int blk = -1, slot = 0;
-  bool in = false;
+  struct Ask {
+    int blk, slot;
+    bool in;
+  };
   auto ask = [&](int t) {
     const int v = t + (lane & 15);
-    in = v < u1;
-    blk = -1;
-    if (in) {
+    Ask a = {-1, 0, v < u1};
+    if (a.in) {
       const int pos = span.position(v), page = div_page(pos, p.page_size, p.page_div);
-      slot = pos - page * p.page_size;
-      blk = __ldg(p.block_table + (int64_t)b * p.bt_stride + page);
+      a.slot = pos - page * p.page_size;
+      a.blk = __ldg(p.block_table + (int64_t)b * p.bt_stride + page);
     }
+    return a;
   };
   // Copies of the block asked for into stage `st`; returns the tokens that are there.
-  auto request = [&](int st) {
-    const bool ok = blk >= 0 && blk < p.num_kv_blocks;
-    if (in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    const int64_t koff = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
-    const int64_t voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
+  auto request = [&](const Ask& a, int st) {
+    const bool ok = a.blk >= 0 && a.blk < p.num_kv_blocks;
+    if (a.in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
+    const int64_t koff = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
+    const int64_t voff = ok ? a.blk * p.vsb + (int64_t)a.slot * p.vst : 0;
     uint8_t* dst = ring + st * (C::kKBytes + C::kVBytes);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -192,58 +195,65 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
   constexpr int kStep = kBlk * kWarps;  // a warp's blocks are this far apart
   const int t_first = u0 + kBlk * warp;
   uint32_t there[ST];  // tokens of the blocks in flight, the oldest first
-  auto fill = [&]() {
+  Ask next;            // the block after them
+  auto fill = [&](auto between) {
+    Ask first[ST - 1];
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) first[i] = ask(t_first + i * kStep);
+    between();
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) {
-      ask(t_first + i * kStep);
-      there[i] = 0u;
-      if (t_first + i * kStep < u1) there[i] = request(i);
+      there[i] = t_first + i * kStep < u1 ? request(first[i], i) : 0u;
       cp_commit();
     }
-    ask(t_first + (ST - 1) * kStep);
+    next = ask(t_first + (ST - 1) * kStep);
   };
-  fill();
 
   // Q -> shared memory as fp16 (bf16 rows scaled by a power of two); rows past
-  // RC are zero.  One warp per row.
-  float sign = 1.f;
-  const float ks = p.k_scale_dev ? *p.k_scale_dev : p.k_scale;
-  const double cd = (double)p.softmax_scale * (double)ks * 1.4426950408889634074;
-  if (cd < 0) sign = -1.f;  // logit factors are non-negative from here on
-  for (int r = warp; r < kR; r += kWarps) {
-    constexpr int V = D / 32;  // elements per lane
-    uint32_t w[V / 2] = {};
-    if (r < RC) {
+  // RC are zero.  One warp per row; the rows are requested before the first
+  // blocks, so that their latencies overlap.
+  constexpr int V = D / 32;  // elements per lane
+  constexpr int kQRows = kR / kWarps;
+  uint32_t qw[kQRows][V / 2];
+  const float ks = p.k_scale_dev ? __ldg(p.k_scale_dev) : p.k_scale;
+  const float vs = p.v_scale_dev ? __ldg(p.v_scale_dev) : p.v_scale;
+  fill([&]() {
+#pragma unroll
+    for (int k = 0; k < kQRows; ++k) {
+      const int r = min(warp + k * kWarps, RC - 1);
       const uint16_t* src = p.q + (int64_t)(req.row0 + token_of(r)) * p.q_st + (int64_t)head_of(r) * p.q_sh;
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + lane * V + 2 * j);
+      if constexpr (V == 2)
+        qw[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
+      else if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(qw[k]) = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+      else
+        *reinterpret_cast<uint4*>(qw[k]) = __ldg(reinterpret_cast<const uint4*>(src) + lane);
     }
-    RowScale rs = {1.f, 1.f};
-    float f[V];
+  });
+  const float cf = p.softmax_scale * ks * kLog2e;
+  const uint32_t flip = cf < 0.f ? 0x80008000u : 0u;  // logit factors are non-negative from here on
+#pragma unroll
+  for (int k = 0; k < kQRows; ++k) {
+    const int r = warp + k * kWarps;
+    uint32_t* w = qw[k];
+    float back = 1.f;
     if (DT == FP8KV_DTYPE_BF16) {
-      float amax = 0.f;
+      uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        // as integers: a NaN is larger than every number, and is not dropped
-        amax = __uint_as_float(max(__float_as_uint(amax), max(__float_as_uint(fabsf(f[2 * j])),
-                                                              __float_as_uint(fabsf(f[2 * j + 1])))));
-      }
-      rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
+      for (int j = 0; j < V / 2; ++j) top = max(top, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+      const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) w[j] = pack_half2(f[2 * j] * rs.to_f16, f[2 * j + 1] * rs.to_f16);
+      for (int j = 0; j < V / 2; ++j)
+        w[j] = pack_half2(__uint_as_float(w[j] << 16) * rs.to_f16, __uint_as_float(w[j] & 0xFFFF0000u) * rs.to_f16);
+      back = rs.back;
     }
-    if (sign < 0.f)
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) w[j] ^= 0x80008000u;
 #pragma unroll
     for (int j = 0; j < V / 2; ++j)
-      *reinterpret_cast<uint32_t*>(sQ + r * C::kQStride + lane * V + 2 * j) = w[j];
-    if (lane == 0) sBack[r] = rs.back;
+      *reinterpret_cast<uint32_t*>(sQ + r * C::kQStride + lane * V + 2 * j) = r < RC ? w[j] ^ flip : 0u;
+    if (lane == 0) sBack[r] = back;
   }
   __syncthreads();
-  const float c0f = (float)(fabs(cd) * sBack[rq]), c1f = (float)(fabs(cd) * sBack[rq + 8]);
+  const float c0f = fabsf(cf) * sBack[rq], c1f = fabsf(cf) * sBack[rq + 8];
 
   // What this lane's two rows see; rows past RC see everything (their values are dropped).
   ChunkRow row0 = {INT_MAX, INT_MIN}, row1 = {INT_MAX, INT_MIN};
@@ -276,6 +286,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
 
   float o[C::kNT][4];
   float m0, m1, l0, l1;
+  float4 acc[C::kIter];  // after the join: numerators of this thread's items, their rows' maxima and sums
+  float Ms[C::kIter], Ls[C::kIter];
   bool zap = false;  // second pass: non-finite V codes enter as 0
   while (true) {
 #pragma unroll
@@ -287,8 +299,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
       // the block ST - 1 ahead goes where the block before this one was
       there[ST - 1] = 0u;
       if (t + (ST - 1) * kStep < u1) {
-        there[ST - 1] = request(st == 0 ? ST - 1 : st - 1);
-        ask(t + ST * kStep);
+        there[ST - 1] = request(next, st == 0 ? ST - 1 : st - 1);
+        next = ask(t + ST * kStep);
       }
       cp_commit();
       cp_wait<ST - 1>();
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
         y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, 2));
         const float n0 = y0 > m0 + kChunkTau || m0 == kNoMax ? fmaxf(m0, ceilf(y0)) : m0;
         const float n1 = y1 > m1 + kChunkTau || m1 == kNoMax ? fmaxf(m1, ceilf(y1)) : m1;
-        const float a0 = n0 == m0 ? 1.f : exp2_int(m0 - n0), a1 = n1 == m1 ? 1.f : exp2_int(m1 - n1);
+        const float a0 = n0 == m0 ? 1.f : exp2_whole(m0 - n0), a1 = n1 == m1 ? 1.f : exp2_whole(m1 - n1);
         m0 = n0;
         m1 = n1;
         l0 *= a0;
@@ -427,91 +439,83 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
         }
     }
     cp_wait<0>();
-    if (zap) break;
-    // Non-finite sums: maybe only from codes of tokens that some rows do not see (0 * NaN).
+
+    // ---------------------------------------------------------- join the warps
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (c == 0) {
+      sM[warp * 16 + rq] = m0;
+      sL[warp * 16 + rq] = l0;
+      if (WIDE) {
+        sM[warp * 16 + rq + 8] = m1;
+        sL[warp * 16 + rq + 8] = l1;
+      }
+    }
+    // n-tile (i, x) column n of O is d = 128 i + PB n + x, PB the bytes of a V piece
+    constexpr int PB = 4 * C::kVWords;
+    float* sO = reinterpret_cast<float*>(ring);  // this warp's numerators [row][D]
+#pragma unroll
+    for (int i = 0; i < C::kVP; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 0; x < PB; x += 4) {
+          const int d = 128 * i + PB * (2 * c + e) + x;
+          float f[4], h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[k] = o[i * PB + x + k][e];
+            h[k] = o[i * PB + x + k][2 + e];
+            if (!WIDE) f[k] = fmaf(h[k], kLoDown, f[k]);
+          }
+          *reinterpret_cast<float4*>(sO + rq * D + d) = make_float4(f[0], f[1], f[2], f[3]);
+          if (WIDE) *reinterpret_cast<float4*>(sO + (rq + 8) * D + d) = make_float4(h[0], h[1], h[2], h[3]);
+        }
+    __syncthreads();
     float bad = 0.f;
 #pragma unroll
-    for (int n = 0; n < C::kNT; ++n)
+    for (int k = 0; k < C::kIter; ++k) {
+      const int x = tid + k * kThreadsS;
+      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+      acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      Ls[k] = 0.f;
+      Ms[k] = kNoMax;
+      if (r >= RC) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) bad = fmaf(o[n][e], 0.f, bad);
+      for (int w = 0; w < kWarps; ++w) Ms[k] = fmaxf(Ms[k], sM[w * 16 + r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sM[w * 16 + r], lw = sL[w * 16 + r];
+        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem + w * C::kRing) + r * D + d);
+        // (a warp that saw nothing has a sum of 0 and numerators of 0)
+        const float a = mw == Ms[k] ? 1.f : exp2_whole(mw - Ms[k]);
+        Ls[k] = fmaf(a, lw, Ls[k]);
+        acc[k].x = fmaf(a, y.x, acc[k].x);
+        acc[k].y = fmaf(a, y.y, acc[k].y);
+        acc[k].z = fmaf(a, y.z, acc[k].z);
+        acc[k].w = fmaf(a, y.w, acc[k].w);
+      }
+      bad = fmaf(acc[k].x + acc[k].y + acc[k].z + acc[k].w, 0.f, bad);
+    }
+    if (zap) break;
+    // Sums that are not finite: maybe only from codes of tokens that some rows do
+    // not see (0 * NaN).  Once more without the non-finite V codes.
     if (!__syncthreads_or(bad != 0.f)) break;
     zap = true;
-    fill();
+    fill([]() {});
   }
 
-  // ------------------------------------------------------------ join the warps
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-  if (c == 0) {
-    sM[warp * 16 + rq] = m0;
-    sL[warp * 16 + rq] = l0;
-    if (WIDE) {
-      sM[warp * 16 + rq + 8] = m1;
-      sL[warp * 16 + rq + 8] = l1;
-    }
-  }
-  // n-tile (i, x) column n of O is d = 128 i + PB n + x, PB the bytes of a V piece
-  constexpr int PB = 4 * C::kVWords;
-  float* sO = reinterpret_cast<float*>(ring);  // this warp's numerators [ROWS][D]
-#pragma unroll
-  for (int i = 0; i < C::kVP; ++i)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int x = 0; x < PB; x += 4) {
-        const int d = 128 * i + PB * (2 * c + e) + x;
-        float f[4], h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k] = o[i * PB + x + k][e];
-          h[k] = o[i * PB + x + k][2 + e];
-          if (!WIDE) f[k] = fmaf(h[k], kLoDown, f[k]);
-        }
-        *reinterpret_cast<float4*>(sO + rq * D + d) = make_float4(f[0], f[1], f[2], f[3]);
-        if (WIDE) *reinterpret_cast<float4*>(sO + (rq + 8) * D + d) = make_float4(h[0], h[1], h[2], h[3]);
-      }
-  __syncthreads();
-  const float vs = p.v_scale_dev ? *p.v_scale_dev : p.v_scale;
-  constexpr int kItems = ROWS * D / 4;  // float4 of the joined numerators
-  constexpr int kIter = (kItems + kThreadsS - 1) / kThreadsS;
-  float4 acc[kIter];
-  float Ms[kIter], Ls[kIter];
-#pragma unroll
-  for (int k = 0; k < kIter; ++k) {
-    const int x = tid + k * kThreadsS;
-    const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    Ls[k] = 0.f;
-    Ms[k] = kNoMax;
-    if (x >= kItems) continue;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) Ms[k] = fmaxf(Ms[k], sM[w * 16 + r]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = sM[w * 16 + r], lw = sL[w * 16 + r];
-      const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem + w * C::kRing) + r * D + d);
-      if (mw == kNoMax && lw == 0.f) continue;  // saw nothing
-      const float a = mw == Ms[k] ? 1.f : exp2_int(mw - Ms[k]);
-      Ls[k] = fmaf(a, lw, Ls[k]);
-      acc[k].x = fmaf(a, y.x, acc[k].x);
-      acc[k].y = fmaf(a, y.y, acc[k].y);
-      acc[k].z = fmaf(a, y.z, acc[k].z);
-      acc[k].w = fmaf(a, y.w, acc[k].w);
-    }
-  }
-  float* sF = reinterpret_cast<float*>(smem);                               // the CTA's numerators [ROWS][D]
-  uint32_t* kinds = reinterpret_cast<uint32_t*>(smem + ROWS * D * 4);       // non-finite marks
-  if (zap || clustered) __syncthreads();
   if (zap) {
+    uint32_t* kinds = reinterpret_cast<uint32_t*>(smem);  // non-finite marks [row][D]
+    __syncthreads();
     mark_nonfinite_v<D, FMT>(p, kinds, b, g, u0, u1, span, RC,
                              [&](int i) { return chunk_row(p, req, span, token_of(i)); });
 #pragma unroll
-    for (int k = 0; k < kIter; ++k) {
+    for (int k = 0; k < C::kIter; ++k) {
       const int x = tid + k * kThreadsS;
-      const int r = x / (D / 4);
-      if (r >= RC) continue;
+      if (x / (D / 4) >= RC) continue;
       const uint32_t kd = kinds[x];
       float y[4] = {acc[k].x, acc[k].y, acc[k].z, acc[k].w};
 #pragma unroll
@@ -527,51 +531,46 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
   };
   if (clustered) {
     // ---------------------------------------------------------- join the cluster
+    const int run = (C::kItems + p.S - 1) / p.S;  // item x belongs to CTA x / run
+    float2* pairs = reinterpret_cast<float2*>(smem + C::kOffPairs);
+    float4* items = reinterpret_cast<float4*>(smem + C::kOffItems);
+    __syncwarp();
+    cluster_wait();
 #pragma unroll
-    for (int k = 0; k < kIter; ++k) {
-      const int x = tid + k * kThreadsS;
-      if (x >= kItems) continue;
-      *reinterpret_cast<float4*>(sF + 4 * x) = acc[k];
-      if (x % (D / 4) == 0) {
-        sMj[x / (D / 4)] = Ms[k];
-        sLj[x / (D / 4)] = Ls[k];
-      }
-    }
-    cluster_sync();
-    for (int x = s * kThreadsS + tid; x < kItems; x += p.S * kThreadsS) {
-      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+    for (int k = 0; k < C::kIter; ++k) {
+      const int x = tid + k * kThreadsS, r = x / (D / 4);
       if (r >= RC) continue;
-      float mw[kChunkClusterMax], lw[kChunkClusterMax];
-      float4 y[kChunkClusterMax];
+      const int owner = x / run;
+      peer_store(peer_addr(items + s * run + (x - owner * run), owner), acc[k]);
+      if (x % (D / 4) == 0)
+        for (int q = 0; q < p.S; ++q) peer_store(peer_addr(pairs + s * 16 + r, q), make_float2(Ms[k], Ls[k]));
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    for (int i = tid; i < run; i += kThreadsS) {
+      const int x = s * run + i, r = x / (D / 4), d = (x % (D / 4)) * 4;
+      if (r >= RC) continue;
       float M = kNoMax, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kChunkClusterMax; ++w) {
-        const int q = min(w, p.S - 1);
-        mw[w] = peer_f32(peer_addr(sMj + r, q));
-        lw[w] = peer_f32(peer_addr(sLj + r, q));
-        y[w] = peer_f32x4(peer_addr(sF + 4 * x, q));
-      }
-#pragma unroll
-      for (int w = 0; w < kChunkClusterMax; ++w)
-        if (w < p.S) M = fmaxf(M, mw[w]);
+      for (int q = 0; q < p.S; ++q) M = fmaxf(M, pairs[q * 16 + r].x);
       float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kChunkClusterMax; ++w) {
-        if (w >= p.S || (mw[w] == kNoMax && lw[w] == 0.f)) continue;
-        const float a = part_weight(mw[w], M);
-        L = fmaf(a, lw[w], L);
-        z.x = fmaf(a, y[w].x, z.x);
-        z.y = fmaf(a, y[w].y, z.y);
-        z.z = fmaf(a, y[w].z, z.z);
-        z.w = fmaf(a, y[w].w, z.w);
+      for (int q = 0; q < p.S; ++q) {
+        const float2 ml = pairs[q * 16 + r];
+        const float4 y = items[q * run + i];
+        if (ml.x == kNoMax && ml.y == 0.f) continue;  // saw nothing
+        const float a = part_weight(ml.x, M);
+        L = fmaf(a, ml.y, L);
+        z.x = fmaf(a, y.x, z.x);
+        z.y = fmaf(a, y.y, z.y);
+        z.z = fmaf(a, y.z, z.z);
+        z.w = fmaf(a, y.w, z.w);
       }
       write_out(r, d, z, L);
     }
-    cluster_sync();  // peers may still be reading this CTA's sums
     return;
   }
 #pragma unroll
-  for (int k = 0; k < kIter; ++k) {
+  for (int k = 0; k < C::kIter; ++k) {
     const int x = tid + k * kThreadsS;
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;
     if (r >= RC) continue;

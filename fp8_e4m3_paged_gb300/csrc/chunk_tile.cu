@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         if (__any_sync(0xffffffffu, top > m + kChunkTau || (m == kNoMax && top > -INFINITY))) {
           const float n = top > m + kChunkTau || m == kNoMax ? fmaxf(m, ceilf(top)) : m;
-          const float a = n == m || m == kNoMax ? 1.f : exp2_int(m - n);
+          const float a = n == m || m == kNoMax ? 1.f : exp2_whole(m - n);
           m = n;
           l *= a;
           if (j > 0 && __any_sync(0xffffffffu, a != 1.f)) {
