@@ -2,10 +2,11 @@
 // of one KV head times a few new tokens): bound by streaming the cache.
 //
 // One CTA of four warps per (request, KV head, 16 query vectors, partition);
-// each warp walks blocks of 16 virtual tokens (chunk_span) on its own, and the four are joined at
-// the end.  A block's FP8 bytes are requested two blocks ahead by cp.async
-// into places of shared memory that only the requesting lane reads, so the
-// loop has no barrier; each lane asks for the bytes that its MMA fragments hold:
+// each warp walks blocks of 16 virtual tokens (chunk_span) on
+// its own, and the four are joined at the end.  A block's FP8 bytes are
+// requested a block or more ahead by cp.async into places of shared memory
+// that only the requesting lane reads, so the loop has no barrier; each lane
+// asks for the bytes that its MMA fragments hold:
 //   S[16 x 8 tokens] = Q . K^T, m16n8k16: a lane of the B operand needs four
 //     d of one token, so lane (n = lane/4, c = lane%4) loads the 16-byte pieces c, c + 4, ... of token n's row; each 32-bit word
 //     decodes to one MMA's B fragment, and the d that a word holds is simply
@@ -40,7 +41,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreadsS = 32 * kWarps;
-constexpr int kBlk = kChunkStreamBlock;
 constexpr int kR = kChunkStreamRows;
 constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;
 
@@ -54,9 +54,11 @@ struct StreamCfg {
   static constexpr int kQStride = D + 8;             // fp16 elements (padding: fragment loads without conflicts)
   static constexpr bool kQRegs = D <= 128;           // Q's fragments stay in registers
   static constexpr int kCtas = D == 256 ? 2 : D == 128 ? 3 : 5;  // resident per SM
+  static constexpr int kBlk = kChunkStreamBlock; // positions per warp step
+  static constexpr int kNB = kBlk / 16;              // ... in sub-blocks of an MMA's 16
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // blocks of a warp in flight or in use
-  static constexpr int kKBytes = 2 * kKP * 512;      // a block's K pieces: [piece][lane] of 16 bytes
-  static constexpr int kVBytes = 4 * kVP * (D >= 128 ? 512 : 256);
+  static constexpr int kKBytes = kNB * 2 * kKP * 512;  // a block's K pieces: [sub-block][piece][lane] of 16 bytes
+  static constexpr int kVBytes = kNB * 4 * kVP * (D >= 128 ? 512 : 256);
   static constexpr int kRing = kStages * (kKBytes + kVBytes);  // per warp; then its numerators [row][D]
   static constexpr int kQBytes = kR * kQStride * 2;
   static constexpr int kOffQ = kWarps * kRing;
@@ -73,7 +75,7 @@ struct StreamCfg {
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -113,7 +115,8 @@ template <int D, int FMT, int DT, bool WIDE>
 __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     chunk_stream(const __grid_constant__ ChunkParams p, const int clustered) {
   using C = StreamCfg<D, WIDE>;
-  constexpr int ST = C::kStages;
+  constexpr int ST = C::kStages, kBlk = C::kBlk, NB = C::kNB;
+  constexpr uint32_t kAll = kBlk == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
   float* sM = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp][16]
@@ -122,8 +125,9 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
-  const int b = blockIdx.x / p.S, s = blockIdx.x - b * p.S;
-  const int g = blockIdx.y;
+  // KV heads next to each other, so that the CTAs that read one token's heads (adjacent
+  // in memory) run at the same time
+  const int g = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv, s = blockIdx.y;
   const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     return;
   }
 
-  // Places of a block's 16 tokens, one per lane (both halves of the warp hold
+  // Places of a block's tokens, one per lane (of 16, both halves of the warp hold
   // them).  The block id is requested a block before it is needed; the copies
   // are unconditional (tokens without a place read the pool's first row and
   // are masked, V also zeroed).
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     bool in;
   };
   auto ask = [&](int t) {
-    const int v = t + (lane & 15);
+    const int v = t + (lane & (kBlk - 1));
     Ask a = {-1, 0, v < u1};
     if (a.in) {
       const int pos = span.position(v), page = div_page(pos, p.page_size, p.page_div);
@@ -173,14 +177,14 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     const int64_t voff = ok ? a.blk * p.vsb + (int64_t)a.slot * p.vst : 0;
     uint8_t* dst = ring + st * (C::kKBytes + C::kVBytes);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * NB; ++h) {
       const uint8_t* src = kbase + __shfl_sync(0xffffffffu, koff, rq + 8 * h);
 #pragma unroll
       for (int i = 0; i < C::kKP; ++i) tc::cp_async16(dst + ((h * C::kKP + i) * 32 + lane) * 16, src + 64 * i);
     }
     dst += C::kKBytes;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4 * NB; ++j) {
       const uint8_t* src = vbase + __shfl_sync(0xffffffffu, voff, 2 * c + (j & 1) + 8 * (j >> 1));
 #pragma unroll
       for (int i = 0; i < C::kVP; ++i) {
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
           cp_async8(dst + (j * 32 + lane) * 8, src);
       }
     }
-    return __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
+    return __ballot_sync(0xffffffffu, ok) & kAll;
   };
   constexpr int kStep = kBlk * kWarps;  // a warp's blocks are this far apart
   const int t_first = u0 + kBlk * warp;
@@ -310,55 +314,38 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
       const uint32_t valid = there[0];
 #pragma unroll
       for (int i = 0; i + 1 < ST; ++i) there[i] = there[i + 1];
-      float sc[2][4];
-      uint4 kr[2][C::kKP];
+      float sc[2 * NB][4];  // [half sub-block]: 8 tokens
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2 * NB; ++h) sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::kKP; ++i) kr[h][i] = *reinterpret_cast<const uint4*>(kst + (h * C::kKP + i) * 512);
+      for (int i = 0; i < C::kKP; ++i) {
+        uint4 kr[2 * NB];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
+        for (int h = 0; h < 2 * NB; ++h) kr[h] = *reinterpret_cast<const uint4*>(kst + (h * C::kKP + i) * 512);
 #pragma unroll
-        for (int i = 0; i < C::kKP; ++i)
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a[4];
+          if (!C::kQRegs) q_frag(i, w, a);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int h = 0; h < 2 * NB; ++h) {
             uint32_t b0, b1;
-            fp8x4_to_f16<FMT>(word(kr[h][i], w), b0, b1);
-            if (C::kQRegs) {
-              mma16816(sc[h], qa[C::kQRegs ? i * 4 + w : 0], b0, b1);
-            } else {
-              uint32_t a[4];
-              q_frag(i, w, a);
-              mma16816(sc[h], a, b0, b1);
-            }
-          }
-      }
-      uint4 vr[4][C::kVP];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < C::kVP; ++i) {
-          if (D >= 128) {
-            vr[j][i] = *reinterpret_cast<const uint4*>(vst + (j * C::kVP + i) * 512);
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(vst + j * 256);
-            vr[j][i] = make_uint4(y.x, y.y, 0u, 0u);
+            fp8x4_to_f16<FMT>(word(kr[h], w), b0, b1);
+            mma16816(sc[h], C::kQRegs ? qa[C::kQRegs ? i * 4 + w : 0] : a, b0, b1);
           }
         }
+      }
       // base-2 logits; tokens that a row does not see by selection
+      float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sc[h][0] *= c0f;
-        sc[h][1] *= c0f;
-        if (WIDE) {
-          sc[h][2] *= c1f;
-          sc[h][3] *= c1f;
+      for (int h = 0; h < 2 * NB; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[h][e] *= c0f;
+          if (WIDE) sc[h][2 + e] *= c1f;
         }
-      }
-      if (valid != 0xFFFFu || t + kBlk > hi_min || !(t >= lo_max || t + kBlk <= span.sk)) {
+      if (valid != kAll || t + kBlk > hi_min || !(t >= lo_max || t + kBlk <= span.sk)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2 * NB; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int x = 8 * h + 2 * c + e, v = t + x;
@@ -367,8 +354,11 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
             if (WIDE && !(ok && v < row1.hi && (v >= row1.lo || v < span.sk))) sc[h][2 + e] = -INFINITY;
           }
       }
-      const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      const float x1 = WIDE ? fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) : -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2 * NB; ++h) {
+        x0 = fmaxf(fmaxf(x0, sc[h][0]), sc[h][1]);
+        if (WIDE) x1 = fmaxf(fmaxf(x1, sc[h][2]), sc[h][3]);
+      }
       if (__any_sync(0xffffffffu, (x0 > -INFINITY && !(x0 <= m0 + kChunkTau)) ||
                                       (x1 > -INFINITY && !(x1 <= m1 + kChunkTau)))) {
         // a row's running maximum moves (integers: rescaling is exact)
@@ -392,50 +382,60 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
         }
       }
       const float s0 = (m0 == kNoMax ? 0.f : m0) - kChunkPShift, s1 = (m1 == kNoMax ? 0.f : m1) - kChunkPShift;
-      uint32_t pa[4];
+      uint32_t pa[NB][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2 * NB; ++h) {
+        uint32_t* q = &pa[h / 2][2 * (h & 1)];
         const float p0 = fast_exp2(sc[h][0] - s0), p1 = fast_exp2(sc[h][1] - s0);
         l0 += p0 + p1;
-        pa[2 * h] = pack_half2(p0, p1);
+        q[0] = pack_half2(p0, p1);
         if (WIDE) {
           const float p2 = fast_exp2(sc[h][2] - s1), p3 = fast_exp2(sc[h][3] - s1);
           l1 += p2 + p3;
-          pa[2 * h + 1] = pack_half2(p2, p3);
+          q[1] = pack_half2(p2, p3);
         } else {
-          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&pa[2 * h]));
-          pa[2 * h + 1] = pack_half2((p0 - f.x) * kLoUp, (p1 - f.y) * kLoUp);
+          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&q[0]));
+          q[1] = pack_half2((p0 - f.x) * kLoUp, (p1 - f.y) * kLoUp);
         }
       }
-      if (valid != 0xFFFFu) {  // 0 * NaN of a token that is not there
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (!((valid >> (2 * c + (j & 1) + 8 * (j >> 1))) & 1u))
+      for (int sb = 0; sb < NB; ++sb)
 #pragma unroll
-            for (int i = 0; i < C::kVP; ++i) vr[j][i] = make_uint4(0, 0, 0, 0);
-      }
-      if (zap) {
-        constexpr bool e5 = FMT == FP8KV_KV_E5M2;
+        for (int i = 0; i < C::kVP; ++i) {
+          uint4 vr[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
+            if (D >= 128) {
+              vr[j] = *reinterpret_cast<const uint4*>(vst + ((4 * sb + j) * C::kVP + i) * 512);
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(vst + (4 * sb + j) * 256);
+              vr[j] = make_uint4(y.x, y.y, 0u, 0u);
+            }
+          }
+          if (valid != kAll) {  // 0 * NaN of a token that is not there
 #pragma unroll
-          for (int i = 0; i < C::kVP; ++i)
-            vr[j][i] = make_uint4(zap_nonfinite(vr[j][i].x, e5), zap_nonfinite(vr[j][i].y, e5),
-                                  zap_nonfinite(vr[j][i].z, e5), zap_nonfinite(vr[j][i].w, e5));
-      }
+            for (int j = 0; j < 4; ++j)
+              if (!((valid >> (16 * sb + 2 * c + (j & 1) + 8 * (j >> 1))) & 1u)) vr[j] = make_uint4(0, 0, 0, 0);
+          }
+          if (zap) {
+            constexpr bool e5 = FMT == FP8KV_KV_E5M2;
 #pragma unroll
-      for (int i = 0; i < C::kVP; ++i)
-#pragma unroll
-        for (int w = 0; w < C::kVWords; ++w) {
-          uint32_t f[2][4];  // [token pair][d of the word]
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t wa = word(vr[2 * j][i], w), wb = word(vr[2 * j + 1][i], w);
-            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[j][0], f[j][1]);
-            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[j][2], f[j][3]);
+            for (int j = 0; j < 4; ++j)
+              vr[j] = make_uint4(zap_nonfinite(vr[j].x, e5), zap_nonfinite(vr[j].y, e5), zap_nonfinite(vr[j].z, e5),
+                                 zap_nonfinite(vr[j].w, e5));
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma16816(o[(i * C::kVWords + w) * 4 + e], pa, f[0][e], f[1][e]);
+          for (int w = 0; w < C::kVWords; ++w) {
+            uint32_t f[2][4];  // [token pair][d of the word]
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t wa = word(vr[2 * j], w), wb = word(vr[2 * j + 1], w);
+              fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[j][0], f[j][1]);
+              fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[j][2], f[j][3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma16816(o[(i * C::kVWords + w) * 4 + e], pa[sb], f[0][e], f[1][e]);
+          }
         }
     }
     cp_wait<0>();
@@ -594,14 +594,14 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
   if (e != cudaSuccess) return e;
   const int chunks = (int)(((int64_t)p.max_q * p.G + kR - 1) / kR);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.S), p.Hkv, chunks);
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), p.S, chunks);
   cfg.blockDim = dim3(kThreadsS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.S;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  attr.val.clusterDim.y = p.S;
+  attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
   const bool clustered = chunk_clustered(plan);
   cfg.attrs = &attr;
   cfg.numAttrs = clustered ? 1 : 0;
