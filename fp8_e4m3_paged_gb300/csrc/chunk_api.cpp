@@ -86,7 +86,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   int64_t units, slots, unit, span_q;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
     units = (int64_t)P.batch * P.num_kv_heads * ceil_div(rows, kChunkStreamRows);
-    slots = (int64_t)sms * (P.head_dim == 64 ? 5 : P.head_dim == 128 ? 3 : 2);
+    slots = (int64_t)sms * (P.head_dim == 64 ? 5 : P.head_dim == 128 ? 4 : 2);
     unit = 4 * kChunkStreamBlock;
     span_q = P.max_q;
   } else {

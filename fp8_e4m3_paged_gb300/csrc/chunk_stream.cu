@@ -7,26 +7,26 @@
 // requested a block or more ahead by cp.async into places of shared memory
 // that only the requesting lane reads, so the loop has no barrier; each lane
 // asks for the bytes that its MMA fragments hold:
-//   S[16 x 8 tokens] = Q . K^T, m16n8k16: a lane of the B operand needs four
-//     d of one token, so lane (n = lane/4, c = lane%4) loads the 16-byte pieces c, c + 4, ... of token n's row; each 32-bit word
-//     decodes to one MMA's B fragment, and the d that a word holds is simply
-//     the order in which Q's A fragments are laid out;
-//   O[16 x D] += P . V: a B fragment needs two tokens of one d in a register,
-//     so the lane loads the same 16-byte piece n of tokens 2c, 2c+1, 2c+8,
-//     2c+9 (a warp reads whole rows) and interleaves their bytes before the
-//     decode; P's fragment is what S's accumulators already hold.
-// So a warp needs about 150 instructions per 4 KB of K and V.  Legacy
-// mma.sync rather than tcgen05: with 4 to 16 useful rows the products are a
+//   S^T[16 tokens x 8 vectors] = K . Q^T, m16n8k16: lane (n = lane/4, c =
+//     lane%4) of the A operand needs four d of tokens n and n + 8, so it asks
+//     for the 16-byte pieces c, c + 4, ... of their rows; a 32-bit word of
+//     each decodes to one MMA's A fragment, and the d that the words hold are
+//     simply the order in which Q's B fragments are laid out;
+//   O^T[16 d x 8 vectors] += V^T . P^T: an A fragment needs two tokens of one
+//     d in a register, so the lane asks for the same 16-byte piece n of tokens
+//     2c, 2c+1, 2c+8, 2c+9 (a warp reads whole rows) and interleaves their
+//     bytes before the decode; P^T's B fragments are S^T's accumulators,
+//     packed to fp16 and transposed 8 by 8 (movmatrix).
+// Tokens and d as the MMA's 16 rows, vectors as its 8 columns: a decode step's
+// 1 to 8 vectors waste no rows, which halves the MMAs and O's registers
+// against the other orientation.  Legacy
+// mma.sync rather than tcgen05: with 4 to 16 vectors the products are a
 // few percent of the tensor peak, and TMEM or shared-memory operands would
 // only add copies and barriers to a kernel whose time is the bytes' arrival.
 //
 // Partitions of one request and KV head form a thread-block cluster when there
 // are at most 8: their sums are joined through distributed shared memory in
 // the same launch.  More go through the workspace and chunk_join.
-//
-// With at most 8 query vectors the upper 8 rows of P's fragment are free:
-// they carry P_lo = 2^11 (p - fp16(p)), which makes the probabilities good
-// to 22 bits at no cost.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -42,25 +42,24 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreadsS = 32 * kWarps;
 constexpr int kR = kChunkStreamRows;
-constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;
+constexpr int kBlk = kChunkStreamBlock;
+static_assert(kBlk == 16, "an MMA's tokens");
 
-template <int D, bool WIDE>
+// NQ: columns of 8 query vectors.
+template <int D, int NQ>
 struct StreamCfg {
-  static constexpr int kRows = WIDE ? 16 : 8;
+  static constexpr int kRows = 8 * NQ;
   static constexpr int kKP = D / 64;                 // 16-byte pieces of a K row per lane
   static constexpr int kVP = D >= 128 ? D / 128 : 1; // pieces of a V row per lane
   static constexpr int kVWords = D >= 128 ? 4 : 2;   // 32-bit words per piece
-  static constexpr int kNT = D / 8;                  // n-tiles of O
   static constexpr int kQStride = D + 8;             // fp16 elements (padding: fragment loads without conflicts)
-  static constexpr bool kQRegs = D <= 128;           // Q's fragments stay in registers
-  static constexpr int kCtas = D == 256 ? 2 : D == 128 ? 3 : 5;  // resident per SM
-  static constexpr int kBlk = kChunkStreamBlock; // positions per warp step
-  static constexpr int kNB = kBlk / 16;              // ... in sub-blocks of an MMA's 16
+  static constexpr bool kQRegs = D * NQ <= 256;      // Q's fragments stay in registers
+  static constexpr int kCtas = D == 256 ? 2 : D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 5 : 4);  // resident per SM
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // blocks of a warp in flight or in use
-  static constexpr int kKBytes = kNB * 2 * kKP * 512;  // a block's K pieces: [sub-block][piece][lane] of 16 bytes
-  static constexpr int kVBytes = kNB * 4 * kVP * (D >= 128 ? 512 : 256);
+  static constexpr int kKBytes = 2 * kKP * 512;      // a block's K pieces: [piece][lane] of 16 bytes
+  static constexpr int kVBytes = 4 * kVP * (D >= 128 ? 512 : 256);
   static constexpr int kRing = kStages * (kKBytes + kVBytes);  // per warp; then its numerators [row][D]
-  static constexpr int kQBytes = kR * kQStride * 2;
+  static constexpr int kQBytes = kRows * kQStride * 2;
   static constexpr int kOffQ = kWarps * kRing;
   static constexpr int kOffRed = kOffQ + kQBytes;    // per warp and row: maximum, sum; then inverse row scales
   // Cluster: the joined numerators, as float4 items, are owned by its CTAs in
@@ -73,6 +72,14 @@ struct StreamCfg {
   static_assert(kRing >= kRows * D * 4, "a warp's numerators fit its ring");
   static_assert(kRing * kWarps >= kRows * D, "non-finite marks");
 };
+
+// The 8 x 8 matrix of 16-bit elements that the warp holds (row lane/4, columns
+// 2 (lane%4) + {0, 1}), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -111,12 +118,11 @@ __device__ __forceinline__ uint32_t word(const uint4& w, int i) {
   return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
 }
 
-template <int D, int FMT, int DT, bool WIDE>
-__global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
+template <int D, int FMT, int DT, int NQ>
+__global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
     chunk_stream(const __grid_constant__ ChunkParams p, const int clustered) {
-  using C = StreamCfg<D, WIDE>;
-  constexpr int ST = C::kStages, kBlk = C::kBlk, NB = C::kNB;
-  constexpr uint32_t kAll = kBlk == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+  using C = StreamCfg<D, NQ>;
+  constexpr int ST = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
   float* sM = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp][16]
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     return;
   }
 
-  // Places of a block's tokens, one per lane (of 16, both halves of the warp hold
+  // Places of a block's tokens, one per lane (both halves of the warp hold
   // them).  The block id is requested a block before it is needed; the copies
   // are unconditional (tokens without a place read the pool's first row and
   // are masked, V also zeroed).
@@ -177,14 +183,14 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     const int64_t voff = ok ? a.blk * p.vsb + (int64_t)a.slot * p.vst : 0;
     uint8_t* dst = ring + st * (C::kKBytes + C::kVBytes);
 #pragma unroll
-    for (int h = 0; h < 2 * NB; ++h) {
+    for (int h = 0; h < 2; ++h) {
       const uint8_t* src = kbase + __shfl_sync(0xffffffffu, koff, rq + 8 * h);
 #pragma unroll
       for (int i = 0; i < C::kKP; ++i) tc::cp_async16(dst + ((h * C::kKP + i) * 32 + lane) * 16, src + 64 * i);
     }
     dst += C::kKBytes;
 #pragma unroll
-    for (int j = 0; j < 4 * NB; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const uint8_t* src = vbase + __shfl_sync(0xffffffffu, voff, 2 * c + (j & 1) + 8 * (j >> 1));
 #pragma unroll
       for (int i = 0; i < C::kVP; ++i) {
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
           cp_async8(dst + (j * 32 + lane) * 8, src);
       }
     }
-    return __ballot_sync(0xffffffffu, ok) & kAll;
+    return __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
   };
   constexpr int kStep = kBlk * kWarps;  // a warp's blocks are this far apart
   const int t_first = u0 + kBlk * warp;
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
   // RC are zero.  One warp per row; the rows are requested before the first
   // blocks, so that their latencies overlap.
   constexpr int V = D / 32;  // elements per lane
-  constexpr int kQRows = kR / kWarps;
+  constexpr int kQRows = C::kRows / kWarps;
   uint32_t qw[kQRows][V / 2];
   const float ks = p.k_scale_dev ? __ldg(p.k_scale_dev) : p.k_scale;
   const float vs = p.v_scale_dev ? __ldg(p.v_scale_dev) : p.v_scale;
@@ -257,47 +263,53 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
     if (lane == 0) sBack[r] = back;
   }
   __syncthreads();
-  const float c0f = fabsf(cf) * sBack[rq], c1f = fabsf(cf) * sBack[rq + 8];
 
-  // What this lane's two rows see; rows past RC see everything (their values are dropped).
-  ChunkRow row0 = {INT_MAX, INT_MIN}, row1 = {INT_MAX, INT_MIN};
-  if (rq < RC) row0 = chunk_row(p, req, span, token_of(rq));
-  if (rq + 8 < RC) row1 = chunk_row(p, req, span, token_of(rq + 8));
-  const int hi_min = __reduce_min_sync(0xffffffffu, min(row0.hi, row1.hi));
-  const int lo_max = __reduce_max_sync(0xffffffffu, max(row0.lo, row1.lo));
-
-  // Q's A fragments: step (i, w) covers d = 16 (c + 4 i) + 4 w + {0..3} of lane c
-  auto q_frag = [&](int i, int w, uint32_t (&a)[4]) {
-    const int d = (c + 4 * i) * 16 + 4 * w;
-    const uint2 x = *reinterpret_cast<const uint2*>(sQ + rq * C::kQStride + d);
-    a[0] = x.x;
-    a[2] = x.y;
-    if (WIDE) {
-      const uint2 y = *reinterpret_cast<const uint2*>(sQ + (rq + 8) * C::kQStride + d);
-      a[1] = y.x;
-      a[3] = y.y;
-    } else {
-      a[1] = a[3] = 0u;
+  // This lane's query vectors 8 n + 2 c + e: logit factors and what they see;
+  // vectors past RC see everything (their values are dropped).
+  float cq[NQ][2];
+  ChunkRow row[NQ][2];
+  int hi_min = INT_MAX, lo_max = INT_MIN;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * c + e;
+      cq[n][e] = fabsf(cf) * sBack[r];
+      row[n][e] = {INT_MAX, INT_MIN};
+      if (r < RC) row[n][e] = chunk_row(p, req, span, token_of(r));
+      hi_min = min(hi_min, row[n][e].hi);
+      lo_max = max(lo_max, row[n][e].lo);
     }
+  hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+  lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+
+  // Q's B fragments: step (i, w) covers d = 16 (c + 4 i) + 4 w + {0..3} of lane c
+  auto q_frag = [&](int n, int i, int w) {
+    return *reinterpret_cast<const uint2*>(sQ + (8 * n + rq) * C::kQStride + (c + 4 * i) * 16 + 4 * w);
   };
-  uint32_t qa[C::kQRegs ? D / 16 : 1][4];
+  uint2 qb[NQ][C::kQRegs ? D / 16 : 1];
   if (C::kQRegs) {
 #pragma unroll
-    for (int i = 0; i < C::kKP; ++i)
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) q_frag(i, w, qa[C::kQRegs ? i * 4 + w : 0]);
+      for (int i = 0; i < C::kKP; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) qb[n][C::kQRegs ? i * 4 + w : 0] = q_frag(n, i, w);
   }
 
-  float o[C::kNT][4];
-  float m0, m1, l0, l1;
-  float4 acc[C::kIter];  // after the join: numerators of this thread's items, their rows' maxima and sums
+  float o[D / 16][NQ][4];         // O^T: d tiles of 16
+  float m[NQ][2], l[NQ][2];       // running maxima (whole numbers, base 2); sums over this lane's tokens
+  float4 acc[C::kIter];           // after the join: numerators of this thread's items, their rows' maxima and sums
   float Ms[C::kIter], Ls[C::kIter];
-  bool zap = false;  // second pass: non-finite V codes enter as 0
+  bool zap = false;               // second pass: non-finite V codes enter as 0
   while (true) {
 #pragma unroll
-    for (int n = 0; n < C::kNT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    m0 = m1 = kNoMax;
-    l0 = l1 = 0.f;
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+      m[n][0] = m[n][1] = kNoMax;
+      l[n][0] = l[n][1] = 0.f;
+    }
     int st = 0;
     for (int t = t_first; t < u1; t += kStep) {
       // the block ST - 1 ahead goes where the block before this one was
@@ -314,165 +326,161 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
       const uint32_t valid = there[0];
 #pragma unroll
       for (int i = 0; i + 1 < ST; ++i) there[i] = there[i + 1];
-      float sc[2 * NB][4];  // [half sub-block]: 8 tokens
+      // S^T: tokens rq, rq + 8 by vectors 8 n + 2 c + {0, 1}, in two chains each
+      float sc[NQ][2][4];
 #pragma unroll
-      for (int h = 0; h < 2 * NB; ++h) sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sc[n][k][0] = sc[n][k][1] = sc[n][k][2] = sc[n][k][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < C::kKP; ++i) {
-        uint4 kr[2 * NB];
-#pragma unroll
-        for (int h = 0; h < 2 * NB; ++h) kr[h] = *reinterpret_cast<const uint4*>(kst + (h * C::kKP + i) * 512);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kst + i * 512);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(kst + (C::kKP + i) * 512);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a[4];
-          if (!C::kQRegs) q_frag(i, w, a);
+          fp8x4_to_f16<FMT>(word(k0, w), a[0], a[2]);
+          fp8x4_to_f16<FMT>(word(k1, w), a[1], a[3]);
 #pragma unroll
-          for (int h = 0; h < 2 * NB; ++h) {
-            uint32_t b0, b1;
-            fp8x4_to_f16<FMT>(word(kr[h], w), b0, b1);
-            mma16816(sc[h], C::kQRegs ? qa[C::kQRegs ? i * 4 + w : 0] : a, b0, b1);
+          for (int n = 0; n < NQ; ++n) {
+            const uint2 q = C::kQRegs ? qb[n][C::kQRegs ? i * 4 + w : 0] : q_frag(n, i, w);
+            mma16816(sc[n][w & 1], a, q.x, q.y);
           }
         }
       }
-      // base-2 logits; tokens that a row does not see by selection
-      float x0 = -INFINITY, x1 = -INFINITY;
+      // base-2 logits x[n][half][e]; tokens that a vector does not see by selection
+      float x[NQ][2][2];
 #pragma unroll
-      for (int h = 0; h < 2 * NB; ++h)
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[n][h][e] = (sc[n][0][2 * h + e] + sc[n][1][2 * h + e]) * cq[n][e];
+      if (valid != 0xFFFFu || t + kBlk > hi_min || !(t >= lo_max || t + kBlk <= span.sk)) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int k = rq + 8 * h, v = t + k;
+              const bool sees = ((valid >> k) & 1u) && v < row[n][e].hi && (v >= row[n][e].lo || v < span.sk);
+              if (!sees) x[n][h][e] = -INFINITY;
+            }
+      }
+      bool moves = false;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sc[h][e] *= c0f;
-          if (WIDE) sc[h][2 + e] *= c1f;
+          const float y = fmaxf(x[n][0][e], x[n][1][e]);
+          moves |= y > -INFINITY && !(y <= m[n][e] + kChunkTau);
         }
-      if (valid != kAll || t + kBlk > hi_min || !(t >= lo_max || t + kBlk <= span.sk)) {
+      if (__any_sync(0xffffffffu, moves)) {
+        // a vector's running maximum moves (whole numbers: rescaling is exact)
 #pragma unroll
-        for (int h = 0; h < 2 * NB; ++h)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int x = 8 * h + 2 * c + e, v = t + x;
-            const bool ok = (valid >> x) & 1u;
-            if (!(ok && v < row0.hi && (v >= row0.lo || v < span.sk))) sc[h][e] = -INFINITY;
-            if (WIDE && !(ok && v < row1.hi && (v >= row1.lo || v < span.sk))) sc[h][2 + e] = -INFINITY;
-          }
-      }
+            float y = fmaxf(x[n][0][e], x[n][1][e]);
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+            const float mo = m[n][e];
+            const float mn = y > mo + kChunkTau || mo == kNoMax ? fmaxf(mo, ceilf(y)) : mo;
+            const float a = mn == mo ? 1.f : exp2_whole(mo - mn);
+            m[n][e] = mn;
+            l[n][e] *= a;
 #pragma unroll
-      for (int h = 0; h < 2 * NB; ++h) {
-        x0 = fmaxf(fmaxf(x0, sc[h][0]), sc[h][1]);
-        if (WIDE) x1 = fmaxf(fmaxf(x1, sc[h][2]), sc[h][3]);
-      }
-      if (__any_sync(0xffffffffu, (x0 > -INFINITY && !(x0 <= m0 + kChunkTau)) ||
-                                      (x1 > -INFINITY && !(x1 <= m1 + kChunkTau)))) {
-        // a row's running maximum moves (integers: rescaling is exact)
-        float y0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-        y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, 2));
-        float y1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-        y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, 2));
-        const float n0 = y0 > m0 + kChunkTau || m0 == kNoMax ? fmaxf(m0, ceilf(y0)) : m0;
-        const float n1 = y1 > m1 + kChunkTau || m1 == kNoMax ? fmaxf(m1, ceilf(y1)) : m1;
-        const float a0 = n0 == m0 ? 1.f : exp2_whole(m0 - n0), a1 = n1 == m1 ? 1.f : exp2_whole(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= a0;
-        l1 *= a1;
-#pragma unroll
-        for (int n = 0; n < C::kNT; ++n) {
-          o[n][0] *= a0;
-          o[n][1] *= a0;
-          o[n][2] *= WIDE ? a1 : a0;
-          o[n][3] *= WIDE ? a1 : a0;
-        }
-      }
-      const float s0 = (m0 == kNoMax ? 0.f : m0) - kChunkPShift, s1 = (m1 == kNoMax ? 0.f : m1) - kChunkPShift;
-      uint32_t pa[NB][4];
-#pragma unroll
-      for (int h = 0; h < 2 * NB; ++h) {
-        uint32_t* q = &pa[h / 2][2 * (h & 1)];
-        const float p0 = fast_exp2(sc[h][0] - s0), p1 = fast_exp2(sc[h][1] - s0);
-        l0 += p0 + p1;
-        q[0] = pack_half2(p0, p1);
-        if (WIDE) {
-          const float p2 = fast_exp2(sc[h][2] - s1), p3 = fast_exp2(sc[h][3] - s1);
-          l1 += p2 + p3;
-          q[1] = pack_half2(p2, p3);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&q[0]));
-          q[1] = pack_half2((p0 - f.x) * kLoUp, (p1 - f.y) * kLoUp);
-        }
-      }
-#pragma unroll
-      for (int sb = 0; sb < NB; ++sb)
-#pragma unroll
-        for (int i = 0; i < C::kVP; ++i) {
-          uint4 vr[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (D >= 128) {
-              vr[j] = *reinterpret_cast<const uint4*>(vst + ((4 * sb + j) * C::kVP + i) * 512);
-            } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(vst + (4 * sb + j) * 256);
-              vr[j] = make_uint4(y.x, y.y, 0u, 0u);
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][n][e] *= a;
+              o[i][n][2 + e] *= a;
             }
           }
-          if (valid != kAll) {  // 0 * NaN of a token that is not there
+      }
+      uint32_t pb[NQ][2];  // P^T: tokens 2 c + {0, 1} (+ 8) of vector 8 n + rq
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (!((valid >> (16 * sb + 2 * c + (j & 1) + 8 * (j >> 1))) & 1u)) vr[j] = make_uint4(0, 0, 0, 0);
-          }
-          if (zap) {
-            constexpr bool e5 = FMT == FP8KV_KV_E5M2;
+      for (int n = 0; n < NQ; ++n) {
+        const float s0 = (m[n][0] == kNoMax ? 0.f : m[n][0]) - kChunkPShift;
+        const float s1 = (m[n][1] == kNoMax ? 0.f : m[n][1]) - kChunkPShift;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              vr[j] = make_uint4(zap_nonfinite(vr[j].x, e5), zap_nonfinite(vr[j].y, e5), zap_nonfinite(vr[j].z, e5),
-                                 zap_nonfinite(vr[j].w, e5));
-          }
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = fast_exp2(x[n][h][0] - s0), p1 = fast_exp2(x[n][h][1] - s1);
+          l[n][0] += p0;
+          l[n][1] += p1;
+          pb[n][h] = transpose8x8(pack_half2(p0, p1));
+        }
+      }
 #pragma unroll
-          for (int w = 0; w < C::kVWords; ++w) {
-            uint32_t f[2][4];  // [token pair][d of the word]
+      for (int i = 0; i < C::kVP; ++i) {
+        uint4 vr[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t wa = word(vr[2 * j], w), wb = word(vr[2 * j + 1], w);
-              fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[j][0], f[j][1]);
-              fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[j][2], f[j][3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mma16816(o[(i * C::kVWords + w) * 4 + e], pa[sb], f[0][e], f[1][e]);
+        for (int j = 0; j < 4; ++j) {
+          if (D >= 128) {
+            vr[j] = *reinterpret_cast<const uint4*>(vst + (j * C::kVP + i) * 512);
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(vst + j * 256);
+            vr[j] = make_uint4(y.x, y.y, 0u, 0u);
           }
         }
+        if (valid != 0xFFFFu) {  // 0 * NaN of a token that is not there
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((valid >> (2 * c + (j & 1) + 8 * (j >> 1))) & 1u)) vr[j] = make_uint4(0, 0, 0, 0);
+        }
+        if (zap) {
+          constexpr bool e5 = FMT == FP8KV_KV_E5M2;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            vr[j] = make_uint4(zap_nonfinite(vr[j].x, e5), zap_nonfinite(vr[j].y, e5), zap_nonfinite(vr[j].z, e5),
+                               zap_nonfinite(vr[j].w, e5));
+        }
+#pragma unroll
+        for (int w = 0; w < C::kVWords; ++w) {
+          uint32_t f[2][4];  // [token pair][d of the word]
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t wa = word(vr[2 * j], w), wb = word(vr[2 * j + 1], w);
+            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[j][0], f[j][1]);
+            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[j][2], f[j][3]);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t a[4] = {f[0][2 * k], f[0][2 * k + 1], f[1][2 * k], f[1][2 * k + 1]};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) mma16816(o[(i * C::kVWords + w) * 2 + k][n], a, pb[n][0], pb[n][1]);
+          }
+        }
+      }
     }
     cp_wait<0>();
 
     // ---------------------------------------------------------- join the warps
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (c == 0) {
-      sM[warp * 16 + rq] = m0;
-      sL[warp * 16 + rq] = l0;
-      if (WIDE) {
-        sM[warp * 16 + rq + 8] = m1;
-        sL[warp * 16 + rq + 8] = l1;
-      }
-    }
-    // n-tile (i, x) column n of O is d = 128 i + PB n + x, PB the bytes of a V piece
-    constexpr int PB = 4 * C::kVWords;
+    // (lane's vectors 8 n + 2 c + e; d tile (i, w, k) holds d = 128 i + PB rq + 4 w + 2 k + {0, 1})
+    constexpr int PB = 4 * C::kVWords;           // bytes of a V piece
     float* sO = reinterpret_cast<float*>(ring);  // this warp's numerators [row][D]
 #pragma unroll
-    for (int i = 0; i < C::kVP; ++i)
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int x = 0; x < PB; x += 4) {
-          const int d = 128 * i + PB * (2 * c + e) + x;
-          float f[4], h[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[k] = o[i * PB + x + k][e];
-            h[k] = o[i * PB + x + k][2 + e];
-            if (!WIDE) f[k] = fmaf(h[k], kLoDown, f[k]);
-          }
-          *reinterpret_cast<float4*>(sO + rq * D + d) = make_float4(f[0], f[1], f[2], f[3]);
-          if (WIDE) *reinterpret_cast<float4*>(sO + (rq + 8) * D + d) = make_float4(h[0], h[1], h[2], h[3]);
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * c + e;
+        float y = l[n][e];
+        y += __shfl_xor_sync(0xffffffffu, y, 4);
+        y += __shfl_xor_sync(0xffffffffu, y, 8);
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
+        if (rq == 0) {
+          sM[warp * 16 + r] = m[n][e];
+          sL[warp * 16 + r] = y;
         }
+#pragma unroll
+        for (int i = 0; i < C::kVP; ++i)
+#pragma unroll
+          for (int w = 0; w < C::kVWords; ++w) {
+            const float (&lo)[4] = o[(i * C::kVWords + w) * 2][n], (&hi)[4] = o[(i * C::kVWords + w) * 2 + 1][n];
+            *reinterpret_cast<float4*>(sO + r * D + 128 * i + PB * rq + 4 * w) =
+                make_float4(lo[e], lo[2 + e], hi[e], hi[2 + e]);
+          }
+      }
     __syncthreads();
     float bad = 0.f;
 #pragma unroll
@@ -585,10 +593,10 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, WIDE>::kCtas)
   }
 }
 
-template <int D, int FMT, int DT, bool WIDE>
+template <int D, int FMT, int DT, int NQ>
 cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
-  auto fn = chunk_stream<D, FMT, DT, WIDE>;
-  constexpr int smem = StreamCfg<D, WIDE>::kSmem;
+  auto fn = chunk_stream<D, FMT, DT, NQ>;
+  constexpr int smem = StreamCfg<D, NQ>::kSmem;
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
@@ -610,7 +618,7 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
 
 template <int D, int FMT, int DT>
 cudaError_t pick_wide(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
-  return (int64_t)p.max_q * p.G > 8 ? run<D, FMT, DT, true>(plan, p, st) : run<D, FMT, DT, false>(plan, p, st);
+  return (int64_t)p.max_q * p.G > 8 ? run<D, FMT, DT, 2>(plan, p, st) : run<D, FMT, DT, 1>(plan, p, st);
 }
 
 template <int D>

@@ -389,9 +389,8 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  * position 0) yields +0.0, rows of q from cu_q[B] on are left as they are.
  *
  * Numerical contract: FP32 logits, running maximum and sum; probabilities
- * enter the PV product as fp16 (2^-11 of their own value; groups of at most 8
- * query vectors: as two fp16 halves), accumulated in FP32, and a context is
- * split where one FP32 sum would run over more than 32768 positions; one
+ * enter the PV product as fp16 (2^-11 of their own value), accumulated in
+ * FP32, and a context is split where one FP32 sum would run over more than 32768 positions; one
  * rounding to q's type at the end.  bf16 queries are scaled to fp16 per row by
  * a power of two, which is exact for elements above 2^-28 of the row's
  * largest.
