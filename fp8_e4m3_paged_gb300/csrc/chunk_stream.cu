@@ -2,20 +2,19 @@
 // of one KV head times a few new tokens): bound by streaming the cache.
 //
 // One CTA of four warps per (request, KV head, 16 query vectors, partition);
-// each warp walks blocks of 16 virtual tokens (chunk_span) on
-// its own, and the four are joined at the end.  A block's FP8 bytes are
-// requested a block or more ahead by cp.async into places of shared memory
-// that only the requesting lane reads, so the loop has no barrier; each lane
-// asks for the bytes that its MMA fragments hold:
+// each warp walks blocks of 16 virtual tokens (chunk_span) on its own, and the
+// four are joined at the end.  A block's rows are requested one to three
+// blocks ahead by cp.async into the warp's own ring (whole rows per
+// instruction: a copy of half a 128-byte line moves the line), so the loop
+// has no CTA barrier.  Each lane then takes the bytes that its MMA fragments hold:
 //   S^T[16 tokens x 8 vectors] = K . Q^T, m16n8k16: lane (n = lane/4, c =
-//     lane%4) of the A operand needs four d of tokens n and n + 8, so it asks
-//     for the 16-byte pieces c, c + 4, ... of their rows; a 32-bit word of
+//     lane%4) of the A operand needs four d of tokens n and n + 8, so it takes
+//     the 16-byte pieces c, c + 4, ... of their rows; a 32-bit word of
 //     each decodes to one MMA's A fragment, and the d that the words hold are
 //     simply the order in which Q's B fragments are laid out;
 //   O^T[16 d x 8 vectors] += V^T . P^T: an A fragment needs two tokens of one
-//     d in a register, so the lane asks for the same 16-byte piece n of tokens
-//     2c, 2c+1, 2c+8, 2c+9 (a warp reads whole rows) and interleaves their
-//     bytes before the decode; P^T's B fragments are S^T's accumulators,
+//     d in a register, so the lane takes the same 16-byte piece n of tokens
+//     2c, 2c+1, 2c+8, 2c+9 and interleaves their bytes before the decode; P^T's B fragments are S^T's accumulators,
 //     packed to fp16 and transposed 8 by 8 (movmatrix).
 // Tokens and d as the MMA's 16 rows, vectors as its 8 columns: a decode step's
 // 1 to 8 vectors waste no rows, which halves the MMAs and O's registers
@@ -56,12 +55,13 @@ struct StreamCfg {
   static constexpr bool kQRegs = D * NQ <= 256;      // Q's fragments stay in registers
   static constexpr int kCtas = D == 256 ? 2 : D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 5 : 4);  // resident per SM
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // blocks of a warp in flight or in use
-  static constexpr int kKBytes = 2 * kKP * 512;      // a block's K pieces: [piece][lane] of 16 bytes
-  static constexpr int kVBytes = 4 * kVP * (D >= 128 ? 512 : 256);
-  static constexpr int kRing = kStages * (kKBytes + kVBytes);  // per warp; then its numerators [row][D]
+  static constexpr int kCh = D / 16;                 // 16-byte pieces of a row, lanes that copy it
+  static constexpr int kRowsIt = 32 / kCh;           // rows that the warp copies at a time
+  static constexpr int kRowBytes = kBlk * D;         // a block's K (V) rows
+  static constexpr int kRing = kStages * 2 * kRowBytes;  // per warp; then its numerators [row][D]
   static constexpr int kQBytes = kRows * kQStride * 2;
   static constexpr int kOffQ = kWarps * kRing;
-  static constexpr int kOffRed = kOffQ + kQBytes;    // per warp and row: maximum, sum; then inverse row scales
+  static constexpr int kOffRed = kOffQ + kQBytes;    // per warp: rows' maxima and sums; then inverse row scales
   // Cluster: the joined numerators, as float4 items, are owned by its CTAs in
   // equal runs; an owner receives every partition's items and (maximum, sum) pairs here.
   static constexpr int kItems = kRows * D / 4;
@@ -88,9 +88,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp_async8(void* dst_smem, const void* src_gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst_smem)), "l"(src_gmem) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -125,9 +122,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   constexpr int ST = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
-  float* sM = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp][16]
-  float* sL = sM + kWarps * 16;
-  float* sBack = sL + kWarps * 16;                          // [16] inverse row scales
+  float* sML = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp]: 16 maxima, then 16 sums
+  float* sBack = sML + 2 * kWarps * 16;                      // [16] inverse row scales
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
@@ -158,9 +154,13 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   // them).  The block id is requested a block before it is needed; the copies
   // are unconditional (tokens without a place read the pool's first row and
   // are masked, V also zeroed).
-  const uint8_t* kbase = p.k_cache + g * p.ksh + c * 16;
-  const uint8_t* vbase = p.v_cache + g * p.vsh + rq * (D >= 128 ? 16 : 8);
+  const uint8_t* kbase = p.k_cache + g * p.ksh + (lane % C::kCh) * 16;
+  const uint8_t* vbase = p.v_cache + g * p.vsh + (lane % C::kCh) * 16;
   uint8_t* ring = smem + warp * C::kRing;
+  // offsets of a block's rows, where the warp's own maxima and sums go after its
+  // loop (a warp that is done must not touch the others' places)
+  int64_t* place = reinterpret_cast<int64_t*>(sML + warp * 32);
+  static_assert(kBlk * 8 == 32 * 4, "one in place of the other");
   struct Ask {
     int blk, slot;
     bool in;
@@ -175,29 +175,29 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
     }
     return a;
   };
+  // K is read by 2 tokens x 4 pieces at a time, V by 4 even (or odd) tokens x 2
+  // pieces (of 8 bytes for D = 64).
+  auto k_swz = [](int r) { return D >= 128 ? 4 * (r & 1) : 0; };
+  auto v_swz = [](int r) { return D >= 128 ? 2 * ((r >> 1) & 3) : (r >> 1) & 3; };
   // Copies of the block asked for into stage `st`; returns the tokens that are there.
   auto request = [&](const Ask& a, int st) {
     const bool ok = a.blk >= 0 && a.blk < p.num_kv_blocks;
     if (a.in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
     const int64_t koff = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
     const int64_t voff = ok ? a.blk * p.vsb + (int64_t)a.slot * p.vst : 0;
-    uint8_t* dst = ring + st * (C::kKBytes + C::kVBytes);
+    // 16-byte piece i of row r goes to position i ^ swz(r), so that the reads
+    // below find eight different banks
+    uint8_t* dst = ring + st * 2 * C::kRowBytes;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* src = kbase + __shfl_sync(0xffffffffu, koff, rq + 8 * h);
+    for (int kv = 0; kv < 2; ++kv) {
+      __syncwarp();  // (the first also ends the reads of this stage)
+      if (lane < kBlk) place[lane] = kv == 0 ? koff : voff;
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < C::kKP; ++i) tc::cp_async16(dst + ((h * C::kKP + i) * 32 + lane) * 16, src + 64 * i);
-    }
-    dst += C::kKBytes;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint8_t* src = vbase + __shfl_sync(0xffffffffu, voff, 2 * c + (j & 1) + 8 * (j >> 1));
-#pragma unroll
-      for (int i = 0; i < C::kVP; ++i) {
-        if (D >= 128)
-          tc::cp_async16(dst + ((j * C::kVP + i) * 32 + lane) * 16, src + 128 * i);
-        else
-          cp_async8(dst + (j * 32 + lane) * 8, src);
+      for (int it = 0; it < kBlk / C::kRowsIt; ++it) {
+        const int r = it * C::kRowsIt + lane / C::kCh, swz = kv == 0 ? k_swz(r) : v_swz(r);
+        tc::cp_async16(dst + kv * C::kRowBytes + r * D + (((lane % C::kCh) ^ swz) * 16),
+                       (kv == 0 ? kbase : vbase) + place[r]);
       }
     }
     return __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       }
       cp_commit();
       cp_wait<ST - 1>();
-      const uint8_t* kst = ring + st * (C::kKBytes + C::kVBytes) + lane * 16;
-      const uint8_t* vst = ring + st * (C::kKBytes + C::kVBytes) + C::kKBytes + lane * (D >= 128 ? 16 : 8);
+      __syncwarp();
+      const uint8_t* krows = ring + st * 2 * C::kRowBytes;
+      const uint8_t* vrows = krows + C::kRowBytes;
       st = st + 1 == ST ? 0 : st + 1;
       const uint32_t valid = there[0];
 #pragma unroll
@@ -334,8 +335,10 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
         for (int k = 0; k < 2; ++k) sc[n][k][0] = sc[n][k][1] = sc[n][k][2] = sc[n][k][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < C::kKP; ++i) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(kst + i * 512);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(kst + (C::kKP + i) * 512);
+        // (rows rq and rq + 8 have the same swizzle)
+        const uint8_t* at = krows + rq * D + (((c + 4 * i) ^ k_swz(rq)) * 16);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(at);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(at + 8 * D);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a[4];
@@ -416,10 +419,11 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
         uint4 vr[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          const int r = 2 * c + (j & 1) + 8 * (j >> 1);
           if (D >= 128) {
-            vr[j] = *reinterpret_cast<const uint4*>(vst + (j * C::kVP + i) * 512);
+            vr[j] = *reinterpret_cast<const uint4*>(vrows + r * D + (((rq + 8 * i) ^ v_swz(r)) * 16));
           } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(vst + j * 256);
+            const uint2 y = *reinterpret_cast<const uint2*>(vrows + r * D + (((rq >> 1) ^ v_swz(r)) * 16) + (rq & 1) * 8);
             vr[j] = make_uint4(y.x, y.y, 0u, 0u);
           }
         }
@@ -469,8 +473,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
         y += __shfl_xor_sync(0xffffffffu, y, 8);
         y += __shfl_xor_sync(0xffffffffu, y, 16);
         if (rq == 0) {
-          sM[warp * 16 + r] = m[n][e];
-          sL[warp * 16 + r] = y;
+          sML[warp * 32 + r] = m[n][e];
+          sML[warp * 32 + 16 + r] = y;
         }
 #pragma unroll
         for (int i = 0; i < C::kVP; ++i)
@@ -492,10 +496,10 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       Ms[k] = kNoMax;
       if (r >= RC) continue;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) Ms[k] = fmaxf(Ms[k], sM[w * 16 + r]);
+      for (int w = 0; w < kWarps; ++w) Ms[k] = fmaxf(Ms[k], sML[w * 32 + r]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = sM[w * 16 + r], lw = sL[w * 16 + r];
+        const float mw = sML[w * 32 + r], lw = sML[w * 32 + 16 + r];
         const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem + w * C::kRing) + r * D + d);
         // (a warp that saw nothing has a sum of 0 and numerators of 0)
         const float a = mw == Ms[k] ? 1.f : exp2_whole(mw - Ms[k]);
