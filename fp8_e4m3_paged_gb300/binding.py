@@ -555,7 +555,7 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
 
 
 def fp8kv_attn_chunk(plan: ChunkPlan, args: ChunkArgs, stream: int = 0) -> None:
-    rc = lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(args), ctypes.c_void_p(stream))
+    rc = lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(args), stream)
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_chunk")
 
@@ -611,7 +611,7 @@ def make_cache_read_args(*, k_cache, v_cache, block_table, cu_len, k_out, v_out,
 
 
 def fp8kv_attn_cache_read(args: CacheReadArgs, stream: int = 0) -> None:
-    rc = lib.fp8kv_attn_cache_read(ctypes.byref(args), ctypes.c_void_p(stream))
+    rc = lib.fp8kv_attn_cache_read(ctypes.byref(args), stream)
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_cache_read")
 
@@ -642,6 +642,6 @@ def make_calibrate_args(*, k, v, k_scale, v_scale, slot_mapping=None, kv_format:
 
 
 def fp8kv_attn_cache_calibrate(args: CalibrateArgs, stream: int = 0) -> None:
-    rc = lib.fp8kv_attn_cache_calibrate(ctypes.byref(args), ctypes.c_void_p(stream))
+    rc = lib.fp8kv_attn_cache_calibrate(ctypes.byref(args), stream)
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_cache_calibrate")

@@ -23,8 +23,10 @@
 namespace fp8kv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kBatch = 8;  // 16-byte pieces in flight per thread
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // 16-byte pieces in flight per thread
+
+__device__ const int64_t kNoSlots = 0;  // the slot of every token when there is no mapping
 
 template <int DT>
 __device__ __forceinline__ uint32_t mag_max(uint32_t m, uint32_t w, bool finite_only) {
@@ -46,25 +48,31 @@ __global__ void __launch_bounds__(kThreads) calibrate_kernel(const fp8kv_calibra
   const int64_t st = is_v ? a.v_stride_token : a.k_stride_token, sh = is_v ? a.v_stride_head : a.k_stride_head;
   const int per_head = a.head_dim / 8, per_token = a.num_kv_heads * per_head;
   const int64_t total = (int64_t)a.num_tokens * per_token;
-  const int64_t step = (int64_t)gridDim.x * kThreads;
   uint32_t best = 0u;
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kBatch * step) {
+  // a CTA takes runs of kBatch * kThreads pieces
+  for (int64_t i0 = (int64_t)blockIdx.x * (kBatch * kThreads) + threadIdx.x; i0 < total;
+       i0 += (int64_t)gridDim.x * (kBatch * kThreads)) {
     uint4 w[kBatch];
+    int64_t slot[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int64_t i = i0 + j * step;
-      w[j] = make_uint4(0, 0, 0, 0);
-      if (i >= total) continue;
+      // past the last: the last once more (a load under a condition is waited for on the spot)
+      const int64_t i = min(i0 + j * kThreads, total - 1);
       const uint16_t* at;
       if (PACKED) {
         at = src + i * 8;
       } else {
         const int64_t n = i / per_token;
-        if (a.slot_mapping && __ldg(a.slot_mapping + n) < 0) continue;
+        slot[j] = __ldg((a.slot_mapping ? a.slot_mapping : &kNoSlots) + (a.slot_mapping ? n : 0));
         const int rem = (int)(i - n * per_token), h = rem / per_head;
         at = src + n * st + h * sh + (rem - h * per_head) * 8;
       }
-      w[j] = __ldg(reinterpret_cast<const uint4*>(at));
+      w[j] = __ldcs(reinterpret_cast<const uint4*>(at));
+    }
+    if (!PACKED) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (slot[j] < 0) w[j] = make_uint4(0, 0, 0, 0);
     }
     uint32_t m = 0u;
 #pragma unroll
@@ -76,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) calibrate_kernel(const fp8kv_calibra
     }
     if ((m & 0xFFFFu) >= kInf || (m >> 16) >= kInf) {
       m = 0u;
-#pragma unroll 1
+#pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         m = mag_max<DT>(m, w[j].x, true);
         m = mag_max<DT>(m, w[j].y, true);
@@ -105,25 +113,29 @@ __global__ void __launch_bounds__(kThreads) calibrate_kernel(const fp8kv_calibra
 
 }  // namespace
 
-cudaError_t launch_calibrate(const fp8kv_calibrate_args& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+namespace {
+
+template <int DT, bool PACKED>
+cudaError_t run(const fp8kv_calibrate_args& a, int64_t total, cudaStream_t st) {
+  static ResidentCtas resident;
+  int cap = 0;
+  const cudaError_t e = resident.get(calibrate_kernel<DT, PACKED>, kThreads, &cap);
   if (e != cudaSuccess) return e;
+  const int64_t need = (total + kBatch * kThreads - 1) / (kBatch * kThreads), half = (cap + 1) / 2;
+  calibrate_kernel<DT, PACKED><<<dim3((unsigned)(need < half ? need : half), 2), kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_calibrate(const fp8kv_calibrate_args& a, cudaStream_t st) {
   // rows that lie side by side need no index arithmetic
-  const int64_t D = a.head_dim, row = D * a.num_kv_heads;
+  const int64_t D = a.head_dim, row = D * a.num_kv_heads, total = (int64_t)a.num_tokens * row / 8;
   const bool packed = !a.slot_mapping && a.k_stride_head == D && a.v_stride_head == D && a.k_stride_token == row &&
                       a.v_stride_token == row;
-  void (*fn)(const fp8kv_calibrate_args);
   if (a.dtype == FP8KV_DTYPE_F16)
-    fn = packed ? calibrate_kernel<FP8KV_DTYPE_F16, true> : calibrate_kernel<FP8KV_DTYPE_F16, false>;
-  else
-    fn = packed ? calibrate_kernel<FP8KV_DTYPE_BF16, true> : calibrate_kernel<FP8KV_DTYPE_BF16, false>;
-  const int64_t total = (int64_t)a.num_tokens * row / 8;
-  const int64_t need = (total + kThreads - 1) / kThreads;
-  const int64_t cap = (int64_t)sms * 2;  // with two streams: 4 CTAs of 512 threads per SM
-  fn<<<dim3((unsigned)(need < cap ? need : cap), 2), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+    return packed ? run<FP8KV_DTYPE_F16, true>(a, total, st) : run<FP8KV_DTYPE_F16, false>(a, total, st);
+  return packed ? run<FP8KV_DTYPE_BF16, true>(a, total, st) : run<FP8KV_DTYPE_BF16, false>(a, total, st);
 }
 
 }  // namespace fp8kv

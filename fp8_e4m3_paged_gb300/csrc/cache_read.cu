@@ -4,9 +4,12 @@
 //
 // dec() is exact in fp16, the product is one FP32 rounding, the output type a
 // second one (none for FP32).  Bound by HBM: one byte in and 2 or 4 out per
-// element.  A CTA takes a run of output rows; its first threads find each
-// row's request (binary search of cu_len) and place once, then
-// all threads move 16-byte pieces, K and V of the same place together.
+// element.  Resident CTAs walk tiles of output rows; each row's request
+// (binary search of cu_len) and place is found by one thread, for the next
+// tile while the current tile's bytes are on their way, so that the chain of dependent
+// loads costs nothing.  All threads then move items of 16 output bytes (8 or 4
+// elements), K and V of the same place together: a store instruction of 16
+// bytes out of every 32 would write half sectors.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -20,76 +23,82 @@ namespace fp8kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;               // 16-byte pieces per thread and stream
-constexpr int kMaxRows = kThreads;      // rows of a CTA
+constexpr int kItems = 4;               // items per thread and stream in flight
+constexpr int kMaxRows = kThreads;      // rows of a tile
 
-// 16 FP8 bytes * scale -> 16 output elements.
+// The FP8 bytes of one item (8 for the 16-bit types, 4 for FP32).
+template <int DT>
+struct Item {
+  using Bytes = uint2;
+};
+template <>
+struct Item<FP8KV_DTYPE_F32> {
+  using Bytes = uint32_t;
+};
+
+template <int FMT>
+__device__ __forceinline__ void scaled4(uint32_t w, float scale, float (&f)[4]) {
+  uint32_t lo, hi;
+  fp8x4_to_f16<FMT>(w, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+  f[0] = a.x * scale;
+  f[1] = a.y * scale;
+  f[2] = b.x * scale;
+  f[3] = b.y * scale;
+}
+
+// FP8 bytes * scale -> 16 bytes of output elements.
 template <int DT, int FMT>
-__device__ __forceinline__ void expand16(const uint4& w, float scale, void* dst) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  float f[16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t lo, hi;
-    fp8x4_to_f16<FMT>(in[j], lo, hi);
-    const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-    f[4 * j] = a.x * scale;
-    f[4 * j + 1] = a.y * scale;
-    f[4 * j + 2] = b.x * scale;
-    f[4 * j + 3] = b.y * scale;
-  }
+__device__ __forceinline__ uint4 expand(const typename Item<DT>::Bytes& w, float scale) {
+  float f[4];
   if constexpr (DT == FP8KV_DTYPE_F32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      reinterpret_cast<float4*>(dst)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+    scaled4<FMT>(w, scale, f);
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      reinterpret_cast<uint4*>(dst)[j] =
-          make_uint4(pack_out<DT>(f[8 * j], f[8 * j + 1]), pack_out<DT>(f[8 * j + 2], f[8 * j + 3]),
-                     pack_out<DT>(f[8 * j + 4], f[8 * j + 5]), pack_out<DT>(f[8 * j + 6], f[8 * j + 7]));
+    float g[4];
+    scaled4<FMT>(w.x, scale, f);
+    scaled4<FMT>(w.y, scale, g);
+    return make_uint4(pack_out<DT>(f[0], f[1]), pack_out<DT>(f[2], f[3]), pack_out<DT>(g[0], g[1]),
+                      pack_out<DT>(g[2], g[3]));
   }
 }
 
-template <int DT, int FMT>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const fp8kv_cache_read_args a, int rows_per_cta) {
-  constexpr int ES = DT == FP8KV_DTYPE_F32 ? 4 : 2;
-  __shared__ int64_t s_k[kMaxRows], s_v[kMaxRows];  // byte offset of the row, -1 bad place, -2 not written
-  const int tid = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * rows_per_cta;
-  const int n = (int)min((int64_t)rows_per_cta, a.total - row0);
-  if (tid < n) {
-    const int row = (int)row0 + tid;
-    // the last request that begins at or below the row
-    int lo = 0, hi = a.batch;  // cu_len[lo] <= row < cu_len[hi], if the row is covered
-    const int first = __ldg(a.cu_len), last = __ldg(a.cu_len + a.batch);
-    int64_t ko = -2, vo = -2;
-    if (row >= first && row < last) {
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu_len + mid) <= row)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int c0 = __ldg(a.cu_len + lo);
-      const int64_t t = (int64_t)row - c0 + (a.start ? __ldg(a.start + lo) : 0);
-      ko = vo = -1;
-      if (t >= 0 && t < (int64_t)a.max_blocks * a.page_size) {
-        const int64_t page = t / a.page_size;
-        const int slot = (int)(t - page * a.page_size);
-        const int64_t blk = __ldg(a.block_table + lo * a.block_table_stride + page);
-        if (blk >= 0 && blk < a.num_kv_blocks) {
-          ko = blk * a.kc_stride_block + slot * a.kc_stride_token;
-          vo = blk * a.vc_stride_block + slot * a.vc_stride_token;
-        }
-      }
-      if (ko == -1 && a.status) set_status(a.status, FP8KV_STATUS_BAD_BLOCK);
-    }
-    s_k[tid] = ko;
-    s_v[tid] = vo;
+// Byte offsets (K, V) of an output row's source: -1 no place (a zero row), -2
+// not covered by any request (not written).
+__device__ __forceinline__ void find_row(const fp8kv_cache_read_args& a, int row, int64_t& ko, int64_t& vo) {
+  ko = vo = -2;
+  const int first = __ldg(a.cu_len), last = __ldg(a.cu_len + a.batch);
+  if (row < first || row >= last) return;
+  // the last request that begins at or below the row
+  int lo = 0, hi = a.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu_len + mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
   }
+  const int64_t t = (int64_t)row - __ldg(a.cu_len + lo) + (a.start ? __ldg(a.start + lo) : 0);
+  ko = vo = -1;
+  if (t >= 0 && t < (int64_t)a.max_blocks * a.page_size) {
+    const int page = (int)(t / a.page_size), slot = (int)(t - (int64_t)page * a.page_size);
+    const int64_t blk = __ldg(a.block_table + lo * a.block_table_stride + page);
+    if (blk >= 0 && blk < a.num_kv_blocks) {
+      ko = blk * a.kc_stride_block + slot * a.kc_stride_token;
+      vo = blk * a.vc_stride_block + slot * a.vc_stride_token;
+    }
+  }
+  if (ko == -1 && a.status) set_status(a.status, FP8KV_STATUS_BAD_BLOCK);
+}
+
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_constant__ fp8kv_cache_read_args a,
+                                                              int rows_per_tile) {
+  using Bytes = typename Item<DT>::Bytes;
+  constexpr int E = sizeof(Bytes), ES = 16 / E;  // elements of an item, bytes of one
+  __shared__ int64_t s_k[2][kMaxRows], s_v[2][kMaxRows];
+  const int tid = threadIdx.x;
   if (blockIdx.x == 0 && a.status) {
     // one CTA checks the lengths; whatever they are, rows stay in [0, total)
     for (int i = tid; i <= a.batch; i += kThreads) {
@@ -99,63 +108,86 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const fp8kv_cache_
   }
   const float ks = a.k_scale_dev ? *a.k_scale_dev : a.k_scale;
   const float vs = a.v_scale_dev ? *a.v_scale_dev : a.v_scale;
+  const int per_head = a.head_dim / E, per_row = a.num_kv_heads * per_head;
+  const int64_t step = (int64_t)gridDim.x * rows_per_tile;
+  auto place = [&](int64_t row0, int buf) {
+    if (tid < rows_per_tile && row0 + tid < a.total) find_row(a, (int)(row0 + tid), s_k[buf][tid], s_v[buf][tid]);
+  };
+  int64_t row0 = (int64_t)blockIdx.x * rows_per_tile;
+  place(row0, 0);
   __syncthreads();
-  const int per_head = a.head_dim / 16, per_row = a.num_kv_heads * per_head;
-  const int64_t items = (int64_t)n * per_row;
-  for (int64_t i0 = tid; i0 < items; i0 += kItems * kThreads) {
-    uint4 kx[kItems], vx[kItems];
-    int row[kItems], h[kItems], c[kItems];
+  for (int buf = 0; row0 < a.total; row0 += step, buf ^= 1) {
+    const int n = (int)min((int64_t)rows_per_tile, a.total - row0);
+    const int64_t items = (int64_t)n * per_row;
+    bool placed = false;
+    for (int64_t i0 = 0; i0 < items; i0 += kItems * kThreads) {
+      Bytes kx[kItems], vx[kItems];
+      int row[kItems], h[kItems], c[kItems];
 #pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      const int64_t i = i0 + j * kThreads;
-      row[j] = -1;
-      if (i >= items) continue;
-      row[j] = (int)(i / per_row);
-      const int rem = (int)(i - (int64_t)row[j] * per_row);
-      h[j] = rem / per_head;
-      c[j] = rem - h[j] * per_head;
-      const int64_t ko = s_k[row[j]], vo = s_v[row[j]];
-      kx[j] = vx[j] = make_uint4(0, 0, 0, 0);
-      if (ko == -2) row[j] = -1;
-      if (ko >= 0) {
-        kx[j] = __ldcs(reinterpret_cast<const uint4*>(a.k_cache + ko + h[j] * a.kc_stride_head + c[j] * 16));
-        vx[j] = __ldcs(reinterpret_cast<const uint4*>(a.v_cache + vo + h[j] * a.vc_stride_head + c[j] * 16));
+      for (int j = 0; j < kItems; ++j) {
+        const int64_t i = min(i0 + j * kThreads + tid, items - 1);  // past the last: read again, not written
+        row[j] = (int)(i / per_row);
+        const int rem = (int)(i - (int64_t)row[j] * per_row);
+        h[j] = rem / per_head;
+        c[j] = rem - h[j] * per_head;
+        // rows without a place read the pool's first one (a load under a condition is waited for on the spot)
+        const int64_t ko = max(s_k[buf][row[j]], (int64_t)0), vo = max(s_v[buf][row[j]], (int64_t)0);
+        kx[j] = __ldcs(reinterpret_cast<const Bytes*>(a.k_cache + ko + h[j] * a.kc_stride_head + c[j] * E));
+        vx[j] = __ldcs(reinterpret_cast<const Bytes*>(a.v_cache + vo + h[j] * a.vc_stride_head + c[j] * E));
+      }
+      if (!placed) place(row0 + step, buf ^ 1);
+      placed = true;
+#pragma unroll
+      for (int j = 0; j < kItems; ++j) {
+        const int64_t at = s_k[buf][row[j]];
+        if (at == -2 || i0 + j * kThreads + tid >= items) continue;
+        const bool gone = at < 0;  // +0.0 whatever the scale's sign
+        if (gone) kx[j] = vx[j] = Bytes{};
+        const int64_t r = row0 + row[j];
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.k_out) +
+                                        (r * a.ko_stride_token + h[j] * a.ko_stride_head + c[j] * E) * ES),
+               expand<DT, FMT>(kx[j], gone ? 1.f : ks));
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.v_out) +
+                                        (r * a.vo_stride_token + h[j] * a.vo_stride_head + c[j] * E) * ES),
+               expand<DT, FMT>(vx[j], gone ? 1.f : vs));
       }
     }
-#pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-      if (row[j] < 0) continue;
-      const bool gone = s_k[row[j]] < 0;  // +0.0 whatever the scale's sign
-      const int64_t r = row0 + row[j];
-      expand16<DT, FMT>(kx[j], gone ? 1.f : ks,
-                        reinterpret_cast<uint8_t*>(a.k_out) +
-                            (r * a.ko_stride_token + h[j] * a.ko_stride_head + c[j] * 16) * ES);
-      expand16<DT, FMT>(vx[j], gone ? 1.f : vs,
-                        reinterpret_cast<uint8_t*>(a.v_out) +
-                            (r * a.vo_stride_token + h[j] * a.vo_stride_head + c[j] * 16) * ES);
-    }
+    __syncthreads();
   }
 }
 
 }  // namespace
 
-cudaError_t launch_cache_read(const fp8kv_cache_read_args& a, cudaStream_t st) {
-  constexpr int E4 = FP8KV_KV_E4M3, E5 = FP8KV_KV_E5M2;
-  constexpr int F16 = FP8KV_DTYPE_F16, BF16 = FP8KV_DTYPE_BF16, F32 = FP8KV_DTYPE_F32;
-  void (*fn)(const fp8kv_cache_read_args, int);
-  const bool e5 = a.kv_format == E5;
-  if (a.dtype == F16)
-    fn = e5 ? cache_read_kernel<F16, E5> : cache_read_kernel<F16, E4>;
-  else if (a.dtype == BF16)
-    fn = e5 ? cache_read_kernel<BF16, E5> : cache_read_kernel<BF16, E4>;
-  else
-    fn = e5 ? cache_read_kernel<F32, E5> : cache_read_kernel<F32, E4>;
-  const int64_t per_row = (int64_t)a.num_kv_heads * (a.head_dim / 16);
+namespace {
+
+template <int DT, int FMT>
+cudaError_t run(const fp8kv_cache_read_args& a, cudaStream_t st) {
+  static ResidentCtas resident;
+  int cap = 0;
+  const cudaError_t e = resident.get(cache_read_kernel<DT, FMT>, kThreads, &cap);
+  if (e != cudaSuccess) return e;
+  constexpr int E = sizeof(typename Item<DT>::Bytes);
+  const int64_t per_row = (int64_t)a.num_kv_heads * (a.head_dim / E);
   int64_t rows = kItems * kThreads / per_row;  // one pass of the CTA
   rows = rows < 1 ? 1 : rows > kMaxRows ? kMaxRows : rows;
-  const int64_t grid = (a.total + rows - 1) / rows;
-  fn<<<(unsigned)grid, kThreads, 0, st>>>(a, (int)rows);
+  const int64_t tiles = (a.total + rows - 1) / rows;
+  cache_read_kernel<DT, FMT><<<(unsigned)(tiles < cap ? tiles : cap), kThreads, 0, st>>>(a, (int)rows);
   return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t pick(const fp8kv_cache_read_args& a, cudaStream_t st) {
+  return a.kv_format == FP8KV_KV_E5M2 ? run<DT, FP8KV_KV_E5M2>(a, st) : run<DT, FP8KV_KV_E4M3>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_read(const fp8kv_cache_read_args& a, cudaStream_t st) {
+  switch (a.dtype) {
+    case FP8KV_DTYPE_F16: return pick<FP8KV_DTYPE_F16>(a, st);
+    case FP8KV_DTYPE_BF16: return pick<FP8KV_DTYPE_BF16>(a, st);
+    default: return pick<FP8KV_DTYPE_F32>(a, st);
+  }
 }
 
 }  // namespace fp8kv

@@ -92,6 +92,28 @@ struct DeviceOnce {
   }
 };
 
+// CTAs of a kernel that are resident on the current device at a time, asked
+// for once per device.
+struct ResidentCtas {
+  std::atomic<int> ctas[64] = {};
+  template <class F>
+  cudaError_t get(F fn, int threads, int* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>& n = ctas[dev & 63];
+    *out = n.load(std::memory_order_relaxed);
+    if (*out) return cudaSuccess;
+    int sms = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, 0);
+    if (e != cudaSuccess) return e;
+    *out = sms * (per_sm > 0 ? per_sm : 1);
+    n.store(*out, std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+};
+
 // Shared-memory bytes of the generic split kernel for a head dim and row chunk.
 int generic_smem_bytes(int D, int row_chunk);
 
