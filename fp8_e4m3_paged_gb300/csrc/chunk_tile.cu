@@ -13,12 +13,27 @@
 //   warps 8-11       decode K and V (D = 256: V): FP8 rows, requested one tile
 //                    ahead into registers, to swizzled fp16 operand tiles.
 // Per tile j and row tile q:  S_q = Q_q . K_j^T (M 128, N 128),
-// P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM),
-// P and PV by halves of 64 positions, so that the first half's PV runs under
-// the second half's exponentials.  Two row tiles alternate: while one's
-// softmax runs, the tensor core works on the other's S and O.  For D = 256
-// two S buffers of the one row tile do the same: QK of tile j+1 is issued between
-// the halves of PV(j).
+// P_q = 2^(s - m + 7) as fp16 over S_q in TMEM, O_q += P_q . V_j (A from TMEM).
+// Two row tiles alternate: while one's softmax runs, the tensor core works on
+// the other's PV(j) and QK(j+1), issued together.  For D = 256 two S buffers of the
+// one row tile do the same: QK of tile j+1 is issued between the halves (64
+// positions each) of PV(j).
+//
+// What bounds it: the four phases of a tile (decode, QK, softmax, PV) share an
+// SM's issue slots and shared memory.  Per tile of 256 x 128 (D 128) the UMMAs take
+// 2048 cycles; the exponentials, the conversions and the decode about 2000 issue
+// cycles per scheduler, and operand reads, decode stores and Q/P traffic 2300
+// shared-memory cycles; together they run in 3400 to 3600.  32 heads over 8, D 128,
+// 2048 queries on 30000 cached positions: 884 us, 1178 TFLOP/s (the FP16 dense rate
+// would take 537); 8192 queries with window 1024: 191 us, of which a CTA's
+// start and end (about 13 us: Q, the first rows, the output) are the
+// larger part of what lies above the tensor time.
+// Measured and not taken: 16 warps of 128 registers with K and V decoded by four
+// warps each (984 us where this took 955), the same split by setmaxnreg (1076 and
+// more), row tiles in strict turns (955 to 978), a running maximum one tile late
+// (986), and one persistent CTA per SM with equal shares of all tiles (890 for
+// the long prompt, but 220 for the windowed one and 236 against 194 us for 16
+// requests: the pieces' changes cost more than the gaps that they fill).
 // TMEM: S at columns 0 and 128, O at 256 (256 columns).
 //
 // Every wait is bounded (see split_tc_kernel.cuh): a wait that gives up sets the
@@ -197,26 +212,42 @@ __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt,
   const uint8_t* kbase = p.k_cache + g * p.ksh;
   const uint8_t* vbase = p.v_cache + g * p.vsh;
   // Position 32 w + lane of a tile: its block id is requested one tile before
-  // the place is needed, so that nothing waits for that load either.
-  int blk = -1, slot = 0;
-  bool in = false;
-  auto ask = [&](int j) {
-    const int v = u0 + j * kT + 32 * w + lane;
-    in = v < u1;
-    blk = -1;
-    if (in) {
-      const int pos = span.position(v), page = div_page(pos, p.page_size, p.page_div);
-      slot = pos - page * p.page_size;
-      blk = __ldg(p.block_table + (int64_t)b * p.bt_stride + page);
-    }
+  // the place is needed, so that nothing waits for that load either.  From
+  // tile to tile page and slot move by a constant step.
+  const int32_t* table = p.block_table + (int64_t)b * p.bt_stride;
+  const int step_page = kT / p.page_size, step_slot = kT - step_page * p.page_size;
+  int v_ask = u0 + 32 * w + lane, page = 0, slot = 0;
+  auto locate_token = [&]() {
+    const int pos = span.position(v_ask);
+    page = div_page(pos, p.page_size, p.page_div);
+    slot = pos - page * p.page_size;
   };
+  locate_token();
+  int blk = -1, slot_now = 0;
+  bool in = false;
+  auto ask = [&]() {  // of the next tile in order
+    in = v_ask < u1;
+    blk = -1;
+    slot_now = slot;
+    if (in) blk = __ldg(table + page);
+    const bool sink = v_ask < span.sk;
+    v_ask += kT;
+    page += step_page;
+    slot += step_slot;
+    if (slot >= p.page_size) {
+      slot -= p.page_size;
+      ++page;
+    }
+    if (sink) locate_token();  // the window may begin in between
+  };
+  const bool same = p.ksb == p.vsb && p.kst == p.vst;  // K and V rows at the same offset
   int64_t koff = 0, voff = 0;
   uint32_t ok_next = 0u;
   auto find = [&]() {
     const bool ok = blk >= 0 && blk < p.num_kv_blocks;
     if (DO_K && in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    if (DO_K) koff = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
-    if (DO_V) voff = ok ? blk * p.vsb + (int64_t)slot * p.vst : 0;
+    if (DO_K) koff = ok ? blk * p.ksb + (int64_t)slot_now * p.kst : 0;
+    if (DO_V) voff = DO_K && same ? koff : ok ? blk * p.vsb + (int64_t)slot_now * p.vst : 0;
     ok_next = __ballot_sync(0xffffffffu, ok);
   };
   int64_t* place = mt.place[DO_K ? 0 : 1][w];
@@ -228,23 +259,27 @@ __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt,
     if constexpr (DO_K) fetch_rows<D>(kbase, place, lane, kr);
   };
   auto fetch_v = [&]() {
-    __syncwarp();
-    place[lane] = voff;
-    __syncwarp();
+    if (!DO_K || !same) {
+      __syncwarp();
+      place[lane] = voff;
+      __syncwarp();
+    }
     if constexpr (DO_V) fetch_rows<D>(vbase, place, lane, vr);
   };
-  ask(0);
+  ask();
   find();
   if (DO_K) fetch_k();
   if (DO_V) fetch_v();
   uint32_t ok_now = ok_next;
-  if (n_tiles > 1) ask(1);
+  ask();
   bool ok = true, bad = false;
   for (int j = 0; j < n_tiles; ++j) {
     const int st = j % NS;
     const uint32_t empty_parity = ((j / NS) - 1) & 1;
-    if (j + 1 < n_tiles) find();
-    if (j + 2 < n_tiles) ask(j + 2);
+    if (j + 1 < n_tiles) {
+      find();
+      ask();
+    }
     // (the last tile is requested again: the requests stay unconditional)
     if constexpr (DO_K) {
       if (j >= NS && !warp_wait(&mt.k_empty[st], empty_parity, abort_flag)) {
@@ -322,7 +357,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileMeta& mt = *reinterpret_cast<TileMeta*>(smem + C::kOffMeta);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // (broadcast: known to be the same in all lanes, so that branches are uniform and a
+  // UMMA's operands stay in uniform registers: 955 us became 922)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = blockIdx.y, s = blockIdx.z;
 
   TileWork work;
@@ -353,7 +391,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
     return;
   }
   const int n_tiles = (u1 - u0 + kT - 1) / kT;
-  const int nq = NQ == 2 && RC > kM ? 2 : 1;  // row tiles in use
+  const int nq = __shfl_sync(0xffffffffu, NQ == 2 && RC > kM ? 2 : 1, 0);  // row tiles in use
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -385,7 +423,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   const uint32_t tmem = __shfl_sync(0xffffffffu, mt.tmem, 0);
   volatile uint32_t* const abort_flag = &mt.abort;
   const float ks = p.k_scale_dev ? *p.k_scale_dev : p.k_scale;
-  const double cd = (double)p.softmax_scale * (double)ks * 1.4426950408889634074;
+  const float cf = p.softmax_scale * ks * kLog2e;  // base-2 logit factor
   bool ok = true;
 
   if (warp < 4 * NQ) {
@@ -395,26 +433,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       // One warp per row: fp16 as it is, bf16 scaled by a power of two; the
       // sign of the logit factor goes into Q.
       constexpr int V = D / 32;  // elements per lane
-      constexpr int kRowsAtOnce = 8;
+      constexpr int kRowsAtOnce = D == 256 ? 16 : 32;  // 64 registers
       uint8_t* sQ = smem + C::kOffQ + q * (kM * D * 2);
-      const uint32_t flip = cd < 0 ? 0x80008000u : 0u;
+      const uint32_t flip = cf < 0.f ? 0x80008000u : 0u;
       const int e = lane * V;  // first element of the lane
       float back = 1.f;        // inverse scale of this thread's row
+      // the warp's first row; rows past RC read the last one (their results are dropped)
+      int rr0 = min(q * kM + 32 * (warp & 3), RC - 1);
+      int head = (work.row0 + rr0) % p.G;
+      const uint16_t* src =
+          p.q + (int64_t)(req.row0 + (work.row0 + rr0) / p.G) * p.q_st + (int64_t)(g * p.G + head) * p.q_sh + e;
 #pragma unroll 1
       for (int k0 = 0; k0 < 32; k0 += kRowsAtOnce) {
         uint32_t w[kRowsAtOnce][V / 2];
-        // all loads first, rows past RC read the last one (their results are dropped)
+        // all loads first
 #pragma unroll
         for (int k = 0; k < kRowsAtOnce; ++k) {
-          const int pr = work.row0 + min(q * kM + 32 * (warp & 3) + k0 + k, RC - 1);
-          const uint16_t* src =
-              p.q + (int64_t)(req.row0 + pr / p.G) * p.q_st + (int64_t)(g * p.G + pr % p.G) * p.q_sh + e;
           if constexpr (V == 2) {
             w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
           } else if constexpr (V == 4) {
             *reinterpret_cast<uint2*>(w[k]) = __ldg(reinterpret_cast<const uint2*>(src));
           } else {
             *reinterpret_cast<uint4*>(w[k]) = __ldg(reinterpret_cast<const uint4*>(src));
+          }
+          if (++rr0 < RC) {
+            const bool wrap = ++head == p.G;
+            if (wrap) head = 0;
+            src += wrap ? p.q_st - (p.G - 1) * p.q_sh : p.q_sh;
           }
         }
 #pragma unroll
@@ -507,7 +552,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       const int rr = q * kM + 32 * (warp & 3) + lane;  // this thread's row of the CTA
       const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
       // (not 0, so that c * -inf stays -inf for masked logits)
-      const float c = fmaxf((float)(fabs(cd) * (double)back), 1e-30f);
+      const float c = fmaxf(fabsf(cf) * back, 1e-30f);
       ChunkRow row = {INT_MAX, INT_MIN};  // rows past RC: everything, dropped at the end
       if (rr < RC) row = chunk_row(p, req, span, (work.row0 + rr) / p.G);
       const int hi_min = __reduce_min_sync(0xffffffffu, row.hi), lo_max = __reduce_max_sync(0xffffffffu, row.lo);
@@ -576,9 +621,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
           __syncwarp();
           if (lane == 0) mbar_arrive(&mt.p_ready[q][h]);
           if (issuer) {
-            if (h == 1 && NQ == 1 && j + 1 < n_tiles) issue_qk(j + 1);  // its buffer held P(j-1)
-            issue_pv(j, h);
-            if (h == 1 && NQ == 2 && j + 1 < n_tiles) issue_qk(j + 1);
+            if (NQ == 1) {
+              if (h == 1 && j + 1 < n_tiles) issue_qk(j + 1);  // its buffer held P(j-1)
+              issue_pv(j, h);
+            } else if (h == 1) {
+              // PV(j) and QK(j+1) of a row tile go to the tensor core in one piece: while it
+              // runs, the other row tile is at its softmax.  (PV of the first half at
+              // h = 0 costs the warp a wait and an issue amid its exponentials.)
+              issue_pv(j, 0);
+              issue_pv(j, 1);
+              if (j + 1 < n_tiles) issue_qk(j + 1);
+            }
           }
         }
         const float2 t = unpair(add2(sum[0], sum[1]));
