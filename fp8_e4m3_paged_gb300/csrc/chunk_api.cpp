@@ -46,7 +46,8 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   if (d->total_q > (1 << 30) || d->max_q > (1 << 24) || d->max_kv_len > (1 << 30) || d->num_kv_heads > 65535 ||
       d->max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32))
     return FP8KV_EUNSUPPORTED;
-  if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > 65535 * (int64_t)kChunkStreamRows) return FP8KV_EUNSUPPORTED;
+  if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > 65535 * (int64_t)kChunkStreamRows)
+    return FP8KV_EUNSUPPORTED;
 
   int sms = d->num_sms;
   if (sms == 0) {
@@ -79,13 +80,36 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   P.num_sms = sms;
 
   const int64_t rows = P.max_q * group;  // query vectors per (request, KV head)
-  P.kernel = d->kernel ? d->kernel : rows <= kChunkStreamRows ? FP8KV_CHUNK_STREAM : FP8KV_CHUNK_TILE;
+  const int64_t stream_units = (int64_t)P.batch * P.num_kv_heads * ceil_div(rows, kChunkStreamRows);
+  auto seen_by = [&](int64_t tokens) -> int64_t {  // positions that so many tokens see together, at most
+    return P.window ? std::min<int64_t>(P.max_kv_len, (int64_t)P.window + P.sinks + tokens - 1) : P.max_kv_len;
+  };
+  P.kernel = d->kernel;
+  if (P.kernel == FP8KV_CHUNK_AUTO) {
+    // The stream kernel takes 16 query vectors at a time and reads the positions
+    // anew for the next 16; the tile kernel serves 256 (128) from one read, but
+    // starts slower and leaves SMs idle where there are few tiles.  So more
+    // than 16 vectors stream while the positions are few (`units`: CTAs of the
+    // stream kernel before the context is split; us, stream / tile):
+    //   units few, any number of vectors: 32 units x 2064 positions 13.9 / 19.1, 24 x 340 (D 64)
+    //   8.1 / 12.2, 26 x 400 (D 256) 14.1 / 19.4, 16 x 2008 13.1 / 14.4, but 16 x 4008 17.5 / 16.4;
+    //   up to 32 vectors: 64 units x 1008 12.8 / 15.7, x 2008 17.2 / 19.0, 256 x 308 12.6 / 13.3,
+    //   but 256 x 2008 53.6 / 39.6, 512 x 8008 270 / 250.
+    const int64_t seen = seen_by(P.max_q);
+    const bool few = 2 * stream_units <= sms || (rows <= 32 && (stream_units <= sms || seen <= 512));
+    const bool stream = rows <= kChunkStreamRows || (seen * P.head_dim <= 5 << 16 && few);
+    P.kernel = stream ? FP8KV_CHUNK_STREAM : FP8KV_CHUNK_TILE;
+  }
 
   // Partitions: about one CTA per slot of the GPU, none shorter than `unit`
   // positions of what one CTA's rows see together.
+  // Stream kernel: more than two CTAs per SM only where each keeps 512
+  // positions (us, with / without that: 128 units x 300 positions S = 2 8.8, S = 4 10.4;
+  // 256 x 500 S = 1 11.7, S = 2 12.8; 64 x 1000 S = 4 9.6, S = 8 10.3; and 256 x 2000 S = 2 32.3,
+  // S = 1 35.3).
   int64_t units, slots, unit, span_q;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
-    units = (int64_t)P.batch * P.num_kv_heads * ceil_div(rows, kChunkStreamRows);
+    units = stream_units;
     slots = (int64_t)sms * (P.head_dim == 64 ? 5 : P.head_dim == 128 ? 4 : 2);
     unit = 4 * kChunkStreamBlock;
     span_q = P.max_q;
@@ -97,12 +121,33 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     unit = kChunkTileTokens;
     span_q = std::min<int64_t>(P.max_q, ceil_div(tile, group) + 1);
   }
-  const int64_t seen =
-      P.window ? std::min<int64_t>(P.max_kv_len, (int64_t)P.window + P.sinks + span_q - 1) : P.max_kv_len;
+  const int64_t seen = seen_by(span_q);
   int64_t S = units ? slots / units : 1;
   S = std::min(S, ceil_div(seen, unit));
-  if (P.kernel == FP8KV_CHUNK_TILE) S = std::max(S, ceil_div(seen, kChunkMaxPart));
-  if (P.kernel == FP8KV_CHUNK_STREAM && S > kChunkClusterMax && seen <= kChunkClusterMax * 8 * unit) S = kChunkClusterMax;
+  if (P.kernel == FP8KV_CHUNK_STREAM) {
+    if (units) S = std::max(std::min(2 * sms / units, ceil_div(seen, unit)), std::min(slots / units, seen / 512));
+    if (S > kChunkClusterMax && seen <= kChunkClusterMax * 8 * unit) S = kChunkClusterMax;
+  } else {
+    // The CTAs of one request are equally long, so the last of their waves is
+    // worth filling: the S whose waves times a CTA's time (its positions, and
+    // about 900 more for its start and end) is least.  8 KV heads x 2048 tokens x 4
+    // on 30000 positions, 152 SMs: S = 1 (2 waves) 926 us, 2 (4) 959, 3 (6) 954, 4 (7)
+    // 883, 5 (9) 922, 7 (12) 932.  (CTAs of several requests differ in length and fill
+    // the gaps themselves: 16 requests, 41 row tiles x 8 heads, S = 1: 194 us, 2: 201, 4: 223.)
+    if (P.batch == 1) {
+      const int64_t ctas = ceil_div(rows, chunk_tile_rows(P.head_dim)) * P.num_kv_heads;
+      const int64_t most = std::min(std::max<int64_t>(8, S), ceil_div(seen, unit));
+      int64_t best = INT64_MAX;
+      for (int64_t n = 1; n <= most; ++n) {
+        const int64_t cost = ceil_div(ctas * n, sms) * (ceil_div(seen, n) + 900);
+        if (cost < best) {
+          best = cost;
+          S = n;
+        }
+      }
+    }
+    S = std::max(S, ceil_div(seen, kChunkMaxPart));
+  }
   S = std::max<int64_t>(1, S);
   if (d->num_splits) S = d->num_splits;
   if (P.batch > 0 && P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;

@@ -404,7 +404,7 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  * Two calls that may overlap on the GPU need a workspace each.  The calls are
  * graph-capturable: lengths may change between replays within the plan.
  * ------------------------------------------------------------------------ */
-#define FP8KV_CHUNK_AUTO 0
+#define FP8KV_CHUNK_AUTO 0   /* by the query vectors and the positions that they see */
 #define FP8KV_CHUNK_STREAM 1 /* streams the cache past 16 query vectors per CTA */
 #define FP8KV_CHUNK_TILE 2   /* tcgen05 tiles of 128 query vectors */
 
@@ -468,7 +468,7 @@ typedef struct {
 /* Validate `d` and fill `plan` (host only). */
 int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan);
 /* Launch the attention on `stream` (one kernel, and a second that joins the
- * partitions when the plan has more than one). */
+ * partitions where the first does not: it joins up to 8 of the stream kernel). */
 int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, fp8kv_stream_t stream);
 
 /* ------------------------------------------------------------------------
