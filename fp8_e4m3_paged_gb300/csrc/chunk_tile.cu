@@ -24,9 +24,9 @@
 // 2048 cycles; the exponentials, the conversions and the decode about 2000 issue
 // cycles per scheduler, and operand reads, decode stores and Q/P traffic 2300
 // shared-memory cycles; together they run in 3400 to 3600.  32 heads over 8, D 128,
-// 2048 queries on 30000 cached positions: 884 us, 1178 TFLOP/s (the FP16 dense rate
-// would take 537); 8192 queries with window 1024: 191 us, of which a CTA's
-// start and end (about 13 us: Q, the first rows, the output) are the
+// 2048 queries on 30000 cached positions: 862 us, 1207 TFLOP/s (the FP16 dense rate
+// would take 537); 8192 queries with window 1024: 180 us, of which a CTA's
+// start and end (about 12 us: lengths, Q, the first rows, the output) are the
 // larger part of what lies above the tensor time.
 // Measured and not taken: 16 warps of 128 registers with K and V decoded by four
 // warps each (984 us where this took 955), the same split by setmaxnreg (1076 and
@@ -332,6 +332,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -462,22 +467,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
             src += wrap ? p.q_st - (p.G - 1) * p.q_sh : p.q_sh;
           }
         }
+        // bf16: all rows' maxima, then each lane the scale of one row, then all rows.  (Row
+        // by row each waited for its maximum, and all lanes made the same scale.)
+        RowScale own = {1.f, 1.f};  // of row k0 + lane
+        if (DT == FP8KV_DTYPE_BF16) {
+          uint32_t own_top = 0u;
+#pragma unroll
+          for (int k = 0; k < kRowsAtOnce; ++k) {
+            uint32_t t = 0u;  // as integers: a NaN is larger than every number, and is not dropped
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) t = __vmaxu2(t, w[k][i] & 0x7FFF7FFFu);
+            t = __reduce_max_sync(0xffffffffu, max(t << 16, t & 0xFFFF0000u));
+            if (lane == k) own_top = t;
+          }
+          own = row_scale_bf16(__uint_as_float(own_top));
+          const float b = __shfl_sync(0xffffffffu, own.back, (lane - k0) & 31);
+          if (lane >= k0 && lane < k0 + kRowsAtOnce) back = b;
+          if (flip) own.to_f16 = -own.to_f16;
+        }
 #pragma unroll
         for (int k = 0; k < kRowsAtOnce; ++k) {
           const int r = 32 * (warp & 3) + k0 + k;
           if (DT == FP8KV_DTYPE_BF16) {
-            uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
+            const float to_f16 = __shfl_sync(0xffffffffu, own.to_f16, k);
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) top = max(top, max((w[k][i] << 16) & 0x7FFFFFFFu, w[k][i] & 0x7FFF0000u));
-            const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+            for (int i = 0; i < V / 2; ++i) {
+              const float2 x = unpair(mul2(pair(__uint_as_float(w[k][i] << 16), __uint_as_float(w[k][i] & 0xFFFF0000u)),
+                                           pair(to_f16, to_f16)));
+              w[k][i] = pack_half2(x.x, x.y);
+            }
+          } else {
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i)
-              w[k][i] = pack_half2(__uint_as_float(w[k][i] << 16) * rs.to_f16,
-                                   __uint_as_float(w[k][i] & 0xFFFF0000u) * rs.to_f16);
-            if (lane == k0 + k) back = rs.back;
+            for (int i = 0; i < V / 2; ++i) w[k][i] ^= flip;
           }
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) w[k][i] ^= flip;
           uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
           if constexpr (V == 2)
             *reinterpret_cast<uint32_t*>(dst) = w[k][0];
@@ -651,33 +673,56 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
         const bool live = rr < RC;
         const float vs = p.v_scale_dev ? *p.v_scale_dev : p.v_scale;
         const int64_t vec = live ? vec_of(rr) : 0;
-        const bool dead = l == 0.f;
-        const float f = p.S > 1 ? kChunkInvPShift : (dead ? 0.f : vs / l);
+        const bool dead = l == 0.f, parts = p.S > 1;
+        const float f = parts ? kChunkInvPShift : (dead ? 0.f : vs / l);
+        if (parts && live) p.ml[s * plane + vec] = make_float2(m, l * kChunkInvPShift);
+        // A thread holds a row, but a store instruction had better write few rows: 128
+        // bytes of each of the warp's 32 rows go through shared memory (the
+        // warp's part of Q, all reads of which are done; 16-byte chunk c of row r
+        // at c ^ (r % 8)) and out as four rows per instruction.  (16 bytes of 32
+        // rows each: 5000 to 6000 cycles of a CTA's end.)
         const int pr = work.row0 + rr;
-        uint16_t* dst = p.out + (int64_t)(req.row0 + pr / p.G) * p.o_st + (int64_t)(g * p.G + pr % p.G) * p.o_sh;
-        if (p.S > 1 && live) p.ml[s * plane + vec] = make_float2(m, l * kChunkInvPShift);
+        char* to = nullptr;  // this thread's row
+        if (live)
+          to = parts ? reinterpret_cast<char*>(p.partial + (s * plane + vec) * D)
+                     : reinterpret_cast<char*>(p.out + (int64_t)(req.row0 + pr / p.G) * p.o_st +
+                                               (int64_t)(g * p.G + pr % p.G) * p.o_sh);
+        char* row_to[8];     // rows 4 i + lane / 8 of the warp
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          row_to[i] = reinterpret_cast<char*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), 4 * i + lane / 8));
+        uint8_t* buf = smem + C::kOffQ + q * (kM * D * 2) + (warp & 3) * 4096;
+        static_assert(kM * D * 2 >= 4 * 4096, "room for the four warps");
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + c0, o);
-          if (!live) {
-          } else if (p.S > 1) {
-            float* part = p.partial + (s * plane + vec) * D + c0;
+        for (int c0 = 0; c0 < D; c0 += parts ? 32 : 64) {
+          uint4 y[8];
+          if (parts) {
+            uint32_t o[32];
+            tmem_ld32(tO + c0, o);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(part + k) =
-                  make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
-                              __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           } else {
-            uint32_t y[16];
+            uint32_t o[64];
+            tmem_ld64(tO + c0, o);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2)
-              y[k / 2] = dead ? 0u : pack_out<DT>(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f);
+            for (int k = 0; k < 32; ++k)
+              o[k] = dead ? 0u : pack_out<DT>(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
 #pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<uint4*>(dst + c0 + 2 * k) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+            for (int k = 0; k < 8; ++k) y[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
           __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(buf + lane * 128 + ((k ^ (lane & 7)) * 16)) = y[k];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane & 7) ^ (r & 7)) * 16));
+            if (row_to[i]) *reinterpret_cast<uint4*>(row_to[i] + c0 * (parts ? 4 : 2) + (lane & 7) * 16) = v;
+          }
         }
       }
     }
