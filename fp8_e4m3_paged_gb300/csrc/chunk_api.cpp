@@ -22,6 +22,10 @@ bool strides_ok(const int64_t* s, int n, int64_t unit) {
     if (s[i] < 0 || s[i] % unit) return false;
   return true;
 }
+// No two rows or heads of an output in one place.
+bool apart(int64_t rows, int64_t stride_row, int64_t heads, int64_t stride_head) {
+  return (rows < 2 || stride_row > 0) && (heads < 2 || stride_head > 0);
+}
 bool fp8_format(int32_t f) { return f == FP8KV_KV_E4M3 || f == FP8KV_KV_E5M2; }
 int done(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ECUDA; }
 
@@ -44,7 +48,8 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   // 32-bit positions, packed rows and grid sizes
   const int64_t group = d->num_q_heads / d->num_kv_heads;
   if (d->total_q > (1 << 30) || d->max_q > (1 << 24) || d->max_kv_len > (1 << 30) || d->num_kv_heads > 65535 ||
-      d->max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32))
+      d->max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32) ||
+      d->num_sms > 65535)
     return FP8KV_EUNSUPPORTED;
   if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > 65535 * (int64_t)kChunkStreamRows)
     return FP8KV_EUNSUPPORTED;
@@ -80,7 +85,8 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   P.num_sms = sms;
 
   const int64_t rows = P.max_q * group;  // query vectors per (request, KV head)
-  const int64_t stream_units = (int64_t)P.batch * P.num_kv_heads * ceil_div(rows, kChunkStreamRows);
+  const int64_t pairs = (int64_t)P.batch * P.num_kv_heads;  // the stream kernel's grid.x
+  const int64_t stream_units = std::min<int64_t>(pairs, 1ll << 32) * ceil_div(rows, kChunkStreamRows);
   auto seen_by = [&](int64_t tokens) -> int64_t {  // positions that so many tokens see together, at most
     return P.window ? std::min<int64_t>(P.max_kv_len, (int64_t)P.window + P.sinks + tokens - 1) : P.max_kv_len;
   };
@@ -148,9 +154,10 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     }
     S = std::max(S, ceil_div(seen, kChunkMaxPart));
   }
-  S = std::max<int64_t>(1, S);
+  S = std::min<int64_t>(std::max<int64_t>(1, S), 65535);
   if (d->num_splits) S = d->num_splits;
-  if (P.batch > 0 && P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;
+  if (P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;
+  if (P.kernel == FP8KV_CHUNK_STREAM && pairs > 0x7fffffff) return FP8KV_EUNSUPPORTED;
   P.num_splits = (int32_t)S;
 
   const int64_t nvec = S > 1 && !chunk_clustered(&P) ? S * P.total_q * P.num_q_heads : 0;
@@ -181,6 +188,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   const int64_t bs[] = {a->k_stride_block, a->k_stride_token, a->k_stride_head,
                         a->v_stride_block, a->v_stride_token, a->v_stride_head};
   if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
+  if (!apart(plan->total_q, es[2], plan->num_q_heads, es[3])) return FP8KV_EINVAL;
   if (!a->cu_q || !a->kv_len || !aligned(a->cu_q, 4) || !aligned(a->kv_len, 4)) return FP8KV_EINVAL;
   if (plan->max_kv_len > 0 && (!a->block_table || !aligned(a->block_table, 4))) return FP8KV_EINVAL;
   if (a->block_table_stride < plan->max_blocks) return FP8KV_EINVAL;
@@ -250,6 +258,7 @@ extern "C" int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_strea
       a->num_kv_blocks < 1)
     return FP8KV_EINVAL;
   if (a->head_dim < 16 || a->head_dim > 1024 || a->head_dim % 16) return FP8KV_EINVAL;
+  if (a->num_kv_heads > 65535) return FP8KV_EUNSUPPORTED;  // 32-bit places within a row
   if (a->dtype != FP8KV_DTYPE_F16 && a->dtype != FP8KV_DTYPE_BF16 && a->dtype != FP8KV_DTYPE_F32)
     return FP8KV_EINVAL;
   if (!fp8_format(a->kv_format)) return FP8KV_EINVAL;
@@ -261,6 +270,9 @@ extern "C" int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_strea
   const int64_t bs[] = {a->kc_stride_block, a->kc_stride_token, a->kc_stride_head,
                         a->vc_stride_block, a->vc_stride_token, a->vc_stride_head};
   if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
+  if (!apart(a->total, es[0], a->num_kv_heads, es[1]) || !apart(a->total, es[2], a->num_kv_heads, es[3]) ||
+      a->k_out == a->v_out)
+    return FP8KV_EINVAL;
   if (!a->block_table || !a->cu_len || a->block_table_stride < a->max_blocks) return FP8KV_EINVAL;
   if (!aligned(a->block_table, 4) || !aligned(a->cu_len, 4) || !aligned(a->start, 4)) return FP8KV_EINVAL;
   if (!a->k_scale_dev && !std::isfinite(a->k_scale)) return FP8KV_EINVAL;
@@ -272,6 +284,7 @@ extern "C" int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_s
   if (!a) return FP8KV_EINVAL;
   if (a->num_tokens < 0 || a->num_kv_heads < 1) return FP8KV_EINVAL;
   if (a->head_dim < 16 || a->head_dim > 1024 || a->head_dim % 16) return FP8KV_EINVAL;
+  if (a->num_kv_heads > 65535) return FP8KV_EUNSUPPORTED;  // 32-bit places within a row
   if (a->dtype != FP8KV_DTYPE_F16 && a->dtype != FP8KV_DTYPE_BF16) return FP8KV_EINVAL;
   if (!fp8_format(a->kv_format)) return FP8KV_EINVAL;
   if (a->num_tokens == 0) return FP8KV_OK;

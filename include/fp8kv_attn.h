@@ -448,7 +448,7 @@ typedef struct {
   const void* q;          /* (row, head, d) at element row*q_stride_token + head*q_stride_head + d; 16-byte aligned */
   int64_t q_stride_token, q_stride_head;     /* elements, multiples of 8, >= 0 */
   void* out;              /* same type and addressing with the out_* values; not overlapping q */
-  int64_t out_stride_token, out_stride_head; /* elements, multiples of 8, >= 0 */
+  int64_t out_stride_token, out_stride_head; /* elements, multiples of 8; 0 only for one row (head) */
   const uint8_t* k_cache; /* as fp8kv_attn_args.k_cache */
   const uint8_t* v_cache;
   int64_t k_stride_block, k_stride_token, k_stride_head; /* bytes, multiples of 16 */
@@ -465,7 +465,8 @@ typedef struct {
   size_t workspace_bytes;
 } fp8kv_chunk_args;
 
-/* Validate `d` and fill `plan` (host only). */
+/* Validate `d` and fill `plan` (host only).  More than 65535 KV heads or SMs, and a
+ * batch x num_kv_heads above 2^31 - 1 with the stream kernel: FP8KV_EUNSUPPORTED. */
 int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan);
 /* Launch the attention on `stream` (one kernel, and a second that joins the
  * partitions where the first does not: it joins up to 8 of the stream kernel). */
@@ -494,7 +495,7 @@ int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, 
 typedef struct {
   int32_t batch;         /* B >= 0 */
   int32_t total;         /* rows of k_out and v_out, >= cu_len[B] */
-  int32_t num_kv_heads;  /* Hkv >= 1 */
+  int32_t num_kv_heads;  /* Hkv, 1..65535 */
   int32_t head_dim;      /* D: a multiple of 16, 16..1024 */
   int32_t page_size;     /* >= 1 */
   int32_t max_blocks;    /* block-table columns, >= 1 */
@@ -511,7 +512,7 @@ typedef struct {
   const int32_t* start;       /* [B] first position of each request; NULL = 0 */
   void* k_out;                /* (row, h, d) at element row*stride_token + h*stride_head + d; 16-byte aligned */
   void* v_out;
-  int64_t ko_stride_token, ko_stride_head; /* elements, multiples of 8, >= 0 */
+  int64_t ko_stride_token, ko_stride_head; /* elements, multiples of 8; 0 only for one row (head) */
   int64_t vo_stride_token, vo_stride_head;
   float k_scale, v_scale;     /* finite (used when the device pointers are NULL) */
   const float* k_scale_dev;
@@ -537,7 +538,7 @@ int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_stream_t stream)
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t num_tokens;     /* N >= 0 (0: nothing to do) */
-  int32_t num_kv_heads;   /* Hkv >= 1 */
+  int32_t num_kv_heads;   /* Hkv, 1..65535 */
   int32_t head_dim;       /* D: a multiple of 16, 16..1024 */
   int32_t dtype;          /* FP8KV_DTYPE_F16 or FP8KV_DTYPE_BF16 */
   int32_t kv_format;      /* FP8KV_KV_E4M3 or FP8KV_KV_E5M2 */

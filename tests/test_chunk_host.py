@@ -92,6 +92,55 @@ def test_chunk_plan_workspace_and_windows(B):
     assert B.fp8kv_attn_chunk_plan(_desc(B, max_q=4)).kernel == B.CHUNK_STREAM
 
 
+@pytest.mark.parametrize("kw,kernel", [
+    (dict(max_q=1), 1), (dict(max_q=4), 1),                       # up to 16 query vectors per KV head
+    (dict(max_q=8, max_kv_len=500), 1),                           # 32 on few positions
+    (dict(max_q=8, window=300), 1),
+    (dict(max_q=8), 2),                                           # 32 on 4000 positions
+    (dict(max_q=8, max_kv_len=500, head_dim=256), 1),
+    (dict(max_q=8, max_kv_len=2000, head_dim=256), 2),
+    (dict(batch=64, total_q=512, max_q=8, max_kv_len=1000), 2),   # ... of many requests
+    (dict(batch=64, total_q=512, max_q=8, max_kv_len=500), 1),
+    (dict(batch=64, total_q=1024, max_q=16, max_kv_len=500), 2),
+    (dict(batch=1, max_q=100, max_kv_len=500), 1),                # 400 of one request
+    (dict(batch=0, total_q=0), 1),
+])
+def test_chunk_plan_chooses_a_kernel(B, kw, kernel):
+    assert B.fp8kv_attn_chunk_plan(_desc(B, **kw)).kernel == kernel
+
+
+def test_chunk_plan_partitions(B):
+    def splits(**kw):
+        return B.fp8kv_attn_chunk_plan(_desc(B, **kw)).num_splits
+
+    long = dict(batch=1, total_q=2048, max_q=2048, num_q_heads=32, num_kv_heads=8, max_kv_len=32048, max_blocks=2003)
+    assert splits(**long) == 4                       # 256 CTAs: 7 waves of a quarter, not 2 whole ones
+    assert splits(**dict(long, num_sms=256)) == 1    # one full wave
+    # no FP32 sum of the tile kernel over more than 32768 positions
+    assert splits(**dict(long, max_kv_len=200000, max_blocks=12500)) >= 7
+    # stream kernel: two CTAs per SM, four where each keeps 512 positions
+    one = dict(max_q=1, num_q_heads=32, num_kv_heads=8)
+    assert splits(batch=16, total_q=16, **dict(one, max_kv_len=300)) == 2
+    assert splits(batch=32, total_q=32, **dict(one, max_kv_len=500)) == 1
+    assert splits(batch=32, total_q=32, **dict(one, max_kv_len=2000)) == 2
+    assert splits(batch=1, total_q=1, **dict(one, max_kv_len=2000)) == 8     # a cluster
+    # whatever the sizes, a grid that can be launched
+    for sms in (1, 65535):
+        for kernel in (1, 2):
+            p = B.fp8kv_attn_chunk_plan(_desc(B, batch=1, max_q=1, num_sms=sms, kernel=kernel, max_kv_len=1 << 30,
+                                              max_blocks=1 << 26))
+            assert 1 <= p.num_splits <= 65535
+
+
+@pytest.mark.parametrize("kw", [
+    dict(num_sms=65536), dict(batch=1 << 30, num_kv_heads=8, max_q=1), dict(batch=(1 << 31) - 1, kernel=1),
+])
+def test_chunk_plan_refuses_grids(B, kw):
+    with pytest.raises(B.Fp8kvError) as e:
+        B.fp8kv_attn_chunk_plan(_desc(B, **kw))
+    assert e.value.code == -2
+
+
 def _args(B, plan, **kw):
     a = B.ChunkArgs()
     a.q = a.out = a.k_cache = a.v_cache = a.block_table = a.cu_q = a.kv_len = FAKE
@@ -120,6 +169,21 @@ def test_chunk_rejects_arguments(B, kw):
     assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(_args(B, plan, **kw)), None) == B.EINVAL
 
 
+def test_outputs_in_one_place_are_refused(B):
+    """A zero stride would write several rows (heads) to one place; inputs may have one."""
+    plan = B.fp8kv_attn_chunk_plan(_desc(B))
+    for kw in (dict(out_stride_token=0), dict(out_stride_head=0)):
+        assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(_args(B, plan, **kw)), None) == B.EINVAL
+    for kw in (dict(ko_stride_token=0), dict(vo_stride_token=0), dict(ko_stride_head=0), dict(vo_stride_head=0),
+               dict(v_out=FAKE)):
+        assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, **kw)), None) == B.EINVAL
+
+
+def test_more_heads_than_a_row_can_count_are_refused(B):
+    assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, num_kv_heads=65536)), None) == -2
+    assert B.lib.fp8kv_attn_cache_calibrate(ctypes.byref(_cal(B, num_kv_heads=65536)), None) == -2
+
+
 def test_chunk_plan_and_workspace_checks(B):
     plan = B.fp8kv_attn_chunk_plan(_desc(B))
     assert B.lib.fp8kv_attn_chunk(None, ctypes.byref(_args(B, plan)), None) == B.EINVAL
@@ -138,7 +202,8 @@ def test_chunk_plan_and_workspace_checks(B):
 def _read(B, **kw):
     a = B.CacheReadArgs()
     a.batch, a.total, a.num_kv_heads, a.head_dim, a.page_size, a.max_blocks, a.num_kv_blocks = 2, 9, 2, 128, 16, 4, 9
-    a.k_cache = a.v_cache = a.block_table = a.cu_len = a.k_out = a.v_out = FAKE
+    a.k_cache = a.v_cache = a.block_table = a.cu_len = a.k_out = FAKE
+    a.v_out = FAKE + (1 << 20)
     a.kc_stride_block = a.vc_stride_block = 4096
     a.kc_stride_token = a.vc_stride_token = 256
     a.kc_stride_head = a.vc_stride_head = a.ko_stride_head = a.vo_stride_head = 128
