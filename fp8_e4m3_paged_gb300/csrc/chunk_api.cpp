@@ -270,8 +270,7 @@ extern "C" int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_strea
   const int64_t bs[] = {a->kc_stride_block, a->kc_stride_token, a->kc_stride_head,
                         a->vc_stride_block, a->vc_stride_token, a->vc_stride_head};
   if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
-  if (!apart(a->total, es[0], a->num_kv_heads, es[1]) || !apart(a->total, es[2], a->num_kv_heads, es[3]) ||
-      a->k_out == a->v_out)
+  if (!apart(a->total, es[0], a->num_kv_heads, es[1]) || !apart(a->total, es[2], a->num_kv_heads, es[3]))
     return FP8KV_EINVAL;
   if (!a->block_table || !a->cu_len || a->block_table_stride < a->max_blocks) return FP8KV_EINVAL;
   if (!aligned(a->block_table, 4) || !aligned(a->cu_len, 4) || !aligned(a->start, 4)) return FP8KV_EINVAL;

@@ -127,6 +127,9 @@ CASES = {
     "negative_scale": Case([(20, 200), (1, 90)], Hq=4, Hkv=2, D=128, softmax_scale=-0.11),
     "large_logits": Case([(20, 200), (1, 90)], Hq=4, Hkv=2, D=128, q_scale=30.0),
     "long": Case([(3, 5000), (1, 4097)], Hq=4, Hkv=2, D=128),
+    "one_chunk": Case([(150, 3000)], Hq=8, Hkv=2, D=128),          # partitions by waves
+    "one_chunk_wide": Case([(130, 2100)], Hq=3, Hkv=1, D=256, dtype=torch.bfloat16),
+    "many_vectors_few_positions": Case([(40, 90)], Hq=12, Hkv=1, D=64),
 }
 
 
@@ -190,6 +193,34 @@ def test_nonfinite_codes_reach_the_rows_that_see_them(fmt, D):
         assert torch.isnan(ref[0]).any() and not torch.isnan(ref[0]).all()
         for kernel, splits in kernels(c):
             check(Run(c, kernel, splits)(), c, ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_nonfinite_queries_reach_their_own_rows_only(dtype):
+    c = Case([(20, 200), (40, 300), (1, 90)], Hq=4, Hkv=2, D=128, dtype=dtype)
+    clean = c.reference()
+    c.q[3, 0, 5] = float("nan")
+    c.q[30, 2, 7] = float("inf")
+    c.q[60, 3, 0] = float("-inf")
+    c.q[17, 1] = float("nan")
+    bad = torch.zeros(c.total, c.Hq, dtype=torch.bool)
+    for row, h in ((3, 0), (30, 2), (60, 3), (17, 1)):
+        bad[row, h] = True
+    for kernel, splits in kernels(c):
+        got = Run(c, kernel, splits)()
+        assert torch.isnan(got[bad]).all()
+        got[bad] = clean[0][bad]
+        check(got, c, clean)
+
+
+def test_requests_that_share_blocks():
+    """A shared prefix: one block in several tables, and twice in one."""
+    c = Case([(5, 160), (30, 170), (1, 64)], Hq=8, Hkv=2, D=128, page=16)
+    c.table[1, :8] = c.table[0, :8]
+    c.table[2, :4] = c.table[0, 0]
+    ref = c.reference()
+    for kernel, splits in kernels(c):
+        check(Run(c, kernel, splits)(), c, ref)
 
 
 def test_bad_blocks_count_as_not_visible():
