@@ -139,7 +139,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     // about 900 more for its start and end) is least.  8 KV heads x 2048 tokens x 4
     // on 30000 positions, 152 SMs: S = 1 (2 waves) 926 us, 2 (4) 959, 3 (6) 954, 4 (7)
     // 883, 5 (9) 922, 7 (12) 932.  (CTAs of several requests differ in length and fill
-    // the gaps themselves: 16 requests, 41 row tiles x 8 heads, S = 1: 194 us, 2: 201, 4: 223.)
+    // the gaps themselves: 16 requests, 41 row tiles x 8 heads, S = 1: 131 us, 2: 155, 4: 189.)
     if (P.batch == 1) {
       const int64_t ctas = ceil_div(rows, chunk_tile_rows(P.head_dim)) * P.num_kv_heads;
       const int64_t most = std::min(std::max<int64_t>(8, S), ceil_div(seen, unit));
@@ -156,8 +156,9 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   }
   S = std::min<int64_t>(std::max<int64_t>(1, S), 65535);
   if (d->num_splits) S = d->num_splits;
-  if (P.batch * S > 0x7fffffff) return FP8KV_EUNSUPPORTED;
-  if (P.kernel == FP8KV_CHUNK_STREAM && pairs > 0x7fffffff) return FP8KV_EUNSUPPORTED;
+  // grid.x
+  if ((P.kernel == FP8KV_CHUNK_STREAM ? pairs : (int64_t)P.row_tiles * P.num_kv_heads) > 0x7fffffff)
+    return FP8KV_EUNSUPPORTED;
   P.num_splits = (int32_t)S;
 
   const int64_t nvec = S > 1 && !chunk_clustered(&P) ? S * P.total_q * P.num_q_heads : 0;

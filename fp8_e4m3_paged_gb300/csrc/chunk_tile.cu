@@ -25,15 +25,15 @@
 // cycles per scheduler, and operand reads, decode stores and Q/P traffic 2300
 // shared-memory cycles; together they run in 3400 to 3600.  32 heads over 8, D 128,
 // 2048 queries on 30000 cached positions: 862 us, 1207 TFLOP/s (the FP16 dense rate
-// would take 537); 8192 queries with window 1024: 180 us, of which a CTA's
+// would take 537); 8192 queries with window 1024: 175 us, of which a CTA's
 // start and end (about 12 us: lengths, Q, the first rows, the output) are the
 // larger part of what lies above the tensor time.
 // Measured and not taken: 16 warps of 128 registers with K and V decoded by four
 // warps each (984 us where this took 955), the same split by setmaxnreg (1076 and
 // more), row tiles in strict turns (955 to 978), a running maximum one tile late
 // (986), and one persistent CTA per SM with equal shares of all tiles (890 for
-// the long prompt, but 220 for the windowed one and 236 against 194 us for 16
-// requests: the pieces' changes cost more than the gaps that they fill).
+// the long prompt, but 220 for the windowed one and 236 for 16 requests: the
+// pieces' changes cost more than the gaps that they fill).
 // TMEM: S at columns 0 and 128, O at 256 (256 columns).
 //
 // Every wait is bounded (see split_tc_kernel.cuh): a wait that gives up sets the
@@ -100,9 +100,12 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// Request and first packed row of this CTA: tiles count over the requests in
-// order, taken from the last (a request's last rows see the most positions,
-// so the longest work starts first).
+// Request and first packed row of a CTA.  The GPU starts CTAs in the order of their
+// index, so the longest go first: requests by the positions that their rows see
+// (above 32 requests: by their index, from the last), a request's row tiles from
+// the last, which sees the most, and the KV heads of a row tile side by side.  16
+// requests on 200 to 8000 positions: 130 us; with requests by index and row tiles
+// before heads, whose longest CTAs started last, 189.
 struct TileWork {
   int b, row0;
 };
@@ -112,13 +115,28 @@ __device__ __forceinline__ int tiles_of(const ChunkParams& p, int b, int rows, b
   bad |= r.bad;
   return (r.n * p.G + rows - 1) / rows;
 }
-__device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int lane, TileWork& w) {
+__device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int idx, int lane, TileWork& w) {
   int total = 0;
   bool bad = false;
+  if (p.B <= 32) {
+    const int mine = tiles_of(p, lane, rows, bad);
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
+    int key = 0, before = 0;  // tiles of the requests that go first
+    if (lane < p.B) key = min(max(p.kv_len[lane], 0), p.window > 0 ? p.window : INT_MAX);
+    for (int i = 0; i < p.B; ++i) {
+      const int k = __shfl_sync(0xffffffffu, key, i), n = __shfl_sync(0xffffffffu, mine, i);
+      if (k > key || (k == key && i > lane)) before += n;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, before <= idx && idx - before < mine);
+    if (here == 0u) return false;
+    const int l = __ffs(here) - 1;
+    w.b = l;
+    w.row0 = (__shfl_sync(0xffffffffu, before + mine, l) - 1 - idx) * rows;
+    return true;
+  }
   for (int b0 = 0; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, tiles_of(p, b0 + lane, rows, bad));
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 32)
-    set_status(p.status, FP8KV_STATUS_BAD_LEN);
-  int idx = total - 1 - (int)blockIdx.x;
+  if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
+  idx = total - 1 - idx;
   if (idx < 0) return false;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int mine = tiles_of(p, b0 + lane, rows, bad);
@@ -366,10 +384,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   // (broadcast: known to be the same in all lanes, so that branches are uniform and a
   // UMMA's operands stay in uniform registers: 955 us became 922)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int g = blockIdx.y, s = blockIdx.z;
+  const int g = blockIdx.x % p.Hkv, tile = blockIdx.x / p.Hkv, s = blockIdx.y;
 
   TileWork work;
-  if (!locate(p, ROWS, lane, work)) return;
+  if (!locate(p, ROWS, tile, lane, work)) return;
   const int b = work.b;
   const ChunkRequest req = chunk_request(p, b);
   const int RC = min(ROWS, req.n * p.G - work.row0);
@@ -467,22 +485,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
             src += wrap ? p.q_st - (p.G - 1) * p.q_sh : p.q_sh;
           }
         }
-        // bf16: all rows' maxima, then each lane the scale of one row, then all rows.  (Row
-        // by row each waited for its maximum, and all lanes made the same scale.)
-        RowScale own = {1.f, 1.f};  // of row k0 + lane
+        // bf16: all rows' maxima at once, then each lane the scale of one row.  The maxima
+        // (as integers: a NaN is larger than every number, and is not dropped) go
+        // through a butterfly that halves the rows a lane holds in each step, two rows
+        // to a register: 16 shuffles for 32 rows, where 32 warp reductions took 2000
+        // cycles more of a CTA's start.
+        RowScale own = {1.f, 1.f};  // of row k0 + lane % kRowsAtOnce
         if (DT == FP8KV_DTYPE_BF16) {
-          uint32_t own_top = 0u;
+          constexpr int N = kRowsAtOnce;
+          auto mag = [&](int k) {
+            uint32_t t = w[k][0] & 0x7FFF7FFFu;
 #pragma unroll
-          for (int k = 0; k < kRowsAtOnce; ++k) {
-            uint32_t t = 0u;  // as integers: a NaN is larger than every number, and is not dropped
+            for (int i = 1; i < V / 2; ++i) t = __vmaxu2(t, w[k][i] & 0x7FFF7FFFu);
+            return t;
+          };
+          uint32_t t[N / 2];  // rows k and k + N / 2
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) t = __vmaxu2(t, w[k][i] & 0x7FFF7FFFu);
-            t = __reduce_max_sync(0xffffffffu, max(t << 16, t & 0xFFFF0000u));
-            if (lane == k) own_top = t;
+          for (int k = 0; k < N / 2; ++k) {
+            const uint32_t a = mag(k), b = mag(k + N / 2);
+            t[k] = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
           }
-          own = row_scale_bf16(__uint_as_float(own_top));
-          const float b = __shfl_sync(0xffffffffu, own.back, (lane - k0) & 31);
-          if (lane >= k0 && lane < k0 + kRowsAtOnce) back = b;
+#pragma unroll
+          for (int o = N / 4; o >= 1; o /= 2) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int k = 0; k < o; ++k) {
+              const uint32_t give = upper ? t[k] : t[k + o], keep = upper ? t[k + o] : t[k];
+              t[k] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, o));
+            }
+          }
+#pragma unroll
+          for (int o = N / 2; o < 32; o *= 2) t[0] = __vmaxu2(t[0], __shfl_xor_sync(0xffffffffu, t[0], o));
+          own = row_scale_bf16(__uint_as_float(lane & (N / 2) ? t[0] & 0xFFFF0000u : t[0] << 16));
+          if (lane / N == k0 / N) back = own.back;
           if (flip) own.to_f16 = -own.to_f16;
         }
 #pragma unroll
@@ -774,7 +809,7 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  fn<<<dim3(p.row_tiles, p.Hkv, p.S), kTileThreads, smem, st>>>(p);
+  fn<<<dim3(p.row_tiles * p.Hkv, p.S), kTileThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
