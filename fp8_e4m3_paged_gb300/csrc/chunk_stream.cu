@@ -29,9 +29,11 @@
 //
 // Measured (32 heads over 8, D 128): 57 requests of one token with window 16384,
 // every SM with three CTAs: 6.36 TB/s; 64 ragged requests with window 4096, 404 MB:
-// 90 us, 4.5 TB/s, because 512 CTAs leave some SMs with four of them and some with
+// 80 us, 5.0 TB/s, because 512 CTAs leave some SMs with four of them and some with
 // three.  One request and window 1024: 8.6 us, most of it the launch and the chain
 // lengths -> block table -> rows -> join.
+#include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -121,9 +123,34 @@ __device__ __forceinline__ uint32_t word(const uint4& w, int i) {
   return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
 }
 
+// The request with the r-th most positions (at most kThreadsS requests); `key` is room
+// for kThreadsS + 1 (a static array would cost the fourth CTA of an SM).
+__device__ __forceinline__ int by_length(const ChunkParams& p, int* key, int r) {
+  const int t = threadIdx.x;
+  int mine = -1;
+  if (t < p.B) {
+    const ChunkRequest q = chunk_request(p, t);
+    if (q.n > 0) mine = p.window > 0 ? min(q.kv, (int)min((int64_t)p.window + p.sinks, (int64_t)INT_MAX)) : q.kv;
+    key[t] = mine;
+  }
+  __syncthreads();
+  if (t < p.B) {
+    int rank = 0;
+    for (int i = 0; i < p.B; ++i) {
+      const int k = key[i];
+      rank += k > mine || (k == mine && i < t);
+    }
+    if (rank == r) key[kThreadsS] = t;
+  }
+  __syncthreads();
+  const int b = key[kThreadsS];
+  __syncthreads();
+  return b;
+}
+
 template <int D, int FMT, int DT, int NQ>
 __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
-    chunk_stream(const __grid_constant__ ChunkParams p, const int clustered) {
+    chunk_stream(const __grid_constant__ ChunkParams p, const int clustered, const int sorted) {
   using C = StreamCfg<D, NQ>;
   constexpr int ST = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -134,8 +161,11 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
   // KV heads next to each other, so that the CTAs that read one token's heads (adjacent
-  // in memory) run at the same time
-  const int g = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv, s = blockIdx.y;
+  // in memory) run at the same time; the requests from the longest where there are
+  // several CTAs to an SM: the last ones, which only some SMs get, are then short.
+  // 64 requests of 512 to 65536 positions in a window of 4096: 80 us so, 90 by index.
+  const int g = blockIdx.x % p.Hkv, s = blockIdx.y;
+  const int b = sorted ? by_length(p, reinterpret_cast<int*>(sML), blockIdx.x / p.Hkv) : blockIdx.x / p.Hkv;
   const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
@@ -623,7 +653,11 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
   const bool clustered = chunk_clustered(plan);
   cfg.attrs = &attr;
   cfg.numAttrs = clustered ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fn, p, (int)clustered);
+  // (by_length takes up to 1 us: 13.9 us instead of 12.9 for 16 equal requests of 1000
+  // positions, which this leaves out)
+  const bool sorted = p.B <= kThreadsS && (int64_t)p.B * p.Hkv * p.S * chunks >= 2 * (int64_t)plan->num_sms &&
+                      (p.window > 0 ? std::min(p.window, p.max_kv_len) : p.max_kv_len) >= 1024;
+  return cudaLaunchKernelEx(&cfg, fn, p, (int)clustered, (int)sorted);
 }
 
 template <int D, int FMT, int DT>
