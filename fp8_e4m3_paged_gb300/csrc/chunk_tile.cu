@@ -64,6 +64,11 @@ template <int D>
 struct TileCfg {
   static constexpr int kNQ = D == 256 ? 1 : 2;
   static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 4;  // K stages, and V stages
+  // V's barriers: one per stage; D = 256: one per half (64 positions) of the only stage,
+  // which is decoded anew as soon as PV of that half is done.  (With one for the
+  // whole tile, PV of the next tile waited for 2500 cycles of decode behind PV of this
+  // one: 87 us for 1000 queries of 6 heads on 8192 positions, 82 so.)
+  static constexpr int kVStages = D == 256 ? 2 : kStages;
   static constexpr int kOpBytes = kT * D * 2;
   static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
   static constexpr int kRowsIt = 32 / kCh;    // rows a warp moves at a time
@@ -313,13 +318,14 @@ __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt,
     }
     if constexpr (DO_V) {
       bad |= clean_v<D, FMT>(vr, ok_now, lane);
-      if (j >= NS && !warp_wait(&mt.v_empty[st], empty_parity, abort_flag)) {
+      const int vs = C::kNQ == 1 ? w / 2 : st;
+      if (j >= NS && !warp_wait(&mt.v_empty[vs], empty_parity, abort_flag)) {
         ok = false;
         break;
       }
       store_rows<D, FMT>(smem + C::kOffV + st * C::kOpBytes, vr, 32 * w, lane);
       fence_proxy_async_smem();
-      mbar_arrive(&mt.v_full[st]);
+      mbar_arrive(&mt.v_full[vs]);
       fetch_v();
     }
     ok_now = ok_next;
@@ -420,7 +426,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&mt.k_full[i], 128);
       mbar_init(&mt.k_empty[i], nq);
-      mbar_init(&mt.v_full[i], 128);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(&mt.v_full[i], NQ == 1 ? 64 : 128);
       mbar_init(&mt.v_empty[i], nq);
     }
     for (int i = 0; i < 2; ++i) {
@@ -579,7 +587,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       };
       // PV of half h, once every warp has written its rows of P
       auto issue_pv = [&](int j, int h) {
-        if (h == 0) ok = ok && warp_wait(&mt.v_full[j % NS], (j / NS) & 1, abort_flag);
+        const int vs = NQ == 1 ? h : j % NS;
+        if (NQ == 1 || h == 0) ok = ok && warp_wait(&mt.v_full[vs], (j / NS) & 1, abort_flag);
         ok = ok && warp_wait(&mt.p_ready[q][h], j & 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
@@ -591,8 +600,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
             mma_ts(tmem + C::kColO + q * D, tmem + buf_of(j) * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
                    idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
           }
+          if (NQ == 1 || h == 1) mma_commit(&mt.v_empty[vs]);
           if (h == 1) {
-            mma_commit(&mt.v_empty[j % NS]);
             if (j + 1 == n_tiles)
               mma_commit(&mt.o_all[q]);
             else if (NQ == 1)
