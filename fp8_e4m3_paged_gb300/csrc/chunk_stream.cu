@@ -30,7 +30,7 @@
 // Measured (32 heads over 8, D 128): 57 requests of one token with window 16384,
 // every SM with three CTAs: 6.36 TB/s; 64 ragged requests with window 4096, 404 MB:
 // 80 us, 5.0 TB/s, because 512 CTAs leave some SMs with four of them and some with
-// three.  One request and window 1024: 8.6 us, most of it the launch and the chain
+// three.  One request and window 1024: 8.3 us, most of it the launch and the chain
 // lengths -> block table -> rows -> join.
 #include <algorithm>
 #include <climits>
@@ -572,9 +572,12 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       acc[k] = make_float4(y[0], y[1], y[2], y[3]);
     }
   }
-  auto write_out = [&](int r, int d, const float4& y, float L) {
+  auto out_at = [&](int r, int d) {
+    return p.out + (int64_t)(req.row0 + token_of(r)) * p.o_st + (int64_t)head_of(r) * p.o_sh + d;
+  };
+  auto write_out = [&](uint16_t* to, const float4& y, float L) {
     const float f = vs / L;
-    *reinterpret_cast<uint2*>(p.out + (int64_t)(req.row0 + token_of(r)) * p.o_st + (int64_t)head_of(r) * p.o_sh + d) =
+    *reinterpret_cast<uint2*>(to) =
         L == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_out<DT>(y.x * f, y.y * f), pack_out<DT>(y.z * f, y.w * f));
   };
   if (clustered) {
@@ -590,30 +593,42 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       if (r >= RC) continue;
       const int owner = x / run;
       peer_store(peer_addr(items + s * run + (x - owner * run), owner), acc[k]);
-      if (x % (D / 4) == 0)
-        for (int q = 0; q < p.S; ++q) peer_store(peer_addr(pairs + s * 16 + r, q), make_float2(Ms[k], Ls[k]));
+      if (x % (D / 4) < p.S)  // one thread of the row per CTA
+        peer_store(peer_addr(pairs + s * 16 + r, x % (D / 4)), make_float2(Ms[k], Ls[k]));
     }
     __syncwarp();
     cluster_arrive();
+    // (the first item's place, while the others arrive)
+    const int x0 = min(s * run + tid, C::kItems - 1);
+    uint16_t* const to0 = out_at(x0 / (D / 4), (x0 % (D / 4)) * 4);
     cluster_wait();
     for (int i = tid; i < run; i += kThreadsS) {
       const int x = s * run + i, r = x / (D / 4), d = (x % (D / 4)) * 4;
       if (r >= RC) continue;
-      float M = kNoMax, L = 0.f;
-      for (int q = 0; q < p.S; ++q) M = fmaxf(M, pairs[q * 16 + r].x);
-      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < p.S; ++q) {
-        const float2 ml = pairs[q * 16 + r];
-        const float4 y = items[q * run + i];
-        if (ml.x == kNoMax && ml.y == 0.f) continue;  // saw nothing
-        const float a = part_weight(ml.x, M);
-        L = fmaf(a, ml.y, L);
-        z.x = fmaf(a, y.x, z.x);
-        z.y = fmaf(a, y.y, z.y);
-        z.z = fmaf(a, y.z, z.z);
-        z.w = fmaf(a, y.w, z.w);
+      // (all loads first; partitions past S read the last one's)
+      float2 ml[kChunkClusterMax];
+      float4 y[kChunkClusterMax];
+#pragma unroll
+      for (int q = 0; q < kChunkClusterMax; ++q) {
+        const int at = min(q, p.S - 1);
+        ml[q] = pairs[at * 16 + r];
+        y[q] = items[at * run + i];
       }
-      write_out(r, d, z, L);
+      float M = kNoMax, L = 0.f;
+#pragma unroll
+      for (int q = 0; q < kChunkClusterMax; ++q) M = fmaxf(M, ml[q].x);
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kChunkClusterMax; ++q) {
+        if (q >= p.S || (ml[q].x == kNoMax && ml[q].y == 0.f)) continue;  // saw nothing
+        const float a = part_weight(ml[q].x, M);
+        L = fmaf(a, ml[q].y, L);
+        z.x = fmaf(a, y[q].x, z.x);
+        z.y = fmaf(a, y[q].y, z.y);
+        z.z = fmaf(a, y[q].z, z.z);
+        z.w = fmaf(a, y[q].w, z.w);
+      }
+      write_out(i == tid ? to0 : out_at(r, d), z, L);
     }
     return;
   }
@@ -628,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
           make_float4(acc[k].x * kChunkInvPShift, acc[k].y * kChunkInvPShift, acc[k].z * kChunkInvPShift,
                       acc[k].w * kChunkInvPShift);
     } else {
-      write_out(r, d, acc[k], Ls[k]);
+      write_out(out_at(r, d), acc[k], Ls[k]);
     }
   }
 }
