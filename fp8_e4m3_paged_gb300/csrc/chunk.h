@@ -25,6 +25,7 @@ struct ChunkParams {
   int32_t B, total_q, max_q, Hq, Hkv, G, S;
   int32_t page_size, max_kv_len, num_kv_blocks;
   uint64_t page_div;       // as Params::page_div
+  uint64_t g_div, s_div, hkv_div;  // the same for G, S and Hkv
   int32_t window, sinks;   // window 0: every earlier position
   int32_t row_tiles;
   const uint16_t* q;

@@ -205,7 +205,11 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   p->G = plan->group;
   p->S = plan->num_splits;
   p->page_size = plan->page_size;
-  p->page_div = plan->page_size >= 2 ? ~0ull / (uint64_t)plan->page_size + 1 : 0ull;
+  auto inverse = [](int32_t n) { return n >= 2 ? ~0ull / (uint64_t)n + 1 : 0ull; };
+  p->page_div = inverse(plan->page_size);
+  p->g_div = inverse(plan->group);
+  p->s_div = inverse(plan->num_splits);
+  p->hkv_div = inverse(plan->num_kv_heads);
   p->max_kv_len = plan->max_kv_len;
   p->num_kv_blocks = plan->num_kv_blocks;
   p->window = plan->window;

@@ -16,6 +16,21 @@ constexpr float kChunkPShift = 7.0f;           // probabilities are kept times 2
 constexpr float kChunkInvPShift = 1.f / 128;   // p turns subnormal only below 2^-21 of the running maximum
 constexpr float kNoMax = -INFINITY;            // running maximum of a row that has seen nothing
 
+// Packed row -> token of the request and query head of the group; partitions' length;
+// KV head of a CTA.  By products with host-made inverses, for the stream kernel: some
+// five divisions in a row took several hundred of the 14000 cycles of a single-token call (8.3
+// us, 7.9 so).  The tile kernel gains nothing by them.
+struct RowAt {
+  int token, head;
+};
+__device__ __forceinline__ RowAt row_at(const ChunkParams& p, int packed) {
+  const int t = div_page(packed, p.G, p.g_div);
+  return {t, packed - t * p.G};
+}
+__device__ __forceinline__ int token_at(const ChunkParams& p, int packed) { return div_page(packed, p.G, p.g_div); }
+__device__ __forceinline__ int div_s(const ChunkParams& p, int x) { return div_page(x, p.S, p.s_div); }
+__device__ __forceinline__ int div_hkv(const ChunkParams& p, int x) { return div_page(x, p.Hkv, p.hkv_div); }
+
 // One request's new tokens, checked against the plan.
 struct ChunkRequest {
   int row0;  // first row of q

@@ -30,7 +30,7 @@
 // Measured (32 heads over 8, D 128): 57 requests of one token with window 16384,
 // every SM with three CTAs: 6.36 TB/s; 64 ragged requests with window 4096, 404 MB:
 // 80 us, 5.0 TB/s, because 512 CTAs leave some SMs with four of them and some with
-// three.  One request and window 1024: 8.3 us, most of it the launch and the chain
+// three.  One request and window 1024: 7.6 us, most of it the launch and the chain
 // lengths -> block table -> rows -> join.
 #include <algorithm>
 #include <climits>
@@ -102,9 +102,13 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Thread-block cluster: barrier over all its CTAs in two halves, and stores
-// into a peer's shared memory (the place that `p` has in CTA `rank`).
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// Thread-block cluster: barrier over all its CTAs in two halves (the first without
+// order, for a CTA that has only begun), and stores into a peer's shared memory
+// (the place that `p` has in CTA `rank`).
+__device__ __forceinline__ void cluster_here() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
   uint32_t r;
@@ -164,21 +168,21 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   // in memory) run at the same time; the requests from the longest where there are
   // several CTAs to an SM: the last ones, which only some SMs get, are then short.
   // 64 requests of 512 to 65536 positions in a window of 4096: 80 us so, 90 by index.
-  const int g = blockIdx.x % p.Hkv, s = blockIdx.y;
-  const int b = sorted ? by_length(p, reinterpret_cast<int*>(sML), blockIdx.x / p.Hkv) : blockIdx.x / p.Hkv;
+  const int nth = div_hkv(p, blockIdx.x), g = blockIdx.x - nth * p.Hkv, s = blockIdx.y;
+  const int b = sorted ? by_length(p, reinterpret_cast<int*>(sML), nth) : nth;
   const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
   const int RC = min(kR, req.n * p.G - row_first);
   if (RC <= 0) return;  // every CTA of the cluster
-  if (clustered) cluster_arrive();  // peers may write here once all have come this far
+  if (clustered) cluster_here();  // peers may write here once all have come this far (ordered: 0.4 us more)
   const int64_t plane = (int64_t)p.total_q * p.Hq;
-  auto token_of = [&](int r) { return (row_first + r) / p.G; };
-  auto head_of = [&](int r) { return g * p.G + (row_first + r) % p.G; };
+  auto token_of = [&](int r) { return token_at(p, row_first + r); };
+  auto head_of = [&](int r) { return g * p.G + row_at(p, row_first + r).head; };
   auto vec_of = [&](int r) { return (int64_t)(req.row0 + token_of(r)) * p.Hq + head_of(r); };
 
   const ChunkSpan span = chunk_span(p, req, token_of(0), token_of(RC - 1));
-  int per = (span.U + p.S - 1) / p.S;
+  int per = div_s(p, span.U + p.S - 1);
   per = (per + kBlk * kWarps - 1) / (kBlk * kWarps) * (kBlk * kWarps);
   const int u0 = (int)min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
   if (u0 >= u1 && p.S > 1 && !clustered) {
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   };
   if (clustered) {
     // ---------------------------------------------------------- join the cluster
-    const int run = (C::kItems + p.S - 1) / p.S;  // item x belongs to CTA x / run
+    const int run = div_s(p, C::kItems + p.S - 1);  // item x belongs to CTA x / run
     float2* pairs = reinterpret_cast<float2*>(smem + C::kOffPairs);
     float4* items = reinterpret_cast<float4*>(smem + C::kOffItems);
     __syncwarp();
@@ -591,7 +595,9 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
     for (int k = 0; k < C::kIter; ++k) {
       const int x = tid + k * kThreadsS, r = x / (D / 4);
       if (r >= RC) continue;
-      const int owner = x / run;
+      int owner = 0;
+#pragma unroll
+      for (int q = 1; q < kChunkClusterMax; ++q) owner += x >= q * run;
       peer_store(peer_addr(items + s * run + (x - owner * run), owner), acc[k]);
       if (x % (D / 4) < p.S)  // one thread of the row per CTA
         peer_store(peer_addr(pairs + s * 16 + r, x % (D / 4)), make_float2(Ms[k], Ls[k]));
