@@ -252,7 +252,8 @@ extern "C" int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chun
   const int rc = build_chunk(plan, a, &p);
   if (rc != FP8KV_OK || plan->batch == 0 || plan->total_q == 0) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = plan->kernel == FP8KV_CHUNK_STREAM ? launch_chunk_stream(plan, p, st) : launch_chunk_tile(plan, p, st);
+  cudaError_t e =
+      plan->kernel == FP8KV_CHUNK_STREAM ? launch_chunk_stream(plan, p, st) : launch_chunk_tile(plan, p, st);
   if (e == cudaSuccess && p.S > 1 && !chunk_clustered(plan)) e = launch_chunk_join(plan, p, st);
   return done(e);
 }

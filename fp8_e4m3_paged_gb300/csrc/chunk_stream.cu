@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
           if (D >= 128) {
             vr[j] = *reinterpret_cast<const uint4*>(vrows + r * D + (((rq + 8 * i) ^ v_swz(r)) * 16));
           } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(vrows + r * D + (((rq >> 1) ^ v_swz(r)) * 16) + (rq & 1) * 8);
+            const uint2 y =
+                *reinterpret_cast<const uint2*>(vrows + r * D + (((rq >> 1) ^ v_swz(r)) * 16) + (rq & 1) * 8);
             vr[j] = make_uint4(y.x, y.y, 0u, 0u);
           }
         }
