@@ -130,6 +130,11 @@ CASES = {
     "one_chunk": Case([(150, 3000)], Hq=8, Hkv=2, D=128),          # partitions by waves
     "one_chunk_wide": Case([(130, 2100)], Hq=3, Hkv=1, D=256, dtype=torch.bfloat16),
     "many_vectors_few_positions": Case([(40, 90)], Hq=12, Hkv=1, D=64),
+    # enough CTAs and positions that the stream kernel takes the requests by length
+    "ragged_decodes": Case([(1 if i % 5 else 0, 1 + (i * 397) % 1500) for i in range(128)], Hq=6, Hkv=3, D=64),
+    "ragged_window_decodes": Case([(1 + i % 2, 2 + (i * 731) % 1800) for i in range(90)], Hq=8, Hkv=4, D=64,
+                                  window=1100, sinks=4, dtype=torch.bfloat16),
+    "more_requests_than_are_sorted": Case([(1, 1 + (i * 211) % 1200) for i in range(131)], Hq=4, Hkv=4, D=64),
 }
 
 
