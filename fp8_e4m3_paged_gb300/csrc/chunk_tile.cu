@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include "chunk_common.cuh"
+#include "chunk_schedule.h"
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -85,7 +86,8 @@ struct TileCfg {
 struct TileMeta {
   uint64_t q_full[2], drain[2];
   uint64_t k_full[kStagesMax], k_empty[kStagesMax], v_full[kStagesMax], v_empty[kStagesMax];
-  uint64_t s_full[2], p_ready[2][2], o_all[2];  // P by halves; o_all: a row tile's last PV is done
+  uint64_t s_full[2], o_all[2];                 // o_all: a row tile's last PV is done
+  uint64_t p_ready[2][2];                       // P by halves (p_ready_at)
   uint64_t o_done;                              // D = 256: PV(j) is done, every tile but the last
   alignas(16) uint32_t valid[8][4];             // per tile (j % 8): positions whose block is in range
   int64_t place[2][4][32];                      // per decoder warp: byte offsets of its rows
@@ -589,7 +591,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       auto issue_pv = [&](int j, int h) {
         const int vs = NQ == 1 ? h : j % NS;
         if (NQ == 1 || h == 0) ok = ok && warp_wait(&mt.v_full[vs], (j / NS) & 1, abort_flag);
-        ok = ok && warp_wait(&mt.p_ready[q][h], j & 1, abort_flag);
+        const BarrierAt pr = p_ready_at(NQ, q, h, j);
+        ok = ok && warp_wait(&mt.p_ready[pr.slot][h], pr.parity, abort_flag);
         if (!ok) return;
         tc_fence_after();
         const uint64_t vd = vdesc + (uint64_t)(((j % NS) * C::kOpBytes) >> 4);
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
           tmem_st32(tS + 32 * h, y);  // over S, all of which is in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&mt.p_ready[q][h]);
+          if (lane == 0) mbar_arrive(&mt.p_ready[p_ready_at(NQ, q, h, j).slot][h]);
           if (issuer) {
             if (NQ == 1) {
               if (h == 1 && j + 1 < n_tiles) issue_qk(j + 1);  // its buffer held P(j-1)
