@@ -502,6 +502,19 @@ def _rows(t, name: str):
     return t.stride()[:2]
 
 
+def _table(t, name: str):
+    """Address and row stride of a block table [B][columns]."""
+    import torch
+
+    rows, cols = t.shape if t.dim() == 2 else (-1, -1)
+    _check(t.dtype == torch.int32 and rows >= 0 and (t.stride(1) == 1 or cols <= 1),
+           f"{name}: int32 [B][columns], columns contiguous")
+    if rows <= 1:  # one request: its next row is never read, whatever the stride says
+        return _ptr(t), max(t.stride(0), cols)
+    _check(t.stride(0) >= cols, f"{name}: rows that overlap (a table that all requests share needs a copy for each)")
+    return _ptr(t), t.stride(0)
+
+
 def make_chunk_desc(*, batch: int, total_q: int, max_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                     page_size: int, max_kv_len: int, max_blocks: int, num_kv_blocks: int, window: int = 0,
                     sinks: int = 0, dtype: int = DTYPE_F16, kv_format: int = KV_E4M3, num_sms: int = 0,
@@ -524,16 +537,13 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
 
     q / out: fp16 or bf16 [total_q][Hq][D] (any row and head strides, d
     contiguous); k_cache / v_cache: uint8 [blocks][page][Hkv][D] views;
-    block_table: int32 [B][columns]; cu_q: int32 [B+1]; kv_len: int32 [B];
-    workspace: a uint8 tensor of at least plan.workspace_bytes bytes, its
+    block_table: int32 [B][columns], a row of its own for each request; cu_q:
+    int32 [B+1]; kv_len: int32 [B]; workspace: a uint8 tensor of at least plan.workspace_bytes bytes, its
     first four bytes (the status word) zeroed once.  The plan's sizes must be
     those of the tensors."""
-    import torch
-
     _torch_dtype(q, DTYPE_F16, DTYPE_BF16)
     _check(out.dtype == q.dtype and out.shape == q.shape, "out: same type and shape as q")
-    _check(block_table.dtype == torch.int32 and block_table.dim() == 2 and
-           (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [B][columns]")
+    table, table_stride = _table(block_table, "block_table")
     _int32(cu_q, block_table.shape[0] + 1, "cu_q")
     _int32(kv_len, block_table.shape[0], "kv_len")
     _device_scale(k_scale_dev, "k_scale_dev")
@@ -544,9 +554,7 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
     a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
     a.k_stride_block, a.k_stride_token, a.k_stride_head = _pages(k_cache, "k_cache")
     a.v_stride_block, a.v_stride_token, a.v_stride_head = _pages(v_cache, "v_cache")
-    a.block_table = _ptr(block_table)
-    # a table of one request may carry any stride: its next row is never read
-    a.block_table_stride = max(block_table.stride(0), block_table.shape[1])
+    a.block_table, a.block_table_stride = table, table_stride
     a.cu_q, a.kv_len = _ptr(cu_q), _ptr(kv_len)
     a.softmax_scale, a.k_scale, a.v_scale = float(softmax_scale), float(k_scale), float(v_scale)
     a.k_scale_dev, a.v_scale_dev = _ptr(k_scale_dev), _ptr(v_scale_dev)
@@ -579,15 +587,12 @@ def make_cache_read_args(*, k_cache, v_cache, block_table, cu_len, k_out, v_out,
     [B][columns]; cu_len: int32 [B+1]; start: optional int32 [B]; k_out /
     v_out: fp16, bf16 or fp32 [total][Hkv][D] (d contiguous); status: optional
     int32 tensor of one element."""
-    import torch
-
     a = CacheReadArgs()
     a.dtype = _torch_dtype(k_out, DTYPE_F16, DTYPE_BF16, DTYPE_F32)
     _check(v_out.dtype == k_out.dtype and v_out.shape == k_out.shape, "v_out: same type and shape as k_out")
     _check(k_cache.shape == v_cache.shape and k_out.shape[1:] == k_cache.shape[2:],
            "k_out / v_out: [total][Hkv][D] with the caches' Hkv and D")
-    _check(block_table.dtype == torch.int32 and block_table.dim() == 2 and
-           (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [B][columns]")
+    table, table_stride = _table(block_table, "block_table")
     _int32(cu_len, block_table.shape[0] + 1, "cu_len")
     if start is not None:
         _int32(start, block_table.shape[0], "start")
@@ -600,8 +605,7 @@ def make_cache_read_args(*, k_cache, v_cache, block_table, cu_len, k_out, v_out,
     a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
     a.kc_stride_block, a.kc_stride_token, a.kc_stride_head = _pages(k_cache, "k_cache")
     a.vc_stride_block, a.vc_stride_token, a.vc_stride_head = _pages(v_cache, "v_cache")
-    a.block_table = _ptr(block_table)
-    a.block_table_stride = max(block_table.stride(0), block_table.shape[1])
+    a.block_table, a.block_table_stride = table, table_stride
     a.cu_len, a.start = _ptr(cu_len), _ptr(start)
     a.k_out, (a.ko_stride_token, a.ko_stride_head) = _ptr(k_out), _rows(k_out, "k_out")
     a.v_out, (a.vo_stride_token, a.vo_stride_head) = _ptr(v_out), _rows(v_out, "v_out")

@@ -287,3 +287,47 @@ def test_binding_refuses_tensors_that_do_not_fit(B):
                 dict(start=cu), dict(block_table=table.long())):
         with pytest.raises(ValueError):
             B.make_cache_read_args(**{**good, **bad})
+
+
+def _table_calls(B):
+    """Both calls that take a block table, as functions of it."""
+    import torch
+
+    q = torch.zeros(4, 8, 64, dtype=torch.float16)
+    cache = torch.zeros(5, 16, 2, 64, dtype=torch.uint8)
+    k = torch.zeros(5, 2, 64, dtype=torch.float16)
+
+    def ints(n):
+        return torch.zeros(n, dtype=torch.int32)
+
+    return [lambda t: B.make_chunk_args(q=q, out=torch.zeros_like(q), k_cache=cache, v_cache=cache,
+                                        workspace=torch.zeros(256, dtype=torch.uint8), softmax_scale=1.0, block_table=t,
+                                        cu_q=ints(t.shape[0] + 1), kv_len=ints(t.shape[0])),
+            lambda t: B.make_cache_read_args(k_cache=cache, v_cache=cache, block_table=t, cu_len=ints(t.shape[0] + 1),
+                                             k_out=k, v_out=torch.zeros_like(k))]
+
+
+def test_binding_keeps_a_block_table_inside_its_storage(B):
+    """Rows of the table as the call reads them: address + request * stride, inside of the tensor for every request."""
+    import torch
+
+    base = torch.arange(24, dtype=torch.int32)
+    for call in _table_calls(B):
+        for t in (base[:3].view(1, 3).expand(2, -1),          # one row for all requests
+                  base.as_strided((3, 4), (2, 1)),             # rows that overlap
+                  base[:1].view(1, 1).expand(5, -1)):
+            with pytest.raises(ValueError):
+                call(t)
+        for t in (base.view(4, 6), base.view(4, 6)[:, :5], base.view(4, 6)[::2], base.view(1, 24), base.view(24, 1),
+                  base[:6].view(1, 6).expand(1, -1), base.as_strided((1, 6), (0, 1)), base.view(4, 6)[:0]):
+            a = call(t)
+            assert a.block_table_stride >= t.shape[1]
+            if t.shape[0] == 0:
+                continue
+            end = a.block_table + 4 * ((t.shape[0] - 1) * a.block_table_stride + t.shape[1])
+            assert end <= base.data_ptr() + 4 * base.numel()
+            for b in range(t.shape[0]):
+                at = (a.block_table - base.data_ptr()) // 4 + b * a.block_table_stride
+                assert base[at:at + t.shape[1]].tolist() == t[b].tolist()
+        with pytest.raises(ValueError):
+            call(base.view(6, 4).t())                          # columns not contiguous
