@@ -152,6 +152,7 @@ class ChunkDesc(ctypes.Structure):
 
 
 class ChunkPlan(ctypes.Structure):
+    same = least = None  # sizes that the tensors must have (fp8kv_attn_chunk_plan)
     _fields_ = [(n, ctypes.c_int32) for n in (
         "revision", "batch", "total_q", "max_q", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
         "max_kv_len", "max_blocks", "num_kv_blocks", "window", "sinks", "dtype", "kv_format", "group", "kernel",
@@ -162,6 +163,7 @@ class ChunkPlan(ctypes.Structure):
 
 
 class ChunkArgs(ctypes.Structure):
+    same = least = None  # sizes that the tensors have (make_chunk_args; None: filled by hand)
     _fields_ = [
         ("q", ctypes.c_void_p), ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
         ("out", ctypes.c_void_p), ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
@@ -528,6 +530,9 @@ def fp8kv_attn_chunk_plan(desc: ChunkDesc) -> ChunkPlan:
     rc = lib.fp8kv_attn_chunk_plan(ctypes.byref(desc), ctypes.byref(plan))
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_chunk_plan")
+    # what the tensors must have (make_chunk_args notes what they have): the same ..., and at least ...
+    plan.same = (plan.num_q_heads, plan.num_kv_heads, plan.head_dim, plan.page_size, plan.dtype)
+    plan.least = (plan.batch, plan.total_q, plan.max_blocks, plan.num_kv_blocks)
     return plan
 
 
@@ -538,10 +543,12 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
     q / out: fp16 or bf16 [total_q][Hq][D] (any row and head strides, d
     contiguous); k_cache / v_cache: uint8 [blocks][page][Hkv][D] views;
     block_table: int32 [B][columns], a row of its own for each request; cu_q:
-    int32 [B+1]; kv_len: int32 [B]; workspace: a uint8 tensor of at least plan.workspace_bytes bytes, its
-    first four bytes (the status word) zeroed once.  The plan's sizes must be
-    those of the tensors."""
-    _torch_dtype(q, DTYPE_F16, DTYPE_BF16)
+    int32 [B+1]; kv_len: int32 [B]; workspace: a uint8 tensor of at least
+    plan.workspace_bytes bytes, its first four bytes (the status word) zeroed
+    once.  fp8kv_attn_chunk compares the tensors with the plan: the same heads,
+    head dim, page size and type, and at least its requests, rows, table columns
+    and blocks."""
+    dtype = _torch_dtype(q, DTYPE_F16, DTYPE_BF16)
     _check(out.dtype == q.dtype and out.shape == q.shape, "out: same type and shape as q")
     table, table_stride = _table(block_table, "block_table")
     _int32(cu_q, block_table.shape[0] + 1, "cu_q")
@@ -559,10 +566,20 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
     a.softmax_scale, a.k_scale, a.v_scale = float(softmax_scale), float(k_scale), float(v_scale)
     a.k_scale_dev, a.v_scale_dev = _ptr(k_scale_dev), _ptr(v_scale_dev)
     a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _check(k_cache.shape[1:] == v_cache.shape[1:], "v_cache: pages of the same shape as k_cache's")
+    _check(q.shape[2] == k_cache.shape[3], "q: the caches' head dim")
+    a.same = (q.shape[1], *k_cache.shape[2:], k_cache.shape[1], dtype)
+    a.least = (block_table.shape[0], q.shape[0], block_table.shape[1], min(k_cache.shape[0], v_cache.shape[0]))
     return a
 
 
 def fp8kv_attn_chunk(plan: ChunkPlan, args: ChunkArgs, stream: int = 0) -> None:
+    same = args.same
+    if same is not None and plan.same is not None:
+        _check(same == plan.same, "the plan's heads, head dim, page size and type are not those of the tensors")
+        (b, n, c, k), (pb, pn, pc, pk) = args.least, plan.least
+        if b < pb or n < pn or c < pc or k < pk:
+            raise ValueError("the plan has more requests, rows, table columns or blocks than the tensors")
     rc = lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(args), stream)
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_chunk")

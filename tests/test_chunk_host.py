@@ -331,3 +331,38 @@ def test_binding_keeps_a_block_table_inside_its_storage(B):
                 assert base[at:at + t.shape[1]].tolist() == t[b].tolist()
         with pytest.raises(ValueError):
             call(base.view(6, 4).t())                          # columns not contiguous
+
+
+def test_binding_compares_plan_and_tensors(B, monkeypatch):
+    """A plan made for other sizes than the tensors' would read or write outside of them."""
+    import torch
+
+    def call(**kw):
+        n = dict(B=2, rows=4, Hq=8, Hkv=2, D=64, page=16, blocks=5, v_blocks=5, v_page=16, v_heads=2, cols=3,
+                 dtype=torch.float16)
+        n.update(kw)
+        q = torch.zeros(n["rows"], n["Hq"], n["D"], dtype=n["dtype"])
+        return B.make_chunk_args(
+            q=q, out=torch.zeros_like(q), k_cache=torch.zeros(n["blocks"], n["page"], n["Hkv"], 64, dtype=torch.uint8),
+            v_cache=torch.zeros(n["v_blocks"], n["v_page"], n["v_heads"], 64, dtype=torch.uint8),
+            workspace=torch.zeros(256, dtype=torch.uint8), softmax_scale=1.0,
+            block_table=torch.zeros(n["B"], n["cols"], dtype=torch.int32),
+            cu_q=torch.zeros(n["B"] + 1, dtype=torch.int32), kv_len=torch.zeros(n["B"], dtype=torch.int32))
+
+    launched = []
+    monkeypatch.setattr(B.lib, "fp8kv_attn_chunk", lambda *a: launched.append(a) or B.OK)
+    plan = B.fp8kv_attn_chunk_plan(_desc(B, batch=2, total_q=4, max_q=4, head_dim=64, max_kv_len=48, max_blocks=3,
+                                         num_kv_blocks=5))
+    for kw in (dict(v_page=8), dict(v_heads=1), dict(D=128)):      # tensors that do not belong together
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(B=1), dict(rows=3), dict(Hq=4), dict(Hkv=1, v_heads=1), dict(page=8, v_page=8), dict(blocks=4),
+               dict(v_blocks=2), dict(cols=2), dict(dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            B.ChunkCall(plan, call(**kw)).run(0)
+    assert not launched
+    for kw in ({}, dict(B=3), dict(rows=9), dict(blocks=7, v_blocks=6), dict(cols=4)):
+        B.ChunkCall(plan, call(**kw)).run(0)
+    assert len(launched) == 5
+    B.fp8kv_attn_chunk(plan, _args(B, plan), 0)                    # a struct filled by hand
+    assert len(launched) == 6
