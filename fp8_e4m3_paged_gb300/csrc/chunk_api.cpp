@@ -26,6 +26,12 @@ bool strides_ok(const int64_t* s, int n, int64_t unit) {
 bool apart(int64_t rows, int64_t stride_row, int64_t heads, int64_t stride_head) {
   return (rows < 2 || stride_row > 0) && (heads < 2 || stride_head > 0);
 }
+// Finite host scales, or device floats on their boundary.
+template <class Args>
+bool scales_ok(const Args& a) {
+  return aligned(a.k_scale_dev, 4) && aligned(a.v_scale_dev, 4) && (a.k_scale_dev || std::isfinite(a.k_scale)) &&
+         (a.v_scale_dev || std::isfinite(a.v_scale));
+}
 bool fp8_format(int32_t f) { return f == FP8KV_KV_E4M3 || f == FP8KV_KV_E5M2; }
 int done(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ECUDA; }
 
@@ -194,8 +200,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   if (plan->max_kv_len > 0 && (!a->block_table || !aligned(a->block_table, 4))) return FP8KV_EINVAL;
   if (a->block_table_stride < plan->max_blocks) return FP8KV_EINVAL;
   if (!std::isfinite(a->softmax_scale)) return FP8KV_EINVAL;
-  if (!a->k_scale_dev && !std::isfinite(a->k_scale)) return FP8KV_EINVAL;
-  if (!a->v_scale_dev && !std::isfinite(a->v_scale)) return FP8KV_EINVAL;
+  if (!scales_ok(*a)) return FP8KV_EINVAL;
 
   p->B = plan->batch;
   p->total_q = plan->total_q;
@@ -279,9 +284,9 @@ extern "C" int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_strea
   if (!apart(a->total, es[0], a->num_kv_heads, es[1]) || !apart(a->total, es[2], a->num_kv_heads, es[3]))
     return FP8KV_EINVAL;
   if (!a->block_table || !a->cu_len || a->block_table_stride < a->max_blocks) return FP8KV_EINVAL;
-  if (!aligned(a->block_table, 4) || !aligned(a->cu_len, 4) || !aligned(a->start, 4)) return FP8KV_EINVAL;
-  if (!a->k_scale_dev && !std::isfinite(a->k_scale)) return FP8KV_EINVAL;
-  if (!a->v_scale_dev && !std::isfinite(a->v_scale)) return FP8KV_EINVAL;
+  if (!aligned(a->block_table, 4) || !aligned(a->cu_len, 4) || !aligned(a->start, 4) || !aligned(a->status, 4))
+    return FP8KV_EINVAL;
+  if (!scales_ok(*a)) return FP8KV_EINVAL;
   return done(launch_cache_read(*a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -366,3 +366,12 @@ def test_binding_compares_plan_and_tensors(B, monkeypatch):
     assert len(launched) == 5
     B.fp8kv_attn_chunk(plan, _args(B, plan), 0)                    # a struct filled by hand
     assert len(launched) == 6
+
+
+def test_device_words_off_their_boundary_are_refused(B):
+    """Device scales and the status word: a misaligned access would fault."""
+    plan = B.fp8kv_attn_chunk_plan(_desc(B))
+    for kw in (dict(k_scale_dev=FAKE + 2), dict(v_scale_dev=FAKE + 1)):
+        assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(_args(B, plan, **kw)), None) == B.EINVAL
+        assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, **kw)), None) == B.EINVAL
+    assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, status=FAKE + 2)), None) == B.EINVAL
