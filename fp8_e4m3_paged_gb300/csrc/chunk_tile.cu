@@ -91,6 +91,7 @@ struct TileMeta {
   uint64_t o_done;                              // D = 256: PV(j) is done, every tile but the last
   alignas(16) uint32_t valid[8][4];             // per tile (j % 8): positions whose block is in range
   int64_t place[2][4][32];                      // per decoder warp: byte offsets of its rows
+  float sum[256];                               // the rows' sums, for non-finite V codes
   uint32_t tmem, abort, vbad;
 };
 static_assert(sizeof(TileMeta) <= kMetaBytes, "meta block");
@@ -723,6 +724,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
         const bool dead = l == 0.f, parts = p.S > 1;
         const float f = parts ? kChunkInvPShift : (dead ? 0.f : vs / l);
         if (parts && live) p.ml[s * plane + vec] = make_float2(m, l * kChunkInvPShift);
+        mt.sum[rr] = l;
         // A thread holds a row, but a store instruction had better write few rows: 128
         // bytes of each of the warp's 32 rows go through shared memory (the
         // warp's part of Q, all reads of which are done; 16-byte chunk c of row r
@@ -805,10 +807,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       const float v = nonfinite_value(kind);
       if (p.S > 1) {
         p.partial[(s * plane + vec_of(i)) * D + d] = v;
-      } else {
+      } else if (mt.sum[i] != 0.f) {
+        // over the row's sum, as every other element: an infinity in a row that is NaN
+        // for its logits stays NaN
         const int rr = work.row0 + i;
         p.out[(int64_t)(req.row0 + rr / p.G) * p.o_st + (int64_t)(g * p.G + rr % p.G) * p.o_sh + d] =
-            (uint16_t)(pack_out<DT>(v * vs, 0.f) & 0xFFFFu);
+            (uint16_t)(pack_out<DT>(v * (vs / mt.sum[i]), 0.f) & 0xFFFFu);
       }
     }
   }

@@ -363,3 +363,25 @@ def test_workspace_and_device_of_tensors():
     with pytest.raises(B.Fp8kvError) as e:
         r()
     assert e.value.code == B.EWORKSPACE
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nan_logits_outweigh_infinite_values(D, dtype):
+    """A row that is NaN for its logits (a NaN K code, a NaN query) stays NaN where it also sees an infinite V code."""
+    for requests in ([(4, 90), (3, 40)], [(150, 170)]):
+        c = Case(requests, Hq=4, Hkv=2, D=D, fmt="e5m2", k_scale=0.001, dtype=dtype, seed=6)
+        n, kv = c.requests[0]
+
+        def put(cache, t, g, d, code):
+            cache[c.table[0, t // c.page].long(), t % c.page, g, d] = code
+
+        put(c.v, 5, 0, 9, 0x7C)             # +inf, seen by every row of KV head 0
+        put(c.v, 5, 0, 10, 0xFC)            # -inf
+        put(c.k, kv - 2, 0, 7, 0x7F)        # NaN, seen by the last two rows of KV head 0
+        c.q[0, 1, 3] = float("nan")         # one query of KV head 0
+        ref = c.reference()
+        assert torch.isnan(ref[0][n - 2:n, :2]).all() and torch.isnan(ref[0][0, 1]).all()
+        assert torch.isinf(ref[0][1, 0, 9:11]).all()
+        for kernel, splits in kernels(c):
+            check(Run(c, kernel, splits)(), c, ref)
