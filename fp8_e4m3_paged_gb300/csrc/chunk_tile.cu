@@ -621,7 +621,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       // ====================================================== softmax
       const int rr = q * kM + 32 * (warp & 3) + lane;  // this thread's row of the CTA
       const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-      // (not 0, so that c * -inf stays -inf for masked logits)
+      // (not 0, so that c * -inf stays -inf for masked logits; nor NaN, for the same reason: a
+      // NaN scale goes into the rows' sums at the end)
       const float c = fmaxf(fabsf(cf) * back, 1e-30f);
       ChunkRow row = {INT_MAX, INT_MIN};  // rows past RC: everything, dropped at the end
       if (rr < RC) row = chunk_row(p, req, span, (work.row0 + rr) / p.G);
@@ -707,6 +708,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
         const float2 t = unpair(add2(sum[0], sum[1]));
         l += t.x + t.y;
       }
+      if (cf != cf && l != 0.f) l = cf;
       if (issuer) {
         // every UMMA issued must be done before TMEM is freed
         if (elect_one()) mma_commit(&mt.drain[q]);

@@ -385,3 +385,16 @@ def test_nan_logits_outweigh_infinite_values(D, dtype):
         assert torch.isinf(ref[0][1, 0, 9:11]).all()
         for kernel, splits in kernels(c):
             check(Run(c, kernel, splits)(), c, ref)
+
+
+@pytest.mark.parametrize("name", ["ragged", "wide", "dead_rows", "dead_rows_many", "window_decode"])
+def test_a_nan_scale_reaches_every_row_that_sees_something(name):
+    """Device scales are not known on the host: a NaN must not become finite weights, nor reach rows that see nothing."""
+    c = CASES[name]
+    sees = torch.cat([torch.arange(kv - n, kv) >= 0 for n, kv in c.requests])
+    for kernel, splits in kernels(c):
+        for i in range(2):  # of K, of V
+            r = Run(c, kernel, splits, device_scales=True)
+            r.scales[i].fill_(float("nan"))
+            got = r()[:int(c.cu[-1])]
+            assert torch.isnan(got[sees]).all() and (got[~sees] == 0).all()
