@@ -13,11 +13,12 @@ constexpr int kChunkStreamRows = 16;      // query vectors per CTA of the stream
 constexpr int kChunkClusterMax = 8;       // partitions that the stream kernel joins in one launch (portable cluster size)
 constexpr int kChunkStreamBlock = 16;     // positions per warp step of the stream kernel
 constexpr int kChunkTileTokens = 128;     // positions per tile of the tile kernel
-// Longest partition of the tile kernel: the tensor core's FP32 accumulation
-// truncates, so one sum drifts by about 2^-25 of itself per K16 step; 2048
-// steps (32768 positions) keep that below 2^-14, a quarter of the half-step of an
-// fp16 output.
-constexpr int kChunkMaxPart = 32768;
+// Most positions of one FP32 sum: the tensor core's accumulation truncates, so
+// a sum drifts by about 2^-25 of itself per K16 step; 2048 steps (32768 positions)
+// keep that below 2^-14, a quarter of the half-step of an fp16 output.  The tile
+// kernel sums a partition in one chain, the stream kernel in one per warp.
+constexpr int kChunkMaxSum = 32768;
+constexpr int kChunkStreamWarps = 4;
 inline int chunk_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }  // query vectors per CTA
 
 // Everything the chunk kernels need, resolved on the host.

@@ -46,7 +46,7 @@
 namespace fp8kv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kChunkStreamWarps;
 constexpr int kThreadsS = 32 * kWarps;
 constexpr int kR = kChunkStreamRows;
 constexpr int kBlk = kChunkStreamBlock;

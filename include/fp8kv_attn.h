@@ -390,8 +390,9 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  *
  * Numerical contract: FP32 logits, running maximum and sum; probabilities
  * enter the PV product as fp16 (2^-11 of their own value), accumulated in
- * FP32, and a context is split where one FP32 sum would run over more than 32768 positions; one
- * rounding to q's type at the end.  bf16 queries are scaled to fp16 per row by
+ * FP32; no FP32 sum runs over more than 32768 positions (the plan has as many
+ * partitions as that takes, more than num_splits if need be); one rounding to
+ * q's type at the end.  bf16 queries are scaled to fp16 per row by
  * a power of two, which is exact for elements above 2^-28 of the row's
  * largest.
  *
@@ -424,7 +425,8 @@ typedef struct {
   int32_t dtype;         /* FP8KV_DTYPE_F16 or FP8KV_DTYPE_BF16 (q and out) */
   int32_t kv_format;     /* FP8KV_KV_E4M3 or FP8KV_KV_E5M2 (bf16 caches: FP8KV_EUNSUPPORTED) */
   int32_t num_sms;       /* SMs to plan for; 0 = ask the current device */
-  int32_t num_splits;    /* partitions of the context; 0 = planner's choice */
+  int32_t num_splits;    /* partitions of the context; 0 = planner's choice (raised where an FP32 sum
+                            would run over more than 32768 positions) */
   int32_t kernel;        /* FP8KV_CHUNK_* */
 } fp8kv_chunk_desc;
 

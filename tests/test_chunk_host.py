@@ -375,3 +375,24 @@ def test_device_words_off_their_boundary_are_refused(B):
         assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(_args(B, plan, **kw)), None) == B.EINVAL
         assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, **kw)), None) == B.EINVAL
     assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, status=FAKE + 2)), None) == B.EINVAL
+
+
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+@pytest.mark.parametrize("kernel,chains", [(1, 4), (2, 1)])  # FP32 sums of a partition: one per warp, one
+def test_no_sum_over_more_than_32768_positions(B, kernel, chains, head_dim):
+    """Whatever the batch, the bound of the lengths or the partitions asked for."""
+    for n in (32768, 32769, 131072, 131073, 262144, 1 << 20, 1 << 30):
+        for batch in (1, 64):
+            for splits in (0, 1, 2, 7):
+                p = B.fp8kv_attn_chunk_plan(_desc(
+                    B, batch=batch, total_q=batch, max_q=1, num_q_heads=32, num_kv_heads=8, head_dim=head_dim,
+                    max_kv_len=n, max_blocks=-(-n // 16), kernel=kernel, num_splits=splits))
+                per = -(-n // p.num_splits)
+                per = -(-per // (64 if kernel == 1 else 128)) * (64 if kernel == 1 else 128)
+                assert per <= chains * 32768
+                if splits and n <= splits * chains * 16384:  # no more than it takes
+                    assert p.num_splits == splits
+    # a window bounds the sums by itself
+    p = B.fp8kv_attn_chunk_plan(_desc(B, max_kv_len=1 << 30, max_blocks=1 << 26, window=4096, sinks=4, kernel=kernel,
+                                      num_splits=1))
+    assert p.num_splits == 1

@@ -398,3 +398,14 @@ def test_a_nan_scale_reaches_every_row_that_sees_something(name):
             r.scales[i].fill_(float("nan"))
             got = r()[:int(c.cu[-1])]
             assert torch.isnan(got[sees]).all() and (got[~sees] == 0).all()
+
+
+def test_long_contexts():
+    """Sums cut at 32768 positions: the bound on their truncation is that of such a sum, whatever the context."""
+    c = Case([(1, 140000), (2, 70001)], Hq=2, Hkv=1, D=64, page=64)
+    out, tol, cond = c.reference()
+    for b, (n, kv) in enumerate(c.requests):  # the reference counts a truncation for every K16 step of the context
+        rows = slice(int(c.cu[b]), int(c.cu[b]) + n)
+        tol[rows] -= (kv - 32768) / 16 * 2.0 ** -23 * cond[rows]
+    for kernel, splits in [(0, 0), (1, 1), (1, 2), (2, 1), (2, 9)]:
+        check(Run(c, kernel, splits)(), c, (out, tol, cond))
