@@ -14,11 +14,15 @@ constexpr int kChunkClusterMax = 8;       // partitions that the stream kernel j
 constexpr int kChunkStreamBlock = 16;     // positions per warp step of the stream kernel
 constexpr int kChunkTileTokens = 128;     // positions per tile of the tile kernel
 // Most positions of one FP32 sum: the tensor core's accumulation truncates, so
-// a sum drifts by about 2^-25 of itself per K16 step; 2048 steps (32768 positions)
-// keep that below 2^-14, a quarter of the half-step of an fp16 output.  The tile
-// kernel sums a partition in one chain, the stream kernel in one per warp.
+// a sum drifts by about 2^-25 of itself per K16 step; 2048 steps keep that below
+// 2^-14, a quarter of the half-step of an fp16 output.  The tile kernel sums a
+// partition in one chain, a step for 16 positions; the stream kernel in a chain per
+// warp, two steps for 16 positions (both halves of P).
 constexpr int kChunkMaxSum = 32768;
 constexpr int kChunkStreamWarps = 4;
+inline int64_t chunk_max_part(int32_t kernel) {
+  return kernel == FP8KV_CHUNK_STREAM ? kChunkStreamWarps * kChunkMaxSum / 2 : kChunkMaxSum;
+}
 inline int chunk_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }  // query vectors per CTA
 
 // Everything the chunk kernels need, resolved on the host.

@@ -161,7 +161,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   }
   if (d->num_splits) S = d->num_splits;
   // No FP32 sum over more than kChunkMaxSum positions, whoever chose the partitions.
-  S = std::max(S, ceil_div(seen, kChunkMaxSum * (P.kernel == FP8KV_CHUNK_STREAM ? kChunkStreamWarps : 1)));
+  S = std::max(S, ceil_div(seen, chunk_max_part(P.kernel)));
   S = std::min<int64_t>(std::max<int64_t>(1, S), 65535);
   // grid.x
   if ((P.kernel == FP8KV_CHUNK_STREAM ? pairs : (int64_t)P.row_tiles * P.num_kv_heads) > 0x7fffffff)

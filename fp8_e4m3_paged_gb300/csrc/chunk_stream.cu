@@ -15,13 +15,14 @@
 //   O^T[16 d x 8 vectors] += V^T . P^T: an A fragment needs two tokens of one
 //     d in a register, so the lane takes the same 16-byte piece n of tokens
 //     2c, 2c+1, 2c+8, 2c+9 and interleaves their bytes before the decode; P^T's B
-//     fragments are S^T's accumulators, packed to fp16 and transposed 8 by 8 (movmatrix).
+//     fragments are S^T's accumulators, packed to fp16 and transposed 8 by 8 (movmatrix),
+//     in two halves (twice the vectors' columns, or twice the products).
 // Tokens and d as the MMA's 16 rows, vectors as its 8 columns: a decode step's
 // 1 to 8 vectors waste no rows, which halves the MMAs and O's registers
 // against the other orientation.  Legacy mma.sync rather than tcgen05: with 4 to
 // 16 vectors the products are a few percent of the tensor peak, and TMEM or
 // shared-memory operands would only add copies and barriers to a kernel whose
-// time is the bytes' arrival.
+// time is the bytes' arrival.  That also pays for P in two fp16 halves.
 //
 // Partitions of one request and KV head form a thread-block cluster when there
 // are at most 8: their sums are joined through distributed shared memory in
@@ -152,9 +153,11 @@ __device__ __forceinline__ int by_length(const ChunkParams& p, int* key, int r) 
   return b;
 }
 
-template <int D, int FMT, int DT, int NQ>
+// TWIN (at most 4 vectors): columns 4 to 7 hold the vectors of columns 0 to 3 again.
+template <int D, int FMT, int DT, int NQ, bool TWIN>
 __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
     chunk_stream(const __grid_constant__ ChunkParams p, const int clustered, const int sorted) {
+  static_assert(!TWIN || NQ == 1, "one column block");
   using C = StreamCfg<D, NQ>;
   constexpr int ST = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -173,7 +176,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-  const int RC = min(kR, req.n * p.G - row_first);
+  const int RC = min(TWIN ? 4 : kR, req.n * p.G - row_first);
+  auto row_of_column = [](int col) { return TWIN ? col & 3 : col; };
   if (RC <= 0) return;  // every CTA of the cluster
   if (clustered) cluster_here();  // peers may write here once all have come this far (ordered: 0.4 us more)
   const int64_t plane = (int64_t)p.total_q * p.Hq;
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   fill([&]() {
 #pragma unroll
     for (int k = 0; k < kQRows; ++k) {
-      const int r = min(warp + k * kWarps, RC - 1);
+      const int r = min(row_of_column(warp + k * kWarps), RC - 1);
       const uint16_t* src = p.q + (int64_t)(req.row0 + token_of(r)) * p.q_st + (int64_t)head_of(r) * p.q_sh;
       if constexpr (V == 2)
         qw[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
     }
 #pragma unroll
     for (int j = 0; j < V / 2; ++j)
-      *reinterpret_cast<uint32_t*>(sQ + r * C::kQStride + lane * V + 2 * j) = r < RC ? w[j] ^ flip : 0u;
+      *reinterpret_cast<uint32_t*>(sQ + r * C::kQStride + lane * V + 2 * j) = row_of_column(r) < RC ? w[j] ^ flip : 0u;
     if (lane == 0) sBack[r] = back;
   }
   __syncthreads();
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       const int r = 8 * n + 2 * c + e;
       cq[n][e] = fabsf(cf) * sBack[r];
       row[n][e] = {INT_MAX, INT_MIN};
-      if (r < RC) row[n][e] = chunk_row(p, req, span, token_of(r));
+      if (row_of_column(r) < RC) row[n][e] = chunk_row(p, req, span, token_of(row_of_column(r)));
       hi_min = min(hi_min, row[n][e].hi);
       lo_max = max(lo_max, row[n][e].lo);
     }
@@ -441,7 +445,13 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
             }
           }
       }
-      uint32_t pb[NQ][2];  // P^T: tokens 2 c + {0, 1} (+ 8) of vector 8 n + rq
+      // P^T: tokens 2 c + {0, 1} (+ 8) of vector 8 n + rq, as an fp16 number and the fp16 of
+      // what that left: 2^-22 of p together, where one alone (2^-11) would be the largest error
+      // of the call.  Up to 4 vectors: the second copy's columns carry the low halves.
+      // More: products of their own.  (us with one half / so, 64 requests in a window of
+      // 4096: 4 vectors 79.9 / 81.1, 8 vectors 80.6 / 85.4, 16 vectors 96.7 / 109; one request
+      // of 8 vectors 7.3 / 7.5.)
+      uint32_t pb[NQ][2], pl[NQ][2];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const float s0 = (m[n][0] == kNoMax ? 0.f : m[n][0]) - kChunkPShift;
@@ -451,7 +461,11 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
           const float p0 = fast_exp2(x[n][h][0] - s0), p1 = fast_exp2(x[n][h][1] - s1);
           l[n][0] += p0;
           l[n][1] += p1;
-          pb[n][h] = transpose8x8(pack_half2(p0, p1));
+          const uint32_t hi = pack_half2(p0, p1);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          const uint32_t lo = pack_half2(p0 - back.x, p1 - back.y);
+          pb[n][h] = transpose8x8(TWIN && c >= 2 ? lo : hi);
+          if (!TWIN) pl[n][h] = transpose8x8(lo);
         }
       }
 #pragma unroll
@@ -480,25 +494,40 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
             vr[j] = make_uint4(zap_nonfinite(vr[j].x, e5), zap_nonfinite(vr[j].y, e5), zap_nonfinite(vr[j].z, e5),
                                zap_nonfinite(vr[j].w, e5));
         }
+        // (the low halves' products go into the same sums a word later, behind other products)
+        uint32_t f[2][2][4];  // [word parity][token pair][d of the word]
 #pragma unroll
-        for (int w = 0; w < C::kVWords; ++w) {
-          uint32_t f[2][4];  // [token pair][d of the word]
+        for (int w = 0; w <= C::kVWords; ++w) {
+          auto product = [&](int u, const uint32_t (&pp)[NQ][2]) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t wa = word(vr[2 * j], w), wb = word(vr[2 * j + 1], w);
-            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[j][0], f[j][1]);
-            fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[j][2], f[j][3]);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t (&g)[2][4] = f[u & 1];
+              const uint32_t a[4] = {g[0][2 * k], g[0][2 * k + 1], g[1][2 * k], g[1][2 * k + 1]};
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) mma16816(o[(i * C::kVWords + u) * 2 + k][n], a, pp[n][0], pp[n][1]);
+            }
+          };
+          if (w < C::kVWords) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t wa = word(vr[2 * j], w), wb = word(vr[2 * j + 1], w);
+              fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x5140), f[w & 1][j][0], f[w & 1][j][1]);
+              fp8x4_to_f16<FMT>(__byte_perm(wa, wb, 0x7362), f[w & 1][j][2], f[w & 1][j][3]);
+            }
+            product(w, pb);
           }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {f[0][2 * k], f[0][2 * k + 1], f[1][2 * k], f[1][2 * k + 1]};
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) mma16816(o[(i * C::kVWords + w) * 2 + k][n], a, pb[n][0], pb[n][1]);
-          }
+          if (!TWIN && w > 0) product(w - 1, pl);
         }
       }
     }
     cp_wait<0>();
+
+    if (TWIN) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][0][k] += __shfl_xor_sync(0xffffffffu, o[i][0][k], 2);
+    }
 
     // ---------------------------------------------------------- join the warps
     // (lane's vectors 8 n + 2 c + e; d tile (i, w, k) holds d = 128 i + PB rq + 4 w + 2 k + {0, 1})
@@ -655,9 +684,9 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   }
 }
 
-template <int D, int FMT, int DT, int NQ>
+template <int D, int FMT, int DT, int NQ, bool TWIN>
 cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
-  auto fn = chunk_stream<D, FMT, DT, NQ>;
+  auto fn = chunk_stream<D, FMT, DT, NQ, TWIN>;
   constexpr int smem = StreamCfg<D, NQ>::kSmem;
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
@@ -684,7 +713,9 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
 
 template <int D, int FMT, int DT>
 cudaError_t pick_wide(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
-  return (int64_t)p.max_q * p.G > 8 ? run<D, FMT, DT, 2>(plan, p, st) : run<D, FMT, DT, 1>(plan, p, st);
+  const int64_t rows = (int64_t)p.max_q * p.G;
+  if (rows > 8) return run<D, FMT, DT, 2, false>(plan, p, st);
+  return rows > 4 ? run<D, FMT, DT, 1, false>(plan, p, st) : run<D, FMT, DT, 1, true>(plan, p, st);
 }
 
 template <int D>

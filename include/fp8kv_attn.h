@@ -389,8 +389,9 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  * position 0) yields +0.0, rows of q from cu_q[B] on are left as they are.
  *
  * Numerical contract: FP32 logits, running maximum and sum; probabilities
- * enter the PV product as fp16 (2^-11 of their own value), accumulated in
- * FP32; no FP32 sum runs over more than 32768 positions (the plan has as many
+ * enter the PV product as two fp16 numbers (2^-22 of their own value) in the
+ * stream kernel, which takes every call of at most 16 query vectors per KV head, and
+ * as one (2^-11) in the tile kernel; accumulated in FP32; no FP32 sum runs over more than 32768 positions (the plan has as many
  * partitions as that takes, more than num_splits if need be); one rounding to
  * q's type at the end.  bf16 queries are scaled to fp16 per row by
  * a power of two, which is exact for elements above 2^-28 of the row's
@@ -404,6 +405,13 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  *
  * Two calls that may overlap on the GPU need a workspace each.  The calls are
  * graph-capturable: lengths may change between replays within the plan.
+ *
+ * Beside fp8kv_attn_split + fp8kv_attn_combine, which serve 1 to 16 rows per
+ * request, the same number for each: those keep more bits (compensated logits and
+ * partition sums), read bf16 caches and sparse entries, write the new rows
+ * themselves, and give a shard's LSE for the context-parallel merge, none of which
+ * this call does; this call takes any number of new tokens per request, windows
+ * and sinks, bf16 queries, and strides.
  * ------------------------------------------------------------------------ */
 #define FP8KV_CHUNK_AUTO 0   /* by the query vectors and the positions that they see */
 #define FP8KV_CHUNK_STREAM 1 /* streams the cache past 16 query vectors per CTA */

@@ -409,3 +409,16 @@ def test_long_contexts():
         tol[rows] -= (kv - 32768) / 16 * 2.0 ** -23 * cond[rows]
     for kernel, splits in [(0, 0), (1, 1), (1, 2), (2, 1), (2, 9)]:
         check(Run(c, kernel, splits)(), c, (out, tol, cond))
+
+
+@pytest.mark.parametrize("name", ["decode", "decode_gqa8", "decode_group1", "decode_group12", "drafts", "window_decode",
+                                  "ragged", "long"])
+def test_the_stream_kernel_keeps_two_halves_of_each_probability(name):
+    """A probability as two fp16 numbers: 2^-22 of its own value, where one leaves 2^-11."""
+    c = CASES[name]
+    out, tol, cond = c.reference()
+    used = int(c.cu[-1])
+    for splits in (0, 1, 3, 11):
+        got = Run(c, 1, splits)()
+        worst = ((got - out).abs() / (tol + 2.0 ** -21 * cond))[:used].max()
+        assert worst <= 1.0, f"{splits} partitions: {float(worst):.3f} of the bound"
