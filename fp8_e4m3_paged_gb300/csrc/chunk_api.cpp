@@ -9,6 +9,7 @@
 
 #include "chunk.h"
 #include "fp8kv_attn.h"
+#include "output_layout.h"
 
 using namespace fp8kv;
 
@@ -21,10 +22,6 @@ bool strides_ok(const int64_t* s, int n, int64_t unit) {
   for (int i = 0; i < n; ++i)
     if (s[i] < 0 || s[i] % unit) return false;
   return true;
-}
-// No two rows or heads of an output in one place.
-bool apart(int64_t rows, int64_t stride_row, int64_t heads, int64_t stride_head) {
-  return (rows < 2 || stride_row > 0) && (heads < 2 || stride_head > 0);
 }
 // Finite host scales, or device floats on their boundary.
 template <class Args>
@@ -196,7 +193,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   const int64_t bs[] = {a->k_stride_block, a->k_stride_token, a->k_stride_head,
                         a->v_stride_block, a->v_stride_token, a->v_stride_head};
   if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
-  if (!apart(plan->total_q, es[2], plan->num_q_heads, es[3])) return FP8KV_EINVAL;
+  if (!apart(plan->total_q, es[2], plan->num_q_heads, es[3], plan->head_dim)) return FP8KV_EINVAL;
   if (!a->cu_q || !a->kv_len || !aligned(a->cu_q, 4) || !aligned(a->kv_len, 4)) return FP8KV_EINVAL;
   if (plan->max_kv_len > 0 && (!a->block_table || !aligned(a->block_table, 4))) return FP8KV_EINVAL;
   if (a->block_table_stride < plan->max_blocks) return FP8KV_EINVAL;
@@ -282,7 +279,8 @@ extern "C" int fp8kv_attn_cache_read(const fp8kv_cache_read_args* a, fp8kv_strea
   const int64_t bs[] = {a->kc_stride_block, a->kc_stride_token, a->kc_stride_head,
                         a->vc_stride_block, a->vc_stride_token, a->vc_stride_head};
   if (!strides_ok(es, 4, 8) || !strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
-  if (!apart(a->total, es[0], a->num_kv_heads, es[1]) || !apart(a->total, es[2], a->num_kv_heads, es[3]))
+  if (!apart(a->total, es[0], a->num_kv_heads, es[1], a->head_dim) ||
+      !apart(a->total, es[2], a->num_kv_heads, es[3], a->head_dim))
     return FP8KV_EINVAL;
   if (!a->block_table || !a->cu_len || a->block_table_stride < a->max_blocks) return FP8KV_EINVAL;
   if (!aligned(a->block_table, 4) || !aligned(a->cu_len, 4) || !aligned(a->start, 4) || !aligned(a->status, 4))

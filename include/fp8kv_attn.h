@@ -458,7 +458,7 @@ typedef struct {
   const void* q;          /* (row, head, d) at element row*q_stride_token + head*q_stride_head + d; 16-byte aligned */
   int64_t q_stride_token, q_stride_head;     /* elements, multiples of 8, >= 0 */
   void* out;              /* same type and addressing with the out_* values; not overlapping q */
-  int64_t out_stride_token, out_stride_head; /* elements, multiples of 8; 0 only for one row (head) */
+  int64_t out_stride_token, out_stride_head; /* elements, multiples of 8; rows and heads must not overlap */
   const uint8_t* k_cache; /* as fp8kv_attn_args.k_cache */
   const uint8_t* v_cache;
   int64_t k_stride_block, k_stride_token, k_stride_head; /* bytes, multiples of 16 */
@@ -522,7 +522,7 @@ typedef struct {
   const int32_t* start;       /* [B] first position of each request; NULL = 0 */
   void* k_out;                /* (row, h, d) at element row*stride_token + h*stride_head + d; 16-byte aligned */
   void* v_out;
-  int64_t ko_stride_token, ko_stride_head; /* elements, multiples of 8; 0 only for one row (head) */
+  int64_t ko_stride_token, ko_stride_head; /* elements, multiples of 8; rows and heads must not overlap */
   int64_t vo_stride_token, vo_stride_head;
   float k_scale, v_scale;     /* finite (used when the device pointers are NULL) */
   const float* k_scale_dev;

@@ -396,3 +396,47 @@ def test_no_sum_over_more_than_32768_positions(B, kernel, chains, head_dim):
     p = B.fp8kv_attn_chunk_plan(_desc(B, max_kv_len=1 << 30, max_blocks=1 << 26, window=4096, sinks=4, kernel=kernel,
                                       num_splits=1))
     assert p.num_splits == 1
+
+
+def test_overlapping_outputs_are_refused(B):
+    """Rows or heads that share elements: what those would hold depends on timing."""
+    plan = B.fp8kv_attn_chunk_plan(_desc(B))
+    for st, sh in ((1024, 8), (1024, 120), (1016, 128), (64, 1024), (128, 12792), (256, 384), (8, 8)):
+        a = _args(B, plan, out_stride_token=st, out_stride_head=sh)
+        assert B.lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(a), None) == B.EINVAL
+    for kw in (dict(ko_stride_head=120), dict(vo_stride_head=120), dict(ko_stride_token=248), dict(vo_stride_token=128)):
+        assert B.lib.fp8kv_attn_cache_read(ctypes.byref(_read(B, **kw)), None) == B.EINVAL
+
+
+def test_every_layout_without_overlap_is_taken(tmp_path):
+    """The check itself against a list of every row's and head's first element, interleaved layouts among them."""
+    import random
+
+    rng = random.Random(5)
+    D = 128
+    cases = [(100, 1024, 8, 8), (100, 64, 8, 1024), (100, 1024, 8, 128), (100, 1000, 8, 128), (100, 128, 8, 12800),
+             (100, 128, 8, 12792), (3, 384, 2, 256), (3, 256, 2, 384), (2, 256, 2, 384), (100, 256, 2, 128),
+             (100, 256, 2, 384), (4, 640, 3, 384), (1, 0, 8, 128), (1, 0, 8, 120), (100, 128, 1, 0), (100, 120, 1, 0),
+             (100, 1 << 62, 8, 128), (100, 1 << 62, 8, 1 << 62)]
+    cases += [(rng.randint(1, 9), 8 * rng.randint(0, 80), rng.randint(1, 5), 8 * rng.randint(0, 80))
+              for _ in range(3000)]
+    src = tmp_path / "layout.cpp"
+    src.write_text("""#include <cstdio>
+#include "output_layout.h"
+int main() {
+  long long r, s, h, t;
+  while (std::scanf("%lld %lld %lld %lld", &r, &s, &h, &t) == 4)
+    std::printf("%d\\n", fp8kv::apart(r, s, h, t, 128));
+}
+""")
+    exe = tmp_path / "layout"
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "fp8_e4m3_paged_gb300", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+    text = "\n".join(" ".join(map(str, c)) for c in cases)
+    got = [x == "1" for x in subprocess.run([str(exe)], input=text, check=True, capture_output=True,
+                                            text=True).stdout.split()]
+    want = []
+    for rows, st, heads, sh in cases:
+        at = sorted(r * st + h * sh for r in range(rows) for h in range(heads))
+        want.append(all(b - a >= D for a, b in zip(at, at[1:])))
+    assert got == want and 300 < sum(want) < len(want) - 300
