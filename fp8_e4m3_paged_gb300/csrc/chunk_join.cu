@@ -33,16 +33,15 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
   const int row = (int)(vec / p.Hq), h = (int)(vec - (int64_t)row * p.Hq);
   bool live = row < p.total_q;
   if (live) {
-    // the request of the row: the number of ends at or below it
-    int b = 0;
-    for (int i0 = 0; i0 < p.B; i0 += 32) {
-      const bool below = i0 + lane < p.B && p.cu_q[i0 + lane + 1] <= row;
-      b += __popc(__ballot_sync(0xffffffffu, below));
-    }
-    live = b < p.B;  // not behind the last request
-    if (live) {
-      const ChunkRequest r = chunk_request(p, b);
-      live = row >= r.row0 && row - r.row0 < r.n;
+    // whether some request has the row among its (clamped) new tokens
+    live = false;
+    for (int i0 = 0; i0 < p.B && !live; i0 += 32) {
+      bool here = false;
+      if (i0 + lane < p.B) {
+        const ChunkRequest r = chunk_request(p, i0 + lane);
+        here = row >= r.row0 && row - r.row0 < r.n;
+      }
+      live = __any_sync(0xffffffffu, here);
     }
   }
   float acc[V] = {};

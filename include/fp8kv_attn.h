@@ -401,7 +401,8 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  * as in fp8kv_attn_split: a position in an out-of-range block counts as not
  * visible (BAD_BLOCK); a kv_len outside [0, max_kv_len], a cu_q that
  * decreases or leaves [0, total_q], and more than max_q new tokens of a
- * request are clamped (BAD_LEN; new tokens past max_q are not computed).
+ * request are clamped (BAD_LEN; new tokens past max_q are not computed, rows
+ * that a decreasing cu_q gives to two requests hold unspecified values).
  *
  * Two calls that may overlap on the GPU need a workspace each.  The calls are
  * graph-capturable: lengths may change between replays within the plan.

@@ -7,6 +7,8 @@ codes, bad blocks and lengths, graph replay, streams.  Every cache slot that no
 new token may see holds a NaN code.
 """
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -422,3 +424,48 @@ def test_the_stream_kernel_keeps_two_halves_of_each_probability(name):
         got = Run(c, 1, splits)()
         worst = ((got - out).abs() / (tol + 2.0 ** -21 * cond))[:used].max()
         assert worst <= 1.0, f"{splits} partitions: {float(worst):.3f} of the bound"
+
+
+@pytest.mark.parametrize("cu,max_q,becomes", [
+    # new tokens past max_q are not computed; the others are the last ones of the context
+    ([0, 4, 7], 3, [(0, 3, 90), (4, 3, 60)]),
+    ([0, 4, 7], 2, [(0, 2, 90), (4, 2, 60)]),
+    # request 0 is empty, request 1 begins at row 0 and has max_q tokens
+    ([0, -3, 7], 4, [(0, 0, 90), (0, 4, 60)]),
+    ([0, -3, 7], 7, [(0, 0, 90), (0, 7, 60)]),
+    # a decrease: request 1 is empty
+    ([0, 4, 2], 4, [(0, 4, 90), (4, 0, 60)]),
+    ([0, 4, 100], 4, [(0, 4, 90), (4, 3, 60)]),
+    ([-9, 4, 7], 4, [(0, 4, 90), (4, 3, 60)]),
+])
+def test_clamped_lengths_compute_what_the_header_says(cu, max_q, becomes):
+    """Rows, new tokens and positions that the clamped lengths leave: those rows right, every other row untouched."""
+    c = Case([(4, 90), (3, 60)], Hq=4, Hkv=2, D=128)
+    for kernel, splits in [(1, 0), (1, 1), (1, 11), (2, 0), (2, 1), (2, 2)]:
+        r = Run(c, kernel, splits, max_q=max_q)
+        r.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+        got = r()
+        assert r.status() == r.B.STATUS_BAD_LEN
+        written = torch.zeros(c.total, dtype=torch.bool)
+        for b, (row0, n, kv) in enumerate(becomes):
+            d = copy.copy(c)
+            d.requests = [(0, kv) if x != b else (n, kv) for x in range(2)]
+            d.cu = np.array([row0] * (b + 1) + [row0 + n] * (2 - b), dtype=np.int32)
+            out, tol, cond = d.reference()
+            rows = slice(row0, row0 + n)
+            assert ((got[rows] - out[rows]).abs() <= tol[rows] + P_ERR * cond[rows]).all()
+            written[rows] = True
+        assert (got[~written] == 7.0).all()
+
+
+def test_rows_before_the_first_request_are_left():
+    c = Case([(4, 90), (3, 60)], Hq=4, Hkv=2, D=128)
+    d = copy.copy(c)
+    d.requests, d.cu = [(2, 90), (3, 60)], np.array([2, 4, 7], dtype=np.int32)
+    out, tol, cond = d.reference()
+    for kernel, splits in kernels(c):
+        r = Run(c, kernel, splits)
+        r.cu[0] = 2
+        got = r()
+        assert r.status() == 0 and (got[:2] == 7.0).all()
+        assert ((got - out).abs() <= tol + P_ERR * cond)[2:].all()
