@@ -386,7 +386,10 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  * any mixture of them; with a window, layers that keep the last `window`
  * positions and the first `sinks`.  Positions outside of a request's windows
  * are never read.  A token that sees nothing (kv_len[b] < n_b puts it before
- * position 0) yields +0.0, rows of q from cu_q[B] on are left as they are.
+ * position 0) yields +0.0, and so does one whose logits are all -inf (infinite
+ * K codes), as in fp8kv_attn_combine; rows of q below cu_q[0] or from cu_q[B] on
+ * are left as they are.  A non-finite V code of a visible position reaches
+ * the output whatever the position's weight is.
  *
  * Numerical contract: FP32 logits, running maximum and sum; probabilities
  * enter the PV product as two fp16 numbers (2^-22 of their own value) in the

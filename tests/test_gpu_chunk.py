@@ -469,3 +469,30 @@ def test_rows_before_the_first_request_are_left():
         got = r()
         assert r.status() == 0 and (got[:2] == 7.0).all()
         assert ((got - out).abs() <= tol + P_ERR * cond)[2:].all()
+
+
+def _minus_infinite_logits(requests, D):
+    """E5M2 case whose request 0 has a logit of -inf at every position but the last two, for KV head 0."""
+    c = Case(requests, Hq=4, Hkv=2, D=D, fmt="e5m2", k_scale=0.001, seed=9)
+    c.q[:, :, 3] = c.q[:, :, 3].abs() + 0.5
+    n, kv = c.requests[0]
+    t = torch.arange(kv - 2)
+    c.k[c.table[0].long()[t // c.page], t % c.page, 0, 3] = 0xFC
+    return c, n
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_whose_logits_are_all_minus_infinity_are_zero(D):
+    """Infinite K codes: a sum of weights of 0 gives +0, as in the decode path's combine."""
+    for requests in ([(4, 90), (1, 40)], [(150, 300)]):
+        c, n = _minus_infinite_logits(requests, D)
+        ref = c.reference()
+        assert (ref[0][:n - 2, :2] == 0).all() and (ref[0][n - 2:n, :2] != 0).any()
+        # The reference has no bound for logits beside infinite codes.  The last rows have one or two finite logits: their
+        # FP32 errors, (D/16 + 16) 2^-23 of a = sum |q k| <= 13 (D = 256: 256 * 0.64 * 256^-0.5 = 10), move the output by
+        # at most twice that of cond: below 2^-13
+        ref[1][:n, :2] = 2.0 ** -11 * ref[0][:n, :2].abs() + 2.0 ** -13 * ref[2][:n, :2] + 2.0 ** -25
+        for kernel, splits in kernels(c):
+            got = Run(c, kernel, splits)()
+            assert not torch.signbit(got[:n - 2, :2]).any()
+            check(got, c, ref)
