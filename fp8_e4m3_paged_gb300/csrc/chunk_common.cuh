@@ -86,6 +86,12 @@ __device__ __forceinline__ float part_weight(float m, float M) {
   return m == M ? 1.f : exp2_whole(fmaxf(m - M, -120.f));
 }
 
+// The sum that a partition leaves for a row, as the join reads it.  +0: the partition was
+// empty and its numerators were not written.  -0: they were, by positions whose logits are
+// all -inf; they are 0, or not finite where such a position has a non-finite V code.
+__device__ __forceinline__ float part_sum(float l) { return l == 0.f ? -0.f : l; }
+__device__ __forceinline__ bool part_written(float2 ml) { return __float_as_uint(ml.y) != 0u; }
+
 // What one row sees on that axis: v < hi and (v >= lo or v < sk).
 struct ChunkRow {
   int hi, lo;

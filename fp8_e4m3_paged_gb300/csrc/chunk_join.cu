@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (s0 + i * ways >= p.S || (ml[i].x == kNoMax && ml[i].y == 0.f)) continue;  // saw nothing (x is stale)
+        if (s0 + i * ways >= p.S || !part_written(ml[i])) continue;  // (x is stale)
         const float w = part_weight(ml[i].x, M);
         L = fmaf(w, ml[i].y, L);
 #pragma unroll
@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
     for (int w = 0; w < ways; ++w) {
-      if (s_m[warp + w] == kNoMax && s_l[warp + w] == 0.f) continue;
       const float a = part_weight(s_m[warp + w], T);
       L = fmaf(a, s_l[warp + w], L);
 #pragma unroll

@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int q = 0; q < kChunkClusterMax; ++q) {
-        if (q >= p.S || (ml[q].x == kNoMax && ml[q].y == 0.f)) continue;  // saw nothing
+        if (q >= p.S) continue;
         const float a = part_weight(ml[q].x, M);
         L = fmaf(a, ml[q].y, L);
         z.x = fmaf(a, y[q].x, z.x);
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;
     if (r >= RC) continue;
     if (p.S > 1) {
-      if (d == 0) p.ml[s * plane + vec_of(r)] = make_float2(Ms[k], Ls[k] * kChunkInvPShift);
+      if (d == 0) p.ml[s * plane + vec_of(r)] = make_float2(Ms[k], part_sum(Ls[k] * kChunkInvPShift));
       *reinterpret_cast<float4*>(p.partial + (s * plane + vec_of(r)) * D + d) =
           make_float4(acc[k].x * kChunkInvPShift, acc[k].y * kChunkInvPShift, acc[k].z * kChunkInvPShift,
                       acc[k].w * kChunkInvPShift);

@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
         const int64_t vec = live ? vec_of(rr) : 0;
         const bool dead = l == 0.f, parts = p.S > 1;
         const float f = parts ? kChunkInvPShift : (dead ? 0.f : vs / l);
-        if (parts && live) p.ml[s * plane + vec] = make_float2(m, l * kChunkInvPShift);
+        if (parts && live) p.ml[s * plane + vec] = make_float2(m, part_sum(l * kChunkInvPShift));
         mt.sum[rr] = l;
         // A thread holds a row, but a store instruction had better write few rows: 128
         // bytes of each of the warp's 32 rows go through shared memory (the

@@ -496,3 +496,22 @@ def test_rows_whose_logits_are_all_minus_infinity_are_zero(D):
             got = Run(c, kernel, splits)()
             assert not torch.signbit(got[:n - 2, :2]).any()
             check(got, c, ref)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nonfinite_values_of_weight_zero_do_not_depend_on_partitions(D):
+    """An infinite V code at a position whose logit is -inf: it reaches the rows that have other positions to see, also
+    where its partition holds nothing else for them; a row without any stays +0."""
+    for requests in ([(4, 90), (1, 40)], [(150, 300)], [(1, 700)]):
+        c, n = _minus_infinite_logits(requests, D)
+        clean = c.reference()[0]
+        c.v[c.table[0, 0].long(), 2, 0, 8] = 0x7C
+        c.v[c.table[0, 0].long(), 3, 0, 9] = 0x7F
+        dead = torch.arange(n) < n - 2
+        for kernel, splits in kernels(c) + [(1, 8), (2, 2)]:
+            got = Run(c, kernel, splits)()[:n, :2]
+            assert (got[dead] == 0).all()
+            assert (got[~dead, :, 8] == float("inf")).all() and torch.isnan(got[~dead, :, 9]).all()
+            others = [d for d in range(D) if d not in (8, 9)]
+            assert torch.isfinite(got[..., others]).all()
+            assert ((got - clean[:n, :2])[..., others].abs() <= 2.0 ** -6 * (1 + clean[:n, :2][..., others].abs())).all()
