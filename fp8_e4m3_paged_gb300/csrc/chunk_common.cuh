@@ -15,6 +15,9 @@ constexpr float kChunkTau = 8.0f;              // the running maximum moves when
 constexpr float kChunkPShift = 7.0f;           // probabilities are kept times 2^7: p <= 2^15 fits fp16, and
 constexpr float kChunkInvPShift = 1.f / 128;   // p turns subnormal only below 2^-21 of the running maximum
 constexpr float kNoMax = -INFINITY;            // running maximum of a row that has seen nothing
+// Logits of 2^24 and more are so far apart that m + tau and m - 7 round: p must not pass
+// 2^15 for it (fp16 ends at 2^16).  Differences of near numbers are exact, so the maximum
+// moves by logit - m > tau, and the shift is rounded to the side of the smaller p.
 
 // Packed row -> token of the request and query head of the group; partitions' length;
 // KV head of a CTA.  By products with host-made inverses, for the stream kernel: some

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float y = fmaxf(x[n][0][e], x[n][1][e]);
-          moves |= y > -INFINITY && !(y <= m[n][e] + kChunkTau);
+          moves |= y - m[n][e] > kChunkTau;  // (false where both are -inf)
         }
       if (__any_sync(0xffffffffu, moves)) {
         // a vector's running maximum moves (whole numbers: rescaling is exact)
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
             const float mo = m[n][e];
-            const float mn = y > mo + kChunkTau || mo == kNoMax ? fmaxf(mo, ceilf(y)) : mo;
+            const float mn = y - mo > kChunkTau ? fmaxf(mo, ceilf(y)) : mo;
             const float a = mn == mo ? 1.f : exp2_whole(mo - mn);
             m[n][e] = mn;
             l[n][e] *= a;
@@ -454,8 +454,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
       uint32_t pb[NQ][2], pl[NQ][2];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const float s0 = (m[n][0] == kNoMax ? 0.f : m[n][0]) - kChunkPShift;
-        const float s1 = (m[n][1] == kNoMax ? 0.f : m[n][1]) - kChunkPShift;
+        const float s0 = __fadd_ru(m[n][0] == kNoMax ? 0.f : m[n][0], -kChunkPShift);
+        const float s1 = __fadd_ru(m[n][1] == kNoMax ? 0.f : m[n][1], -kChunkPShift);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float p0 = fast_exp2(x[n][h][0] - s0), p1 = fast_exp2(x[n][h][1] - s1);

@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       if (rr < RC) row = chunk_row(p, req, span, (work.row0 + rr) / p.G);
       const int hi_min = __reduce_min_sync(0xffffffffu, row.hi), lo_max = __reduce_max_sync(0xffffffffu, row.lo);
       float m = kNoMax, l = 0.f;
+      bool far = false;  // some row of the warp has logits past 2^22
       const uint32_t tO = tmem + C::kColO + q * D + lane_off;
       for (int j = 0; j < n_tiles; ++j) {
         const int buf = buf_of(j);
@@ -658,10 +659,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
           for (int i = 0; i < 4; ++i)
             mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[k + 2 * i])), __uint_as_float(x[k + 2 * i + 1]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        if (__any_sync(0xffffffffu, top > m + kChunkTau || (m == kNoMax && top > -INFINITY))) {
-          const float n = top > m + kChunkTau || m == kNoMax ? fmaxf(m, ceilf(top)) : m;
+        if (__any_sync(0xffffffffu, top - m > kChunkTau)) {  // (false where both are -inf)
+          const float n = top - m > kChunkTau ? fmaxf(m, ceilf(top)) : m;
           const float a = n == m || m == kNoMax ? 1.f : exp2_whole(m - n);
           m = n;
+          far = __any_sync(0xffffffffu, fabsf(m) >= 0x1p22f && m != kNoMax);
           l *= a;
           if (j > 0 && __any_sync(0xffffffffu, a != 1.f)) {
             // O holds the PVs of the tiles before this one.  Two row tiles: S(j)
@@ -680,8 +682,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
             }
           }
         }
-        const float sh = kChunkPShift - (m == kNoMax ? 0.f : m);
-        const uint64_t c2 = pair(c, c), sh2 = pair(sh, sh);
+        const float sh = __fadd_rd(kChunkPShift, m == kNoMax ? -0.f : -m);
+        if (far) {
+          // the maximum is that of the rounded products, which the fma below would not round
+#pragma unroll
+          for (int k = 0; k < 128; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * c);
+        }
+        const uint64_t c2 = far ? pair(1.f, 1.f) : pair(c, c), sh2 = pair(sh, sh);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

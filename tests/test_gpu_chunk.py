@@ -13,7 +13,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests._chunk_ref import Case
+from tests._chunk_ref import POISON, Case, decode_table
 
 pytestmark = pytest.mark.gpu
 
@@ -515,3 +515,31 @@ def test_nonfinite_values_of_weight_zero_do_not_depend_on_partitions(D):
             others = [d for d in range(D) if d not in (8, 9)]
             assert torch.isfinite(got[..., others]).all()
             assert ((got - clean[:n, :2])[..., others].abs() <= 2.0 ** -6 * (1 + clean[:n, :2][..., others].abs())).all()
+
+
+@pytest.mark.parametrize("negative", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_logits_past_the_integers_of_32_bits(D, negative):
+    """Logits whose neighbours in FP32 are further apart than the softmax resolves.  Every V row is the same, so any
+    weights give that row: a probability that overflows, or a sum that vanishes, would show."""
+    for power in (10, 20, 22, 23, 24, 25, 26, 27, 28, 30, 34, 50):
+        for requests in ([(4, 300), (1, 90)], [(150, 300)]):
+            c = Case(requests, Hq=4, Hkv=2, D=D, dtype=torch.bfloat16, k_scale=1.0, v_scale=0.5,
+                     softmax_scale=-0.7 if negative else 0.7, seed=power)
+            # K: 1 and a small number; q: 2^power and, for the second, about its unit in the last place
+            g = torch.Generator().manual_seed(power)
+            small = torch.randint(0, 17, c.k.shape[:3], generator=g).float()
+            k = torch.zeros(c.k.shape)
+            k[..., 0], k[..., 1] = 1.0, small
+            c.k = k.to(torch.float8_e4m3fn).view(torch.uint8)
+            c.v[:] = c.v[1, 0, :, :][None, None]
+            c.v[c.v == POISON["e4m3"]] = 0x38
+            c.q[:] = 0
+            c.q[..., 0] = 2.0 ** power
+            c.q[..., 1] = torch.randint(0, 9, c.q.shape[:2], generator=g) * 2.0 ** (power - 24)
+            v = decode_table("e4m3")[c.v[1, 0].long()] * 0.5
+            want = v.repeat_interleave(2, 0)[None].expand(c.total, -1, -1)
+            for kernel, splits in kernels(c):
+                got = Run(c, kernel, splits)()
+                # rounding of the output and of the probabilities, and 2^-12 for sums and vanishing ones
+                assert ((got - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12)).all(), (power, kernel)
