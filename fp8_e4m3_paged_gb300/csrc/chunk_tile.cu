@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
       // (not 0, so that c * -inf stays -inf for masked logits; nor NaN, for the same reason: a
       // NaN scale goes into the rows' sums at the end)
       const float c = fmaxf(fabsf(cf) * back, 1e-30f);
-      ChunkRow row = {INT_MAX, INT_MIN};  // rows past RC: everything, dropped at the end
+      ChunkRow row = {INT_MAX, 0};  // rows past RC: everything, dropped at the end
       if (rr < RC) row = chunk_row(p, req, span, (work.row0 + rr) / p.G);
       const int hi_min = __reduce_min_sync(0xffffffffu, row.hi), lo_max = __reduce_max_sync(0xffffffffu, row.lo);
       float m = kNoMax, l = 0.f;
