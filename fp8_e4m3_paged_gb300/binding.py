@@ -479,6 +479,12 @@ def _check(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _one_device(*tensors) -> None:
+    """The call's tensors lie on one GPU (pinned host tensors may stand beside them)."""
+    on = {t.device for t in tensors if t is not None and t.device.type != "cpu"}
+    _check(len(on) <= 1, f"tensors on several devices: {', '.join(sorted(map(str, on)))}")
+
+
 def _int32(t, n: int, name: str) -> None:
     import torch
 
@@ -555,6 +561,7 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
     _int32(kv_len, block_table.shape[0], "kv_len")
     _device_scale(k_scale_dev, "k_scale_dev")
     _device_scale(v_scale_dev, "v_scale_dev")
+    _one_device(q, k_cache, v_cache, out, workspace, block_table, cu_q, kv_len, k_scale_dev, v_scale_dev)
     a = ChunkArgs()
     a.q, (a.q_stride_token, a.q_stride_head) = _ptr(q), _rows(q, "q")
     a.out, (a.out_stride_token, a.out_stride_head) = _ptr(out), _rows(out, "out")
@@ -604,6 +611,7 @@ def make_cache_read_args(*, k_cache, v_cache, block_table, cu_len, k_out, v_out,
     [B][columns]; cu_len: int32 [B+1]; start: optional int32 [B]; k_out /
     v_out: fp16, bf16 or fp32 [total][Hkv][D] (d contiguous); status: optional
     int32 tensor of one element."""
+    _one_device(k_cache, v_cache, block_table, cu_len, k_out, v_out, start, k_scale_dev, v_scale_dev, status)
     a = CacheReadArgs()
     a.dtype = _torch_dtype(k_out, DTYPE_F16, DTYPE_BF16, DTYPE_F32)
     _check(v_out.dtype == k_out.dtype and v_out.shape == k_out.shape, "v_out: same type and shape as k_out")
@@ -645,6 +653,7 @@ def make_calibrate_args(*, k, v, k_scale, v_scale, slot_mapping=None, kv_format:
     (tokens with a negative slot do not count)."""
     import torch
 
+    _one_device(k, v, k_scale, v_scale, slot_mapping)
     a = CalibrateArgs()
     a.dtype = _torch_dtype(k, DTYPE_F16, DTYPE_BF16)
     _check(v.dtype == k.dtype and v.shape == k.shape, "v: same type and shape as k")

@@ -409,6 +409,8 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  *
  * Two calls that may overlap on the GPU need a workspace each.  The calls are
  * graph-capturable: lengths may change between replays within the plan.
+ * Buffers and stream belong to the current device, as in every call of this
+ * library.
  *
  * Beside fp8kv_attn_split + fp8kv_attn_combine, which serve 1 to 16 rows per
  * request, the same number for each: those keep more bits (compensated logits and

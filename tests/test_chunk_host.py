@@ -440,3 +440,42 @@ int main() {
         at = sorted(r * st + h * sh for r in range(rows) for h in range(heads))
         want.append(all(b - a >= D for a, b in zip(at, at[1:])))
     assert got == want and 300 < sum(want) < len(want) - 300
+
+
+def test_binding_refuses_tensors_on_several_devices(B, monkeypatch):
+    """Tensors of two GPUs in one call: a kernel would fault on the other's memory.  (No GPU here: tensors that say so.)"""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        where = "cuda:1"
+
+        @property
+        def device(self):
+            return torch.device(self.where)
+
+    class There(Elsewhere):
+        where = "cuda:0"
+
+    q = torch.zeros(4, 8, 64, dtype=torch.float16)
+    k = torch.zeros(5, 2, 64, dtype=torch.float16)
+    cache = torch.zeros(5, 16, 2, 64, dtype=torch.uint8)
+    i = torch.zeros(3, dtype=torch.int32)
+    one = torch.ones(1)
+    calls = [(B.make_chunk_args, dict(q=q, out=q.clone(), k_cache=cache, v_cache=cache, softmax_scale=1.0, cu_q=i,
+                                      workspace=torch.zeros(256, dtype=torch.uint8), kv_len=i[:2],
+                                      block_table=torch.zeros(2, 3, dtype=torch.int32), k_scale_dev=one,
+                                      v_scale_dev=one)),
+             (B.make_cache_read_args, dict(k_cache=cache, v_cache=cache, cu_len=i, start=i[:2], k_out=k, v_out=k.clone(),
+                                           block_table=torch.zeros(2, 3, dtype=torch.int32), k_scale_dev=one,
+                                           v_scale_dev=one, status=i[:1])),
+             (B.make_calibrate_args, dict(k=k, v=k, k_scale=one, v_scale=one.clone(),
+                                          slot_mapping=torch.zeros(5, dtype=torch.int64)))]
+    for make, good in calls:
+        tensors = [n for n, t in good.items() if isinstance(t, torch.Tensor)]
+        make(**good)
+        make(**{n: t.as_subclass(There) if n in tensors else t for n, t in good.items()})
+        make(**{n: t.as_subclass(There) if n == tensors[0] else t for n, t in good.items()})  # the others on the host
+        for other in tensors[1:]:
+            with pytest.raises(ValueError, match="several devices"):
+                make(**{n: t.as_subclass(There if n != other else Elsewhere) if n in tensors else t
+                        for n, t in good.items()})
