@@ -202,3 +202,33 @@ def test_calibrate_write_attend_read():
     cond = (w @ vd.abs()).transpose(0, 1)
     # output rounding, probabilities as fp16 (2^-11 each), 2^-14 for the FP32 logits and sums
     assert float(((out.double() - ref).abs() / (ref.abs() * 2.0 ** -11 + cond * (2.0 ** -11 + 2.0 ** -14))).max()) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_read_positions_outside_of_the_table_give_zero_rows(dtype):
+    """Rows before position 0 or past the table: +0.0 whatever the scale's sign, flagged; the others as ever."""
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randint(1, 120, (9, 16, 2, 64), generator=g, dtype=torch.uint8) for _ in "kv")
+    table = torch.randperm(8, generator=g).to(torch.int32).view(2, 4)
+    for start in ([-3, 60], [-(2 ** 31), 2 ** 31 - 5], [0, 0]):
+        lens = [10, 9]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ko, vo = (torch.full((19, 2, 64), 5.0, dtype=dtype, device="cuda") for _ in "kv")
+        B.fp8kv_attn_cache_read(B.make_cache_read_args(
+            k_cache=k.cuda(), v_cache=v.cuda(), block_table=table.cuda(), k_out=ko, v_out=vo, k_scale=-0.5, v_scale=2.0,
+            cu_len=torch.tensor([0, 10, 19], dtype=torch.int32, device="cuda"),
+            start=torch.tensor(start, dtype=torch.int32, device="cuda"), status=status),
+            torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert int(status.item()) == (0 if start == [0, 0] else B.STATUS_BAD_BLOCK)
+        tab = decode_table("e4m3")
+        for cache, scale, out in ((k, -0.5, ko.cpu()), (v, 2.0, vo.cpu())):
+            for b in range(2):
+                for i in range(lens[b]):
+                    t, got = start[b] + i, out[10 * b + i]
+                    if 0 <= t < 64:
+                        assert torch.equal(got, (tab[cache[table[b, t // 16].long(), t % 16].long()] * scale).to(dtype))
+                    else:
+                        assert (got == 0).all() and not torch.signbit(got).any()
