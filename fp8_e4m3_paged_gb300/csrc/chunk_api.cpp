@@ -100,10 +100,10 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     // starts slower and leaves SMs idle where there are few tiles.  So more
     // than 16 vectors stream while the positions are few (`units`: CTAs of the
     // stream kernel before the context is split; us, stream / tile):
-    //   units few, any number of vectors: 32 units x 2064 positions 13.9 / 19.1, 24 x 340 (D 64)
-    //   8.1 / 12.2, 26 x 400 (D 256) 14.1 / 19.4, 16 x 2008 13.1 / 14.4, but 16 x 4008 17.5 / 16.4;
-    //   up to 32 vectors: 64 units x 1008 12.8 / 15.7, x 2008 17.2 / 19.0, 256 x 308 12.6 / 13.3,
-    //   but 256 x 2008 53.6 / 39.6, 512 x 8008 270 / 250.
+    //   units few, any number of vectors: 32 units x 2064 positions 13.9 / 15.6, 24 x 340 (D 64)
+    //   6.9 / 12.1, 26 x 400 (D 256) 13.1 / 16.6, 16 x 2008 12.6 / 13.6, but 16 x 4008 17.0 / 15.5;
+    //   up to 32 vectors: 64 units x 1008 12.7 / 15.1, x 2008 17.2 / 18.3, 256 x 308 13.2 / 13.8,
+    //   but 256 x 2008 54.7 / 38.6, 512 x 8008 309 / 249.
     const int64_t seen = seen_by(P.max_q);
     const bool few = 2 * stream_units <= sms || (rows <= 32 && (stream_units <= sms || seen <= 512));
     const bool stream = rows <= kChunkStreamRows || (seen * P.head_dim <= 5 << 16 && few);
@@ -113,9 +113,9 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   // Partitions: about one CTA per slot of the GPU, none shorter than `unit`
   // positions of what one CTA's rows see together.
   // Stream kernel: more than two CTAs per SM only where each keeps 512
-  // positions (us, with / without that: 128 units x 300 positions S = 2 8.8, S = 4 10.4;
-  // 256 x 500 S = 1 11.7, S = 2 12.8; 64 x 1000 S = 4 9.6, S = 8 10.3; and 256 x 2000 S = 2 32.3,
-  // S = 1 35.3).
+  // positions (us, with / without that: 128 units x 300 positions S = 2 8.4, S = 4 9.8;
+  // 256 x 500 S = 1 11.9, S = 2 12.4; 64 x 1000 S = 4 9.1, S = 8 10.0; and 256 x 2000 S = 2 32.5,
+  // S = 1 35.4).
   int64_t units, slots, unit, span_q;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
     units = stream_units;
@@ -140,9 +140,9 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     // The CTAs of one request are equally long, so the last of their waves is
     // worth filling: the S whose waves times a CTA's time (its positions, and
     // about 900 more for its start and end) is least.  8 KV heads x 2048 tokens x 4
-    // on 30000 positions, 152 SMs: S = 1 (2 waves) 926 us, 2 (4) 959, 3 (6) 954, 4 (7)
-    // 883, 5 (9) 922, 7 (12) 932.  (CTAs of several requests differ in length and fill
-    // the gaps themselves: 16 requests, 41 row tiles x 8 heads, S = 1: 131 us, 2: 155, 4: 189.)
+    // on 30000 positions, 152 SMs: S = 1 (2 waves) 897 us, 2 (4) 929, 3 (6) 937, 4 (7)
+    // 861, 5 (9) 899, 7 (12) 902.  (CTAs of several requests differ in length and fill
+    // the gaps themselves: 16 requests, 41 row tiles x 8 heads, S = 1: 133 us, 2: 164, 4: 192.)
     if (P.batch == 1) {
       const int64_t ctas = ceil_div(rows, chunk_tile_rows(P.head_dim)) * P.num_kv_heads;
       const int64_t most = std::min(std::max<int64_t>(8, S), ceil_div(seen, unit));

@@ -30,8 +30,8 @@
 //
 // Measured (32 heads over 8, D 128): 57 requests of one token with window 16384,
 // every SM with three CTAs: 6.36 TB/s; 64 ragged requests with window 4096, 404 MB:
-// 80 us, 5.0 TB/s, because 512 CTAs leave some SMs with four of them and some with
-// three.  One request and window 1024: 7.6 us, most of it the launch and the chain
+// 81 us, 5.0 TB/s, because 512 CTAs leave some SMs with four of them and some with
+// three.  One request and window 1024: 7.7 us, most of it the launch and the chain
 // lengths -> block table -> rows -> join.
 #include <algorithm>
 #include <climits>
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   // KV heads next to each other, so that the CTAs that read one token's heads (adjacent
   // in memory) run at the same time; the requests from the longest where there are
   // several CTAs to an SM: the last ones, which only some SMs get, are then short.
-  // 64 requests of 512 to 65536 positions in a window of 4096: 80 us so, 90 by index.
+  // 64 requests of 512 to 65536 positions in a window of 4096: 80 us so, 90 by index
+  // (P in one half then).  Up to as many requests as the CTA has threads; beyond, by index.
   const int nth = div_hkv(p, blockIdx.x), g = blockIdx.x - nth * p.Hkv, s = blockIdx.y;
   const int b = sorted ? by_length(p, reinterpret_cast<int*>(sML), nth) : nth;
   const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group

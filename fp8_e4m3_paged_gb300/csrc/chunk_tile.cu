@@ -24,8 +24,8 @@
 // 2048 cycles; the exponentials, the conversions and the decode about 2000 issue
 // cycles per scheduler, and operand reads, decode stores and Q/P traffic 2300
 // shared-memory cycles; together they run in 3400 to 3600.  32 heads over 8, D 128,
-// 2048 queries on 30000 cached positions: 862 us, 1207 TFLOP/s (the FP16 dense rate
-// would take 537); 8192 queries with window 1024: 175 us, of which a CTA's
+// 2048 queries on 30000 cached positions: 865 us, 1204 TFLOP/s (the FP16 dense rate
+// would take 537); 8192 queries with window 1024: 177 us, of which a CTA's
 // start and end (about 12 us: lengths, Q, the first rows, the output) are the
 // larger part of what lies above the tensor time.
 // Measured and not taken: 16 warps of 128 registers with K and V decoded by four
@@ -68,7 +68,8 @@ struct TileCfg {
   // V's barriers: one per stage; D = 256: one per half (64 positions) of the only stage,
   // which is decoded anew as soon as PV of that half is done.  (With one for the
   // whole tile, PV of the next tile waited for 2500 cycles of decode behind PV of this
-  // one: 87 us for 1000 queries of 6 heads on 8192 positions, 82 so.)
+  // one: 87 us for 1000 queries of 6 heads on 8192 positions, 82 so; 84 with the care for
+  // large logits and NaN since.)
   static constexpr int kVStages = D == 256 ? 2 : kStages;
   static constexpr int kOpBytes = kT * D * 2;
   static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
@@ -110,10 +111,11 @@ __device__ __forceinline__ bool elect_one() {
 
 // Request and first packed row of a CTA.  The GPU starts CTAs in the order of their
 // index, so the longest go first: requests by the positions that their rows see
-// (above 32 requests: by their index, from the last), a request's row tiles from
-// the last, which sees the most, and the KV heads of a row tile side by side.  16
-// requests on 200 to 8000 positions: 130 us; with requests by index and row tiles
-// before heads, whose longest CTAs started last, 189.
+// (above 32 requests, more than a warp's lanes: by their index, from the last; not
+// measured against an order by length), a request's row tiles from the last, which sees
+// the most, and the KV heads of a row tile side by side.  16 requests on 200 to 8000
+// positions: 133 us; with requests by index and row tiles before heads, whose longest
+// CTAs started last, 189.
 struct TileWork {
   int b, row0;
 };
