@@ -48,13 +48,15 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   if (d->kv_format == FP8KV_KV_BF16) return FP8KV_EUNSUPPORTED;
   if (!fp8_format(d->kv_format)) return FP8KV_EINVAL;
   if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return FP8KV_EUNSUPPORTED;
+  // no request has more new tokens than there are rows
+  const int32_t max_q = std::min(d->max_q, std::max(d->total_q, 1));
   // 32-bit positions, packed rows and grid sizes
   const int64_t group = d->num_q_heads / d->num_kv_heads;
   if (d->total_q > (1 << 30) || d->max_q > (1 << 24) || d->max_kv_len > (1 << 30) || d->num_kv_heads > 65535 ||
-      d->max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32) ||
+      max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32) ||
       d->num_sms > 65535)
     return FP8KV_EUNSUPPORTED;
-  if (d->kernel == FP8KV_CHUNK_STREAM && d->max_q * group > 65535 * (int64_t)kChunkStreamRows)
+  if (d->kernel == FP8KV_CHUNK_STREAM && max_q * group > 65535 * (int64_t)kChunkStreamRows)
     return FP8KV_EUNSUPPORTED;
 
   int sms = d->num_sms;
@@ -70,8 +72,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   P.revision = FP8KV_ATTN_REVISION;
   P.batch = d->batch;
   P.total_q = d->total_q;
-  // no request has more new tokens than there are rows
-  P.max_q = std::min(d->max_q, std::max(d->total_q, 1));
+  P.max_q = max_q;
   P.num_q_heads = d->num_q_heads;
   P.num_kv_heads = d->num_kv_heads;
   P.head_dim = d->head_dim;

@@ -479,3 +479,11 @@ def test_binding_refuses_tensors_on_several_devices(B, monkeypatch):
             with pytest.raises(ValueError, match="several devices"):
                 make(**{n: t.as_subclass(There if n != other else Elsewhere) if n in tensors else t
                         for n, t in good.items()})
+
+
+def test_a_loose_bound_of_new_tokens_is_taken(B):
+    """max_q only counts up to the rows that there are, also for the sizes that grids and packed rows allow."""
+    p = B.fp8kv_attn_chunk_plan(_desc(B, kernel=1, max_q=1 << 24, num_q_heads=32, num_kv_heads=1))
+    assert p.max_q == 100
+    p = B.fp8kv_attn_chunk_plan(_desc(B, max_q=1 << 24, num_q_heads=128, num_kv_heads=1))
+    assert p.max_q == 100
