@@ -158,7 +158,7 @@ class ChunkPlan(ctypes.Structure):
         "max_kv_len", "max_blocks", "num_kv_blocks", "window", "sinks", "dtype", "kv_format", "group", "kernel",
         "num_splits", "row_tiles", "num_sms")] + [
         ("partial_offset", ctypes.c_int64), ("ml_offset", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
-        ("reserved", ctypes.c_int32 * 8),
+        ("min_splits", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7),
     ]
 
 

@@ -28,9 +28,10 @@ inline int chunk_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 // Everything the chunk kernels need, resolved on the host.
 struct ChunkParams {
   int32_t B, total_q, max_q, Hq, Hkv, G, S;
+  int32_t parts, max_part;  // a context's partitions: `parts`, more (up to S) of max_part positions if it is longer
   int32_t page_size, max_kv_len, num_kv_blocks;
   uint64_t page_div;       // as Params::page_div
-  uint64_t g_div, s_div, hkv_div;  // the same for G, S and Hkv
+  uint64_t g_div, s_div, parts_div, hkv_div;  // the same for G, S, parts and Hkv
   int32_t window, sinks;   // window 0: every earlier position
   int32_t row_tiles;
   const uint16_t* q;
@@ -52,9 +53,13 @@ struct ChunkParams {
   float2* ml;              // [S][total_q][Hq]
 };
 
-// Whether the partitions form a cluster that joins them itself.
+// Whether the partitions form a cluster that joins them itself: only where all of them have
+// work, since a CTA that waits for its cluster holds its place on the SM (64 decodes of 4000
+// positions planned for 131072, two partitions of which one is empty: 158 us in
+// clusters, 98 through the workspace).
 inline bool chunk_clustered(const fp8kv_chunk_plan_t* plan) {
-  return plan->kernel == FP8KV_CHUNK_STREAM && plan->num_splits > 1 && plan->num_splits <= kChunkClusterMax;
+  return plan->kernel == FP8KV_CHUNK_STREAM && plan->num_splits > 1 && plan->num_splits <= kChunkClusterMax &&
+         plan->min_splits == plan->num_splits;
 }
 
 cudaError_t launch_chunk_stream(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);

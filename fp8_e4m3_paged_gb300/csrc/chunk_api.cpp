@@ -158,9 +158,12 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     }
   }
   if (d->num_splits) S = d->num_splits;
-  // No FP32 sum over more than kChunkMaxSum positions, whoever chose the partitions.
-  S = std::max(S, ceil_div(seen, chunk_max_part(P.kernel)));
   S = std::min<int64_t>(std::max<int64_t>(1, S), 65535);
+  P.min_splits = (int32_t)S;
+  // No FP32 sum over more than kChunkMaxSum positions, whoever chose the partitions: the
+  // kernels use the further ones for contexts that need them.  (64 decodes of 4000 positions,
+  // planned for 4000: 93 us; planned for 2^20: 102, and 162 were all 16 partitions used.)
+  S = std::max(S, ceil_div(seen, chunk_max_part(P.kernel)));
   // grid.x
   if ((P.kernel == FP8KV_CHUNK_STREAM ? pairs : (int64_t)P.row_tiles * P.num_kv_heads) > 0x7fffffff)
     return FP8KV_EUNSUPPORTED;
@@ -181,7 +184,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   if (plan->revision != FP8KV_ATTN_REVISION) return FP8KV_EVERSION;
   std::memset(p, 0, sizeof(*p));
   if (plan->kernel != FP8KV_CHUNK_STREAM && plan->kernel != FP8KV_CHUNK_TILE) return FP8KV_EINVAL;
-  if (plan->num_splits < 1 || plan->group < 1 || plan->page_size < 1 || !fp8_format(plan->kv_format) ||
+  if (plan->num_splits < 1 || plan->min_splits < 1 || plan->min_splits > plan->num_splits || plan->group < 1 || plan->page_size < 1 || !fp8_format(plan->kv_format) ||
       (plan->dtype != FP8KV_DTYPE_F16 && plan->dtype != FP8KV_DTYPE_BF16))
     return FP8KV_EINVAL;
   if (!a->workspace || !aligned(a->workspace, 256)) return FP8KV_EINVAL;
@@ -208,11 +211,14 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   p->Hkv = plan->num_kv_heads;
   p->G = plan->group;
   p->S = plan->num_splits;
+  p->parts = plan->min_splits;
+  p->max_part = (int32_t)chunk_max_part(plan->kernel);
   p->page_size = plan->page_size;
   auto inverse = [](int32_t n) { return n >= 2 ? ~0ull / (uint64_t)n + 1 : 0ull; };
   p->page_div = inverse(plan->page_size);
   p->g_div = inverse(plan->group);
   p->s_div = inverse(plan->num_splits);
+  p->parts_div = inverse(plan->min_splits);
   p->hkv_div = inverse(plan->num_kv_heads);
   p->max_kv_len = plan->max_kv_len;
   p->num_kv_blocks = plan->num_kv_blocks;

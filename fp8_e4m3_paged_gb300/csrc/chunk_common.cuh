@@ -32,6 +32,7 @@ __device__ __forceinline__ RowAt row_at(const ChunkParams& p, int packed) {
 }
 __device__ __forceinline__ int token_at(const ChunkParams& p, int packed) { return div_page(packed, p.G, p.g_div); }
 __device__ __forceinline__ int div_s(const ChunkParams& p, int x) { return div_page(x, p.S, p.s_div); }
+__device__ __forceinline__ int div_parts(const ChunkParams& p, int x) { return div_page(x, p.parts, p.parts_div); }
 __device__ __forceinline__ int div_hkv(const ChunkParams& p, int x) { return div_page(x, p.Hkv, p.hkv_div); }
 
 // One request's new tokens, checked against the plan.

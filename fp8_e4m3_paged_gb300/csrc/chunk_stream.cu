@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   auto vec_of = [&](int r) { return (int64_t)(req.row0 + token_of(r)) * p.Hq + head_of(r); };
 
   const ChunkSpan span = chunk_span(p, req, token_of(0), token_of(RC - 1));
-  int per = div_s(p, span.U + p.S - 1);
+  int per = min(div_parts(p, span.U + p.parts - 1), p.max_part);
   per = (per + kBlk * kWarps - 1) / (kBlk * kWarps) * (kBlk * kWarps);
   const int u0 = (int)min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
   if (u0 >= u1 && p.S > 1 && !clustered) {

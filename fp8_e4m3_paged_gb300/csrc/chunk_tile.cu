@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
     return (int64_t)(req.row0 + rr / p.G) * p.Hq + g * p.G + rr % p.G;
   };
   const ChunkSpan span = chunk_span(p, req, work.row0 / p.G, (work.row0 + RC - 1) / p.G);
-  int per = (span.U + p.S - 1) / p.S;
+  int per = min((span.U + p.parts - 1) / p.parts, p.max_part);
   per = (per + kT - 1) / kT * kT;
   const int u0 = (int)min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
   if (u0 >= u1) {  // nothing to see here: an empty partition, or rows before position 0

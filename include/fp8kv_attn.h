@@ -439,7 +439,7 @@ typedef struct {
   int32_t dtype;         /* FP8KV_DTYPE_F16 or FP8KV_DTYPE_BF16 (q and out) */
   int32_t kv_format;     /* FP8KV_KV_E4M3 or FP8KV_KV_E5M2 (bf16 caches: FP8KV_EUNSUPPORTED) */
   int32_t num_sms;       /* SMs to plan for; 0 = ask the current device */
-  int32_t num_splits;    /* partitions of the context; 0 = planner's choice (raised where an FP32 sum
+  int32_t num_splits;    /* partitions of the context; 0 = planner's choice (more where an FP32 sum
                             would run over more than 32768 positions) */
   int32_t kernel;        /* FP8KV_CHUNK_* */
 } fp8kv_chunk_desc;
@@ -457,7 +457,8 @@ typedef struct {
   int64_t partial_offset;  /* workspace: FP32 numerators [S][total_q][Hq][D] (S > 1) */
   int64_t ml_offset;       /* workspace: FP32 (max, sum) pairs [S][total_q][Hq] (S > 1) */
   int64_t workspace_bytes; /* minimum workspace size */
-  int32_t reserved[8];
+  int32_t min_splits;      /* partitions of a context that no FP32 sum limit splits further */
+  int32_t reserved[7];
 } fp8kv_chunk_plan_t;
 
 typedef struct {

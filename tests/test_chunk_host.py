@@ -487,3 +487,17 @@ def test_a_loose_bound_of_new_tokens_is_taken(B):
     assert p.max_q == 100
     p = B.fp8kv_attn_chunk_plan(_desc(B, max_q=1 << 24, num_q_heads=128, num_kv_heads=1))
     assert p.max_q == 100
+
+
+def test_further_partitions_wait_for_contexts_that_need_them(B):
+    """A bound far above the lengths: the partitions that the sum limit adds are not forced on short contexts."""
+    one = dict(batch=64, total_q=64, max_q=1, num_q_heads=32, num_kv_heads=8, max_kv_len=1 << 20, max_blocks=1 << 16)
+    p = B.fp8kv_attn_chunk_plan(_desc(B, **one))
+    assert p.min_splits == 1 and p.num_splits == 16
+    p = B.fp8kv_attn_chunk_plan(_desc(B, **one, num_splits=3))
+    assert p.min_splits == 3 and p.num_splits == 16
+    p = B.fp8kv_attn_chunk_plan(_desc(B, **one, num_splits=20))
+    assert p.min_splits == p.num_splits == 20
+    for bad in (0, 21):
+        p.min_splits = bad
+        assert B.lib.fp8kv_attn_chunk(ctypes.byref(p), ctypes.byref(_args(B, p)), None) == B.EINVAL

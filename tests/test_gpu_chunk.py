@@ -543,3 +543,22 @@ def test_logits_past_the_integers_of_32_bits(D, negative):
                 got = Run(c, kernel, splits)()
                 # rounding of the output and of the probabilities, and 2^-12 for sums and vanishing ones
                 assert ((got - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12)).all(), (power, kernel)
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("splits", [0, 1, 2, 7])
+def test_plans_for_far_longer_contexts(kernel, splits):
+    """Partitions that only the planned bound asks for stay empty; parity as with the exact plan."""
+    c = Case([(3, 400), (1, 65), (9, 1000), (1, 0)], Hq=4, Hkv=2, D=64, page=64)
+    d = copy.copy(c)
+    d.cols = 1 << 14
+    d.table = torch.zeros(len(c.requests), d.cols, dtype=torch.int32)
+    d.table[:, :c.cols] = c.table
+    exact, wide = Run(c, kernel, splits or 1), Run(d, kernel, splits, max_kv_len=1 << 20)
+    assert wide.plan.num_splits >= 16 > exact.plan.num_splits
+    got = wide()
+    check(got, c)
+    if splits:
+        assert wide.plan.min_splits == splits
+        a, b = exact(), got  # the same partitions, perhaps joined in another order
+        assert ((a - b).abs() <= a.abs() * 2.0 ** -9 + 2.0 ** -20).all()
