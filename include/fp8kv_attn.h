@@ -393,8 +393,9 @@ int fp8kv_attn_select_to_entries(const fp8kv_select_args* a, fp8kv_stream_t stre
  *
  * Numerical contract: FP32 logits, running maximum and sum; probabilities
  * enter the PV product as two fp16 numbers (2^-22 of their own value) in the
- * stream kernel, which takes every call of at most 16 query vectors per KV head, and
- * as one (2^-11) in the tile kernel; accumulated in FP32; no FP32 sum runs over more than 32768 positions (the plan has as many
+ * stream kernel (FP8KV_CHUNK_AUTO: every call of at most 16 query vectors per KV
+ * head, and more on few positions) and as one (2^-11) in the tile kernel;
+ * accumulated in FP32; no FP32 sum runs over more than 32768 positions (the plan has as many
  * partitions as that takes, more than num_splits if need be); one rounding to
  * q's type at the end.  bf16 queries are scaled to fp16 per row by
  * a power of two, which is exact for elements above 2^-28 of the row's
