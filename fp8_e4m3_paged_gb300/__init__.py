@@ -17,11 +17,16 @@ _EXPORTS = (
     "CacheWriteArgs", "MergeArgs", "SelectArgs",
     "fp8kv_attn_cache_write", "fp8kv_attn_combine_lse", "fp8kv_attn_merge", "fp8kv_attn_merge_scale",
     "fp8kv_attn_select_to_entries", "make_cache_write_args", "make_merge_args", "make_select_args",
-    "KV_E4M3", "KV_E5M2",
+    "KV_E4M3", "KV_E5M2", "KV_BF16",
     # ragged chunk attention (window, sinks), cache read, scale calibration
     "ChunkArgs", "ChunkCall", "ChunkDesc", "ChunkPlan", "CacheReadArgs", "CalibrateArgs",
     "fp8kv_attn_chunk", "fp8kv_attn_chunk_plan", "fp8kv_attn_cache_read", "fp8kv_attn_cache_calibrate",
     "make_chunk_args", "make_chunk_desc", "make_cache_read_args", "make_calibrate_args",
+    # trees of drafted tokens
+    "TreeArgs", "TreeCall", "fp8kv_attn_tree", "fp8kv_attn_tree_plan", "make_tree_args",
+    # which positions stay in the cache, and their move
+    "CacheSelectArgs", "CacheMoveArgs", "fp8kv_attn_cache_select", "fp8kv_attn_cache_move",
+    "make_cache_select_args", "make_cache_move_args",
     "DTYPE_F16", "DTYPE_BF16", "DTYPE_F32", "CHUNK_AUTO", "CHUNK_STREAM", "CHUNK_TILE",
 )
 

@@ -15,7 +15,7 @@ from typing import Optional
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp8kv_attn.so")
 
-REVISION = 5
+REVISION = 6
 OK = 0
 EINVAL = -1
 EUNSUPPORTED = -2
@@ -158,7 +158,7 @@ class ChunkPlan(ctypes.Structure):
         "max_kv_len", "max_blocks", "num_kv_blocks", "window", "sinks", "dtype", "kv_format", "group", "kernel",
         "num_splits", "row_tiles", "num_sms")] + [
         ("partial_offset", ctypes.c_int64), ("ml_offset", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
-        ("min_splits", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7),
+        ("min_splits", ctypes.c_int32), ("tree", ctypes.c_int32), ("reserved", ctypes.c_int32 * 6),
     ]
 
 
@@ -176,6 +176,12 @@ class ChunkArgs(ctypes.Structure):
         ("k_scale_dev", ctypes.c_void_p), ("v_scale_dev", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = [("chunk", ChunkArgs), ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("depth", ctypes.c_void_p)]
+    same = least = None  # as ChunkArgs; `words`: what a row of the mask has
 
 
 class CacheReadArgs(ctypes.Structure):
@@ -203,6 +209,36 @@ class CalibrateArgs(ctypes.Structure):
         ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
         ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
         ("slot_mapping", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class CacheSelectArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_kv_heads", "lists", "max_len", "budget", "sinks", "recent")] + [
+        ("score", ctypes.c_void_p), ("score_stride_req", ctypes.c_int64), ("score_stride_head", ctypes.c_int64),
+        ("kv_len", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p), ("keep_stride_req", ctypes.c_int64), ("keep_stride_list", ctypes.c_int64),
+        ("n_keep", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class CacheMoveArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_kv_heads", "lists", "max_count", "head_dim", "page_size", "max_blocks", "dst_max_blocks",
+        "num_kv_blocks", "kv_format")] + [
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("kc_stride_block", ctypes.c_int64), ("kc_stride_token", ctypes.c_int64),
+        ("kc_stride_head", ctypes.c_int64),
+        ("vc_stride_block", ctypes.c_int64), ("vc_stride_token", ctypes.c_int64),
+        ("vc_stride_head", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+        ("dst_table", ctypes.c_void_p), ("dst_table_stride", ctypes.c_int64),
+        ("src", ctypes.c_void_p), ("src_stride_req", ctypes.c_int64), ("src_stride_list", ctypes.c_int64),
+        ("count", ctypes.c_void_p), ("first", ctypes.c_void_p),
+        ("score", ctypes.c_void_p), ("score_out", ctypes.c_void_p),
+        ("score_stride_req", ctypes.c_int64), ("score_stride_head", ctypes.c_int64),
+        ("score_out_stride_req", ctypes.c_int64), ("score_out_stride_head", ctypes.c_int64),
+        ("max_len", ctypes.c_int32), ("status", ctypes.c_void_p),
     ]
 
 
@@ -240,8 +276,16 @@ lib.fp8kv_attn_chunk_plan.restype = ctypes.c_int
 lib.fp8kv_attn_chunk_plan.argtypes = [ctypes.POINTER(ChunkDesc), ctypes.POINTER(ChunkPlan)]
 lib.fp8kv_attn_chunk.restype = ctypes.c_int
 lib.fp8kv_attn_chunk.argtypes = [ctypes.POINTER(ChunkPlan), ctypes.POINTER(ChunkArgs), ctypes.c_void_p]
+lib.fp8kv_attn_tree_plan.restype = ctypes.c_int
+lib.fp8kv_attn_tree_plan.argtypes = [ctypes.POINTER(ChunkDesc), ctypes.POINTER(ChunkPlan)]
+lib.fp8kv_attn_tree.restype = ctypes.c_int
+lib.fp8kv_attn_tree.argtypes = [ctypes.POINTER(ChunkPlan), ctypes.POINTER(TreeArgs), ctypes.c_void_p]
 lib.fp8kv_attn_cache_read.restype = ctypes.c_int
 lib.fp8kv_attn_cache_read.argtypes = [ctypes.POINTER(CacheReadArgs), ctypes.c_void_p]
+lib.fp8kv_attn_cache_select.restype = ctypes.c_int
+lib.fp8kv_attn_cache_select.argtypes = [ctypes.POINTER(CacheSelectArgs), ctypes.c_void_p]
+lib.fp8kv_attn_cache_move.restype = ctypes.c_int
+lib.fp8kv_attn_cache_move.argtypes = [ctypes.POINTER(CacheMoveArgs), ctypes.c_void_p]
 lib.fp8kv_attn_cache_calibrate.restype = ctypes.c_int
 lib.fp8kv_attn_cache_calibrate.argtypes = [ctypes.POINTER(CalibrateArgs), ctypes.c_void_p]
 
@@ -532,10 +576,14 @@ def make_chunk_desc(*, batch: int, total_q: int, max_q: int, num_q_heads: int, n
 
 
 def fp8kv_attn_chunk_plan(desc: ChunkDesc) -> ChunkPlan:
+    return _chunk_plan(lib.fp8kv_attn_chunk_plan, desc, "fp8kv_attn_chunk_plan")
+
+
+def _chunk_plan(make, desc: ChunkDesc, name: str) -> ChunkPlan:
     plan = ChunkPlan()
-    rc = lib.fp8kv_attn_chunk_plan(ctypes.byref(desc), ctypes.byref(plan))
+    rc = make(ctypes.byref(desc), ctypes.byref(plan))
     if rc != OK:
-        raise Fp8kvError(rc, "fp8kv_attn_chunk_plan")
+        raise Fp8kvError(rc, name)
     # what the tensors must have (make_chunk_args notes what they have): the same ..., and at least ...
     plan.same = (plan.num_q_heads, plan.num_kv_heads, plan.head_dim, plan.page_size, plan.dtype)
     plan.least = (plan.batch, plan.total_q, plan.max_blocks, plan.num_kv_blocks)
@@ -580,13 +628,18 @@ def make_chunk_args(*, q, k_cache, v_cache, out, workspace, softmax_scale: float
     return a
 
 
-def fp8kv_attn_chunk(plan: ChunkPlan, args: ChunkArgs, stream: int = 0) -> None:
+def _fits(plan, args) -> None:
+    """The tensors are those that the plan is for."""
     same = args.same
     if same is not None and plan.same is not None:
         _check(same == plan.same, "the plan's heads, head dim, page size and type are not those of the tensors")
         (b, n, c, k), (pb, pn, pc, pk) = args.least, plan.least
         if b < pb or n < pn or c < pc or k < pk:
             raise ValueError("the plan has more requests, rows, table columns or blocks than the tensors")
+
+
+def fp8kv_attn_chunk(plan: ChunkPlan, args: ChunkArgs, stream: int = 0) -> None:
+    _fits(plan, args)
     rc = lib.fp8kv_attn_chunk(ctypes.byref(plan), ctypes.byref(args), stream)
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_chunk")
@@ -600,6 +653,54 @@ class ChunkCall:
 
     def run(self, stream: int) -> None:
         fp8kv_attn_chunk(self.plan, self.args, stream)
+
+
+def fp8kv_attn_tree_plan(desc: ChunkDesc) -> ChunkPlan:
+    return _chunk_plan(lib.fp8kv_attn_tree_plan, desc, "fp8kv_attn_tree_plan")
+
+
+def make_tree_args(*, mask, depth=None, **chunk) -> TreeArgs:
+    """Fill a TreeArgs struct from torch CUDA tensors.
+
+    chunk: as for make_chunk_args; mask: int32 [total_q][words] (the uint32 bit
+    patterns), words contiguous, at least one for 32 nodes of the plan's max_q;
+    depth: int32 [total_q], needed with a window."""
+    import torch
+
+    q = chunk["q"]
+    _check(mask.dtype == torch.int32 and mask.dim() == 2 and mask.shape[0] == q.shape[0] and
+           (mask.stride(1) == 1 or mask.shape[1] <= 1) and mask.stride(0) >= 0,
+           "mask: int32 [total_q][words], words contiguous")
+    if depth is not None:
+        _int32(depth, q.shape[0], "depth")
+    _one_device(q, mask, depth)
+    a = TreeArgs()
+    made = make_chunk_args(**chunk)
+    a.chunk = made
+    a.mask, a.mask_stride, a.depth = _ptr(mask), mask.stride(0), _ptr(depth)
+    if mask.shape[0] <= 1:  # one row: its next is never read
+        a.mask_stride = max(mask.stride(0), mask.shape[1])
+    a.same, a.least, a.words = made.same, made.least, mask.shape[1]
+    return a
+
+
+def fp8kv_attn_tree(plan: ChunkPlan, args: TreeArgs, stream: int = 0) -> None:
+    _fits(plan, args)
+    if args.same is not None:
+        _check(32 * args.words >= plan.max_q, "mask: fewer words than the plan's max_q nodes take")
+    rc = lib.fp8kv_attn_tree(ctypes.byref(plan), ctypes.byref(args), stream)
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_tree")
+
+
+@dataclass
+class TreeCall:
+    """A planned tree attention over fixed device buffers (graph friendly)."""
+    plan: ChunkPlan
+    args: TreeArgs
+
+    def run(self, stream: int) -> None:
+        fp8kv_attn_tree(self.plan, self.args, stream)
 
 
 def make_cache_read_args(*, k_cache, v_cache, block_table, cu_len, k_out, v_out, start=None, k_scale: float = 1.0,
@@ -675,3 +776,110 @@ def fp8kv_attn_cache_calibrate(args: CalibrateArgs, stream: int = 0) -> None:
     rc = lib.fp8kv_attn_cache_calibrate(ctypes.byref(args), stream)
     if rc != OK:
         raise Fp8kvError(rc, "fp8kv_attn_cache_calibrate")
+
+
+# ---------------------------------------------------------------- which positions stay, and their move
+
+def _status(t) -> None:
+    import torch
+
+    _check(t is None or (t.dtype in (torch.int32, torch.uint32) and t.numel() == 1), "status: one int32 element")
+
+
+def _lists(t, name: str):
+    """Strides (request, list) of an int32 tensor [B][lists][entries], entries contiguous."""
+    import torch
+
+    _check(t.dtype == torch.int32 and t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] <= 1),
+           f"{name}: int32 [B][lists][entries], entries contiguous")
+    return t.stride()[:2]
+
+
+def _weights(t, name: str):
+    """Strides (request, head) of a float32 tensor [B][Hkv][positions], positions contiguous."""
+    import torch
+
+    _check(t.dtype == torch.float32 and t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] <= 1),
+           f"{name}: float32 [B][Hkv][positions], positions contiguous")
+    return t.stride()[:2]
+
+
+def make_cache_select_args(*, score, kv_len, budget: int, keep, n_keep, sinks: int = 0, recent: int = 0,
+                           status=None) -> CacheSelectArgs:
+    """Fill a CacheSelectArgs struct from torch CUDA tensors.
+
+    score: float32 [B][Hkv][positions]; kv_len, n_keep: int32 [B]; keep: int32
+    [B][Hkv][>= min(budget, positions)] for a list per KV head, [B][1][...] for
+    one list by the heads' sum; status: optional int32 tensor of one element."""
+    _one_device(score, kv_len, keep, n_keep, status)
+    a = CacheSelectArgs()
+    a.score_stride_req, a.score_stride_head = _weights(score, "score")
+    a.keep_stride_req, a.keep_stride_list = _lists(keep, "keep")
+    a.batch, a.num_kv_heads, a.max_len = score.shape
+    _check(keep.shape[0] == a.batch and keep.shape[1] in (1, a.num_kv_heads) and
+           keep.shape[2] >= min(budget, a.max_len), "keep: [B][1 or Hkv][at least min(budget, positions)]")
+    _int32(kv_len, a.batch, "kv_len")
+    _int32(n_keep, a.batch, "n_keep")
+    _status(status)
+    a.lists, a.budget, a.sinks, a.recent = keep.shape[1], budget, sinks, recent
+    a.score, a.kv_len, a.keep, a.n_keep, a.status = (_ptr(t) for t in (score, kv_len, keep, n_keep, status))
+    return a
+
+
+def fp8kv_attn_cache_select(args: CacheSelectArgs, stream: int = 0) -> None:
+    rc = lib.fp8kv_attn_cache_select(ctypes.byref(args), stream)
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_cache_select")
+
+
+def make_cache_move_args(*, k_cache, v_cache, block_table, src, count, first=None, dst_table=None, score=None,
+                         score_out=None, status=None, kv_format: int = KV_E4M3) -> CacheMoveArgs:
+    """Fill a CacheMoveArgs struct from torch CUDA tensors.
+
+    k_cache / v_cache: uint8 [blocks][page][Hkv][D] views (int16 or bfloat16 for
+    bf16 caches); block_table, dst_table: int32 [B][columns] (dst_table None: in
+    place); src: int32 [B][1 or Hkv][entries], as fp8kv_attn_cache_select writes
+    them; count, first: int32 [B] (first None: 0); score / score_out: optional
+    float32 [B][Hkv][positions], not overlapping; status: optional int32 tensor of
+    one element."""
+    _one_device(k_cache, v_cache, block_table, src, count, first, dst_table, score, score_out, status)
+    a = CacheMoveArgs()
+    size = 2 if kv_format == KV_BF16 else 1
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t.dim() == 4 and t.element_size() == size and t.stride(3) == 1,
+               f"{name}: elements of {size} bytes, [blocks][page][Hkv][D] with d contiguous")
+    _check(k_cache.shape == v_cache.shape, "v_cache: the same shape as k_cache")
+    a.num_kv_blocks, a.page_size, a.num_kv_heads, a.head_dim = k_cache.shape
+    a.kv_format = kv_format
+    a.block_table, a.block_table_stride = _table(block_table, "block_table")
+    a.batch, a.max_blocks = block_table.shape
+    if dst_table is not None:
+        a.dst_table, a.dst_table_stride = _table(dst_table, "dst_table")
+        _check(dst_table.shape[0] == a.batch, "dst_table: a row for each request")
+        a.dst_max_blocks = dst_table.shape[1]
+    a.src_stride_req, a.src_stride_list = _lists(src, "src")
+    _check(src.shape[0] == a.batch and src.shape[1] in (1, a.num_kv_heads), "src: [B][1 or Hkv][entries]")
+    a.lists, a.max_count = src.shape[1:]
+    _int32(count, a.batch, "count")
+    if first is not None:
+        _int32(first, a.batch, "first")
+    _status(status)
+    _check((score is None) == (score_out is None), "score and score_out: both or none")
+    if score is not None:
+        a.score_stride_req, a.score_stride_head = _weights(score, "score")
+        a.score_out_stride_req, a.score_out_stride_head = _weights(score_out, "score_out")
+        _check(score.shape == score_out.shape and score.shape[:2] == (a.batch, a.num_kv_heads),
+               "score, score_out: [B][Hkv][positions], the same shape")
+        a.max_len = score.shape[2]
+    a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+    a.kc_stride_block, a.kc_stride_token, a.kc_stride_head = (x * size for x in k_cache.stride()[:3])
+    a.vc_stride_block, a.vc_stride_token, a.vc_stride_head = (x * size for x in v_cache.stride()[:3])
+    a.src, a.count, a.first, a.score, a.score_out, a.status = (
+        _ptr(t) for t in (src, count, first, score, score_out, status))
+    return a
+
+
+def fp8kv_attn_cache_move(args: CacheMoveArgs, stream: int = 0) -> None:
+    rc = lib.fp8kv_attn_cache_move(ctypes.byref(args), stream)
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_cache_move")

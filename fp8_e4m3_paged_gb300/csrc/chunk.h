@@ -23,6 +23,7 @@ constexpr int kChunkStreamWarps = 4;
 inline int64_t chunk_max_part(int32_t kernel) {
   return kernel == FP8KV_CHUNK_STREAM ? kChunkStreamWarps * kChunkMaxSum / 2 : kChunkMaxSum;
 }
+constexpr int kTreeNodesMax = 1024;         // nodes of one request's tree
 inline int chunk_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }  // query vectors per CTA
 
 // Everything the chunk kernels need, resolved on the host.
@@ -51,6 +52,10 @@ struct ChunkParams {
   unsigned int* status;
   float* partial;          // [S][total_q][Hq][D] (S > 1)
   float2* ml;              // [S][total_q][Hq]
+  // trees of drafted tokens
+  const uint32_t* mask;    // [total_q][mask_stride] bit j % 32 of word j / 32: the row sees new token j
+  int64_t mask_stride;     // words
+  const int32_t* depth;    // [total_q] (windows only)
 };
 
 // Whether the partitions form a cluster that joins them itself: only where all of them have
@@ -64,6 +69,8 @@ inline bool chunk_clustered(const fp8kv_chunk_plan_t* plan) {
 
 cudaError_t launch_chunk_stream(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_chunk_tile(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
+cudaError_t launch_tree_stream(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
+cudaError_t launch_tree_tile(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_chunk_join(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_cache_read(const fp8kv_cache_read_args& a, cudaStream_t s);
 cudaError_t launch_calibrate(const fp8kv_calibrate_args& a, cudaStream_t s);

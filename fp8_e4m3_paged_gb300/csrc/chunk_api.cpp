@@ -7,6 +7,7 @@
 
 #include <cuda_runtime.h>
 
+#include "args_check.h"
 #include "chunk.h"
 #include "fp8kv_attn.h"
 #include "output_layout.h"
@@ -15,26 +16,7 @@ using namespace fp8kv;
 
 namespace {
 
-int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
-bool strides_ok(const int64_t* s, int n, int64_t unit) {
-  for (int i = 0; i < n; ++i)
-    if (s[i] < 0 || s[i] % unit) return false;
-  return true;
-}
-// Finite host scales, or device floats on their boundary.
-template <class Args>
-bool scales_ok(const Args& a) {
-  return aligned(a.k_scale_dev, 4) && aligned(a.v_scale_dev, 4) && (a.k_scale_dev || std::isfinite(a.k_scale)) &&
-         (a.v_scale_dev || std::isfinite(a.v_scale));
-}
-bool fp8_format(int32_t f) { return f == FP8KV_KV_E4M3 || f == FP8KV_KV_E5M2; }
-int done(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ECUDA; }
-
-}  // namespace
-
-extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan) {
+int make_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan, bool tree) {
   if (!d || !plan) return FP8KV_EINVAL;
   if (d->batch < 0 || d->total_q < 0 || d->max_q < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1)
     return FP8KV_EINVAL;
@@ -56,6 +38,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
       max_q * group > (1 << 30) || (int64_t)d->total_q * d->num_q_heads > ((int64_t)1 << 32) ||
       d->num_sms > 65535)
     return FP8KV_EUNSUPPORTED;
+  if (tree && max_q > kTreeNodesMax) return FP8KV_EUNSUPPORTED;
   if (d->kernel == FP8KV_CHUNK_STREAM && max_q * group > 65535 * (int64_t)kChunkStreamRows)
     return FP8KV_EUNSUPPORTED;
 
@@ -85,6 +68,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   P.sinks = P.window ? std::min(d->sinks, d->max_kv_len) : 0;
   P.dtype = d->dtype;
   P.kv_format = d->kv_format;
+  P.tree = tree;
   P.group = (int32_t)group;
   P.num_sms = sms;
 
@@ -129,7 +113,7 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
     units = (int64_t)P.row_tiles * P.num_kv_heads;
     slots = sms;
     unit = kChunkTileTokens;
-    span_q = std::min<int64_t>(P.max_q, ceil_div(tile, group) + 1);
+    span_q = tree ? P.max_q : std::min<int64_t>(P.max_q, ceil_div(tile, group) + 1);
   }
   const int64_t seen = seen_by(span_q);
   int64_t S = units ? slots / units : 1;
@@ -176,8 +160,6 @@ extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan
   *plan = P;
   return FP8KV_OK;
 }
-
-namespace {
 
 int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, ChunkParams* p) {
   if (!plan || !a) return FP8KV_EINVAL;
@@ -257,13 +239,40 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
 
 }  // namespace
 
+extern "C" int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan) {
+  return make_plan(d, plan, false);
+}
+
+extern "C" int fp8kv_attn_tree_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan) {
+  return make_plan(d, plan, true);
+}
+
 extern "C" int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, fp8kv_stream_t stream) {
   ChunkParams p;
   const int rc = build_chunk(plan, a, &p);
-  if (rc != FP8KV_OK || plan->batch == 0 || plan->total_q == 0) return rc;
+  if (rc != FP8KV_OK) return rc;
+  if (plan->tree) return FP8KV_EINVAL;  // (causal rows: not what the plan is for)
+  if (plan->batch == 0 || plan->total_q == 0) return FP8KV_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e =
       plan->kernel == FP8KV_CHUNK_STREAM ? launch_chunk_stream(plan, p, st) : launch_chunk_tile(plan, p, st);
+  if (e == cudaSuccess && p.S > 1 && !chunk_clustered(plan)) e = launch_chunk_join(plan, p, st);
+  return done(e);
+}
+
+extern "C" int fp8kv_attn_tree(const fp8kv_chunk_plan_t* plan, const fp8kv_tree_args* a, fp8kv_stream_t stream) {
+  ChunkParams p;
+  const int rc = build_chunk(plan, a ? &a->chunk : nullptr, &p);
+  if (rc != FP8KV_OK) return rc;
+  if (!plan->tree || plan->max_q > kTreeNodesMax) return FP8KV_EINVAL;
+  if (plan->batch == 0 || plan->total_q == 0) return FP8KV_OK;
+  if (!a->mask || !aligned(a->mask, 4) || a->mask_stride < ceil_div(plan->max_q, 32)) return FP8KV_EINVAL;
+  if (plan->window > 0 && (!a->depth || !aligned(a->depth, 4))) return FP8KV_EINVAL;
+  p.mask = a->mask;
+  p.mask_stride = a->mask_stride;
+  p.depth = a->depth;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = plan->kernel == FP8KV_CHUNK_STREAM ? launch_tree_stream(plan, p, st) : launch_tree_tile(plan, p, st);
   if (e == cudaSuccess && p.S > 1 && !chunk_clustered(plan)) e = launch_chunk_join(plan, p, st);
   return done(e);
 }

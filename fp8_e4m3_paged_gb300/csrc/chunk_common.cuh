@@ -1,6 +1,7 @@
 // Geometry and small device helpers shared by the chunk-attention kernels.
 #pragma once
 
+#include <climits>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -64,8 +65,20 @@ struct ChunkSpan {
   __device__ __forceinline__ int position(int v) const { return v < sk ? v : v + skip; }
 };
 
+// TREE: the new tokens are a tree's nodes, which all stand behind the context whatever the
+// order that they are stored in: the context from the root's window on, and all nodes.
+template <bool TREE = false>
 __device__ __forceinline__ ChunkSpan chunk_span(const ChunkParams& p, const ChunkRequest& r, int ia, int ib) {
   ChunkSpan s = {0, 0, 0};
+  if (TREE) {
+    const int base = max(r.kv - r.n, 0);
+    if (p.window > 0) {
+      s.sk = min(p.sinks, base);
+      s.skip = max(max(0, base - p.window + 1) - s.sk, 0);
+    }
+    s.U = r.kv - s.skip;
+    return s;
+  }
   const int first = r.kv - r.n + ia;
   const int hi = max(r.kv - r.n + ib + 1, 0);
   if (p.window > 0) {
@@ -99,14 +112,58 @@ __device__ __forceinline__ bool part_written(float2 ml) { return __float_as_uint
 // What one row sees on that axis: v < hi and (v >= lo or v < sk).
 struct ChunkRow {
   int hi, lo;
+  __device__ __forceinline__ bool sees(int v, int sk) const { return v < hi && (v >= lo || v < sk); }
 };
-__device__ __forceinline__ ChunkRow chunk_row(const ChunkParams& p, const ChunkRequest& r, const ChunkSpan& s,
-                                              int i) {
-  const int pos = r.kv - r.n + i;
-  ChunkRow c;
-  c.hi = pos + 1 - s.skip;
-  c.lo = (p.window > 0 ? max(pos - p.window + 1, 0) : 0) - s.skip;
-  return c;
+// ... and a tree's row: of the context (v < hi) the same, of the nodes (v >= hi: node v - hi)
+// those of its mask.  (Node numbers stay below the request's nodes: v < U.)
+struct TreeRow {
+  int hi, lo;
+  const uint32_t* mask;
+  __device__ __forceinline__ bool sees(int v, int sk) const {
+    if (v < hi) return v >= lo || v < sk;
+    const int j = v - hi;
+    return (__ldg(mask + (j >> 5)) >> (j & 31)) & 1u;
+  }
+};
+template <bool TREE>
+struct RowOfTree {
+  using type = ChunkRow;
+};
+template <>
+struct RowOfTree<true> {
+  using type = TreeRow;
+};
+
+// A row that sees everything (rows past the last one, whose results are dropped).
+template <bool TREE>
+__device__ __forceinline__ typename RowOfTree<TREE>::type any_row(int lo) {
+  if constexpr (TREE)
+    return {INT_MAX, lo, nullptr};
+  else
+    return {INT_MAX, lo};
+}
+
+template <bool TREE = false>
+__device__ __forceinline__ typename RowOfTree<TREE>::type chunk_row(const ChunkParams& p, const ChunkRequest& r,
+                                                                    const ChunkSpan& s, int i) {
+  if constexpr (TREE) {
+    TreeRow c;
+    c.hi = r.kv - r.n - s.skip;
+    c.lo = -s.skip;
+    c.mask = p.mask + (int64_t)(r.row0 + i) * p.mask_stride;
+    if (p.window > 0) {
+      const int d = __ldg(p.depth + r.row0 + i), at = min(max(d, 0), r.n - 1);
+      if (at != d) set_status(p.status, FP8KV_STATUS_BAD_LEN);
+      c.lo = max(r.kv - r.n + at - p.window + 1, 0) - s.skip;
+    }
+    return c;
+  } else {
+    const int pos = r.kv - r.n + i;
+    ChunkRow c;
+    c.hi = pos + 1 - s.skip;
+    c.lo = (p.window > 0 ? max(pos - p.window + 1, 0) : 0) - s.skip;
+    return c;
+  }
 }
 
 // Physical place of a position: false when its block is out of range.
@@ -201,8 +258,8 @@ __device__ __noinline__ void mark_nonfinite_v(const ChunkParams& p, uint32_t* ki
       if (kind == 0u) continue;
       const int d = c * 16 + j;
       for (int i = 0; i < RC; ++i) {
-        const ChunkRow row = row_of(i);
-        if (v < row.hi && (v >= row.lo || v < span.sk)) atomicOr(&kinds[i * (D / 4) + d / 4], kind << (8 * (d % 4)));
+        const auto row = row_of(i);
+        if (row.sees(v, span.sk)) atomicOr(&kinds[i * (D / 4) + d / 4], kind << (8 * (d % 4)));
       }
     }
   }

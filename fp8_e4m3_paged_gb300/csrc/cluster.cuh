@@ -1,0 +1,26 @@
+// Thread-block clusters of the cache kernels: barrier over all their CTAs in two halves,
+// rank, size, and a load from the place that `p` has in the shared memory of CTA `rank`.
+#pragma once
+
+#include <cstdint>
+
+#include "tc_ptx.cuh"
+
+namespace fp8kv {
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ uint32_t peer_load(const uint32_t* p, int rank) {
+  uint32_t a, x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+  return x;
+}
+
+}  // namespace fp8kv

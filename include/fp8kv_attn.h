@@ -70,7 +70,7 @@ extern "C" {
  * stale plan cannot reach kernels with another partial layout ("DFlash2 E4M3
  * attention with FP32 state", intro paragraph 5: the wrapper requires a given
  * precision capability revision). */
-#define FP8KV_ATTN_REVISION 5
+#define FP8KV_ATTN_REVISION 6
 
 /* Return codes. */
 #define FP8KV_OK 0
@@ -459,7 +459,8 @@ typedef struct {
   int64_t ml_offset;       /* workspace: FP32 (max, sum) pairs [S][total_q][Hq] (S > 1) */
   int64_t workspace_bytes; /* minimum workspace size */
   int32_t min_splits;      /* partitions of a context that no FP32 sum limit splits further */
-  int32_t reserved[7];
+  int32_t tree;            /* 1: made by fp8kv_attn_tree_plan */
+  int32_t reserved[6];
 } fp8kv_chunk_plan_t;
 
 typedef struct {
@@ -489,6 +490,42 @@ int fp8kv_attn_chunk_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan);
 /* Launch the attention on `stream` (one kernel, and a second that joins the
  * partitions where the first does not: it joins up to 8 of the stream kernel). */
 int fp8kv_attn_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, fp8kv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Tree attention: trees of drafted tokens over the paged FP8 cache.
+ *
+ * A verify step whose drafts branch.  The new tokens of request b are the n_b
+ * nodes of a tree (of several, or of any other graph), one after another in
+ * the order that the caller likes, at the last n_b of its kv_len[b] positions:
+ * node i at position base + i with base = kv_len[b] - n_b, its K and V rows in the
+ * cache already.  It attends to
+ *
+ *   the context t < base                                    window = 0
+ *   t < base with base + depth[i] - t < window or t < sinks window > 0
+ *   the nodes j whose bit is set in its row of the mask     (itself only if its bit is)
+ *
+ * so that a mask of all ancestors and the node itself gives every path of the
+ * tree the attention that it would have alone.  depth[i] is the node's distance from
+ * its root (what its position in the text is behind base); it matters to the
+ * window over the context only, never among nodes.  A node that sees
+ * nothing yields +0.0.
+ *
+ * Everything else is as in fp8kv_attn_chunk: logits, scales, numerical contract,
+ * anomalies (a depth outside [0, n_b) is clamped and sets FP8KV_STATUS_BAD_LEN; mask bits
+ * past the last node are ignored; nodes that kv_len[b] < n_b puts before position 0 are
+ * seen by none), rows behind the last request, workspaces, capture.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  fp8kv_chunk_args chunk; /* as for fp8kv_attn_chunk */
+  const uint32_t* mask;   /* bit j % 32 of word row*mask_stride + j / 32: new token `row` sees node j of its request */
+  int64_t mask_stride;    /* words, >= ceil(plan->max_q / 32) */
+  const int32_t* depth;   /* [total_q]; NULL without a window */
+} fp8kv_tree_args;
+
+/* As fp8kv_attn_chunk_plan, for fp8kv_attn_tree; more than 1024 nodes (max_q): FP8KV_EUNSUPPORTED. */
+int fp8kv_attn_tree_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan);
+/* Launch the attention on `stream`; plans of fp8kv_attn_chunk_plan: FP8KV_EINVAL (and the other way round). */
+int fp8kv_attn_tree(const fp8kv_chunk_plan_t* plan, const fp8kv_tree_args* a, fp8kv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Cache read: rows of the paged cache back as fp16, bf16 or FP32.
@@ -570,6 +607,95 @@ typedef struct {
 } fp8kv_calibrate_args;
 
 int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Cache selection: which positions stay, by the weights that they gathered.
+ *
+ * Of the kv_len[b] positions of request b, n_keep[b] = min(kv_len[b], budget) stay: the
+ * first `sinks` and the last `recent`, and of those between the ones with the
+ * largest weights; a tie goes to the lower position, -0 equals +0, a NaN is below
+ * every number.  keep[b][l][0 .. n_keep[b]-1] receives them in increasing order;
+ * what lies behind is left as it is.
+ *
+ * lists = num_kv_heads: a list for each KV head by its own weights.  lists = 1: one for all
+ * heads, by the FP32 sum of their weights, added head after head.  Exact
+ * and deterministic; graph-capturable, no workspace.  A kv_len outside [0, max_len] is
+ * clamped and sets FP8KV_STATUS_BAD_LEN in *status.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch;         /* B >= 0 */
+  int32_t num_kv_heads;  /* Hkv, 1..65535 */
+  int32_t lists;         /* 1 or num_kv_heads */
+  int32_t max_len;       /* positions of a row of weights, 0..2^30 */
+  int32_t budget;        /* positions that stay at most, >= 1 */
+  int32_t sinks, recent; /* >= 0, sinks + recent <= budget */
+  const float* score;    /* (b, h, t) at b*score_stride_req + h*score_stride_head + t */
+  int64_t score_stride_req, score_stride_head; /* elements, >= 0 */
+  const int32_t* kv_len; /* [B] */
+  int32_t* keep;         /* (b, l, k) at b*keep_stride_req + l*keep_stride_list + k; lists must not overlap */
+  int64_t keep_stride_req, keep_stride_list;   /* elements */
+  int32_t* n_keep;       /* [B] */
+  uint32_t* status;      /* optional device word, NULL = none */
+} fp8kv_cache_select_args;
+
+int fp8kv_attn_cache_select(const fp8kv_cache_select_args* a, fp8kv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Cache move: rows of the paged cache from one position to another.
+ *
+ * For request b, KV head h and k < count[b], with s = src[b][h's list][k]: the K and the V
+ * row at position first[b] + s go to position first[b] + k, byte for byte.  So
+ * the positions that fp8kv_attn_cache_select keeps come together at the front
+ * (first = 0; the context is then count[b] long), and so do the nodes of a tree's accepted
+ * path (first = the tree's first position, src = node numbers).
+ *
+ * dst_table = NULL: within the pages that the rows are in.  All moves happen as if every row was
+ * read before any was written; a move towards the end (s < k) is not made and sets
+ * FP8KV_STATUS_BAD_ENTRIES.  Rows that stay where they are (s = k) are not touched, so a
+ * shared prefix in front of the first row that goes is safe; pages of rows that
+ * move belong to one request alone.
+ * dst_table: into other pages.  Any s >= 0; no page is both read and written.
+ *
+ * score / score_out (both or none): the weights' row of each head moves likewise,
+ * score_out[b][h][first + k] = score[b][h][first + s], between two buffers that do not
+ * overlap; what is not moved to is left as it is.
+ *
+ * A position outside its table, or whose block is out of range: the row is not moved,
+ * FP8KV_STATUS_BAD_BLOCK; weights outside [0, max_len): FP8KV_STATUS_BAD_LEN, as is a
+ * count outside [0, max_count], which is clamped.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch;          /* B >= 0 */
+  int32_t num_kv_heads;   /* Hkv, 1..65535 */
+  int32_t lists;          /* 1 (all heads move alike) or num_kv_heads */
+  int32_t max_count;      /* bound of count, 0..2^30 */
+  int32_t head_dim;       /* D: a multiple of 16, 16..1024 */
+  int32_t page_size;      /* >= 1 */
+  int32_t max_blocks;     /* columns of block_table, >= 1 */
+  int32_t dst_max_blocks; /* columns of dst_table (ignored without one) */
+  int32_t num_kv_blocks;  /* >= 1 */
+  int32_t kv_format;      /* FP8KV_KV_*: a row is D bytes, 2 D with bf16 caches */
+  uint8_t* k_cache;       /* as fp8kv_attn_args.k_cache */
+  uint8_t* v_cache;
+  int64_t kc_stride_block, kc_stride_token, kc_stride_head; /* bytes, multiples of 16 */
+  int64_t vc_stride_block, vc_stride_token, vc_stride_head;
+  const int32_t* block_table; /* [B][block_table_stride] */
+  int64_t block_table_stride; /* elements, >= max_blocks */
+  const int32_t* dst_table;   /* [B][dst_table_stride], NULL = in place */
+  int64_t dst_table_stride;   /* elements, >= dst_max_blocks */
+  const int32_t* src;         /* (b, l, k) at b*src_stride_req + l*src_stride_list + k */
+  int64_t src_stride_req, src_stride_list; /* elements, >= 0 */
+  const int32_t* count;       /* [B] rows of each list */
+  const int32_t* first;       /* [B], NULL = 0 */
+  const float* score;         /* optional weights, strides as in fp8kv_cache_select_args */
+  float* score_out;
+  int64_t score_stride_req, score_stride_head;         /* elements, >= 0 */
+  int64_t score_out_stride_req, score_out_stride_head; /* elements; rows must not overlap */
+  int32_t max_len;            /* positions of a row of weights */
+  uint32_t* status;           /* optional device word, NULL = none */
+} fp8kv_cache_move_args;
+
+int fp8kv_attn_cache_move(const fp8kv_cache_move_args* a, fp8kv_stream_t stream);
 
 /* Size of the library-owned device scratch used by fp8kv_attn_forward_static
  * (16 MiB; one copy per GPU that loads the library, held until exit). */
