@@ -24,7 +24,9 @@ _EXPORTS = (
     "make_chunk_args", "make_chunk_desc", "make_cache_read_args", "make_calibrate_args",
     # trees of drafted tokens
     "TreeArgs", "TreeCall", "fp8kv_attn_tree", "fp8kv_attn_tree_plan", "make_tree_args",
-    # which positions stay in the cache, and their move
+    # what cached positions gather, which of them stay, and their move
+    "CacheScoreArgs", "CacheScoreCall", "CacheScorePlan", "fp8kv_attn_cache_score", "fp8kv_attn_cache_score_plan",
+    "make_cache_score_args",
     "CacheSelectArgs", "CacheMoveArgs", "fp8kv_attn_cache_select", "fp8kv_attn_cache_move",
     "make_cache_select_args", "make_cache_move_args",
     "DTYPE_F16", "DTYPE_BF16", "DTYPE_F32", "CHUNK_AUTO", "CHUNK_STREAM", "CHUNK_TILE",

@@ -212,6 +212,33 @@ class CalibrateArgs(ctypes.Structure):
     ]
 
 
+class CacheScorePlan(ctypes.Structure):
+    same = least = None  # as ChunkPlan
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "revision", "batch", "total_q", "max_q", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
+        "max_kv_len", "max_blocks", "num_kv_blocks", "dtype", "kv_format", "group", "kernel", "num_splits",
+        "vectors", "row_tiles", "stat_part", "col_part", "row_groups", "num_sms")] + [
+        ("partial_offset", ctypes.c_int64), ("ml_offset", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 6),
+    ]
+
+
+class CacheScoreArgs(ctypes.Structure):
+    same = least = None  # as ChunkArgs
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("k_cache", ctypes.c_void_p),
+        ("k_stride_block", ctypes.c_int64), ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+        ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("softmax_scale", ctypes.c_float), ("k_scale", ctypes.c_float), ("k_scale_dev", ctypes.c_void_p),
+        ("score_in", ctypes.c_void_p),
+        ("score_in_stride_req", ctypes.c_int64), ("score_in_stride_head", ctypes.c_int64),
+        ("score", ctypes.c_void_p), ("score_stride_req", ctypes.c_int64), ("score_stride_head", ctypes.c_int64),
+        ("decay", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class CacheSelectArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "num_kv_heads", "lists", "max_len", "budget", "sinks", "recent")] + [
@@ -282,6 +309,10 @@ lib.fp8kv_attn_tree.restype = ctypes.c_int
 lib.fp8kv_attn_tree.argtypes = [ctypes.POINTER(ChunkPlan), ctypes.POINTER(TreeArgs), ctypes.c_void_p]
 lib.fp8kv_attn_cache_read.restype = ctypes.c_int
 lib.fp8kv_attn_cache_read.argtypes = [ctypes.POINTER(CacheReadArgs), ctypes.c_void_p]
+lib.fp8kv_attn_cache_score_plan.restype = ctypes.c_int
+lib.fp8kv_attn_cache_score_plan.argtypes = [ctypes.POINTER(ChunkDesc), ctypes.POINTER(CacheScorePlan)]
+lib.fp8kv_attn_cache_score.restype = ctypes.c_int
+lib.fp8kv_attn_cache_score.argtypes = [ctypes.POINTER(CacheScorePlan), ctypes.POINTER(CacheScoreArgs), ctypes.c_void_p]
 lib.fp8kv_attn_cache_select.restype = ctypes.c_int
 lib.fp8kv_attn_cache_select.argtypes = [ctypes.POINTER(CacheSelectArgs), ctypes.c_void_p]
 lib.fp8kv_attn_cache_move.restype = ctypes.c_int
@@ -802,6 +833,71 @@ def _weights(t, name: str):
     _check(t.dtype == torch.float32 and t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] <= 1),
            f"{name}: float32 [B][Hkv][positions], positions contiguous")
     return t.stride()[:2]
+
+
+def fp8kv_attn_cache_score_plan(desc: ChunkDesc) -> CacheScorePlan:
+    plan = CacheScorePlan()
+    rc = lib.fp8kv_attn_cache_score_plan(ctypes.byref(desc), ctypes.byref(plan))
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_cache_score_plan")
+    plan.same = (plan.num_q_heads, plan.num_kv_heads, plan.head_dim, plan.page_size, plan.dtype)
+    plan.least = (plan.batch, plan.total_q, plan.max_blocks, plan.num_kv_blocks)
+    return plan
+
+
+def make_cache_score_args(*, q, k_cache, block_table, cu_q, kv_len, softmax_scale: float, score, workspace,
+                          score_in=None, decay: float = 1.0, k_scale: float = 1.0, k_scale_dev=None) -> CacheScoreArgs:
+    """Fill a CacheScoreArgs struct from torch CUDA tensors.
+
+    q, k_cache, block_table, cu_q, kv_len, workspace: as for make_chunk_args;
+    score, score_in: float32 [B][Hkv][at least the plan's max_kv_len] (positions
+    contiguous), score_in None (nothing gathered before), score itself, or a
+    buffer that does not overlap it."""
+    dtype = _torch_dtype(q, DTYPE_F16, DTYPE_BF16)
+    table, table_stride = _table(block_table, "block_table")
+    b = block_table.shape[0]
+    _int32(cu_q, b + 1, "cu_q")
+    _int32(kv_len, b, "kv_len")
+    _device_scale(k_scale_dev, "k_scale_dev")
+    _one_device(q, k_cache, block_table, cu_q, kv_len, k_scale_dev, score, score_in, workspace)
+    a = CacheScoreArgs()
+    a.q, (a.q_stride_token, a.q_stride_head) = _ptr(q), _rows(q, "q")
+    a.k_cache = _ptr(k_cache)
+    a.k_stride_block, a.k_stride_token, a.k_stride_head = _pages(k_cache, "k_cache")
+    a.block_table, a.block_table_stride = table, table_stride
+    a.cu_q, a.kv_len = _ptr(cu_q), _ptr(kv_len)
+    a.softmax_scale, a.k_scale, a.k_scale_dev = float(softmax_scale), float(k_scale), _ptr(k_scale_dev)
+    a.score, (a.score_stride_req, a.score_stride_head) = _ptr(score), _weights(score, "score")
+    _check(score.shape[:2] == (b, k_cache.shape[2]), "score: [B][Hkv][positions]")
+    if score_in is not None:
+        a.score_in, (a.score_in_stride_req, a.score_in_stride_head) = _ptr(score_in), _weights(score_in, "score_in")
+        _check(score_in.shape == score.shape, "score_in: the same shape as score")
+    a.decay = float(decay)
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _check(q.shape[2] == k_cache.shape[3], "q: the cache's head dim")
+    a.same = (q.shape[1], *k_cache.shape[2:], k_cache.shape[1], dtype)
+    a.least = (b, q.shape[0], block_table.shape[1], k_cache.shape[0])
+    a.positions = score.shape[2]
+    return a
+
+
+def fp8kv_attn_cache_score(plan: CacheScorePlan, args: CacheScoreArgs, stream: int = 0) -> None:
+    _fits(plan, args)
+    if args.same is not None:
+        _check(args.positions >= plan.max_kv_len, "score: fewer positions than the plan's max_kv_len")
+    rc = lib.fp8kv_attn_cache_score(ctypes.byref(plan), ctypes.byref(args), stream)
+    if rc != OK:
+        raise Fp8kvError(rc, "fp8kv_attn_cache_score")
+
+
+@dataclass
+class CacheScoreCall:
+    """Planned gathered weights over fixed device buffers (graph friendly)."""
+    plan: CacheScorePlan
+    args: CacheScoreArgs
+
+    def run(self, stream: int) -> None:
+        fp8kv_attn_cache_score(self.plan, self.args, stream)
 
 
 def make_cache_select_args(*, score, kv_len, budget: int, keep, n_keep, sinks: int = 0, recent: int = 0,

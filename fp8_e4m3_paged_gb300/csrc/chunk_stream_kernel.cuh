@@ -44,6 +44,7 @@
 
 #include "chunk_common.cuh"
 #include "internal.h"
+#include "stream_ptx.cuh"
 #include "tc_ptx.cuh"
 
 namespace fp8kv {
@@ -92,19 +93,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return r;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Thread-block cluster: barrier over all its CTAs in two halves (the first without
 // order, for a CTA that has only begun), and stores into a peer's shared memory
 // (the place that `p` has in CTA `rank`).
@@ -124,35 +112,6 @@ __device__ __forceinline__ void peer_store(uint32_t a, float2 x) {
 __device__ __forceinline__ void peer_store(uint32_t a, float4 x) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
                : "memory");
-}
-
-__device__ __forceinline__ uint32_t word(const uint4& w, int i) {
-  return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-}
-
-// The request with the r-th most positions (at most kThreadsS requests); `key` is room
-// for kThreadsS + 1 (a static array would cost the fourth CTA of an SM).
-__device__ __forceinline__ int by_length(const ChunkParams& p, int* key, int r) {
-  const int t = threadIdx.x;
-  int mine = -1;
-  if (t < p.B) {
-    const ChunkRequest q = chunk_request(p, t);
-    if (q.n > 0) mine = p.window > 0 ? min(q.kv, (int)min((int64_t)p.window + p.sinks, (int64_t)INT_MAX)) : q.kv;
-    key[t] = mine;
-  }
-  __syncthreads();
-  if (t < p.B) {
-    int rank = 0;
-    for (int i = 0; i < p.B; ++i) {
-      const int k = key[i];
-      rank += k > mine || (k == mine && i < t);
-    }
-    if (rank == r) key[kThreadsS] = t;
-  }
-  __syncthreads();
-  const int b = key[kThreadsS];
-  __syncthreads();
-  return b;
 }
 
 // TWIN (at most 4 vectors): columns 4 to 7 hold the vectors of columns 0 to 3 again.
@@ -176,7 +135,7 @@ __global__ void __launch_bounds__(kThreadsS, StreamCfg<D, NQ>::kCtas)
   // 64 requests of 512 to 65536 positions in a window of 4096: 80 us so, 90 by index
   // (P in one half then).  Up to as many requests as the CTA has threads; beyond, by index.
   const int nth = div_hkv(p, blockIdx.x), g = blockIdx.x - nth * p.Hkv, s = blockIdx.y;
-  const int b = sorted ? by_length(p, reinterpret_cast<int*>(sML), nth) : nth;
+  const int b = sorted ? by_length<kThreadsS>(p, reinterpret_cast<int*>(sML), nth) : nth;
   const int row_first = blockIdx.z * kR;  // packed rows: token * G + head of the group
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);

@@ -50,21 +50,19 @@
 #include "chunk_schedule.h"
 #include "internal.h"
 #include "tc_ptx.cuh"
+#include "tile_rows.cuh"
 
 namespace fp8kv {
 namespace {
 
 using namespace tc;
 
-constexpr int kT = kChunkTileTokens;
-constexpr int kM = 128;                  // rows per tile
 constexpr int kTileThreads = 12 * 32;
 constexpr int kStagesMax = 4;
-constexpr uint32_t kPolls = 1u << 20;    // polls per wait
 constexpr int kMetaBytes = 4096;
 
 template <int D>
-struct TileCfg {
+struct TileCfg : RowCfg<D> {
   static constexpr int kNQ = D == 256 ? 1 : 2;
   static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 4;  // K stages, and V stages
   // V's barriers: one per stage; D = 256: one per half (64 positions) of the only stage,
@@ -74,9 +72,6 @@ struct TileCfg {
   // large logits and NaN since.)
   static constexpr int kVStages = D == 256 ? 2 : kStages;
   static constexpr int kOpBytes = kT * D * 2;
-  static constexpr int kCh = D / 16;          // 16-byte pieces of an FP8 row
-  static constexpr int kRowsIt = 32 / kCh;    // rows a warp moves at a time
-  static constexpr int kIts = 32 / kRowsIt;   // times, for its 32 rows
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kNQ * kM * D * 2;
   static constexpr int kOffV = kOffK + kStages * kOpBytes;
@@ -98,115 +93,6 @@ struct TileMeta {
   uint32_t tmem, abort, vbad;
 };
 static_assert(sizeof(TileMeta) <= kMetaBytes, "meta block");
-
-// A bounded wait of a whole warp: all lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPolls, abort_flag));
-}
-
-// One lane of a converged warp (always the same).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
-// Request and first packed row of a CTA.  The GPU starts CTAs in the order of their
-// index, so the longest go first: requests by the positions that their rows see
-// (above 32 requests, more than a warp's lanes: by their index, from the last; not
-// measured against an order by length), a request's row tiles from the last, which sees
-// the most, and the KV heads of a row tile side by side.  16 requests on 200 to 8000
-// positions: 133 us; with requests by index and row tiles before heads, whose longest
-// CTAs started last, 189.
-struct TileWork {
-  int b, row0;
-};
-__device__ __forceinline__ int tiles_of(const ChunkParams& p, int b, int rows, bool& bad) {
-  if (b >= p.B) return 0;
-  const ChunkRequest r = chunk_request(p, b);
-  bad |= r.bad;
-  return (r.n * p.G + rows - 1) / rows;
-}
-__device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int idx, int lane, TileWork& w) {
-  int total = 0;
-  bool bad = false;
-  if (p.B <= 32) {
-    const int mine = tiles_of(p, lane, rows, bad);
-    if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-    int key = 0, before = 0;  // tiles of the requests that go first
-    if (lane < p.B) key = min(max(p.kv_len[lane], 0), p.window > 0 ? p.window : INT_MAX);
-    for (int i = 0; i < p.B; ++i) {
-      const int k = __shfl_sync(0xffffffffu, key, i), n = __shfl_sync(0xffffffffu, mine, i);
-      if (k > key || (k == key && i > lane)) before += n;
-    }
-    const uint32_t here = __ballot_sync(0xffffffffu, before <= idx && idx - before < mine);
-    if (here == 0u) return false;
-    const int l = __ffs(here) - 1;
-    w.b = l;
-    w.row0 = (__shfl_sync(0xffffffffu, before + mine, l) - 1 - idx) * rows;
-    return true;
-  }
-  for (int b0 = 0; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, tiles_of(p, b0 + lane, rows, bad));
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-  idx = total - 1 - idx;
-  if (idx < 0) return false;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int mine = tiles_of(p, b0 + lane, rows, bad);
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, upto > idx);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      w.b = b0 + l;
-      w.row0 = (idx - __shfl_sync(0xffffffffu, upto - mine, l)) * rows;
-      return true;
-    }
-    idx -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return false;
-}
-
-// A decoder lane's 16-byte pieces of one tile (piece lane % kCh of rows it *
-// kRowsIt + lane / kCh of the warp's 32).  The loads are unconditional (rows
-// without a place read the pool's first one): a load under a condition is
-// waited for on the spot, one after the other.  The rows' offsets come
-// through shared memory: one access each, where a shuffle would take two.
-template <int D>
-__device__ __forceinline__ void fetch_rows(const uint8_t* base, const int64_t* place, int lane,
-                                           uint4 (&w)[TileCfg<D>::kIts]) {
-  using C = TileCfg<D>;
-  base += (lane % C::kCh) * 16;
-  place += lane / C::kCh;
-#pragma unroll
-  for (int it = 0; it < C::kIts; ++it) w[it] = __ldg(reinterpret_cast<const uint4*>(base + place[it * C::kRowsIt]));
-}
-
-// ... and as fp16 in the operand tile: 64-column blocks of kT rows of 128
-// bytes, 16-byte chunk c of row r at c ^ (r % 8).  Odd column blocks store
-// their two chunks in the other order, so that eight lanes hit eight banks.
-template <int D, int FMT>
-__device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[TileCfg<D>::kIts], int row_base, int lane) {
-  using C = TileCfg<D>;
-  const int c = lane % C::kCh, db = c / 4, h0 = (c % 4) * 2;
-  const bool swap = db & 1;
-  const int first = swap ? h0 + 1 : h0, second = swap ? h0 : h0 + 1;
-#pragma unroll
-  for (int it = 0; it < C::kIts; ++it) {
-    const int r = row_base + it * C::kRowsIt + lane / C::kCh;
-    uint8_t* row = op + db * (kT * 128) + r * 128;
-    uint4 a, b;
-    fp8x4_to_f16<FMT>(w[it].x, a.x, a.y);
-    fp8x4_to_f16<FMT>(w[it].y, a.z, a.w);
-    fp8x4_to_f16<FMT>(w[it].z, b.x, b.y);
-    fp8x4_to_f16<FMT>(w[it].w, b.z, b.w);
-    *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) * 16)) = swap ? b : a;
-    *reinterpret_cast<uint4*>(row + ((second ^ (r & 7)) * 16)) = swap ? a : b;
-  }
-}
 
 // V pieces before they are stored: zero for rows whose block is out of range or that
 // lie past the partition (their weight is 0, and 0 * NaN would not be; K rows
@@ -339,51 +225,6 @@ __device__ __forceinline__ bool decode_tiles(const ChunkParams& p, TileMeta& mt,
   }
   if (bad) mt.vbad = 1u;
   return ok;
-}
-
-// Visibility of 32 virtual tokens v0 .. v0+31 for one row, as bits.
-__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
-__device__ __forceinline__ uint32_t sees32(const ChunkRow& r, int sk, int v0) {
-  return below(r.hi - v0) & (~below(r.lo - v0) | below(sk - v0));
-}
-// (words of the mask: nodes past the last one are bits of words that are there, or 0)
-__device__ __forceinline__ uint32_t sees32(const TreeRow& r, int sk, int v0, int words) {
-  const uint32_t context = below(r.hi - v0);
-  uint32_t vis = context & (~below(r.lo - v0) | below(sk - v0));
-  if (context != 0xFFFFFFFFu) {
-    const int j0 = v0 - r.hi, w = j0 >> 5;  // node of the first token; negative: context in front
-    const uint32_t lo = w >= 0 && w < words ? __ldg(r.mask + w) : 0u;
-    const uint32_t hi = w + 1 >= 0 && w + 1 < words ? __ldg(r.mask + w + 1) : 0u;
-    vis |= __funnelshift_r(lo, hi, j0 & 31) & ~context;
-  }
-  return vis;
-}
-
-// Two FP32 values in a register pair (packed arithmetic of sm_100).
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // P = 2^(c S + sh) as fp16 for 64 of a row's logits; adds to the row's sums.

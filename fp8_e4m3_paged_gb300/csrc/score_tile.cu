@@ -1,0 +1,601 @@
+// Gathered weights for many query vectors: two passes of tcgen05 products over K.
+//
+//   rows     S = Q . K^T (M = 128 query vectors, N = 128 positions): a thread has a row, and leaves
+//            its maximum and sum, M_r and L_r, per partition of the positions;
+//   columns  S = K . Q^T (M = 128 positions, N = 128 query vectors): a thread has a position,
+//            and adds up 2^(S_tr c_r - M_r) / L_r over the rows that see it.
+//
+// Every product is computed twice (the column sums need all of M and L first); kept
+// logits, as the streaming kernel has them, would be 4 bytes per product: more than K from the second
+// row of a group on.  Both orientations take the same swizzled operand tiles, with the roles
+// exchanged, so the two passes are one kernel; a position's sum stays within a thread, in
+// a fixed order, without atomics.
+//
+// Thirteen warps: 0-3 and 4-7, two groups that take turns at the S buffers (four of 128 columns,
+// all of TMEM: the tensor core runs two products ahead of each group); 8-11 decode K,
+// FP8 rows requested one tile ahead, to fp16; 12 issues the UMMAs.  With two row tiles each group has
+// one, and both share a decoded K tile; with one, the groups take every other K tile.
+// The column pass walks several row blocks with the same positions (their sums in shared
+// memory), so that a prompt of n tokens leaves n / col_part x groups partial sums and not n^2 / 128.
+//
+// Every wait is bounded, as in the attention's tile kernel.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "score_common.cuh"
+#include "tile_rows.cuh"
+
+namespace fp8kv {
+namespace {
+
+constexpr int kThreadsT = 13 * 32;
+constexpr int kIssuer = 12;
+constexpr int kBufs = 4;
+
+template <int D>
+struct Cfg : RowCfg<D> {
+  static constexpr int kNQ = D == 256 ? 1 : 2;                      // row tiles
+  static constexpr int kRows = kNQ * kM;
+  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;   // K tiles
+  static constexpr int kOpBytes = kT * D * 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kNQ * kOpBytes;
+  static constexpr int kOffMeta = kOffK + kStages * kOpBytes;
+  static constexpr int kMetaBytes = 8192 + 2 * kScoreAccTokens * 4;
+  // (at least half an SM's shared memory: one CTA per SM, which takes all of its TMEM)
+  static constexpr int kSmem = (kOffMeta + kMetaBytes > 118000 ? kOffMeta + kMetaBytes : 118000) + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Meta {
+  uint64_t q_full, drain;
+  uint64_t k_full[4], k_empty[4];
+  uint64_t s_full[kBufs], s_empty[kBufs];
+  alignas(16) uint32_t valid[8][4];   // per tile (% 8): positions whose block is in range
+  int64_t place[4][32];               // per decoder warp: byte offsets of its rows
+  alignas(16) float c[256], m[256], inv[256];  // rows: logit factor; -maximum; 1 / sum
+  alignas(16) int hi[256];            // rows: positions below are seen (0: a row that is not there)
+  float back[256];
+  float2 other[128];
+  uint32_t tmem, abort;
+};
+static_assert(sizeof(Meta) <= 8192, "meta block");
+
+// The K tiles of a CTA: row blocks [r0, r1), of each the positions from u0 on that its rows see, up to u1.
+struct Walk {
+  int u0, u1, r0, r1;
+  int base, G, rows, n;  // first new token's position, group, rows of a block, new tokens
+  __device__ __forceinline__ int last_of(int rb) const {  // positions that the block's last row sees
+    return base + (min((rb + 1) * rows, n * G) - 1) / G + 1;
+  }
+  __device__ __forceinline__ int tiles_of(int rb) const { return (min(u1, last_of(rb)) - u0 + kT - 1) / kT; }
+};
+
+// Decoders: the K tiles of the walk, in order.
+template <int D, int FMT>
+__device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t* smem, int b, int g, const Walk& walk,
+                                         int w, int lane) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages;
+  volatile uint32_t* const abort_flag = &mt.abort;
+  const uint8_t* kbase = p.k_cache + g * p.ksh;
+  const int32_t* table = p.block_table + (int64_t)b * p.bt_stride;
+  int64_t* place = mt.place[w];
+  // the tile after the one whose rows are requested: row block, tile of it
+  int rb = walk.r0, j = 0, n_tiles = walk.tiles_of(rb);
+  int blk = -1, slot = 0;
+  bool in = false;
+  auto ask = [&]() {
+    if (rb >= walk.r1) {
+      in = false;
+      blk = -1;
+      return;
+    }
+    const int v = walk.u0 + j * kT + 32 * w + lane;
+    const int page = div_page(v, p.page_size, p.page_div);
+    slot = v - page * p.page_size;
+    in = v < walk.u1;
+    blk = -1;
+    if (in) blk = __ldg(table + page);
+    if (++j == n_tiles) {
+      j = 0;
+      if (++rb < walk.r1) n_tiles = walk.tiles_of(rb);
+    }
+  };
+  uint4 kr[C::kIts];
+  uint32_t ok_next = 0u;
+  auto fetch = [&]() {  // the rows asked for
+    const bool ok = blk >= 0 && blk < p.num_kv_blocks;
+    if (in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
+    ok_next = __ballot_sync(0xffffffffu, ok);
+    __syncwarp();
+    place[lane] = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
+    __syncwarp();
+    fetch_rows<D>(kbase, place, lane, kr);
+  };
+  ask();
+  fetch();
+  ask();
+  int kt = 0;
+  for (int r = walk.r0; r < walk.r1; ++r) {
+    const int n = walk.tiles_of(r);
+    for (int i = 0; i < n; ++i, ++kt) {
+      const int st = kt % NS;
+      if (kt >= NS && !warp_wait(&mt.k_empty[st], ((kt / NS) - 1) & 1, abort_flag)) return false;
+      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w, lane);
+      // valid[kt % 8] was read before QK(kt - 4) could be issued, and k_empty says that one of
+      // kt - NS or later is done
+      if (lane == 0) mt.valid[kt & 7][w] = ok_next;
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.k_full[st]);
+      fetch();  // (past the last tile: the pool's first row)
+      ask();
+    }
+  }
+  return true;
+}
+
+// Q tile of a group: 32 rows per warp, fp16 as it is, bf16 scaled by a power of two; the sign of the
+// logit factor goes into Q; rows past RC are zero.
+template <int D, int DT>
+__device__ __forceinline__ void load_q(const ChunkParams& p, Meta& mt, uint8_t* sQ, const ChunkRequest& req, int g,
+                                       int row0, int tile, int RC, uint32_t flip, int warp, int lane) {
+  constexpr int V = D / 32;  // elements per lane
+  constexpr int kAtOnce = 8;
+  const int e = lane * V;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 32; k0 += kAtOnce) {
+    uint32_t w[kAtOnce][V / 2];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int r = min(tile * kM + 32 * warp + k0 + k, RC - 1), rr = row0 + r;
+      const uint16_t* src = p.q + (int64_t)(req.row0 + token_at(p, rr)) * p.q_st +
+                            (int64_t)(g * p.G + row_at(p, rr).head) * p.q_sh + e;
+      if constexpr (V == 2)
+        w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      else if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(w[k]) = __ldg(reinterpret_cast<const uint2*>(src));
+      else
+        *reinterpret_cast<uint4*>(w[k]) = __ldg(reinterpret_cast<const uint4*>(src));
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int r = 32 * warp + k0 + k;
+      const bool live = tile * kM + r < RC;
+      float back = 1.f;
+      if (DT == FP8KV_DTYPE_BF16) {
+        uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) top = max(top, max((w[k][i] << 16) & 0x7FFFFFFFu, w[k][i] & 0x7FFF0000u));
+        const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+          w[k][i] = pack_half2(__uint_as_float(w[k][i] << 16) * rs.to_f16, __uint_as_float(w[k][i] & 0xFFFF0000u) * rs.to_f16);
+        back = rs.back;
+      }
+      if (lane == 0) mt.back[tile * kM + r] = back;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) w[k][i] = live ? w[k][i] ^ flip : 0u;
+      uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
+      if constexpr (V == 2)
+        *reinterpret_cast<uint32_t*>(dst) = w[k][0];
+      else if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[k][0], w[k][1]);
+      else
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    }
+  }
+}
+
+// Sum of 2^(c S - m) / l over 64 columns.  FAR: logits so large that the product is rounded
+// before the maximum is taken off, as it was when the maximum was found.  MASKED: of the columns whose rows
+// see position t alone.
+template <bool MASKED, bool FAR>
+__device__ __forceinline__ float column_sum(const uint32_t (&x)[64], const Meta& mt, int r0, int t) {
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int k = 0; k < 64; k += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(mt.c + r0 + k), m = *reinterpret_cast<const float4*>(mt.m + r0 + k),
+                 inv = *reinterpret_cast<const float4*>(mt.inv + r0 + k);
+    uint64_t e[2];
+    const uint64_t x0 = pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])),
+                   x1 = pair(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+    if (FAR) {
+      // (scalar: a packed product and sum came out as one fma)
+      e[0] = pair(__fadd_rn(__fmul_rn(__uint_as_float(x[k]), c.x), m.x),
+                  __fadd_rn(__fmul_rn(__uint_as_float(x[k + 1]), c.y), m.y));
+      e[1] = pair(__fadd_rn(__fmul_rn(__uint_as_float(x[k + 2]), c.z), m.z),
+                  __fadd_rn(__fmul_rn(__uint_as_float(x[k + 3]), c.w), m.w));
+    } else {
+      e[0] = fma2(x0, pair(c.x, c.y), pair(m.x, m.y));
+      e[1] = fma2(x1, pair(c.z, c.w), pair(m.z, m.w));
+    }
+    float i4[4] = {inv.x, inv.y, inv.z, inv.w};
+    float2 e0 = unpair(e[0]), e1 = unpair(e[1]);
+    if (MASKED) {
+      const int4 hi = *reinterpret_cast<const int4*>(mt.hi + r0 + k);
+      // neither a NaN logit nor a NaN sum of rows that do not see the position
+      if (t >= hi.x) e0.x = -INFINITY, i4[0] = 0.f;
+      if (t >= hi.y) e0.y = -INFINITY, i4[1] = 0.f;
+      if (t >= hi.z) e1.x = -INFINITY, i4[2] = 0.f;
+      if (t >= hi.w) e1.y = -INFINITY, i4[3] = 0.f;
+    }
+    sum[0] = fma2(pair(fast_exp2(e0.x), fast_exp2(e0.y)), pair(i4[0], i4[1]), sum[0]);
+    sum[1] = fma2(pair(fast_exp2(e1.x), fast_exp2(e1.y)), pair(i4[2], i4[3]), sum[1]);
+  }
+  const float2 s = unpair(add2(sum[0], sum[1]));
+  return s.x + s.y;
+}
+
+template <int D, int FMT, int DT, bool COLS>
+__global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant__ ScoreParams sp) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages, ROWS = C::kRows;
+  const ChunkParams& p = sp.c;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Meta& mt = *reinterpret_cast<Meta*>(smem + C::kOffMeta);
+  float* acc = reinterpret_cast<float*>(smem + C::kOffMeta + 8192);  // [group][position of the CTA]
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int64_t plane = (int64_t)p.total_q * p.Hq;
+
+  // ------------------------------------------------------ what this CTA has
+  int b, g, s = 0;
+  Walk walk;
+  ChunkRequest req;
+  if (COLS) {
+    b = div_hkv(p, blockIdx.x);
+    g = blockIdx.x - b * p.Hkv;
+    req = chunk_request(p, b);
+    walk.u0 = (int)min((int64_t)blockIdx.y * sp.col_part, (int64_t)INT_MAX);
+    walk.u1 = (int)min((int64_t)walk.u0 + sp.col_part, (int64_t)req.kv);
+    if (req.n <= 0 || walk.u0 >= req.kv) return;
+    // the row blocks that see anything here, and this group's share of them
+    const int base = req.kv - req.n, blocks = (req.n * p.G + ROWS - 1) / ROWS;
+    const int first = max(0, walk.u0 - base) * p.G / ROWS, share = (blocks - first + sp.groups - 1) / sp.groups;
+    walk.r0 = min(first + (int)blockIdx.z * share, blocks);
+    walk.r1 = min(walk.r0 + share, blocks);
+    s = blockIdx.z;
+    if (walk.r0 >= walk.r1) {  // (only one of several groups)
+      float* to = sp.partial + (((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len;
+      for (int t = walk.u0 + tid; t < walk.u1; t += kThreadsT) to[t] = 0.f;
+      return;
+    }
+  } else {
+    TileWork work;
+    g = blockIdx.x % p.Hkv;
+    s = blockIdx.y;
+    if (!locate(p, ROWS, blockIdx.x / p.Hkv, lane, work)) return;
+    b = work.b;
+    req = chunk_request(p, b);
+    if (req.n * p.G <= work.row0 || work.row0 < 0) return;
+    walk.r0 = work.row0 / ROWS;
+    walk.r1 = walk.r0 + 1;
+    walk.u0 = (int)min((int64_t)s * sp.stat_part, (int64_t)INT_MAX);
+  }
+  walk.base = req.kv - req.n;
+  walk.G = p.G;
+  walk.rows = ROWS;
+  walk.n = req.n;
+  const int RC0 = min(ROWS, req.n * p.G - walk.r0 * ROWS);  // rows of the first block
+  auto vec_of = [&](int rr) { return (int64_t)(req.row0 + token_at(p, rr)) * p.Hq + g * p.G + row_at(p, rr).head; };
+  if (!COLS) {
+    const int U = max(walk.last_of(walk.r0), 0);
+    walk.u1 = (int)min((int64_t)walk.u0 + sp.stat_part, (int64_t)U);
+    if (walk.u0 >= walk.u1) {
+      for (int r = tid; r < RC0; r += kThreadsT)
+        p.ml[s * plane + vec_of(walk.r0 * ROWS + r)] = make_float2(kNoMax, 0.f);
+      return;
+    }
+  }
+  // row tiles in use; one alone only where there is no second row block (D = 256: always one)
+  const int nq = __shfl_sync(0xffffffffu, C::kNQ == 2 && (walk.r1 - walk.r0 > 1 || RC0 > kM) ? 2 : 1, 0);
+  const bool gather = COLS && (nq == 2 || walk.r1 - walk.r0 > 1);  // sums of several row tiles meet in `acc`
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&mt.k_full[i], 128);
+      mbar_init(&mt.k_empty[i], 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&mt.s_full[i], 1);
+      mbar_init(&mt.s_empty[i], 4);  // one lane of each of the group's warps
+    }
+    mbar_init(&mt.q_full, 256);
+    mbar_init(&mt.drain, 1);
+    mt.abort = 0u;
+    mbar_init_fence();
+  }
+  if (warp == kIssuer) {
+    tmem_alloc(&mt.tmem, 512);
+    tmem_relinquish();
+  }
+  if (gather)
+    for (int i = tid; i < 2 * kScoreAccTokens; i += kThreadsT) acc[i] = 0.f;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, mt.tmem, 0);
+  volatile uint32_t* const abort_flag = &mt.abort;
+  const float ks = p.k_scale_dev ? *p.k_scale_dev : p.k_scale;
+  const float cf = p.softmax_scale * ks * kLog2e;  // base-2 logit factor
+  bool ok = true;
+
+  if (warp < 8) {
+    const int w = warp >> 2, wl = warp & 3;             // group, warp of it
+    const int tile = nq == 2 ? w : 0;                   // the group's row tile
+    const int mine = tile * kM + 32 * wl + lane;        // rows: this thread's row; columns: the row it prepares
+    const uint32_t lane_off = (uint32_t)(32 * wl) << 16;
+    int kt = 0, uses = 0;                               // K tiles and products of this group so far
+    for (int rb = walk.r0; rb < walk.r1; ++rb) {
+      // ---------------------------------------------------- Q, and what is known of its rows
+      // (the group has waited for every product of the last block's tile: with two tiles its own, with
+      // one both groups')
+      const int row0 = rb * ROWS, RC = min(ROWS, req.n * p.G - row0);
+      named_bar_sync(1, 256);
+      if (w < nq) {
+        load_q<D, DT>(p, mt, smem + C::kOffQ + w * C::kOpBytes, req, g, row0, w, RC, cf < 0.f ? 0x80008000u : 0u, wl, lane);
+        __syncwarp();
+        // (not 0, so that c * -inf stays -inf; nor NaN: a NaN scale goes into the rows' sums)
+        const float c = fmaxf(fabsf(cf) * mt.back[mine], 1e-30f);
+        const bool live = mine < RC;
+        mt.c[mine] = c;
+        mt.hi[mine] = live ? max(walk.base + token_at(p, row0 + mine) + 1, 0) : 0;
+        if (COLS) {
+          const Norm n = live ? join_norm(p.ml, plane, vec_of(row0 + mine), p.S) : Norm{0.f, 0.f};
+          mt.m[mine] = -n.m;
+          mt.inv[mine] = n.inv;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&mt.q_full);
+      named_bar_sync(1, 256);
+      const int n_tiles = walk.tiles_of(rb);
+      if (COLS) {
+        // the tile's rows: the least that one sees, and whether logits are past 2^22
+        int hi_min = INT_MAX;
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hi_min = min(hi_min, mt.hi[tile * kM + 32 * i + lane]);
+          top = fmaxf(top, fabsf(mt.m[tile * kM + 32 * i + lane]));
+        }
+        hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+        const bool far = __any_sync(0xffffffffu, top >= 0x1p22f);
+        for (int j = 0; j < n_tiles; ++j, ++kt) {
+          if (nq == 1 && (kt & 1) != w) continue;
+          const int buf = w + 2 * (uses & 1);
+          ok = ok && warp_wait(&mt.s_full[buf], (uses >> 1) & 1, abort_flag);
+          ++uses;
+          if (!ok) continue;
+          tc_fence_after();
+          const int v0 = walk.u0 + j * kT, t = v0 + 32 * wl + lane;
+          const bool there = (mt.valid[kt & 7][wl] >> lane) & 1u;
+          const bool masked = v0 + kT > hi_min;
+          float sum = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[64];
+            tmem_ld64(tmem + buf * 128 + lane_off + 64 * h, x);
+            if (h == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&mt.s_empty[buf]);
+            }
+            const int r0 = tile * kM + 64 * h;
+            if (far)
+              sum += masked ? column_sum<true, true>(x, mt, r0, t) : column_sum<false, true>(x, mt, r0, t);
+            else
+              sum += masked ? column_sum<true, false>(x, mt, r0, t) : column_sum<false, false>(x, mt, r0, t);
+          }
+          if (!there) sum = 0.f;
+          if (t < walk.u1) {
+            if (gather)
+              acc[w * kScoreAccTokens + t - walk.u0] += sum;
+            else if (sp.groups == 1)
+              write_score(sp, b, g, t, walk.base, sum);
+            else
+              sp.partial[(((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len + t] = sum;
+          }
+        }
+      } else {
+        const float c = mt.c[mine];
+        const int hi = mine < RC ? mt.hi[mine] : INT_MAX;  // rows past RC: everything, dropped at the end
+        const int hi_min = __reduce_min_sync(0xffffffffu, hi);
+        float m = kNoMax, l = 0.f;
+        for (int j = 0; j < n_tiles; ++j, ++kt) {
+          if (nq == 1 && (kt & 1) != w) continue;
+          const int buf = w + 2 * (uses & 1);
+          ok = ok && warp_wait(&mt.s_full[buf], (uses >> 1) & 1, abort_flag);
+          ++uses;
+          if (!ok) continue;
+          tc_fence_after();
+          const int v0 = walk.u0 + j * kT;
+          const uint4 there = *reinterpret_cast<const uint4*>(mt.valid[kt & 7]);
+          const bool masked = (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu || v0 + kT > hi_min;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[64];
+            tmem_ld64(tmem + buf * 128 + lane_off + 64 * h, x);
+            if (h == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&mt.s_empty[buf]);
+            }
+            if (masked) {
+              // logits that the row does not see become -inf (a NaN among them too)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t vis = (h == 0 ? (i == 0 ? there.x : there.y) : (i == 0 ? there.z : there.w)) &
+                                     below(hi - v0 - 64 * h - 32 * i);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[32 * i + k] = ((vis >> k) & 1u) ? x[32 * i + k] : 0xFF800000u;
+              }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is passed over: it makes the sum NaN)
+#pragma unroll
+            for (int k = 0; k < 64; k += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[k + 2 * i])), __uint_as_float(x[k + 2 * i + 1]));
+            const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c);
+            if (top - m > kChunkTau) {  // (false where both are -inf)
+              const float n = fmaxf(m, ceilf(top));
+              if (m != kNoMax) l *= exp2_whole(m - n);
+              m = n;
+            }
+            const float sh = m == kNoMax ? 0.f : -m;
+            const bool far = __any_sync(0xffffffffu, fabsf(sh) >= 0x1p22f);
+            uint64_t sum[2] = {0ull, 0ull};
+            if (far) {
+              // the maximum is that of the rounded products, which the fma below would not round
+#pragma unroll
+              for (int k = 0; k < 64; ++k) x[k] = __float_as_uint(__fmul_rn(__uint_as_float(x[k]), c));
+            }
+            const uint64_t c2 = far ? pair(1.f, 1.f) : pair(c, c), sh2 = pair(sh, sh);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+              const float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
+              sum[(k / 2) & 1] = add2(sum[(k / 2) & 1], pair(fast_exp2(e.x), fast_exp2(e.y)));
+            }
+            const float2 y = unpair(add2(sum[0], sum[1]));
+            l += y.x + y.y;
+          }
+        }
+        if (cf != cf && l != 0.f) l = cf;
+        if (nq == 1) {  // the groups' halves of the positions
+          if (w == 1) mt.other[32 * wl + lane] = make_float2(m, l);
+          named_bar_sync(1, 256);
+          if (w == 0) {
+            const float2 y = mt.other[32 * wl + lane];
+            const float M = fmaxf(m, y.x);
+            l = (l != 0.f ? l * part_weight(m, M) : 0.f) + (y.y != 0.f ? y.y * part_weight(y.x, M) : 0.f);
+            m = M;
+          }
+        }
+        if (ok && w < nq && mine < RC) p.ml[s * plane + vec_of(row0 + mine)] = make_float2(m, l);
+      }
+    }
+    if (COLS && !gather && sp.groups > 1) {  // positions that none of the block's rows sees
+      float* to = sp.partial + (((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len;
+      for (int t = walk.u0 + walk.tiles_of(walk.r0) * kT + tid; t < walk.u1; t += 256) to[t] = 0.f;
+    }
+    if (gather) {
+      named_bar_sync(1, 256);
+      if (ok)
+        for (int t = walk.u0 + tid; t < walk.u1; t += 256) {
+          const float sum = acc[t - walk.u0] + acc[kScoreAccTokens + t - walk.u0];
+          if (sp.groups == 1)
+            write_score(sp, b, g, t, walk.base, sum);
+          else
+            sp.partial[(((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len + t] = sum;
+        }
+    }
+  } else if (warp < kIssuer) {
+    ok = decode_k<D, FMT>(p, mt, smem, b, g, walk, warp - 8, lane);
+  } else {
+    // ======================================================== UMMA issue
+    const uint32_t idesc = idesc_f16_f32(kM, kT, false, false);
+    const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kSw128);
+    const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
+    int kt = 0, it = 0;
+    for (int rb = walk.r0; rb < walk.r1 && ok; ++rb) {
+      ok = warp_wait(&mt.q_full, (rb - walk.r0) & 1, abort_flag);
+      const int n_tiles = walk.tiles_of(rb);
+      for (int j = 0; j < n_tiles && ok; ++j, ++kt) {
+        ok = warp_wait(&mt.k_full[kt % NS], (kt / NS) & 1, abort_flag);
+        for (int q = 0; q < nq && ok; ++q, ++it) {
+          const int buf = it & 3;
+          if (it >= kBufs) ok = warp_wait(&mt.s_empty[buf], ((it >> 2) - 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = qdesc + (uint64_t)((q * C::kOpBytes) >> 4);
+          const uint64_t kd = kdesc + (uint64_t)(((kt % NS) * C::kOpBytes) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);
+              mma_ss(tmem + buf * 128, (COLS ? kd : qd) + step, (COLS ? qd : kd) + step, idesc, kk > 0);
+            }
+            mma_commit(&mt.s_full[buf]);
+            if (q == nq - 1) mma_commit(&mt.k_empty[kt % NS]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    // every UMMA issued must be done before TMEM is freed
+    if (elect_one()) mma_commit(&mt.drain);
+    __syncwarp();
+    mbar_wait_plain(&mt.drain, 0, kPolls);
+    __syncwarp();
+  }
+  if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Sums of the row groups: a thread per position.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) score_sum(const __grid_constant__ ScoreParams sp) {
+  const ChunkParams& p = sp.c;
+  const int b = div_hkv(p, blockIdx.y), g = blockIdx.y - b * p.Hkv;
+  const ChunkRequest req = chunk_request(p, b);
+  const int t = (int)min((int64_t)blockIdx.x * kSumThreads + threadIdx.x, (int64_t)INT_MAX);
+  if (req.n <= 0 || t >= req.kv) return;
+  const int64_t step = (int64_t)p.B * p.Hkv * p.max_kv_len;
+  const float* from = sp.partial + ((int64_t)b * p.Hkv + g) * p.max_kv_len + t;
+  float sum = 0.f;
+  for (int i = 0; i < sp.groups; ++i) sum += from[i * step];
+  write_score(sp, b, g, t, req.kv - req.n, sum);
+}
+
+template <int D, int FMT, int DT>
+cudaError_t run(const fp8kv_cache_score_plan_t*, const ScoreParams& p, cudaStream_t st) {
+  auto rows = score_tile<D, FMT, DT, false>;
+  auto cols = score_tile<D, FMT, DT, true>;
+  constexpr int smem = Cfg<D>::kSmem;
+  static DeviceOnce once;
+  cudaError_t e = once.run([&] {
+    const cudaError_t x = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return x != cudaSuccess ? x : cudaFuncSetAttribute(cols, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  const int pairs = p.c.B * p.c.Hkv;
+  rows<<<dim3(p.c.row_tiles * p.c.Hkv, p.c.S), kThreadsT, smem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int parts = (int)(((int64_t)p.c.max_kv_len + p.col_part - 1) / p.col_part);
+  cols<<<dim3(pairs, parts, p.groups), kThreadsT, smem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.groups == 1) return e;
+  score_sum<<<dim3((unsigned)((p.c.max_kv_len + kSumThreads - 1) / kSumThreads), pairs), kSumThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t pick(const fp8kv_cache_score_plan_t* plan, const ScoreParams& p, cudaStream_t st) {
+  constexpr int E4 = FP8KV_KV_E4M3, E5 = FP8KV_KV_E5M2, F16 = FP8KV_DTYPE_F16, BF16 = FP8KV_DTYPE_BF16;
+  if (plan->kv_format == E5)
+    return plan->dtype == BF16 ? run<D, E5, BF16>(plan, p, st) : run<D, E5, F16>(plan, p, st);
+  return plan->dtype == BF16 ? run<D, E4, BF16>(plan, p, st) : run<D, E4, F16>(plan, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_score_tile(const fp8kv_cache_score_plan_t* plan, const ScoreParams& p, cudaStream_t st) {
+  switch (plan->head_dim) {
+    case 64: return pick<64>(plan, p, st);
+    case 128: return pick<128>(plan, p, st);
+    default: return pick<256>(plan, p, st);
+  }
+}
+
+}  // namespace fp8kv

@@ -609,6 +609,76 @@ typedef struct {
 int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Cache score: the attention weight that each cached position gathers.
+ *
+ * For request b with new tokens (the last n_b of its kv_len[b] positions, as in
+ * fp8kv_attn_chunk), KV head g and position t < kv_len[b]:
+ *
+ *   score[b][g][t] = decay * score_in[b][g][t]   (positions in front of the new tokens; else,
+ *                                                 and with score_in = NULL, 0)
+ *                  + sum over the new tokens i at p_i >= t and the query heads h of g
+ *                    of softmax(z_ih)_t
+ *
+ * with the logits z of fp8kv_attn_chunk without a window.  One call per decode step accumulates
+ * (score_in = score is allowed: the same buffer, element by element); one with the last rows
+ * of a prompt, or all of them, rates the prompt's positions.  A request without new tokens and
+ * positions from kv_len[b] on are left as they are.
+ *
+ * FP32 throughout: logits accumulate as in fp8kv_attn_chunk, weights, their sums and the
+ * score are FP32, added in a fixed order (no atomics: the same inputs give the same bits).
+ * A new token that sees nothing, or only logits of -inf, adds nothing; one with a NaN or
+ * +inf logit makes the positions that it sees NaN, and no others.  A position in an
+ * out-of-range block is seen by none.  Device-side anomalies, plans, workspaces, capture and the
+ * arguments that are named alike: as in fp8kv_attn_chunk.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t revision; /* FP8KV_ATTN_REVISION */
+  int32_t batch, total_q, max_q, num_q_heads, num_kv_heads, head_dim, page_size;
+  int32_t max_kv_len, max_blocks, num_kv_blocks, dtype, kv_format;
+  int32_t group;           /* Hq / Hkv */
+  int32_t kernel;          /* FP8KV_CHUNK_STREAM (logits kept, up to 16 query vectors per KV head) or FP8KV_CHUNK_TILE */
+  int32_t num_splits;      /* partitions of the rows' sums */
+  int32_t vectors;         /* stream: logits kept per position */
+  int32_t row_tiles;       /* tile: bound of the row blocks of all requests */
+  int32_t stat_part;       /* tile: positions of a partition of the rows' sums */
+  int32_t col_part;        /* tile: positions of a CTA of the column pass */
+  int32_t row_groups;      /* tile: shares of the row blocks in the column pass */
+  int32_t num_sms;
+  int64_t partial_offset;  /* workspace: logits [B][Hkv][max_kv_len][vectors], or sums [row_groups][B][Hkv][max_kv_len] */
+  int64_t ml_offset;       /* workspace: FP32 (max, sum) pairs [num_splits][total_q][Hq] */
+  int64_t workspace_bytes; /* minimum workspace size */
+  int32_t reserved[6];
+} fp8kv_cache_score_plan_t;
+
+typedef struct {
+  const void* q;          /* as fp8kv_chunk_args.q */
+  int64_t q_stride_token, q_stride_head;
+  const uint8_t* k_cache; /* as fp8kv_attn_args.k_cache */
+  int64_t k_stride_block, k_stride_token, k_stride_head;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  float softmax_scale;
+  float k_scale;
+  const float* k_scale_dev;
+  const float* score_in;  /* (b, g, t) at b*score_in_stride_req + g*score_in_stride_head + t; NULL = zeros */
+  int64_t score_in_stride_req, score_in_stride_head; /* elements, >= 0 */
+  float* score;           /* likewise; rows of plan->max_kv_len elements must not overlap */
+  int64_t score_stride_req, score_stride_head;
+  float decay;            /* finite */
+  void* workspace;        /* >= plan->workspace_bytes, 256-byte aligned; status word first */
+  size_t workspace_bytes;
+} fp8kv_cache_score_args;
+
+/* Validate `d` (as fp8kv_attn_chunk_plan; kernel and num_splits choose likewise) and fill `plan`.
+ * A window, more than 65535 pairs of request and KV head, max_kv_len above 2^26, and FP8KV_CHUNK_STREAM with more than 16
+ * query vectors per KV head: FP8KV_EUNSUPPORTED. */
+int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cache_score_plan_t* plan);
+int fp8kv_attn_cache_score(const fp8kv_cache_score_plan_t* plan, const fp8kv_cache_score_args* a,
+                           fp8kv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Cache selection: which positions stay, by the weights that they gathered.
  *
  * Of the kv_len[b] positions of request b, n_keep[b] = min(kv_len[b], budget) stay: the
