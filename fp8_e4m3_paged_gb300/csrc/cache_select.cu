@@ -29,6 +29,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kClusterMax = 8;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
+constexpr int kAhead = 8;                      // positions of a thread whose loads are in flight together
 constexpr int kKeys = 49152;                   // keys of a CTA's run that stay in shared memory
 constexpr int kMinRun = 4096;                  // positions per CTA before a list gets a further one
 
@@ -47,7 +48,23 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// The weight of a position: one head's, or the sum over all heads, one after another.
+// The weights of kAhead positions, kThreads apart (past the last one: that again): one head's, or the
+// sums over all heads, one after another.  All loads of a head are in flight together.
+__device__ __forceinline__ void weights_at(const fp8kv_cache_select_args& a, const float* row, int i, int n,
+                                           float (&x)[kAhead]) {
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) x[j] = __ldg(row + min(i + j * kThreads, n - 1));
+  if (a.lists == 1) {
+#pragma unroll 4
+    for (int h = 1; h < a.num_kv_heads; ++h) {
+      float y[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) y[j] = __ldg(row + h * a.score_stride_head + min(i + j * kThreads, n - 1));
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) x[j] = __fadd_rn(x[j], y[j]);
+    }
+  }
+}
 __device__ __forceinline__ float weight_at(const fp8kv_cache_select_args& a, const float* row, int t) {
   float x = __ldg(row + t);
   if (a.lists == 1)
@@ -89,15 +106,24 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
   for (int pass = 0; pass < kPasses; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     uint32_t* hist = sh.hist[pass];
-    for (int i = tid; i < n; i += kThreads) {
-      uint32_t k;
+    for (int i0 = tid; i0 < n; i0 += kAhead * kThreads) {
+      uint32_t k[kAhead];
       if (pass == 0 || !stay) {
-        k = key_of(weight_at(a, row, t0 + i));
-        if (stay) keys[i] = k;
+        float x[kAhead];
+        weights_at(a, row + t0, i0, n, x);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          k[j] = key_of(x[j]);
+          if (stay && i0 + j * kThreads < n) keys[i0 + j * kThreads] = k[j];
+        }
       } else {
-        k = keys[i];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) k[j] = keys[min(i0 + j * kThreads, n - 1)];
       }
-      if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j * kThreads < n && (pass == 0 || (k[j] >> (shift + bits)) == prefix))
+          atomicAdd(&hist[(k[j] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     __syncthreads();
     if (ctas > 1) cluster_sync();
@@ -140,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
   const int w0 = min(warp * part, n), w1 = min(w0 + part, n);
   auto key_at = [&](int i) { return stay ? keys[i] : key_of(weight_at(a, row, t0 + i)); };
   uint32_t above = 0u, tie = 0u;
+#pragma unroll 8
   for (int i = w0 + lane; i < w1; i += 32) {
     const uint32_t k = key_at(i);
     above += k > cut;
@@ -165,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
       tie0 += peer_load(&sh.total[1], q);
     }
   }
+#pragma unroll 4
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < w1 ? key_at(i) : 0u;

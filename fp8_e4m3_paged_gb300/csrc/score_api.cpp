@@ -54,14 +54,14 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
   P.partial_offset = 256;
   int64_t floats;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
-    // partitions: two CTAs per SM while each has 64 positions, more while each has 512
-    const int64_t units = std::max<int64_t>(pairs, 1);
-    int64_t S = std::max(std::min(2 * sms / units, ceil_div(len, 64)), std::min(4 * sms / units, len / 512));
-    if (d->num_splits) S = d->num_splits;
-    P.num_splits = (int32_t)std::min<int64_t>(std::max<int64_t>(S, 1), 65535);
+    // partitions of one length: some four CTAs per SM, of 64 to 1024 positions
+    int64_t part = std::min<int64_t>(1024, std::max<int64_t>(64, ceil_div(pairs * len, 4 * sms)));
+    if (d->num_splits) part = ceil_div(len, d->num_splits);
+    part = align_up(std::max(part, ceil_div(len, 65535)), 64);
+    P.num_splits = (int32_t)ceil_div(len, part);
     P.vectors = score_vectors(rows);
     P.row_groups = 1;
-    P.stat_part = P.col_part = (int32_t)len;
+    P.stat_part = P.col_part = (int32_t)part;
     floats = pairs * len * P.vectors;
   } else {
     const int64_t tile = P.head_dim == 256 ? 128 : 256, tiles = ceil_div(len, kChunkTileTokens);
@@ -70,6 +70,7 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     // rows' sums: some four CTAs per SM of at least 8 tiles, one per row block where those are many
     int64_t part = units >= 2 * sms ? tiles : std::min(tiles, std::max<int64_t>(8, ceil_div(units * tiles, 4 * sms)));
     if (d->num_splits) part = ceil_div(tiles, d->num_splits);
+    part = std::max<int64_t>(part, ceil_div(tiles, 65535));
     P.stat_part = (int32_t)(part * kChunkTileTokens);
     P.num_splits = (int32_t)ceil_div(len, P.stat_part);
     // columns: likewise; several row tiles meet in shared memory, which holds 2048 positions

@@ -14,15 +14,40 @@ struct Norm {
   float m, inv;
 };
 
-// Joins the partitions' (maximum, sum) pairs of a vector (whole maxima: weights are powers of two).
-__device__ __forceinline__ Norm join_norm(const float2* ml, int64_t plane, int64_t vec, int S) {
+// Joins the partitions' (maximum, sum) pairs of a vector (whole maxima: weights are powers of
+// two), lane after lane of `lanes` neighbouring ones, each of which gets the result.
+__device__ __forceinline__ Norm join_norm(const float2* ml, int64_t plane, int64_t vec, int S, int lane = 0,
+                                          int lanes = 1) {
   float M = kNoMax, L = 0.f;
-  for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s * plane + vec].x);
-  for (int s = 0; s < S; ++s) {
+  for (int s = lane; s < S; s += lanes) M = fmaxf(M, ml[s * plane + vec].x);
+  for (int o = lanes / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int s = lane; s < S; s += lanes) {
     const float2 y = ml[s * plane + vec];
     if (y.y != 0.f) L = fmaf(part_weight(y.x, M), y.y, L);
   }
+  for (int o = lanes / 2; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
   return {M == kNoMax ? 0.f : M, L == 0.f ? 0.f : 1.f / L};
+}
+
+// A kernel whose launch attribute lets it start while the one before it in the stream still runs:
+// nothing of that one's may be read above this line.  The other side lets it start.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launch with that attribute.
+template <class P>
+cudaError_t launch_dependent(void (*fn)(const P), dim3 grid, int threads, int smem, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 // The new weight of position t: what it had gathered, unless it is one of the new tokens, and `got`.

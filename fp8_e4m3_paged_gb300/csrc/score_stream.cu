@@ -31,6 +31,7 @@ constexpr int kWarps = kChunkStreamWarps;
 constexpr int kThreadsS = 32 * kWarps;
 constexpr int kBlk = kChunkStreamBlock;
 constexpr int kFoldThreads = 256;
+constexpr int kFoldEach = 4;
 
 template <int D, int NQ>
 struct Cfg {
@@ -50,7 +51,7 @@ struct Cfg {
 
 template <int D, int FMT, int DT, int NQ>
 __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
-    score_logits(const __grid_constant__ ScoreParams sp, const int sorted) {
+    score_logits(const __grid_constant__ ScoreParams sp) {
   using C = Cfg<D, NQ>;
   constexpr int ST = C::kStages, R = 8 * NQ;
   const ChunkParams& p = sp.c;
@@ -61,8 +62,8 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
-  const int nth = div_hkv(p, blockIdx.x), g = blockIdx.x - nth * p.Hkv, s = blockIdx.y;
-  const int b = sorted ? by_length<kThreadsS>(p, reinterpret_cast<int*>(sML), nth) : nth;
+  let_next_kernel_start();
+  const int b = div_hkv(p, blockIdx.x), g = blockIdx.x - b * p.Hkv, s = blockIdx.y;
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
   const int RC = min(R, req.n * p.G);
@@ -71,14 +72,11 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   auto token_of = [&](int r) { return token_at(p, r); };
   auto head_of = [&](int r) { return g * p.G + row_at(p, r).head; };
   auto vec_of = [&](int r) { return (int64_t)(req.row0 + token_of(r)) * p.Hq + head_of(r); };
-  const int U = req.kv;
-  int per = div_s(p, U + p.S - 1);
-  per = (per + kBlk * kWarps - 1) / (kBlk * kWarps) * (kBlk * kWarps);
-  const int u0 = (int)min((int64_t)s * per, (int64_t)U), u1 = min(U, u0 + per);
-  if (u0 >= u1) {
-    if (tid < RC) p.ml[s * plane + vec_of(tid)] = make_float2(kNoMax, 0.f);
-    return;
-  }
+  // (partitions of one length, whatever the request's: a batch of 64 between 512 and 16000 positions,
+  // whose longest CTAs had 16000, took 160 us)
+  const int u0 = (int)min((int64_t)s * sp.stat_part, (int64_t)req.kv);
+  const int u1 = (int)min((int64_t)u0 + sp.stat_part, (int64_t)req.kv);
+  if (u0 >= u1) return;  // (nor does the second kernel read it)
 
   // (as in the attention's streaming kernel: block ids one block ahead, unconditional copies,
   // tokens without a place read the pool's first row and are masked)
@@ -318,74 +316,80 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   }
 }
 
-// Second kernel: a thread per position.
+// Second kernel: kFoldEach positions per thread.
 template <int RV>
 __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant__ ScoreParams sp) {
   const ChunkParams& p = sp.c;
   __shared__ Norm norm[16];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = div_hkv(p, blockIdx.y), g = blockIdx.y - b * p.Hkv;
   const ChunkRequest req = chunk_request(p, b);
   const int RC = min(RV, req.n * p.G), base = req.kv - req.n;
-  if (RC <= 0 || (int64_t)blockIdx.x * kFoldThreads >= req.kv) return;
-  if (tid < RV) {
-    norm[tid] = {0.f, 0.f};
-    if (tid < RC) {
-      const RowAt at = row_at(p, tid);
-      norm[tid] = join_norm(p.ml, (int64_t)p.total_q * p.Hq, (int64_t)(req.row0 + at.token) * p.Hq + g * p.G + at.head, p.S);
+  const int t0 = (int)min((int64_t)blockIdx.x * kFoldThreads * kFoldEach, (int64_t)req.kv);
+  if (RC <= 0 || t0 >= req.kv) return;
+  wait_for_previous_kernel();
+  const int S = (req.kv - 1) / sp.stat_part + 1;
+  for (int r = warp; r < RV; r += kFoldThreads / 32) {
+    Norm n = {0.f, 0.f};
+    if (r < RC) {
+      const RowAt at = row_at(p, r);
+      n = join_norm(p.ml, (int64_t)p.total_q * p.Hq, (int64_t)(req.row0 + at.token) * p.Hq + g * p.G + at.head, S, lane, 32);
     }
+    if (lane == 0) norm[r] = n;
   }
+  const float4* from = reinterpret_cast<const float4*>(sp.logits + ((int64_t)b * p.Hkv + g) * p.max_kv_len * RV);
+  float4 y[kFoldEach][RV / 4];
+#pragma unroll
+  for (int j = 0; j < kFoldEach; ++j)
+#pragma unroll
+    for (int i = 0; i < RV / 4; ++i)  // (past the last position: read again, not used)
+      y[j][i] = __ldcg(from + (int64_t)min(t0 + j * kFoldThreads + tid, req.kv - 1) * (RV / 4) + i);
   __syncthreads();
-  const int t = blockIdx.x * kFoldThreads + tid;
-  if (t >= req.kv) return;
-  const float4* x = reinterpret_cast<const float4*>(sp.logits + (((int64_t)b * p.Hkv + g) * p.max_kv_len + t) * RV);
-  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < RV / 4; ++i) {
-    const float4 y = __ldg(x + i);
-    const float z[4] = {y.x, y.y, y.z, y.w};
+  for (int j = 0; j < kFoldEach; ++j) {
+    const int t = t0 + j * kFoldThreads + tid;
+    if (t >= req.kv) return;
+    float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 4 * i + k;
-      // (a position that the vector does not see, or a column without a vector, adds nothing, NaN sums included)
-      if (r < RC && z[k] != -INFINITY) sum = fmaf(fast_exp2(z[k] - norm[r].m), norm[r].inv, sum);
+    for (int i = 0; i < RV / 4; ++i) {
+      const float z[4] = {y[j][i].x, y[j][i].y, y[j][i].z, y[j][i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 4 * i + k;
+        // (a position that the vector does not see, or a column without a vector, adds nothing, NaN sums included)
+        if (r < RC && z[k] != -INFINITY) sum = fmaf(fast_exp2(z[k] - norm[r].m), norm[r].inv, sum);
+      }
     }
+    write_score(sp, b, g, t, base, sum);
   }
-  write_score(sp, b, g, t, base, sum);
 }
 
 template <int D, int FMT, int DT, int NQ>
-cudaError_t run(const fp8kv_cache_score_plan_t* plan, const ScoreParams& p, cudaStream_t st) {
+cudaError_t run(const ScoreParams& p, cudaStream_t st) {
   auto fn = score_logits<D, FMT, DT, NQ>;
   constexpr int smem = Cfg<D, NQ>::kSmem;
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  const int64_t pairs = (int64_t)p.c.B * p.c.Hkv;
-  const bool sorted = p.c.B <= kThreadsS && pairs * p.c.S >= 2 * (int64_t)plan->num_sms && p.c.max_kv_len >= 1024;
-  fn<<<dim3((unsigned)pairs, p.c.S), kThreadsS, smem, st>>>(p, (int)sorted);
+  const unsigned pairs = (unsigned)(p.c.B * p.c.Hkv);
+  fn<<<dim3(pairs, p.c.S), kThreadsS, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const dim3 grid((unsigned)((p.c.max_kv_len + kFoldThreads - 1) / kFoldThreads), (unsigned)pairs);
-  if (p.vectors == 4)
-    score_fold<4><<<grid, kFoldThreads, 0, st>>>(p);
-  else if (p.vectors == 8)
-    score_fold<8><<<grid, kFoldThreads, 0, st>>>(p);
-  else
-    score_fold<16><<<grid, kFoldThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((p.c.max_kv_len + kFoldThreads * kFoldEach - 1) / (kFoldThreads * kFoldEach)), pairs);
+  return launch_dependent(p.vectors == 4 ? score_fold<4> : p.vectors == 8 ? score_fold<8> : score_fold<16>, grid,
+                          kFoldThreads, 0, st, p);
 }
 
 template <int D, int FMT, int DT>
-cudaError_t pick_width(const fp8kv_cache_score_plan_t* plan, const ScoreParams& p, cudaStream_t st) {
-  return p.vectors > 8 ? run<D, FMT, DT, 2>(plan, p, st) : run<D, FMT, DT, 1>(plan, p, st);
+cudaError_t pick_width(const ScoreParams& p, cudaStream_t st) {
+  return p.vectors > 8 ? run<D, FMT, DT, 2>(p, st) : run<D, FMT, DT, 1>(p, st);
 }
 
 template <int D>
 cudaError_t pick(const fp8kv_cache_score_plan_t* plan, const ScoreParams& p, cudaStream_t st) {
   constexpr int E4 = FP8KV_KV_E4M3, E5 = FP8KV_KV_E5M2, F16 = FP8KV_DTYPE_F16, BF16 = FP8KV_DTYPE_BF16;
   if (plan->kv_format == E5)
-    return plan->dtype == BF16 ? pick_width<D, E5, BF16>(plan, p, st) : pick_width<D, E5, F16>(plan, p, st);
-  return plan->dtype == BF16 ? pick_width<D, E4, BF16>(plan, p, st) : pick_width<D, E4, F16>(plan, p, st);
+    return plan->dtype == BF16 ? pick_width<D, E5, BF16>(p, st) : pick_width<D, E5, F16>(p, st);
+  return plan->dtype == BF16 ? pick_width<D, E4, BF16>(p, st) : pick_width<D, E4, F16>(p, st);
 }
 
 }  // namespace
