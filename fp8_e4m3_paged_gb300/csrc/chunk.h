@@ -72,6 +72,7 @@ cudaError_t launch_chunk_tile(const fp8kv_chunk_plan_t* plan, const ChunkParams&
 cudaError_t launch_tree_stream(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_tree_tile(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_chunk_join(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
+cudaError_t launch_tree_join(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_cache_read(const fp8kv_cache_read_args& a, cudaStream_t s);
 cudaError_t launch_calibrate(const fp8kv_calibrate_args& a, cudaStream_t s);
 

@@ -130,7 +130,8 @@ int make_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan, bool tree) {
     // the gaps themselves: 16 requests, 41 row tiles x 8 heads, S = 1: 133 us, 2: 164, 4: 192.)
     if (P.batch == 1) {
       const int64_t ctas = ceil_div(rows, chunk_tile_rows(P.head_dim)) * P.num_kv_heads;
-      const int64_t most = std::min(std::max<int64_t>(8, S), ceil_div(seen, unit));
+      // (a tree's CTAs are all equally long and few: up to one wave of them)
+      const int64_t most = std::min(std::max<int64_t>(8, tree ? sms / ctas : S), ceil_div(seen, unit));
       int64_t best = INT64_MAX;
       for (int64_t n = 1; n <= most; ++n) {
         const int64_t cost = ceil_div(ctas * n, sms) * (ceil_div(seen, n) + 900);
@@ -147,7 +148,17 @@ int make_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan, bool tree) {
   // No FP32 sum over more than kChunkMaxSum positions, whoever chose the partitions: the
   // kernels use the further ones for contexts that need them.  (64 decodes of 4000 positions,
   // planned for 4000: 93 us; planned for 2^20: 102, and 162 were all 16 partitions used.)
-  S = std::max(S, ceil_div(seen, chunk_max_part(P.kernel)));
+  P.max_part = (int32_t)chunk_max_part(P.kernel);
+  if (tree && P.kernel == FP8KV_CHUNK_TILE && P.batch > 1 && d->num_splits == 0) {
+    // Trees of several requests: partitions of one length, so that a long context beside short
+    // ones becomes as many CTAs as it takes (16 trees on 100 to 8000 positions, one CTA for each row block
+    // and KV head: 143 us, of which the longest CTA 140).
+    const int64_t tiles = ceil_div(seen, unit);
+    const int64_t part = std::min<int64_t>(32, std::max<int64_t>(8, units * tiles / (8 * sms)));
+    P.max_part = (int32_t)std::min<int64_t>(P.max_part, part * unit);
+    P.min_splits = 1;
+  }
+  S = std::max(S, ceil_div(seen, P.max_part));
   // grid.x
   if ((P.kernel == FP8KV_CHUNK_STREAM ? pairs : (int64_t)P.row_tiles * P.num_kv_heads) > 0x7fffffff)
     return FP8KV_EUNSUPPORTED;
@@ -166,7 +177,8 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   if (plan->revision != FP8KV_ATTN_REVISION) return FP8KV_EVERSION;
   std::memset(p, 0, sizeof(*p));
   if (plan->kernel != FP8KV_CHUNK_STREAM && plan->kernel != FP8KV_CHUNK_TILE) return FP8KV_EINVAL;
-  if (plan->num_splits < 1 || plan->min_splits < 1 || plan->min_splits > plan->num_splits || plan->group < 1 || plan->page_size < 1 || !fp8_format(plan->kv_format) ||
+  if (plan->num_splits < 1 || plan->min_splits < 1 || plan->min_splits > plan->num_splits || plan->max_part < 1 ||
+      plan->group < 1 || plan->page_size < 1 || !fp8_format(plan->kv_format) ||
       (plan->dtype != FP8KV_DTYPE_F16 && plan->dtype != FP8KV_DTYPE_BF16))
     return FP8KV_EINVAL;
   if (!a->workspace || !aligned(a->workspace, 256)) return FP8KV_EINVAL;
@@ -194,7 +206,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   p->G = plan->group;
   p->S = plan->num_splits;
   p->parts = plan->min_splits;
-  p->max_part = (int32_t)chunk_max_part(plan->kernel);
+  p->max_part = plan->max_part;
   p->page_size = plan->page_size;
   auto inverse = [](int32_t n) { return n >= 2 ? ~0ull / (uint64_t)n + 1 : 0ull; };
   p->page_div = inverse(plan->page_size);
@@ -273,7 +285,7 @@ extern "C" int fp8kv_attn_tree(const fp8kv_chunk_plan_t* plan, const fp8kv_tree_
   p.depth = a->depth;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = plan->kernel == FP8KV_CHUNK_STREAM ? launch_tree_stream(plan, p, st) : launch_tree_tile(plan, p, st);
-  if (e == cudaSuccess && p.S > 1 && !chunk_clustered(plan)) e = launch_chunk_join(plan, p, st);
+  if (e == cudaSuccess && p.S > 1 && !chunk_clustered(plan)) e = launch_tree_join(plan, p, st);
   return done(e);
 }
 

@@ -21,7 +21,9 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 // A CTA's warps are split over vectors and partitions: `ways` warps per vector
 // (a power of two) take every ways-th partition each and meet in shared
 // memory.  Loads of four partitions are in flight at a time.
-template <int D, int DT>
+// TREE: all rows of a request see the same positions, so its partitions that hold any are
+// known, and the others' places are not read.
+template <int D, int DT, bool TREE>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant__ ChunkParams p, const int ways) {
   constexpr int V = D / 32;  // floats per lane
   constexpr int kAhead = 4;
@@ -32,6 +34,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
   const int64_t vec = (int64_t)blockIdx.x * (kJoinWarps / ways) + warp / ways;
   const int row = (int)(vec / p.Hq), h = (int)(vec - (int64_t)row * p.Hq);
   bool live = row < p.total_q;
+  int S = p.S;
   if (live) {
     // whether some request has the row among its (clamped) new tokens
     live = false;
@@ -40,23 +43,31 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
       if (i0 + lane < p.B) {
         const ChunkRequest r = chunk_request(p, i0 + lane);
         here = row >= r.row0 && row - r.row0 < r.n;
+        if (TREE && here) {
+          // (the kernels round partitions up to whole steps: no fewer than these)
+          const int U = chunk_span<true>(p, r, 0, 0).U;
+          const int per = max(1, min((U + p.parts - 1) / p.parts, p.max_part));
+          S = min(p.S, max(1, (U + per - 1) / per));
+        }
       }
-      live = __any_sync(0xffffffffu, here);
+      const uint32_t who = __ballot_sync(0xffffffffu, here);
+      live = who != 0u;
+      if (TREE && live) S = __shfl_sync(0xffffffffu, S, __ffs(who) - 1);
     }
   }
   float acc[V] = {};
   float M = kNoMax, L = 0.f;
   if (live) {
     const int64_t plane = (int64_t)p.total_q * p.Hq;
-    for (int s = way + ways * lane; s < p.S; s += 32 * ways) M = fmaxf(M, p.ml[s * plane + vec].x);
+    for (int s = way + ways * lane; s < S; s += 32 * ways) M = fmaxf(M, p.ml[s * plane + vec].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int s0 = way; s0 < p.S; s0 += kAhead * ways) {
+    for (int s0 = way; s0 < S; s0 += kAhead * ways) {
       float2 ml[kAhead];
       float x[kAhead][V];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int64_t at = min(s0 + i * ways, p.S - 1) * plane + vec;  // past the last: loaded, not used
+        const int64_t at = min(s0 + i * ways, S - 1) * plane + vec;  // past the last: loaded, not used
         ml[i] = p.ml[at];
         const float* src = p.partial + at * D + lane * V;
         if constexpr (V == 2) {
@@ -69,7 +80,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (s0 + i * ways >= p.S || !part_written(ml[i])) continue;  // (x is stale)
+        if (s0 + i * ways >= S || !part_written(ml[i])) continue;  // (x is stale)
         const float w = part_weight(ml[i].x, M);
         L = fmaf(w, ml[i].y, L);
 #pragma unroll
@@ -114,16 +125,15 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-}  // namespace
-
-cudaError_t launch_chunk_join(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+template <bool TREE>
+cudaError_t launch(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
   constexpr int F16 = FP8KV_DTYPE_F16, BF16 = FP8KV_DTYPE_BF16;
   const bool bf = plan->dtype == BF16;
   void (*fn)(const ChunkParams, int) = nullptr;
   switch (plan->head_dim) {
-    case 64: fn = bf ? chunk_join<64, BF16> : chunk_join<64, F16>; break;
-    case 128: fn = bf ? chunk_join<128, BF16> : chunk_join<128, F16>; break;
-    default: fn = bf ? chunk_join<256, BF16> : chunk_join<256, F16>; break;
+    case 64: fn = bf ? chunk_join<64, BF16, TREE> : chunk_join<64, F16, TREE>; break;
+    case 128: fn = bf ? chunk_join<128, BF16, TREE> : chunk_join<128, F16, TREE>; break;
+    default: fn = bf ? chunk_join<256, BF16, TREE> : chunk_join<256, F16, TREE>; break;
   }
   // one warp per vector, more of them while the GPU has idle SMs and each still has partitions
   const int64_t n = (int64_t)p.total_q * p.Hq;
@@ -132,6 +142,16 @@ cudaError_t launch_chunk_join(const fp8kv_chunk_plan_t* plan, const ChunkParams&
   const int64_t per = kJoinWarps / ways;
   fn<<<(unsigned)((n + per - 1) / per), kJoinThreads, 0, st>>>(p, ways);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_join(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  return launch<false>(plan, p, st);
+}
+
+cudaError_t launch_tree_join(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream_t st) {
+  return launch<true>(plan, p, st);
 }
 
 }  // namespace fp8kv

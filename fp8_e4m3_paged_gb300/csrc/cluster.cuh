@@ -23,4 +23,15 @@ __device__ __forceinline__ uint32_t peer_load(const uint32_t* p, int rank) {
   return x;
 }
 
+__device__ __forceinline__ uint4 peer_load4(const uint32_t* p, int rank) {
+  uint32_t a;
+  uint4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
 }  // namespace fp8kv

@@ -8,6 +8,6 @@
 namespace fp8kv {
 
 cudaError_t launch_cache_select(const fp8kv_cache_select_args& a, int sms, cudaStream_t s);
-cudaError_t launch_cache_move(const fp8kv_cache_move_args& a, cudaStream_t s);
+cudaError_t launch_cache_move(const fp8kv_cache_move_args& a, int sms, cudaStream_t s);
 
 }  // namespace fp8kv

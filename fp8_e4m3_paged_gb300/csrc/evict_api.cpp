@@ -75,5 +75,7 @@ extern "C" int fp8kv_attn_cache_move(const fp8kv_cache_move_args* a, fp8kv_strea
       return FP8KV_EINVAL;
     if (!apart(a->batch, es[4], a->num_kv_heads, es[5], a->max_len)) return FP8KV_EINVAL;
   }
-  return done(launch_cache_move(*a, reinterpret_cast<cudaStream_t>(stream)));
+  const int sms = sm_count();
+  if (sms < 1) return FP8KV_ECUDA;
+  return done(launch_cache_move(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }

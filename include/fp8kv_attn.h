@@ -460,7 +460,8 @@ typedef struct {
   int64_t workspace_bytes; /* minimum workspace size */
   int32_t min_splits;      /* partitions of a context that no FP32 sum limit splits further */
   int32_t tree;            /* 1: made by fp8kv_attn_tree_plan */
-  int32_t reserved[6];
+  int32_t max_part;        /* positions of a partition at most */
+  int32_t reserved[5];
 } fp8kv_chunk_plan_t;
 
 typedef struct {
