@@ -11,10 +11,13 @@
 // exchanged, so the two passes are one kernel; a position's sum stays within a thread, in
 // a fixed order, without atomics.
 //
-// Thirteen warps: 0-3 and 4-7, two groups that take turns at the S buffers (four of 128 columns,
-// all of TMEM: the tensor core runs two products ahead of each group); 8-11 decode K,
-// FP8 rows requested one tile ahead, to fp16; 12 issues the UMMAs.  With two row tiles each group has
-// one, and both share a decoded K tile; with one, the groups take every other K tile.
+// Twenty warps: four groups of four, each with one S buffer (128 columns; the four are all of
+// TMEM), whose first warp issues the group's next product as soon as the last one is read; four decode K,
+// FP8 rows brought by cp.async into a ring of tiles, to fp16.  While one group waits for its product,
+// the others have 32 columns at a time in registers: four warps on each scheduler, where two
+// groups with two buffers each, ahead of the tensor core, took 2500 cycles for 128 x 128, most of it
+// latencies of one warp's instructions.  With two row tiles two groups share each, K tile after
+// K tile; with one, the groups take every fourth K tile.
 // The column pass walks several row blocks with the same positions (their sums in shared
 // memory), so that a prompt of n tokens leaves n / col_part x groups partial sums and not n^2 / 128.
 //
@@ -31,38 +34,43 @@
 namespace fp8kv {
 namespace {
 
-constexpr int kThreadsT = 13 * 32;
-constexpr int kIssuer = 12;
-constexpr int kBufs = 4;
+constexpr int kGroups = 4;
+constexpr int kEpilogue = kGroups * 128;         // threads
+constexpr int kThreadsT = kEpilogue + 128;
+constexpr int kMetaHead = 11264;
+constexpr int kCols = 32;                        // columns in registers
 
 template <int D>
 struct Cfg : RowCfg<D> {
   static constexpr int kNQ = D == 256 ? 1 : 2;                      // row tiles
   static constexpr int kRows = kNQ * kM;
-  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;   // K tiles
+  static constexpr int kStages = D == 256 ? 1 : 2;                   // K tiles, as fp16
+  static constexpr int kRing = D == 256 ? 2 : D == 128 ? 3 : 6;      // ... on their way, as bytes
   static constexpr int kOpBytes = kT * D * 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kNQ * kOpBytes;
-  static constexpr int kOffMeta = kOffK + kStages * kOpBytes;
-  static constexpr int kMetaBytes = 8192 + 2 * kScoreAccTokens * 4;
+  static constexpr int kRawBytes = kT * D;
+  static constexpr int kOffRaw = kOffK + kStages * kOpBytes;
+  static constexpr int kOffMeta = kOffRaw + kRing * kRawBytes;
+  static constexpr int kMetaBytes = kMetaHead + 2 * kScoreAccTokens * 4;
   // (at least half an SM's shared memory: one CTA per SM, which takes all of its TMEM)
   static constexpr int kSmem = (kOffMeta + kMetaBytes > 118000 ? kOffMeta + kMetaBytes : 118000) + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct Meta {
-  uint64_t q_full, drain;
-  uint64_t k_full[4], k_empty[4];
-  uint64_t s_full[kBufs], s_empty[kBufs];
+  uint64_t k_full[4], k_empty[2];     // per tile (% 4), per stage
+  uint64_t s_full[kGroups], s_empty[kGroups], drain[kGroups];
   alignas(16) uint32_t valid[8][4];   // per tile (% 8): positions whose block is in range
   int64_t place[4][32];               // per decoder warp: byte offsets of its rows
-  alignas(16) float c[256], m[256], inv[256];  // rows: logit factor; -maximum; 1 / sum
+  alignas(16) float c[256], ml[256];           // rows: logit factor; -(maximum + log2 of the sum)
+  alignas(16) float m[256], inv[256];          // ... apart: -maximum; 1 / sum
   alignas(16) int hi[256];            // rows: positions below are seen (0: a row that is not there)
   float back[256];
-  float2 other[128];
+  float2 other[kGroups - 1][128];     // rows: (maximum, sum) of the other groups with the same rows
   uint32_t tmem, abort;
 };
-static_assert(sizeof(Meta) <= 8192, "meta block");
+static_assert(sizeof(Meta) <= kMetaHead, "meta block");
 
 // The K tiles of a CTA: row blocks [r0, r1), of each the positions from u0 on that its rows see, up to u1.
 struct Walk {
@@ -84,150 +92,191 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
   const uint8_t* kbase = p.k_cache + g * p.ksh;
   const int32_t* table = p.block_table + (int64_t)b * p.bt_stride;
   int64_t* place = mt.place[w];
-  // the tile after the one whose rows are requested: row block, tile of it
-  int rb = walk.r0, j = 0, n_tiles = walk.tiles_of(rb);
-  int blk = -1, slot = 0;
-  bool in = false;
+  constexpr int R = C::kRing;
+  // a lane copies, and reads back, piece lane % kCh of rows it * kRowsIt + lane / kCh of the warp's 32
+  uint8_t* raw = smem + C::kOffRaw + (32 * w + lane / C::kCh) * D + (lane % C::kCh) * 16;
+  int rb = walk.r0, j = 0, n_tiles = walk.tiles_of(rb);  // the next tile to ask for: row block, tile of it
+  struct Ask {
+    int blk, slot;
+    bool in;
+  };
   auto ask = [&]() {
-    if (rb >= walk.r1) {
-      in = false;
-      blk = -1;
-      return;
-    }
+    Ask a = {-1, 0, false};
+    if (rb >= walk.r1) return a;
     const int v = walk.u0 + j * kT + 32 * w + lane;
     const int page = div_page(v, p.page_size, p.page_div);
-    slot = v - page * p.page_size;
-    in = v < walk.u1;
-    blk = -1;
-    if (in) blk = __ldg(table + page);
+    a.slot = v - page * p.page_size;
+    a.in = v < walk.u1;
+    if (a.in) a.blk = __ldg(table + page);
     if (++j == n_tiles) {
       j = 0;
       if (++rb < walk.r1) n_tiles = walk.tiles_of(rb);
     }
+    return a;
   };
-  uint4 kr[C::kIts];
-  uint32_t ok_next = 0u;
-  auto fetch = [&]() {  // the rows asked for
-    const bool ok = blk >= 0 && blk < p.num_kv_blocks;
-    if (in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    ok_next = __ballot_sync(0xffffffffu, ok);
+  auto request = [&](const Ask& a, int slot) {  // returns the rows that are there
+    const bool ok = a.blk >= 0 && a.blk < p.num_kv_blocks;
+    if (a.in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
     __syncwarp();
-    place[lane] = ok ? blk * p.ksb + (int64_t)slot * p.kst : 0;
+    place[lane] = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
     __syncwarp();
-    fetch_rows<D>(kbase, place, lane, kr);
+    const uint8_t* from = kbase + (lane % C::kCh) * 16;
+#pragma unroll
+    for (int it = 0; it < C::kIts; ++it)
+      cp_async16(raw + slot * C::kRawBytes + it * C::kRowsIt * D, from + place[it * C::kRowsIt + lane / C::kCh]);
+    return __ballot_sync(0xffffffffu, ok);
   };
-  ask();
-  fetch();
-  ask();
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  uint32_t there[R];
+  Ask next;
+  {
+    Ask first[R + 1];
+#pragma unroll
+    for (int i = 0; i <= R; ++i) first[i] = ask();
+#pragma unroll
+    for (int i = 0; i < R; ++i) {  // (past the last tile: the pool's first row)
+      there[i] = request(first[i], i);
+      commit();
+    }
+    next = first[R];
+  }
   int kt = 0;
   for (int r = walk.r0; r < walk.r1; ++r) {
     const int n = walk.tiles_of(r);
     for (int i = 0; i < n; ++i, ++kt) {
-      const int st = kt % NS;
-      if (kt >= NS && !warp_wait(&mt.k_empty[st], ((kt / NS) - 1) & 1, abort_flag)) return false;
+      const int st = kt % NS, slot = kt % R;
+      asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+      uint4 kr[C::kIts];
+#pragma unroll
+      for (int it = 0; it < C::kIts; ++it)
+        kr[it] = *reinterpret_cast<const uint4*>(raw + slot * C::kRawBytes + it * C::kRowsIt * D);
+      if (kt >= NS && !warp_wait(&mt.k_empty[st], ((kt / NS) - 1) & 1, abort_flag)) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        return false;
+      }
       store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w, lane);
-      // valid[kt % 8] was read before QK(kt - 4) could be issued, and k_empty says that one of
-      // kt - NS or later is done
-      if (lane == 0) mt.valid[kt & 7][w] = ok_next;
+      // (valid[kt % 8] of tile kt - 8 has been read: the product of kt - 4 is done, which that tile's
+      // group issued behind it)
+      if (lane == 0) mt.valid[kt & 7][w] = there[0];
       fence_proxy_async_smem();
-      mbar_arrive(&mt.k_full[st]);
-      fetch();  // (past the last tile: the pool's first row)
-      ask();
+      mbar_arrive(&mt.k_full[kt & 3]);
+#pragma unroll
+      for (int q = 0; q + 1 < R; ++q) there[q] = there[q + 1];
+      there[R - 1] = request(next, slot);
+      commit();
+      next = ask();
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   return true;
 }
 
-// Q tile of a group: 32 rows per warp, fp16 as it is, bf16 scaled by a power of two; the sign of the
+// Eight rows of the Q tiles: fp16 as it is, bf16 scaled by a power of two; the sign of the
 // logit factor goes into Q; rows past RC are zero.
 template <int D, int DT>
-__device__ __forceinline__ void load_q(const ChunkParams& p, Meta& mt, uint8_t* sQ, const ChunkRequest& req, int g,
-                                       int row0, int tile, int RC, uint32_t flip, int warp, int lane) {
+__device__ __forceinline__ void load_q(const ChunkParams& p, Meta& mt, uint8_t* smem, const ChunkRequest& req, int g,
+                                       int row0, int first, int RC, uint32_t flip, int lane) {
   constexpr int V = D / 32;  // elements per lane
   constexpr int kAtOnce = 8;
   const int e = lane * V;
-#pragma unroll 1
-  for (int k0 = 0; k0 < 32; k0 += kAtOnce) {
-    uint32_t w[kAtOnce][V / 2];
+  uint8_t* sQ = smem + Cfg<D>::kOffQ + (first / kM) * Cfg<D>::kOpBytes;
+  uint32_t w[kAtOnce][V / 2];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int r = min(tile * kM + 32 * warp + k0 + k, RC - 1), rr = row0 + r;
-      const uint16_t* src = p.q + (int64_t)(req.row0 + token_at(p, rr)) * p.q_st +
-                            (int64_t)(g * p.G + row_at(p, rr).head) * p.q_sh + e;
-      if constexpr (V == 2)
-        w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-      else if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(w[k]) = __ldg(reinterpret_cast<const uint2*>(src));
-      else
-        *reinterpret_cast<uint4*>(w[k]) = __ldg(reinterpret_cast<const uint4*>(src));
+  for (int k = 0; k < kAtOnce; ++k) {
+    const int rr = row0 + min(first + k, RC - 1);
+    const uint16_t* src = p.q + (int64_t)(req.row0 + token_at(p, rr)) * p.q_st +
+                          (int64_t)(g * p.G + row_at(p, rr).head) * p.q_sh + e;
+    if constexpr (V == 2)
+      w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    else if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(w[k]) = __ldg(reinterpret_cast<const uint2*>(src));
+    else
+      *reinterpret_cast<uint4*>(w[k]) = __ldg(reinterpret_cast<const uint4*>(src));
+  }
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) {
+    const int r = (first + k) % kM;
+    const bool live = first + k < RC;
+    float back = 1.f;
+    if (DT == FP8KV_DTYPE_BF16) {
+      uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) top = max(top, max((w[k][i] << 16) & 0x7FFFFFFFu, w[k][i] & 0x7FFF0000u));
+      const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        w[k][i] = pack_half2(__uint_as_float(w[k][i] << 16) * rs.to_f16, __uint_as_float(w[k][i] & 0xFFFF0000u) * rs.to_f16);
+      back = rs.back;
     }
+    if (lane == 0) mt.back[first + k] = back;
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int r = 32 * warp + k0 + k;
-      const bool live = tile * kM + r < RC;
-      float back = 1.f;
-      if (DT == FP8KV_DTYPE_BF16) {
-        uint32_t top = 0u;  // as integers: a NaN is larger than every number, and is not dropped
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) top = max(top, max((w[k][i] << 16) & 0x7FFFFFFFu, w[k][i] & 0x7FFF0000u));
-        const RowScale rs = row_scale_bf16(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-          w[k][i] = pack_half2(__uint_as_float(w[k][i] << 16) * rs.to_f16, __uint_as_float(w[k][i] & 0xFFFF0000u) * rs.to_f16);
-        back = rs.back;
-      }
-      if (lane == 0) mt.back[tile * kM + r] = back;
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) w[k][i] = live ? w[k][i] ^ flip : 0u;
-      uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
-      if constexpr (V == 2)
-        *reinterpret_cast<uint32_t*>(dst) = w[k][0];
-      else if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[k][0], w[k][1]);
-      else
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-    }
+    for (int i = 0; i < V / 2; ++i) w[k][i] = live ? w[k][i] ^ flip : 0u;
+    uint8_t* dst = sQ + (e / 64) * (kM * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) * 16) + (e % 8) * 2;
+    if constexpr (V == 2)
+      *reinterpret_cast<uint32_t*>(dst) = w[k][0];
+    else if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[k][0], w[k][1]);
+    else
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
   }
 }
 
-// Sum of 2^(c S - m) / l over 64 columns.  FAR: logits so large that the product is rounded
-// before the maximum is taken off, as it was when the maximum was found.  MASKED: of the columns whose rows
-// see position t alone.
-template <bool MASKED, bool FAR>
-__device__ __forceinline__ float column_sum(const uint32_t (&x)[64], const Meta& mt, int r0, int t) {
+// Sum of 2^(c S - m) / l over kCols columns.  The quotient goes into the exponent, as m + log2 l: a
+// value that all lanes read costs a cycle of shared memory per warp and word, and three of them
+// for each column (factor, maximum, 1 / sum) took 3100 cycles of a tile of 256 x 128.
+// FAR: logits so large that the product is rounded before the maximum is taken off, as it was when the
+// maximum was found, and that the sum of m and log2 l would lose the latter.  MASKED: of
+// the columns whose rows see position t alone.  ONE: all rows have the factor c1.
+template <bool MASKED, bool FAR, bool ONE>
+__device__ __forceinline__ float column_sum(const uint32_t (&x)[kCols], const Meta& mt, int r0, int t, float c1) {
   uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-  for (int k = 0; k < 64; k += 4) {
-    const float4 c = *reinterpret_cast<const float4*>(mt.c + r0 + k), m = *reinterpret_cast<const float4*>(mt.m + r0 + k),
-                 inv = *reinterpret_cast<const float4*>(mt.inv + r0 + k);
-    uint64_t e[2];
-    const uint64_t x0 = pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])),
-                   x1 = pair(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+  for (int k = 0; k < kCols; k += 4) {
+    const float4 c = ONE ? make_float4(c1, c1, c1, c1) : *reinterpret_cast<const float4*>(mt.c + r0 + k);
+    float2 e0, e1, i0 = make_float2(1.f, 1.f), i1 = make_float2(1.f, 1.f);
+    const float s0 = __uint_as_float(x[k]), s1 = __uint_as_float(x[k + 1]), s2 = __uint_as_float(x[k + 2]),
+                s3 = __uint_as_float(x[k + 3]);
     if (FAR) {
       // (scalar: a packed product and sum came out as one fma)
-      e[0] = pair(__fadd_rn(__fmul_rn(__uint_as_float(x[k]), c.x), m.x),
-                  __fadd_rn(__fmul_rn(__uint_as_float(x[k + 1]), c.y), m.y));
-      e[1] = pair(__fadd_rn(__fmul_rn(__uint_as_float(x[k + 2]), c.z), m.z),
-                  __fadd_rn(__fmul_rn(__uint_as_float(x[k + 3]), c.w), m.w));
+      const float4 m = *reinterpret_cast<const float4*>(mt.m + r0 + k), inv = *reinterpret_cast<const float4*>(mt.inv + r0 + k);
+      e0 = make_float2(__fadd_rn(__fmul_rn(s0, c.x), m.x), __fadd_rn(__fmul_rn(s1, c.y), m.y));
+      e1 = make_float2(__fadd_rn(__fmul_rn(s2, c.z), m.z), __fadd_rn(__fmul_rn(s3, c.w), m.w));
+      i0 = make_float2(inv.x, inv.y);
+      i1 = make_float2(inv.z, inv.w);
     } else {
-      e[0] = fma2(x0, pair(c.x, c.y), pair(m.x, m.y));
-      e[1] = fma2(x1, pair(c.z, c.w), pair(m.z, m.w));
+      const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(mt.ml + r0 + k);
+      e0 = unpair(fma2(pair(s0, s1), pair(c.x, c.y), m.x));
+      e1 = unpair(fma2(pair(s2, s3), pair(c.z, c.w), m.y));
     }
-    float i4[4] = {inv.x, inv.y, inv.z, inv.w};
-    float2 e0 = unpair(e[0]), e1 = unpair(e[1]);
     if (MASKED) {
       const int4 hi = *reinterpret_cast<const int4*>(mt.hi + r0 + k);
       // neither a NaN logit nor a NaN sum of rows that do not see the position
-      if (t >= hi.x) e0.x = -INFINITY, i4[0] = 0.f;
-      if (t >= hi.y) e0.y = -INFINITY, i4[1] = 0.f;
-      if (t >= hi.z) e1.x = -INFINITY, i4[2] = 0.f;
-      if (t >= hi.w) e1.y = -INFINITY, i4[3] = 0.f;
+      if (t >= hi.x) e0.x = -INFINITY, i0.x = 0.f;
+      if (t >= hi.y) e0.y = -INFINITY, i0.y = 0.f;
+      if (t >= hi.z) e1.x = -INFINITY, i1.x = 0.f;
+      if (t >= hi.w) e1.y = -INFINITY, i1.y = 0.f;
     }
-    sum[0] = fma2(pair(fast_exp2(e0.x), fast_exp2(e0.y)), pair(i4[0], i4[1]), sum[0]);
-    sum[1] = fma2(pair(fast_exp2(e1.x), fast_exp2(e1.y)), pair(i4[2], i4[3]), sum[1]);
+    const uint64_t p0 = pair(fast_exp2(e0.x), fast_exp2(e0.y)), p1 = pair(fast_exp2(e1.x), fast_exp2(e1.y));
+    sum[0] = FAR ? fma2(p0, pair(i0.x, i0.y), sum[0]) : add2(p0, sum[0]);
+    sum[1] = FAR ? fma2(p1, pair(i1.x, i1.y), sum[1]) : add2(p1, sum[1]);
   }
   const float2 s = unpair(add2(sum[0], sum[1]));
   return s.x + s.y;
+}
+
+// -(m + log2 l) of a row: the exponent of l joins the whole m exactly, the rest is below 1/2, so that
+// one rounding is left (2^-20 at 2^4: 7e-7 of the row's weights).
+__device__ __forceinline__ float folded(const Norm& n) {
+  if (n.inv == 0.f) return -INFINITY;  // (nothing seen)
+  const uint32_t u = __float_as_uint(n.inv);
+  int e = (int)(u >> 23) - 127;
+  if (n.inv != n.inv || (u >> 23) == 0u || (u >> 23) == 255u) return n.inv != n.inv ? n.inv : log2f(n.inv) - n.m;
+  float f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);  // 1 / l = 2^e f
+  if (f > 1.41421356f) {
+    f *= 0.5f;
+    ++e;
+  }
+  return ((float)e - n.m) + log2f(f);
 }
 
 template <int D, int FMT, int DT, bool COLS>
@@ -238,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta& mt = *reinterpret_cast<Meta*>(smem + C::kOffMeta);
-  float* acc = reinterpret_cast<float*>(smem + C::kOffMeta + 8192);  // [group][position of the CTA]
+  float* acc = reinterpret_cast<float*>(smem + C::kOffMeta + kMetaHead);  // [row tile][position of the CTA]
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int64_t plane = (int64_t)p.total_q * p.Hq;
@@ -298,19 +347,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&mt.k_full[i], 128);
-      mbar_init(&mt.k_empty[i], 1);
+      mbar_init(&mt.k_empty[i], nq);
     }
-    for (int i = 0; i < kBufs; ++i) {
+    for (int i = 0; i < 4; ++i) mbar_init(&mt.k_full[i], 128);
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&mt.s_full[i], 1);
       mbar_init(&mt.s_empty[i], 4);  // one lane of each of the group's warps
+      mbar_init(&mt.drain[i], 1);
     }
-    mbar_init(&mt.q_full, 256);
-    mbar_init(&mt.drain, 1);
     mt.abort = 0u;
     mbar_init_fence();
   }
-  if (warp == kIssuer) {
+  if (warp == 0) {
     tmem_alloc(&mt.tmem, 512);
     tmem_relinquish();
   }
@@ -325,120 +373,119 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   const float cf = p.softmax_scale * ks * kLog2e;  // base-2 logit factor
   bool ok = true;
 
-  if (warp < 8) {
+  if (warp < 4 * kGroups) {
     const int w = warp >> 2, wl = warp & 3;             // group, warp of it
-    const int tile = nq == 2 ? w : 0;                   // the group's row tile
-    const int mine = tile * kM + 32 * wl + lane;        // rows: this thread's row; columns: the row it prepares
-    const uint32_t lane_off = (uint32_t)(32 * wl) << 16;
-    int kt = 0, uses = 0;                               // K tiles and products of this group so far
+    const int tile = nq == 2 ? w & 1 : 0;               // the group's row tile
+    const int j0 = nq == 2 ? w >> 1 : w, j_step = nq == 2 ? 2 : 4;  // ... and K tiles of a row block
+    const uint32_t tS = tmem + w * 128 + ((uint32_t)(32 * wl) << 16);
+    const uint32_t idesc = idesc_f16_f32(kM, kT, false, false);
+    const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ + tile * C::kOpBytes), 16, 1024, kSw128);
+    const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
+    // The product with K tile kt, by the group's first warp.  A group may be several stages behind the
+    // decoders, and a barrier's parity tells two neighbouring phases apart, no more: of the
+    // barrier for every fourth tile, the phase before this one (kt - 4) is one that the group, or a
+    // row block that all groups are past, has used.
+    auto issue = [&](int kt) {
+      ok = ok && warp_wait(&mt.k_full[kt & 3], (kt >> 2) & 1, abort_flag);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t kd = kdesc + (uint64_t)(((kt % NS) * C::kOpBytes) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);
+          mma_ss(tmem + w * 128, (COLS ? kd : qdesc) + step, (COLS ? qdesc : kd) + step, idesc, kk > 0);
+        }
+        mma_commit(&mt.s_full[w]);
+        mma_commit(&mt.k_empty[kt % NS]);
+      }
+      __syncwarp();
+    };
+    int ktb = 0, uses = 0;                              // K tiles of earlier row blocks; products of this group so far
     for (int rb = walk.r0; rb < walk.r1; ++rb) {
       // ---------------------------------------------------- Q, and what is known of its rows
-      // (the group has waited for every product of the last block's tile: with two tiles its own, with
-      // one both groups')
+      // (every group has waited for its products of the last block)
       const int row0 = rb * ROWS, RC = min(ROWS, req.n * p.G - row0);
-      named_bar_sync(1, 256);
-      if (w < nq) {
-        load_q<D, DT>(p, mt, smem + C::kOffQ + w * C::kOpBytes, req, g, row0, w, RC, cf < 0.f ? 0x80008000u : 0u, wl, lane);
-        __syncwarp();
+      named_bar_sync(1, kEpilogue);
+      for (int k = 0; k < nq; ++k)
+        load_q<D, DT>(p, mt, smem, req, g, row0, (warp * nq + k) * 8, RC, cf < 0.f ? 0x80008000u : 0u, lane);
+      fence_proxy_async_smem();
+      named_bar_sync(1, kEpilogue);
+      if (tid < nq * kM) {
         // (not 0, so that c * -inf stays -inf; nor NaN: a NaN scale goes into the rows' sums)
-        const float c = fmaxf(fabsf(cf) * mt.back[mine], 1e-30f);
-        const bool live = mine < RC;
-        mt.c[mine] = c;
-        mt.hi[mine] = live ? max(walk.base + token_at(p, row0 + mine) + 1, 0) : 0;
+        mt.c[tid] = fmaxf(fabsf(cf) * mt.back[tid], 1e-30f);
+        const bool live = tid < RC;
+        mt.hi[tid] = live ? max(walk.base + token_at(p, row0 + tid) + 1, 0) : 0;
         if (COLS) {
-          const Norm n = live ? join_norm(p.ml, plane, vec_of(row0 + mine), p.S) : Norm{0.f, 0.f};
-          mt.m[mine] = -n.m;
-          mt.inv[mine] = n.inv;
+          const Norm n = live ? join_norm(p.ml, plane, vec_of(row0 + tid), p.S) : Norm{0.f, 0.f};
+          mt.m[tid] = -n.m;
+          mt.inv[tid] = n.inv;
+          mt.ml[tid] = folded(n);
         }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&mt.q_full);
-      named_bar_sync(1, 256);
+      named_bar_sync(1, kEpilogue);
       const int n_tiles = walk.tiles_of(rb);
+      if (wl == 0 && j0 < n_tiles) issue(ktb + j0);
+      // the group's rows: the least that one sees; columns: whether logits are past 2^22
+      const int mine = tile * kM + 32 * wl + lane;      // rows: this thread's
+      int hi = mine < RC ? mt.hi[mine] : INT_MAX;       // rows past RC: everything, dropped at the end
+      const float c = mt.c[mine];
+      bool far_cols = false;
       if (COLS) {
-        // the tile's rows: the least that one sees, and whether logits are past 2^22
-        int hi_min = INT_MAX;
         float top = 0.f;
+        hi = INT_MAX;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          hi_min = min(hi_min, mt.hi[tile * kM + 32 * i + lane]);
+          hi = min(hi, mt.hi[tile * kM + 32 * i + lane]);
           top = fmaxf(top, fabsf(mt.m[tile * kM + 32 * i + lane]));
         }
-        hi_min = __reduce_min_sync(0xffffffffu, hi_min);
-        const bool far = __any_sync(0xffffffffu, top >= 0x1p22f);
-        for (int j = 0; j < n_tiles; ++j, ++kt) {
-          if (nq == 1 && (kt & 1) != w) continue;
-          const int buf = w + 2 * (uses & 1);
-          ok = ok && warp_wait(&mt.s_full[buf], (uses >> 1) & 1, abort_flag);
-          ++uses;
-          if (!ok) continue;
-          tc_fence_after();
-          const int v0 = walk.u0 + j * kT, t = v0 + 32 * wl + lane;
-          const bool there = (mt.valid[kt & 7][wl] >> lane) & 1u;
-          const bool masked = v0 + kT > hi_min;
-          float sum = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[64];
-            tmem_ld64(tmem + buf * 128 + lane_off + 64 * h, x);
-            if (h == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&mt.s_empty[buf]);
+        far_cols = __any_sync(0xffffffffu, top >= 0x1p22f);
+      }
+      const int hi_min = __reduce_min_sync(0xffffffffu, hi);
+      constexpr bool kOne = DT == FP8KV_DTYPE_F16;      // (bf16 rows have scales of their own)
+      float m = kNoMax, l = 0.f;
+      for (int j = j0; j < n_tiles; j += j_step) {
+        const int kt = ktb + j, parity = uses & 1;
+        ok = ok && warp_wait(&mt.s_full[w], parity, abort_flag);
+        ++uses;
+        if (!ok) break;
+        tc_fence_after();
+        const int v0 = walk.u0 + j * kT;
+        const uint4 there = *reinterpret_cast<const uint4*>(mt.valid[kt & 7]);
+        const bool masked = v0 + kT > hi_min || (!COLS && (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu);
+        const int t = v0 + 32 * wl + lane;              // columns: this thread's position
+        float sum = 0.f;
+#pragma unroll 1
+        for (int h = 0; h < kT / kCols; ++h) {
+          uint32_t x[kCols];
+          tmem_ld32(tS + kCols * h, x);
+          if (h == kT / kCols - 1) {
+            // S is read: the next product may be written over it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mt.s_empty[w]);
+            if (wl == 0 && j + j_step < n_tiles) {
+              ok = warp_wait(&mt.s_empty[w], parity, abort_flag);
+              issue(kt + j_step);
             }
-            const int r0 = tile * kM + 64 * h;
-            if (far)
-              sum += masked ? column_sum<true, true>(x, mt, r0, t) : column_sum<false, true>(x, mt, r0, t);
-            else
-              sum += masked ? column_sum<true, false>(x, mt, r0, t) : column_sum<false, false>(x, mt, r0, t);
           }
-          if (!there) sum = 0.f;
-          if (t < walk.u1) {
-            if (gather)
-              acc[w * kScoreAccTokens + t - walk.u0] += sum;
-            else if (sp.groups == 1)
-              write_score(sp, b, g, t, walk.base, sum);
+          if (COLS) {
+            const int r0 = tile * kM + kCols * h;
+            if (far_cols)
+              sum += masked ? column_sum<true, true, false>(x, mt, r0, t, c) : column_sum<false, true, false>(x, mt, r0, t, c);
             else
-              sp.partial[(((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len + t] = sum;
-          }
-        }
-      } else {
-        const float c = mt.c[mine];
-        const int hi = mine < RC ? mt.hi[mine] : INT_MAX;  // rows past RC: everything, dropped at the end
-        const int hi_min = __reduce_min_sync(0xffffffffu, hi);
-        float m = kNoMax, l = 0.f;
-        for (int j = 0; j < n_tiles; ++j, ++kt) {
-          if (nq == 1 && (kt & 1) != w) continue;
-          const int buf = w + 2 * (uses & 1);
-          ok = ok && warp_wait(&mt.s_full[buf], (uses >> 1) & 1, abort_flag);
-          ++uses;
-          if (!ok) continue;
-          tc_fence_after();
-          const int v0 = walk.u0 + j * kT;
-          const uint4 there = *reinterpret_cast<const uint4*>(mt.valid[kt & 7]);
-          const bool masked = (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu || v0 + kT > hi_min;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[64];
-            tmem_ld64(tmem + buf * 128 + lane_off + 64 * h, x);
-            if (h == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&mt.s_empty[buf]);
-            }
+              sum += masked ? column_sum<true, false, kOne>(x, mt, r0, t, c) : column_sum<false, false, kOne>(x, mt, r0, t, c);
+          } else {
             if (masked) {
               // logits that the row does not see become -inf (a NaN among them too)
+              const uint32_t vis =
+                  (h == 0 ? there.x : h == 1 ? there.y : h == 2 ? there.z : there.w) & below(hi - v0 - kCols * h);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t vis = (h == 0 ? (i == 0 ? there.x : there.y) : (i == 0 ? there.z : there.w)) &
-                                     below(hi - v0 - 64 * h - 32 * i);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[32 * i + k] = ((vis >> k) & 1u) ? x[32 * i + k] : 0xFF800000u;
-              }
+              for (int k = 0; k < kCols; ++k) x[k] = ((vis >> k) & 1u) ? x[k] : 0xFF800000u;
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is passed over: it makes the sum NaN)
 #pragma unroll
-            for (int k = 0; k < 64; k += 8)
+            for (int k = 0; k < kCols; k += 8)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[k + 2 * i])), __uint_as_float(x[k + 2 * i + 1]));
@@ -450,44 +497,59 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
             }
             const float sh = m == kNoMax ? 0.f : -m;
             const bool far = __any_sync(0xffffffffu, fabsf(sh) >= 0x1p22f);
-            uint64_t sum[2] = {0ull, 0ull};
             if (far) {
               // the maximum is that of the rounded products, which the fma below would not round
 #pragma unroll
-              for (int k = 0; k < 64; ++k) x[k] = __float_as_uint(__fmul_rn(__uint_as_float(x[k]), c));
+              for (int k = 0; k < kCols; ++k) x[k] = __float_as_uint(__fmul_rn(__uint_as_float(x[k]), c));
             }
             const uint64_t c2 = far ? pair(1.f, 1.f) : pair(c, c), sh2 = pair(sh, sh);
+            uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
-            for (int k = 0; k < 64; k += 2) {
+            for (int k = 0; k < kCols; k += 2) {
               const float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
-              sum[(k / 2) & 1] = add2(sum[(k / 2) & 1], pair(fast_exp2(e.x), fast_exp2(e.y)));
+              part[(k / 2) & 1] = add2(part[(k / 2) & 1], pair(fast_exp2(e.x), fast_exp2(e.y)));
             }
-            const float2 y = unpair(add2(sum[0], sum[1]));
+            const float2 y = unpair(add2(part[0], part[1]));
             l += y.x + y.y;
           }
         }
-        if (cf != cf && l != 0.f) l = cf;
-        if (nq == 1) {  // the groups' halves of the positions
-          if (w == 1) mt.other[32 * wl + lane] = make_float2(m, l);
-          named_bar_sync(1, 256);
-          if (w == 0) {
-            const float2 y = mt.other[32 * wl + lane];
-            const float M = fmaxf(m, y.x);
-            l = (l != 0.f ? l * part_weight(m, M) : 0.f) + (y.y != 0.f ? y.y * part_weight(y.x, M) : 0.f);
-            m = M;
-          }
+        if (COLS && t < walk.u1) {
+          if (!(((wl == 0 ? there.x : wl == 1 ? there.y : wl == 2 ? there.z : there.w) >> lane) & 1u)) sum = 0.f;
+          if (gather)
+            acc[tile * kScoreAccTokens + t - walk.u0] += sum;
+          else if (sp.groups == 1)
+            write_score(sp, b, g, t, walk.base, sum);
+          else
+            sp.partial[(((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len + t] = sum;
         }
-        if (ok && w < nq && mine < RC) p.ml[s * plane + vec_of(row0 + mine)] = make_float2(m, l);
+      }
+      ktb += n_tiles;
+      if (!COLS) {
+        if (cf != cf && l != 0.f) l = cf;
+        // the groups' shares of the positions
+        const int heirs = nq;  // groups 0 (and 1) take over
+        if (w >= heirs) mt.other[w - 1][32 * wl + lane] = make_float2(m, l);
+        named_bar_sync(1, kEpilogue);
+        if (w < heirs) {
+          float M = m;
+          for (int q = w + heirs; q < kGroups; q += heirs) M = fmaxf(M, mt.other[q - 1][32 * wl + lane].x);
+          float L = l != 0.f ? l * part_weight(m, M) : 0.f;
+          for (int q = w + heirs; q < kGroups; q += heirs) {
+            const float2 y = mt.other[q - 1][32 * wl + lane];
+            if (y.y != 0.f) L = fmaf(y.y, part_weight(y.x, M), L);
+          }
+          if (ok && mine < RC) p.ml[s * plane + vec_of(row0 + mine)] = make_float2(M, L);
+        }
       }
     }
     if (COLS && !gather && sp.groups > 1) {  // positions that none of the block's rows sees
       float* to = sp.partial + (((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len;
-      for (int t = walk.u0 + walk.tiles_of(walk.r0) * kT + tid; t < walk.u1; t += 256) to[t] = 0.f;
+      for (int t = walk.u0 + walk.tiles_of(walk.r0) * kT + tid; t < walk.u1; t += kEpilogue) to[t] = 0.f;
     }
     if (gather) {
-      named_bar_sync(1, 256);
+      named_bar_sync(1, kEpilogue);
       if (ok)
-        for (int t = walk.u0 + tid; t < walk.u1; t += 256) {
+        for (int t = walk.u0 + tid; t < walk.u1; t += kEpilogue) {
           const float sum = acc[t - walk.u0] + acc[kScoreAccTokens + t - walk.u0];
           if (sp.groups == 1)
             write_score(sp, b, g, t, walk.base, sum);
@@ -495,50 +557,21 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
             sp.partial[(((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len + t] = sum;
         }
     }
-  } else if (warp < kIssuer) {
-    ok = decode_k<D, FMT>(p, mt, smem, b, g, walk, warp - 8, lane);
-  } else {
-    // ======================================================== UMMA issue
-    const uint32_t idesc = idesc_f16_f32(kM, kT, false, false);
-    const uint64_t qdesc = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kSw128);
-    const uint64_t kdesc = smem_desc(smem_u32(smem + C::kOffK), 16, 1024, kSw128);
-    int kt = 0, it = 0;
-    for (int rb = walk.r0; rb < walk.r1 && ok; ++rb) {
-      ok = warp_wait(&mt.q_full, (rb - walk.r0) & 1, abort_flag);
-      const int n_tiles = walk.tiles_of(rb);
-      for (int j = 0; j < n_tiles && ok; ++j, ++kt) {
-        ok = warp_wait(&mt.k_full[kt % NS], (kt / NS) & 1, abort_flag);
-        for (int q = 0; q < nq && ok; ++q, ++it) {
-          const int buf = it & 3;
-          if (it >= kBufs) ok = warp_wait(&mt.s_empty[buf], ((it >> 2) - 1) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t qd = qdesc + (uint64_t)((q * C::kOpBytes) >> 4);
-          const uint64_t kd = kdesc + (uint64_t)(((kt % NS) * C::kOpBytes) >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t step = (uint64_t)(((kk / 4) * (kM * 128) + (kk % 4) * 32) >> 4);
-              mma_ss(tmem + buf * 128, (COLS ? kd : qd) + step, (COLS ? qd : kd) + step, idesc, kk > 0);
-            }
-            mma_commit(&mt.s_full[buf]);
-            if (q == nq - 1) mma_commit(&mt.k_empty[kt % NS]);
-          }
-          __syncwarp();
-        }
-      }
+    if (wl == 0) {
+      // every UMMA issued must be done before TMEM is freed
+      if (elect_one()) mma_commit(&mt.drain[w]);
+      __syncwarp();
+      mbar_wait_plain(&mt.drain[w], 0, kPolls);
+      __syncwarp();
     }
-    // every UMMA issued must be done before TMEM is freed
-    if (elect_one()) mma_commit(&mt.drain);
-    __syncwarp();
-    mbar_wait_plain(&mt.drain, 0, kPolls);
-    __syncwarp();
+  } else {
+    ok = decode_k<D, FMT>(p, mt, smem, b, g, walk, warp - 4 * kGroups, lane);
   }
   if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
