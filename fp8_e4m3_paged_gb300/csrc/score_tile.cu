@@ -11,8 +11,8 @@
 // exchanged, so the two passes are one kernel; a position's sum stays within a thread, in
 // a fixed order, without atomics.
 //
-// Twenty warps: four groups of four, each with one S buffer (128 columns; the four are all of
-// TMEM), whose first warp issues the group's next product as soon as the last one is read; four decode K,
+// Twenty-four warps: four groups of four, each with one S buffer (128 columns; the four are all of
+// TMEM), whose first warp issues the group's next product as soon as the last one is read; two teams of four decode K,
 // FP8 rows brought by cp.async into a ring of tiles, to fp16.  While one group waits for its product,
 // the others have 32 columns at a time in registers: four warps on each scheduler, where two
 // groups with two buffers each, ahead of the tensor core, took 2500 cycles for 128 x 128, most of it
@@ -36,8 +36,9 @@ namespace {
 
 constexpr int kGroups = 4;
 constexpr int kEpilogue = kGroups * 128;         // threads
-constexpr int kThreadsT = kEpilogue + 128;
-constexpr int kMetaHead = 11264;
+constexpr int kTeams = 2;                        // of four decoder warps: every other K tile each
+constexpr int kThreadsT = kEpilogue + kTeams * 128;
+constexpr int kMetaHead = 12288;
 constexpr int kCols = 32;                        // columns in registers
 
 template <int D>
@@ -45,13 +46,13 @@ struct Cfg : RowCfg<D> {
   static constexpr int kNQ = D == 256 ? 1 : 2;                      // row tiles
   static constexpr int kRows = kNQ * kM;
   static constexpr int kStages = D == 256 ? 1 : 2;                   // K tiles, as fp16
-  static constexpr int kRing = D == 256 ? 2 : D == 128 ? 3 : 6;      // ... on their way, as bytes
+  static constexpr int kRing = D == 256 ? 1 : D == 128 ? 2 : 4;      // ... on their way, as bytes, of each team
   static constexpr int kOpBytes = kT * D * 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kNQ * kOpBytes;
   static constexpr int kRawBytes = kT * D;
   static constexpr int kOffRaw = kOffK + kStages * kOpBytes;
-  static constexpr int kOffMeta = kOffRaw + kRing * kRawBytes;
+  static constexpr int kOffMeta = kOffRaw + kTeams * kRing * kRawBytes;
   static constexpr int kMetaBytes = kMetaHead + 2 * kScoreAccTokens * 4;
   // (at least half an SM's shared memory: one CTA per SM, which takes all of its TMEM)
   static constexpr int kSmem = (kOffMeta + kMetaBytes > 118000 ? kOffMeta + kMetaBytes : 118000) + 1024;
@@ -59,10 +60,10 @@ struct Cfg : RowCfg<D> {
 };
 
 struct Meta {
-  uint64_t k_full[4], k_empty[2];     // per tile (% 4), per stage
+  uint64_t k_full[4], k_empty[2];     // per tile (% 4, % 2)
   uint64_t s_full[kGroups], s_empty[kGroups], drain[kGroups];
   alignas(16) uint32_t valid[8][4];   // per tile (% 8): positions whose block is in range
-  int64_t place[4][32];               // per decoder warp: byte offsets of its rows
+  int64_t place[4 * kTeams][32];      // per decoder warp: byte offsets of its rows
   alignas(16) float c[256], ml[256];           // rows: logit factor; -(maximum + log2 of the sum)
   alignas(16) float m[256], inv[256];          // ... apart: -maximum; 1 / sum
   alignas(16) int hi[256];            // rows: positions below are seen (0: a row that is not there)
@@ -82,20 +83,27 @@ struct Walk {
   __device__ __forceinline__ int tiles_of(int rb) const { return (min(u1, last_of(rb)) - u0 + kT - 1) / kT; }
 };
 
-// Decoders: the K tiles of the walk, in order.
+// Decoders: every other K tile of the walk, in order.  A tile costs its warps some 250 instructions in
+// a chain (the copies' completion, the stage, the conversions, the next copies and block ids), one
+// warp to a scheduler: two teams, so that a tile is ready twice as often.
 template <int D, int FMT>
 __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t* smem, int b, int g, const Walk& walk,
-                                         int w, int lane) {
+                                         int team, int w, int lane) {
   using C = Cfg<D>;
-  constexpr int NS = C::kStages;
+  constexpr int NS = C::kStages, R = C::kRing;
   volatile uint32_t* const abort_flag = &mt.abort;
-  const uint8_t* kbase = p.k_cache + g * p.ksh;
+  const uint8_t* kbase = p.k_cache + g * p.ksh + (lane % C::kCh) * 16;
   const int32_t* table = p.block_table + (int64_t)b * p.bt_stride;
-  int64_t* place = mt.place[w];
-  constexpr int R = C::kRing;
+  int64_t* place = mt.place[4 * team + w];
   // a lane copies, and reads back, piece lane % kCh of rows it * kRowsIt + lane / kCh of the warp's 32
-  uint8_t* raw = smem + C::kOffRaw + (32 * w + lane / C::kCh) * D + (lane % C::kCh) * 16;
+  uint8_t* raw = smem + C::kOffRaw + team * R * C::kRawBytes + (32 * w + lane / C::kCh) * D + (lane % C::kCh) * 16;
   int rb = walk.r0, j = 0, n_tiles = walk.tiles_of(rb);  // the next tile to ask for: row block, tile of it
+  auto forward = [&]() {
+    if (rb < walk.r1 && ++j == n_tiles) {
+      j = 0;
+      if (++rb < walk.r1) n_tiles = walk.tiles_of(rb);
+    }
+  };
   struct Ask {
     int blk, slot;
     bool in;
@@ -108,10 +116,7 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
     a.slot = v - page * p.page_size;
     a.in = v < walk.u1;
     if (a.in) a.blk = __ldg(table + page);
-    if (++j == n_tiles) {
-      j = 0;
-      if (++rb < walk.r1) n_tiles = walk.tiles_of(rb);
-    }
+    for (int i = 0; i < kTeams; ++i) forward();
     return a;
   };
   auto request = [&](const Ask& a, int slot) {  // returns the rows that are there
@@ -120,13 +125,13 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
     __syncwarp();
     place[lane] = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
     __syncwarp();
-    const uint8_t* from = kbase + (lane % C::kCh) * 16;
 #pragma unroll
     for (int it = 0; it < C::kIts; ++it)
-      cp_async16(raw + slot * C::kRawBytes + it * C::kRowsIt * D, from + place[it * C::kRowsIt + lane / C::kCh]);
+      cp_async16(raw + slot * C::kRawBytes + it * C::kRowsIt * D, kbase + place[it * C::kRowsIt + lane / C::kCh]);
     return __ballot_sync(0xffffffffu, ok);
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  for (int i = 0; i < team; ++i) forward();
   uint32_t there[R];
   Ask next;
   {
@@ -140,32 +145,37 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
     }
     next = first[R];
   }
-  int kt = 0;
-  for (int r = walk.r0; r < walk.r1; ++r) {
-    const int n = walk.tiles_of(r);
-    for (int i = 0; i < n; ++i, ++kt) {
-      const int st = kt % NS, slot = kt % R;
-      asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
-      uint4 kr[C::kIts];
-#pragma unroll
-      for (int it = 0; it < C::kIts; ++it)
-        kr[it] = *reinterpret_cast<const uint4*>(raw + slot * C::kRawBytes + it * C::kRowsIt * D);
-      if (kt >= NS && !warp_wait(&mt.k_empty[st], ((kt / NS) - 1) & 1, abort_flag)) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        return false;
-      }
-      store_rows<D, FMT>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w, lane);
-      // (valid[kt % 8] of tile kt - 8 has been read: the product of kt - 4 is done, which that tile's
-      // group issued behind it)
-      if (lane == 0) mt.valid[kt & 7][w] = there[0];
-      fence_proxy_async_smem();
-      mbar_arrive(&mt.k_full[kt & 3]);
-#pragma unroll
-      for (int q = 0; q + 1 < R; ++q) there[q] = there[q + 1];
-      there[R - 1] = request(next, slot);
-      commit();
-      next = ask();
+  int total = 0;
+  for (int r = walk.r0; r < walk.r1; ++r) total += walk.tiles_of(r);
+  int slot = 0;
+  for (int kt = team; kt < total; kt += kTeams) {
+    const int st = kt % NS, before = kt - NS;  // the tile that was there
+    asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+    if (before >= 0 && !warp_wait(&mt.k_empty[before & 1], (before >> 1) & 1, abort_flag)) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      return false;
     }
+    constexpr int kAtOnce = C::kIts < 8 ? C::kIts : 8;
+#pragma unroll
+    for (int i0 = 0; i0 < C::kIts; i0 += kAtOnce) {
+      uint4 kr[kAtOnce];
+#pragma unroll
+      for (int it = 0; it < kAtOnce; ++it)
+        kr[it] = *reinterpret_cast<const uint4*>(raw + slot * C::kRawBytes + (i0 + it) * C::kRowsIt * D);
+      store_rows<D, FMT, kAtOnce>(smem + C::kOffK + st * C::kOpBytes, kr, 32 * w + i0 * C::kRowsIt, lane);
+    }
+    // (valid[kt % 8] of tile kt - 8 has been read: the product of kt - 4 is done, which that tile's
+    // group issued behind it)
+    if (lane == 0) mt.valid[kt & 7][w] = there[0];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&mt.k_full[kt & 3]);
+#pragma unroll
+    for (int q = 0; q + 1 < R; ++q) there[q] = there[q + 1];
+    there[R - 1] = request(next, slot);
+    commit();
+    next = ask();
+    slot = slot + 1 == R ? 0 : slot + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   return true;
@@ -346,10 +356,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   const bool gather = COLS && (nq == 2 || walk.r1 - walk.r0 > 1);  // sums of several row tiles meet in `acc`
 
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&mt.k_empty[i], nq);
-    }
-    for (int i = 0; i < 4; ++i) mbar_init(&mt.k_full[i], 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&mt.k_empty[i], nq);
+    for (int i = 0; i < 4; ++i) mbar_init(&mt.k_full[i], 4);  // one lane of each decoder warp
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&mt.s_full[i], 1);
       mbar_init(&mt.s_empty[i], 4);  // one lane of each of the group's warps
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
           mma_ss(tmem + w * 128, (COLS ? kd : qdesc) + step, (COLS ? qdesc : kd) + step, idesc, kk > 0);
         }
         mma_commit(&mt.s_full[w]);
-        mma_commit(&mt.k_empty[kt % NS]);
+        mma_commit(&mt.k_empty[kt & 1]);
       }
       __syncwarp();
     };
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       __syncwarp();
     }
   } else {
-    ok = decode_k<D, FMT>(p, mt, smem, b, g, walk, warp - 4 * kGroups, lane);
+    ok = decode_k<D, FMT>(p, mt, smem, b, g, walk, (warp >> 2) - kGroups, warp & 3, lane);
   }
   if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
   __syncwarp();

@@ -112,14 +112,15 @@ __device__ __forceinline__ void fetch_rows(const uint8_t* base, const int64_t* p
 // ... and as fp16 in the operand tile: 64-column blocks of kT rows of 128
 // bytes, 16-byte chunk c of row r at c ^ (r % 8).  Odd column blocks store
 // their two chunks in the other order, so that eight lanes hit eight banks.
-template <int D, int FMT>
-__device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[RowCfg<D>::kIts], int row_base, int lane) {
+// (ITS: of the warp's rows, as many times kRowsIt as one call stores.)
+template <int D, int FMT, int ITS = RowCfg<D>::kIts>
+__device__ __forceinline__ void store_rows(uint8_t* op, const uint4 (&w)[ITS], int row_base, int lane) {
   using C = RowCfg<D>;
   const int c = lane % C::kCh, db = c / 4, h0 = (c % 4) * 2;
   const bool swap = db & 1;
   const int first = swap ? h0 + 1 : h0, second = swap ? h0 : h0 + 1;
 #pragma unroll
-  for (int it = 0; it < C::kIts; ++it) {
+  for (int it = 0; it < ITS; ++it) {
     const int r = row_base + it * C::kRowsIt + lane / C::kCh;
     uint8_t* row = op + db * (kT * 128) + r * 128;
     uint4 a, b;
