@@ -68,7 +68,7 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     P.row_tiles = (int32_t)(P.total_q * (int64_t)P.group / tile + std::min(P.batch, P.total_q));
     const int64_t units = std::max<int64_t>((int64_t)P.row_tiles * P.num_kv_heads, 1);
     // rows' sums: some four CTAs per SM of at least 8 tiles, one per row block where those are many
-    int64_t part = units >= 2 * sms ? tiles : std::min(tiles, std::max<int64_t>(8, ceil_div(units * tiles, 4 * sms)));
+    int64_t part = units >= 2 * sms ? tiles : std::min(tiles, std::max<int64_t>(8, ceil_div(units * tiles, 10 * sms)));
     if (d->num_splits) part = ceil_div(tiles, d->num_splits);
     part = std::max<int64_t>(part, ceil_div(tiles, 65535));
     P.stat_part = (int32_t)(part * kChunkTileTokens);
@@ -76,7 +76,7 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     // columns: likewise; several row tiles meet in shared memory, which holds 2048 positions
     const int64_t blocks = ceil_div(rows, tile);
     const int64_t most = rows > 128 ? kScoreAccTokens / kChunkTileTokens : tiles;
-    part = std::min(most, std::max<int64_t>(8, ceil_div(pairs * tiles, 4 * sms)));
+    part = std::min(most, std::max<int64_t>(8, ceil_div(pairs * tiles, 10 * sms)));
     P.col_part = (int32_t)(std::max<int64_t>(part, 1) * kChunkTileTokens);
     const int64_t ctas = std::max<int64_t>(pairs * ceil_div(len, P.col_part), 1);
     P.row_groups = (int32_t)std::max<int64_t>(1, std::min({blocks, 4 * sms / ctas, (int64_t)32}));

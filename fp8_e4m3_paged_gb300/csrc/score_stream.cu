@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   const int u1 = (int)min((int64_t)u0 + sp.stat_part, (int64_t)req.kv);
   if (u0 >= u1) return;  // (nor does the second kernel read it)
 
-  // (as in the attention's streaming kernel: block ids one block ahead, unconditional copies,
-  // tokens without a place read the pool's first row and are masked)
+  // (as in the attention's streaming kernel, block ids one block ahead; rows of tokens without a
+  // place are zeros, and masked)
   const uint8_t* kbase = p.k_cache + g * p.ksh + (lane % C::kCh) * 16;
   uint8_t* ring = smem + warp * C::kRing;
   int64_t* place = reinterpret_cast<int64_t*>(sML + warp * 32);
@@ -102,16 +102,17 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   auto request = [&](const Ask& a, int st) {
     const bool ok = a.blk >= 0 && a.blk < p.num_kv_blocks;
     if (a.in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    __syncwarp();
+    const uint32_t rows = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
     if (lane < kBlk) place[lane] = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
     __syncwarp();
     uint8_t* dst = ring + st * C::kRowBytes;
 #pragma unroll
     for (int it = 0; it < kBlk / C::kRowsIt; ++it) {
       const int r = it * C::kRowsIt + lane / C::kCh;
-      tc::cp_async16(dst + r * D + (((lane % C::kCh) ^ swz(r)) * 16), kbase + place[r]);
+      tc::cp_async16_or_zero(dst + r * D + (((lane % C::kCh) ^ swz(r)) * 16), kbase + place[r], (rows >> r) & 1u ? 16u : 0u);
     }
-    return __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
+    __syncwarp();
+    return rows;
   };
   constexpr int kStep = kBlk * kWarps;
   const int t_first = u0 + kBlk * warp;

@@ -122,13 +122,19 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
   auto request = [&](const Ask& a, int slot) {  // returns the rows that are there
     const bool ok = a.blk >= 0 && a.blk < p.num_kv_blocks;
     if (a.in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    __syncwarp();
+    const uint32_t rows = __ballot_sync(0xffffffffu, ok);
+    if (rows == 0u) return rows;  // (their logits are masked, whatever the bytes)
     place[lane] = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
     __syncwarp();
+    // Rows that are not there are not read: one row in their place, the same for every CTA, took 5 us
+    // of each CTA's 15 in waiting for its part of the L2.
 #pragma unroll
-    for (int it = 0; it < C::kIts; ++it)
-      cp_async16(raw + slot * C::kRawBytes + it * C::kRowsIt * D, kbase + place[it * C::kRowsIt + lane / C::kCh]);
-    return __ballot_sync(0xffffffffu, ok);
+    for (int it = 0; it < C::kIts; ++it) {
+      const int r = it * C::kRowsIt + lane / C::kCh;
+      cp_async16_or_zero(raw + slot * C::kRawBytes + it * C::kRowsIt * D, kbase + place[r], (rows >> r) & 1u ? 16u : 0u);
+    }
+    __syncwarp();
+    return rows;
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
   for (int i = 0; i < team; ++i) forward();
@@ -139,7 +145,7 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
 #pragma unroll
     for (int i = 0; i <= R; ++i) first[i] = ask();
 #pragma unroll
-    for (int i = 0; i < R; ++i) {  // (past the last tile: the pool's first row)
+    for (int i = 0; i < R; ++i) {
       there[i] = request(first[i], i);
       commit();
     }
@@ -287,6 +293,12 @@ __device__ __forceinline__ float folded(const Norm& n) {
     ++e;
   }
   return ((float)e - n.m) + log2f(f);
+}
+
+// Logits for which the rounded products count.
+__device__ __forceinline__ void scale(uint32_t (&x)[kCols], float c) {
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) x[k] = __float_as_uint(__fmul_rn(__uint_as_float(x[k]), c));
 }
 
 template <int D, int FMT, int DT, bool COLS>
@@ -451,7 +463,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       }
       const int hi_min = __reduce_min_sync(0xffffffffu, hi);
       constexpr bool kOne = DT == FP8KV_DTYPE_F16;      // (bf16 rows have scales of their own)
-      float m = kNoMax, l = 0.f;
+      float m = 0.f, l = 0.f;                           // rows: a whole number near the largest logit; sum
+      bool started = false;                             // ... a logit above -inf was seen
+      bool far = false;                                 // some row of the warp has logits past 2^22: products are rounded
+                                                        // before the maximum is taken off
       for (int j = j0; j < n_tiles; j += j_step) {
         const int kt = ktb + j, parity = uses & 1;
         ok = ok && warp_wait(&mt.s_full[w], parity, abort_flag);
@@ -491,34 +506,37 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
 #pragma unroll
               for (int k = 0; k < kCols; ++k) x[k] = ((vis >> k) & 1u) ? x[k] : 0xFF800000u;
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is passed over: it makes the sum NaN)
+            // Sum of the weights over the maximum so far: in FP32 it may be any near one, so it moves only
+            // when the sum has grown past 2^40 (or is not a number), and no maximum is looked for else.
+            auto weights = [&]() {
+              const uint64_t c2 = far ? pair(1.f, 1.f) : pair(c, c), sh2 = pair(-m, -m);
+              uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
-            for (int k = 0; k < kCols; k += 8)
+              for (int k = 0; k < kCols; k += 2) {
+                const float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
+                part[(k / 2) & 1] = add2(part[(k / 2) & 1], pair(fast_exp2(e.x), fast_exp2(e.y)));
+              }
+              const float2 y = unpair(add2(part[0], part[1]));
+              return y.x + y.y;
+            };
+            if (far) scale(x, c);
+            float y = started ? weights() : INFINITY;
+            if (__any_sync(0xffffffffu, !(y < 0x1p40f))) {
+              float top = -INFINITY;  // (a NaN is passed over: it makes the sum NaN)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[k + 2 * i])), __uint_as_float(x[k + 2 * i + 1]));
-            const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c);
-            if (top - m > kChunkTau) {  // (false where both are -inf)
-              const float n = fmaxf(m, ceilf(top));
-              if (m != kNoMax) l *= exp2_whole(m - n);
+              for (int k = 0; k < kCols; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+              top = far ? top : __fmul_rn(top, c);
+              const float n = top == -INFINITY ? m : started ? fmaxf(m, ceilf(top)) : ceilf(top);
+              if (started) l *= exp2_whole(m - n);
               m = n;
+              started |= top != -INFINITY;
+              if (!far && __any_sync(0xffffffffu, fabsf(m) >= 0x1p22f)) {
+                far = true;
+                scale(x, c);
+              }
+              y = started ? weights() : 0.f;
             }
-            const float sh = m == kNoMax ? 0.f : -m;
-            const bool far = __any_sync(0xffffffffu, fabsf(sh) >= 0x1p22f);
-            if (far) {
-              // the maximum is that of the rounded products, which the fma below would not round
-#pragma unroll
-              for (int k = 0; k < kCols; ++k) x[k] = __float_as_uint(__fmul_rn(__uint_as_float(x[k]), c));
-            }
-            const uint64_t c2 = far ? pair(1.f, 1.f) : pair(c, c), sh2 = pair(sh, sh);
-            uint64_t part[2] = {0ull, 0ull};
-#pragma unroll
-            for (int k = 0; k < kCols; k += 2) {
-              const float2 e = unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, sh2));
-              part[(k / 2) & 1] = add2(part[(k / 2) & 1], pair(fast_exp2(e.x), fast_exp2(e.y)));
-            }
-            const float2 y = unpair(add2(part[0], part[1]));
-            l += y.x + y.y;
+            l += y;
           }
         }
         if (COLS && t < walk.u1) {
@@ -534,6 +552,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       ktb += n_tiles;
       if (!COLS) {
         if (cf != cf && l != 0.f) l = cf;
+        if (!started) m = kNoMax;
         // the groups' shares of the positions
         const int heirs = nq;  // groups 0 (and 1) take over
         if (w >= heirs) mt.other[w - 1][32 * wl + lane] = make_float2(m, l);

@@ -72,6 +72,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 __device__ __forceinline__ void cp_async16(void* dst_smem, const void* src_gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem) : "memory");
 }
+// ... of `bytes` (0 or 16); with 0 nothing is read, and zeros are written.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst_smem, const void* src_gmem, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem), "r"(bytes)
+               : "memory");
+}
 // Arrive on `bar` once every cp.async this thread issued so far has completed
 // (the arrival counts toward the barrier's expected count).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
