@@ -218,9 +218,9 @@ class CacheScorePlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "revision", "batch", "total_q", "max_q", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
         "max_kv_len", "max_blocks", "num_kv_blocks", "dtype", "kv_format", "group", "kernel", "num_splits",
-        "vectors", "row_tiles", "stat_part", "col_part", "row_groups", "num_sms")] + [
+        "vectors", "row_tiles", "stat_part", "col_part", "row_groups", "per_head", "num_sms")] + [
         ("partial_offset", ctypes.c_int64), ("ml_offset", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
-        ("reserved", ctypes.c_int32 * 6),
+        ("reserved", ctypes.c_int32 * 7),
     ]
 
 

@@ -6,6 +6,7 @@
 namespace fp8kv {
 
 constexpr int kScoreStreamRows = 16;    // most query vectors per KV head of the streaming kernel
+constexpr int kScoreShareRequests = 128; // requests that a CTA of the tile kernel finds its share among
 constexpr int kScoreAccTokens = 2048;   // positions of a CTA that adds up several row blocks
 
 // Vectors that the streaming kernel keeps the logits of, per position: 4, 8 or 16.
@@ -16,6 +17,7 @@ struct ScoreParams {
   int32_t stat_part;       // positions of such a partition (tile kernel)
   int32_t col_part;        // positions of a CTA of the column pass (tile kernel)
   int32_t groups;          // row groups of the column pass; above 1 they meet in `partial`
+  int32_t per_head;        // tile kernel, above 0: CTAs per KV head, which find their shares from the lengths
   int32_t vectors;         // as score_vectors
   float* logits;           // [B][Hkv][max_kv_len][vectors] base-2 logits (streaming kernel)
   float* partial;          // [groups][B][Hkv][max_kv_len] (tile kernel, groups > 1)

@@ -68,7 +68,7 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     P.row_tiles = (int32_t)(P.total_q * (int64_t)P.group / tile + std::min(P.batch, P.total_q));
     const int64_t units = std::max<int64_t>((int64_t)P.row_tiles * P.num_kv_heads, 1);
     // rows' sums: some four CTAs per SM of at least 8 tiles, one per row block where those are many
-    int64_t part = units >= 2 * sms ? tiles : std::min(tiles, std::max<int64_t>(8, ceil_div(units * tiles, 10 * sms)));
+    int64_t part = units >= 2 * sms ? tiles : std::min(tiles, std::max<int64_t>(8, ceil_div(units * tiles, 3 * sms)));
     if (d->num_splits) part = ceil_div(tiles, d->num_splits);
     part = std::max<int64_t>(part, ceil_div(tiles, 65535));
     P.stat_part = (int32_t)(part * kChunkTileTokens);
@@ -76,11 +76,19 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     // columns: likewise; several row tiles meet in shared memory, which holds 2048 positions
     const int64_t blocks = ceil_div(rows, tile);
     const int64_t most = rows > 128 ? kScoreAccTokens / kChunkTileTokens : tiles;
-    part = std::min(most, std::max<int64_t>(8, ceil_div(pairs * tiles, 10 * sms)));
+    part = std::min(most, std::max<int64_t>(8, ceil_div(pairs * tiles, 3 * sms)));
     P.col_part = (int32_t)(std::max<int64_t>(part, 1) * kChunkTileTokens);
     const int64_t ctas = std::max<int64_t>(pairs * ceil_div(len, P.col_part), 1);
-    P.row_groups = (int32_t)std::max<int64_t>(1, std::min({blocks, 4 * sms / ctas, (int64_t)32}));
+    P.row_groups = (int32_t)std::max<int64_t>(1, std::min({blocks, 6 * sms / ctas, (int64_t)64}));
     floats = P.row_groups > 1 ? P.row_groups * pairs * len : 0;
+    // One row block per request, and CTAs enough for one wave: shares by the lengths on the device.
+    const int64_t per_head = sms / P.num_kv_heads;
+    if (d->num_splits == 0 && blocks <= 1 && P.batch <= std::min<int64_t>(per_head, kScoreShareRequests)) {
+      P.per_head = (int32_t)per_head;
+      P.num_splits = (int32_t)std::min(tiles, per_head);
+      P.row_groups = rows <= 128 ? 1 : 2;  // (two row tiles: each has its sums in the workspace)
+      floats = P.row_groups > 1 ? P.row_groups * pairs * len : 0;
+    }
   }
   if (P.num_splits > 65535 || (int64_t)P.row_tiles * P.num_kv_heads > 0x7fffffff) return FP8KV_EUNSUPPORTED;
   P.ml_offset = align_up(P.partial_offset + floats * 4, 256);
@@ -155,6 +163,7 @@ extern "C" int fp8kv_attn_cache_score(const fp8kv_cache_score_plan_t* plan, cons
   p.stat_part = plan->stat_part;
   p.col_part = plan->col_part;
   p.groups = plan->row_groups;
+  p.per_head = plan->per_head;
   p.vectors = plan->vectors;
   p.logits = p.partial = reinterpret_cast<float*>(ws + plan->partial_offset);
   p.in = a->score_in;

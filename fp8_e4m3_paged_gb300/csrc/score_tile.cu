@@ -39,6 +39,7 @@ constexpr int kEpilogue = kGroups * 128;         // threads
 constexpr int kTeams = 2;                        // of four decoder warps: every other K tile each
 constexpr int kThreadsT = kEpilogue + kTeams * 128;
 constexpr int kMetaHead = 12288;
+constexpr int kShareRequests = kScoreShareRequests / 32;
 constexpr int kCols = 32;                        // columns in registers
 
 template <int D>
@@ -82,6 +83,60 @@ struct Walk {
   }
   __device__ __forceinline__ int tiles_of(int rb) const { return (min(u1, last_of(rb)) - u0 + kT - 1) / kT; }
 };
+
+// A CTA's share where every request is one row block: the partitions' length T (tiles) is the least with
+// which all requests' partitions fit the `per_head` CTAs of a KV head, so that one wave of CTAs
+// has nearly equal work whatever the lengths are, and no CTA's start (10 us, and 17 in a further
+// wave) is paid twice on an SM.  (Four requests of 8000 to 60000 positions: 133 us with one length
+// chosen for the longest.)  By a whole warp; at most 32 kShareRequests requests.
+struct Share {
+  int b, s, T, parts;  // request, partition of it, tiles of a partition, partitions of the request
+};
+__device__ __forceinline__ bool share_of(const ChunkParams& p, int per_head, int idx, int lane, Share& out) {
+  int t[kShareRequests], most = 1;
+#pragma unroll
+  for (int i = 0; i < kShareRequests; ++i) {
+    const int b = lane + 32 * i;
+    t[i] = 0;
+    if (b < p.B) {
+      const ChunkRequest r = chunk_request(p, b);
+      if (r.bad && blockIdx.x == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
+      if (r.n > 0) t[i] = (r.kv + kT - 1) / kT;
+    }
+    most = max(most, t[i]);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  int lo = 1, hi = most;  // (as many CTAs as requests: with T = most they fit)
+  while (lo < hi) {
+    const int T = (lo + hi) >> 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kShareRequests; ++i) n += (t[i] + T - 1) / T;
+    if (__reduce_add_sync(0xffffffffu, n) <= (unsigned)per_head)
+      hi = T;
+    else
+      lo = T + 1;
+  }
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < kShareRequests; ++i) {
+    const int mine = (t[i] + lo - 1) / lo;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, upto > idx && upto - mine <= idx);
+    if (here && !found) {
+      found = true;
+      const int l = __ffs(here) - 1;
+      out = {l + 32 * i, idx - __shfl_sync(0xffffffffu, upto - mine, l), lo, __shfl_sync(0xffffffffu, mine, l)};
+    }
+    idx -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return found;
+}
 
 // Decoders: every other K tile of the walk, in order.  A tile costs its warps some 250 instructions in
 // a chain (the copies' completion, the stage, the conversions, the next copies and block ids), one
@@ -197,11 +252,17 @@ __device__ __forceinline__ void load_q(const ChunkParams& p, Meta& mt, uint8_t* 
   const int e = lane * V;
   uint8_t* sQ = smem + Cfg<D>::kOffQ + (first / kM) * Cfg<D>::kOpBytes;
   uint32_t w[kAtOnce][V / 2];
+  // (rows past RC read the last one)
+  RowAt at = row_at(p, row0 + min(first, RC - 1));
+  const uint16_t* next = p.q + (int64_t)(req.row0 + at.token) * p.q_st + (int64_t)(g * p.G + at.head) * p.q_sh + e;
 #pragma unroll
   for (int k = 0; k < kAtOnce; ++k) {
-    const int rr = row0 + min(first + k, RC - 1);
-    const uint16_t* src = p.q + (int64_t)(req.row0 + token_at(p, rr)) * p.q_st +
-                          (int64_t)(g * p.G + row_at(p, rr).head) * p.q_sh + e;
+    const uint16_t* src = next;
+    if (first + k + 1 < RC) {
+      const bool wrap = ++at.head == p.G;
+      if (wrap) at.head = 0;
+      next += wrap ? p.q_st - (p.G - 1) * p.q_sh : p.q_sh;
+    }
     if constexpr (V == 2)
       w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
     else if constexpr (V == 4)
@@ -315,22 +376,34 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   const int64_t plane = (int64_t)p.total_q * p.Hq;
 
   // ------------------------------------------------------ what this CTA has
-  int b, g, s = 0;
+  int b, g, s = 0, S = p.S;  // S: partitions of the rows' sums
   Walk walk;
   ChunkRequest req;
-  if (COLS) {
+  if (sp.per_head > 0) {
+    g = blockIdx.x % p.Hkv;
+    Share share;
+    if (!share_of(p, sp.per_head, blockIdx.x / p.Hkv, lane, share)) return;
+    b = share.b;
+    s = share.s;
+    S = share.parts;
+    req = chunk_request(p, b);
+    walk.r0 = 0;
+    walk.r1 = 1;
+    walk.u0 = share.s * share.T * kT;
+    walk.u1 = (int)min((int64_t)walk.u0 + (int64_t)share.T * kT, (int64_t)req.kv);
+  } else if (COLS) {
     b = div_hkv(p, blockIdx.x);
     g = blockIdx.x - b * p.Hkv;
     req = chunk_request(p, b);
-    walk.u0 = (int)min((int64_t)blockIdx.y * sp.col_part, (int64_t)INT_MAX);
+    walk.u0 = (int)min((int64_t)blockIdx.z * sp.col_part, (int64_t)INT_MAX);  // (the first, longest ones start first)
     walk.u1 = (int)min((int64_t)walk.u0 + sp.col_part, (int64_t)req.kv);
     if (req.n <= 0 || walk.u0 >= req.kv) return;
     // the row blocks that see anything here, and this group's share of them
     const int base = req.kv - req.n, blocks = (req.n * p.G + ROWS - 1) / ROWS;
     const int first = max(0, walk.u0 - base) * p.G / ROWS, share = (blocks - first + sp.groups - 1) / sp.groups;
-    walk.r0 = min(first + (int)blockIdx.z * share, blocks);
+    walk.r0 = min(first + (int)blockIdx.y * share, blocks);
     walk.r1 = min(walk.r0 + share, blocks);
-    s = blockIdx.z;
+    s = blockIdx.y;
     if (walk.r0 >= walk.r1) {  // (only one of several groups)
       float* to = sp.partial + (((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len;
       for (int t = walk.u0 + tid; t < walk.u1; t += kThreadsT) to[t] = 0.f;
@@ -354,7 +427,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   walk.n = req.n;
   const int RC0 = min(ROWS, req.n * p.G - walk.r0 * ROWS);  // rows of the first block
   auto vec_of = [&](int rr) { return (int64_t)(req.row0 + token_at(p, rr)) * p.Hq + g * p.G + row_at(p, rr).head; };
-  if (!COLS) {
+  if (!COLS && sp.per_head == 0) {
     const int U = max(walk.last_of(walk.r0), 0);
     walk.u1 = (int)min((int64_t)walk.u0 + sp.stat_part, (int64_t)U);
     if (walk.u0 >= walk.u1) {
@@ -365,7 +438,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   }
   // row tiles in use; one alone only where there is no second row block (D = 256: always one)
   const int nq = __shfl_sync(0xffffffffu, C::kNQ == 2 && (walk.r1 - walk.r0 > 1 || RC0 > kM) ? 2 : 1, 0);
-  const bool gather = COLS && (nq == 2 || walk.r1 - walk.r0 > 1);  // sums of several row tiles meet in `acc`
+  // sums of several row tiles meet in `acc` (in shares of any length: each has its place in `partial`)
+  const bool gather = COLS && sp.per_head == 0 && (nq == 2 || walk.r1 - walk.r0 > 1);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) mbar_init(&mt.k_empty[i], nq);
@@ -437,7 +511,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
         const bool live = tid < RC;
         mt.hi[tid] = live ? max(walk.base + token_at(p, row0 + tid) + 1, 0) : 0;
         if (COLS) {
-          const Norm n = live ? join_norm(p.ml, plane, vec_of(row0 + tid), p.S) : Norm{0.f, 0.f};
+          const Norm n = live ? join_norm(p.ml, plane, vec_of(row0 + tid), S) : Norm{0.f, 0.f};
           mt.m[tid] = -n.m;
           mt.inv[tid] = n.inv;
           mt.ml[tid] = folded(n);
@@ -478,7 +552,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
         const bool masked = v0 + kT > hi_min || (!COLS && (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu);
         const int t = v0 + 32 * wl + lane;              // columns: this thread's position
         float sum = 0.f;
-#pragma unroll 1
+#pragma unroll
         for (int h = 0; h < kT / kCols; ++h) {
           uint32_t x[kCols];
           tmem_ld32(tS + kCols * h, x);
@@ -545,8 +619,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
             acc[tile * kScoreAccTokens + t - walk.u0] += sum;
           else if (sp.groups == 1)
             write_score(sp, b, g, t, walk.base, sum);
-          else
-            sp.partial[(((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len + t] = sum;
+          else {
+            const int64_t row_len = (int64_t)p.B * p.Hkv * p.max_kv_len;
+            float* to = sp.partial + ((int64_t)b * p.Hkv + g) * p.max_kv_len + t;
+            to[(sp.per_head > 0 ? tile : s) * row_len] = sum;
+            if (sp.per_head > 0 && nq == 1) to[row_len] = 0.f;  // (a request without a second row tile)
+          }
         }
       }
       ktb += n_tiles;
@@ -569,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
         }
       }
     }
-    if (COLS && !gather && sp.groups > 1) {  // positions that none of the block's rows sees
+    if (COLS && !gather && sp.groups > 1 && sp.per_head == 0) {  // positions that none of the block's rows sees
       float* to = sp.partial + (((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len;
       for (int t = walk.u0 + walk.tiles_of(walk.r0) * kT + tid; t < walk.u1; t += kEpilogue) to[t] = 0.f;
     }
@@ -631,10 +709,16 @@ cudaError_t run(const fp8kv_cache_score_plan_t*, const ScoreParams& p, cudaStrea
   });
   if (e != cudaSuccess) return e;
   const int pairs = p.c.B * p.c.Hkv;
-  rows<<<dim3(p.c.row_tiles * p.c.Hkv, p.c.S), kThreadsT, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int parts = (int)(((int64_t)p.c.max_kv_len + p.col_part - 1) / p.col_part);
-  cols<<<dim3(pairs, parts, p.groups), kThreadsT, smem, st>>>(p);
+  if (p.per_head > 0) {
+    rows<<<dim3(p.per_head * p.c.Hkv), kThreadsT, smem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cols<<<dim3(p.per_head * p.c.Hkv), kThreadsT, smem, st>>>(p);
+  } else {
+    rows<<<dim3(p.c.row_tiles * p.c.Hkv, p.c.S), kThreadsT, smem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int parts = (int)(((int64_t)p.c.max_kv_len + p.col_part - 1) / p.col_part);
+    cols<<<dim3(pairs, p.groups, parts), kThreadsT, smem, st>>>(p);
+  }
   if ((e = cudaGetLastError()) != cudaSuccess || p.groups == 1) return e;
   score_sum<<<dim3((unsigned)((p.c.max_kv_len + kSumThreads - 1) / kSumThreads), pairs), kSumThreads, 0, st>>>(p);
   return cudaGetLastError();

@@ -644,11 +644,12 @@ typedef struct {
   int32_t stat_part;       /* tile: positions of a partition of the rows' sums */
   int32_t col_part;        /* tile: positions of a CTA of the column pass */
   int32_t row_groups;      /* tile: shares of the row blocks in the column pass */
+  int32_t per_head;        /* tile, above 0: CTAs per KV head, which find their shares from the lengths */
   int32_t num_sms;
   int64_t partial_offset;  /* workspace: logits [B][Hkv][max_kv_len][vectors], or sums [row_groups][B][Hkv][max_kv_len] */
   int64_t ml_offset;       /* workspace: FP32 (max, sum) pairs [num_splits][total_q][Hq] */
   int64_t workspace_bytes; /* minimum workspace size */
-  int32_t reserved[6];
+  int32_t reserved[7];
 } fp8kv_cache_score_plan_t;
 
 typedef struct {
