@@ -54,10 +54,10 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
   P.partial_offset = 256;
   int64_t floats;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
-    // partitions of one length: some four CTAs per SM, of 64 to 1024 positions
-    int64_t part = std::min<int64_t>(1024, std::max<int64_t>(64, ceil_div(pairs * len, 4 * sms)));
+    // partitions of one length: some four CTAs per SM, of 128 to 2048 positions
+    int64_t part = std::min<int64_t>(2048, std::max<int64_t>(128, ceil_div(pairs * len, 4 * sms)));
     if (d->num_splits) part = ceil_div(len, d->num_splits);
-    part = align_up(std::max(part, ceil_div(len, 65535)), 64);
+    part = align_up(std::max(part, ceil_div(len, 65535)), 128);
     P.num_splits = (int32_t)ceil_div(len, part);
     P.vectors = score_vectors(rows);
     P.row_groups = 1;

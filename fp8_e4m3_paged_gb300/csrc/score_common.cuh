@@ -19,13 +19,21 @@ struct Norm {
 __device__ __forceinline__ Norm join_norm(const float2* ml, int64_t plane, int64_t vec, int S, int lane = 0,
                                           int lanes = 1) {
   float M = kNoMax, L = 0.f;
-  for (int s = lane; s < S; s += lanes) M = fmaxf(M, ml[s * plane + vec].x);
-  for (int o = lanes / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   for (int s = lane; s < S; s += lanes) {
     const float2 y = ml[s * plane + vec];
-    if (y.y != 0.f) L = fmaf(part_weight(y.x, M), y.y, L);
+    if (y.y == 0.f) continue;
+    const float top = fmaxf(M, y.x);
+    L = (L == 0.f ? 0.f : L * part_weight(M, top)) + y.y * part_weight(y.x, top);
+    M = top;
   }
-  for (int o = lanes / 2; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
+  for (int o = lanes / 2; o > 0; o /= 2) {
+    const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, L, o);
+    const float top = fmaxf(M, m);
+    // (the same order of the two in both lanes: the sum is the same)
+    const float a = L == 0.f ? 0.f : L * part_weight(M, top), b = l == 0.f ? 0.f : l * part_weight(m, top);
+    L = a + b;
+    M = top;
+  }
   return {M == kNoMax ? 0.f : M, L == 0.f ? 0.f : 1.f / L};
 }
 

@@ -8,7 +8,9 @@
 // logits' weights up per position.  Reading K a second time instead would double the bytes.
 //
 // First kernel: one CTA of four warps per (request, KV head, partition); each warp walks
-// blocks of 16 positions on its own, rows requested by cp.async into its ring.
+// blocks of 32 positions on its own, rows requested by cp.async into its ring, a lane for each row's
+// place.  (Blocks of 16, one chain of products and exponentials at a time, took 2400 cycles each with
+// four warps on a scheduler: 60 us for 64 requests of 4000 positions.)
 // S^T[16 tokens x 8 vectors] = K . Q^T by mma.sync m16n8k16: lane (n = lane/4, c = lane%4) of
 // the A operand takes the 16-byte pieces c, c + 4, ... of rows n and n + 8, a word of each decodes to
 // one fragment, and Q's B fragments are laid out in that order of d.
@@ -29,9 +31,11 @@ namespace {
 
 constexpr int kWarps = kChunkStreamWarps;
 constexpr int kThreadsS = 32 * kWarps;
-constexpr int kBlk = kChunkStreamBlock;
+constexpr int kBlk = 32;                            // positions of a warp's block
+constexpr int kSub = kBlk / 16;                     // ... in MMAs of 16
 constexpr int kFoldThreads = 256;
-constexpr int kFoldEach = 4;
+// positions of a thread of the second kernel
+constexpr int fold_each(int vectors) { return vectors == 16 ? 2 : 4; }
 
 template <int D, int NQ>
 struct Cfg {
@@ -39,14 +43,14 @@ struct Cfg {
   static constexpr int kQStride = D + 8;             // fp16 elements (padding: fragment loads without conflicts)
   static constexpr bool kQRegs = D * NQ <= 256;      // Q's fragments stay in registers
   static constexpr int kCtas = D == 256 ? 3 : 4;     // resident per SM
-  static constexpr int kStages = D == 64 ? 8 : D == 128 ? 6 : 4;
+  static constexpr int kStages = D == 64 ? 5 : D == 128 ? 3 : 2;
   static constexpr int kCh = D / 16;                 // 16-byte pieces of a row, lanes that copy it
   static constexpr int kRowsIt = 32 / kCh;           // rows that the warp copies at a time
   static constexpr int kRowBytes = kBlk * D;         // a block's rows
   static constexpr int kRing = kStages * kRowBytes;  // per warp
   static constexpr int kOffQ = kWarps * kRing;
   static constexpr int kOffRed = kOffQ + 8 * NQ * kQStride * 2;  // per warp: row offsets, then maxima and sums
-  static constexpr int kSmem = kOffRed + (2 * kWarps + 1) * 16 * 4;
+  static constexpr int kSmem = kOffRed + kWarps * kBlk * 8 + 16 * 4;
 };
 
 template <int D, int FMT, int DT, int NQ>
@@ -57,8 +61,8 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   const ChunkParams& p = sp.c;
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
-  float* sML = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp]: 16 maxima, then 16 sums
-  float* sBack = sML + 2 * kWarps * 16;                      // [16] inverse row scales
+  float* sML = reinterpret_cast<float*>(smem + C::kOffRed);  // [warp][64]: 16 maxima, then 16 sums
+  float* sBack = sML + kWarps * kBlk * 2;                    // [16] inverse row scales
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;
@@ -82,14 +86,14 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   // place are zeros, and masked)
   const uint8_t* kbase = p.k_cache + g * p.ksh + (lane % C::kCh) * 16;
   uint8_t* ring = smem + warp * C::kRing;
-  int64_t* place = reinterpret_cast<int64_t*>(sML + warp * 32);
-  static_assert(kBlk * 8 == 32 * 4, "one in place of the other");
+  int64_t* place = reinterpret_cast<int64_t*>(sML + warp * 64);
+  static_assert(kBlk * 8 == 64 * 4, "one in place of the other");
   struct Ask {
     int blk, slot;
     bool in;
   };
   auto ask = [&](int t) {
-    const int v = t + (lane & (kBlk - 1));
+    const int v = t + lane;
     Ask a = {-1, 0, v < u1};
     if (a.in) {
       const int page = div_page(v, p.page_size, p.page_div);
@@ -102,8 +106,8 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   auto request = [&](const Ask& a, int st) {
     const bool ok = a.blk >= 0 && a.blk < p.num_kv_blocks;
     if (a.in && !ok) set_status(p.status, FP8KV_STATUS_BAD_BLOCK);
-    const uint32_t rows = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
-    if (lane < kBlk) place[lane] = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
+    const uint32_t rows = __ballot_sync(0xffffffffu, ok);
+    place[lane] = ok ? a.blk * p.ksb + (int64_t)a.slot * p.kst : 0;
     __syncwarp();
     uint8_t* dst = ring + st * C::kRowBytes;
 #pragma unroll
@@ -212,58 +216,72 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
     const uint32_t valid = there[0];
 #pragma unroll
     for (int i = 0; i + 1 < ST; ++i) there[i] = there[i + 1];
-    float sc[NQ][2][4];
+    float sc[NQ][kSub][2][4];
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) sc[n][k][0] = sc[n][k][1] = sc[n][k][2] = sc[n][k][3] = 0.f;
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sc[n][u][k][0] = sc[n][u][k][1] = sc[n][u][k][2] = sc[n][u][k][3] = 0.f;
 #pragma unroll
     for (int i = 0; i < C::kKP; ++i) {
-      const uint8_t* at = krows + rq * D + (((c + 4 * i) ^ swz(rq)) * 16);
-      const uint4 k0 = *reinterpret_cast<const uint4*>(at);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(at + 8 * D);
+      uint4 k0[kSub], k1[kSub];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t a[4];
-        fp8x4_to_f16<FMT>(word(k0, w), a[0], a[2]);
-        fp8x4_to_f16<FMT>(word(k1, w), a[1], a[3]);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          const uint2 q = C::kQRegs ? qb[n][C::kQRegs ? i * 4 + w : 0] : q_frag(n, i, w);
-          mma16816(sc[n][w & 1], a, q.x, q.y);
-        }
+      for (int u = 0; u < kSub; ++u) {
+        const uint8_t* at = krows + (16 * u + rq) * D + (((c + 4 * i) ^ swz(rq)) * 16);
+        k0[u] = *reinterpret_cast<const uint4*>(at);
+        k1[u] = *reinterpret_cast<const uint4*>(at + 8 * D);
       }
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+          uint32_t a[4];
+          fp8x4_to_f16<FMT>(word(k0[u], w), a[0], a[2]);
+          fp8x4_to_f16<FMT>(word(k1[u], w), a[1], a[3]);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            const uint2 q = C::kQRegs ? qb[n][C::kQRegs ? i * 4 + w : 0] : q_frag(n, i, w);
+            mma16816(sc[n][u][w & 1], a, q.x, q.y);
+          }
+        }
     }
-    float x[NQ][2][2];
+    float x[NQ][2 * kSub][2];  // [.][16-row half][.]
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2 * kSub; ++h)
 #pragma unroll
         for (int e = 0; e < 2; ++e)  // (rounded: the maximum is of these numbers, and they are what is kept)
-          x[n][h][e] = __fmul_rn(sc[n][0][2 * h + e] + sc[n][1][2 * h + e], cq[n][e]);
-    if (valid != 0xFFFFu || t + kBlk > hi_min) {
+          x[n][h][e] = __fmul_rn(sc[n][h / 2][0][2 * (h & 1) + e] + sc[n][h / 2][1][2 * (h & 1) + e], cq[n][e]);
+    if (valid != 0xFFFFFFFFu || t + kBlk > hi_min) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2 * kSub; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int k = rq + 8 * h;
             if (!((valid >> k) & 1u) || t + k >= hi[n][e]) x[n][h][e] = -INFINITY;
           }
     }
+    auto top = [&](int n, int e) {
+      float y = x[n][0][e];
+#pragma unroll
+      for (int h = 1; h < 2 * kSub; ++h) y = fmaxf(y, x[n][h][e]);
+      return y;
+    };
     bool moves = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) moves |= fmaxf(x[n][0][e], x[n][1][e]) - m[n][e] > kChunkTau;
+      for (int e = 0; e < 2; ++e) moves |= top(n, e) - m[n][e] > kChunkTau;
     if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(x[n][0][e], x[n][1][e]);
+          float y = top(n, e);
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
@@ -277,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
     for (int n = 0; n < NQ; ++n) {
       const float s0 = m[n][0] == kNoMax ? 0.f : m[n][0], s1 = m[n][1] == kNoMax ? 0.f : m[n][1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2 * kSub; ++h) {
         l[n][0] += fast_exp2(x[n][h][0] - s0);
         l[n][1] += fast_exp2(x[n][h][1] - s1);
         const int tt = t + rq + 8 * h;
@@ -299,34 +317,35 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
       y += __shfl_xor_sync(0xffffffffu, y, 8);
       y += __shfl_xor_sync(0xffffffffu, y, 16);
       if (rq == 0) {
-        sML[warp * 32 + r] = m[n][e];
-        sML[warp * 32 + 16 + r] = y;
+        sML[warp * 64 + r] = m[n][e];
+        sML[warp * 64 + 16 + r] = y;
       }
     }
   __syncthreads();
   if (tid < RC) {
     float M = kNoMax, L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sML[w * 32 + tid]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sML[w * 64 + tid]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float mw = sML[w * 32 + tid], lw = sML[w * 32 + 16 + tid];
+      const float mw = sML[w * 64 + tid], lw = sML[w * 64 + 16 + tid];
       if (lw != 0.f) L = fmaf(part_weight(mw, M), lw, L);
     }
     p.ml[s * plane + vec_of(tid)] = make_float2(M, L);
   }
 }
 
-// Second kernel: kFoldEach positions per thread.
+// Second kernel: a few positions per thread.
 template <int RV>
 __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant__ ScoreParams sp) {
+  constexpr int EACH = fold_each(RV);
   const ChunkParams& p = sp.c;
   __shared__ Norm norm[16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = div_hkv(p, blockIdx.y), g = blockIdx.y - b * p.Hkv;
   const ChunkRequest req = chunk_request(p, b);
   const int RC = min(RV, req.n * p.G), base = req.kv - req.n;
-  const int t0 = (int)min((int64_t)blockIdx.x * kFoldThreads * kFoldEach, (int64_t)req.kv);
+  const int t0 = (int)min((int64_t)blockIdx.x * kFoldThreads * EACH, (int64_t)req.kv);
   if (RC <= 0 || t0 >= req.kv) return;
   wait_for_previous_kernel();
   const int S = (req.kv - 1) / sp.stat_part + 1;
@@ -339,15 +358,15 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
     if (lane == 0) norm[r] = n;
   }
   const float4* from = reinterpret_cast<const float4*>(sp.logits + ((int64_t)b * p.Hkv + g) * p.max_kv_len * RV);
-  float4 y[kFoldEach][RV / 4];
+  float4 y[EACH][RV / 4];
 #pragma unroll
-  for (int j = 0; j < kFoldEach; ++j)
+  for (int j = 0; j < EACH; ++j)
 #pragma unroll
     for (int i = 0; i < RV / 4; ++i)  // (past the last position: read again, not used)
       y[j][i] = __ldcg(from + (int64_t)min(t0 + j * kFoldThreads + tid, req.kv - 1) * (RV / 4) + i);
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kFoldEach; ++j) {
+  for (int j = 0; j < EACH; ++j) {
     const int t = t0 + j * kFoldThreads + tid;
     if (t >= req.kv) return;
     float sum = 0.f;
@@ -375,7 +394,8 @@ cudaError_t run(const ScoreParams& p, cudaStream_t st) {
   const unsigned pairs = (unsigned)(p.c.B * p.c.Hkv);
   fn<<<dim3(pairs, p.c.S), kThreadsS, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const dim3 grid((unsigned)((p.c.max_kv_len + kFoldThreads * kFoldEach - 1) / (kFoldThreads * kFoldEach)), pairs);
+  const int each = kFoldThreads * fold_each(p.vectors);
+  const dim3 grid((unsigned)((p.c.max_kv_len + each - 1) / each), pairs);
   return launch_dependent(p.vectors == 4 ? score_fold<4> : p.vectors == 8 ? score_fold<8> : score_fold<16>, grid,
                           kFoldThreads, 0, st, p);
 }

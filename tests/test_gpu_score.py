@@ -299,7 +299,7 @@ def test_long_context(requests, group, kernel):
 @pytest.mark.parametrize("d,dtype", [(128, torch.float16), (256, torch.bfloat16), (64, torch.float16)])
 def test_long_prompt(d, dtype):
     """Many row blocks, and positions over several CTAs and groups."""
-    c = Case([(2600, 4700)], Hq=2, Hkv=1, D=d, dtype=dtype)
+    c = Case([(2600, 4700)], Hq=4, Hkv=2, D=d, dtype=dtype)
     ref = reference(c)
     for over in (dict(), dict(num_sms=1), dict(num_splits=2)):
         r = Run(c, 2, **over)
