@@ -159,7 +159,7 @@ class ChunkPlan(ctypes.Structure):
         "num_splits", "row_tiles", "num_sms")] + [
         ("partial_offset", ctypes.c_int64), ("ml_offset", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
         ("min_splits", ctypes.c_int32), ("tree", ctypes.c_int32), ("max_part", ctypes.c_int32),
-        ("reserved", ctypes.c_int32 * 5),
+        ("per_head", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4),
     ]
 
 

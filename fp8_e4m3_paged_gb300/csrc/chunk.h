@@ -23,6 +23,7 @@ constexpr int kChunkStreamWarps = 4;
 inline int64_t chunk_max_part(int32_t kernel) {
   return kernel == FP8KV_CHUNK_STREAM ? kChunkStreamWarps * kChunkMaxSum / 2 : kChunkMaxSum;
 }
+constexpr int kShareMax = 128;             // requests that a CTA finds its share among (share_of)
 constexpr int kTreeNodesMax = 1024;         // nodes of one request's tree
 inline int chunk_tile_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }  // query vectors per CTA
 
@@ -56,6 +57,8 @@ struct ChunkParams {
   const uint32_t* mask;    // [total_q][mask_stride] bit j % 32 of word j / 32: the row sees new token j
   int64_t mask_stride;     // words
   const int32_t* depth;    // [total_q] (windows only)
+  int32_t per_head;        // above 0: CTAs per KV head, which find their shares from the lengths (share_of)
+  int32_t* share;          // where they leave the partitions' length for the join
 };
 
 // Whether the partitions form a cluster that joins them itself: only where all of them have

@@ -150,15 +150,26 @@ int make_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan, bool tree) {
   // planned for 4000: 93 us; planned for 2^20: 102, and 162 were all 16 partitions used.)
   P.max_part = (int32_t)chunk_max_part(P.kernel);
   if (tree && P.kernel == FP8KV_CHUNK_TILE && P.batch > 1 && d->num_splits == 0) {
-    // Trees of several requests: partitions of one length, so that a long context beside short
-    // ones becomes as many CTAs as it takes (16 trees on 100 to 8000 positions, one CTA for each row block
-    // and KV head: 143 us, of which the longest CTA 140).
-    const int64_t tiles = ceil_div(seen, unit);
-    const int64_t part = std::min<int64_t>(32, std::max<int64_t>(8, units * tiles / (8 * sms)));
-    P.max_part = (int32_t)std::min<int64_t>(P.max_part, part * unit);
-    P.min_splits = 1;
+    // Trees of several requests, a CTA for each row block and KV head: the longest of 16 contexts of 100 to
+    // 8000 positions took 140 of 143 us.  One row block per request: shares by the lengths on the device, of a
+    // wave of CTAs and half as many more as there are requests, whose last partitions are
+    // short (that batch in us with none more 89, half 76, as many 83; partitions of one length chosen here 82).
+    // Else partitions of one length, so that a long context becomes as many CTAs as it takes.
+    const int64_t tiles = ceil_div(seen, unit), per_head = sms / P.num_kv_heads + (P.batch - 1) / 2;
+    // (the longest share that the lengths can lead to, lengthened for requests of one row tile)
+    const int64_t longest = per_head > P.batch ? ceil_div(seen * P.batch, per_head - P.batch) : seen;
+    if (rows <= chunk_tile_rows(P.head_dim) && P.batch <= std::min<int64_t>(per_head, kShareMax) &&
+        std::min(seen, 2 * longest + 2 * unit) <= P.max_part) {
+      P.per_head = (int32_t)per_head;
+      S = std::max<int64_t>(1, std::min(tiles, per_head));
+      P.min_splits = (int32_t)S;
+    } else {
+      const int64_t part = std::min<int64_t>(32, std::max<int64_t>(8, units * tiles / (8 * sms)));
+      P.max_part = (int32_t)std::min<int64_t>(P.max_part, part * unit);
+      P.min_splits = 1;
+    }
   }
-  S = std::max(S, ceil_div(seen, P.max_part));
+  if (P.per_head == 0) S = std::max(S, ceil_div(seen, P.max_part));
   // grid.x
   if ((P.kernel == FP8KV_CHUNK_STREAM ? pairs : (int64_t)P.row_tiles * P.num_kv_heads) > 0x7fffffff)
     return FP8KV_EUNSUPPORTED;
@@ -207,6 +218,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   p->S = plan->num_splits;
   p->parts = plan->min_splits;
   p->max_part = plan->max_part;
+  p->per_head = plan->per_head;
   p->page_size = plan->page_size;
   auto inverse = [](int32_t n) { return n >= 2 ? ~0ull / (uint64_t)n + 1 : 0ull; };
   p->page_div = inverse(plan->page_size);
@@ -244,6 +256,7 @@ int build_chunk(const fp8kv_chunk_plan_t* plan, const fp8kv_chunk_args* a, Chunk
   p->v_scale_dev = a->v_scale_dev;
   char* ws = reinterpret_cast<char*>(a->workspace);
   p->status = reinterpret_cast<unsigned int*>(ws);
+  p->share = reinterpret_cast<int32_t*>(ws) + 1;
   p->partial = reinterpret_cast<float*>(ws + plan->partial_offset);
   p->ml = reinterpret_cast<float2*>(ws + plan->ml_offset);
   return FP8KV_OK;

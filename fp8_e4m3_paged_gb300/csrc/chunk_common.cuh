@@ -166,6 +166,13 @@ __device__ __forceinline__ typename RowOfTree<TREE>::type chunk_row(const ChunkP
   }
 }
 
+// Tiles of a partition where CTAs find their shares (share_of), from the length T for requests of two
+// row tiles.
+template <bool TREE>
+__device__ __forceinline__ int share_tiles(int T, bool light) {
+  return TREE && light ? (7 * T + 3) / 4 : T;
+}
+
 // Physical place of a position: false when its block is out of range.
 __device__ __forceinline__ bool chunk_place(const ChunkParams& p, int b, int pos, int64_t& blk, int& slot) {
   const int page = div_page(pos, p.page_size, p.page_div);

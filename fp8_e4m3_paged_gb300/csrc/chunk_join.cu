@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
         if (TREE && here) {
           // (the kernels round partitions up to whole steps: no fewer than these)
           const int U = chunk_span<true>(p, r, 0, 0).U;
-          const int per = max(1, min((U + p.parts - 1) / p.parts, p.max_part));
+          int per = max(1, min((U + p.parts - 1) / p.parts, p.max_part));
+          if (p.per_head > 0) per = share_tiles<true>(*p.share, r.n * p.G <= kChunkTileTokens) * kChunkTileTokens;
           S = min(p.S, max(1, (U + per - 1) / per));
         }
       }

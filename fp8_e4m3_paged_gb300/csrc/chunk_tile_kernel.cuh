@@ -251,10 +251,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   // (broadcast: known to be the same in all lanes, so that branches are uniform and a
   // UMMA's operands stay in uniform registers: 955 us became 922)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int g = blockIdx.x % p.Hkv, tile = blockIdx.x / p.Hkv, s = blockIdx.y;
+  const int g = blockIdx.x % p.Hkv, tile = blockIdx.x / p.Hkv;
+  int s = blockIdx.y, share_len = 0;
 
   TileWork work;
-  if (!locate(p, ROWS, tile, lane, work)) return;
+  if (TREE && p.per_head > 0) {
+    Share share;
+    const bool found = share_of<true>(p, p.per_head, tile, lane, share);
+    // (the join derives every request's partitions from the length for requests of two row tiles)
+    if (blockIdx.x == 0 && tid == 0) *p.share = share.base;
+    if (!found) return;
+    work = {share.b, 0};
+    s = share.s;
+    share_len = share.T * kT;
+  } else if (!locate(p, ROWS, tile, lane, work)) {
+    return;
+  }
   const int b = work.b;
   const ChunkRequest req = chunk_request(p, b);
   const int RC = min(ROWS, req.n * p.G - work.row0);
@@ -267,6 +279,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   const ChunkSpan span = chunk_span<TREE>(p, req, work.row0 / p.G, (work.row0 + RC - 1) / p.G);
   int per = min((span.U + p.parts - 1) / p.parts, p.max_part);
   per = (per + kT - 1) / kT * kT;
+  if (TREE && p.per_head > 0) per = share_len;
   const int u0 = (int)min((int64_t)s * per, (int64_t)span.U), u1 = min(span.U, u0 + per);
   if (u0 >= u1) {  // nothing to see here: an empty partition, or rows before position 0
     if (p.S > 1) {
@@ -695,7 +708,8 @@ cudaError_t run(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStream
   static DeviceOnce once;
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  fn<<<dim3(p.row_tiles * p.Hkv, p.S), kTileThreads, smem, st>>>(p);
+  const dim3 grid = TREE && p.per_head > 0 ? dim3(p.per_head * p.Hkv) : dim3(p.row_tiles * p.Hkv, p.S);
+  fn<<<grid, kTileThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 

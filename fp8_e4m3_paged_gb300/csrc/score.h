@@ -6,7 +6,6 @@
 namespace fp8kv {
 
 constexpr int kScoreStreamRows = 16;    // most query vectors per KV head of the streaming kernel
-constexpr int kScoreShareRequests = 128; // requests that a CTA of the tile kernel finds its share among
 constexpr int kScoreAccTokens = 2048;   // positions of a CTA that adds up several row blocks
 
 // Vectors that the streaming kernel keeps the logits of, per position: 4, 8 or 16.

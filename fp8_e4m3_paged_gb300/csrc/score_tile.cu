@@ -39,7 +39,6 @@ constexpr int kEpilogue = kGroups * 128;         // threads
 constexpr int kTeams = 2;                        // of four decoder warps: every other K tile each
 constexpr int kThreadsT = kEpilogue + kTeams * 128;
 constexpr int kMetaHead = 12288;
-constexpr int kShareRequests = kScoreShareRequests / 32;
 constexpr int kCols = 32;                        // columns in registers
 
 template <int D>
@@ -83,60 +82,6 @@ struct Walk {
   }
   __device__ __forceinline__ int tiles_of(int rb) const { return (min(u1, last_of(rb)) - u0 + kT - 1) / kT; }
 };
-
-// A CTA's share where every request is one row block: the partitions' length T (tiles) is the least with
-// which all requests' partitions fit the `per_head` CTAs of a KV head, so that one wave of CTAs
-// has nearly equal work whatever the lengths are, and no CTA's start (10 us, and 17 in a further
-// wave) is paid twice on an SM.  (Four requests of 8000 to 60000 positions: 133 us with one length
-// chosen for the longest.)  By a whole warp; at most 32 kShareRequests requests.
-struct Share {
-  int b, s, T, parts;  // request, partition of it, tiles of a partition, partitions of the request
-};
-__device__ __forceinline__ bool share_of(const ChunkParams& p, int per_head, int idx, int lane, Share& out) {
-  int t[kShareRequests], most = 1;
-#pragma unroll
-  for (int i = 0; i < kShareRequests; ++i) {
-    const int b = lane + 32 * i;
-    t[i] = 0;
-    if (b < p.B) {
-      const ChunkRequest r = chunk_request(p, b);
-      if (r.bad && blockIdx.x == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-      if (r.n > 0) t[i] = (r.kv + kT - 1) / kT;
-    }
-    most = max(most, t[i]);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  int lo = 1, hi = most;  // (as many CTAs as requests: with T = most they fit)
-  while (lo < hi) {
-    const int T = (lo + hi) >> 1;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kShareRequests; ++i) n += (t[i] + T - 1) / T;
-    if (__reduce_add_sync(0xffffffffu, n) <= (unsigned)per_head)
-      hi = T;
-    else
-      lo = T + 1;
-  }
-  bool found = false;
-#pragma unroll
-  for (int i = 0; i < kShareRequests; ++i) {
-    const int mine = (t[i] + lo - 1) / lo;
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t here = __ballot_sync(0xffffffffu, upto > idx && upto - mine <= idx);
-    if (here && !found) {
-      found = true;
-      const int l = __ffs(here) - 1;
-      out = {l + 32 * i, idx - __shfl_sync(0xffffffffu, upto - mine, l), lo, __shfl_sync(0xffffffffu, mine, l)};
-    }
-    idx -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return found;
-}
 
 // Decoders: every other K tile of the walk, in order.  A tile costs its warps some 250 instructions in
 // a chain (the copies' completion, the stage, the conversions, the next copies and block ids), one
@@ -382,14 +327,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   if (sp.per_head > 0) {
     g = blockIdx.x % p.Hkv;
     Share share;
-    if (!share_of(p, sp.per_head, blockIdx.x / p.Hkv, lane, share)) return;
+    if (!share_of<false>(p, sp.per_head, blockIdx.x / p.Hkv, lane, share)) return;
     b = share.b;
     s = share.s;
     S = share.parts;
     req = chunk_request(p, b);
     walk.r0 = 0;
     walk.r1 = 1;
-    walk.u0 = share.s * share.T * kT;
+    walk.u0 = share.s * share.T * kT;  // (no more partitions than tiles)
     walk.u1 = (int)min((int64_t)walk.u0 + (int64_t)share.T * kT, (int64_t)req.kv);
   } else if (COLS) {
     b = div_hkv(p, blockIdx.x);

@@ -94,6 +94,82 @@ __device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int idx, 
   return false;
 }
 
+// A CTA's share where every request is one row block: the partitions' length T (tiles) is the least with
+// which all requests' partitions fit the `per_head` CTAs of a KV head, so that one wave of CTAs
+// has nearly equal work whatever the lengths are, and no CTA's start (10 us of the weights' kernel,
+// and 17 in a further wave) is paid twice on an SM.  By a whole warp; at most kShareMax requests.
+// TREE: a request of up to 128 rows takes a little over half the time for a tile, so its
+// partitions are longer; one without positions has a CTA too (its rows are 0).
+struct Share {
+  int b, s, T, parts;  // request, partition of it, tiles of a partition, partitions of the request
+  int base;            // T of a request whose partitions are not lengthened
+};
+constexpr int kShareRequests = kShareMax / 32;
+template <bool TREE>
+__device__ __forceinline__ bool share_of(const ChunkParams& p, int per_head, int idx, int lane, Share& out) {
+  int t[kShareRequests], most = 1;
+  bool light[kShareRequests];
+#pragma unroll
+  for (int i = 0; i < kShareRequests; ++i) {
+    const int b = lane + 32 * i;
+    t[i] = 0;
+    light[i] = false;
+    if (b < p.B) {
+      const ChunkRequest r = chunk_request(p, b);
+      if (r.bad && blockIdx.x == 0 && threadIdx.x < 32) set_status(p.status, FP8KV_STATUS_BAD_LEN);
+      if (r.n > 0) {
+        t[i] = (chunk_span<TREE>(p, r, 0, r.n - 1).U + kT - 1) / kT;
+        if (TREE) t[i] = max(t[i], 1);
+        light[i] = r.n * p.G <= kM;
+      }
+    }
+    most = max(most, t[i]);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  int lo = 1, hi = most;  // (as many CTAs as requests: with T = most they fit)
+  while (lo < hi) {
+    const int T = (lo + hi) >> 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kShareRequests; ++i) {
+      const int len = share_tiles<TREE>(T, light[i]);
+      n += (t[i] + len - 1) / len;
+    }
+    if (__reduce_add_sync(0xffffffffu, n) <= (unsigned)per_head)
+      hi = T;
+    else
+      lo = T + 1;
+  }
+  // The GPU starts CTAs in the order of their index: whole partitions first, requests' last ones,
+  // which are shorter, behind them.
+  out.base = lo;
+  bool found = false;
+#pragma unroll
+  for (int rest = 0; rest < 2; ++rest)
+#pragma unroll
+    for (int i = 0; i < kShareRequests; ++i) {
+      const int len = share_tiles<TREE>(lo, light[i]), whole = t[i] / len, parts = (t[i] + len - 1) / len;
+      const int mine = rest ? parts - whole : whole;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t here = __ballot_sync(0xffffffffu, upto > idx && upto - mine <= idx);
+      if (here && !found) {
+        found = true;
+        const int l = __ffs(here) - 1;
+        out.b = l + 32 * i;
+        out.s = __shfl_sync(0xffffffffu, (rest ? whole : 0) + idx - (upto - mine), l);
+        out.T = __shfl_sync(0xffffffffu, len, l);
+        out.parts = __shfl_sync(0xffffffffu, parts, l);
+      }
+      idx -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+  return found;
+}
+
 // A decoder lane's 16-byte pieces of one tile (piece lane % kCh of rows it *
 // kRowsIt + lane / kCh of the warp's 32).  The loads are unconditional (rows
 // without a place read the pool's first one): a load under a condition is

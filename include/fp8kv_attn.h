@@ -461,7 +461,8 @@ typedef struct {
   int32_t min_splits;      /* partitions of a context that no FP32 sum limit splits further */
   int32_t tree;            /* 1: made by fp8kv_attn_tree_plan */
   int32_t max_part;        /* positions of a partition at most */
-  int32_t reserved[5];
+  int32_t per_head;        /* trees, above 0: CTAs per KV head, which find their shares from the lengths */
+  int32_t reserved[4];
 } fp8kv_chunk_plan_t;
 
 typedef struct {
