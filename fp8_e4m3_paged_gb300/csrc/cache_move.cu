@@ -9,8 +9,9 @@
 // enough, then, that rows are taken in rounds by k and that a round is written only when all rows up
 // to its end have been read; later rows may be read as early as one likes.  One unit (a request's KV
 // head, K and V) is walked by one CTA, or by one cluster, whose barrier in each round says that
-// all CTAs' reads have arrived (its release and acquire order them before the writes).  To pages
-// of their own no such order is needed.
+// all CTAs' reads have arrived: what cp.async has brought is in shared memory and no later write
+// changes it, so the barrier orders nothing else.  (With release, each round also waited for the
+// writes of the round before it.)  To pages of their own no such order is needed.
 //
 // Rounds of 32 KB per CTA through shared memory: cp.async brings the rows of the next two
 // rounds while this one is written, and the list and the table of the round after them are
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kResident) move_kernel(const __grid_
     if (more) read_table();
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");  // this round's rows
     if (IN_PLACE && geo.ctas > 1)
-      cluster_sync();
+      cluster_sync_relaxed();
     else
       __syncthreads();
     const int slot = round % kStages;
