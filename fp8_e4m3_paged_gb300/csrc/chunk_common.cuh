@@ -170,7 +170,7 @@ __device__ __forceinline__ typename RowOfTree<TREE>::type chunk_row(const ChunkP
 // row tiles.
 template <bool TREE>
 __device__ __forceinline__ int share_tiles(int T, bool light) {
-  return TREE && light ? (7 * T + 3) / 4 : T;
+  return TREE && light ? (5 * T + 3) / 4 : T;
 }
 
 // Physical place of a position: false when its block is out of range.

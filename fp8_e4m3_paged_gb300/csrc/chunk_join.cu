@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "chunk_common.cuh"
+#include "dependent.cuh"
 
 namespace fp8kv {
 namespace {
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
   const int64_t vec = (int64_t)blockIdx.x * (kJoinWarps / ways) + warp / ways;
   const int row = (int)(vec / p.Hq), h = (int)(vec - (int64_t)row * p.Hq);
   bool live = row < p.total_q;
-  int S = p.S;
+  int S = p.S, U = 0, light = 0;
   if (live) {
     // whether some request has the row among its (clamped) new tokens
     live = false;
@@ -44,17 +45,24 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
         const ChunkRequest r = chunk_request(p, i0 + lane);
         here = row >= r.row0 && row - r.row0 < r.n;
         if (TREE && here) {
-          // (the kernels round partitions up to whole steps: no fewer than these)
-          const int U = chunk_span<true>(p, r, 0, 0).U;
-          int per = max(1, min((U + p.parts - 1) / p.parts, p.max_part));
-          if (p.per_head > 0) per = share_tiles<true>(*p.share, r.n * p.G <= kChunkTileTokens) * kChunkTileTokens;
-          S = min(p.S, max(1, (U + per - 1) / per));
+          U = chunk_span<true>(p, r, 0, 0).U;
+          light = r.n * p.G <= kChunkTileTokens;
         }
       }
       const uint32_t who = __ballot_sync(0xffffffffu, here);
       live = who != 0u;
-      if (TREE && live) S = __shfl_sync(0xffffffffu, S, __ffs(who) - 1);
+      if (TREE && live) {
+        U = __shfl_sync(0xffffffffu, U, __ffs(who) - 1);
+        light = __shfl_sync(0xffffffffu, light, __ffs(who) - 1);
+      }
     }
+  }
+  if (TREE) {
+    wait_for_previous_kernel();
+    // (the kernels round partitions up to whole steps: no fewer than these)
+    int per = max(1, min((U + p.parts - 1) / p.parts, p.max_part));
+    if (p.per_head > 0) per = share_tiles<true>(__ldcg(p.share), light) * kChunkTileTokens;
+    S = min(p.S, max(1, (U + per - 1) / per));
   }
   float acc[V] = {};
   float M = kNoMax, L = 0.f;
@@ -141,7 +149,9 @@ cudaError_t launch(const fp8kv_chunk_plan_t* plan, const ChunkParams& p, cudaStr
   int ways = 1;
   while (ways < kJoinWarps && 2 * ways <= p.S && n * ways < (int64_t)plan->num_sms * kJoinWarps) ways *= 2;
   const int64_t per = kJoinWarps / ways;
-  fn<<<(unsigned)((n + per - 1) / per), kJoinThreads, 0, st>>>(p, ways);
+  const dim3 grid((unsigned)((n + per - 1) / per));
+  if (TREE) return launch_dependent(fn, grid, kJoinThreads, 0, st, p, ways);
+  fn<<<grid, kJoinThreads, 0, st>>>(p, ways);
   return cudaGetLastError();
 }
 

@@ -48,6 +48,7 @@
 
 #include "chunk_common.cuh"
 #include "chunk_schedule.h"
+#include "dependent.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
 #include "tile_rows.cuh"
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chunk_tile(const __grid_const
   // (broadcast: known to be the same in all lanes, so that branches are uniform and a
   // UMMA's operands stay in uniform registers: 955 us became 922)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (TREE) let_next_kernel_start();
   const int g = blockIdx.x % p.Hkv, tile = blockIdx.x / p.Hkv;
   int s = blockIdx.y, share_len = 0;
 

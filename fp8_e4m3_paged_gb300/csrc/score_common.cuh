@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "chunk_common.cuh"
+#include "dependent.cuh"
 #include "score.h"
 
 namespace fp8kv {
@@ -35,27 +36,6 @@ __device__ __forceinline__ Norm join_norm(const float2* ml, int64_t plane, int64
     M = top;
   }
   return {M == kNoMax ? 0.f : M, L == 0.f ? 0.f : 1.f / L};
-}
-
-// A kernel whose launch attribute lets it start while the one before it in the stream still runs:
-// nothing of that one's may be read above this line.  The other side lets it start.
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// Launch with that attribute.
-template <class P>
-cudaError_t launch_dependent(void (*fn)(const P), dim3 grid, int threads, int smem, cudaStream_t st, const P& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 // The new weight of position t: what it had gathered, unless it is one of the new tokens, and `got`.

@@ -346,7 +346,10 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
   const ChunkRequest req = chunk_request(p, b);
   const int RC = min(RV, req.n * p.G), base = req.kv - req.n;
   const int t0 = (int)min((int64_t)blockIdx.x * kFoldThreads * EACH, (int64_t)req.kv);
-  if (RC <= 0 || t0 >= req.kv) return;
+  if (RC <= 0 || t0 >= req.kv) {
+    leave_in_order();
+    return;
+  }
   wait_for_previous_kernel();
   const int S = (req.kv - 1) / sp.stat_part + 1;
   for (int r = warp; r < RV; r += kFoldThreads / 32) {

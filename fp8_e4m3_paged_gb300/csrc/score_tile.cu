@@ -320,6 +320,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int64_t plane = (int64_t)p.total_q * p.Hq;
 
+  // (the column pass prepares everything that does not need the rows' sums while the row pass ends)
+  if (!COLS) let_next_kernel_start();
   // ------------------------------------------------------ what this CTA has
   int b, g, s = 0, S = p.S;  // S: partitions of the rows' sums
   Walk walk;
@@ -327,7 +329,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
   if (sp.per_head > 0) {
     g = blockIdx.x % p.Hkv;
     Share share;
-    if (!share_of<false>(p, sp.per_head, blockIdx.x / p.Hkv, lane, share)) return;
+    if (!share_of<false>(p, sp.per_head, blockIdx.x / p.Hkv, lane, share)) {
+      if (COLS) leave_in_order();
+      return;
+    }
     b = share.b;
     s = share.s;
     S = share.parts;
@@ -342,7 +347,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
     req = chunk_request(p, b);
     walk.u0 = (int)min((int64_t)blockIdx.z * sp.col_part, (int64_t)INT_MAX);  // (the first, longest ones start first)
     walk.u1 = (int)min((int64_t)walk.u0 + sp.col_part, (int64_t)req.kv);
-    if (req.n <= 0 || walk.u0 >= req.kv) return;
+    if (req.n <= 0 || walk.u0 >= req.kv) {
+      leave_in_order();
+      return;
+    }
     // the row blocks that see anything here, and this group's share of them
     const int base = req.kv - req.n, blocks = (req.n * p.G + ROWS - 1) / ROWS;
     const int first = max(0, walk.u0 - base) * p.G / ROWS, share = (blocks - first + sp.groups - 1) / sp.groups;
@@ -352,6 +360,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
     if (walk.r0 >= walk.r1) {  // (only one of several groups)
       float* to = sp.partial + (((int64_t)s * p.B + b) * p.Hkv + g) * p.max_kv_len;
       for (int t = walk.u0 + tid; t < walk.u1; t += kThreadsT) to[t] = 0.f;
+      leave_in_order();
       return;
     }
   } else {
@@ -450,6 +459,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
         load_q<D, DT>(p, mt, smem, req, g, row0, (warp * nq + k) * 8, RC, cf < 0.f ? 0x80008000u : 0u, lane);
       fence_proxy_async_smem();
       named_bar_sync(1, kEpilogue);
+      if (COLS && rb == walk.r0) wait_for_previous_kernel();
       if (tid < nq * kM) {
         // (not 0, so that c * -inf stays -inf; nor NaN: a NaN scale goes into the rows' sums)
         mt.c[tid] = fmaxf(fabsf(cf) * mt.back[tid], 1e-30f);
@@ -657,14 +667,14 @@ cudaError_t run(const fp8kv_cache_score_plan_t*, const ScoreParams& p, cudaStrea
   if (p.per_head > 0) {
     rows<<<dim3(p.per_head * p.c.Hkv), kThreadsT, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cols<<<dim3(p.per_head * p.c.Hkv), kThreadsT, smem, st>>>(p);
+    e = launch_dependent(cols, dim3(p.per_head * p.c.Hkv), kThreadsT, smem, st, p);
   } else {
     rows<<<dim3(p.c.row_tiles * p.c.Hkv, p.c.S), kThreadsT, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int parts = (int)(((int64_t)p.c.max_kv_len + p.col_part - 1) / p.col_part);
-    cols<<<dim3(pairs, p.groups, parts), kThreadsT, smem, st>>>(p);
+    e = launch_dependent(cols, dim3(pairs, p.groups, parts), kThreadsT, smem, st, p);
   }
-  if ((e = cudaGetLastError()) != cudaSuccess || p.groups == 1) return e;
+  if (e != cudaSuccess || p.groups == 1) return e;
   score_sum<<<dim3((unsigned)((p.c.max_kv_len + kSumThreads - 1) / kSumThreads), pairs), kSumThreads, 0, st>>>(p);
   return cudaGetLastError();
 }

@@ -98,8 +98,8 @@ __device__ __forceinline__ bool locate(const ChunkParams& p, int rows, int idx, 
 // which all requests' partitions fit the `per_head` CTAs of a KV head, so that one wave of CTAs
 // has nearly equal work whatever the lengths are, and no CTA's start (10 us of the weights' kernel,
 // and 17 in a further wave) is paid twice on an SM.  By a whole warp; at most kShareMax requests.
-// TREE: a request of up to 128 rows takes a little over half the time for a tile, so its
-// partitions are longer; one without positions has a CTA too (its rows are 0).
+// TREE: a request of up to 128 rows takes less time for a tile, so its partitions are longer by a
+// quarter; one without positions has a CTA too (its rows are 0).
 struct Share {
   int b, s, T, parts;  // request, partition of it, tiles of a partition, partitions of the request
   int base;            // T of a request whose partitions are not lengthened
