@@ -25,8 +25,6 @@
 namespace fp8kv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kClusterMax = 8;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
@@ -34,7 +32,9 @@ constexpr int kAhead = 8;                      // positions of a thread whose lo
 constexpr int kKeys = 49152;                   // keys of a CTA's run that stay in shared memory
 constexpr int kMinRun = 2048;                  // positions per CTA before a list gets a further one
 
+template <int kThreads>
 struct Shared {
+  static constexpr int kWarps = kThreads / 32;
   alignas(16) uint32_t hist[kPasses][kBins];
   uint32_t tie[kWarps], above[kWarps];         // selected ones and equal ones of each warp's run
   uint32_t warp_sum[kWarps];
@@ -51,6 +51,7 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 // The weights of kAhead positions, kThreads apart (past the last one: that again): one head's, or the
 // sums over all heads, one after another.  All loads of a head are in flight together.
+template <int kThreads>
 __device__ __forceinline__ void weights_at(const fp8kv_cache_select_args& a, const float* row, int i, int n,
                                            float (&x)[kAhead]) {
 #pragma unroll
@@ -73,10 +74,12 @@ __device__ __forceinline__ float weight_at(const fp8kv_cache_select_args& a, con
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_constant__ fp8kv_cache_select_args a,
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 3 : 1) select_kernel(const __grid_constant__ fp8kv_cache_select_args a,
                                                              const int ctas) {
   extern __shared__ uint32_t keys[];
-  __shared__ Shared sh;
+  constexpr int kWarps = kThreads / 32;
+  __shared__ Shared<kThreads> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = ctas > 1 ? cluster_rank() : 0;
   const int unit = blockIdx.x / ctas, b = unit / a.lists, l = unit - b * a.lists;
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
       uint32_t k[kAhead];
       if (pass == 0 || !stay) {
         float x[kAhead];
-        weights_at(a, row + t0, i0, n, x);
+        weights_at<kThreads>(a, row + t0, i0, n, x);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           k[j] = key_of(x[j]);
@@ -131,18 +134,20 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
       cluster_sync();
     else
       __syncthreads();
-    // bins from the top: thread tid holds four, from kBins - 1 - 4 tid down
-    constexpr int kEach = kBins / kThreads;
-    static_assert(kEach == 4, "a thread's bins are one load");
+    // bins from the top: a thread holds four, from kBins - 1 - 4 tid down
+    constexpr int kEach = 4;
+    static_assert(kBins <= kEach * kThreads, "a thread's bins are one load");
     uint32_t c[kEach] = {0u, 0u, 0u, 0u};
+    if (kEach * tid < kBins) {
 #pragma unroll 4
-    for (int q = 0; q < ctas; ++q) {
-      const uint4 x = ctas == 1 ? *reinterpret_cast<const uint4*>(hist + kBins - 4 - 4 * tid)
-                                : peer_load4(hist + kBins - 4 - 4 * tid, q);
-      c[0] += x.w;
-      c[1] += x.z;
-      c[2] += x.y;
-      c[3] += x.x;
+      for (int q = 0; q < ctas; ++q) {
+        const uint4 x = ctas == 1 ? *reinterpret_cast<const uint4*>(hist + kBins - kEach - kEach * tid)
+                                  : peer_load4(hist + kBins - kEach - kEach * tid, q);
+        c[0] += x.w;
+        c[1] += x.z;
+        c[2] += x.y;
+        c[3] += x.x;
+      }
     }
     const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t upto = sum;
@@ -214,24 +219,17 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
   if (ctas > 1) cluster_sync();  // peers may still read this CTA's counts
 }
 
-}  // namespace
-
-cudaError_t launch_cache_select(const fp8kv_cache_select_args& a, int sms, cudaStream_t st) {
+template <int kThreads>
+cudaError_t run(const fp8kv_cache_select_args& a, int64_t lists, int ctas, cudaStream_t st) {
   static DeviceOnce once;
-  cudaError_t e = once.run(
-      [] { return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4); });
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
+  });
   if (e != cudaSuccess) return e;
-  // CTAs per list: while the GPU has room for them (three to an SM) and each keeps kMinRun positions
-  const int64_t lists = (int64_t)a.batch * a.lists;
-  int ctas = 1;
-  while (ctas < kClusterMax && lists * ctas * 2 <= 4 * (int64_t)sms && a.max_len / (2 * ctas) >= kMinRun) ctas *= 2;
-  while (ctas < kClusterMax && (a.max_len + ctas - 1) / ctas > kKeys) ctas *= 2;
-  if (lists * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const int run = std::min(kKeys, ((a.max_len + ctas - 1) / ctas + 31) / 32 * 32);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(lists * ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = run * 4;
+  cfg.dynamicSmemBytes = 4 * std::min(kKeys, ((a.max_len + ctas - 1) / ctas + 31) / 32 * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -239,7 +237,21 @@ cudaError_t launch_cache_select(const fp8kv_cache_select_args& a, int sms, cudaS
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, select_kernel, a, ctas);
+  return cudaLaunchKernelEx(&cfg, select_kernel<kThreads>, a, ctas);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_select(const fp8kv_cache_select_args& a, int sms, cudaStream_t st) {
+  // CTAs per list: while the GPU has room for them (three to an SM) and each keeps kMinRun positions
+  const int64_t lists = (int64_t)a.batch * a.lists;
+  int ctas = 1;
+  while (ctas < kClusterMax && lists * ctas * 2 <= 4 * (int64_t)sms && a.max_len / (2 * ctas) >= kMinRun) ctas *= 2;
+  while (ctas < kClusterMax && (a.max_len + ctas - 1) / ctas > kKeys) ctas *= 2;
+  if (lists * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // twice the threads, so twice the loads on their way, where every CTA has an SM and much to read
+  const bool wide = lists * ctas <= sms && a.max_len / ctas >= 4096;
+  return wide ? run<1024>(a, lists, ctas, st) : run<512>(a, lists, ctas, st);
 }
 
 }  // namespace fp8kv
