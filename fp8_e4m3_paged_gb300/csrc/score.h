@@ -5,11 +5,12 @@
 
 namespace fp8kv {
 
-constexpr int kScoreStreamRows = 16;    // most query vectors per KV head of the streaming kernel
+constexpr int kScoreStreamRows = 256;   // most query vectors per KV head of the streaming kernel
+constexpr int kScoreGroupRows = 16;     // ... of one of its CTAs
 constexpr int kScoreAccTokens = 2048;   // positions of a CTA that adds up several row blocks
 
-// Vectors that the streaming kernel keeps the logits of, per position: 4, 8 or 16.
-inline int score_vectors(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+// Vectors that the streaming kernel keeps the logits of, per position: 4, 8 or a multiple of 16.
+inline int score_vectors(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : (int)((rows + 15) / 16 * 16); }
 
 struct ScoreParams {
   ChunkParams c;           // no V, no output; c.S partitions of the rows' sums, c.ml [S][total_q][Hq]

@@ -14,6 +14,10 @@
 
 using namespace fp8kv;
 
+namespace {
+constexpr int64_t kScoreStreamBytes = 56 << 20;
+}
+
 extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cache_score_plan_t* plan) {
   if (!d || !plan) return FP8KV_EINVAL;
   // the chunk attention's checks; its plan is not used further
@@ -48,14 +52,24 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
   P.num_sms = chunk.num_sms;
   const int64_t rows = (int64_t)P.max_q * P.group;  // query vectors per (request, KV head)
   const int64_t len = std::max(P.max_kv_len, 1), sms = P.num_sms;
-  P.kernel = d->kernel != FP8KV_CHUNK_AUTO ? d->kernel
-                                           : rows <= kScoreStreamRows ? FP8KV_CHUNK_STREAM : FP8KV_CHUNK_TILE;
+  P.kernel = d->kernel;
+  if (P.kernel == FP8KV_CHUNK_AUTO) {
+    // Up to 16 query vectors stream K once.  More stream it anew for each 16 and keep all logits, which
+    // pays while that is little, because the tile kernel's two passes take 20 us on the shortest contexts.
+    // us, stream / tile, 8 KV heads x 4, D 128, by the bytes counted here: 32 tokens on 500 (8 MB) 9.8 / 18.5,
+    // 4 x 500 (31 MB) 16.6 / 24.9, 4 x 1000 (63 MB) 27.0 / 26.3, 16 x 500 (125 MB) 44 / 28; 8 tokens on
+    // 4 x 2000 (31 MB) 13.6 / 29.1, 16 x 1000 (63 MB) 20 / 37; 48 requests of 16 tokens on 20 (8 MB) 13 / 48.
+    const int64_t bytes = pairs * len * (8 * rows + ceil_div(rows, kScoreGroupRows) * P.head_dim);
+    const bool stream = rows <= kScoreGroupRows || (rows <= kScoreStreamRows && bytes <= kScoreStreamBytes);
+    P.kernel = stream ? FP8KV_CHUNK_STREAM : FP8KV_CHUNK_TILE;
+  }
   if (P.kernel == FP8KV_CHUNK_STREAM && rows > kScoreStreamRows) return FP8KV_EUNSUPPORTED;
   P.partial_offset = 256;
   int64_t floats;
   if (P.kernel == FP8KV_CHUNK_STREAM) {
     // partitions of one length: some four CTAs per SM, of 128 to 2048 positions
-    int64_t part = std::min<int64_t>(2048, std::max<int64_t>(128, ceil_div(pairs * len, 4 * sms)));
+    const int64_t row_groups = ceil_div(rows, kScoreGroupRows);
+    int64_t part = std::min<int64_t>(2048, std::max<int64_t>(128, ceil_div(pairs * row_groups * len, 4 * sms)));
     if (d->num_splits) part = ceil_div(len, d->num_splits);
     part = align_up(std::max(part, ceil_div(len, 65535)), 128);
     P.num_splits = (int32_t)ceil_div(len, part);

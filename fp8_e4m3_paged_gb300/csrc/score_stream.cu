@@ -1,4 +1,5 @@
-// Gathered weights for few query vectors (at most 16 per KV head: decode steps, short drafts).
+// Gathered weights for few query vectors (decode steps, short drafts: 16 per CTA and KV head), and for more
+// of them on few positions.
 //
 //   x_rt = c q_r . k_t (base 2),  p_rt = 2^(x_rt - M_r) / L_r,  score_t = decay score_t + sum_r p_rt
 //
@@ -70,11 +71,12 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   const int b = div_hkv(p, blockIdx.x), g = blockIdx.x - b * p.Hkv, s = blockIdx.y;
   const ChunkRequest req = chunk_request(p, b);
   if (tid == 0 && req.bad) set_status(p.status, FP8KV_STATUS_BAD_LEN);
-  const int RC = min(R, req.n * p.G);
+  const int row_first = blockIdx.z * kScoreGroupRows;
+  const int RC = min(R, req.n * p.G - row_first);
   if (RC <= 0) return;
   const int64_t plane = (int64_t)p.total_q * p.Hq;
-  auto token_of = [&](int r) { return token_at(p, r); };
-  auto head_of = [&](int r) { return g * p.G + row_at(p, r).head; };
+  auto token_of = [&](int r) { return token_at(p, row_first + r); };
+  auto head_of = [&](int r) { return g * p.G + row_at(p, row_first + r).head; };
   auto vec_of = [&](int r) { return (int64_t)(req.row0 + token_of(r)) * p.Hq + head_of(r); };
   // (partitions of one length, whatever the request's: a batch of 64 between 512 and 16000 positions,
   // whose longest CTAs had 16000, took 160 us)
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
 #pragma unroll
   for (int n = 0; n < NQ; ++n) m[n][0] = m[n][1] = kNoMax, l[n][0] = l[n][1] = 0.f;
   const int RV = sp.vectors;
-  float* keep = sp.logits + ((int64_t)b * p.Hkv + g) * p.max_kv_len * RV + 2 * c;
+  float* keep = sp.logits + ((int64_t)b * p.Hkv + g) * p.max_kv_len * RV + row_first + 2 * c;
   int st = 0;
   for (int t = t_first; t < u1; t += kStep) {
     // the block ST - 1 ahead goes where the block before this one was
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
         l[n][0] += fast_exp2(x[n][h][0] - s0);
         l[n][1] += fast_exp2(x[n][h][1] - s1);
         const int tt = t + rq + 8 * h;
-        if (8 * n + 2 * c < RV && tt < u1)
+        if (row_first + 8 * n + 2 * c < RV && tt < u1)
           *reinterpret_cast<float2*>(keep + (int64_t)tt * RV + 8 * n) = make_float2(x[n][h][0], x[n][h][1]);
       }
     }
@@ -387,6 +389,50 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
   }
 }
 
+// More than 16 vectors: `lanes` neighbouring threads per position (a power of two), 16 vectors each.
+__global__ void __launch_bounds__(kFoldThreads) score_fold_many(const __grid_constant__ ScoreParams sp, const int lanes) {
+  const ChunkParams& p = sp.c;
+  __shared__ Norm norm[kScoreStreamRows];
+  static_assert(kScoreStreamRows == kFoldThreads, "a thread for each vector's sum");
+  const int tid = threadIdx.x, RV = sp.vectors;
+  const int b = div_hkv(p, blockIdx.y), g = blockIdx.y - b * p.Hkv;
+  const ChunkRequest req = chunk_request(p, b);
+  const int RC = min(RV, req.n * p.G), base = req.kv - req.n;
+  const int each = kFoldThreads / lanes, t0 = (int)min((int64_t)blockIdx.x * each, (int64_t)req.kv);
+  if (RC <= 0 || t0 >= req.kv) {
+    leave_in_order();
+    return;
+  }
+  wait_for_previous_kernel();
+  const int t = t0 + tid / lanes, r0 = (tid & (lanes - 1)) * kScoreGroupRows;
+  // (positions past the last one and vectors past RV: read again, not used)
+  const float4* from = reinterpret_cast<const float4*>(
+      sp.logits + (((int64_t)b * p.Hkv + g) * p.max_kv_len + min(t, req.kv - 1)) * RV + min(r0, RV - kScoreGroupRows));
+  float4 y[kScoreGroupRows / 4];
+#pragma unroll
+  for (int i = 0; i < kScoreGroupRows / 4; ++i) y[i] = __ldcg(from + i);
+  Norm mine = {0.f, 0.f};
+  if (tid < RC) {
+    const RowAt at = row_at(p, tid);
+    mine = join_norm(p.ml, (int64_t)p.total_q * p.Hq, (int64_t)(req.row0 + at.token) * p.Hq + g * p.G + at.head,
+                     (req.kv - 1) / sp.stat_part + 1);
+  }
+  norm[tid] = mine;
+  __syncthreads();
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kScoreGroupRows / 4; ++i) {
+    const float z[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + 4 * i + k;
+      if (r < RC && z[k] != -INFINITY) sum = fmaf(fast_exp2(z[k] - norm[r].m), norm[r].inv, sum);
+    }
+  }
+  for (int o = lanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (t < req.kv && r0 == 0) write_score(sp, b, g, t, base, sum);
+}
+
 template <int D, int FMT, int DT, int NQ>
 cudaError_t run(const ScoreParams& p, cudaStream_t st) {
   auto fn = score_logits<D, FMT, DT, NQ>;
@@ -395,8 +441,15 @@ cudaError_t run(const ScoreParams& p, cudaStream_t st) {
   cudaError_t e = once.run([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
   const unsigned pairs = (unsigned)(p.c.B * p.c.Hkv);
-  fn<<<dim3(pairs, p.c.S), kThreadsS, smem, st>>>(p);
+  fn<<<dim3(pairs, p.c.S, (p.vectors + kScoreGroupRows - 1) / kScoreGroupRows), kThreadsS, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.vectors > kScoreGroupRows) {
+    int lanes = 2;
+    while (lanes * kScoreGroupRows < p.vectors) lanes *= 2;
+    const int each = kFoldThreads / lanes;
+    return launch_dependent(score_fold_many, dim3((unsigned)((p.c.max_kv_len + each - 1) / each), pairs), kFoldThreads, 0,
+                            st, p, lanes);
+  }
   const int each = kFoldThreads * fold_each(p.vectors);
   const dim3 grid((unsigned)((p.c.max_kv_len + each - 1) / each), pairs);
   return launch_dependent(p.vectors == 4 ? score_fold<4> : p.vectors == 8 ? score_fold<8> : score_fold<16>, grid,

@@ -638,7 +638,7 @@ typedef struct {
   int32_t batch, total_q, max_q, num_q_heads, num_kv_heads, head_dim, page_size;
   int32_t max_kv_len, max_blocks, num_kv_blocks, dtype, kv_format;
   int32_t group;           /* Hq / Hkv */
-  int32_t kernel;          /* FP8KV_CHUNK_STREAM (logits kept, up to 16 query vectors per KV head) or FP8KV_CHUNK_TILE */
+  int32_t kernel;          /* FP8KV_CHUNK_STREAM (logits kept, up to 256 query vectors per KV head) or FP8KV_CHUNK_TILE */
   int32_t num_splits;      /* partitions of the rows' sums */
   int32_t vectors;         /* stream: logits kept per position */
   int32_t row_tiles;       /* tile: bound of the row blocks of all requests */
@@ -675,7 +675,7 @@ typedef struct {
 } fp8kv_cache_score_args;
 
 /* Validate `d` (as fp8kv_attn_chunk_plan; kernel and num_splits choose likewise) and fill `plan`.
- * A window, more than 65535 pairs of request and KV head, max_kv_len above 2^26, and FP8KV_CHUNK_STREAM with more than 16
+ * A window, more than 65535 pairs of request and KV head, max_kv_len above 2^26, and FP8KV_CHUNK_STREAM with more than 256
  * query vectors per KV head: FP8KV_EUNSUPPORTED. */
 int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cache_score_plan_t* plan);
 int fp8kv_attn_cache_score(const fp8kv_cache_score_plan_t* plan, const fp8kv_cache_score_args* a,

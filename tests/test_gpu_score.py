@@ -134,7 +134,7 @@ def check(got, c, ref, untouched=-7.0):
 
 def kernels(c):
     tile = [(2, 0), (2, 1), (2, 3), (0, 0)]
-    return tile + [(1, 0), (1, 1), (1, 3), (1, 11)] if c.max_q * c.group <= 16 else tile
+    return tile + [(1, 0), (1, 1), (1, 3), (1, 11)] if c.max_q * c.group <= 256 else tile
 
 
 CASES = {
