@@ -40,6 +40,9 @@
  *                       count, grid and workspace size.
  *   fp8kv_attn_split    launches the split kernel (partials into workspace).
  *   fp8kv_attn_combine  launches the combine kernel (workspace -> out).
+ * and, each described where it is declared: the cache write, read, calibration, the merge of
+ * context shards, the grouped planner, attention of ragged new tokens (chunk) and of drafted
+ * trees, and what bounds a cache's length: score, select, move.
  *
  * split and combine must run on the same stream with the same workspace; one
  * workspace serves one stream at a time.  The library never allocates, frees,
