@@ -492,7 +492,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       }
       const int hi_min = __reduce_min_sync(0xffffffffu, hi);
       constexpr bool kOne = DT == FP8KV_DTYPE_F16;      // (bf16 rows have scales of their own)
-      float m = 0.f, l = 0.f;                           // rows: a whole number near the largest logit; sum
+      // rows: a whole number near the largest logit; the sum, and what its additions rounded off (a row has
+      // up to 2^26 / 32 of them)
+      float m = 0.f, l = 0.f, l_rest = 0.f;
       bool started = false;                             // ... a logit above -inf was seen
       bool far = false;                                 // some row of the warp has logits past 2^22: products are rounded
                                                         // before the maximum is taken off
@@ -556,7 +558,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
               for (int k = 0; k < kCols; ++k) top = fmaxf(top, __uint_as_float(x[k]));
               top = far ? top : __fmul_rn(top, c);
               const float n = top == -INFINITY ? m : started ? fmaxf(m, ceilf(top)) : ceilf(top);
-              if (started) l *= exp2_whole(m - n);
+              if (started) {
+                const float a = exp2_whole(m - n);
+                l *= a;
+                l_rest *= a;
+              }
               m = n;
               started |= top != -INFINITY;
               if (!far && __any_sync(0xffffffffu, fabsf(m) >= 0x1p22f)) {
@@ -565,7 +571,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
               }
               y = started ? weights() : 0.f;
             }
-            l += y;
+            two_sum_acc(l, l_rest, y);
           }
         }
         if (COLS && t < walk.u1) {
@@ -584,6 +590,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       }
       ktb += n_tiles;
       if (!COLS) {
+        l += l_rest;
         if (cf != cf && l != 0.f) l = cf;
         if (!started) m = kNoMax;
         // the groups' shares of the positions
