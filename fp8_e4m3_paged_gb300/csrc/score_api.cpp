@@ -16,6 +16,7 @@ using namespace fp8kv;
 
 namespace {
 constexpr int64_t kScoreStreamBytes = 56 << 20;
+constexpr int64_t kScoreLogitBytes = 4ll << 30;
 }
 
 extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cache_score_plan_t* plan) {
@@ -60,7 +61,9 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     // 4 x 500 (31 MB) 16.6 / 24.9, 4 x 1000 (63 MB) 27.0 / 26.3, 16 x 500 (125 MB) 44 / 28; 8 tokens on
     // 4 x 2000 (31 MB) 13.6 / 29.1, 16 x 1000 (63 MB) 20 / 37; 48 requests of 16 tokens on 20 (8 MB) 13 / 48.
     const int64_t bytes = pairs * len * (8 * rows + ceil_div(rows, kScoreGroupRows) * P.head_dim);
-    const bool stream = rows <= kScoreGroupRows || (rows <= kScoreStreamRows && bytes <= kScoreStreamBytes);
+    // (and the workspace stays in bounds: the tile kernel keeps no logits)
+    const bool stream = pairs * len * score_vectors(rows) * 4 <= kScoreLogitBytes &&
+                        (rows <= kScoreGroupRows || (rows <= kScoreStreamRows && bytes <= kScoreStreamBytes));
     P.kernel = stream ? FP8KV_CHUNK_STREAM : FP8KV_CHUNK_TILE;
   }
   if (P.kernel == FP8KV_CHUNK_STREAM && rows > kScoreStreamRows) return FP8KV_EUNSUPPORTED;
@@ -91,7 +94,8 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     const int64_t blocks = ceil_div(rows, tile);
     const int64_t most = rows > 128 ? kScoreAccTokens / kChunkTileTokens : tiles;
     part = std::min(most, std::max<int64_t>(8, ceil_div(pairs * tiles, 3 * sms)));
-    P.col_part = (int32_t)(std::max<int64_t>(part, 1) * kChunkTileTokens);
+    part = std::max<int64_t>({part, 1, rows > 128 ? 1 : ceil_div(tiles, 65535)});  // (16 tiles are enough for 2^26)
+    P.col_part = (int32_t)(part * kChunkTileTokens);
     const int64_t ctas = std::max<int64_t>(pairs * ceil_div(len, P.col_part), 1);
     P.row_groups = (int32_t)std::max<int64_t>(1, std::min({blocks, 6 * sms / ctas, (int64_t)64}));
     floats = P.row_groups > 1 ? P.row_groups * pairs * len : 0;

@@ -678,6 +678,8 @@ typedef struct {
 } fp8kv_cache_score_args;
 
 /* Validate `d` (as fp8kv_attn_chunk_plan; kernel and num_splits choose likewise) and fill `plan`.
+ * With FP8KV_CHUNK_AUTO the logits that FP8KV_CHUNK_STREAM keeps in the workspace stay below 4 GiB (else, and
+ * for many query vectors, FP8KV_CHUNK_TILE, which keeps none).
  * A window, more than 65535 pairs of request and KV head, max_kv_len above 2^26, and FP8KV_CHUNK_STREAM with more than 256
  * query vectors per KV head: FP8KV_EUNSUPPORTED. */
 int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cache_score_plan_t* plan);
