@@ -198,6 +198,68 @@ def test_strides(name):
         check(Run(c, kernel, S, spread=True)(), c, ref)
 
 
+def test_more_requests_than_shares():
+    """Batches whose CTAs do not find their shares from the lengths: partitions of one length."""
+    c = Case([(9 + i % 9, 20 + (i * 37) % 150 + 9) for i in range(150)] + [(20, 3000)], Hq=4, Hkv=2, D=64)
+    r = Run(c, 2)
+    assert r.plan.per_head == 0
+    check(r(), c, reference(c))
+
+
+def test_device_scale():
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    for name in ("decode_gqa4", "last_rows"):
+        c = CASES[name]
+        ref = reference(c)
+        scale = torch.tensor([c.k_scale], dtype=torch.float32, device="cuda")
+        for kernel in (1, 2):
+            r = Run(c, kernel)
+            kw = dict(q=r.q, k_cache=r.k, block_table=r.table, cu_q=r.cu, kv_len=r.kv_len, score=r.score, workspace=r.ws,
+                      softmax_scale=c.softmax_scale, k_scale=float("nan"), k_scale_dev=scale)
+            r.args = B.make_cache_score_args(**kw)
+            check(r(), c, ref)
+            # a NaN scale: every position that a token sees
+            scale.fill_(float("nan"))
+            got = r()
+            for b, (n, kv) in enumerate(c.requests):
+                assert torch.isnan(got[b, :, :kv]).all() and (got[b, :, kv:] == -7.0).all()
+            scale.fill_(c.k_scale)
+
+
+def test_two_calls_at_once():
+    """Calls in flight on streams of their own, each with its workspace."""
+    c, d = CASES["prompt"], CASES["decode_gqa4"]
+    a, b = Run(c, 2), Run(d, 1)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.B.CacheScoreCall(a.plan, a.args).run(s.cuda_stream)
+        b.B.CacheScoreCall(b.plan, b.args).run(t.cuda_stream)
+    torch.cuda.synchronize()
+    check(a.score.cpu(), c, reference(c))
+    check(b.score.cpu(), d, reference(d))
+
+
+def test_calls_in_a_row():
+    """The second kernel of a call starts early; the next call on the same buffers starts behind it."""
+    for name in ("decode_gqa4", "last_rows", "prompt"):
+        c = CASES[name]
+        zero = torch.zeros((len(c.requests), c.Hkv, c.max_kv))
+        once = Run(c, 0, before=zero)()
+        r = Run(c, 0, before=zero.clone(), in_place=True)
+        s = torch.cuda.current_stream()
+        torch.cuda.synchronize()
+        for _ in range(6):
+            r.B.CacheScoreCall(r.plan, r.args).run(s.cuda_stream)
+        torch.cuda.synchronize()
+        got = r.score.cpu()
+        for b, (n, kv) in enumerate(c.requests):
+            # in front of the new tokens six times the weights (five roundings), at them one time
+            want = once[b, :, :kv].double() * torch.where(torch.arange(kv) < kv - n, 6.0, 1.0)
+            assert ((got[b, :, :kv].double() - want).abs() <= 6 * 2.0 ** -24 * want).all()
+
+
 def test_the_same_bits_every_time():
     for name in ("decode_gqa4", "prompt", "wide"):
         r = Run(CASES[name])

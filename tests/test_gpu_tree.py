@@ -204,7 +204,7 @@ def test_bad_blocks_and_depths():
 def test_other_stream_and_replay_with_other_trees():
     c = TreeCase([(26, 637), (9, 200), (40, 90)], Hq=8, Hkv=2, D=128)
     d = TreeCase([(26, 500), (9, 150), (40, 70)], Hq=8, Hkv=2, D=128, seed=0, masks=_odd_masks((26, 9, 40), 9))
-    for kernel, S in ((1, 0), (2, 2)):
+    for kernel, S in ((1, 0), (2, 2), (2, 0)):
         s = torch.cuda.Stream()
         r = Run(c, kernel, S)
         s.wait_stream(torch.cuda.current_stream())
@@ -222,6 +222,28 @@ def test_other_stream_and_replay_with_other_trees():
         g.replay()
         torch.cuda.synchronize()
         check(r.out.cpu().double(), e)
+
+
+def test_many_requests_and_row_blocks():
+    """Batches whose CTAs do not find their shares from the lengths: partitions of one length."""
+    for c in (TreeCase([(1 + i % 5, 9 + (i * 37) % 90) for i in range(140)] + [(5, 3000)], Hq=2, Hkv=1, D=64),
+              TreeCase([(300, 2900), (5, 40), (0, 7)], Hq=2, Hkv=1, D=128)):
+        ref = c.reference()
+        r = Run(c, 2)
+        assert r.plan.per_head == 0 and r.plan.num_splits > 1
+        check(r(), c, ref)
+
+
+def test_shares_with_nothing_to_see():
+    """Requests without positions, without tokens, with a mask that is empty, beside a long one."""
+    n = [3, 0, 40, 5, 1, 0]
+    c = TreeCase([(3, 0), (0, 50), (40, 1500), (5, 5), (1, 1), (0, 0)], Hq=8, Hkv=2, D=128,
+                 masks=[np.zeros((k, k), bool) for k in n], extra_rows=3)
+    r = Run(c, 2)
+    assert r.plan.per_head > 0
+    got = r()
+    check(got, c)
+    assert (got[:3] == 0).all() and (got[43:49] == 0).all()
 
 
 def test_two_graphs_share_no_workspace():
