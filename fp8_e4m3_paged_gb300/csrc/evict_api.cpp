@@ -22,6 +22,12 @@ int sm_count() {
   return sms;
 }
 
+// Whether two arrays of n int32 share bytes.
+bool overlap(const int32_t* x, const int32_t* y, int64_t n) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(x), q = reinterpret_cast<uintptr_t>(y);
+  return (p < q ? q - p : p - q) < (uintptr_t)(4 * n);
+}
+
 }  // namespace
 
 extern "C" int fp8kv_attn_cache_select(const fp8kv_cache_select_args* a, fp8kv_stream_t stream) {
@@ -34,6 +40,8 @@ extern "C" int fp8kv_attn_cache_select(const fp8kv_cache_select_args* a, fp8kv_s
   if (a->batch == 0) return FP8KV_OK;
   if (!a->kv_len || !a->n_keep || !aligned(a->kv_len, 4) || !aligned(a->n_keep, 4) || !aligned(a->status, 4))
     return FP8KV_EINVAL;
+  // a list reads its length while another one's first CTA writes the number kept
+  if (overlap(a->kv_len, a->n_keep, a->batch)) return FP8KV_EINVAL;
   if (a->max_len > 0 && (!a->score || !a->keep)) return FP8KV_EINVAL;
   const int64_t s[] = {a->score_stride_req, a->score_stride_head, a->keep_stride_req, a->keep_stride_list};
   if (!aligned(a->score, 4) || !aligned(a->keep, 4) || !strides_ok(s, 4, 1)) return FP8KV_EINVAL;
@@ -61,6 +69,7 @@ extern "C" int fp8kv_attn_cache_move(const fp8kv_cache_move_args* a, fp8kv_strea
                         a->vc_stride_block, a->vc_stride_token, a->vc_stride_head};
   if (!strides_ok(bs, 6, 16)) return FP8KV_EINVAL;
   if (!a->block_table || a->block_table_stride < a->max_blocks || !aligned(a->block_table, 4)) return FP8KV_EINVAL;
+  if (a->dst_table == a->block_table) return FP8KV_EINVAL;  // (no order between reads and writes of the same pages)
   if (a->dst_table && (a->dst_max_blocks < 1 || a->dst_table_stride < a->dst_max_blocks || !aligned(a->dst_table, 4)))
     return FP8KV_EINVAL;
   if (!a->src || !a->count || !aligned(a->src, 4) || !aligned(a->count, 4) || !aligned(a->first, 4) ||

@@ -625,7 +625,7 @@ int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t str
  *                    of softmax(z_ih)_t
  *
  * with the logits z of fp8kv_attn_chunk without a window.  One call per decode step accumulates
- * (score_in = score is allowed: the same buffer, element by element); one with the last rows
+ * (score_in = score is allowed: the same buffer with the same strides; others do not overlap); one with the last rows
  * of a prompt, or all of them, rates the prompt's positions.  A request without new tokens and
  * positions from kv_len[b] on are left as they are.
  *
@@ -697,7 +697,8 @@ int fp8kv_attn_cache_score(const fp8kv_cache_score_plan_t* plan, const fp8kv_cac
  *
  * lists = num_kv_heads: a list for each KV head by its own weights.  lists = 1: one for all
  * heads, by the FP32 sum of their weights, added head after head.  Exact
- * and deterministic; graph-capturable, no workspace.  A kv_len outside [0, max_len] is
+ * and deterministic; graph-capturable, no workspace.  keep and n_keep overlap no input: n_keep in
+ * place of kv_len is refused (copy it over behind the call).  A kv_len outside [0, max_len] is
  * clamped and sets FP8KV_STATUS_BAD_LEN in *status.
  * ------------------------------------------------------------------------ */
 typedef struct {
@@ -732,7 +733,7 @@ int fp8kv_attn_cache_select(const fp8kv_cache_select_args* a, fp8kv_stream_t str
  * FP8KV_STATUS_BAD_ENTRIES.  Rows that stay where they are (s = k) are not touched, so a
  * shared prefix in front of the first row that goes is safe; pages of rows that
  * move belong to one request alone.
- * dst_table: into other pages.  Any s >= 0; no page is both read and written.
+ * dst_table: into other pages.  Any s >= 0; no page is both read and written (block_table itself is refused).
  *
  * score / score_out (both or none): the weights' row of each head moves likewise,
  * score_out[b][h][first + k] = score[b][h][first + s], between two buffers that do not

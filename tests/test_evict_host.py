@@ -241,7 +241,8 @@ def _select_args(B, **kw):
     a = B.CacheSelectArgs()
     a.batch, a.num_kv_heads, a.lists, a.max_len = 3, 2, 2, 1000
     a.budget, a.sinks, a.recent = 100, 4, 10
-    a.score = a.kv_len = a.keep = a.n_keep = FAKE
+    a.score = a.kv_len = a.keep = FAKE
+    a.n_keep = FAKE << 20
     a.score_stride_req, a.score_stride_head = 2000, 1000
     a.keep_stride_req, a.keep_stride_list = 200, 100
     for k, v in kw.items():
@@ -257,6 +258,9 @@ def _select_args(B, **kw):
     (dict(status=FAKE + 2), -1), (dict(score_stride_req=-1), -1), (dict(keep_stride_list=99), -1),
     (dict(keep_stride_req=150), -1), (dict(num_kv_heads=65536, lists=1), -2), (dict(max_len=(1 << 30) + 1), -2),
     (dict(batch=1 << 28, lists=1, num_kv_heads=1, keep_stride_req=100), -2),
+    # the lengths are read while the numbers kept are written
+    (dict(n_keep=FAKE), -1), (dict(n_keep=FAKE + 8), -1), (dict(n_keep=FAKE - 8), -1),
+    (dict(n_keep=FAKE, batch=1, lists=1, num_kv_heads=1), -1),
 ])
 def test_select_rejects(B, kw, code):
     _rejects(B, lambda: B.fp8kv_attn_cache_select(_select_args(B, **kw)), code)
@@ -269,7 +273,7 @@ def _move_args(B, **kw):
     a.k_cache = a.v_cache = a.block_table = a.src = a.count = FAKE
     a.kc_stride_block, a.kc_stride_token, a.kc_stride_head = 4096, 256, 128
     a.vc_stride_block, a.vc_stride_token, a.vc_stride_head = 4096, 256, 128
-    a.block_table_stride = 20
+    a.block_table_stride, a.dst_table_stride = 20, 20
     a.src_stride_req, a.src_stride_list = 200, 100
     for k, v in kw.items():
         setattr(a, k, v)
@@ -281,8 +285,9 @@ def _move_args(B, **kw):
     (dict(head_dim=1040), -1), (dict(head_dim=24), -1), (dict(page_size=0), -1), (dict(max_blocks=0), -1),
     (dict(num_kv_blocks=0), -1), (dict(kv_format=3), -1), (dict(kv_format=-1), -1), (dict(k_cache=None), -1),
     (dict(v_cache=FAKE + 8), -1), (dict(kc_stride_token=8), -1), (dict(vc_stride_head=-16), -1), (dict(block_table=None), -1),
-    (dict(block_table_stride=19), -1), (dict(dst_table=FAKE, dst_max_blocks=0), -1),
-    (dict(dst_table=FAKE, dst_max_blocks=9, dst_table_stride=8), -1), (dict(dst_table=FAKE + 2, dst_max_blocks=1, dst_table_stride=1), -1),
+    (dict(block_table_stride=19), -1), (dict(dst_table=FAKE * 2, dst_max_blocks=0), -1),
+    (dict(dst_table=FAKE * 2, dst_max_blocks=9, dst_table_stride=8), -1),
+    (dict(dst_table=FAKE + 2, dst_max_blocks=1, dst_table_stride=1), -1), (dict(dst_table=FAKE, dst_max_blocks=20), -1),
     (dict(src=None), -1), (dict(src=FAKE + 2), -1), (dict(count=None), -1), (dict(first=FAKE + 1), -1), (dict(status=FAKE + 2), -1),
     (dict(src_stride_list=-1), -1), (dict(score=FAKE), -1), (dict(score_out=FAKE), -1),
     (dict(score=FAKE, score_out=FAKE, max_len=10, score_out_stride_req=20, score_out_stride_head=10), -1),
