@@ -101,7 +101,7 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     floats = P.row_groups > 1 ? P.row_groups * pairs * len : 0;
     // One row block per request, and CTAs enough for one wave: shares by the lengths on the device.
     const int64_t per_head = sms / P.num_kv_heads;
-    if (d->num_splits == 0 && blocks <= 1 && P.batch <= std::min<int64_t>(per_head, kShareMax)) {
+    if (d->num_splits == 0 && blocks <= 1 && per_head >= 1 && P.batch <= std::min<int64_t>(per_head, kShareMax)) {
       P.per_head = (int32_t)per_head;
       P.num_splits = (int32_t)std::min(tiles, per_head);
       P.row_groups = rows <= 128 ? 1 : 2;  // (two row tiles: each has its sums in the workspace)

@@ -171,14 +171,15 @@ def test_score_plan(B):
                dict(max_kv_len=1 << 26, max_blocks=1 << 22), dict(max_kv_len=1 << 26, max_blocks=1 << 22, num_sms=65535),
                dict(max_kv_len=1 << 26, max_blocks=1 << 22, max_q=4, batch=1), dict(max_kv_len=0, max_blocks=0),
                dict(max_kv_len=1 << 20, max_blocks=1 << 16, batch=256, total_q=256, max_q=1, num_q_heads=32, num_kv_heads=8), dict(num_splits=7),
-               dict(head_dim=256, max_q=40), dict(batch=0, total_q=0), dict(num_kv_heads=8, num_sms=4)):
+               dict(head_dim=256, max_q=40), dict(batch=0, total_q=0), dict(num_kv_heads=8, num_sms=4),
+               dict(num_kv_heads=8, num_sms=4, batch=0, total_q=0, kernel=2)):
         p = B.fp8kv_attn_cache_score_plan(_desc(B, **kw))
         rows = p.max_q * p.group
         pairs = p.batch * p.num_kv_heads
-        if rows <= 16 and pairs * p.max_kv_len * 64 <= 1 << 32:
+        if "kernel" not in kw and rows <= 16 and pairs * p.max_kv_len * 64 <= 1 << 32:
             assert p.kernel == B.CHUNK_STREAM
         assert p.kernel == B.CHUNK_TILE or rows <= 256 and 4 * pairs * p.max_kv_len * p.vectors <= 1 << 32
-        assert -(-p.max_kv_len // p.col_part) <= 65535 and p.num_splits <= 65535
+        assert -(-p.max_kv_len // p.col_part) <= 65535 and 1 <= p.num_splits <= 65535
         keep = pairs * p.max_kv_len * (p.vectors if p.kernel == B.CHUNK_STREAM else p.row_groups if p.row_groups > 1 else 0)
         assert p.ml_offset >= p.partial_offset + 4 * keep
         assert p.workspace_bytes >= p.ml_offset + 8 * p.num_splits * p.total_q * p.num_q_heads
