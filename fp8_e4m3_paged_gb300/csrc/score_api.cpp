@@ -74,7 +74,8 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     const int64_t row_groups = ceil_div(rows, kScoreGroupRows);
     int64_t part = std::min<int64_t>(2048, std::max<int64_t>(128, ceil_div(pairs * row_groups * len, 4 * sms)));
     if (d->num_splits) part = ceil_div(len, d->num_splits);
-    part = align_up(std::max(part, ceil_div(len, 65535)), 128);
+    // (a lane's FP32 sum has 1 of 32 positions; 2^26 positions are 1024 partitions at least)
+    part = align_up(std::min<int64_t>(std::max(part, ceil_div(len, 65535)), 65536), 128);
     P.num_splits = (int32_t)ceil_div(len, part);
     P.vectors = score_vectors(rows);
     P.row_groups = 1;

@@ -172,13 +172,16 @@ def test_score_plan(B):
                dict(max_kv_len=1 << 26, max_blocks=1 << 22, max_q=4, batch=1), dict(max_kv_len=0, max_blocks=0),
                dict(max_kv_len=1 << 20, max_blocks=1 << 16, batch=256, total_q=256, max_q=1, num_q_heads=32, num_kv_heads=8), dict(num_splits=7),
                dict(head_dim=256, max_q=40), dict(batch=0, total_q=0), dict(num_kv_heads=8, num_sms=4),
-               dict(num_kv_heads=8, num_sms=4, batch=0, total_q=0, kernel=2)):
+               dict(num_kv_heads=8, num_sms=4, batch=0, total_q=0, kernel=2),
+               dict(max_kv_len=1 << 26, max_blocks=1 << 22, max_q=1, num_splits=1, kernel=1)):
         p = B.fp8kv_attn_cache_score_plan(_desc(B, **kw))
         rows = p.max_q * p.group
         pairs = p.batch * p.num_kv_heads
         if "kernel" not in kw and rows <= 16 and pairs * p.max_kv_len * 64 <= 1 << 32:
             assert p.kernel == B.CHUNK_STREAM
-        assert p.kernel == B.CHUNK_TILE or rows <= 256 and 4 * pairs * p.max_kv_len * p.vectors <= 1 << 32
+        if p.kernel == B.CHUNK_STREAM:  # FP32 sums, whoever chose the partitions
+            assert p.stat_part <= 65536 and p.num_splits * p.stat_part >= p.max_kv_len
+        assert "kernel" in kw or p.kernel == B.CHUNK_TILE or rows <= 256 and 4 * pairs * p.max_kv_len * p.vectors <= 1 << 32
         assert -(-p.max_kv_len // p.col_part) <= 65535 and 1 <= p.num_splits <= 65535
         keep = pairs * p.max_kv_len * (p.vectors if p.kernel == B.CHUNK_STREAM else p.row_groups if p.row_groups > 1 else 0)
         assert p.ml_offset >= p.partial_offset + 4 * keep
