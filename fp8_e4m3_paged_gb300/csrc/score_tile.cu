@@ -86,7 +86,7 @@ struct Walk {
 // Decoders: every other K tile of the walk, in order.  A tile costs its warps some 250 instructions in
 // a chain (the copies' completion, the stage, the conversions, the next copies and block ids), one
 // warp to a scheduler: two teams, so that a tile is ready twice as often.
-template <int D, int FMT>
+template <int D, int FMT, bool COLS>
 __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t* smem, int b, int g, const Walk& walk,
                                          int team, int w, int lane) {
   using C = Cfg<D>;
@@ -157,6 +157,9 @@ __device__ __forceinline__ bool decode_k(const ChunkParams& p, Meta& mt, uint8_t
   for (int kt = team; kt < total; kt += kTeams) {
     const int st = kt % NS, before = kt - NS;  // the tile that was there
     asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+    // The first tile that a product has to make room for: no product starts before the row pass has ended, however
+    // long that takes, so the bounded wait starts then.
+    if (COLS && before >= 0 && before < kTeams) wait_for_previous_kernel();
     if (before >= 0 && !warp_wait(&mt.k_empty[before & 1], (before >> 1) & 1, abort_flag)) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       return false;
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       __syncwarp();
     }
   } else {
-    ok = decode_k<D, FMT>(p, mt, smem, b, g, walk, (warp >> 2) - kGroups, warp & 3, lane);
+    ok = decode_k<D, FMT, COLS>(p, mt, smem, b, g, walk, (warp >> 2) - kGroups, warp & 3, lane);
   }
   if (!ok) set_status(p.status, FP8KV_STATUS_TIMEOUT);
   __syncwarp();

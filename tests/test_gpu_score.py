@@ -206,6 +206,48 @@ def test_more_requests_than_shares():
     check(r(), c, reference(c))
 
 
+def test_rows_before_the_first_position():
+    """Row blocks whose tokens all stand in front of position 0."""
+    c = Case([(2000, 50), (700, 300)], Hq=4, Hkv=2, D=128)
+    check(Run(c, 2)(), c, reference(c))
+
+
+def test_one_long_partition():
+    """2^25 positions, all rows' sums in one partition: the column pass waits for the row pass however long that takes, and
+    the sums hold.  All positions are in one block of 1024, so position t weighs what t mod 1024 does."""
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    L, n, Hq, D, page = 1 << 25, 33, 4, 64, 1024
+    gen = torch.Generator().manual_seed(5)
+    q = torch.randn(n, Hq, D, generator=gen).half()
+    k = torch.randn(1, page, 1, D, generator=gen).to(torch.float8_e4m3fn)
+    logits = torch.einsum("nhd,td->nht", q.double(), k[0, :, 0].double()) * 0.125
+    # every new token sees all positions in front of them; at most 32 of 2^25 others are not in a token's sum, which
+    # moves no weight by more than 33 * 2^-25 times the largest one over the mean
+    w = torch.exp(logits - logits.amax(-1, keepdim=True))
+    w = w / w.sum(-1, keepdim=True) / (L // page)
+    want = w.sum((0, 1))
+    assert 33 * float((w.amax(-1) / w.mean(-1)).max()) * 2.0 ** -25 < 2.0 ** -12
+    plan = B.fp8kv_attn_cache_score_plan(B.make_chunk_desc(
+        batch=1, total_q=n, max_q=n, num_q_heads=Hq, num_kv_heads=1, head_dim=D, page_size=page, max_kv_len=L,
+        max_blocks=L // page, num_kv_blocks=1, kernel=B.CHUNK_TILE, num_splits=1, num_sms=152))
+    assert plan.num_splits == 1 and plan.stat_part >= L
+    score = torch.zeros(1, 1, L, device="cuda")
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    args = B.make_cache_score_args(
+        q=q.cuda(), k_cache=k.cuda().view(torch.uint8), block_table=torch.zeros(1, L // page, dtype=torch.int32, device="cuda"),
+        cu_q=torch.tensor([0, n], dtype=torch.int32, device="cuda"), kv_len=torch.tensor([L], dtype=torch.int32, device="cuda"),
+        score=score, workspace=ws, softmax_scale=0.125, k_scale=1.0)
+    B.CacheScoreCall(plan, args).run(torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32)) == 0
+    got = score[0, 0, : L - page].view(-1, page).cpu().double()
+    # Logits of 64 FP32 products and sums, |z| < 8, base 2 at 2^4 (each term at most 2^-20 in all: 2^-14 with the factor), the
+    # exponential 2^-22, sums by the kernel's compensated addition of 32 terms each (2^-19), the positions left out above
+    # (2^-12): 2^-11 covers them.
+    assert ((got - want).abs() <= 2.0 ** -11 * want).all()
+
+
 def test_device_scale():
     from fp8_e4m3_paged_gb300 import binding as B
 
