@@ -290,6 +290,47 @@ def test_move_interleaved_caches(B):
         p.check(B, rising(2, 2, 600, 1100, 8), [600, 77])
 
 
+@pytest.mark.parametrize("fresh", [0, 3])
+def test_move_past_32_bits(B, fresh):
+    """Pages 600 MB apart: byte offsets up to 6 GB."""
+    p = Pool(2, 5, 16, 2, 128, seed=16, fresh=fresh)
+    blocks, far = p.k.shape[0], (600 << 20) // 128 * 128
+    pool = torch.empty(blocks * far, dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 1 << 32
+    p.dk = pool.as_strided((blocks, 16, 2, 128), (far, 256, 128, 1))
+    p.dv = pool.as_strided((blocks, 16, 2, 128), (far, 256, 128, 1), 4096)
+    p.dk.copy_(p.k)
+    p.dv.copy_(p.v)
+    p.check(B, rising(2, 2, 48, 80, 17), [48, 31])
+
+
+def test_two_streams_at_once(B):
+    """Selections and moves in flight on streams of their own."""
+    score = weights(3, 2, 20000, 21)
+    x, lens = torch.from_numpy(score).cuda(), torch.tensor([20000, 9000, 100], dtype=torch.int32).cuda()
+    outs = [(torch.full((3, 2, 500), -7, dtype=torch.int32, device="cuda"),
+             torch.zeros(3, dtype=torch.int32, device="cuda")) for _ in range(2)]
+    chosen_by = [B.make_cache_select_args(score=x, kv_len=lens, budget=500, sinks=i, recent=9, keep=keep, n_keep=n)
+                 for i, (keep, n) in enumerate(outs)]
+    pools = [Pool(2, 70, 16, 2, 128, seed=22 + i) for i in range(2)]
+    lists = [rising(2, 2, 600, 1100, 24 + i) for i in range(2)]
+    moved = [p.args(B, src, [600, 77 + i]) for i, (p, src) in enumerate(zip(pools, lists))]
+    want = [p.expected(src, [600, 77 + i], [0, 0]) for i, (p, src) in enumerate(zip(pools, lists))]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        B.fp8kv_attn_cache_select(chosen_by[i], streams[i].cuda_stream)
+        B.fp8kv_attn_cache_move(moved[i], streams[2 + i].cuda_stream)
+    torch.cuda.synchronize()
+    for i, (keep, n_keep) in enumerate(outs):
+        assert n_keep.tolist() == [500, 500, 100]
+        for b, n in enumerate((20000, 9000, 100)):
+            for h in range(2):
+                line = chosen(score[b, h:h + 1], n, 500, i, 9)
+                assert (keep[b, h, :len(line)].cpu().numpy() == line).all()
+        assert torch.equal(pools[i].dk.cpu(), want[i][0]) and torch.equal(pools[i].dv.cpu(), want[i][1])
+
+
 def test_move_bad_places(B):
     """Positions outside the table and blocks out of range are not moved; counts are clamped."""
     src = rising(2, 1, 100, 200, 9)

@@ -248,6 +248,23 @@ def test_one_long_partition():
     assert ((got - want).abs() <= 2.0 ** -11 * want).all()
 
 
+@pytest.mark.parametrize("kernel", [1, 2])
+def test_pages_past_32_bits(kernel):
+    """Pages 600 MB apart: byte offsets up to 6 GB."""
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    c = Case([(5, 60), (1, 40)], Hq=8, Hkv=2, D=128, page=16)
+    far = (600 << 20) // 128 * 128
+    r = Run(c, kernel)
+    pool = torch.empty(c.blocks * far, dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 1 << 32
+    k = pool.as_strided((c.blocks, 16, 2, 128), (far, 256, 128, 1))
+    k.copy_(r.k)
+    r.args = B.make_cache_score_args(q=r.q, k_cache=k, block_table=r.table, cu_q=r.cu, kv_len=r.kv_len, score=r.score,
+                                     workspace=r.ws, softmax_scale=c.softmax_scale, k_scale=c.k_scale)
+    check(r(), c, reference(c))
+
+
 def test_device_scale():
     from fp8_e4m3_paged_gb300 import binding as B
 

@@ -246,6 +246,26 @@ def test_shares_with_nothing_to_see():
     assert (got[:3] == 0).all() and (got[43:49] == 0).all()
 
 
+@pytest.mark.parametrize("kernel", [1, 2])
+def test_pages_past_32_bits(kernel):
+    """Pages 600 MB apart: byte offsets up to 6 GB."""
+    from fp8_e4m3_paged_gb300 import binding as B
+
+    c = TreeCase([(9, 60), (20, 40)], Hq=8, Hkv=2, D=128, page=16)
+    far = (600 << 20) // 128 * 128
+    r = Run(c, kernel)
+    pool = torch.empty(c.blocks * far, dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 1 << 32
+    k = pool.as_strided((c.blocks, 16, 2, 128), (far, 256, 128, 1))
+    v = pool.as_strided((c.blocks, 16, 2, 128), (far, 256, 128, 1), 4096)
+    k.copy_(c.k.cuda())
+    v.copy_(c.v.cuda())
+    r.args = B.make_tree_args(q=r.q, k_cache=k, v_cache=v, out=r.out, workspace=r.ws, mask=r.mask, depth=r.depth,
+                              softmax_scale=c.softmax_scale, block_table=r.table, cu_q=r.cu, kv_len=r.kv_len,
+                              k_scale=c.k_scale, v_scale=c.v_scale)
+    check(r(), c)
+
+
 def test_two_graphs_share_no_workspace():
     """Two calls in flight on streams of their own, each with its workspace."""
     c, d = CASES["many_nodes"], CASES["small"]
