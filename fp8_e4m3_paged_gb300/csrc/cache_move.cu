@@ -18,6 +18,9 @@
 // looked up meanwhile, so that a CTA always has rows in flight (in registers, one round at a
 // time, 16 x 2052 rows of 8 heads took 58 us).  16 bytes per thread and access, eight lanes to a
 // row of 128: rows are whole sectors whatever the list.
+//
+// 8 x 4096 rows of 8 heads (D 128, by lists, with weights) 37 us, 16 x 2052 in place 36: 3.7 TB/s read and
+// written, where whole pages copy at 6.8.  64 accepted paths of up to five rows: 4.4 us.
 #include <algorithm>
 #include <cstdint>
 

@@ -11,7 +11,8 @@
 // shared memory after the first read (up to kKeys; longer runs are read again, from L2).  Bound by
 // latency for the usual sizes: the bytes of a list are read once, eight loads of a thread in flight,
 // and each of the histograms costs its CTA barriers and, in a cluster, a barrier and the peers'
-// counts.  (Keys in registers, all loops unrolled: twice the time, most of it fetching instructions.)
+// counts.  128 lists of 1000 to 40000, budget 4096: 23 us; a joint list of 131072 over 8 heads: 25 us, where
+// eight SMs read 4 MB.  (Keys in registers, all loops unrolled: twice the time, most of it fetching instructions.)
 #include <algorithm>
 #include <cstdint>
 

@@ -12,6 +12,9 @@
 // blocks of 32 positions on its own, rows requested by cp.async into its ring, a lane for each row's
 // place.  (Blocks of 16, one chain of products and exponentials at a time, took 2400 cycles each with
 // four warps on a scheduler: 60 us for 64 requests of 4000 positions.)
+// 64 requests of 512 to 16000 positions, 32 heads over 8, D 128: 80 us with the second kernel (59 % of the bytes'
+// time at the copy rate), of which this one takes 65: four warps' chains on each scheduler, not DRAM, bound it.
+// One request of 4001: 7.1 us, two launches and the chain lengths -> block table -> rows.
 // S^T[16 tokens x 8 vectors] = K . Q^T by mma.sync m16n8k16: lane (n = lane/4, c = lane%4) of
 // the A operand takes the 16-byte pieces c, c + 4, ... of rows n and n + 8, a word of each decodes to
 // one fragment, and Q's B fragments are laid out in that order of d.

