@@ -9,9 +9,11 @@
 //
 // One thread-block cluster per list, each CTA with a run of the positions, whose keys stay in
 // shared memory after the first read (up to kKeys; longer runs are read again, from L2).  Bound by
-// latency for the usual sizes: the bytes of a list are read once, eight loads of a thread in flight,
-// and each of the histograms costs its CTA barriers and, in a cluster, a barrier and the peers'
-// counts.  128 lists of 1000 to 40000, budget 4096: 23 us; a joint list of 131072 over 8 heads: 25 us, where
+// latency and by instructions per key: the bytes of a list are read once, eight loads of a thread in
+// flight, and keys leave shared memory in fours (one at a time, with tests for the end of the run on
+// each: 25.4 us instead of 20.8 for the first case below); each of the histograms costs its CTA
+// barriers and, in a cluster, a barrier and the peers' counts (two CTAs 1.3 us, four 3, eight 7).
+// 128 lists of 1000 to 40000, budget 4096: 20.8 us; a joint list of 131072 over 8 heads: 23.6, where
 // eight SMs read 4 MB.  (Keys in registers, all loops unrolled: twice the time, most of it fetching instructions.)
 #include <algorithm>
 #include <cstdint>
@@ -31,7 +33,7 @@ constexpr int kBins = 2048;
 constexpr int kPasses = 3;
 constexpr int kAhead = 8;                      // positions of a thread whose loads are in flight together
 constexpr int kKeys = 49152;                   // keys of a CTA's run that stay in shared memory
-constexpr int kMinRun = 2048;                  // positions per CTA before a list gets a further one
+constexpr int kMinRun = 4096;                  // positions per CTA before a list gets a further one
 
 template <int kThreads>
 struct Shared {
@@ -43,26 +45,26 @@ struct Shared {
   uint32_t total[2];                           // of the CTA: above, equal
 };
 
-// Keys in the order of the weights: larger weight, larger key.  -0 is +0; a NaN is below all.
+// Keys in the order of the weights: larger weight, larger key.  -0 is +0; a NaN is below all.  0 is no
+// position's key: places behind the last one hold it, are below the cut whatever it is, and need no test.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.f);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return x != x ? 1u : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
-// The weights of kAhead positions, kThreads apart (past the last one: that again): one head's, or the
-// sums over all heads, one after another.  All loads of a head are in flight together.
-template <int kThreads>
-__device__ __forceinline__ void weights_at(const fp8kv_cache_select_args& a, const float* row, int i, int n,
-                                           float (&x)[kAhead]) {
+// The weights of kAhead positions, kThreads apart, from `row` on (FULL; else of those below n, past them the last
+// one again): one head's, or the sums over all heads, one after another.  All loads of a head are in flight together.
+template <int kThreads, bool FULL>
+__device__ __forceinline__ void weights_at(const fp8kv_cache_select_args& a, const float* row, int n, float (&x)[kAhead]) {
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) x[j] = __ldg(row + min(i + j * kThreads, n - 1));
+  for (int j = 0; j < kAhead; ++j) x[j] = __ldg(row + (FULL ? j * kThreads : min(j * kThreads, n - 1)));
   if (a.lists == 1) {
 #pragma unroll 4
     for (int h = 1; h < a.num_kv_heads; ++h) {
+      row += a.score_stride_head;
       float y[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) y[j] = __ldg(row + h * a.score_stride_head + min(i + j * kThreads, n - 1));
+      for (int j = 0; j < kAhead; ++j) y[j] = __ldg(row + (FULL ? j * kThreads : min(j * kThreads, n - 1)));
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) x[j] = __fadd_rn(x[j], y[j]);
     }
@@ -78,7 +80,7 @@ __device__ __forceinline__ float weight_at(const fp8kv_cache_select_args& a, con
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 3 : 1) select_kernel(const __grid_constant__ fp8kv_cache_select_args a,
                                                              const int ctas) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   constexpr int kWarps = kThreads / 32;
   __shared__ Shared<kThreads> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -102,7 +104,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 3 : 1) select_kern
   // This CTA's run of the positions between, and each warp's part of it (whole 32s)
   const int run = ((hi - lo + ctas - 1) / ctas + 31) / 32 * 32;
   const int t0 = min(lo + rank * run, hi), n = min(t0 + run, hi) - t0;
-  const bool stay = n <= kKeys;
+  const int n4 = (n + 3) / 4 * 4;  // ... with the places behind the last position, so that keys are read in fours
+  const bool stay = n4 <= kKeys;
+  auto keys_at = [&](int i) {  // of positions i .. i + 3 of the run
+    if (stay) return *reinterpret_cast<const uint4*>(keys + i);
+    uint32_t k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = i + j < n ? key_of(weight_at(a, row, t0 + i + j)) : 0u;
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
   for (int i = tid; i < kPasses * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0u;
   __syncthreads();
 
@@ -111,25 +121,39 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 3 : 1) select_kern
   for (int pass = 0; pass < kPasses; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     uint32_t* hist = sh.hist[pass];
-    const uint32_t mask = (1u << bits) - 1u;
-    for (int i0 = tid; i0 < n; i0 += kAhead * kThreads) {
-      uint32_t k[kAhead];
-      if (pass == 0 || !stay) {
+    if (pass == 0) {
+      for (int i0 = tid; i0 < n4; i0 += kAhead * kThreads) {
         float x[kAhead];
-        weights_at<kThreads>(a, row + t0, i0, n, x);
+        if (i0 - tid + kAhead * kThreads <= n) {
+          weights_at<kThreads, true>(a, row + t0 + i0, n, x);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          k[j] = key_of(x[j]);
-          if (stay && i0 + j * kThreads < n) keys[i0 + j * kThreads] = k[j];
+          for (int j = 0; j < kAhead; ++j) {
+            const uint32_t k = key_of(x[j]);
+            if (stay) keys[i0 + j * kThreads] = k;
+            atomicAdd(&hist[k >> shift], 1u);
+          }
+        } else {
+          const int i = min(i0, n - 1);
+          weights_at<kThreads, false>(a, row + t0 + i, n - i, x);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int at = i0 + j * kThreads;
+            const uint32_t k = at < n ? key_of(x[j]) : 0u;
+            if (stay && at < n4) keys[at] = k;
+            if (at < n) atomicAdd(&hist[k >> shift], 1u);
+          }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) k[j] = keys[min(i0 + j * kThreads, n - 1)];
       }
+    } else {
+      const uint32_t base = prefix << (shift + bits), range = 1u << (shift + bits);
+#pragma unroll 2
+      for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+        const uint4 k4 = keys_at(i);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i0 + j * kThreads < n && (pass == 0 || (k[j] >> (shift + bits)) == prefix))
-          atomicAdd(&hist[(k[j] >> shift) & mask], 1u);
+        for (int j = 0; j < 4; ++j)
+          if (k[j] - base < range) atomicAdd(&hist[(k[j] - base) >> shift], 1u);
+      }
     }
     if (ctas > 1)
       cluster_sync();
@@ -175,15 +199,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 3 : 1) select_kern
   const uint32_t cut = prefix;  // keys above it stay, and the first `want` equal ones
 
   // ------------------------------------------------ positions in order
-  const int part = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
+  constexpr int kSpan = 128;  // of a warp at a time: four of each lane
+  const int part = ((n + kWarps - 1) / kWarps + kSpan - 1) / kSpan * kSpan;
   const int w0 = min(warp * part, n), w1 = min(w0 + part, n);
-  auto key_at = [&](int i) { return stay ? keys[i] : key_of(weight_at(a, row, t0 + i)); };
   uint32_t above = 0u, tie = 0u;
-#pragma unroll 8
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = key_at(i);
-    above += k > cut;
-    tie += k == cut;
+#pragma unroll 2
+  for (int i = w0 + 4 * lane; i < w1; i += kSpan) {
+    const uint4 k4 = keys_at(i);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      above += k[j] > cut;
+      tie += k[j] == cut;
+    }
   }
   above = __reduce_add_sync(0xffffffffu, above);
   tie = __reduce_add_sync(0xffffffffu, tie);
@@ -205,17 +233,31 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 3 : 1) select_kern
       tie0 += peer_load(&sh.total[1], q);
     }
   }
-#pragma unroll 4
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < w1 ? key_at(i) : 0u;
-    const uint32_t up = __ballot_sync(0xffffffffu, i < w1 && k > cut), eq = __ballot_sync(0xffffffffu, i < w1 && k == cut);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t above_i = above0 + __popc(up & below), tie_i = tie0 + __popc(eq & below);
-    if ((up >> lane & 1u) || ((eq >> lane & 1u) && tie_i < want))
-      keep[a.sinks + above_i + min(tie_i, want)] = t0 + i;
-    above0 += __popc(up);
-    tie0 += __popc(eq);
+#pragma unroll 2
+  for (int i0 = w0; i0 < w1; i0 += kSpan) {
+    const int i = i0 + 4 * lane;
+    const uint4 k4 = i < w1 ? keys_at(i) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    uint32_t mine = 0u;  // above it, and equal ones << 16
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine += k[j] > cut ? 1u : k[j] == cut ? 0x10000u : 0u;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+    uint32_t above_i = above0 + ((upto - mine) & 0xFFFFu), tie_i = tie0 + ((upto - mine) >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool up = k[j] > cut, eq = k[j] == cut;
+      if (up || (eq && tie_i < want)) keep[a.sinks + above_i + min(tie_i, want)] = t0 + i + j;
+      above_i += up;
+      tie_i += eq;
+    }
+    above0 += all & 0xFFFFu;
+    tie0 += all >> 16;
   }
   if (ctas > 1) cluster_sync();  // peers may still read this CTA's counts
 }
@@ -244,14 +286,18 @@ cudaError_t run(const fp8kv_cache_select_args& a, int64_t lists, int ctas, cudaS
 }  // namespace
 
 cudaError_t launch_cache_select(const fp8kv_cache_select_args& a, int sms, cudaStream_t st) {
-  // CTAs per list: while the GPU has room for them (three to an SM) and each keeps kMinRun positions
+  // CTAs per list: while every CTA has an SM and keeps kMinRun positions.  (A cluster's CTAs wait for one another
+  // at every barrier, so they must not wait for an SM: 64 lists of 20000 in clusters of two 13 us, in
+  // clusters of eight on 512 threads, four times as many CTAs as SMs, 53.  16 lists of 32000: four CTAs 13.2,
+  // eight 21.)
   const int64_t lists = (int64_t)a.batch * a.lists;
   int ctas = 1;
-  while (ctas < kClusterMax && lists * ctas * 2 <= 4 * (int64_t)sms && a.max_len / (2 * ctas) >= kMinRun) ctas *= 2;
+  while (ctas < kClusterMax && lists * ctas * 2 <= sms && a.max_len / (2 * ctas) >= kMinRun) ctas *= 2;
   while (ctas < kClusterMax && (a.max_len + ctas - 1) / ctas > kKeys) ctas *= 2;
   if (lists * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  // twice the threads, so twice the loads on their way, where every CTA has an SM and much to read
-  const bool wide = lists * ctas <= sms && a.max_len / ctas >= 4096;
+  // Twice the threads, so twice the loads on their way, where every CTA has an SM, or its keys leave no room for
+  // another one, and much to read (128 lists of up to 40000: 25 / 33 us before keys were read in fours).
+  const bool wide = (lists * ctas <= sms || a.max_len / ctas > 22000) && a.max_len / ctas >= 4096;
   return wide ? run<1024>(a, lists, ctas, st) : run<512>(a, lists, ctas, st);
 }
 

@@ -112,6 +112,24 @@ def test_select_long(B, hkv, width, budget, joint):
         check_select(B, weights(2, hkv, width, 5, kind), [width, width - 4099], budget, min(4, budget), min(budget // 4, 300), joint)
 
 
+@pytest.mark.parametrize("width", [1001, 5002, 20003, 33001, 420003])
+def test_select_cut_among_nans(B, width):
+    """More positions wanted than have a number: the first NaNs stay too, up to the end of runs of any length."""
+    r = np.random.default_rng(width)
+    score = r.random((2, 1, width)).astype(np.float32)
+    score[r.random(score.shape) < 0.7] = np.nan
+    score[:, :, 1::7] = -np.inf
+    lens = [width, width - 3]
+    check_select(B, score, lens, width // 2, 1, 2)
+    check_select(B, score, lens, width - 4, 0, 0)
+    check_select(B, np.full_like(score, np.nan), lens, width - 5, 0, 1)
+
+
+def test_more_lists_than_room(B):
+    """Lists whose keys leave room for one CTA on an SM, more of them than SMs."""
+    check_select(B, weights(20, 9, 24000, 8), [24000 - 997 * i for i in range(20)], 1000, 4, 64)
+
+
 def test_select_sums_head_after_head(B):
     """The joint weight is the FP32 sum in the order of the heads: 1e8 + 1 - 1e8 is not 1."""
     score = np.zeros((1, 3, 64), dtype=np.float32)
