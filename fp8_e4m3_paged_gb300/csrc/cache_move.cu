@@ -244,12 +244,19 @@ cudaError_t launch_cache_move(const fp8kv_cache_move_args& a, int sms, cudaStrea
   const int64_t units = (int64_t)a.batch * (a.num_kv_heads / g.heads);
   const int runs = (int)(((int64_t)a.max_count + g.rows - 1) / g.rows);
   // As many CTAs per unit as fill the GPU, and no more: each then has rounds to overlap.
-  const int64_t want = std::max<int64_t>(1, (int64_t)kResident * sms / units);
+  const int64_t slots = (int64_t)kResident * sms, want = std::max<int64_t>(1, slots / units);
   g.ctas = 1;
   if (in_place) {
     while (g.ctas < kClusterMax && 2 * g.ctas <= want && g.ctas < runs) g.ctas *= 2;
   } else {
     g.ctas = (int)std::min<int64_t>(want, runs);
+    // Where that leaves the last wave less than two thirds of the others' use, four waves of shorter CTAs, of three
+    // rounds at least (160 units of 2052 rows 62 -> 50 us, 320 120 -> 90; 64 units, whose waves
+    // are full, 17.0 either way, and 8 units 5.9 -> 10 in shorter CTAs: those stay).  In place, where
+    // a unit's CTAs wait for one another, it was no faster (51 / 51, 60 -> 66 for 224 units).
+    const int64_t waves = (units * g.ctas + slots - 1) / slots;
+    if (units * 2 > slots && 2 * waves * slots > 3 * units * g.ctas)
+      g.ctas = (int)std::max<int64_t>(g.ctas, std::min<int64_t>((4 * slots + units - 1) / units, runs / 3));
   }
   if (units * g.ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int rounds = (int)(((int64_t)a.max_count + (int64_t)g.rows * g.ctas - 1) / ((int64_t)g.rows * g.ctas));

@@ -286,8 +286,8 @@ cudaError_t run(const fp8kv_cache_select_args& a, int64_t lists, int ctas, cudaS
 }  // namespace
 
 cudaError_t launch_cache_select(const fp8kv_cache_select_args& a, int sms, cudaStream_t st) {
-  // CTAs per list: while every CTA has an SM and keeps kMinRun positions.  (A cluster's CTAs wait for one another
-  // at every barrier, so they must not wait for an SM: 64 lists of 20000 in clusters of two 13 us, in
+  // CTAs per list: while every CTA has an SM and keeps kMinRun positions.  (More CTAs than that start late,
+  // since a cluster waits until all of its CTAs have room side by side: 64 lists of 20000 in clusters of two 13 us, in
   // clusters of eight on 512 threads, four times as many CTAs as SMs, 53.  16 lists of 32000: four CTAs 13.2,
   // eight 21.)
   const int64_t lists = (int64_t)a.batch * a.lists;

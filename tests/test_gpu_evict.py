@@ -427,3 +427,10 @@ def test_move_replay(B):
 def test_move_nothing(B):
     p = Pool(1, 2, 16, 1, 64)
     p.check(B, torch.zeros(1, 1, 0, dtype=torch.int32), [0])
+
+
+def test_move_units_that_leave_a_wave_empty(B):
+    """More units than half of the GPU's CTAs, in shorter CTAs to other pages; in place one each."""
+    for fresh in (0, 30):
+        p = Pool(22, 38, 16, 8, 256, seed=18, fresh=fresh)
+        p.check(B, rising(22, 8, 470, 600, 19), [470 - 13 * i for i in range(22)])
