@@ -577,7 +577,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
                 far = true;
                 scale(x, c);
               }
-              y = started ? weights() : 0.f;
+              // (before the first logit above -inf m is 0, and what is added 0, or NaN for a NaN logit)
+              y = weights();
             }
             two_sum_acc(l, l_rest, y);
           }

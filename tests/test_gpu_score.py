@@ -477,3 +477,20 @@ def test_score_select_move_attend():
             want = w @ V * c.v_scale
             bound = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -14) * (w @ V.abs()) * c.v_scale + 2.0 ** -24
             assert ((out[b, 4 * g:4 * g + 4].cpu().double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("n", [1, 20, 50, 100])
+@pytest.mark.parametrize("where", ["last", "pages"])
+def test_nan_with_nothing_finite_beside_it(n, where):
+    """A NaN logit reaches its row where every other logit that the row sees of the same columns is masked, or NaN too: in
+    the newest position alone behind whole tiles, and all over the first columns of tiles (n: one and two row tiles, and
+    several row blocks)."""
+    for kv in (129, 257, 385):
+        c = Case([(n, kv), (1, 40)], Hq=8, Hkv=2, D=128)
+        bad = [kv - 1] if where == "last" else [t for t in [*range(32), *range(128, 160)] if t < kv]
+        for t in bad:
+            c.k[c.table[0, t // c.page].long(), t % c.page, 1, 5] = 0x7F
+        ref = reference(c)
+        assert torch.isnan(ref[0][0, 1, :kv]).all() and torch.isfinite(ref[0][0, 0, :kv]).all()
+        for kernel, S in kernels(c):
+            check(Run(c, kernel, S)(), c, ref)
