@@ -340,6 +340,17 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   }
 }
 
+// Whether a vector whose sum is NaN sees position t: its weight there is NaN whatever its own logit is, also one of -inf, which
+// the kept logits do not tell from one that is not there.  (Read again from lengths and table: only where a sum is NaN.)
+__device__ bool seen_by_nan(const ChunkParams& p, const Norm* norm, int RC, int b, int base, int t) {
+  int64_t blk;
+  int slot;
+  if (!chunk_place(p, b, t, blk, slot)) return false;
+  for (int r = 0; r < RC; ++r)
+    if (norm[r].inv != norm[r].inv && t <= base + token_at(p, r)) return true;
+  return false;
+}
+
 // Second kernel: a few positions per thread.
 template <int RV>
 __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant__ ScoreParams sp) {
@@ -357,6 +368,7 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
   }
   wait_for_previous_kernel();
   const int S = (req.kv - 1) / sp.stat_part + 1;
+  bool nan = false;  // a vector's sum is
   for (int r = warp; r < RV; r += kFoldThreads / 32) {
     Norm n = {0.f, 0.f};
     if (r < RC) {
@@ -364,6 +376,7 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
       n = join_norm(p.ml, (int64_t)p.total_q * p.Hq, (int64_t)(req.row0 + at.token) * p.Hq + g * p.G + at.head, S, lane, 32);
     }
     if (lane == 0) norm[r] = n;
+    nan |= n.inv != n.inv;
   }
   const float4* from = reinterpret_cast<const float4*>(sp.logits + ((int64_t)b * p.Hkv + g) * p.max_kv_len * RV);
   float4 y[EACH][RV / 4];
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
 #pragma unroll
     for (int i = 0; i < RV / 4; ++i)  // (past the last position: read again, not used)
       y[j][i] = __ldcg(from + (int64_t)min(t0 + j * kFoldThreads + tid, req.kv - 1) * (RV / 4) + i);
-  __syncthreads();
+  nan = __syncthreads_or(nan);
 #pragma unroll
   for (int j = 0; j < EACH; ++j) {
     const int t = t0 + j * kFoldThreads + tid;
@@ -388,6 +401,7 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
         if (r < RC && z[k] != -INFINITY) sum = fmaf(fast_exp2(z[k] - norm[r].m), norm[r].inv, sum);
       }
     }
+    if (nan && seen_by_nan(p, norm, RC, b, base, t)) sum = NAN;
     write_score(sp, b, g, t, base, sum);
   }
 }
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold_many(const __grid_con
                      (req.kv - 1) / sp.stat_part + 1);
   }
   norm[tid] = mine;
-  __syncthreads();
+  const bool nan = __syncthreads_or(mine.inv != mine.inv);
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kScoreGroupRows / 4; ++i) {
@@ -433,7 +447,9 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold_many(const __grid_con
     }
   }
   for (int o = lanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (t < req.kv && r0 == 0) write_score(sp, b, g, t, base, sum);
+  if (t >= req.kv || r0 != 0) return;
+  if (nan && seen_by_nan(p, norm, RC, b, base, t)) sum = NAN;
+  write_score(sp, b, g, t, base, sum);
 }
 
 template <int D, int FMT, int DT, int NQ>

@@ -494,3 +494,24 @@ def test_nan_with_nothing_finite_beside_it(n, where):
         assert torch.isnan(ref[0][0, 1, :kv]).all() and torch.isfinite(ref[0][0, 0, :kv]).all()
         for kernel, S in kernels(c):
             check(Run(c, kernel, S)(), c, ref)
+
+
+@pytest.mark.parametrize("n", [1, 3, 12, 60])
+@pytest.mark.parametrize("code", [0x7E, 0x7C])
+def test_minus_infinity_in_a_row_that_is_nan(n, code):
+    """Positions whose own logit is -inf are NaN too where a row that sees them is; those in a block out of range, which no
+    row sees, are not.  (n: up to 16 query vectors, more, and row tiles.)"""
+    c = Case([(n, 200), (1, 77)], Hq=8, Hkv=2, D=128, fmt="e5m2", k_scale=0.001)
+    c.q = c.q.abs() + c.q.new_tensor(2.0 ** -6)  # (an infinity times q keeps its sign)
+    t = 200 - n  # the first new token: all rows see it
+    c.k[c.table[0, t // c.page].long(), t % c.page, 1, 5] = code
+    for low in (7, 100, 150):
+        c.k[c.table[0, low // c.page].long(), low % c.page, 1, 9] = 0xFC
+    hidden = int(c.table[0, 40 // c.page])
+    ref = reference(c, bad_blocks=[hidden])
+    out = ref[0][0, 1, :200]
+    assert torch.isnan(out[[7, 100, 150]]).all() and (out[32:48] == 0).all()
+    bad = copy.deepcopy(c)
+    bad.table[0, 40 // c.page] = -1
+    for kernel, S in kernels(c):
+        check(Run(bad, kernel, S)(), bad, ref)
