@@ -45,6 +45,11 @@ constexpr int kTeams = 2;                        // of four decoder warps: every
 constexpr int kThreadsT = kEpilogue + kTeams * 128;
 constexpr int kMetaHead = 12288;
 constexpr int kCols = 32;                        // columns in registers
+// Maxima (base 2) from which on both passes round a logit before the maximum is taken off, and the column pass keeps 1 / l
+// apart.  Below, m + log2 l is one FP32 number below 2^7 (l < 2^66), which moves all of a row's weights by at most 2^-18 ln 2 =
+// 2.6e-6, and a row's logits are rounded in one pass at the most, 2^-18 again.  (At 2^22, from which on it is a
+// matter of finite results alone, a row's weights summed to 1 within 2^-24 m ln 2 only: 4e-5 at 2^10, 9 % below 2^22.)
+constexpr float kFar = 64.f;
 
 template <int D>
 struct Cfg : RowCfg<D> {
@@ -254,8 +259,8 @@ __device__ __forceinline__ void load_q(const ChunkParams& p, Meta& mt, uint8_t* 
 // Sum of 2^(c S - m) / l over kCols columns.  The quotient goes into the exponent, as m + log2 l: a
 // value that all lanes read costs a cycle of shared memory per warp and word, and three of them
 // for each column (factor, maximum, 1 / sum) took 3100 cycles of a tile of 256 x 128.
-// FAR: logits so large that the product is rounded before the maximum is taken off, as it was when the
-// maximum was found, and that the sum of m and log2 l would lose the latter.  MASKED: of
+// FAR: logits so large that the product is rounded before the maximum is taken off, as it was when the row's
+// sum was found, and that the sum of m and log2 l would lose of the latter (kFar).  MASKED: of
 // the columns whose rows see position t alone.  ONE: all rows have the factor c1.
 template <bool MASKED, bool FAR, bool ONE>
 __device__ __forceinline__ float column_sum(const uint32_t (&x)[kCols], const Meta& mt, int r0, int t, float c1) {
@@ -295,7 +300,7 @@ __device__ __forceinline__ float column_sum(const uint32_t (&x)[kCols], const Me
 }
 
 // -(m + log2 l) of a row: the exponent of l joins the whole m exactly, the rest is below 1/2, so that
-// one rounding is left (2^-20 at 2^4: 7e-7 of the row's weights).
+// one rounding is left (half an ulp of m + log2 l: 2^-20 at 2^4, 7e-7 of the row's weights; 2^-18 at kFar).
 __device__ __forceinline__ float folded(const Norm& n) {
   if (n.inv == 0.f) return -INFINITY;  // (nothing seen)
   const uint32_t u = __float_as_uint(n.inv);
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       named_bar_sync(1, kEpilogue);
       const int n_tiles = walk.tiles_of(rb);
       if (wl == 0 && j0 < n_tiles) issue(ktb + j0);
-      // the group's rows: the least that one sees; columns: whether logits are past 2^22
+      // the group's rows: the least that one sees; columns: whether logits are past kFar
       const int mine = tile * kM + 32 * wl + lane;      // rows: this thread's
       int hi = mine < RC ? mt.hi[mine] : INT_MAX;       // rows past RC: everything, dropped at the end
       const float c = mt.c[mine];
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
           hi = min(hi, mt.hi[tile * kM + 32 * i + lane]);
           top = fmaxf(top, fabsf(mt.m[tile * kM + 32 * i + lane]));
         }
-        far_cols = __any_sync(0xffffffffu, top >= 0x1p22f);
+        far_cols = __any_sync(0xffffffffu, top >= kFar);
       }
       const int hi_min = __reduce_min_sync(0xffffffffu, hi);
       constexpr bool kOne = DT == FP8KV_DTYPE_F16;      // (bf16 rows have scales of their own)
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
       // up to 2^26 / 32 of them)
       float m = 0.f, l = 0.f, l_rest = 0.f;
       bool started = false;                             // ... a logit above -inf was seen
-      bool far = false;                                 // some row of the warp has logits past 2^22: products are rounded
+      bool far = false;                                 // some row of the warp has logits past kFar: products are rounded
                                                         // before the maximum is taken off
       for (int j = j0; j < n_tiles; j += j_step) {
         const int kt = ktb + j, parity = uses & 1;
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) score_tile(const __grid_constant
               }
               m = n;
               started |= top != -INFINITY;
-              if (!far && __any_sync(0xffffffffu, fabsf(m) >= 0x1p22f)) {
+              if (!far && __any_sync(0xffffffffu, fabsf(m) >= kFar)) {
                 far = true;
                 scale(x, c);
               }

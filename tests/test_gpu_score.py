@@ -14,6 +14,7 @@ with a_rt the scaled sum of |q_d k_td|.
 """
 
 import copy
+import math
 
 import numpy as np
 import pytest
@@ -515,3 +516,31 @@ def test_minus_infinity_in_a_row_that_is_nan(n, code):
     bad.table[0, 40 // c.page] = -1
     for kernel, S in kernels(c):
         check(Run(bad, kernel, S)(), bad, ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("power", [3, 5, 6, 7, 9, 11, 13, 15, 17, 19, 20, 21, 22, 24, "mixed", "apart"])
+def test_equal_keys_share_a_row(power, dtype):
+    """Where all of a row's logits are equal its weights are 1 / (positions seen), however large the logits are.
+
+    Per row, relative: the logits of a row are the same number x, so in exact arithmetic of the exponent the factor 2^(x - m)
+    cancels.  Up to |x| = 2^7 that is off by the rounding of numbers of that size at the most, 2 x 2^-18 ln 2 in all; past it
+    both passes round the same product.  The row's sum of N weights (N/64 + 32) 2^-23 (as above), the sum over R rows (R/64 + 80) 2^-24."""
+    for requests in ([(1, 3), (2, 300)], [(30, 300), (1, 129), (40, 45)], [(100, 700), (70, 200)]):
+        c = Case(requests, Hq=8, Hkv=2, D=128, dtype=dtype, softmax_scale=45.0, k_scale=1.0)
+        c.k[:] = 0x38  # 1.0
+        # (mixed: within eight tokens, a warp's 32 rows; apart: from eight to eight)
+        p = torch.full((c.total,), float(power)) if not isinstance(power, str) else \
+            torch.tensor([22.0, 21.0, 3.0, 6.0, 13.0, 20.0])[torch.arange(c.total) // (1 if power == "mixed" else 8) % 6]
+        # 128 q 45 log2 e = 2^13.02 q
+        c.q[:] = (torch.where(torch.arange(c.Hq)[None] % 2 == 1, -1.0, 1.0) * 2.0 ** (p[:, None] - 13))[..., None].to(dtype)
+        want = torch.full((len(requests), 2, c.max_kv), float("nan"), dtype=torch.float64)
+        tol = want.clone()
+        for b, (n, kv) in enumerate(requests):
+            for t in range(kv):
+                seen = torch.arange(max(t, kv - n), kv) + 1  # positions that each row that sees t sees
+                want[b, :, t] = c.group * (1.0 / seen.double()).sum()
+            tol[b, :, :kv] = want[b, :, :kv] * (2.0 ** -17 * math.log(2) + (kv / 64 + 32) * 2.0 ** -23 +
+                                                (n * c.group / 64 + 80) * 2.0 ** -24)
+        for kernel, S in kernels(c):
+            check(Run(c, kernel, S)(), c, (want, tol))
