@@ -340,20 +340,28 @@ __global__ void __launch_bounds__(kThreadsS, Cfg<D, NQ>::kCtas)
   }
 }
 
-// Whether a vector whose sum is NaN sees position t: its weight there is NaN whatever its own logit is, also one of -inf, which
-// the kept logits do not tell from one that is not there.  (Read again from lengths and table: only where a sum is NaN.)
-__device__ bool seen_by_nan(const ChunkParams& p, const Norm* norm, int RC, int b, int base, int t) {
+// Position t, its weight written, becomes NaN if a vector with a NaN sum sees it, also where that vector's own logit is
+// -inf: which is what is kept, too, where a vector does not see the position, so lengths and table tell them apart.  (Behind
+// the sums, since in their midst it took 3 to 10 us of a batch's 80.)
+__device__ __forceinline__ void pass_nan_on(const ScoreParams& sp, const Norm* norm, int RC, int b, int g, int base, int t) {
   int64_t blk;
   int slot;
-  if (!chunk_place(p, b, t, blk, slot)) return false;
+  if (!chunk_place(sp.c, b, t, blk, slot)) return;
+#pragma unroll 1
   for (int r = 0; r < RC; ++r)
-    if (norm[r].inv != norm[r].inv && t <= base + token_at(p, r)) return true;
-  return false;
+    if (norm[r].inv != norm[r].inv && t <= base + token_at(sp.c, r)) sp.out[b * sp.out_sr + g * sp.out_sh + t] = norm[r].inv;
+}
+// Whether there is such a vector.
+__device__ __forceinline__ bool any_nan(const Norm* norm, int n) {
+  bool nan = false;
+  for (int r = 0; r < n; ++r) nan |= norm[r].inv != norm[r].inv;
+  return nan;
 }
 
 // Second kernel: a few positions per thread.
+// (CTAs of an SM as without the look for NaN, which took more registers: 82 us for a batch's 80)
 template <int RV>
-__global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant__ ScoreParams sp) {
+__global__ void __launch_bounds__(kFoldThreads, RV == 4 ? 8 : RV == 8 ? 4 : 5) score_fold(const __grid_constant__ ScoreParams sp) {
   constexpr int EACH = fold_each(RV);
   const ChunkParams& p = sp.c;
   __shared__ Norm norm[16];
@@ -368,7 +376,6 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
   }
   wait_for_previous_kernel();
   const int S = (req.kv - 1) / sp.stat_part + 1;
-  bool nan = false;  // a vector's sum is
   for (int r = warp; r < RV; r += kFoldThreads / 32) {
     Norm n = {0.f, 0.f};
     if (r < RC) {
@@ -376,7 +383,6 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
       n = join_norm(p.ml, (int64_t)p.total_q * p.Hq, (int64_t)(req.row0 + at.token) * p.Hq + g * p.G + at.head, S, lane, 32);
     }
     if (lane == 0) norm[r] = n;
-    nan |= n.inv != n.inv;
   }
   const float4* from = reinterpret_cast<const float4*>(sp.logits + ((int64_t)b * p.Hkv + g) * p.max_kv_len * RV);
   float4 y[EACH][RV / 4];
@@ -385,11 +391,11 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
 #pragma unroll
     for (int i = 0; i < RV / 4; ++i)  // (past the last position: read again, not used)
       y[j][i] = __ldcg(from + (int64_t)min(t0 + j * kFoldThreads + tid, req.kv - 1) * (RV / 4) + i);
-  nan = __syncthreads_or(nan);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < EACH; ++j) {
     const int t = t0 + j * kFoldThreads + tid;
-    if (t >= req.kv) return;
+    if (t >= req.kv) break;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < RV / 4; ++i) {
@@ -401,8 +407,14 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold(const __grid_constant
         if (r < RC && z[k] != -INFINITY) sum = fmaf(fast_exp2(z[k] - norm[r].m), norm[r].inv, sum);
       }
     }
-    if (nan && seen_by_nan(p, norm, RC, b, base, t)) sum = NAN;
     write_score(sp, b, g, t, base, sum);
+  }
+  if (any_nan(norm, RV)) {
+#pragma unroll 1
+    for (int j = 0; j < EACH; ++j) {
+      const int t = t0 + j * kFoldThreads + tid;
+      if (t < req.kv) pass_nan_on(sp, norm, RC, b, g, base, t);
+    }
   }
 }
 
@@ -448,8 +460,8 @@ __global__ void __launch_bounds__(kFoldThreads) score_fold_many(const __grid_con
   }
   for (int o = lanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (t >= req.kv || r0 != 0) return;
-  if (nan && seen_by_nan(p, norm, RC, b, base, t)) sum = NAN;
   write_score(sp, b, g, t, base, sum);
+  if (nan) pass_nan_on(sp, norm, RC, b, g, base, t);
 }
 
 template <int D, int FMT, int DT, int NQ>
