@@ -18,6 +18,10 @@ inline bool strides_ok(const int64_t* s, int n, int64_t unit) {
     if (s[i] < 0 || s[i] % unit) return false;
   return true;
 }
+// From x to y, in floats (both on their boundary).
+inline int64_t floats_between(const float* x, const float* y) {
+  return ((int64_t)reinterpret_cast<uintptr_t>(y) - (int64_t)reinterpret_cast<uintptr_t>(x)) / 4;
+}
 // Finite host scales, or device floats on their boundary.
 template <class Args>
 inline bool scales_ok(const Args& a) {

@@ -80,9 +80,13 @@ extern "C" int fp8kv_attn_cache_move(const fp8kv_cache_move_args* a, fp8kv_strea
   if (!strides_ok(es, 6, 1)) return FP8KV_EINVAL;
   if (!a->score != !a->score_out) return FP8KV_EINVAL;
   if (a->score) {
-    if (!aligned(a->score, 4) || !aligned(a->score_out, 4) || a->score == a->score_out || a->max_len < 1)
+    if (!aligned(a->score, 4) || !aligned(a->score_out, 4) || a->max_len < 1)
       return FP8KV_EINVAL;
     if (!apart(a->batch, es[4], a->num_kv_heads, es[5], a->max_len)) return FP8KV_EINVAL;
+    // (weights are read while others are written, in no order)
+    if (meet({a->batch, es[2], a->num_kv_heads, es[3]}, {a->batch, es[4], a->num_kv_heads, es[5]}, a->max_len,
+             floats_between(a->score, a->score_out)))
+      return FP8KV_EINVAL;
   }
   const int sms = sm_count();
   if (sms < 1) return FP8KV_ECUDA;

@@ -140,8 +140,12 @@ extern "C" int fp8kv_attn_cache_score(const fp8kv_cache_score_plan_t* plan, cons
     return FP8KV_EINVAL;
   if (!a->score || !aligned(a->score, 4) || !aligned(a->score_in, 4)) return FP8KV_EINVAL;
   if (!apart(plan->batch, fs[2], plan->num_kv_heads, fs[3], plan->max_kv_len)) return FP8KV_EINVAL;
-  // the same buffer is read and written element by element
-  if (a->score_in == a->score && (fs[0] != fs[2] || fs[1] != fs[3])) return FP8KV_EINVAL;
+  // The same buffer is read and written element by element; others, in no order, share no place.
+  if (a->score_in == a->score ? fs[0] != fs[2] || fs[1] != fs[3]
+                              : a->score_in && meet({plan->batch, fs[0], plan->num_kv_heads, fs[1]},
+                                                    {plan->batch, fs[2], plan->num_kv_heads, fs[3]}, plan->max_kv_len,
+                                                    floats_between(a->score_in, a->score)))
+    return FP8KV_EINVAL;
 
   ScoreParams p;
   std::memset(&p, 0, sizeof(p));

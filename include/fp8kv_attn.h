@@ -625,8 +625,8 @@ int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t str
  *                    of softmax(z_ih)_t
  *
  * with the logits z of fp8kv_attn_chunk without a window.  One call per decode step accumulates
- * (score_in = score is allowed: the same buffer with the same strides; others do not overlap); one with the last rows
- * of a prompt, or all of them, rates the prompt's positions.  A request without new tokens and
+ * (score_in = score is allowed: the same buffer with the same strides; other arrays whose rows share places with
+ * score's are refused); one with the last rows of a prompt, or all of them, rates the prompt's positions.  A request without new tokens and
  * positions from kv_len[b] on are left as they are.
  *
  * FP32 throughout: logits accumulate as in fp8kv_attn_chunk, weights, their sums and the
@@ -736,8 +736,9 @@ int fp8kv_attn_cache_select(const fp8kv_cache_select_args* a, fp8kv_stream_t str
  * dst_table: into other pages.  Any s >= 0; no page is both read and written (block_table itself is refused).
  *
  * score / score_out (both or none): the weights' row of each head moves likewise,
- * score_out[b][h][first + k] = score[b][h][first + s], between two buffers that do not
- * overlap; what is not moved to is left as it is.
+ * score_out[b][h][first + k] = score[b][h][first + s], between two arrays whose rows share
+ * no place (views of one buffer may lie between each other; others are refused); what is not
+ * moved to is left as it is.
  *
  * A position outside its table, or whose block is out of range: the row is not moved,
  * FP8KV_STATUS_BAD_BLOCK; weights outside [0, max_len): FP8KV_STATUS_BAD_LEN, as is a

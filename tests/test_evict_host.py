@@ -389,3 +389,93 @@ def test_binding_checks_select_and_move(B):
                 dict(score=t["score"][:2], score_out=t["score"][:2]), dict(block_table=t["table"].expand(3, 4).t())):
         with pytest.raises(ValueError):
             B.make_cache_move_args(**{**base, **bad})
+
+
+# ---------------------------------------------------------------- weights that share places
+
+def test_meet(tmp_path):
+    """Whether rows of two arrays share a place, against all pairs of them."""
+    import numpy as np
+
+    r = np.random.default_rng(11)
+    L, cases = 8, []
+    for _ in range(4000):
+        x, y = ([int(r.integers(1, 6)), int(r.integers(0, 90)), int(r.integers(1, 5)), int(r.integers(0, 60))] for _ in "xy")
+        kind = r.integers(0, 4)
+        if kind == 1:  # the same strides
+            y[1], y[3] = x[1], x[3]
+        elif kind == 2:  # rows of one buffer in turn
+            x[3], x[1] = 2 * L, 2 * L * x[2]
+            y[1:] = x[1:]
+        elif kind == 3:
+            y[1] = x[1]
+        cases.append((*x, *y, int(r.integers(-400, 400)) if kind != 2 else int(r.choice([-L - 1, -L, L, L - 1, L + 1, 0, 5 * L]))))
+    src = tmp_path / "meet.cpp"
+    src.write_text("""#include <cstdio>
+#include "output_layout.h"
+int main() {
+  long long a[9];
+  while (true) {
+    for (auto& x : a)
+      if (std::scanf("%lld", &x) != 1) return 0;
+    std::printf("%d\\n", fp8kv::meet({a[0], a[1], a[2], a[3]}, {a[4], a[5], a[6], a[7]}, 8, a[8]));
+  }
+}
+""")
+    exe = tmp_path / "meet"
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "fp8_e4m3_paged_gb300", "csrc"), str(src), "-o", str(exe)],
+                   check=True)
+    text = "\n".join(" ".join(map(str, c)) for c in cases)
+    got = [x == "1" for x in subprocess.run([str(exe)], input=text, check=True, capture_output=True, text=True).stdout.split()]
+    want = []
+    for c in cases:
+        starts = [(np.arange(c[i])[:, None] * c[i + 1] + np.arange(c[i + 2])[None] * c[i + 3]).ravel() for i in (0, 4)]
+        want.append(bool((np.abs(starts[1][None] + c[8] - starts[0][:, None]) < L).any()))
+    assert got == want and 500 < sum(want) < len(want) - 500
+
+
+SHARED = [  # (first places in floats, strides by request and head) of the weights read, and of those written; rows of 10
+    ((0, 20, 10), (5, 20, 10)),     # some elements on
+    ((5, 20, 10), (0, 20, 10)),     # ... back
+    ((0, 20, 10), (59, 20, 10)),    # the last one
+    ((0, 40, 10), (10, 40, 10)),    # another head's row of the same buffer
+    ((0, 40, 20), (15, 40, 20)),    # rows in turn, too near
+    ((0, 20, 10), (0, 40, 20)),     # the same rows, other strides
+    ((0, 0, 0), (9, 30, 10)),       # one row for all
+]
+APART = [
+    ((0, 20, 10), (60, 20, 10)),
+    ((60, 20, 10), (0, 20, 10)),
+    ((0, 40, 20), (10, 40, 20)),    # rows in turn
+    ((0, 40, 10), (20, 40, 10)),    # requests in turn
+    ((0, 100, 10), (20, 100, 40)),  # other strides
+    ((0, 0, 0), (10, 30, 10)),
+]
+
+
+@pytest.mark.parametrize("read,written", SHARED)
+def test_weights_that_share_places_are_refused(B, read, written):
+    at = 4 * read[0] + FAKE, 4 * written[0] + FAKE
+    kw = dict(score=at[0], score_out=at[1], max_len=10, score_stride_req=read[1], score_stride_head=read[2],
+              score_out_stride_req=written[1], score_out_stride_head=written[2])
+    _rejects(B, lambda: B.fp8kv_attn_cache_move(_move_args(B, **kw)), -1)
+    for max_q in (1, 64):
+        plan = B.fp8kv_attn_cache_score_plan(_desc(B, max_q=max_q, max_kv_len=10))
+        kw = dict(score_in=at[0], score=at[1], score_in_stride_req=read[1], score_in_stride_head=read[2],
+                  score_stride_req=written[1], score_stride_head=written[2])
+        _rejects(B, lambda: B.fp8kv_attn_cache_score(plan, _score_args(B, plan, **kw)), -1)
+
+
+@pytest.mark.parametrize("read,written", APART)
+def test_weights_beside_each_other_are_taken(B, tmp_path, read, written):
+    """Views of one buffer whose rows share no place.  (The check itself: a call that passes it would launch.)"""
+    src = tmp_path / "apart.cpp"
+    src.write_text(f"""#include "output_layout.h"
+int main() {{
+  return fp8kv::meet({{3, {read[1]}, 2, {read[2]}}}, {{3, {written[1]}, 2, {written[2]}}}, 10, {written[0] - read[0]});
+}}
+""")
+    exe = tmp_path / "apart"
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "fp8_e4m3_paged_gb300", "csrc"), str(src), "-o", str(exe)],
+                   check=True)
+    assert subprocess.run([str(exe)]).returncode == 0

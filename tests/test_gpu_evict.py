@@ -434,3 +434,23 @@ def test_move_units_that_leave_a_wave_empty(B):
     for fresh in (0, 30):
         p = Pool(22, 38, 16, 8, 256, seed=18, fresh=fresh)
         p.check(B, rising(22, 8, 470, 600, 19), [470 - 13 * i for i in range(22)])
+
+
+def test_move_weights_between_views(B):
+    """Weights from and to rows of one buffer in turn; views that share a place are refused."""
+    p = Pool(3, 20, 16, 2, 64, seed=30)
+    src = rising(3, 2, 200, 300, 31)
+    both = torch.rand((3, 2, 2, 300), generator=torch.Generator().manual_seed(32)).cuda()
+    want = both.cpu()
+    for b in range(3):
+        for h in range(2):
+            want[b, 1, h, :200] = want[b, 0, h, src[b, h].long()]
+    B.fp8kv_attn_cache_move(p.args(B, src, [200, 200, 200], score=both[:, 0], score_out=both[:, 1]), stream())
+    torch.cuda.synchronize()
+    assert torch.equal(both.cpu(), want)
+    line = torch.rand(3 * 2 * 300 + 50, device="cuda")
+    for k in (0, 1, 50):
+        with pytest.raises(B.Fp8kvError) as e:
+            B.fp8kv_attn_cache_move(p.args(B, src, [200, 200, 200], score=line[:1800].view(3, 2, 300),
+                                           score_out=line[k:k + 1800].view(3, 2, 300)), stream())
+        assert e.value.code == B.EINVAL
