@@ -9,9 +9,10 @@
 // enough, then, that rows are taken in rounds by k and that a round is written only when all rows up
 // to its end have been read; later rows may be read as early as one likes.  One unit (a request's KV
 // head, K and V) is walked by one CTA, or by one cluster, whose barrier in each round says that
-// all CTAs' reads have arrived, and orders them before the others' writes.  (Its release waits for the
-// writes of the round before it, too: 16 x 2052 rows 38.7 us, 35.4 without, one request 9.6 and 8.3.  Without release nothing but cp.async's completion
-// would stand between one CTA's read of a row and another's write of it.)  To pages of their own no such order is needed.
+// all CTAs' reads have arrived, and orders them before the others' writes.  (Its release waits for
+// the writes of the round before it, too: 16 x 2052 rows 38.7 us, 35.4 without it, one request 9.6 and
+// 8.3.  Without it, nothing but cp.async's completion would stand between one CTA's read of a row and
+// another's write of it.)  To pages of their own no such order is needed.
 //
 // Rounds of 32 KB per CTA through shared memory: cp.async brings the rows of the next two
 // rounds while this one is written, and the list and the table of the round after them are
@@ -138,9 +139,10 @@ __global__ void __launch_bounds__(kThreads, kResident) move_kernel(const __grid_
     s_place[slot][tid] = p;
   };
 
-  // This thread's pieces of a round, the same in every one: place, head, piece of the row, K or V.
+  // This thread's pieces of a round, the same in every one: the place, whether K or V, and where the
+  // piece of that head's row lies in the row at offset 0.
   const int per_head = geo.rows * geo.chunks, per_cache = per_head * geo.heads;
-  int piece[kItems];  // place | V << 9 | piece of the row << 10; -1: none
+  int piece[kItems];  // place | V << 9; -1: none
   uint8_t* base[kItems];
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {

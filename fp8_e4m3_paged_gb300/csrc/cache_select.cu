@@ -39,7 +39,7 @@ template <int kThreads>
 struct Shared {
   static constexpr int kWarps = kThreads / 32;
   alignas(16) uint32_t hist[kPasses][kBins];
-  uint32_t tie[kWarps], above[kWarps];         // selected ones and equal ones of each warp's run
+  uint32_t tie[kWarps], above[kWarps];         // of each warp's run: keys equal to the cut, and above it
   uint32_t warp_sum[kWarps];
   uint32_t digit, left;                        // found by one thread for all
   uint32_t total[2];                           // of the CTA: above, equal

@@ -1,5 +1,5 @@
-// Thread-block clusters of the cache kernels: barrier over all their CTAs in two halves,
-// rank, size, and a load from the place that `p` has in the shared memory of CTA `rank`.
+// Thread-block clusters: barrier over all their CTAs, rank, and loads from the place that `p` has in
+// the shared memory of CTA `rank`.
 #pragma once
 
 #include <cstdint>

@@ -14,7 +14,7 @@ inline int score_vectors(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 
 
 struct ScoreParams {
   ChunkParams c;           // no V, no output; c.S partitions of the rows' sums, c.ml [S][total_q][Hq]
-  int32_t stat_part;       // positions of such a partition (tile kernel)
+  int32_t stat_part;       // positions of such a partition (tile kernel with per_head above 0: not used)
   int32_t col_part;        // positions of a CTA of the column pass (tile kernel)
   int32_t groups;          // row groups of the column pass; above 1 they meet in `partial`
   int32_t per_head;        // tile kernel, above 0: CTAs per KV head, which find their shares from the lengths

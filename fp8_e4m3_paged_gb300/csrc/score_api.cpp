@@ -59,7 +59,9 @@ extern "C" int fp8kv_attn_cache_score_plan(const fp8kv_chunk_desc* d, fp8kv_cach
     // pays while that is little, because the tile kernel's two passes take 20 us on the shortest contexts.
     // us, stream / tile, 8 KV heads x 4, D 128, by the bytes counted here: 32 tokens on 500 (8 MB) 9.8 / 18.5,
     // 4 x 500 (31 MB) 16.6 / 24.9, 4 x 1000 (63 MB) 27.0 / 26.3, 16 x 500 (125 MB) 44 / 28; 8 tokens on
-    // 4 x 2000 (31 MB) 13.6 / 29.1, 16 x 1000 (63 MB) 20 / 37; 48 requests of 16 tokens on 20 (8 MB) 13 / 48.
+    // 4 x 2000 (31 MB) 13.6 / 29.1, 16 x 1000 (66 MB) 20 / 37; 48 requests of 16 tokens on 20 (8 MB) 13 / 48.
+    // The border is the one of 32 tokens.  Fewer still stream faster past it and do not: those 8, and 5 tokens
+    // on 64 x 500 (108 MB) 35 / 80; 64 on 4 x 500 (74 MB) 42 / 31 are on the right side.
     const int64_t bytes = pairs * len * (8 * rows + ceil_div(rows, kScoreGroupRows) * P.head_dim);
     // (and the workspace stays in bounds: the tile kernel keeps no logits)
     const bool stream = pairs * len * score_vectors(rows) * 4 <= kScoreLogitBytes &&

@@ -626,8 +626,8 @@ int fp8kv_attn_cache_calibrate(const fp8kv_calibrate_args* a, fp8kv_stream_t str
  *
  * with the logits z of fp8kv_attn_chunk without a window.  One call per decode step accumulates
  * (score_in = score is allowed: the same buffer with the same strides; other arrays whose rows share places with
- * score's are refused); one with the last rows of a prompt, or all of them, rates the prompt's positions.  A request without new tokens and
- * positions from kv_len[b] on are left as they are.
+ * score's are refused); one with the last rows of a prompt, or all of them, rates the prompt's positions.
+ * A request without new tokens and positions from kv_len[b] on are left as they are.
  *
  * FP32 throughout: logits accumulate as in fp8kv_attn_chunk, weights, their sums and the
  * score are FP32, added in a fixed order (no atomics: the same inputs give the same bits).
@@ -645,7 +645,7 @@ typedef struct {
   int32_t num_splits;      /* partitions of the rows' sums */
   int32_t vectors;         /* stream: logits kept per position */
   int32_t row_tiles;       /* tile: bound of the row blocks of all requests */
-  int32_t stat_part;       /* tile: positions of a partition of the rows' sums */
+  int32_t stat_part;       /* positions of a partition of the rows' sums (per_head above 0: not used) */
   int32_t col_part;        /* tile: positions of a CTA of the column pass */
   int32_t row_groups;      /* tile: shares of the row blocks in the column pass */
   int32_t per_head;        /* tile, above 0: CTAs per KV head, which find their shares from the lengths */
