@@ -43,6 +43,7 @@
 #include <cuda_runtime.h>
 
 #include "chunk_common.cuh"
+#include "cluster.cuh"
 #include "internal.h"
 #include "stream_ptx.cuh"
 #include "tc_ptx.cuh"
@@ -91,27 +92,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-// Thread-block cluster: barrier over all its CTAs in two halves (the first without
-// order, for a CTA that has only begun), and stores into a peer's shared memory
-// (the place that `p` has in CTA `rank`).
-__device__ __forceinline__ void cluster_here() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void peer_store(uint32_t a, float2 x) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(x.x), "f"(x.y) : "memory");
-}
-__device__ __forceinline__ void peer_store(uint32_t a, float4 x) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
-               : "memory");
 }
 
 // TWIN (at most 4 vectors): columns 4 to 7 hold the vectors of columns 0 to 3 again.
