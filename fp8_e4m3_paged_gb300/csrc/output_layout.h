@@ -3,7 +3,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <utility>
 
 namespace fp8kv {
 
@@ -33,62 +32,51 @@ struct RowsAt {
   int64_t requests, stride_request, heads, stride_head;
 };
 
+// Whether `from` and a whole number (lo to hi) of each of n strides, the longest first, add up to less than L on
+// either side of 0.  Of a stride only the numbers are tried that the shorter ones can make up for.
+struct Steps {
+  int64_t stride, lo, hi;
+};
+inline bool reach_zero(const Steps* step, int n, __int128 from, int64_t L) {
+  using wide = __int128;
+  if (n == 0) return from < L && from > -L;
+  wide lo = from, hi = from;  // with the shorter ones
+  for (int i = 1; i < n; ++i) {
+    lo += (wide)step[i].stride * step[i].lo;
+    hi += (wide)step[i].stride * step[i].hi;
+  }
+  auto floor_div = [](wide a, wide b) { return a / b - (a % b < 0); };
+  const wide stride = step->stride;
+  const wide first = std::max<wide>(step->lo, floor_div(-L - hi, stride) + 1);
+  const wide last = std::min<wide>(step->hi, -floor_div(lo - L, stride) - 1);
+  for (wide k = first; k <= last; ++k)
+    if (reach_zero(step + 1, n - 1, from + stride * k, L)) return true;
+  return false;
+}
+
 // Whether a row of x and a row of y share a place; y begins `ahead` elements behind x.
 inline bool meet(const RowsAt& x, const RowsAt& y, int64_t L, int64_t ahead) {
-  using wide = __int128;
   if (x.requests < 1 || x.heads < 1 || y.requests < 1 || y.heads < 1) return false;
-  // Row starts differ by `ahead` and a whole number of each of these steps, equal ones joined.
-  struct {
-    int64_t stride, lo, hi;
-  } step[4];
+  // Row starts differ by `ahead` and a whole number of each stride, equal ones joined.
+  Steps step[4];
   int n = 0;
   auto add = [&](int64_t stride, int64_t lo, int64_t hi) {
     if (stride == 0 || lo == hi) return;
-    for (int i = 0; i < n; ++i)
-      if (step[i].stride == stride) {
-        step[i].lo += lo;
-        step[i].hi += hi;
-        return;
-      }
-    step[n++] = {stride, lo, hi};
+    int i = 0;
+    while (i < n && step[i].stride > stride) ++i;
+    if (i < n && step[i].stride == stride) {
+      step[i].lo += lo;
+      step[i].hi += hi;
+      return;
+    }
+    for (int k = n++; k > i; --k) step[k] = step[k - 1];
+    step[i] = {stride, lo, hi};
   };
   add(x.stride_request, 1 - x.requests, 0);
   add(x.stride_head, 1 - x.heads, 0);
   add(y.stride_request, 0, y.requests - 1);
   add(y.stride_head, 0, y.heads - 1);
-  wide lo = ahead, hi = ahead;
-  for (int i = 0; i < n; ++i) {
-    lo += (wide)step[i].stride * step[i].lo;
-    hi += (wide)step[i].stride * step[i].hi;
-  }
-  if (lo >= L || hi <= -L) return false;  // one behind the other, as usual
-  if (n == 0) return true;
-  // Views into each other: all of the shorter steps, and of the longest one the two that come nearest.
-  for (int i = 0; i + 1 < n; ++i)
-    if (step[i].hi - step[i].lo > step[n - 1].hi - step[n - 1].lo) std::swap(step[i], step[n - 1]);
-  const wide stride = step[n - 1].stride;
-  int64_t at[3];
-  wide from = ahead;
-  for (int i = 0; i + 1 < n; ++i) {
-    at[i] = step[i].lo;
-    from += (wide)step[i].stride * at[i];
-  }
-  while (true) {
-    const wide below = -from / stride - (-from % stride < 0);
-    for (wide k = below; k <= below + 1; ++k) {
-      const wide d = from + stride * std::min<wide>(std::max<wide>(k, step[n - 1].lo), step[n - 1].hi);
-      if (d < L && d > -L) return true;
-    }
-    int i = 0;
-    while (i + 1 < n && at[i] == step[i].hi) {
-      from -= (wide)step[i].stride * (step[i].hi - step[i].lo);
-      at[i] = step[i].lo;
-      ++i;
-    }
-    if (i + 1 >= n) return false;
-    ++at[i];
-    from += step[i].stride;
-  }
+  return reach_zero(step, n, ahead, L);
 }
 
 }  // namespace fp8kv
