@@ -527,7 +527,8 @@ typedef struct {
   const int32_t* depth;   /* [total_q]; NULL without a window */
 } fp8kv_tree_args;
 
-/* As fp8kv_attn_chunk_plan, for fp8kv_attn_tree; more than 1024 nodes (max_q): FP8KV_EUNSUPPORTED. */
+/* As fp8kv_attn_chunk_plan, for fp8kv_attn_tree; more than 1024 nodes (max_q): FP8KV_EUNSUPPORTED.  Partitions
+ * and workspace follow max_kv_len: near the longest request it is fastest. */
 int fp8kv_attn_tree_plan(const fp8kv_chunk_desc* d, fp8kv_chunk_plan_t* plan);
 /* Launch the attention on `stream`; plans of fp8kv_attn_chunk_plan: FP8KV_EINVAL (and the other way round). */
 int fp8kv_attn_tree(const fp8kv_chunk_plan_t* plan, const fp8kv_tree_args* a, fp8kv_stream_t stream);
@@ -678,6 +679,7 @@ typedef struct {
 } fp8kv_cache_score_args;
 
 /* Validate `d` (as fp8kv_attn_chunk_plan; kernel and num_splits choose likewise) and fill `plan`.
+ * Kernel, partitions and workspace follow max_kv_len, not the lengths: near the longest request it is fastest.
  * With FP8KV_CHUNK_AUTO the logits that FP8KV_CHUNK_STREAM keeps in the workspace stay below 4 GiB (else, and
  * for many query vectors, FP8KV_CHUNK_TILE, which keeps none).
  * A window, more than 65535 pairs of request and KV head, max_kv_len above 2^26, and FP8KV_CHUNK_STREAM with more than 256
